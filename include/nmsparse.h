@@ -412,6 +412,35 @@ nm_status nm_diag_spmm(const void* values, const int32_t* offsets, int64_t D, in
                        const void* act, int64_t T, int64_t ldx, const int32_t* perm, void* Y, int64_t ldy,
                        int out_dtype, void* stream);
 
+/*
+ * Layer norm over the H features of each of T tokens: with mu the mean, var the
+ * mean of (x - mu)^2 and rstd = (var + eps)^(-1/2) of a row,
+ *   nm_layernorm:     xh = (x - mu) rstd,  y = xh * weight + bias;
+ *   nm_layernorm_bwd: with p = dy * weight,
+ *                     dx = rstd (p - mean(p) - xh mean(p xh)),
+ *                     dw[h] = sum_t dy xh,  db[h] = sum_t dy.
+ *   x, y, dy, dx   device [T, H] row-major with leading dimensions >= H,
+ *                  dtype NM_F16, NM_BF16 or NM_F32 (one for all); 1 <= H <= 2^24.
+ *   weight, bias   device [H] of dtype, or NULL (ones, zeros).
+ *   mean, rstd     device fp32 [T]; written by the forward pass (both NULL: not
+ *                  kept), read by the backward pass.
+ *   dw, db         device [H], out_dtype NM_F32 or dtype, or NULL (not wanted);
+ *                  T == 0 writes zeros.
+ *   workspace      device, nm_layernorm_bwd_workspace_size bytes, 16-byte
+ *                  aligned; only needed for dw or db.
+ * Statistics and sums are fp32 (the variance taken about the mean), outputs are
+ * rounded once.  Pointers need the alignment of their element only, leading
+ * dimensions are free.  Outputs must not overlap inputs or each other
+ * (NM_ERR_ALIAS).  A token holding Inf or NaN gives NaN in its own row and in
+ * dw / db.
+ */
+nm_status nm_layernorm(const void* x, int64_t T, int64_t H, int64_t ldx, int dtype, const void* weight,
+                       const void* bias, float eps, void* y, int64_t ldy, float* mean, float* rstd, void* stream);
+nm_status nm_layernorm_bwd_workspace_size(int64_t T, int64_t H, size_t* bytes);
+nm_status nm_layernorm_bwd(const void* dy, int64_t ldg, const void* x, int64_t ldx, int64_t T, int64_t H, int dtype,
+                           const float* mean, const float* rstd, const void* weight, void* dx, int64_t lddx, void* dw,
+                           void* db, int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,7 +18,7 @@ __all__ = ["NM_OK", "NM_F16", "NM_BF16", "NM_F32", "NM_I8", "NM_I32", "NM_FP8", 
            "nm_packed_sizes", "nm_compress", "nm_decompress", "nm_spmm", "nm_spmm_perm",
            "nm_spmm_perm_workspace_size", "nm_spmm_perm_static", "nm_check_perm", "nm_spmm_dx", "nm_spmm_dw",
            "nm_hybrid_layout", "nm_hybrid_compress", "nm_hybrid_spmm", "nm_block_structure", "nm_block_compress",
-           "nm_block_spmm", "nm_diag_compress", "nm_diag_spmm", "PATTERNS"]
+           "nm_block_spmm", "nm_diag_compress", "nm_diag_spmm", "nm_layernorm", "nm_layernorm_bwd", "PATTERNS"]
 
 NM_OK = 0
 NM_F16, NM_BF16, NM_F32, NM_I8, NM_I32, NM_FP8 = 0, 1, 2, 3, 4, 5
@@ -96,6 +96,13 @@ def lib() -> ctypes.CDLL:
     L.nm_diag_compress.argtypes = [vp, i64, i64, i64, i32, vp, i64, vp, vp]
     L.nm_diag_spmm.restype = i32
     L.nm_diag_spmm.argtypes = [vp, vp, i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, i32, vp]
+    f32 = ctypes.c_float
+    L.nm_layernorm.restype = i32
+    L.nm_layernorm.argtypes = [vp, i64, i64, i64, i32, vp, vp, f32, vp, i64, vp, vp, vp]
+    L.nm_layernorm_bwd_workspace_size.restype = i32
+    L.nm_layernorm_bwd_workspace_size.argtypes = [i64, i64, ctypes.POINTER(sz)]
+    L.nm_layernorm_bwd.restype = i32
+    L.nm_layernorm_bwd.argtypes = [vp, i64, vp, i64, i64, i64, i32, vp, vp, vp, vp, i64, vp, vp, i32, vp, sz, vp]
     _lib = L
     return L
 
@@ -603,3 +610,94 @@ def nm_diag_spmm(values, offsets, act, perm=None, out_dtype=None, out=None):
                               T, act.stride(0), perm.data_ptr() if perm is not None else None, out.data_ptr(),
                               out.stride(0), od, _stream_ptr(act.device)))
     return out
+
+
+# --------------------------------------------------------------------------
+# layer norm
+# --------------------------------------------------------------------------
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _norm_code(t) -> int:
+    torch = _torch()
+    if t.dtype == torch.float32:
+        return NM_F32
+    if t.dtype in (torch.float16, torch.bfloat16):
+        return _dtype_code(t)
+    raise TypeError(f"layer norm takes float16, bfloat16 or float32, got {t.dtype}")
+
+
+def _row_stride(t):
+    """Leading dimension of a matrix (a matrix of one row may have any stride)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _vector(t, name, size, dtype, device):
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != (size,) or not t.is_contiguous()
+                          or t.device != device):
+        raise ValueError(f"{name} must be a contiguous {dtype} [{size}] tensor on {device}")
+
+
+def _matrix(t, name, rows, cols, dtype, device):
+    _row_major(t, name)
+    if t.dtype != dtype or tuple(t.shape) != (rows, cols) or t.device != device:
+        raise ValueError(f"{name} must be a [{rows}, {cols}] {dtype} tensor on {device}")
+
+
+def nm_layernorm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool = False, out=None):
+    """Layer norm of each row of x [T, H] (float16, bfloat16 or float32): y, or with
+    stats (y, mean [T], rstd [T]), the fp32 statistics nm_layernorm_bwd reads."""
+    torch = _torch()
+    _row_major(x, "x")
+    dt = _norm_code(x)
+    T, H = x.shape
+    _vector(weight, "weight", H, x.dtype, x.device)
+    _vector(bias, "bias", H, x.dtype, x.device)
+    if out is not None:
+        _matrix(out, "out", T, H, x.dtype, x.device)
+    _require_cuda(x)
+    if out is None:
+        out = torch.empty((T, H), dtype=x.dtype, device=x.device)
+    mean = rstd = None
+    if stats:
+        mean, rstd = torch.empty((2, T), dtype=torch.float32, device=x.device).unbind(0)
+    _check(lib().nm_layernorm(x.data_ptr(), T, H, _row_stride(x), dt, _ptr(weight), _ptr(bias), eps, out.data_ptr(),
+                              _row_stride(out), _ptr(mean), _ptr(rstd), _stream_ptr(x.device)))
+    return (out, mean, rstd) if stats else out
+
+
+def nm_layernorm_bwd(dy, x, mean, rstd, weight=None, out_dtype=None, affine: bool = True, out=None):
+    """(dx, dw, db) of nm_layernorm from dy = dL/dy and the statistics it returned.
+    dw and db are float32 unless out_dtype names x's dtype; affine=False leaves them out
+    (None) for a norm whose weights are frozen."""
+    torch = _torch()
+    _row_major(x, "x")
+    dt = _norm_code(x)
+    T, H = x.shape
+    _matrix(dy, "dy", T, H, x.dtype, x.device)
+    _vector(mean, "mean", T, torch.float32, x.device)
+    _vector(rstd, "rstd", T, torch.float32, x.device)
+    _vector(weight, "weight", H, x.dtype, x.device)
+    if out_dtype not in (None, torch.float32, x.dtype):
+        raise TypeError("out_dtype must be float32 or the dtype of x")
+    od = dt if out_dtype == x.dtype else NM_F32
+    if out is not None:
+        _matrix(out, "out", T, H, x.dtype, x.device)
+    _require_cuda(x)
+    if out is None:
+        out = torch.empty((T, H), dtype=x.dtype, device=x.device)
+    dw = db = ws = None
+    need = 0
+    L = lib()
+    if affine:
+        dw, db = (torch.empty(H, dtype=_torch_dtype(od), device=x.device) for _ in range(2))
+        b = ctypes.c_size_t()
+        _check(L.nm_layernorm_bwd_workspace_size(T, H, ctypes.byref(b)))
+        need = b.value
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    _check(L.nm_layernorm_bwd(dy.data_ptr(), _row_stride(dy), x.data_ptr(), _row_stride(x), T, H, dt, mean.data_ptr(),
+                              rstd.data_ptr(), _ptr(weight), out.data_ptr(), _row_stride(out), _ptr(dw), _ptr(db), od,
+                              _ptr(ws), need, _stream_ptr(x.device)))
+    return out, dw, db

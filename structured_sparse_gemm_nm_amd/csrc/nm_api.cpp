@@ -835,4 +835,122 @@ nm_status nm_diag_spmm(const void* values, const int32_t* offsets, int64_t D, in
   return hip_status(nm::launch_host_spmm(a, static_cast<hipStream_t>(stream)), "nm_diag_spmm launch");
 }
 
+// Shared checks of layer norm: a 16-bit or fp32 matrix [T, H].
+static nm_status check_norm(int64_t T, int64_t H, int dtype) {
+  if (dtype != NM_F16 && dtype != NM_BF16 && dtype != NM_F32)
+    return fail(NM_ERR_UNSUPPORTED, "layer norm takes NM_F16, NM_BF16 or NM_F32, not dtype %d", dtype);
+  if (T < 0 || T > kMaxRT) return fail(NM_ERR_SHAPE, "T = %lld out of range", (long long)T);
+  if (H < 1 || H > kMaxK) return fail(NM_ERR_SHAPE, "H = %lld out of range [1, 2^24]", (long long)H);
+  return NM_OK;
+}
+
+// A leading dimension of a [T, W] matrix.
+static nm_status check_ld(const char* name, int64_t ld, int64_t T, int64_t W) {
+  if (ld < W) return fail(NM_ERR_STRIDE, "%s = %lld < %lld", name, (long long)ld, (long long)W);
+  if (ld > kMaxElems || T * ld > kMaxElems) return fail(NM_ERR_SHAPE, "T*%s too large", name);
+  return NM_OK;
+}
+
+static bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+nm_status nm_layernorm(const void* x, int64_t T, int64_t H, int64_t ldx, int dtype, const void* weight,
+                       const void* bias, float eps, void* y, int64_t ldy, float* mean, float* rstd, void* stream) {
+  nm_status st = check_norm(T, H, dtype);
+  if (st != NM_OK) return st;
+  if (!(eps >= 0.f)) return fail(NM_ERR_SHAPE, "eps = %g is negative or not a number", double(eps));
+  if ((st = check_ld("ldx", ldx, T, H)) != NM_OK || (st = check_ld("ldy", ldy, T, H)) != NM_OK) return st;
+  if (T == 0) return ok();
+  if (!x || !y) return fail(NM_ERR_NULL, "x and y must be non-NULL");
+  if (!mean != !rstd) return fail(NM_ERR_NULL, "mean and rstd go together");
+  const size_t e = elt_bytes(dtype);
+  if (!aligned_to(x, e) || !aligned_to(y, e) || !aligned_to(weight, e) || !aligned_to(bias, e) ||
+      !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+    return fail(NM_ERR_ALIGN, "a pointer is not aligned to its element");
+  const size_t xb = extent(T, H, ldx, e), yb = extent(T, H, ldy, e), wb = size_t(H) * e, sb = size_t(T) * 4;
+  const void* outs[3] = {y, mean, rstd};
+  const size_t outb[3] = {yb, sb, sb};
+  for (int i = 0; i < 3; ++i) {
+    if (overlaps(outs[i], outb[i], x, xb) || overlaps(outs[i], outb[i], weight, wb) ||
+        overlaps(outs[i], outb[i], bias, wb))
+      return fail(NM_ERR_ALIAS, "an output overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (overlaps(outs[i], outb[i], outs[j], outb[j])) return fail(NM_ERR_ALIAS, "outputs overlap each other");
+  }
+  nm::LayerNormArgs a;
+  a.T = T;
+  a.H = H;
+  a.dtype = dtype;
+  a.x = x;
+  a.ldx = ldx;
+  a.weight = weight;
+  a.bias = bias;
+  a.eps = eps;
+  a.y = y;
+  a.ldy = ldy;
+  a.mean_out = mean;
+  a.rstd_out = rstd;
+  return hip_status(nm::launch_layernorm(a, static_cast<hipStream_t>(stream)), "nm_layernorm launch");
+}
+
+nm_status nm_layernorm_bwd_workspace_size(int64_t T, int64_t H, size_t* bytes) {
+  nm_status st = check_norm(T, H, NM_F32);
+  if (st != NM_OK) return st;
+  if (!bytes) return fail(NM_ERR_NULL, "bytes must be non-NULL");
+  *bytes = nm::layernorm_bwd_workspace(T, H);
+  return ok();
+}
+
+nm_status nm_layernorm_bwd(const void* dy, int64_t ldg, const void* x, int64_t ldx, int64_t T, int64_t H, int dtype,
+                           const float* mean, const float* rstd, const void* weight, void* dx, int64_t lddx, void* dw,
+                           void* db, int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  nm_status st = check_norm(T, H, dtype);
+  if (st != NM_OK) return st;
+  if (out_dtype != NM_F32 && out_dtype != dtype)
+    return fail(NM_ERR_UNSUPPORTED, "out_dtype %d must be NM_F32 or the input dtype", out_dtype);
+  if ((st = check_ld("ldg", ldg, T, H)) != NM_OK || (st = check_ld("ldx", ldx, T, H)) != NM_OK ||
+      (st = check_ld("lddx", lddx, T, H)) != NM_OK)
+    return st;
+  const bool sums = dw || db;
+  if (T == 0 && !sums) return ok();
+  if (T > 0 && (!dy || !x || !mean || !rstd || !dx))
+    return fail(NM_ERR_NULL, "dy, x, mean, rstd and dx must be non-NULL");
+  const size_t need = sums ? nm::layernorm_bwd_workspace(T, H) : 0;
+  if (need > 0 && !workspace) return fail(NM_ERR_NULL, "dw and db need a workspace");
+  if (workspace_bytes < need)
+    return fail(NM_ERR_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  const size_t e = elt_bytes(dtype), o = elt_bytes(out_dtype);
+  if (!aligned_to(dy, e) || !aligned_to(x, e) || !aligned_to(dx, e) || !aligned_to(weight, e) ||
+      !aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(dw, o) || !aligned_to(db, o))
+    return fail(NM_ERR_ALIGN, "a pointer is not aligned to its element");
+  if (need > 0 && !aligned16(workspace)) return fail(NM_ERR_ALIGN, "workspace must be 16-byte aligned");
+  const void* ins[5] = {dy, x, mean, rstd, weight};
+  const size_t inb[5] = {extent(T, H, ldg, e), extent(T, H, ldx, e), size_t(T) * 4, size_t(T) * 4, size_t(H) * e};
+  const void* outs[4] = {dx, dw, db, need ? workspace : nullptr};
+  const size_t outb[4] = {extent(T, H, lddx, e), size_t(H) * o, size_t(H) * o, need};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 5; ++j)
+      if (overlaps(outs[i], outb[i], ins[j], inb[j])) return fail(NM_ERR_ALIAS, "an output overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (overlaps(outs[i], outb[i], outs[j], outb[j])) return fail(NM_ERR_ALIAS, "outputs overlap each other");
+  }
+  nm::LayerNormArgs a;
+  a.T = T;
+  a.H = H;
+  a.dtype = dtype;
+  a.x = x;
+  a.ldx = ldx;
+  a.weight = weight;
+  a.dy = dy;
+  a.ldg = ldg;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.dx = dx;
+  a.lddx = lddx;
+  a.dw = dw;
+  a.db = db;
+  a.out_dtype = out_dtype;
+  a.workspace = workspace;
+  return hip_status(nm::launch_layernorm_bwd(a, static_cast<hipStream_t>(stream)), "nm_layernorm_bwd launch");
+}
+
 }  // extern "C"

@@ -160,6 +160,36 @@ hipError_t launch_diag_pack(const uint16_t* W, int64_t ldw, int64_t R, int64_t K
                             uint16_t* values, hipStream_t s);
 hipError_t launch_host_spmm(const HostArgs& a, hipStream_t s);
 
+// Layer norm (nm_layernorm.hip).  Forward: x, weight, bias -> y (and mean_out,
+// rstd_out when given); backward: dy, x, mean, rstd, weight -> dx, dw, db (the
+// last two through partial sums in `workspace`).
+struct LayerNormArgs {
+  int64_t T = 0, H = 0;
+  int dtype = 0;
+  const void* x = nullptr;
+  int64_t ldx = 0;
+  const void* weight = nullptr;
+  const void* bias = nullptr;
+  float eps = 0.f;
+  void* y = nullptr;
+  int64_t ldy = 0;
+  float* mean_out = nullptr;
+  float* rstd_out = nullptr;
+  const void* dy = nullptr;
+  int64_t ldg = 0;
+  const float* mean = nullptr;
+  const float* rstd = nullptr;
+  void* dx = nullptr;
+  int64_t lddx = 0;
+  void* dw = nullptr;
+  void* db = nullptr;
+  int out_dtype = 0;
+  void* workspace = nullptr;
+};
+size_t layernorm_bwd_workspace(int64_t T, int64_t H);
+hipError_t launch_layernorm(const LayerNormArgs& a, hipStream_t s);
+hipError_t launch_layernorm_bwd(const LayerNormArgs& a, hipStream_t s);
+
 // Device properties and per-kernel launch set-up, kept per device and safe to
 // call from several host threads (nm_api.cpp).
 int device_cu_count();                 // CUs of the current device (256 if the query fails)
