@@ -441,6 +441,51 @@ nm_status nm_layernorm_bwd(const void* dy, int64_t ldg, const void* x, int64_t l
                            const float* mean, const float* rstd, const void* weight, void* dx, int64_t lddx, void* dw,
                            void* db, int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Low-rank adapters of many requests beside a shared N:M projection.  Token t
+ * names adapter a = adapter[t]; an entry outside [0, adapters) (-1, say) means
+ * the shared projection alone.
+ *   nm_adapter_spmm:      xa[t] = A_a act[t],
+ *                         Y[t] = W_nm act[t] + scale_a B_a xa[t];
+ *   nm_adapter_spmm_bwd:  with G = dL/dY, W_nm frozen, u[t] = scale_a B_a^T G[t],
+ *                         dX[t] = W_nm^T G[t] + A_a^T u[t],
+ *                         dA_a = sum over a's tokens of u[t] act[t]^T,
+ *                         dB_a = scale_a sum over a's tokens of G[t] xa[t]^T.
+ *   values, idx, act, Y, G, dX   as nm_spmm and nm_spmm_dx (16-bit weights; the
+ *              backward pass with their R % 8 and K % 32); Y and dX in
+ *              out_dtype NM_F32 or the input dtype.
+ *   adapter    device int32 [T], in any order; requests whose tokens are
+ *              adjacent are the fastest.
+ *   A          device [adapters, rank, K],  B  device [adapters, R, rank], dtype
+ *              of the weight, contiguous; 1 <= rank <= 256, 0 <= adapters <=
+ *              65535.  Adapters of several ranks are padded with zeros.
+ *   scale      device fp32 [adapters].
+ *   xa         device fp32 [T, rank]: written by the forward pass (zeros for a
+ *              token without an adapter), read by the backward pass.
+ *   dX         may be NULL (not wanted);  dA, dB  device fp32, shaped as A and B,
+ *              overwritten: an adapter without tokens gets zeros.
+ *   workspace  device, the bytes of the matching _workspace_size, 16-byte aligned.
+ * xa and u stay fp32; between the two low-rank products they enter the matrix
+ * cores as two bf16 parts (off by 2^-16 of the sum of |terms| at most).  Inf or
+ * NaN in one token or adapter reaches the outputs of that token or adapter only.
+ * T <= 2^24, R and K <= 2^22.  Pointers 16-byte aligned (adapter, scale: 4),
+ * ldx and ldg multiples of 8; outputs and workspace must not overlap anything
+ * (NM_ERR_ALIAS).  Stream-ordered; nothing is allocated or synchronised.
+ */
+nm_status nm_adapter_spmm_workspace_size(int64_t R, int64_t K, int n, int m, int dtype, int64_t T, int64_t adapters,
+                                         int64_t rank, int out_dtype, size_t* bytes);
+nm_status nm_adapter_spmm(const void* values, const uint32_t* idx, int64_t R, int64_t K, int n, int m, int dtype,
+                          const void* act, int64_t T, int64_t ldx, const int32_t* adapter, const void* A,
+                          const void* B, const float* scale, int64_t adapters, int64_t rank, float* xa, void* Y,
+                          int64_t ldy, int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+nm_status nm_adapter_spmm_bwd_workspace_size(int64_t R, int64_t K, int n, int m, int dtype, int64_t T,
+                                             int64_t adapters, int64_t rank, int out_dtype, size_t* bytes);
+nm_status nm_adapter_spmm_bwd(const void* values, const uint32_t* idx, int64_t R, int64_t K, int n, int m, int dtype,
+                              const void* G, int64_t T, int64_t ldg, const void* act, int64_t ldx, const float* xa,
+                              const int32_t* adapter, const void* A, const void* B, const float* scale,
+                              int64_t adapters, int64_t rank, void* dX, int64_t lddx, float* dA, float* dB,
+                              int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

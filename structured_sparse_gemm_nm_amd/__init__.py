@@ -18,7 +18,8 @@ __all__ = ["NM_OK", "NM_F16", "NM_BF16", "NM_F32", "NM_I8", "NM_I32", "NM_FP8", 
            "nm_packed_sizes", "nm_compress", "nm_decompress", "nm_spmm", "nm_spmm_perm",
            "nm_spmm_perm_workspace_size", "nm_spmm_perm_static", "nm_check_perm", "nm_spmm_dx", "nm_spmm_dw",
            "nm_hybrid_layout", "nm_hybrid_compress", "nm_hybrid_spmm", "nm_block_structure", "nm_block_compress",
-           "nm_block_spmm", "nm_diag_compress", "nm_diag_spmm", "nm_layernorm", "nm_layernorm_bwd", "PATTERNS"]
+           "nm_block_spmm", "nm_diag_compress", "nm_diag_spmm", "nm_layernorm", "nm_layernorm_bwd", "nm_adapter_spmm",
+           "nm_adapter_spmm_bwd", "PATTERNS"]
 
 NM_OK = 0
 NM_F16, NM_BF16, NM_F32, NM_I8, NM_I32, NM_FP8 = 0, 1, 2, 3, 4, 5
@@ -103,6 +104,15 @@ def lib() -> ctypes.CDLL:
     L.nm_layernorm_bwd_workspace_size.argtypes = [i64, i64, ctypes.POINTER(sz)]
     L.nm_layernorm_bwd.restype = i32
     L.nm_layernorm_bwd.argtypes = [vp, i64, vp, i64, i64, i64, i32, vp, vp, vp, vp, i64, vp, vp, i32, vp, sz, vp]
+    for f in (L.nm_adapter_spmm_workspace_size, L.nm_adapter_spmm_bwd_workspace_size):
+        f.restype = i32
+        f.argtypes = [i64, i64, i32, i32, i32, i64, i64, i64, i32, ctypes.POINTER(sz)]
+    L.nm_adapter_spmm.restype = i32
+    L.nm_adapter_spmm.argtypes = [vp, vp, i64, i64, i32, i32, i32, vp, i64, i64, vp, vp, vp, vp, i64, i64, vp, vp, i64,
+                                  i32, vp, sz, vp]
+    L.nm_adapter_spmm_bwd.restype = i32
+    L.nm_adapter_spmm_bwd.argtypes = [vp, vp, i64, i64, i32, i32, i32, vp, i64, i64, vp, i64, vp, vp, vp, vp, vp, i64,
+                                      i64, vp, i64, vp, vp, i32, vp, sz, vp]
     _lib = L
     return L
 
@@ -630,8 +640,8 @@ def _norm_code(t) -> int:
 
 
 def _row_stride(t):
-    """Leading dimension of a matrix (a matrix of one row may have any stride)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    """Leading dimension of a matrix (torch gives a matrix of one row any stride)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def _vector(t, name, size, dtype, device):
@@ -701,3 +711,89 @@ def nm_layernorm_bwd(dy, x, mean, rstd, weight=None, out_dtype=None, affine: boo
                               rstd.data_ptr(), _ptr(weight), out.data_ptr(), _row_stride(out), _ptr(dw), _ptr(db), od,
                               _ptr(ws), need, _stream_ptr(x.device)))
     return out, dw, db
+
+
+# --------------------------------------------------------------------------
+# low-rank adapters beside a shared projection
+# --------------------------------------------------------------------------
+
+def _check_adapters(values, idx, act, adapter, A, B, scale, K, n, m, dt):
+    """Tensors of both passes; returns (R, T, adapters, rank)."""
+    torch = _torch()
+    R, T = values.shape[0], act.shape[0]
+    _check_packed(values, idx, R, K, n, m, dt)
+    _matrix(act, "act", T, K, values.dtype, values.device)
+    _vector(adapter, "adapter", T, torch.int32, values.device)
+    if A.dim() != 3 or A.shape[2] != K or A.dtype != values.dtype or not A.is_contiguous() \
+            or A.device != values.device:
+        raise ValueError(f"A must be a contiguous [adapters, rank, {K}] {values.dtype} tensor on {values.device}")
+    na, r = A.shape[0], A.shape[1]
+    if tuple(B.shape) != (na, R, r) or B.dtype != values.dtype or not B.is_contiguous() or B.device != values.device:
+        raise ValueError(f"B must be a contiguous [{na}, {R}, {r}] {values.dtype} tensor on {values.device}")
+    _vector(scale, "scale", na, torch.float32, values.device)
+    _require_cuda(values, idx, act, adapter, A, B, scale)
+    return R, T, na, r
+
+
+def _workspace(size_of, *args, device):
+    b = ctypes.c_size_t()
+    _check(size_of(*args, ctypes.byref(b)))
+    return (_torch().empty(b.value, dtype=_torch().uint8, device=device) if b.value else None), b.value
+
+
+def nm_adapter_spmm(values, idx, act, adapter, A, B, scale, K: int, n: int = 2, m: int = 4, out_dtype=None, out=None,
+                    xa=None):
+    """(Y [T, R], xa [T, rank]): Y[t] = W_nm act[t] + scale[a] B[a] xa[t], xa[t] = A[a] act[t], with
+    a = adapter[t] the token's own low-rank adapter (outside [0, adapters): none, xa zeros).
+    A [adapters, rank, K], B [adapters, R, rank] in the weights' dtype; scale float32 [adapters];
+    xa float32, kept for nm_adapter_spmm_bwd."""
+    torch = _torch()
+    _row_major(act, "act")
+    dt = _dtype_code(values)
+    od = _train_out_dtype(torch, dt, out_dtype)
+    R, T, na, r = _check_adapters(values, idx, act, adapter, A, B, scale, K, n, m, dt)
+    if out is not None:
+        _matrix(out, "out", T, R, _torch_dtype(od), act.device)
+    else:
+        out = torch.empty((T, R), dtype=_torch_dtype(od), device=act.device)
+    if xa is None:
+        xa = torch.empty((T, r), dtype=torch.float32, device=act.device)
+    elif xa.dtype != torch.float32 or tuple(xa.shape) != (T, r) or not xa.is_contiguous() or xa.device != act.device:
+        raise ValueError(f"xa must be a contiguous float32 [{T}, {r}] tensor on {act.device}")
+    L = lib()
+    ws, need = _workspace(L.nm_adapter_spmm_workspace_size, R, K, n, m, dt, T, na, r, od, device=act.device)
+    _check(L.nm_adapter_spmm(values.data_ptr(), idx.data_ptr(), R, K, n, m, dt, act.data_ptr(), T, _row_stride(act),
+                             adapter.data_ptr(), A.data_ptr(), B.data_ptr(), scale.data_ptr(), na, r, xa.data_ptr(),
+                             out.data_ptr(), _row_stride(out), od, _ptr(ws), need, _stream_ptr(act.device)))
+    return out, xa
+
+
+def nm_adapter_spmm_bwd(values, idx, G, act, xa, adapter, A, B, scale, K: int, n: int = 2, m: int = 4, out_dtype=None,
+                        need_dx: bool = True, out=None):
+    """(dX [T, K], dA, dB) of nm_adapter_spmm from G = dL/dY [T, R], the packed weight frozen.  dX is
+    float32 or out_dtype (None with need_dx=False); dA and dB are float32, zeros for an adapter no
+    token uses."""
+    torch = _torch()
+    _row_major(act, "act")
+    dt = _dtype_code(values)
+    od = _train_out_dtype(torch, dt, out_dtype)
+    R, T, na, r = _check_adapters(values, idx, act, adapter, A, B, scale, K, n, m, dt)
+    _matrix(G, "G", T, R, values.dtype, values.device)
+    if xa.dtype != torch.float32 or tuple(xa.shape) != (T, r) or not xa.is_contiguous() or xa.device != act.device:
+        raise ValueError(f"xa must be a contiguous float32 [{T}, {r}] tensor on {act.device}")
+    if not need_dx:
+        out = None
+    elif out is not None:
+        _matrix(out, "out", T, K, _torch_dtype(od), act.device)
+    else:
+        out = torch.empty((T, K), dtype=_torch_dtype(od), device=act.device)
+    dA = torch.empty((na, r, K), dtype=torch.float32, device=act.device)
+    dB = torch.empty((na, R, r), dtype=torch.float32, device=act.device)
+    L = lib()
+    ws, need = _workspace(L.nm_adapter_spmm_bwd_workspace_size, R, K, n, m, dt, T, na, r, od, device=act.device)
+    _check(L.nm_adapter_spmm_bwd(values.data_ptr(), idx.data_ptr(), R, K, n, m, dt, G.data_ptr(), T, _row_stride(G),
+                                 act.data_ptr(), _row_stride(act), xa.data_ptr(), adapter.data_ptr(), A.data_ptr(),
+                                 B.data_ptr(), scale.data_ptr(), na, r, _ptr(out),
+                                 _row_stride(out) if out is not None else K, dA.data_ptr(), dB.data_ptr(), od,
+                                 _ptr(ws), need, _stream_ptr(act.device)))
+    return out, dA, dB

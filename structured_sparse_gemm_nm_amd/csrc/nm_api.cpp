@@ -95,6 +95,25 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   return a0 < b0 + nb && b0 < a0 + na;
 }
 
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+
+// NM_ERR_ALIAS if an output overlaps an input or another output.
+template <int NI, int NO>
+nm_status check_alias(const Span (&in)[NI], const Span (&out)[NO]) {
+  for (int i = 0; i < NO; ++i) {
+    for (int j = 0; j < NI; ++j)
+      if (overlaps(out[i].p, out[i].bytes, in[j].p, in[j].bytes))
+        return fail(NM_ERR_ALIAS, "an output overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+        return fail(NM_ERR_ALIAS, "outputs or workspace overlap each other");
+  }
+  return NM_OK;
+}
+
 nm_status hip_status(hipError_t e, const char* what) {
   if (e == hipSuccess) return ok();
   return fail(NM_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
@@ -951,6 +970,163 @@ nm_status nm_layernorm_bwd(const void* dy, int64_t ldg, const void* x, int64_t l
   a.out_dtype = out_dtype;
   a.workspace = workspace;
   return hip_status(nm::launch_layernorm_bwd(a, static_cast<hipStream_t>(stream)), "nm_layernorm_bwd launch");
+}
+
+// Shared checks of the adapters: the packed weight (16-bit), the token count,
+// the adapters' sizes and the output type.
+static nm_status check_adapter(int64_t R, int64_t K, int n, int m, int dtype, int64_t T, int64_t adapters,
+                               int64_t rank, int out_dtype) {
+  nm_status st = check_format(R, K, n, m, dtype);
+  if (st != NM_OK) return st;
+  if (dtype != NM_F16 && dtype != NM_BF16) return fail(NM_ERR_UNSUPPORTED, "adapters take fp16 or bf16 weights");
+  if (out_dtype != NM_F32 && out_dtype != dtype)
+    return fail(NM_ERR_UNSUPPORTED, "out_dtype %d must be NM_F32 or the input dtype", out_dtype);
+  if (T < 0 || T > nm::kAdapterMaxTokens)
+    return fail(NM_ERR_SHAPE, "T = %lld out of range [0, 2^24]", (long long)T);
+  if (R > nm::kAdapterMaxWidth || K > nm::kAdapterMaxWidth)
+    return fail(NM_ERR_SHAPE, "R = %lld or K = %lld above 2^22", (long long)R, (long long)K);
+  if (rank < 1 || rank > nm::kAdapterMaxRank)
+    return fail(NM_ERR_SHAPE, "rank = %lld out of range [1, %lld]", (long long)rank, (long long)nm::kAdapterMaxRank);
+  if (adapters < 0 || adapters > nm::kAdapterMaxCount)
+    return fail(NM_ERR_SHAPE, "adapters = %lld out of range [0, %lld]", (long long)adapters,
+                (long long)nm::kAdapterMaxCount);
+  return NM_OK;
+}
+
+nm_status nm_adapter_spmm_workspace_size(int64_t R, int64_t K, int n, int m, int dtype, int64_t T, int64_t adapters,
+                                         int64_t rank, int out_dtype, size_t* bytes) {
+  nm_status st = check_adapter(R, K, n, m, dtype, T, adapters, rank, out_dtype);
+  if (st != NM_OK) return st;
+  if (!bytes) return fail(NM_ERR_NULL, "bytes must be non-NULL");
+  *bytes = nm::adapter_workspace(R, T, out_dtype);
+  return ok();
+}
+
+nm_status nm_adapter_spmm(const void* values, const uint32_t* idx, int64_t R, int64_t K, int n, int m, int dtype,
+                          const void* act, int64_t T, int64_t ldx, const int32_t* adapter, const void* A,
+                          const void* B, const float* scale, int64_t adapters, int64_t rank, float* xa, void* Y,
+                          int64_t ldy, int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  nm_status st = check_adapter(R, K, n, m, dtype, T, adapters, rank, out_dtype);
+  if (st != NM_OK) return st;
+  if ((st = check_ld("ldx", ldx, T, K)) != NM_OK || (st = check_ld("ldy", ldy, T, R)) != NM_OK) return st;
+  if (T == 0) return ok();
+  if (!act || !adapter || !xa || (R > 0 && (!values || !idx || !Y)) || (adapters > 0 && (!A || !scale)) ||
+      (adapters > 0 && R > 0 && !B))
+    return fail(NM_ERR_NULL, "values, idx, act, adapter, A, B, scale, xa and Y must be non-NULL");
+  if (ldx % 8) return fail(NM_ERR_ALIGN, "ldx = %lld is not a multiple of 8", (long long)ldx);
+  if (!aligned16(values) || !aligned16(idx) || !aligned16(act) || !aligned16(Y) || !aligned16(A) || !aligned16(B) ||
+      !aligned16(xa) || !aligned16(workspace) || !aligned_to(adapter, 4) || !aligned_to(scale, 4))
+    return fail(NM_ERR_ALIGN, "device pointers must be 16-byte aligned (adapter and scale: 4)");
+  const size_t need = nm::adapter_workspace(R, T, out_dtype);
+  if (need > 0 && !workspace) return fail(NM_ERR_NULL, "workspace must be non-NULL");
+  if (workspace_bytes < need)
+    return fail(NM_ERR_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  const Sizes z = sizes_of(R, K, n, m, dtype);
+  const size_t ab = size_t(adapters) * size_t(rank) * size_t(K) * 2, bb = size_t(adapters) * size_t(rank) * size_t(R) * 2;
+  const Span in[] = {{values, z.values_bytes}, {idx, z.idx_bytes}, {act, extent(T, K, ldx, 2)},
+                     {adapter, size_t(T) * 4}, {A, ab}, {B, bb}, {scale, size_t(adapters) * 4}};
+  const Span out[] = {{Y, extent(T, R, ldy, elt_bytes(out_dtype))}, {xa, size_t(T) * size_t(rank) * 4},
+                      {workspace, need}};
+  if ((st = check_alias(in, out)) != NM_OK) return st;
+  nm::AdapterArgs a;
+  a.base.values = static_cast<const uint16_t*>(values);
+  a.base.idx = idx;
+  a.base.R = R;
+  a.base.K = K;
+  a.base.n = n;
+  a.base.m = m;
+  a.base.dtype = dtype;
+  a.base.act = static_cast<const uint16_t*>(act);
+  a.base.T = T;
+  a.base.ldx = ldx;
+  a.base.Y = Y;
+  a.base.ldy = ldy;
+  a.base.out_dtype = out_dtype;
+  a.base.idx_row_words = z.words;
+  a.ids = adapter;
+  a.n = adapters;
+  a.r = rank;
+  a.A = static_cast<const uint16_t*>(A);
+  a.B = static_cast<const uint16_t*>(B);
+  a.scale = scale;
+  a.xa = xa;
+  a.workspace = workspace;
+  return hip_status(nm::launch_adapter(a, static_cast<hipStream_t>(stream)), "nm_adapter_spmm launch");
+}
+
+nm_status nm_adapter_spmm_bwd_workspace_size(int64_t R, int64_t K, int n, int m, int dtype, int64_t T,
+                                             int64_t adapters, int64_t rank, int out_dtype, size_t* bytes) {
+  nm_status st = check_adapter(R, K, n, m, dtype, T, adapters, rank, out_dtype);
+  if (st != NM_OK) return st;
+  if (!bytes) return fail(NM_ERR_NULL, "bytes must be non-NULL");
+  *bytes = nm::adapter_bwd_workspace(K, T, rank, out_dtype);
+  return ok();
+}
+
+nm_status nm_adapter_spmm_bwd(const void* values, const uint32_t* idx, int64_t R, int64_t K, int n, int m, int dtype,
+                              const void* G, int64_t T, int64_t ldg, const void* act, int64_t ldx, const float* xa,
+                              const int32_t* adapter, const void* A, const void* B, const float* scale,
+                              int64_t adapters, int64_t rank, void* dX, int64_t lddx, float* dA, float* dB,
+                              int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  nm_status st = check_train(R, K, n, m, dtype, T, ldg, out_dtype);
+  if (st != NM_OK) return st;
+  if ((st = check_adapter(R, K, n, m, dtype, T, adapters, rank, out_dtype)) != NM_OK) return st;
+  if ((st = check_ld("ldg", ldg, T, R)) != NM_OK || (st = check_ld("ldx", ldx, T, K)) != NM_OK) return st;
+  if (dX && (st = check_ld("lddx", lddx, T, K)) != NM_OK) return st;
+  if (T == 0 && adapters == 0) return ok();
+  if (T > 0 && (!act || !xa || !adapter || !workspace || (R > 0 && (!G || !values || !idx))))
+    return fail(NM_ERR_NULL, "values, idx, G, act, xa, adapter and workspace must be non-NULL");
+  if (adapters > 0 && (!A || !scale || !dA || (R > 0 && (!B || !dB))))
+    return fail(NM_ERR_NULL, "A, B, scale, dA and dB must be non-NULL");
+  if (ldg % 8 || ldx % 8) return fail(NM_ERR_ALIGN, "ldg and ldx must be multiples of 8");
+  if (!aligned16(values) || !aligned16(idx) || !aligned16(G) || !aligned16(act) || !aligned16(xa) || !aligned16(A) ||
+      !aligned16(B) || !aligned16(dX) || !aligned16(dA) || !aligned16(dB) || !aligned16(workspace) ||
+      !aligned_to(adapter, 4) || !aligned_to(scale, 4))
+    return fail(NM_ERR_ALIGN, "device pointers must be 16-byte aligned (adapter and scale: 4)");
+  const size_t need = nm::adapter_bwd_workspace(K, T, rank, out_dtype);
+  if (T > 0 && workspace_bytes < need)
+    return fail(NM_ERR_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  const Sizes z = sizes_of(R, K, n, m, dtype);
+  // nm_spmm_dx's limits
+  if (z.values_bytes >= (size_t(1) << 32) || z.idx_bytes >= (size_t(1) << 32) || 128 * ldg * 2 >= (int64_t(1) << 32))
+    return fail(NM_ERR_SHAPE, "packed W of 4 GiB or more, or ldg of 2^24 or more");
+  const size_t ab = size_t(adapters) * size_t(rank) * size_t(K), bb = size_t(adapters) * size_t(rank) * size_t(R);
+  const Span in[] = {{values, z.values_bytes}, {idx, z.idx_bytes}, {G, extent(T, R, ldg, 2)},
+                     {act, extent(T, K, ldx, 2)}, {xa, size_t(T) * size_t(rank) * 4}, {adapter, size_t(T) * 4},
+                     {A, ab * 2}, {B, bb * 2}, {scale, size_t(adapters) * 4}};
+  const Span out[] = {{dX, dX ? extent(T, K, lddx, elt_bytes(out_dtype)) : 0}, {dA, ab * 4}, {dB, bb * 4},
+                      {workspace, T > 0 ? need : 0}};
+  if ((st = check_alias(in, out)) != NM_OK) return st;
+  nm::AdapterBwdArgs a;
+  a.dx.values = static_cast<const uint16_t*>(values);
+  a.dx.values_bytes = z.values_bytes;
+  a.dx.idx = idx;
+  a.dx.idx_bytes = z.idx_bytes;
+  a.dx.R = R;
+  a.dx.K = K;
+  a.dx.n = n;
+  a.dx.m = m;
+  a.dx.dtype = dtype;
+  a.dx.idx_row_words = z.words;
+  a.dx.G = static_cast<const uint16_t*>(G);
+  a.dx.T = T;
+  a.dx.ldg = ldg;
+  a.dx.act = static_cast<const uint16_t*>(act);
+  a.dx.ldx = ldx;
+  a.dx.out = dX;
+  a.dx.ldo = lddx;
+  a.dx.out_dtype = out_dtype;
+  a.ids = adapter;
+  a.n = adapters;
+  a.r = rank;
+  a.A = static_cast<const uint16_t*>(A);
+  a.B = static_cast<const uint16_t*>(B);
+  a.scale = scale;
+  a.xa = xa;
+  a.dA = dA;
+  a.dB = dB;
+  a.workspace = workspace;
+  return hip_status(nm::launch_adapter_bwd(a, static_cast<hipStream_t>(stream)), "nm_adapter_spmm_bwd launch");
 }
 
 }  // extern "C"

@@ -160,6 +160,38 @@ hipError_t launch_diag_pack(const uint16_t* W, int64_t ldw, int64_t R, int64_t K
                             uint16_t* values, hipStream_t s);
 hipError_t launch_host_spmm(const HostArgs& a, hipStream_t s);
 
+// Low-rank adapters beside an N:M product (nm_adapter.hip).
+struct AdapterArgs {
+  SpmmArgs base{};                  // the shared product, Y the final output
+  const int32_t* ids = nullptr;     // [T]
+  int64_t n = 0, r = 0;             // adapters, rank
+  const uint16_t* A = nullptr;      // [n][r][K]
+  const uint16_t* B = nullptr;      // [n][R][r]
+  const float* scale = nullptr;     // [n]
+  float* xa = nullptr;              // [T][r] (written)
+  void* workspace = nullptr;        // adapter_workspace bytes
+};
+struct AdapterBwdArgs {
+  TrainArgs dx{};                   // G, act and dX (out, may be null)
+  const int32_t* ids = nullptr;
+  int64_t n = 0, r = 0;
+  const uint16_t* A = nullptr;
+  const uint16_t* B = nullptr;
+  const float* scale = nullptr;
+  const float* xa = nullptr;
+  float* dA = nullptr;              // [n][r][K]
+  float* dB = nullptr;              // [n][R][r]
+  void* workspace = nullptr;        // adapter_bwd_workspace bytes
+};
+constexpr int64_t kAdapterMaxRank = 256, kAdapterMaxCount = 65535;
+constexpr int64_t kAdapterMaxTokens = int64_t(1) << 24, kAdapterMaxWidth = int64_t(1) << 22;   // grid limits
+// Elements of the backward workspace's first part (u, padded to 16 bytes).
+inline int64_t adapter_u_elems(int64_t T, int64_t r) { return (T * r + 3) / 4 * 4; }
+size_t adapter_workspace(int64_t R, int64_t T, int out_dtype);
+size_t adapter_bwd_workspace(int64_t K, int64_t T, int64_t r, int out_dtype);
+hipError_t launch_adapter(const AdapterArgs& a, hipStream_t s);
+hipError_t launch_adapter_bwd(const AdapterBwdArgs& a, hipStream_t s);
+
 // Layer norm (nm_layernorm.hip).  Forward: x, weight, bias -> y (and mean_out,
 // rstd_out when given); backward: dy, x, mean, rstd, weight -> dx, dw, db (the
 // last two through partial sums in `workspace`).

@@ -1,0 +1,143 @@
+// The low-rank term of a token tile on the matrix cores, shared by the kernels
+// that add it to a product they hold in registers.
+//
+//   D[c][t] = s_a sum_j M_a[c][j] V[t][j],   a = ids[t],
+//
+// for the 16 tokens of a fragment and any number of 16-column fragments.  V is
+// fp32 (the shrunk activations or gradients).  The matrix cores take 16-bit
+// operands, so V is split into two bf16 parts, hi + lo, which keep 16 of its 24
+// bits (the term is off by at most 2^-16 of sum |M V|); an fp16 M is split the
+// same way, exactly, since bf16's exponent range covers fp16's and 8 + 8 bits
+// its 11.  bf16 throughout also means that no V, however large or small,
+// leaves the operand's range.
+#pragma once
+
+#include "nm_device.h"
+
+namespace nm {
+
+struct LowRank {
+  const int32_t* ids = nullptr;   // [T]: the token's adapter; outside [0, n): none
+  const uint16_t* M = nullptr;    // [n][C][r], or [n][r][C] (TRANS)
+  const float* scale = nullptr;   // [n], or null: 1
+  const float* V = nullptr;       // [T][r]
+  int n = 0, r = 0, T = 0;
+  int C = 0;                      // columns of the product
+};
+
+// Eight floats as bf16 operand halves hi and lo, hi + lo ~ f.  A part that is
+// not finite (f infinite, NaN, or rounded up to infinity) stays in hi alone.
+__device__ inline void split8(const float (&f)[8], u32x4& hi, u32x4& lo) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t h = pack_half2<NM_BF16>(f[2 * e], f[2 * e + 1]);
+    float l0 = f[2 * e] - __builtin_bit_cast(float, h << 16);
+    float l1 = f[2 * e + 1] - __builtin_bit_cast(float, h & 0xFFFF0000u);
+    l0 = fabsf(l0) < __builtin_inff() ? l0 : 0.f;
+    l1 = fabsf(l1) < __builtin_inff() ? l1 : 0.f;
+    hi[e] = h;
+    lo[e] = pack_half2<NM_BF16>(l0, l1);
+  }
+}
+
+// A 16-bit operand as bf16 parts: bf16 as it is, fp16 split exactly.
+template <int DT>
+__device__ inline void operand_parts(const u32x4& raw, u32x4& hi, u32x4& lo) {
+  if constexpr (DT == NM_BF16) {
+    hi = raw;
+  } else {
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = half_to_f32<DT>((raw[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+    split8(f, hi, lo);
+  }
+}
+
+// acc += M x V with both operands in parts (lo x lo is below the kept bits
+// when M is bf16; an fp16 M's lo part is needed against both).
+template <int DT>
+__device__ inline f32x4 mfma_parts(const u32x4& mh, const u32x4& ml, const u32x4& vh, const u32x4& vl, f32x4 acc) {
+  acc = mfma32<NM_BF16>(mh, vl, acc);
+  if constexpr (DT == NM_F16) {
+    acc = mfma32<NM_BF16>(ml, vl, acc);
+    acc = mfma32<NM_BF16>(ml, vh, acc);
+  }
+  return mfma32<NM_BF16>(mh, vh, acc);
+}
+
+// Operand lane (row c, quarter q) of M: elements j0 .. j0 + 7 (zeros past r).
+// TRANS: M is [r][C], the lane's elements lie C apart.
+template <bool TRANS>
+__device__ inline u32x4 lowrank_operand(const uint16_t* Ma, int c, int64_t C, int j0, int r) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (j0 >= r) return v;
+  if constexpr (TRANS) {
+    const uint16_t* p = Ma + int64_t(j0) * C + c;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t x = j0 + e < r ? p[int64_t(e) * C] : 0u;
+      v[e >> 1] |= x << (16 * (e & 1));
+    }
+  } else {
+    const uint16_t* p = Ma + int64_t(c) * r + j0;
+    if ((r & 7) == 0) {
+      v = *reinterpret_cast<const u32x4*>(p);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t x = j0 + e < r ? p[e] : 0u;
+        v[e >> 1] |= x << (16 * (e & 1));
+      }
+    }
+  }
+  return v;
+}
+
+// Calls add(f, d, mine) for every adapter that occurs among tokens t0 .. t0+15
+// and every fragment f < F (columns c0 + 16 f ..): d the fragment of the term, in
+// the matrix cores' result layout (lane (t, q): columns 4q .. 4q+3 of token t),
+// mine true where the lane's token uses that adapter.  The term of a token
+// that does not use the adapter is whatever the product gives, Inf and NaN
+// among it, so callers select on `mine` and never multiply by a mask.
+// Columns past C reread column C - 1.
+template <int DT, bool TRANS, int F, typename Add>
+__device__ inline void lowrank_term(const LowRank& p, int t0, int c0, Add&& add) {
+  const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
+  const int t = t0 + li;
+  const int id = t < p.T ? p.ids[t] : -1;
+  uint32_t todo = uint32_t(__ballot(uint32_t(id) < uint32_t(p.n))) & 0xFFFFu;
+  const float* vrow = p.V + int64_t(min(t, p.T - 1)) * p.r;
+  while (todo) {
+    const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+    const bool mine = id == a;
+    todo &= ~uint32_t(__ballot(mine));
+    const uint16_t* Ma = p.M + int64_t(a) * p.r * p.C;
+    f32x4 d[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f) d[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < p.r; j += 32) {
+      const int j0 = j + 8 * lq;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = j0 + e < p.r ? vrow[j0 + e] : 0.f;
+      u32x4 vh, vl;
+      split8(v, vh, vl);
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const int c = min(c0 + 16 * f + li, p.C - 1);
+        u32x4 mh, ml;
+        operand_parts<DT>(lowrank_operand<TRANS>(Ma, c, p.C, j0, p.r), mh, ml);
+        d[f] = mfma_parts<DT>(mh, ml, vh, vl, d[f]);
+      }
+    }
+    const float s = p.scale ? p.scale[a] : 1.f;
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[f][e] *= s;
+      add(f, d[f], mine);
+    }
+  }
+}
+
+}  // namespace nm

@@ -52,3 +52,48 @@ def test_layernorm_workspace_size():
     assert f(4, 64, ctypes.byref(b)) == OK and b.value >= 64 * 8
     assert f(1 << 20, 4096, ctypes.byref(b)) == OK and b.value <= 1 << 26
     assert f(-1, 64, ctypes.byref(b)) == SHAPE and f(4, 64, None) == NULL
+
+
+def adapter(values=P, idx=2 * P, R=64, K=64, n=2, m=4, dt=nm.NM_BF16, act=3 * P, T=4, ldx=64, ids=4 * P, A=5 * P,
+            B=6 * P, scale=7 * P, na=3, r=8, xa=8 * P, Y=9 * P, ldy=64, od=nm.NM_BF16, ws=10 * P, wsb=1 << 20):
+    return nm.lib().nm_adapter_spmm(values, idx, R, K, n, m, dt, act, T, ldx, ids, A, B, scale, na, r, xa, Y, ldy, od,
+                                    ws, wsb, None)
+
+
+def adapter_bwd(values=P, idx=2 * P, R=64, K=64, n=2, m=4, dt=nm.NM_BF16, G=11 * P, ldg=64, act=3 * P, T=4, ldx=64,
+                xa=8 * P, ids=4 * P, A=5 * P, B=6 * P, scale=7 * P, na=3, r=8, dX=9 * P, lddx=64, dA=12 * P, dB=13 * P,
+                od=nm.NM_BF16, ws=10 * P, wsb=1 << 20):
+    return nm.lib().nm_adapter_spmm_bwd(values, idx, R, K, n, m, dt, G, T, ldg, act, ldx, xa, ids, A, B, scale, na, r,
+                                        dX, lddx, dA, dB, od, ws, wsb, None)
+
+
+def test_adapter_errors():
+    for name in ("values", "idx", "act", "ids", "A", "B", "scale", "xa", "Y"):
+        assert adapter(**{name: None}) == NULL, name
+    assert adapter(dt=nm.NM_I8) == UNSUPPORTED and adapter(od=nm.NM_F16) == UNSUPPORTED and adapter(n=3) == UNSUPPORTED
+    assert adapter(r=0) == SHAPE and adapter(r=257) == SHAPE and adapter(na=-1) == SHAPE and adapter(na=65536) == SHAPE
+    assert adapter(T=(1 << 24) + 1) == SHAPE and adapter(T=-1) == SHAPE and adapter(K=40, ldx=40) == SHAPE
+    assert adapter(R=1 << 23, ldy=1 << 23) == SHAPE
+    assert adapter(ldx=56) == STRIDE and adapter(ldy=63) == STRIDE and adapter(ldx=68) == ALIGN
+    assert adapter(A=5 * P + 8) == ALIGN and adapter(ids=4 * P + 2) == ALIGN and adapter(xa=8 * P + 4) == ALIGN
+    assert adapter(Y=3 * P) == ALIAS and adapter(xa=9 * P) == ALIAS and adapter(Y=7 * P) == ALIAS
+    assert adapter(T=0, values=None, idx=None, act=None, ids=None, xa=None, Y=None) == OK
+
+
+def test_adapter_bwd_errors():
+    for name in ("values", "idx", "G", "act", "ids", "A", "B", "scale", "xa", "dA", "dB", "ws"):
+        assert adapter_bwd(**{name: None}) == NULL, name
+    assert adapter_bwd(R=60, ldg=64) == SHAPE and adapter_bwd(K=48) == SHAPE and adapter_bwd(wsb=16) == SHAPE
+    assert adapter_bwd(od=nm.NM_F16) == UNSUPPORTED and adapter_bwd(dt=nm.NM_FP8) == UNSUPPORTED
+    assert adapter_bwd(ldg=56) == STRIDE and adapter_bwd(lddx=56) == STRIDE and adapter_bwd(ldx=68) == ALIGN
+    assert adapter_bwd(dA=5 * P) == ALIAS and adapter_bwd(dB=12 * P) == ALIAS and adapter_bwd(dX=11 * P) == ALIAS
+    assert adapter_bwd(dA=12 * P + 4) == ALIGN
+    assert adapter_bwd(T=0, na=0, A=None, B=None, scale=None, dA=None, dB=None, G=None, act=None) == OK
+
+
+def test_adapter_workspace_sizes():
+    b = ctypes.c_size_t()
+    for f in (nm.lib().nm_adapter_spmm_workspace_size, nm.lib().nm_adapter_spmm_bwd_workspace_size):
+        assert f(64, 64, 2, 4, nm.NM_BF16, 16, 3, 8, nm.NM_BF16, ctypes.byref(b)) == OK
+        assert f(64, 64, 2, 4, nm.NM_BF16, 16, 3, 8, nm.NM_F16, ctypes.byref(b)) == UNSUPPORTED
+        assert f(64, 64, 2, 4, nm.NM_BF16, 16, 3, 8, nm.NM_BF16, None) == NULL
