@@ -486,6 +486,43 @@ nm_status nm_adapter_spmm_bwd(const void* values, const uint32_t* idx, int64_t R
                               int64_t adapters, int64_t rank, void* dX, int64_t lddx, float* dA, float* dB,
                               int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Softmax cross entropy over a large vocabulary, the logits never kept: the
+ * head and the loss of a model whose layers are retrained (the head itself
+ * stays dense).  With l[t][v] = sum_h x[t][h] w[v][h]:
+ *   nm_xent:      lse[t] = log sum_v exp l[t][v],  loss[t] = lse[t] - l[t][labels[t]];
+ *   nm_xent_bwd:  d[t][v] = dloss[t] (exp(l[t][v] - lse[t]) - [v == labels[t]]),
+ *                 dx[t][h] = sum_v d[t][v] w[v][h],  dw[v][h] = sum_t d[t][v] x[t][h].
+ *   x, w       device [T, H] and [V, H] row-major, NM_F16 or NM_BF16, H % 8 == 0,
+ *              ldx, ldw >= H and multiples of 8, below 2^23.
+ *   labels     device int32 [T]; a label outside [0, V) (-100, say) is ignored:
+ *              loss 0, no gradient, lse still written.
+ *   loss, lse  device fp32 [T];  dloss  device fp32 [T], dL/dloss (1 over the
+ *              count of labels for a mean).
+ *   dx, dw     device, NM_F32 or the input dtype each (dx_dtype, dw_dtype),
+ *              lddx, lddw >= H and multiples of 4; either may be NULL (not
+ *              wanted).  T == 0 writes zeros to dw.
+ *   workspace  device, the bytes of the matching _workspace_size (the backward
+ *              pass: for the same choice of dx and dw), 16-byte aligned.
+ * Logits, statistics and sums are fp32.  The backward pass walks the vocabulary
+ * in pieces and computes the logits again; d is rounded to the inputs' 16-bit
+ * type before its two products (relative 2^-8 in bf16, 2^-11 in fp16 an
+ * element; fp16 scaled by a power of two against underflow).
+ * T <= 2^22, V <= 2^24, H <= 2^20.  Matrices and workspace 16-byte aligned, vectors 4;
+ * outputs and workspace must not overlap anything (NM_ERR_ALIAS).
+ * Stream-ordered; nothing is allocated or synchronised.
+ */
+nm_status nm_xent_workspace_size(int64_t T, int64_t V, int64_t H, int dtype, size_t* bytes);
+nm_status nm_xent(const void* x, int64_t T, int64_t H, int64_t ldx, const void* w, int64_t V, int64_t ldw, int dtype,
+                  const int32_t* labels, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                  void* stream);
+nm_status nm_xent_bwd_workspace_size(int64_t T, int64_t V, int64_t H, int dtype, int need_dx, int need_dw,
+                                     size_t* bytes);
+nm_status nm_xent_bwd(const void* x, int64_t T, int64_t H, int64_t ldx, const void* w, int64_t V, int64_t ldw,
+                      int dtype, const int32_t* labels, const float* lse, const float* dloss, void* dx, int64_t lddx,
+                      int dx_dtype, void* dw, int64_t lddw, int dw_dtype, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,7 +19,7 @@ __all__ = ["NM_OK", "NM_F16", "NM_BF16", "NM_F32", "NM_I8", "NM_I32", "NM_FP8", 
            "nm_spmm_perm_workspace_size", "nm_spmm_perm_static", "nm_check_perm", "nm_spmm_dx", "nm_spmm_dw",
            "nm_hybrid_layout", "nm_hybrid_compress", "nm_hybrid_spmm", "nm_block_structure", "nm_block_compress",
            "nm_block_spmm", "nm_diag_compress", "nm_diag_spmm", "nm_layernorm", "nm_layernorm_bwd", "nm_adapter_spmm",
-           "nm_adapter_spmm_bwd", "PATTERNS"]
+           "nm_adapter_spmm_bwd", "nm_xent", "nm_xent_bwd", "PATTERNS"]
 
 NM_OK = 0
 NM_F16, NM_BF16, NM_F32, NM_I8, NM_I32, NM_FP8 = 0, 1, 2, 3, 4, 5
@@ -113,6 +113,14 @@ def lib() -> ctypes.CDLL:
     L.nm_adapter_spmm_bwd.restype = i32
     L.nm_adapter_spmm_bwd.argtypes = [vp, vp, i64, i64, i32, i32, i32, vp, i64, i64, vp, i64, vp, vp, vp, vp, vp, i64,
                                       i64, vp, i64, vp, vp, i32, vp, sz, vp]
+    L.nm_xent_workspace_size.restype = i32
+    L.nm_xent_workspace_size.argtypes = [i64, i64, i64, i32, ctypes.POINTER(sz)]
+    L.nm_xent.restype = i32
+    L.nm_xent.argtypes = [vp, i64, i64, i64, vp, i64, i64, i32, vp, vp, vp, vp, sz, vp]
+    L.nm_xent_bwd_workspace_size.restype = i32
+    L.nm_xent_bwd_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32, ctypes.POINTER(sz)]
+    L.nm_xent_bwd.restype = i32
+    L.nm_xent_bwd.argtypes = [vp, i64, i64, i64, vp, i64, i64, i32, vp, vp, vp, vp, i64, i32, vp, i64, i32, vp, sz, vp]
     _lib = L
     return L
 
@@ -797,3 +805,58 @@ def nm_adapter_spmm_bwd(values, idx, G, act, xa, adapter, A, B, scale, K: int, n
                                  _row_stride(out) if out is not None else K, dA.data_ptr(), dB.data_ptr(), od,
                                  _ptr(ws), need, _stream_ptr(act.device)))
     return out, dA, dB
+
+
+# --------------------------------------------------------------------------
+# softmax cross entropy over a large vocabulary
+# --------------------------------------------------------------------------
+
+def _check_xent(x, w, labels, ignore_index):
+    torch = _torch()
+    _row_major(x, "x")
+    _row_major(w, "w")
+    T, H = x.shape
+    V = w.shape[0]
+    if x.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"cross entropy takes float16 or bfloat16, got {x.dtype}")
+    _matrix(w, "w", V, H, x.dtype, x.device)
+    _vector(labels, "labels", T, torch.int32, x.device)
+    if 0 <= ignore_index < V:
+        raise ValueError("ignore_index must lie outside the vocabulary (every label outside it is ignored)")
+    _require_cuda(x)
+    return T, V, H, _dtype_code(x)
+
+
+def nm_xent(x, w, labels, ignore_index: int = -100):
+    """(loss [T], lse [T]) of the logits x @ w.T without keeping them: x [T, H], w [V, H] (float16 or
+    bfloat16), labels int32 [T].  loss[t] = lse[t] - logit of the label, in float32; a label outside
+    [0, V), ignore_index among them, gives loss 0."""
+    torch = _torch()
+    T, V, H, dt = _check_xent(x, w, labels, ignore_index)
+    loss, lse = torch.empty((2, T), dtype=torch.float32, device=x.device).unbind(0)
+    L = lib()
+    ws, need = _workspace(L.nm_xent_workspace_size, T, V, H, dt, device=x.device)
+    _check(L.nm_xent(x.data_ptr(), T, H, _row_stride(x), w.data_ptr(), V, _row_stride(w), dt, labels.data_ptr(),
+                     loss.data_ptr(), lse.data_ptr(), _ptr(ws), need, _stream_ptr(x.device)))
+    return loss, lse
+
+
+def nm_xent_bwd(x, w, labels, lse, dloss, ignore_index: int = -100, out_dtype=None, need_dx: bool = True,
+                need_dw: bool = True):
+    """(dx [T, H], dw [V, H]) of nm_xent from dloss = dL/dloss (float32 [T]) and the lse it returned;
+    float32 unless out_dtype names the dtype of x.  need_dx / need_dw False leave one out (None)."""
+    torch = _torch()
+    T, V, H, dt = _check_xent(x, w, labels, ignore_index)
+    _vector(lse, "lse", T, torch.float32, x.device)
+    _vector(dloss, "dloss", T, torch.float32, x.device)
+    if out_dtype not in (None, torch.float32, x.dtype):
+        raise TypeError("out_dtype must be float32 or the dtype of x")
+    od = dt if out_dtype == x.dtype else NM_F32
+    dx = torch.empty((T, H), dtype=_torch_dtype(od), device=x.device) if need_dx else None
+    dw = torch.empty((V, H), dtype=_torch_dtype(od), device=x.device) if need_dw else None
+    L = lib()
+    ws, need = _workspace(L.nm_xent_bwd_workspace_size, T, V, H, dt, int(need_dx), int(need_dw), device=x.device)
+    _check(L.nm_xent_bwd(x.data_ptr(), T, H, _row_stride(x), w.data_ptr(), V, _row_stride(w), dt, labels.data_ptr(),
+                         lse.data_ptr(), dloss.data_ptr(), _ptr(dx), H, od, _ptr(dw), H, od, _ptr(ws), need,
+                         _stream_ptr(x.device)))
+    return dx, dw

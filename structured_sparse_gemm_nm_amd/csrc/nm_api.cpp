@@ -1129,4 +1129,128 @@ nm_status nm_adapter_spmm_bwd(const void* values, const uint32_t* idx, int64_t R
   return hip_status(nm::launch_adapter_bwd(a, static_cast<hipStream_t>(stream)), "nm_adapter_spmm_bwd launch");
 }
 
+// Shared checks of cross entropy: x [T, H] and w [V, H] in a 16-bit type.
+static nm_status check_xent(int64_t T, int64_t V, int64_t H, int dtype) {
+  if (dtype != NM_F16 && dtype != NM_BF16)
+    return fail(NM_ERR_UNSUPPORTED, "cross entropy takes NM_F16 or NM_BF16, not dtype %d", dtype);
+  if (T < 0 || T > nm::kXentMaxTokens) return fail(NM_ERR_SHAPE, "T = %lld out of range [0, 2^22]", (long long)T);
+  if (V < 1 || V > nm::kXentMaxVocab) return fail(NM_ERR_SHAPE, "V = %lld out of range [1, 2^24]", (long long)V);
+  if (H < 8 || H > nm::kXentMaxH || H % 8)
+    return fail(NM_ERR_SHAPE, "H = %lld is not a multiple of 8 in [8, 2^20]", (long long)H);
+  // tiles of the products are counted in 32 bits
+  if (((T + 15) / 16) * ((V + 127) / 128) > (int64_t(1) << 22) * 16)
+    return fail(NM_ERR_SHAPE, "T x V = %lld x %lld is too large", (long long)T, (long long)V);
+  return NM_OK;
+}
+
+// A 16-bit operand of cross entropy: rows on 16 bytes, 256 of them within 4 GiB.
+static nm_status check_xent_ld(const char* name, int64_t ld, int64_t rows, int64_t H) {
+  nm_status st = check_ld(name, ld, rows, H);
+  if (st != NM_OK) return st;
+  if (ld % 8) return fail(NM_ERR_ALIGN, "%s = %lld is not a multiple of 8", name, (long long)ld);
+  if (ld >= (int64_t(1) << 23)) return fail(NM_ERR_SHAPE, "%s of 2^23 or more", name);
+  return NM_OK;
+}
+
+nm_status nm_xent_workspace_size(int64_t T, int64_t V, int64_t H, int dtype, size_t* bytes) {
+  nm_status st = check_xent(T, V, H, dtype);
+  if (st != NM_OK) return st;
+  if (!bytes) return fail(NM_ERR_NULL, "bytes must be non-NULL");
+  *bytes = nm::xent_workspace(T, V);
+  return ok();
+}
+
+nm_status nm_xent(const void* x, int64_t T, int64_t H, int64_t ldx, const void* w, int64_t V, int64_t ldw, int dtype,
+                  const int32_t* labels, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+  nm_status st = check_xent(T, V, H, dtype);
+  if (st != NM_OK) return st;
+  if ((st = check_xent_ld("ldx", ldx, T, H)) != NM_OK || (st = check_xent_ld("ldw", ldw, V, H)) != NM_OK) return st;
+  if (T == 0) return ok();
+  if (!x || !w || !labels || !loss || !lse || !workspace)
+    return fail(NM_ERR_NULL, "x, w, labels, loss, lse and workspace must be non-NULL");
+  if (!aligned16(x) || !aligned16(w) || !aligned16(workspace) || !aligned_to(labels, 4) || !aligned_to(loss, 4) ||
+      !aligned_to(lse, 4))
+    return fail(NM_ERR_ALIGN, "x, w and workspace must be 16-byte aligned, labels, loss and lse 4-byte");
+  const size_t need = nm::xent_workspace(T, V);
+  if (workspace_bytes < need)
+    return fail(NM_ERR_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  const size_t tb = size_t(T) * 4;
+  const Span in[] = {{x, extent(T, H, ldx, 2)}, {w, extent(V, H, ldw, 2)}, {labels, tb}};
+  const Span out[] = {{loss, tb}, {lse, tb}, {workspace, need}};
+  if ((st = check_alias(in, out)) != NM_OK) return st;
+  nm::XentArgs a;
+  a.x = static_cast<const uint16_t*>(x);
+  a.w = static_cast<const uint16_t*>(w);
+  a.labels = labels;
+  a.ldx = ldx;
+  a.ldw = ldw;
+  a.T = T;
+  a.V = V;
+  a.H = H;
+  a.dtype = dtype;
+  a.loss = loss;
+  a.lse_out = lse;
+  a.workspace = workspace;
+  return hip_status(nm::launch_xent(a, static_cast<hipStream_t>(stream)), "nm_xent launch");
+}
+
+nm_status nm_xent_bwd_workspace_size(int64_t T, int64_t V, int64_t H, int dtype, int need_dx, int need_dw,
+                                     size_t* bytes) {
+  nm_status st = check_xent(T, V, H, dtype);
+  if (st != NM_OK) return st;
+  if (!bytes) return fail(NM_ERR_NULL, "bytes must be non-NULL");
+  *bytes = nm::xent_bwd_workspace(T, V, H, need_dx != 0, need_dw != 0);
+  return ok();
+}
+
+nm_status nm_xent_bwd(const void* x, int64_t T, int64_t H, int64_t ldx, const void* w, int64_t V, int64_t ldw,
+                      int dtype, const int32_t* labels, const float* lse, const float* dloss, void* dx, int64_t lddx,
+                      int dx_dtype, void* dw, int64_t lddw, int dw_dtype, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  nm_status st = check_xent(T, V, H, dtype);
+  if (st != NM_OK) return st;
+  if ((dx && dx_dtype != NM_F32 && dx_dtype != dtype) || (dw && dw_dtype != NM_F32 && dw_dtype != dtype))
+    return fail(NM_ERR_UNSUPPORTED, "dx_dtype and dw_dtype must be NM_F32 or the input dtype");
+  if ((st = check_xent_ld("ldx", ldx, T, H)) != NM_OK || (st = check_xent_ld("ldw", ldw, V, H)) != NM_OK) return st;
+  if ((dx && (st = check_ld("lddx", lddx, T, H)) != NM_OK) || (dw && (st = check_ld("lddw", lddw, V, H)) != NM_OK))
+    return st;
+  if (!dx && !dw) return ok();
+  if (T == 0 && !dw) return ok();
+  if (T > 0 && (!x || !w || !labels || !lse || !dloss || !workspace))
+    return fail(NM_ERR_NULL, "x, w, labels, lse, dloss and workspace must be non-NULL");
+  if ((dx && lddx % 4) || (dw && lddw % 4)) return fail(NM_ERR_ALIGN, "lddx and lddw must be multiples of 4");
+  if (!aligned16(x) || !aligned16(w) || !aligned16(dx) || !aligned16(dw) || !aligned16(workspace) ||
+      !aligned_to(labels, 4) || !aligned_to(lse, 4) || !aligned_to(dloss, 4))
+    return fail(NM_ERR_ALIGN, "matrices and workspace must be 16-byte aligned, vectors 4-byte");
+  const size_t need = nm::xent_bwd_workspace(T, V, H, dx != nullptr, dw != nullptr);
+  if (workspace_bytes < need)
+    return fail(NM_ERR_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  const size_t tb = size_t(T) * 4;
+  const Span in[] = {{x, extent(T, H, ldx, 2)}, {w, extent(V, H, ldw, 2)}, {labels, tb}, {lse, tb}, {dloss, tb}};
+  const Span out[] = {{dx, dx ? extent(T, H, lddx, elt_bytes(dx_dtype)) : 0},
+                      {dw, dw ? extent(V, H, lddw, elt_bytes(dw_dtype)) : 0}, {workspace, need}};
+  if ((st = check_alias(in, out)) != NM_OK) return st;
+  nm::XentArgs a;
+  a.x = static_cast<const uint16_t*>(x);
+  a.w = static_cast<const uint16_t*>(w);
+  a.labels = labels;
+  a.ldx = ldx;
+  a.ldw = ldw;
+  a.T = T;
+  a.V = V;
+  a.H = H;
+  a.dtype = dtype;
+  a.lse = lse;
+  a.dloss = dloss;
+  a.dx = dx;
+  a.dw = dw;
+  a.lddx = lddx;
+  a.lddw = lddw;
+  a.dx_dtype = dx_dtype;
+  a.dw_dtype = dw_dtype;
+  a.workspace = workspace;
+  return hip_status(nm::launch_xent_bwd(a, static_cast<hipStream_t>(stream)), "nm_xent_bwd launch");
+}
+
 }  // extern "C"

@@ -192,6 +192,29 @@ size_t adapter_bwd_workspace(int64_t K, int64_t T, int64_t r, int out_dtype);
 hipError_t launch_adapter(const AdapterArgs& a, hipStream_t s);
 hipError_t launch_adapter_bwd(const AdapterBwdArgs& a, hipStream_t s);
 
+// Softmax cross entropy over a vocabulary (nm_xent.hip).
+struct XentArgs {
+  const uint16_t* x = nullptr;      // [T, H], ldx
+  const uint16_t* w = nullptr;      // [V, H], ldw
+  const int32_t* labels = nullptr;  // [T]
+  int64_t ldx = 0, ldw = 0, T = 0, V = 0, H = 0;
+  int dtype = 0;
+  float* loss = nullptr;            // forward: [T]
+  float* lse_out = nullptr;
+  const float* lse = nullptr;       // backward: [T]
+  const float* dloss = nullptr;
+  void* dx = nullptr;               // [T, H], lddx, or null
+  void* dw = nullptr;               // [V, H], lddw, or null
+  int64_t lddx = 0, lddw = 0;
+  int dx_dtype = 0, dw_dtype = 0;
+  void* workspace = nullptr;
+};
+constexpr int64_t kXentMaxTokens = int64_t(1) << 22, kXentMaxVocab = int64_t(1) << 24, kXentMaxH = int64_t(1) << 20;
+size_t xent_workspace(int64_t T, int64_t V);
+size_t xent_bwd_workspace(int64_t T, int64_t V, int64_t H, bool dx, bool dw);
+hipError_t launch_xent(const XentArgs& a, hipStream_t s);
+hipError_t launch_xent_bwd(const XentArgs& a, hipStream_t s);
+
 // Layer norm (nm_layernorm.hip).  Forward: x, weight, bias -> y (and mean_out,
 // rstd_out when given); backward: dy, x, mean, rstd, weight -> dx, dw, db (the
 // last two through partial sums in `workspace`).

@@ -1,0 +1,495 @@
+// Softmax cross entropy over a large vocabulary, the logits never kept.
+//
+//   l[t][v] = x_t . w_v,  lse_t = log sum_v exp l[t][v],  loss_t = lse_t - l[t][y_t]
+//   d[t][v] = g_t (exp(l[t][v] - lse_t) - [v = y_t]),   g = dL/dloss,
+//   dx = d W,   dW = d^T x;
+// a label outside [0, V) carries no loss and no gradient.
+//
+// Forward: one product X W^T whose tiles are reduced in registers to a running
+// maximum and sum of exponentials per token (and the label's logit), 8 bytes a
+// token and vocabulary tile, joined by a second small kernel.
+// Backward: the vocabulary is walked in pieces.  For each, the logits are
+// computed again and turned into d in the epilogue (written in both orders, so
+// that every product reads its operands along the reduction), then the
+// piece's rows of dW and its share of dx are two more products.  dx gathers in
+// fp32 over the pieces.
+// d enters the matrix cores in the inputs' 16-bit type.  It lies in [-g, g]: in
+// bf16 it keeps 8 bits whatever its size; in fp16 it is scaled by a power of
+// two so that the largest |g| lies just under 2^15, and the products are
+// scaled back.
+#include "nm_gemm_nt.h"
+#include "nm_internal.h"
+
+#include <algorithm>
+
+namespace nm {
+namespace {
+
+constexpr float kInf = __builtin_inff();
+
+// 256 x 256 tiles, 8 waves of 128 x 64; for few tokens, narrow tiles with a
+// deeper ring (the product is then a stream of W)
+using TileBig = GemmTile<256, 256, 2, 4, 2>;
+using Tile64 = GemmTile<128, 64, 4, 1, 4>;
+using Tile16 = GemmTile<128, 16, 4, 1, 6>;
+
+// exp(m - top) for parts of a sum: 0 for an empty part (m = -inf).
+__device__ inline float part_weight(float m, float top) { return m == -kInf ? 0.f : __expf(m - top); }
+
+// ---------------------------------------------------------------------------
+// Forward
+// ---------------------------------------------------------------------------
+struct XentArgsDev {
+  const uint16_t* x;
+  const uint16_t* w;
+  const int32_t* labels;
+  int64_t ldx, ldw;
+  int T, V, H;
+};
+
+template <int DT, class C>
+__global__ __launch_bounds__(C::THREADS) void xent_stats_kernel(XentArgsDev p, float2* __restrict__ part,
+                                                                float* __restrict__ at_label, int tilesV, int tilesT,
+                                                                int group) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  int tv, tt;
+  grouped_tile(xcd_tile(blockIdx.x, gridDim.x), tilesV, tilesT, group, tv, tt);
+  gemm_nt<DT, C>(p.w, p.ldw, p.V, p.x, p.ldx, p.T, p.H, tv, tt, smem, [&](auto& acc, int wm, int wn, int li, int lq) {
+    float2* red = reinterpret_cast<float2*>(smem);   // [WM][BN]
+    const int v0 = tv * C::BM + wm * C::FM * 16 + 4 * lq;
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+      const int n = wn * C::FN * 16 + j * 16 + li, t = tt * C::BN + n;
+      const int label = t < p.T ? p.labels[t] : -1;
+      float m = -kInf;
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int v = v0 + i * 16 + e;
+          if (v >= p.V) acc[i][j][e] = -kInf;
+          m = fmaxf(m, acc[i][j][e]);
+          if (v == label && v < p.V) at_label[t] = acc[i][j][e];
+        }
+      m = fmaxf(m, __shfl_xor(m, 16));
+      m = fmaxf(m, __shfl_xor(m, 32));
+      const float base = m == -kInf ? 0.f : m;
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s += __expf(acc[i][j][e] - base);
+      s += __shfl_xor(s, 16);
+      s += __shfl_xor(s, 32);
+      if (lq == 0) red[wm * C::BN + n] = make_float2(m, s);
+    }
+    __syncthreads();
+    for (int n = threadIdx.x; n < C::BN; n += C::THREADS) {
+      const int t = tt * C::BN + n;
+      if (t >= p.T) break;
+      float m = red[n].x;
+#pragma unroll
+      for (int w = 1; w < C::WM; ++w) m = fmaxf(m, red[w * C::BN + n].x);
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < C::WM; ++w) s += red[w * C::BN + n].y * part_weight(red[w * C::BN + n].x, m);
+      part[int64_t(tv) * p.T + t] = make_float2(m, s);
+    }
+  });
+}
+
+// lse and loss from the parts: a workgroup takes 64 tokens, its 16 waves every
+// 16th vocabulary tile; the waves' sums are joined in wave order.
+__global__ __launch_bounds__(1024) void xent_join_kernel(const float2* __restrict__ part,
+                                                         const float* __restrict__ at_label,
+                                                         const int32_t* __restrict__ labels, int tilesV, int T, int V,
+                                                         float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ float2 red[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int t = blockIdx.x * 64 + lane;
+  float m = -kInf, s = 0.f;
+  if (t < T) {
+#pragma unroll 4
+    for (int i = wave; i < tilesV; i += 16) {
+      const float2 q = part[int64_t(i) * T + t];
+      const float top = fmaxf(m, q.x);
+      s = s * part_weight(m, top) + q.y * part_weight(q.x, top);
+      m = top;
+    }
+  }
+  red[wave][lane] = make_float2(m, s);
+  __syncthreads();
+  if (wave != 0 || t >= T) return;
+  for (int w = 1; w < 16; ++w) m = fmaxf(m, red[w][lane].x);
+  s = 0.f;
+  for (int w = 0; w < 16; ++w) s += red[w][lane].y * part_weight(red[w][lane].x, m);
+  const float l = m + logf(s);
+  const int y = labels[t];
+  lse[t] = l;
+  loss[t] = uint32_t(y) < uint32_t(V) ? l - at_label[t] : 0.f;
+}
+
+// ---------------------------------------------------------------------------
+// Backward
+// ---------------------------------------------------------------------------
+
+// out[c][r] = in[r][c] for a 16-bit matrix [rows][cols], cols a multiple of 8;
+// out rows hold ldo elements (a multiple of 64), zeros past `rows` and, given
+// labels, for rows whose label lies outside [0, V): whatever an ignored token
+// holds, Inf and NaN among it, then meets its zero gradient as a zero.
+__global__ __launch_bounds__(256) void xent_transpose_kernel(const uint16_t* __restrict__ in, int64_t ldi, int rows,
+                                                             int cols, const int32_t* __restrict__ labels, int V,
+                                                             uint16_t* __restrict__ out, int64_t ldo) {
+  __shared__ uint16_t tile[64][64 + 2];
+  const int r0 = blockIdx.x * 64, c0 = blockIdx.y * 64;
+  const int piece = threadIdx.x & 7, line = threadIdx.x >> 3;   // 32 lines of 8 pieces
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = line + 32 * h, c = piece * 8;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (r0 + r < rows && c0 + c < cols && (!labels || uint32_t(labels[r0 + r]) < uint32_t(V)))
+      v = *reinterpret_cast<const u32x4*>(in + int64_t(r0 + r) * ldi + c0 + c);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t*>(&tile[r][c + 2 * e]) = v[e];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = line + 32 * h, r = piece * 8;
+    if (c0 + c >= cols || r0 + r >= ldo) continue;
+    u32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      v[e] = uint32_t(tile[r + 2 * e][c]) | (uint32_t(tile[r + 2 * e + 1][c]) << 16);
+    *reinterpret_cast<u32x4*>(out + int64_t(c0 + c) * ldo + r0 + r) = v;
+  }
+}
+
+// fp16 only: the power of two that brings the largest |dloss| of a counted
+// token to [2^14, 2^15), and its inverse.  All zeros, Inf or NaN: 1.
+__global__ __launch_bounds__(1024) void xent_scale_kernel(const float* __restrict__ dloss,
+                                                          const int32_t* __restrict__ labels, int T, int V,
+                                                          float* __restrict__ scale) {
+  __shared__ float red[16];
+  float m = 0.f;
+  for (int t = threadIdx.x; t < T; t += 1024)
+    if (uint32_t(labels[t]) < uint32_t(V)) m = fmaxf(m, fabsf(dloss[t]));
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < 16; ++w) m = fmaxf(m, red[w]);
+  int e = 0;
+  if (m > 0.f && m < kInf) {
+    e = 14 - ilogbf(m);
+    e = e < -120 ? -120 : e > 120 ? 120 : e;   // both powers are normal numbers
+  }
+  scale[0] = ldexpf(1.f, e);
+  scale[1] = ldexpf(1.f, -e);
+}
+
+struct XentBwdDev {
+  XentArgsDev a;
+  const float* lse;
+  const float* dloss;
+  const float* scale;   // {s, 1/s} (fp16), or null: 1
+  uint16_t* d;          // [T][ldd]
+  uint16_t* dt;         // [piece][ldt]
+  int64_t ldd, ldt;
+  int v0, vn, vpad;     // the piece: rows v0 .. v0 + vn of W, padded to vpad
+};
+
+template <int DT, class C>
+__global__ __launch_bounds__(C::THREADS) void xent_dlogits_kernel(XentBwdDev p, int tilesV, int tilesT, int group) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  int tv, tt;
+  grouped_tile(xcd_tile(blockIdx.x, gridDim.x), tilesV, tilesT, group, tv, tt);
+  const uint16_t* w = p.a.w + int64_t(p.v0) * p.a.ldw;
+  gemm_nt<DT, C>(w, p.a.ldw, p.vn, p.a.x, p.a.ldx, p.a.T, p.a.H, tv, tt, smem,
+                 [&](auto& acc, int wm, int wn, int li, int lq) {
+    const float up = p.scale ? p.scale[0] : 1.f;
+    const int vb = tv * C::BM + wm * C::FM * 16 + 4 * lq;
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+      const int t = tt * C::BN + wn * C::FN * 16 + j * 16 + li;
+      const bool live = t < p.a.T;
+      const int label = live ? p.a.labels[t] : -1;
+      const bool counted = uint32_t(label) < uint32_t(p.a.V);
+      const float lse = live ? p.lse[t] : 0.f;
+      const float g = counted ? p.dloss[t] * up : 0.f;
+      const int mine = label - p.v0;
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) {
+        const int v = vb + i * 16;
+        float d[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float q = __expf(acc[i][j][e] - lse) - (v + e == mine ? 1.f : 0.f);
+          d[e] = counted && v + e < p.vn ? g * q : 0.f;
+        }
+        const uint32_t lo = pack_half2<DT>(d[0], d[1]), hi = pack_half2<DT>(d[2], d[3]);
+        if (v >= p.vpad) continue;     // vpad is a multiple of 4
+        if (live) *reinterpret_cast<uint2*>(p.d + int64_t(t) * p.ldd + v) = make_uint2(lo, hi);
+        if (t < p.ldt) {
+          uint16_t* q = p.dt + int64_t(v) * p.ldt + t;
+          q[0] = uint16_t(lo);
+          q[p.ldt] = uint16_t(lo >> 16);
+          q[2 * p.ldt] = uint16_t(hi);
+          q[3 * p.ldt] = uint16_t(hi >> 16);
+        }
+      }
+    }
+  });
+}
+
+// out[n][m] (+)= sum_k P[m][k] Q[n][k] over the split's share of K.
+struct XentProduct {
+  const uint16_t* P;
+  const uint16_t* Q;
+  int64_t ldp, ldq;
+  int M, N, K, ksplit;  // a split takes ksplit of K (a multiple of 64)
+  const float* scale;   // as above: the result is multiplied by scale[1]
+  void* out;            // rows of ldo elements; split z at out + z * split_stride (fp32)
+  int64_t ldo, split_stride;
+  bool add;             // onto what out holds (fp32 only)
+};
+
+template <int DT, class C, int OUT>
+__global__ __launch_bounds__(C::THREADS) void xent_product_kernel(XentProduct p, int tilesM, int tilesN, int group) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  int tm, tn;
+  grouped_tile(xcd_tile(blockIdx.x, gridDim.x), tilesM, tilesN, group, tm, tn);
+  const int k0 = blockIdx.y * p.ksplit;
+  const int K = min(p.K - k0, p.ksplit);
+  gemm_nt<DT, C>(p.P + k0, p.ldp, p.M, p.Q + k0, p.ldq, p.N, K, tm, tn, smem,
+                 [&](auto& acc, int wm, int wn, int li, int lq) {
+    const float down = p.scale ? p.scale[1] : 1.f;
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+      const int n = tn * C::BN + wn * C::FN * 16 + j * 16 + li;
+      if (n >= p.N) continue;
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) {
+        const int m = tm * C::BM + wm * C::FM * 16 + i * 16 + 4 * lq;
+        if (m >= p.M) continue;        // M is a multiple of 8
+        f32x4 v = acc[i][j];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] *= down;
+        if constexpr (OUT == NM_F32) {
+          float* o = static_cast<float*>(p.out) + blockIdx.y * p.split_stride + int64_t(n) * p.ldo + m;
+          if (p.add) v += *reinterpret_cast<const f32x4*>(o);
+          *reinterpret_cast<f32x4*>(o) = v;
+        } else {
+          uint16_t* o = static_cast<uint16_t*>(p.out) + int64_t(n) * p.ldo + m;
+          *reinterpret_cast<uint2*>(o) = make_uint2(pack_half2<OUT>(v[0], v[1]), pack_half2<OUT>(v[2], v[3]));
+        }
+      }
+    }
+  });
+}
+
+// dx = the sum of the splits' fp32 shares, in order, rounded once.
+template <int OUT>
+__global__ __launch_bounds__(256) void xent_finish_kernel(const float* __restrict__ acc, int splits, int T, int H,
+                                                          void* __restrict__ out, int64_t ldo) {
+  const int64_t all = int64_t(T) * H;
+  for (int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4; i < all; i += int64_t(gridDim.x) * 1024) {
+    f32x4 v = *reinterpret_cast<const f32x4*>(acc + i);
+    for (int z = 1; z < splits; ++z) v += *reinterpret_cast<const f32x4*>(acc + z * all + i);
+    const int64_t t = i / H, h = i - t * H;
+    if constexpr (OUT == NM_F32) {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(out) + t * ldo + h) = v;
+    } else {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + t * ldo + h) =
+          make_uint2(pack_half2<OUT>(v[0], v[1]), pack_half2<OUT>(v[2], v[3]));
+    }
+  }
+}
+
+int64_t up_to(int64_t n, int64_t q) { return (n + q - 1) / q * q; }
+
+// Launches kern on a tilesA x tilesB x splits grid of C's workgroups.
+template <class C, typename Kern, typename Args, typename... Rest>
+hipError_t launch_tiles(Kern kern, const Args& args, int64_t tilesA, int64_t tilesB, int64_t splits, hipStream_t s,
+                        Rest... rest) {
+  if (tilesA * tilesB * C::THREADS > 0xFFFFFFFFll) return hipErrorInvalidValue;
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), C::LDS); e != hipSuccess) return e;
+  // an XCD's run of tiles covers about 4 tiles of A by what fits of B
+  const int group = int(std::min<int64_t>(tilesA, 4));
+  hipLaunchKernelGGL(kern, dim3(unsigned(tilesA * tilesB), unsigned(splits)), dim3(C::THREADS), C::LDS, s, args,
+                     rest..., int(tilesA), int(tilesB), group);
+  return hipGetLastError();
+}
+
+XentArgsDev dev_args(const XentArgs& a) {
+  return XentArgsDev{a.x, a.w, a.labels, a.ldx, a.ldw, int(a.T), int(a.V), int(a.H)};
+}
+
+int64_t stats_tile_v(int64_t T) { return T <= 64 ? 128 : 256; }
+
+template <int DT, class C>
+hipError_t stats(const XentArgs& a, float2* part, float* at_label, hipStream_t s) {
+  return launch_tiles<C>(xent_stats_kernel<DT, C>, dev_args(a), (a.V + C::BM - 1) / C::BM, (a.T + C::BN - 1) / C::BN,
+                         1, s, part, at_label);
+}
+
+template <int DT>
+hipError_t forward_dt(const XentArgs& a, hipStream_t s) {
+  const int64_t tilesV = (a.V + stats_tile_v(a.T) - 1) / stats_tile_v(a.T);
+  float2* part = static_cast<float2*>(a.workspace);
+  float* at_label = reinterpret_cast<float*>(part + tilesV * a.T);
+  hipError_t e;
+  if (a.T <= 16) e = stats<DT, Tile16>(a, part, at_label, s);
+  else if (a.T <= 64) e = stats<DT, Tile64>(a, part, at_label, s);
+  else e = stats<DT, TileBig>(a, part, at_label, s);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(xent_join_kernel, dim3(unsigned((a.T + 63) / 64)), dim3(1024), 0, s, part, at_label, a.labels,
+                     int(tilesV), int(a.T), int(a.V), a.loss, a.lse_out);
+  return hipGetLastError();
+}
+
+// Where the backward pass keeps things in its workspace (bytes).
+struct BwdPlan {
+  int64_t piece, ldt, ldd, splits, ksplit;
+  size_t xt, wt, d, dt, acc, scale, total;
+};
+
+// The vocabulary is cut into pieces of at most 2^26 logits (128 MB in each
+// order): large enough that dx's fp32 sums, read and written once a piece,
+// stay a few percent of its products.
+BwdPlan plan_bwd(int64_t T, int64_t V, int64_t H, bool dx, bool dw) {
+  BwdPlan p;
+  p.ldt = up_to(T, 64);
+  const int64_t most = std::max<int64_t>((int64_t(1) << 26) / std::max<int64_t>(p.ldt, 1) / 256 * 256, 256);
+  const int64_t pieces = (V + most - 1) / most;
+  p.piece = up_to((V + pieces - 1) / pieces, 256);
+  p.ldd = p.piece;
+  // dx has few tiles: its reduction is split until the chip is covered
+  const int64_t tiles = ((T + 255) / 256) * ((H + 255) / 256);
+  p.splits = std::min<int64_t>(std::max<int64_t>(256 / tiles, 1), std::max<int64_t>(p.piece / 512, 1));
+  p.ksplit = up_to((p.piece + p.splits - 1) / p.splits, 64);
+  p.splits = (p.piece + p.ksplit - 1) / p.ksplit;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  p.scale = take(8);
+  p.xt = take(dw ? size_t(H) * p.ldt * 2 : 0);
+  p.dt = take(size_t(p.piece) * p.ldt * 2);
+  p.d = take(size_t(T) * p.ldd * 2);
+  p.wt = take(dx ? size_t(H) * p.ldd * 2 : 0);
+  p.acc = take(dx ? size_t(p.splits) * T * H * 4 : 0);
+  p.total = at;
+  return p;
+}
+
+hipError_t transpose(const uint16_t* in, int64_t ldi, int64_t rows, int64_t cols, const int32_t* labels, int64_t V,
+                     uint16_t* out, int64_t ldo, hipStream_t s) {
+  hipLaunchKernelGGL(xent_transpose_kernel, dim3(unsigned((ldo + 63) / 64), unsigned((cols + 63) / 64)), dim3(256), 0,
+                     s, in, ldi, int(rows), int(cols), labels, int(V), out, ldo);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t product(const XentProduct& p, int out_dtype, int64_t splits, hipStream_t s) {
+  using C = TileBig;
+  const int64_t tm = (p.M + C::BM - 1) / C::BM, tn = (p.N + C::BN - 1) / C::BN;
+  return out_dtype == NM_F32 ? launch_tiles<C>(xent_product_kernel<DT, C, NM_F32>, p, tm, tn, splits, s)
+                             : launch_tiles<C>(xent_product_kernel<DT, C, DT>, p, tm, tn, splits, s);
+}
+
+template <int DT>
+hipError_t backward_dt(const XentArgs& a, hipStream_t s) {
+  const BwdPlan pl = plan_bwd(a.T, a.V, a.H, a.dx != nullptr, a.dw != nullptr);
+  char* ws = static_cast<char*>(a.workspace);
+  float* scale = DT == NM_F16 ? reinterpret_cast<float*>(ws + pl.scale) : nullptr;
+  uint16_t* xt = reinterpret_cast<uint16_t*>(ws + pl.xt);
+  uint16_t* wt = reinterpret_cast<uint16_t*>(ws + pl.wt);
+  float* acc = reinterpret_cast<float*>(ws + pl.acc);
+  hipError_t e = hipSuccess;
+  if (scale) {
+    hipLaunchKernelGGL(xent_scale_kernel, dim3(1), dim3(1024), 0, s, a.dloss, a.labels, int(a.T), int(a.V), scale);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (a.dw && (e = transpose(a.x, a.ldx, a.T, a.H, a.labels, a.V, xt, pl.ldt, s)) != hipSuccess) return e;
+  XentBwdDev b;
+  b.a = dev_args(a);
+  b.lse = a.lse;
+  b.dloss = a.dloss;
+  b.scale = scale;
+  b.d = reinterpret_cast<uint16_t*>(ws + pl.d);
+  b.dt = reinterpret_cast<uint16_t*>(ws + pl.dt);
+  b.ldd = pl.ldd;
+  b.ldt = pl.ldt;
+  for (int64_t v0 = 0; v0 < a.V; v0 += pl.piece) {
+    const int64_t vn = std::min(pl.piece, a.V - v0), vpad = up_to(vn, 64);
+    b.v0 = int(v0);
+    b.vn = int(vn);
+    b.vpad = int(vpad);
+    using C = TileBig;
+    e = launch_tiles<C>(xent_dlogits_kernel<DT, C>, b, (vpad + C::BM - 1) / C::BM, (pl.ldt + C::BN - 1) / C::BN, 1, s);
+    if (e != hipSuccess) return e;
+    if (a.dx) {
+      if ((e = transpose(a.w + v0 * a.ldw, a.ldw, vn, a.H, nullptr, 0, wt, pl.ldd, s)) != hipSuccess) return e;
+      XentProduct p{wt, b.d, pl.ldd, pl.ldd, int(a.H), int(a.T), int(vpad), int(pl.ksplit), scale, acc, a.H,
+                    a.T * a.H, v0 > 0};
+      // (a last piece shorter than the others may need fewer splits: the rest keep their sums)
+      if ((e = product<DT>(p, NM_F32, (vpad + pl.ksplit - 1) / pl.ksplit, s)) != hipSuccess) return e;
+    }
+    if (a.dw) {
+      const size_t es = a.dw_dtype == NM_F32 ? 4 : 2;
+      XentProduct p{xt, b.dt, pl.ldt, pl.ldt, int(a.H), int(vn), int(pl.ldt), int(pl.ldt), scale,
+                    static_cast<char*>(a.dw) + size_t(v0) * a.lddw * es, a.lddw, 0, false};
+      if ((e = product<DT>(p, a.dw_dtype, 1, s)) != hipSuccess) return e;
+    }
+  }
+  if (a.dx) {
+    const unsigned grid = unsigned(std::min<int64_t>((a.T * a.H / 4 + 255) / 256, int64_t(1) << 20));
+    const int splits = int((std::min(pl.piece, up_to(a.V, 64)) + pl.ksplit - 1) / pl.ksplit);
+    if (a.dx_dtype == NM_F32)
+      hipLaunchKernelGGL((xent_finish_kernel<NM_F32>), dim3(grid), dim3(256), 0, s, acc, splits, int(a.T), int(a.H),
+                         a.dx, a.lddx);
+    else
+      hipLaunchKernelGGL((xent_finish_kernel<DT>), dim3(grid), dim3(256), 0, s, acc, splits, int(a.T), int(a.H), a.dx,
+                         a.lddx);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+}  // namespace
+
+size_t xent_workspace(int64_t T, int64_t V) {
+  const int64_t tilesV = (V + stats_tile_v(T) - 1) / stats_tile_v(T);
+  return size_t(tilesV) * T * 8 + size_t(T) * 4;
+}
+
+size_t xent_bwd_workspace(int64_t T, int64_t V, int64_t H, bool dx, bool dw) {
+  return T == 0 ? 0 : plan_bwd(T, V, H, dx, dw).total;
+}
+
+hipError_t launch_xent(const XentArgs& a, hipStream_t s) {
+  return a.dtype == NM_F16 ? forward_dt<NM_F16>(a, s) : forward_dt<NM_BF16>(a, s);
+}
+
+// T == 0: dw is zeros.
+static __global__ __launch_bounds__(256) void xent_zero_kernel(uint16_t* out, int64_t ldo, int rows, int cols) {
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int c = threadIdx.x; c < cols; c += 256) out[r * ldo + c] = 0;
+}
+
+hipError_t launch_xent_bwd(const XentArgs& a, hipStream_t s) {
+  if (a.T == 0) {
+    if (!a.dw) return hipSuccess;
+    const int64_t k = a.dw_dtype == NM_F32 ? 2 : 1;   // in 16-bit units
+    hipLaunchKernelGGL(xent_zero_kernel, dim3(unsigned(std::min<int64_t>(a.V, 65536))), dim3(256), 0, s,
+                       static_cast<uint16_t*>(a.dw), a.lddw * k, int(a.V), int(a.H * k));
+    return hipGetLastError();
+  }
+  return a.dtype == NM_F16 ? backward_dt<NM_F16>(a, s) : backward_dt<NM_BF16>(a, s);
+}
+
+}  // namespace nm

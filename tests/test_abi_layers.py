@@ -97,3 +97,47 @@ def test_adapter_workspace_sizes():
         assert f(64, 64, 2, 4, nm.NM_BF16, 16, 3, 8, nm.NM_BF16, ctypes.byref(b)) == OK
         assert f(64, 64, 2, 4, nm.NM_BF16, 16, 3, 8, nm.NM_F16, ctypes.byref(b)) == UNSUPPORTED
         assert f(64, 64, 2, 4, nm.NM_BF16, 16, 3, 8, nm.NM_BF16, None) == NULL
+
+
+def xent(x=P, T=4, H=64, ldx=64, w=2 * P, V=100, ldw=64, dt=nm.NM_BF16, labels=3 * P, loss=4 * P, lse=5 * P, ws=6 * P,
+         wsb=1 << 20):
+    return nm.lib().nm_xent(x, T, H, ldx, w, V, ldw, dt, labels, loss, lse, ws, wsb, None)
+
+
+def xent_bwd(x=P, T=4, H=64, ldx=64, w=2 * P, V=100, ldw=64, dt=nm.NM_BF16, labels=3 * P, lse=5 * P, dloss=7 * P,
+             dx=8 * P, lddx=64, dxt=nm.NM_F32, dw=9 * P, lddw=64, dwt=nm.NM_BF16, ws=6 * P, wsb=1 << 24):
+    return nm.lib().nm_xent_bwd(x, T, H, ldx, w, V, ldw, dt, labels, lse, dloss, dx, lddx, dxt, dw, lddw, dwt, ws, wsb,
+                                None)
+
+
+def test_xent_errors():
+    for name in ("x", "w", "labels", "loss", "lse", "ws"):
+        assert xent(**{name: None}) == NULL, name
+    assert xent(dt=nm.NM_F32) == UNSUPPORTED
+    assert xent(H=60) == SHAPE and xent(H=0) == SHAPE and xent(V=0) == SHAPE and xent(T=-1) == SHAPE
+    assert xent(T=1 << 23) == SHAPE and xent(V=1 << 25) == SHAPE and xent(T=1 << 22, V=1 << 24) == SHAPE
+    assert xent(ldx=1 << 23) == SHAPE and xent(wsb=8) == SHAPE
+    assert xent(ldx=56) == STRIDE and xent(ldw=56) == STRIDE and xent(ldw=68) == ALIGN
+    assert xent(x=P + 8) == ALIGN and xent(labels=3 * P + 2) == ALIGN
+    assert xent(loss=5 * P) == ALIAS and xent(lse=P) == ALIAS and xent(ws=2 * P) == ALIAS
+    assert xent(T=0, x=None, labels=None, loss=None, lse=None, ws=None) == OK
+
+
+def test_xent_bwd_errors():
+    for name in ("x", "w", "labels", "lse", "dloss", "ws"):
+        assert xent_bwd(**{name: None}) == NULL, name
+    assert xent_bwd(dxt=nm.NM_F16) == UNSUPPORTED and xent_bwd(dwt=nm.NM_F16) == UNSUPPORTED
+    assert xent_bwd(lddx=56) == STRIDE and xent_bwd(lddw=66) == ALIGN and xent_bwd(wsb=1000) == SHAPE
+    assert xent_bwd(dx=9 * P) == ALIAS and xent_bwd(dw=P) == ALIAS and xent_bwd(ws=8 * P) == ALIAS
+    assert xent_bwd(dx=None, dw=None) == OK and xent_bwd(T=0, dw=None) == OK
+
+
+def test_xent_workspace_sizes():
+    b = ctypes.c_size_t()
+    L = nm.lib()
+    assert L.nm_xent_workspace_size(2048, 32000, 4096, nm.NM_BF16, ctypes.byref(b)) == OK
+    assert b.value < 2048 * 32000 // 8                      # far below the logits
+    assert L.nm_xent_bwd_workspace_size(4096, 1 << 20, 4096, nm.NM_BF16, 1, 1, ctypes.byref(b)) == OK
+    assert b.value < 1 << 30                                # pieces: bounded whatever the vocabulary
+    assert L.nm_xent_bwd_workspace_size(4, 100, 60, nm.NM_BF16, 1, 1, ctypes.byref(b)) == SHAPE
+    assert L.nm_xent_workspace_size(4, 100, 64, nm.NM_BF16, None) == NULL
