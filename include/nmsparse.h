@@ -466,8 +466,7 @@ nm_status nm_layernorm_bwd(const void* dy, int64_t ldg, const void* x, int64_t l
  *              overwritten: an adapter without tokens gets zeros.
  *   workspace  device, the bytes of the matching _workspace_size, 16-byte aligned.
  * xa and u stay fp32; between the two low-rank products they enter the matrix
- * cores as two bf16 parts (off by 2^-16 of the sum of |terms| at most).  Inf or
- * NaN in one token or adapter reaches the outputs of that token or adapter only.
+ * cores as three bf16 parts, which hold their 24 bits.  Inf or NaN in one token or adapter reaches the outputs of that token or adapter only.
  * T <= 2^24, R and K <= 2^22.  Pointers 16-byte aligned (adapter, scale: 4),
  * ldx and ldg multiples of 8; outputs and workspace must not overlap anything
  * (NM_ERR_ALIAS).  Stream-ordered; nothing is allocated or synchronised.
@@ -505,9 +504,10 @@ nm_status nm_adapter_spmm_bwd(const void* values, const uint32_t* idx, int64_t R
  *   workspace  device, the bytes of the matching _workspace_size (the backward
  *              pass: for the same choice of dx and dw), 16-byte aligned.
  * Logits, statistics and sums are fp32.  The backward pass walks the vocabulary
- * in pieces and computes the logits again; d is rounded to the inputs' 16-bit
- * type before its two products (relative 2^-8 in bf16, 2^-11 in fp16 an
- * element; fp16 scaled by a power of two against underflow).
+ * in pieces and computes the logits again; softmax - onehot (for dw: times dloss
+ * over its largest magnitude) is rounded to the inputs' 16-bit type before its
+ * two products, relative 2^-8 in bf16, 2^-11 in fp16 an element; dloss itself
+ * multiplies the fp32 results.
  * T <= 2^22, V <= 2^24, H <= 2^20.  Matrices and workspace 16-byte aligned, vectors 4;
  * outputs and workspace must not overlap anything (NM_ERR_ALIAS).
  * Stream-ordered; nothing is allocated or synchronised.

@@ -201,34 +201,27 @@ __global__ __launch_bounds__(kGradWaves * 64) void adapter_grad_kernel(GradArgs 
     if (in == 0) continue;
     const uint32_t mine = (in >> (8 * lq)) & 0xFFu;   // this lane's 8 tokens
     const int64_t t0 = int64_t(k) * 32 + 8 * lq;
-    u32x4 vh[RF], vl[RF];
+    u32x4 vp[RF][3];
 #pragma unroll
     for (int i = 0; i < RF; ++i) {
       const int j = min(r0 + i * 16 + li, g.r - 1);   // ranks past r: results not stored
       float v[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = (mine >> e) & 1u ? g.V[(t0 + e) * g.r + j] : 0.f;
-      split8(v, vh[i], vl[i]);
+      split8(v, vp[i]);
     }
 #pragma unroll
     for (int j = 0; j < CF; ++j) {
       const int c = min(c0 + j * 16 + li, g.C - 1);
-      u32x4 z = {0u, 0u, 0u, 0u}, zh, zl;
+      u32x4 z = {0u, 0u, 0u, 0u}, zp[operand_count<DT>()];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint32_t x = (mine >> e) & 1u ? g.Z[(t0 + e) * g.ldz + c] : 0u;
         z[e >> 1] |= x << (16 * (e & 1));
       }
-      operand_parts<DT>(z, zh, zl);
+      operand_parts<DT>(z, zp);
 #pragma unroll
-      for (int i = 0; i < RF; ++i) {
-        acc[i][j] = mfma32<NM_BF16>(vl[i], zh, acc[i][j]);
-        if constexpr (DT == NM_F16) {
-          acc[i][j] = mfma32<NM_BF16>(vl[i], zl, acc[i][j]);
-          acc[i][j] = mfma32<NM_BF16>(vh[i], zl, acc[i][j]);
-        }
-        acc[i][j] = mfma32<NM_BF16>(vh[i], zh, acc[i][j]);
-      }
+      for (int i = 0; i < RF; ++i) acc[i][j] = mfma_parts(vp[i], zp, acc[i][j]);
     }
   }
   // waves 4..7 onto 0..3, 2..3 onto 0..1, 1 onto 0

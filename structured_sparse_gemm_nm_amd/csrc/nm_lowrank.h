@@ -5,11 +5,11 @@
 //
 // for the 16 tokens of a fragment and any number of 16-column fragments.  V is
 // fp32 (the shrunk activations or gradients).  The matrix cores take 16-bit
-// operands, so V is split into two bf16 parts, hi + lo, which keep 16 of its 24
-// bits (the term is off by at most 2^-16 of sum |M V|); an fp16 M is split the
-// same way, exactly, since bf16's exponent range covers fp16's and 8 + 8 bits
-// its 11.  bf16 throughout also means that no V, however large or small,
-// leaves the operand's range.
+// operands, so V is split into three bf16 parts, which hold its 24 bits; an
+// fp16 M is split into two, exactly, since bf16's exponent range covers fp16's
+// and 8 + 8 bits its 11.  bf16 throughout also means that no V, however large
+// or small, leaves the operand's range.  (Two parts for V would keep 16 bits:
+// an fp32 output then has four times the error of an fp32 product.)
 #pragma once
 
 #include "nm_device.h"
@@ -25,44 +25,54 @@ struct LowRank {
   int C = 0;                      // columns of the product
 };
 
-// Eight floats as bf16 operand halves hi and lo, hi + lo ~ f.  A part that is
-// not finite (f infinite, NaN, or rounded up to infinity) stays in hi alone.
-__device__ inline void split8(const float (&f)[8], u32x4& hi, u32x4& lo) {
+// Eight floats as N bf16 operands that add up to them, the largest first.  A
+// part that is not finite (f infinite, NaN, or rounded up to infinity) stays in
+// the first alone.
+template <int N>
+__device__ inline void split8(const float (&f)[8], u32x4 (&part)[N]) {
+  float r[8];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t h = pack_half2<NM_BF16>(f[2 * e], f[2 * e + 1]);
-    float l0 = f[2 * e] - __builtin_bit_cast(float, h << 16);
-    float l1 = f[2 * e + 1] - __builtin_bit_cast(float, h & 0xFFFF0000u);
-    l0 = fabsf(l0) < __builtin_inff() ? l0 : 0.f;
-    l1 = fabsf(l1) < __builtin_inff() ? l1 : 0.f;
-    hi[e] = h;
-    lo[e] = pack_half2<NM_BF16>(l0, l1);
+  for (int e = 0; e < 8; ++e) r[e] = f[e];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t h = pack_half2<NM_BF16>(r[2 * e], r[2 * e + 1]);
+      part[n][e] = h;
+      const float r0 = r[2 * e] - __builtin_bit_cast(float, h << 16);
+      const float r1 = r[2 * e + 1] - __builtin_bit_cast(float, h & 0xFFFF0000u);
+      r[2 * e] = fabsf(r0) < __builtin_inff() ? r0 : 0.f;
+      r[2 * e + 1] = fabsf(r1) < __builtin_inff() ? r1 : 0.f;
+    }
   }
 }
 
-// A 16-bit operand as bf16 parts: bf16 as it is, fp16 split exactly.
+// A 16-bit operand as bf16 parts: bf16 as it is (one part), fp16 in two.
 template <int DT>
-__device__ inline void operand_parts(const u32x4& raw, u32x4& hi, u32x4& lo) {
+constexpr int operand_count() { return DT == NM_BF16 ? 1 : 2; }
+
+template <int DT>
+__device__ inline void operand_parts(const u32x4& raw, u32x4 (&part)[operand_count<DT>()]) {
   if constexpr (DT == NM_BF16) {
-    hi = raw;
+    part[0] = raw;
   } else {
     float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = half_to_f32<DT>((raw[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-    split8(f, hi, lo);
+    split8(f, part);
   }
 }
 
-// acc += M x V with both operands in parts (lo x lo is below the kept bits
-// when M is bf16; an fp16 M's lo part is needed against both).
-template <int DT>
-__device__ inline f32x4 mfma_parts(const u32x4& mh, const u32x4& ml, const u32x4& vh, const u32x4& vl, f32x4 acc) {
-  acc = mfma32<NM_BF16>(mh, vl, acc);
-  if constexpr (DT == NM_F16) {
-    acc = mfma32<NM_BF16>(ml, vl, acc);
-    acc = mfma32<NM_BF16>(ml, vh, acc);
-  }
-  return mfma32<NM_BF16>(mh, vh, acc);
+// acc += a x b with both operands in parts, the smallest products first;
+// products of parts more than 2^-24 below the largest are left out.
+template <int NA, int NB>
+__device__ inline f32x4 mfma_parts(const u32x4 (&a)[NA], const u32x4 (&b)[NB], f32x4 acc) {
+#pragma unroll
+  for (int k = 2; k >= 0; --k)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (k - i >= 0 && k - i < NB) acc = mfma32<NM_BF16>(a[i], b[k - i], acc);
+  return acc;
 }
 
 // Operand lane (row c, quarter q) of M: elements j0 .. j0 + 7 (zeros past r).
@@ -120,14 +130,14 @@ __device__ inline void lowrank_term(const LowRank& p, int t0, int c0, Add&& add)
       float v[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = j0 + e < p.r ? vrow[j0 + e] : 0.f;
-      u32x4 vh, vl;
-      split8(v, vh, vl);
+      u32x4 vp[3];
+      split8(v, vp);
 #pragma unroll
       for (int f = 0; f < F; ++f) {
         const int c = min(c0 + 16 * f + li, p.C - 1);
-        u32x4 mh, ml;
-        operand_parts<DT>(lowrank_operand<TRANS>(Ma, c, p.C, j0, p.r), mh, ml);
-        d[f] = mfma_parts<DT>(mh, ml, vh, vl, d[f]);
+        u32x4 mp[operand_count<DT>()];
+        operand_parts<DT>(lowrank_operand<TRANS>(Ma, c, p.C, j0, p.r), mp);
+        d[f] = mfma_parts(mp, vp, d[f]);
       }
     }
     const float s = p.scale ? p.scale[a] : 1.f;

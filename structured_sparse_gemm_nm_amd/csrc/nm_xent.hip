@@ -13,10 +13,13 @@
 // that every product reads its operands along the reduction), then the
 // piece's rows of dW and its share of dx are two more products.  dx gathers in
 // fp32 over the pieces.
-// d enters the matrix cores in the inputs' 16-bit type.  It lies in [-g, g]: in
-// bf16 it keeps 8 bits whatever its size; in fp16 it is scaled by a power of
-// two so that the largest |g| lies just under 2^15, and the products are
-// scaled back.
+// d enters the matrix cores in the inputs' 16-bit type, with as much of dloss
+// as possible left to the fp32 results: dx's operand is q = softmax - onehot
+// (its rows are multiplied by g_t at the end), dW's is q g_t / G with G the
+// largest |g|, multiplied by G at the end.  With the usual constant g both are
+// q itself; g q rounded as a whole would give every label's entry, all near -g,
+// the same rounding error (4e-3 of dW measured, against 2e-3 now).  fp16 holds
+// the operands times 2^14, so that probabilities down to 2^-38 are not flushed.
 #include "nm_gemm_nt.h"
 #include "nm_internal.h"
 
@@ -165,11 +168,10 @@ __global__ __launch_bounds__(256) void xent_transpose_kernel(const uint16_t* __r
   }
 }
 
-// fp16 only: the power of two that brings the largest |dloss| of a counted
-// token to [2^14, 2^15), and its inverse.  All zeros, Inf or NaN: 1.
-__global__ __launch_bounds__(1024) void xent_scale_kernel(const float* __restrict__ dloss,
-                                                          const int32_t* __restrict__ labels, int T, int V,
-                                                          float* __restrict__ scale) {
+// The largest |dloss| of a counted token.
+__global__ __launch_bounds__(1024) void xent_largest_kernel(const float* __restrict__ dloss,
+                                                            const int32_t* __restrict__ labels, int T, int V,
+                                                            float* __restrict__ largest) {
   __shared__ float red[16];
   float m = 0.f;
   for (int t = threadIdx.x; t < T; t += 1024)
@@ -180,22 +182,20 @@ __global__ __launch_bounds__(1024) void xent_scale_kernel(const float* __restric
   __syncthreads();
   if (threadIdx.x != 0) return;
   for (int w = 1; w < 16; ++w) m = fmaxf(m, red[w]);
-  int e = 0;
-  if (m > 0.f && m < kInf) {
-    e = 14 - ilogbf(m);
-    e = e < -120 ? -120 : e > 120 ? 120 : e;   // both powers are normal numbers
-  }
-  scale[0] = ldexpf(1.f, e);
-  scale[1] = ldexpf(1.f, -e);
+  *largest = m;
 }
+
+// What an operand is multiplied by before it is rounded to 16 bits.
+template <int DT>
+constexpr float kOperandScale = DT == NM_F16 ? 16384.f : 1.f;
 
 struct XentBwdDev {
   XentArgsDev a;
   const float* lse;
   const float* dloss;
-  const float* scale;   // {s, 1/s} (fp16), or null: 1
-  uint16_t* d;          // [T][ldd]
-  uint16_t* dt;         // [piece][ldt]
+  const float* largest; // of |dloss|
+  uint16_t* d;          // q [T][ldd], or null
+  uint16_t* dt;         // q g / G, transposed: [piece][ldt], or null
   int64_t ldd, ldt;
   int v0, vn, vpad;     // the piece: rows v0 .. v0 + vn of W, padded to vpad
 };
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(C::THREADS) void xent_dlogits_kernel(XentBwdDev p, 
   const uint16_t* w = p.a.w + int64_t(p.v0) * p.a.ldw;
   gemm_nt<DT, C>(w, p.a.ldw, p.vn, p.a.x, p.a.ldx, p.a.T, p.a.H, tv, tt, smem,
                  [&](auto& acc, int wm, int wn, int li, int lq) {
-    const float up = p.scale ? p.scale[0] : 1.f;
+    const float G = *p.largest;
     const int vb = tv * C::BM + wm * C::FM * 16 + 4 * lq;
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) {
@@ -217,7 +217,8 @@ __global__ __launch_bounds__(C::THREADS) void xent_dlogits_kernel(XentBwdDev p, 
       const int label = live ? p.a.labels[t] : -1;
       const bool counted = uint32_t(label) < uint32_t(p.a.V);
       const float lse = live ? p.lse[t] : 0.f;
-      const float g = counted ? p.dloss[t] * up : 0.f;
+      // g == G gives exactly 1; G == 0 (no gradient at all) gives 0
+      const float ratio = counted && G != 0.f ? p.dloss[t] / G : 0.f;
       const int mine = label - p.v0;
 #pragma unroll
       for (int i = 0; i < C::FM; ++i) {
@@ -226,12 +227,15 @@ __global__ __launch_bounds__(C::THREADS) void xent_dlogits_kernel(XentBwdDev p, 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float q = __expf(acc[i][j][e] - lse) - (v + e == mine ? 1.f : 0.f);
-          d[e] = counted && v + e < p.vn ? g * q : 0.f;
+          d[e] = counted && v + e < p.vn ? kOperandScale<DT> * q : 0.f;
         }
-        const uint32_t lo = pack_half2<DT>(d[0], d[1]), hi = pack_half2<DT>(d[2], d[3]);
         if (v >= p.vpad) continue;     // vpad is a multiple of 4
-        if (live) *reinterpret_cast<uint2*>(p.d + int64_t(t) * p.ldd + v) = make_uint2(lo, hi);
-        if (t < p.ldt) {
+        if (p.d && live)
+          *reinterpret_cast<uint2*>(p.d + int64_t(t) * p.ldd + v) =
+              make_uint2(pack_half2<DT>(d[0], d[1]), pack_half2<DT>(d[2], d[3]));
+        if (p.dt && t < p.ldt) {
+          const uint32_t lo = pack_half2<DT>(ratio * d[0], ratio * d[1]);
+          const uint32_t hi = pack_half2<DT>(ratio * d[2], ratio * d[3]);
           uint16_t* q = p.dt + int64_t(v) * p.ldt + t;
           q[0] = uint16_t(lo);
           q[p.ldt] = uint16_t(lo >> 16);
@@ -249,7 +253,7 @@ struct XentProduct {
   const uint16_t* Q;
   int64_t ldp, ldq;
   int M, N, K, ksplit;  // a split takes ksplit of K (a multiple of 64)
-  const float* scale;   // as above: the result is multiplied by scale[1]
+  const float* largest; // G (dw: the result is multiplied by it), or null
   void* out;            // rows of ldo elements; split z at out + z * split_stride (fp32)
   int64_t ldo, split_stride;
   bool add;             // onto what out holds (fp32 only)
@@ -264,7 +268,7 @@ __global__ __launch_bounds__(C::THREADS) void xent_product_kernel(XentProduct p,
   const int K = min(p.K - k0, p.ksplit);
   gemm_nt<DT, C>(p.P + k0, p.ldp, p.M, p.Q + k0, p.ldq, p.N, K, tm, tn, smem,
                  [&](auto& acc, int wm, int wn, int li, int lq) {
-    const float down = p.scale ? p.scale[1] : 1.f;
+    const float down = (p.largest ? *p.largest : 1.f) / kOperandScale<DT>;
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) {
       const int n = tn * C::BN + wn * C::FN * 16 + j * 16 + li;
@@ -289,15 +293,21 @@ __global__ __launch_bounds__(C::THREADS) void xent_product_kernel(XentProduct p,
   });
 }
 
-// dx = the sum of the splits' fp32 shares, in order, rounded once.
+// dx = g times the sum of the splits' fp32 shares, in order, rounded once.  A
+// token that carries no loss gets zeros whatever its g.
 template <int OUT>
 __global__ __launch_bounds__(256) void xent_finish_kernel(const float* __restrict__ acc, int splits, int T, int H,
+                                                          const float* __restrict__ dloss,
+                                                          const int32_t* __restrict__ labels, int V,
                                                           void* __restrict__ out, int64_t ldo) {
   const int64_t all = int64_t(T) * H;
   for (int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4; i < all; i += int64_t(gridDim.x) * 1024) {
     f32x4 v = *reinterpret_cast<const f32x4*>(acc + i);
     for (int z = 1; z < splits; ++z) v += *reinterpret_cast<const f32x4*>(acc + z * all + i);
     const int64_t t = i / H, h = i - t * H;
+    const float g = uint32_t(labels[t]) < uint32_t(V) ? dloss[t] : 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] *= g;
     if constexpr (OUT == NM_F32) {
       *reinterpret_cast<f32x4*>(static_cast<float*>(out) + t * ldo + h) = v;
     } else {
@@ -352,7 +362,7 @@ hipError_t forward_dt(const XentArgs& a, hipStream_t s) {
 // Where the backward pass keeps things in its workspace (bytes).
 struct BwdPlan {
   int64_t piece, ldt, ldd, splits, ksplit;
-  size_t xt, wt, d, dt, acc, scale, total;
+  size_t xt, wt, d, dt, acc, largest, total;
 };
 
 // The vocabulary is cut into pieces of at most 2^26 logits (128 MB in each
@@ -376,10 +386,10 @@ BwdPlan plan_bwd(int64_t T, int64_t V, int64_t H, bool dx, bool dw) {
     at += (bytes + 255) / 256 * 256;
     return here;
   };
-  p.scale = take(8);
+  p.largest = take(4);
   p.xt = take(dw ? size_t(H) * p.ldt * 2 : 0);
-  p.dt = take(size_t(p.piece) * p.ldt * 2);
-  p.d = take(size_t(T) * p.ldd * 2);
+  p.dt = take(dw ? size_t(p.piece) * p.ldt * 2 : 0);
+  p.d = take(dx ? size_t(T) * p.ldd * 2 : 0);
   p.wt = take(dx ? size_t(H) * p.ldd * 2 : 0);
   p.acc = take(dx ? size_t(p.splits) * T * H * 4 : 0);
   p.total = at;
@@ -405,23 +415,21 @@ template <int DT>
 hipError_t backward_dt(const XentArgs& a, hipStream_t s) {
   const BwdPlan pl = plan_bwd(a.T, a.V, a.H, a.dx != nullptr, a.dw != nullptr);
   char* ws = static_cast<char*>(a.workspace);
-  float* scale = DT == NM_F16 ? reinterpret_cast<float*>(ws + pl.scale) : nullptr;
+  float* largest = reinterpret_cast<float*>(ws + pl.largest);
   uint16_t* xt = reinterpret_cast<uint16_t*>(ws + pl.xt);
   uint16_t* wt = reinterpret_cast<uint16_t*>(ws + pl.wt);
   float* acc = reinterpret_cast<float*>(ws + pl.acc);
-  hipError_t e = hipSuccess;
-  if (scale) {
-    hipLaunchKernelGGL(xent_scale_kernel, dim3(1), dim3(1024), 0, s, a.dloss, a.labels, int(a.T), int(a.V), scale);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
+  hipLaunchKernelGGL(xent_largest_kernel, dim3(1), dim3(1024), 0, s, a.dloss, a.labels, int(a.T), int(a.V), largest);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   if (a.dw && (e = transpose(a.x, a.ldx, a.T, a.H, a.labels, a.V, xt, pl.ldt, s)) != hipSuccess) return e;
   XentBwdDev b;
   b.a = dev_args(a);
   b.lse = a.lse;
   b.dloss = a.dloss;
-  b.scale = scale;
-  b.d = reinterpret_cast<uint16_t*>(ws + pl.d);
-  b.dt = reinterpret_cast<uint16_t*>(ws + pl.dt);
+  b.largest = largest;
+  b.d = a.dx ? reinterpret_cast<uint16_t*>(ws + pl.d) : nullptr;
+  b.dt = a.dw ? reinterpret_cast<uint16_t*>(ws + pl.dt) : nullptr;
   b.ldd = pl.ldd;
   b.ldt = pl.ldt;
   for (int64_t v0 = 0; v0 < a.V; v0 += pl.piece) {
@@ -434,14 +442,14 @@ hipError_t backward_dt(const XentArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
     if (a.dx) {
       if ((e = transpose(a.w + v0 * a.ldw, a.ldw, vn, a.H, nullptr, 0, wt, pl.ldd, s)) != hipSuccess) return e;
-      XentProduct p{wt, b.d, pl.ldd, pl.ldd, int(a.H), int(a.T), int(vpad), int(pl.ksplit), scale, acc, a.H,
+      XentProduct p{wt, b.d, pl.ldd, pl.ldd, int(a.H), int(a.T), int(vpad), int(pl.ksplit), nullptr, acc, a.H,
                     a.T * a.H, v0 > 0};
       // (a last piece shorter than the others may need fewer splits: the rest keep their sums)
       if ((e = product<DT>(p, NM_F32, (vpad + pl.ksplit - 1) / pl.ksplit, s)) != hipSuccess) return e;
     }
     if (a.dw) {
       const size_t es = a.dw_dtype == NM_F32 ? 4 : 2;
-      XentProduct p{xt, b.dt, pl.ldt, pl.ldt, int(a.H), int(vn), int(pl.ldt), int(pl.ldt), scale,
+      XentProduct p{xt, b.dt, pl.ldt, pl.ldt, int(a.H), int(vn), int(pl.ldt), int(pl.ldt), largest,
                     static_cast<char*>(a.dw) + size_t(v0) * a.lddw * es, a.lddw, 0, false};
       if ((e = product<DT>(p, a.dw_dtype, 1, s)) != hipSuccess) return e;
     }
@@ -451,10 +459,10 @@ hipError_t backward_dt(const XentArgs& a, hipStream_t s) {
     const int splits = int((std::min(pl.piece, up_to(a.V, 64)) + pl.ksplit - 1) / pl.ksplit);
     if (a.dx_dtype == NM_F32)
       hipLaunchKernelGGL((xent_finish_kernel<NM_F32>), dim3(grid), dim3(256), 0, s, acc, splits, int(a.T), int(a.H),
-                         a.dx, a.lddx);
+                         a.dloss, a.labels, int(a.V), a.dx, a.lddx);
     else
-      hipLaunchKernelGGL((xent_finish_kernel<DT>), dim3(grid), dim3(256), 0, s, acc, splits, int(a.T), int(a.H), a.dx,
-                         a.lddx);
+      hipLaunchKernelGGL((xent_finish_kernel<DT>), dim3(grid), dim3(256), 0, s, acc, splits, int(a.T), int(a.H),
+                         a.dloss, a.labels, int(a.V), a.dx, a.lddx);
     e = hipGetLastError();
   }
   return e;
