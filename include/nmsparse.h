@@ -468,11 +468,11 @@ nm_status nm_layernorm_bwd(const void* dy, int64_t ldg, const void* x, int64_t l
  * xa and u stay fp32; between the two low-rank products they enter the matrix
  * cores as three bf16 parts, which hold their 24 bits.  Inf or NaN in one token or adapter reaches the outputs of that token or adapter only.
  * T <= 2^24, R and K <= 2^22.  Pointers 16-byte aligned (adapter, scale: 4),
- * ldx and ldg multiples of 8; outputs and workspace must not overlap anything
+ * ldx and ldg multiples of 8 below 2^24; outputs and workspace must not overlap anything
  * (NM_ERR_ALIAS).  Stream-ordered; nothing is allocated or synchronised.
  */
-nm_status nm_adapter_spmm_workspace_size(int64_t R, int64_t K, int n, int m, int dtype, int64_t T, int64_t adapters,
-                                         int64_t rank, int out_dtype, size_t* bytes);
+nm_status nm_adapter_spmm_workspace_size(int64_t R, int64_t K, int n, int m, int dtype, int64_t T, int64_t ldx,
+                                         int64_t adapters, int64_t rank, int out_dtype, size_t* bytes);
 nm_status nm_adapter_spmm(const void* values, const uint32_t* idx, int64_t R, int64_t K, int n, int m, int dtype,
                           const void* act, int64_t T, int64_t ldx, const int32_t* adapter, const void* A,
                           const void* B, const float* scale, int64_t adapters, int64_t rank, float* xa, void* Y,

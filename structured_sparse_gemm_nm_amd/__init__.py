@@ -104,9 +104,10 @@ def lib() -> ctypes.CDLL:
     L.nm_layernorm_bwd_workspace_size.argtypes = [i64, i64, ctypes.POINTER(sz)]
     L.nm_layernorm_bwd.restype = i32
     L.nm_layernorm_bwd.argtypes = [vp, i64, vp, i64, i64, i64, i32, vp, vp, vp, vp, i64, vp, vp, i32, vp, sz, vp]
-    for f in (L.nm_adapter_spmm_workspace_size, L.nm_adapter_spmm_bwd_workspace_size):
-        f.restype = i32
-        f.argtypes = [i64, i64, i32, i32, i32, i64, i64, i64, i32, ctypes.POINTER(sz)]
+    L.nm_adapter_spmm_workspace_size.restype = i32
+    L.nm_adapter_spmm_workspace_size.argtypes = [i64, i64, i32, i32, i32, i64, i64, i64, i64, i32, ctypes.POINTER(sz)]
+    L.nm_adapter_spmm_bwd_workspace_size.restype = i32
+    L.nm_adapter_spmm_bwd_workspace_size.argtypes = [i64, i64, i32, i32, i32, i64, i64, i64, i32, ctypes.POINTER(sz)]
     L.nm_adapter_spmm.restype = i32
     L.nm_adapter_spmm.argtypes = [vp, vp, i64, i64, i32, i32, i32, vp, i64, i64, vp, vp, vp, vp, i64, i64, vp, vp, i64,
                                   i32, vp, sz, vp]
@@ -769,7 +770,8 @@ def nm_adapter_spmm(values, idx, act, adapter, A, B, scale, K: int, n: int = 2, 
     elif xa.dtype != torch.float32 or tuple(xa.shape) != (T, r) or not xa.is_contiguous() or xa.device != act.device:
         raise ValueError(f"xa must be a contiguous float32 [{T}, {r}] tensor on {act.device}")
     L = lib()
-    ws, need = _workspace(L.nm_adapter_spmm_workspace_size, R, K, n, m, dt, T, na, r, od, device=act.device)
+    ws, need = _workspace(L.nm_adapter_spmm_workspace_size, R, K, n, m, dt, T, _row_stride(act), na, r, od,
+                          device=act.device)
     _check(L.nm_adapter_spmm(values.data_ptr(), idx.data_ptr(), R, K, n, m, dt, act.data_ptr(), T, _row_stride(act),
                              adapter.data_ptr(), A.data_ptr(), B.data_ptr(), scale.data_ptr(), na, r, xa.data_ptr(),
                              out.data_ptr(), _row_stride(out), od, _ptr(ws), need, _stream_ptr(act.device)))

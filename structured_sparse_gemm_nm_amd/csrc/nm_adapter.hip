@@ -17,33 +17,34 @@
 // The shrunk activations are fp32 (nothing between the two products is
 // rounded to 16 bits).  All three kernels are bound by reading what they
 // multiply: x or g once for the shrink and the gradients, Y once for the
-// expand; the adapters themselves are small.
+// expand; the adapters themselves are small.  The expand step costs no pass of
+// its own where the shared product's kernel holds its tile in registers and
+// adds the term there (few tokens, 2:4 prefill, and dx).
 #include "nm_internal.h"
 #include "nm_lowrank.h"
 
 namespace nm {
 namespace {
 
-// Operand lane (row, quarter): 8 consecutive elements at row + c, zeros past C
-// (C a multiple of 8).
-__device__ inline u32x4 piece8(const uint16_t* row, int c, int C) {
-  if (c >= C) return u32x4{0u, 0u, 0u, 0u};
-  return *reinterpret_cast<const u32x4*>(row + c);
+// Offset past every descriptor here: a load from it returns zeros.
+constexpr uint32_t kDeadOff = 0xFFFFFFF0u;
+
+__device__ inline u32x4 load16(__amdgpu_buffer_rsrc_t rsrc, uint32_t off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0));
 }
 
 // ---------------------------------------------------------------------------
 // Shrink: V[t][j] = s_a sum_c M_a[j][c] Z[t][c] for 16 tokens x RF*16 ranks.
 // A workgroup of 16 waves splits the columns: wave w takes the 64-column steps
-// w, w + 16, ..., and the waves' partial tiles are added in LDS in wave order.
-// 16 tokens a workgroup keeps enough workgroups for short batches; Z is read
-// once (rank tiles past the first reread it from L2).  blockIdx.z deals out
-// the adapters that occur among the 16 tokens, so a batch of single tokens
-// with an adapter each is not walked one after the other.
+// w, w + 16, ..., U of them at a time so that their loads are in flight
+// together, and the waves' partial tiles are added in LDS in wave order.  16
+// tokens a workgroup keeps enough workgroups for short batches; Z is read once
+// (rank tiles past the first reread it from L2).
 // TRANS: M_a is stored [C][r] (B), else [r][C] (A).
 // ---------------------------------------------------------------------------
 constexpr int kShrinkWaves = 16;
 
-template <int DT, bool TRANS, int RF>
+template <int DT, bool TRANS, int RF, int U>
 __global__ __launch_bounds__(kShrinkWaves * 64) void adapter_shrink_kernel(
     const int32_t* __restrict__ ids, int n, const uint16_t* __restrict__ M, const float* __restrict__ scale,
     const uint16_t* __restrict__ Z, int64_t ldz, int T, int C, int r, float* __restrict__ V) {
@@ -56,45 +57,58 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void adapter_shrink_kernel(
   const bool valid = uint32_t(id) < uint32_t(n);
   // every wave holds the same ids, so the loop and its barriers are uniform
   uint32_t todo = uint32_t(__ballot(valid)) & 0xFFFFu;
-  if (blockIdx.z == 0 && wave < RF && !valid && t < T) {   // no adapter: zeros
+  if (wave < RF && !valid && t < T) {   // no adapter: zeros
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int j = r0 + wave * 16 + lq * 4 + e;
       if (j < r) V[int64_t(t) * r + j] = 0.f;
     }
   }
-  const uint16_t* zrow = Z + int64_t(min(t, T - 1)) * ldz;
+  const int last = min(t0 + 16, T) - 1;
+  const __amdgpu_buffer_rsrc_t rz = make_rsrc(Z + int64_t(t0) * ldz, uint32_t((int64_t(last - t0) * ldz + C) * 2));
+  const uint32_t zrow = uint32_t(min(t, last) - t0) * uint32_t(ldz) * 2u;
   const int steps = (C + 63) / 64;
-  for (uint32_t d = 0; todo; ++d) {
+  while (todo) {
     const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
     const bool mine = id == a;
     todo &= ~uint32_t(__ballot(mine));
-    if (d % gridDim.z != blockIdx.z) continue;
-    const uint16_t* Ma = M + int64_t(a) * r * C;
+    const __amdgpu_buffer_rsrc_t rm = make_rsrc(M + int64_t(a) * r * C, uint32_t(r) * uint32_t(C) * 2u);
     f32x4 acc[RF];
 #pragma unroll
     for (int f = 0; f < RF; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int s = wave; s < steps; s += kShrinkWaves) {
+    for (int s = wave; s < steps; s += kShrinkWaves * U) {
+      u32x4 z[U][2], m[U][2][RF];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = s * 64 + h * 32 + lq * 8;
-        const u32x4 z = piece8(zrow, c, C);
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int f = 0; f < RF; ++f) {
-          const int j = min(r0 + f * 16 + li, r - 1);   // rows past r: results not stored
-          u32x4 m = {0u, 0u, 0u, 0u};
-          if constexpr (TRANS) {
-            if (c < C) {
-              const uint16_t* p = Ma + int64_t(c) * r + j;
+        for (int h = 0; h < 2; ++h) {
+          const int c = (s + u * kShrinkWaves) * 64 + h * 32 + lq * 8;
+          const bool in = c < C;    // C is a multiple of 8
+          z[u][h] = load16(rz, in ? zrow + uint32_t(c) * 2u : kDeadOff);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) m[e >> 1] |= uint32_t(p[e * r]) << (16 * (e & 1));
+          for (int f = 0; f < RF; ++f) {
+            const int j = min(r0 + f * 16 + li, r - 1);   // rows past r: results not stored
+            if constexpr (TRANS) {
+              const uint32_t at = (uint32_t(c) * uint32_t(r) + uint32_t(j)) * 2u;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b16(
+                    rm, in ? at + uint32_t(2 * e) * uint32_t(r) * 2u : kDeadOff, 0, 0);
+                const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b16(
+                    rm, in ? at + uint32_t(2 * e + 1) * uint32_t(r) * 2u : kDeadOff, 0, 0);
+                m[u][h][f][e] = lo | (hi << 16);
+              }
+            } else {
+              m[u][h][f] = load16(rm, in ? (uint32_t(j) * uint32_t(C) + uint32_t(c)) * 2u : kDeadOff);
             }
-          } else {
-            m = piece8(Ma + int64_t(j) * C, c, C);
           }
-          acc[f] = mfma32<DT>(m, z, acc[f]);
         }
-      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int f = 0; f < RF; ++f) acc[f] = mfma32<DT>(m[u][h][f], z[u][h], acc[f]);
     }
 #pragma unroll
     for (int f = 0; f < RF; ++f) part[wave][f][lane] = acc[f];
@@ -116,6 +130,43 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void adapter_shrink_kernel(
   }
 }
 
+// The same for few tokens, M as [r][C]: a wave takes one number, V[t][j], with
+// all its loads (16 bytes a lane of both rows, 4096 columns at a time) in
+// flight at once.  Every token may have its own adapter.
+template <int DT>
+__global__ __launch_bounds__(256) void adapter_dots_kernel(const int32_t* __restrict__ ids, int n,
+                                                           const uint16_t* __restrict__ M,
+                                                           const uint16_t* __restrict__ Z, int64_t ldz, int T, int C,
+                                                           int r, float* __restrict__ V) {
+  const int lane = threadIdx.x & 63;
+  const int dot = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (dot >= T * r) return;
+  const int t = dot / r, j = dot - t * r;
+  const int a = ids[t];
+  float sum = 0.f;
+  if (uint32_t(a) < uint32_t(n)) {
+    const __amdgpu_buffer_rsrc_t rz = make_rsrc(Z + int64_t(t) * ldz, uint32_t(C) * 2u);
+    const __amdgpu_buffer_rsrc_t rm = make_rsrc(M + (int64_t(a) * r + j) * C, uint32_t(C) * 2u);
+    for (int c0 = 0; c0 < C; c0 += 4096) {
+      u32x4 z[8], m[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {   // pieces past C lie past both descriptors: zeros
+        z[i] = load16(rz, uint32_t(c0 + (i * 64 + lane) * 8) * 2u);
+        m[i] = load16(rm, uint32_t(c0 + (i * 64 + lane) * 8) * 2u);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          sum += half_to_f32<DT>((z[i][e >> 1] >> (16 * (e & 1))) & 0xFFFFu) *
+                 half_to_f32<DT>((m[i][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+  }
+  if (lane == 0) V[dot] = sum;
+}
+
 // ---------------------------------------------------------------------------
 // Expand: Y[t][c] = base[t][c] + (low-rank term), base fp32 (Y itself or a
 // workspace).  A wave takes 16 tokens x 64 columns.
@@ -133,9 +184,10 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(LowRank p, const fl
     acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int c = c0 + 16 * f + 4 * lq;
     if (t >= p.T) continue;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (c + e < p.C) acc[f][e] = base[int64_t(t) * ldb + c + e];
+    const float* b = base + int64_t(t) * ldb + c;
+    if ((ldb & 3) == 0 && c + 3 < p.C) acc[f] = *reinterpret_cast<const f32x4*>(b);
+    else
+      for (int e = 0; e < 4 && c + e < p.C; ++e) acc[f][e] = b[e];
   }
   lowrank_term<DT, TRANS, 4>(p, t0, c0, [&](int f, const f32x4& d, bool mine) {
 #pragma unroll
@@ -162,68 +214,101 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(LowRank p, const fl
 
 // ---------------------------------------------------------------------------
 // Gradients: D_a[j][c] = s_a sum_{t in a} V[t][j] Z[t][c], written [r][C] (dA,
-// Z = x, V = u) or [C][r] (dB, Z = g, V = xa).  A workgroup of 8 waves owns one
-// adapter, RF*16 ranks and CF*16 columns; wave w takes the 32-token chunks w,
-// w + 8, ... that hold a token of the adapter, and the waves' tiles are added in
-// LDS in a fixed order.  Tokens of other adapters enter as zeros in both
-// operands (loads are not even made), so an Inf or NaN among them reaches
-// nothing.  An adapter without tokens gets zeros.
+// Z = x, V = u) or [C][r] (dB, Z = g, V = xa); one launch does both, the first
+// column tiles dA's, the rest dB's.  A workgroup of 8 waves owns one adapter,
+// RF*16 ranks and CF*16 columns.  The tokens are gone through 4096 at a time:
+// the workgroup marks each 32-token chunk's tokens of the adapter in LDS, the
+// chunks that hold any are dealt to the waves in turn, and in the end the
+// waves' tiles are added in a fixed order.  Tokens of other adapters enter as
+// zeros selected in both operands, so an Inf or NaN among them reaches nothing.
+// An adapter without tokens gets zeros.
 // ---------------------------------------------------------------------------
 constexpr int kGradWaves = 8;
+constexpr int kGradSpan = 4096, kGradChunks = kGradSpan / 32;
 
-struct GradArgs {
-  const int32_t* ids;
-  int n;
+struct GradSide {
   const float* scale;   // or null: 1
   const float* V;       // [T][r]
   const uint16_t* Z;    // [T][C]
   int64_t ldz;
-  int T, C, r;
+  int C, tiles;
   float* out;
-  bool rank_minor;      // [C][r] instead of [r][C]
+};
+struct GradArgs {
+  const int32_t* ids;
+  int T, r;
+  GradSide a, b;        // dA, written [r][C]; dB, written [C][r]
 };
 
 template <int DT, int RF, int CF>
 __global__ __launch_bounds__(kGradWaves * 64) void adapter_grad_kernel(GradArgs g) {
   __shared__ f32x4 part[kGradWaves / 2][RF * CF][64];
+  __shared__ uint32_t mark[kGradChunks];
   const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c0 = blockIdx.x * (CF * 16), r0 = blockIdx.y * (RF * 16), a = blockIdx.z;
+  const bool rank_minor = int(blockIdx.x) >= g.a.tiles;
+  const GradSide& z = rank_minor ? g.b : g.a;
+  const int c0 = (blockIdx.x - (rank_minor ? g.a.tiles : 0)) * (CF * 16), r0 = blockIdx.y * (RF * 16), a = blockIdx.z;
+  const int r = g.r, C = z.C;
   f32x4 acc[RF][CF];
 #pragma unroll
   for (int i = 0; i < RF; ++i)
 #pragma unroll
     for (int j = 0; j < CF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int chunks = (g.T + 31) / 32;
-  for (int k = wave; k < chunks; k += kGradWaves) {
-    const int tl = k * 32 + (lane & 31);
-    const uint32_t in = uint32_t(__ballot(tl < g.T && g.ids[min(tl, g.T - 1)] == a));
-    if (in == 0) continue;
-    const uint32_t mine = (in >> (8 * lq)) & 0xFFu;   // this lane's 8 tokens
-    const int64_t t0 = int64_t(k) * 32 + 8 * lq;
-    u32x4 vp[RF][3];
+
+  for (int64_t base = 0; base < g.T; base += kGradSpan) {
+    __syncthreads();                      // the marks of the span before are read
 #pragma unroll
-    for (int i = 0; i < RF; ++i) {
-      const int j = min(r0 + i * 16 + li, g.r - 1);   // ranks past r: results not stored
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = (mine >> e) & 1u ? g.V[(t0 + e) * g.r + j] : 0.f;
-      split8(v, vp[i]);
+    for (int i = 0; i < kGradSpan / (kGradWaves * 64); ++i) {
+      const int k = (i * kGradWaves + wave) * 64 + lane;
+      const int64_t t = base + k;
+      const uint64_t in = __ballot(t < g.T && g.ids[t < g.T ? t : 0] == a);
+      if (lane < 2) mark[(i * kGradWaves + wave) * 2 + lane] = uint32_t(in >> (32 * lane));
     }
+    __syncthreads();
+    // chunks that hold a token of the adapter, as two 64-bit maps
+    uint64_t some[2] = {__ballot(mark[lane] != 0), __ballot(mark[64 + lane] != 0)};
+    int turn = 0;
+    for (int half = 0; half < 2; ++half) {
+      for (uint64_t left = some[half]; left; left &= left - 1, ++turn) {
+        if (turn % kGradWaves != wave) continue;
+        const int chunk = half * 64 + __builtin_ctzll(left);
+        const uint32_t mine = (mark[chunk] >> (8 * lq)) & 0xFFu;   // this lane's 8 tokens
+        const int64_t t0 = base + chunk * 32 + 8 * lq;
+        // loads are unconditional (tokens past T reread the last) and
+        // selected afterwards, so that all are in flight together
+        float v[RF][8];
+        uint32_t x[CF][8];
 #pragma unroll
-    for (int j = 0; j < CF; ++j) {
-      const int c = min(c0 + j * 16 + li, g.C - 1);
-      u32x4 z = {0u, 0u, 0u, 0u}, zp[operand_count<DT>()];
+        for (int e = 0; e < 8; ++e) {
+          const int64_t t = t0 + e < g.T ? t0 + e : g.T - 1;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t x = (mine >> e) & 1u ? g.Z[(t0 + e) * g.ldz + c] : 0u;
-        z[e >> 1] |= x << (16 * (e & 1));
+          for (int i = 0; i < RF; ++i) v[i][e] = z.V[t * r + min(r0 + i * 16 + li, r - 1)];
+#pragma unroll
+          for (int j = 0; j < CF; ++j) x[j][e] = z.Z[t * z.ldz + min(c0 + j * 16 + li, C - 1)];
+        }
+        u32x4 vp[RF][3];
+#pragma unroll
+        for (int i = 0; i < RF; ++i) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[i][e] = (mine >> e) & 1u ? v[i][e] : 0.f;
+          split8(v[i], vp[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < CF; ++j) {
+          u32x4 raw, zp[operand_count<DT>()];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            raw[e] = ((mine >> (2 * e)) & 1u ? x[j][2 * e] : 0u) |
+                     ((mine >> (2 * e + 1)) & 1u ? x[j][2 * e + 1] << 16 : 0u);
+          operand_parts<DT>(raw, zp);
+#pragma unroll
+          for (int i = 0; i < RF; ++i) acc[i][j] = mfma_parts(vp[i], zp, acc[i][j]);
+        }
       }
-      operand_parts<DT>(z, zp);
-#pragma unroll
-      for (int i = 0; i < RF; ++i) acc[i][j] = mfma_parts(vp[i], zp, acc[i][j]);
     }
   }
+  __syncthreads();
   // waves 4..7 onto 0..3, 2..3 onto 0..1, 1 onto 0
 #pragma unroll
   for (int half = kGradWaves / 2; half > 0; half >>= 1) {
@@ -243,38 +328,43 @@ __global__ __launch_bounds__(kGradWaves * 64) void adapter_grad_kernel(GradArgs 
     __syncthreads();
   }
   if (wave != 0) return;
-  const float s = g.scale ? g.scale[a] : 1.f;
-  float* out = g.out + int64_t(a) * g.r * g.C;
+  const float s = z.scale ? z.scale[a] : 1.f;
+  float* out = z.out + int64_t(a) * r * C;
 #pragma unroll
   for (int i = 0; i < RF; ++i)
 #pragma unroll
     for (int j = 0; j < CF; ++j) {
       const int c = c0 + j * 16 + li, q = r0 + i * 16 + lq * 4;
-      if (c >= g.C) continue;
+      if (c >= C) continue;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (q + e >= g.r) break;
-        const int64_t o = g.rank_minor ? int64_t(c) * g.r + q + e : int64_t(q + e) * g.C + c;
-        out[o] = acc[i][j][e] * s;
-      }
+      for (int e = 0; e < 4; ++e)
+        if (q + e < r) out[rank_minor ? int64_t(c) * r + q + e : int64_t(q + e) * C + c] = acc[i][j][e] * s;
     }
 }
+
+// Up to this many tokens a wave computes one number of V: past it, a token's
+// row would be read by too many waves.
+constexpr int64_t kFewTokens = 16;
 
 template <int DT, bool TRANS>
 hipError_t shrink(const int32_t* ids, int64_t n, const uint16_t* M, const float* scale, const uint16_t* Z, int64_t ldz,
                   int64_t T, int64_t C, int64_t r, float* V, hipStream_t s) {
-  const unsigned tiles = unsigned((T + 15) / 16);
-  // up to 16 adapters side by side while the batch alone does not fill the chip
-  const unsigned z = unsigned(tiles <= 8 ? 16 : 1);
+  if constexpr (!TRANS) {
+    if (T <= kFewTokens) {
+      hipLaunchKernelGGL((adapter_dots_kernel<DT>), dim3(unsigned((T * r + 3) / 4)), dim3(256), 0, s, ids, int(n), M, Z,
+                         ldz, int(T), int(C), int(r), V);
+      return hipGetLastError();
+    }
+  }
   auto go = [&](auto kern, int rf) {
-    hipLaunchKernelGGL(kern, dim3(tiles, unsigned((r + rf * 16 - 1) / (rf * 16)), z), dim3(kShrinkWaves * 64), 0, s,
-                       ids, int(n), M, scale, Z, ldz, int(T), int(C), int(r), V);
+    hipLaunchKernelGGL(kern, dim3(unsigned((T + 15) / 16), unsigned((r + rf * 16 - 1) / (rf * 16))),
+                       dim3(kShrinkWaves * 64), 0, s, ids, int(n), M, scale, Z, ldz, int(T), int(C), int(r), V);
     return hipGetLastError();
   };
-  // few tokens: a rank tile a workgroup; many: every rank of the tile, so Z is read once
-  if (r <= 16 || tiles <= 8) return go(adapter_shrink_kernel<DT, TRANS, 1>, 1);
-  if (r <= 32) return go(adapter_shrink_kernel<DT, TRANS, 2>, 2);
-  return go(adapter_shrink_kernel<DT, TRANS, 4>, 4);
+  // as many steps in flight as the 128 registers of a 1024-thread workgroup hold
+  if (r <= 16) return go(adapter_shrink_kernel<DT, TRANS, 1, 4>, 1);
+  if (r <= 32) return go(adapter_shrink_kernel<DT, TRANS, 2, TRANS ? 2 : 4>, 2);
+  return go(adapter_shrink_kernel<DT, TRANS, 4, TRANS ? 1 : 2>, 4);
 }
 
 template <int DT, bool TRANS>
@@ -289,10 +379,12 @@ hipError_t expand(const LowRank& p, const float* base, int64_t ldb, void* Y, int
 }
 
 template <int DT>
-hipError_t gradient(const GradArgs& g, hipStream_t s) {
+hipError_t gradients(GradArgs g, int64_t n, hipStream_t s) {
   auto go = [&](auto kern, int rf, int cf) {
-    hipLaunchKernelGGL(kern, dim3(unsigned((g.C + cf * 16 - 1) / (cf * 16)), unsigned((g.r + rf * 16 - 1) / (rf * 16)),
-                                  unsigned(g.n)),
+    g.a.tiles = (g.a.C + cf * 16 - 1) / (cf * 16);
+    g.b.tiles = (g.b.C + cf * 16 - 1) / (cf * 16);
+    hipLaunchKernelGGL(kern, dim3(unsigned(g.a.tiles + g.b.tiles), unsigned((g.r + rf * 16 - 1) / (rf * 16)),
+                                  unsigned(n)),
                        dim3(kGradWaves * 64), 0, s, g);
     return hipGetLastError();
   };
@@ -301,19 +393,14 @@ hipError_t gradient(const GradArgs& g, hipStream_t s) {
   return go(adapter_grad_kernel<DT, 4, 4>, 4, 4);
 }
 
+// Whether the shared product's kernel adds the low-rank term itself: the
+// few-token family (T <= 16) and the all-LDS family (prefill, 2:4).
+bool fused_forward(const SpmmArgs& b) { return spmm_decode_applies(b) || spmm_lds_applies(b); }
+
 template <int DT>
 hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
   hipError_t e = shrink<DT, false>(a.ids, a.n, a.A, nullptr, a.base.act, a.base.ldx, a.base.T, a.base.K, a.r, a.xa, s);
-  if (e != hipSuccess) return e;
-  // the product in fp32, in Y itself or in the workspace; then the low-rank term
-  SpmmArgs b = a.base;
-  if (a.base.out_dtype != NM_F32) {
-    b.Y = a.workspace;
-    b.ldy = a.base.R;
-    b.out_dtype = NM_F32;
-  }
-  e = launch_spmm(b, s);
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || a.base.R == 0) return e;
   LowRank p;
   p.ids = a.ids;
   p.M = a.B;
@@ -323,25 +410,30 @@ hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
   p.r = int(a.r);
   p.T = int(a.base.T);
   p.C = int(a.base.R);
+  SpmmArgs b = a.base;
+  if (fused_forward(b)) {
+    b.lowrank = &p;
+    return spmm_decode_applies(b) ? launch_spmm_decode(b, s) : launch_spmm_lds(b, s);
+  }
+  // the product in fp32, in Y itself or in the workspace; then the low-rank term
+  if (a.base.out_dtype != NM_F32) {
+    b.Y = a.workspace;
+    b.ldy = a.base.R;
+    b.out_dtype = NM_F32;
+  }
+  e = launch_spmm(b, s);
+  if (e != hipSuccess) return e;
   return expand<DT, false>(p, static_cast<const float*>(b.Y), b.ldy, a.base.Y, a.base.ldy, a.base.out_dtype, s);
 }
 
 template <int DT>
 hipError_t backward_dt(const AdapterBwdArgs& a, hipStream_t s) {
-  const TrainArgs& d = a.dx;
+  TrainArgs d = a.dx;
   float* u = static_cast<float*>(a.workspace);
   hipError_t e = hipSuccess;
   if (d.T > 0) e = shrink<DT, true>(a.ids, a.n, a.B, a.scale, d.G, d.ldg, d.T, d.R, a.r, u, s);
   if (e != hipSuccess) return e;
   if (d.out && d.T > 0) {
-    TrainArgs b = d;
-    if (d.out_dtype != NM_F32) {
-      b.out = u + adapter_u_elems(d.T, a.r);
-      b.ldo = d.K;
-      b.out_dtype = NM_F32;
-    }
-    e = launch_spmm_dx(b, s);
-    if (e != hipSuccess) return e;
     LowRank p;
     p.ids = a.ids;
     p.M = a.A;
@@ -350,24 +442,23 @@ hipError_t backward_dt(const AdapterBwdArgs& a, hipStream_t s) {
     p.r = int(a.r);
     p.T = int(d.T);
     p.C = int(d.K);
-    e = expand<DT, true>(p, static_cast<const float*>(b.out), b.ldo, d.out, d.ldo, d.out_dtype, s);
+    d.lowrank = &p;
+    e = launch_spmm_dx(d, s);
     if (e != hipSuccess) return e;
   }
-  GradArgs g{a.ids, int(a.n), nullptr, u, d.act, d.ldx, int(d.T), int(d.K), int(a.r), a.dA, false};
-  e = gradient<DT>(g, s);
-  if (e != hipSuccess) return e;
-  return gradient<DT>(GradArgs{a.ids, int(a.n), a.scale, a.xa, d.G, d.ldg, int(d.T), int(d.R), int(a.r), a.dB, true}, s);
+  if (a.n == 0) return e;
+  GradArgs g{a.ids, int(d.T), int(a.r), GradSide{nullptr, u, d.act, d.ldx, int(d.K), 0, a.dA},
+             GradSide{a.scale, a.xa, d.G, d.ldg, int(d.R), 0, a.dB}};
+  return gradients<DT>(g, a.n, s);
 }
 
 }  // namespace
 
-size_t adapter_workspace(int64_t R, int64_t T, int out_dtype) {
-  return out_dtype == NM_F32 ? 0 : size_t(T) * size_t(R) * 4;
+size_t adapter_workspace(const SpmmArgs& base) {
+  return base.out_dtype == NM_F32 || fused_forward(base) ? 0 : size_t(base.T) * size_t(base.R) * 4;
 }
 
-size_t adapter_bwd_workspace(int64_t K, int64_t T, int64_t r, int out_dtype) {
-  return size_t(adapter_u_elems(T, r)) * 4 + (out_dtype == NM_F32 ? 0 : size_t(T) * size_t(K) * 4);
-}
+size_t adapter_bwd_workspace(int64_t T, int64_t r) { return size_t(T) * size_t(r) * 4; }
 
 hipError_t launch_adapter(const AdapterArgs& a, hipStream_t s) {
   return a.base.dtype == NM_F16 ? forward_dt<NM_F16>(a, s) : forward_dt<NM_BF16>(a, s);

@@ -993,12 +993,28 @@ static nm_status check_adapter(int64_t R, int64_t K, int n, int m, int dtype, in
   return NM_OK;
 }
 
-nm_status nm_adapter_spmm_workspace_size(int64_t R, int64_t K, int n, int m, int dtype, int64_t T, int64_t adapters,
-                                         int64_t rank, int out_dtype, size_t* bytes) {
+static nm::SpmmArgs adapter_base(int64_t R, int64_t K, int n, int m, int dtype, int64_t T, int64_t ldx,
+                                 int out_dtype) {
+  nm::SpmmArgs b{};
+  b.R = R;
+  b.K = K;
+  b.n = n;
+  b.m = m;
+  b.dtype = dtype;
+  b.T = T;
+  b.ldx = ldx;
+  b.out_dtype = out_dtype;
+  b.idx_row_words = sizes_of(R, K, n, m, dtype).words;
+  return b;
+}
+
+nm_status nm_adapter_spmm_workspace_size(int64_t R, int64_t K, int n, int m, int dtype, int64_t T, int64_t ldx,
+                                         int64_t adapters, int64_t rank, int out_dtype, size_t* bytes) {
   nm_status st = check_adapter(R, K, n, m, dtype, T, adapters, rank, out_dtype);
   if (st != NM_OK) return st;
   if (!bytes) return fail(NM_ERR_NULL, "bytes must be non-NULL");
-  *bytes = nm::adapter_workspace(R, T, out_dtype);
+  nm::SpmmArgs b = adapter_base(R, K, n, m, dtype, T, ldx, out_dtype);
+  *bytes = T == 0 ? 0 : nm::adapter_workspace(b);
   return ok();
 }
 
@@ -1009,6 +1025,7 @@ nm_status nm_adapter_spmm(const void* values, const uint32_t* idx, int64_t R, in
   nm_status st = check_adapter(R, K, n, m, dtype, T, adapters, rank, out_dtype);
   if (st != NM_OK) return st;
   if ((st = check_ld("ldx", ldx, T, K)) != NM_OK || (st = check_ld("ldy", ldy, T, R)) != NM_OK) return st;
+  if (ldx >= (int64_t(1) << 24)) return fail(NM_ERR_SHAPE, "ldx of 2^24 or more");
   if (T == 0) return ok();
   if (!act || !adapter || !xa || (R > 0 && (!values || !idx || !Y)) || (adapters > 0 && (!A || !scale)) ||
       (adapters > 0 && R > 0 && !B))
@@ -1017,7 +1034,9 @@ nm_status nm_adapter_spmm(const void* values, const uint32_t* idx, int64_t R, in
   if (!aligned16(values) || !aligned16(idx) || !aligned16(act) || !aligned16(Y) || !aligned16(A) || !aligned16(B) ||
       !aligned16(xa) || !aligned16(workspace) || !aligned_to(adapter, 4) || !aligned_to(scale, 4))
     return fail(NM_ERR_ALIGN, "device pointers must be 16-byte aligned (adapter and scale: 4)");
-  const size_t need = nm::adapter_workspace(R, T, out_dtype);
+  nm::AdapterArgs a;
+  a.base = adapter_base(R, K, n, m, dtype, T, ldx, out_dtype);
+  const size_t need = nm::adapter_workspace(a.base);
   if (need > 0 && !workspace) return fail(NM_ERR_NULL, "workspace must be non-NULL");
   if (workspace_bytes < need)
     return fail(NM_ERR_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
@@ -1028,21 +1047,11 @@ nm_status nm_adapter_spmm(const void* values, const uint32_t* idx, int64_t R, in
   const Span out[] = {{Y, extent(T, R, ldy, elt_bytes(out_dtype))}, {xa, size_t(T) * size_t(rank) * 4},
                       {workspace, need}};
   if ((st = check_alias(in, out)) != NM_OK) return st;
-  nm::AdapterArgs a;
   a.base.values = static_cast<const uint16_t*>(values);
   a.base.idx = idx;
-  a.base.R = R;
-  a.base.K = K;
-  a.base.n = n;
-  a.base.m = m;
-  a.base.dtype = dtype;
   a.base.act = static_cast<const uint16_t*>(act);
-  a.base.T = T;
-  a.base.ldx = ldx;
   a.base.Y = Y;
   a.base.ldy = ldy;
-  a.base.out_dtype = out_dtype;
-  a.base.idx_row_words = z.words;
   a.ids = adapter;
   a.n = adapters;
   a.r = rank;
@@ -1059,7 +1068,7 @@ nm_status nm_adapter_spmm_bwd_workspace_size(int64_t R, int64_t K, int n, int m,
   nm_status st = check_adapter(R, K, n, m, dtype, T, adapters, rank, out_dtype);
   if (st != NM_OK) return st;
   if (!bytes) return fail(NM_ERR_NULL, "bytes must be non-NULL");
-  *bytes = nm::adapter_bwd_workspace(K, T, rank, out_dtype);
+  *bytes = nm::adapter_bwd_workspace(T, rank);
   return ok();
 }
 
@@ -1083,7 +1092,7 @@ nm_status nm_adapter_spmm_bwd(const void* values, const uint32_t* idx, int64_t R
       !aligned16(B) || !aligned16(dX) || !aligned16(dA) || !aligned16(dB) || !aligned16(workspace) ||
       !aligned_to(adapter, 4) || !aligned_to(scale, 4))
     return fail(NM_ERR_ALIGN, "device pointers must be 16-byte aligned (adapter and scale: 4)");
-  const size_t need = nm::adapter_bwd_workspace(K, T, rank, out_dtype);
+  const size_t need = nm::adapter_bwd_workspace(T, rank);
   if (T > 0 && workspace_bytes < need)
     return fail(NM_ERR_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
   const Sizes z = sizes_of(R, K, n, m, dtype);

@@ -30,6 +30,19 @@ hipError_t launch_prune_pack_i8(const uint8_t* W, int64_t R, int64_t K, int64_t 
 hipError_t launch_decompress_i8(const uint8_t* values, const uint32_t* idx, int64_t R, int64_t K,
                                 int64_t idx_row_words, uint8_t* W, int64_t ldw, hipStream_t s);
 
+// The low-rank term s_a sum_j M_a[c][j] V[t][j], a = ids[t], of a product's
+// columns c (nm_lowrank.h).
+struct LowRank {
+  const int32_t* ids = nullptr;   // [T]: the token's adapter; outside [0, n): none
+  const uint16_t* M = nullptr;    // [n][C][r], or [n][r][C] where the user says so
+  const float* scale = nullptr;   // [n], or null: 1
+  const float* V = nullptr;       // [T][r]
+  int n = 0, r = 0, T = 0;
+  int C = 0;                      // columns of the product
+};
+// In the place of a LowRank: none.
+struct NoLowRank {};
+
 struct SpmmArgs {
   const uint16_t* values;
   const uint32_t* idx;
@@ -46,6 +59,7 @@ struct SpmmArgs {
   int variant;           // NM_VARIANT_* (0 = choose by shape)
   void* workspace;       // permuted product: caller memory for X' = act[:, perm], or null
   size_t workspace_bytes;
+  const LowRank* lowrank = nullptr;   // added in the epilogue (few-token and all-LDS families, no map)
 };
 
 hipError_t launch_spmm(const SpmmArgs& a, hipStream_t s);
@@ -66,6 +80,7 @@ struct TrainArgs {
   void* out;               // dX [T, K] (ldo) or dW [R, S] (contiguous)
   int64_t ldo;
   int out_dtype;           // NM_F32 or dtype
+  const LowRank* lowrank = nullptr;   // dX only: added in the epilogue, M as [n][r][K]
 };
 hipError_t launch_spmm_dx(const TrainArgs& a, hipStream_t s);
 hipError_t launch_spmm_dw(const TrainArgs& a, hipStream_t s);
@@ -185,10 +200,8 @@ struct AdapterBwdArgs {
 };
 constexpr int64_t kAdapterMaxRank = 256, kAdapterMaxCount = 65535;
 constexpr int64_t kAdapterMaxTokens = int64_t(1) << 24, kAdapterMaxWidth = int64_t(1) << 22;   // grid limits
-// Elements of the backward workspace's first part (u, padded to 16 bytes).
-inline int64_t adapter_u_elems(int64_t T, int64_t r) { return (T * r + 3) / 4 * 4; }
-size_t adapter_workspace(int64_t R, int64_t T, int out_dtype);
-size_t adapter_bwd_workspace(int64_t K, int64_t T, int64_t r, int out_dtype);
+size_t adapter_workspace(const SpmmArgs& base);   // pointers are not looked at
+size_t adapter_bwd_workspace(int64_t T, int64_t r);
 hipError_t launch_adapter(const AdapterArgs& a, hipStream_t s);
 hipError_t launch_adapter_bwd(const AdapterBwdArgs& a, hipStream_t s);
 

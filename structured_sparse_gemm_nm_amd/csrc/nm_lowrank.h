@@ -13,17 +13,9 @@
 #pragma once
 
 #include "nm_device.h"
+#include "nm_internal.h"
 
 namespace nm {
-
-struct LowRank {
-  const int32_t* ids = nullptr;   // [T]: the token's adapter; outside [0, n): none
-  const uint16_t* M = nullptr;    // [n][C][r], or [n][r][C] (TRANS)
-  const float* scale = nullptr;   // [n], or null: 1
-  const float* V = nullptr;       // [T][r]
-  int n = 0, r = 0, T = 0;
-  int C = 0;                      // columns of the product
-};
 
 // Eight floats as N bf16 operands that add up to them, the largest first.  A
 // part that is not finite (f infinite, NaN, or rounded up to infinity) stays in
@@ -103,6 +95,50 @@ __device__ inline u32x4 lowrank_operand(const uint16_t* Ma, int c, int64_t C, in
   return v;
 }
 
+// Elements j0 .. j0 + 7 of a row of r floats, zeros past r.
+__device__ inline void load_v8(const float* row, int j0, int r, float (&v)[8]) {
+  if ((r & 7) == 0 && j0 < r) {   // whole, aligned pieces
+    const f32x4 a = *reinterpret_cast<const f32x4*>(row + j0), b = *reinterpret_cast<const f32x4*>(row + j0 + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = a[e];
+      v[4 + e] = b[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = j0 + e < r ? row[j0 + e] : 0.f;
+  }
+}
+
+// sum[e] += s_a sum_j M_a[c + e][j] V[t][j] for 4 columns of one token, on the
+// vector ALUs: for few tokens, where every token has its own adapter and a
+// matrix-core fragment would hold one column of use.  Columns past C reread
+// column C - 1.  M as [n][C][r].
+template <int DT>
+__device__ inline void lowrank_columns4(const LowRank& p, int t, int c, f32x4& sum) {
+  const int a = p.ids[t];
+  if (uint32_t(a) >= uint32_t(p.n)) return;
+  const float s = p.scale ? p.scale[a] : 1.f;
+  const uint16_t* Ma = p.M + int64_t(a) * p.r * p.C;
+  const float* vrow = p.V + int64_t(t) * p.r;
+  f32x4 d = {0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < p.r; j += 8) {
+    float v[8];
+    load_v8(vrow, j, p.r, v);
+    u32x4 m[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = lowrank_operand<false>(Ma, min(c + e, p.C - 1), p.C, j, p.r);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        // past r both are zero
+        d[e] += half_to_f32<DT>((m[e][q >> 1] >> (16 * (q & 1))) & 0xFFFFu) * v[q];
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sum[e] += s * d[e];
+}
+
 // Calls add(f, d, mine) for every adapter that occurs among tokens t0 .. t0+15
 // and every fragment f < F (columns c0 + 16 f ..): d the fragment of the term, in
 // the matrix cores' result layout (lane (t, q): columns 4q .. 4q+3 of token t),
@@ -128,8 +164,7 @@ __device__ inline void lowrank_term(const LowRank& p, int t0, int c0, Add&& add)
     for (int j = 0; j < p.r; j += 32) {
       const int j0 = j + 8 * lq;
       float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = j0 + e < p.r ? vrow[j0 + e] : 0.f;
+      load_v8(vrow, j0, p.r, v);
       u32x4 vp[3];
       split8(v, vp);
 #pragma unroll

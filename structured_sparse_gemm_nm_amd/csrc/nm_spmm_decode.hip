@@ -16,6 +16,9 @@
 // Operand layouts and the 1:4 / 1:8 widening are those of nm_spmm.hip.
 #include "nm_device.h"
 #include "nm_internal.h"
+#include "nm_lowrank.h"
+
+#include <type_traits>
 
 namespace nm {
 namespace {
@@ -133,11 +136,11 @@ __device__ inline void barrier_lds() {
 }
 
 // SPW: K steps per wave (compile time, so the loads sit in registers).
-template <int P, int DT, int OUT, bool PERM, int RB, int SPW>
+template <int P, int DT, int OUT, bool PERM, int RB, int SPW, class LR>
 __global__ __launch_bounds__(kWaves * 64) void spmm_decode_kernel(
     const uint16_t* __restrict__ values, const uint32_t* __restrict__ idx, int R, int K,
     int64_t words, const uint16_t* __restrict__ act, int T, int64_t ldx,
-    const int32_t* __restrict__ perm, void* __restrict__ Y, int64_t ldy) {
+    const int32_t* __restrict__ perm, void* __restrict__ Y, int64_t ldy, LR lowrank) {
   __shared__ f32x4 part[kWaves][RB][64];
   const int tid = threadIdx.x;
   const int lane = tid & 63, wave = tid >> 6;
@@ -179,6 +182,7 @@ __global__ __launch_bounds__(kWaves * 64) void spmm_decode_kernel(
     const int t = li;
     const int r = R0 + wave * 16 + lq * 4;
     if (t < T && r < R) {
+      if constexpr (std::is_same_v<LR, LowRank>) lowrank_columns4<DT>(lowrank, t, r, sum);
       const bool vec_ok = (ldy & 3) == 0 && r + 3 < R;
       if constexpr (OUT == NM_F32) {
         float* y = static_cast<float*>(Y) + int64_t(t) * ldy + r;
@@ -207,11 +211,11 @@ __global__ __launch_bounds__(kWaves * 64) void spmm_decode_kernel(
 // sits at row*CPR + (c ^ (row & 15)) (CPR 16-byte chunks per row) so a
 // fragment read by 8 consecutive rows hits distinct banks.  Index bits take
 // one more load per wave: 16 rows x SPW*8 bytes.
-template <int DT, int OUT, bool PERM, int SPW>
+template <int DT, int OUT, bool PERM, int SPW, class LR>
 __global__ __launch_bounds__(kWaves * 64) void spmm_decode_lds_kernel(
     const uint16_t* __restrict__ values, const uint32_t* __restrict__ idx, int R, int K,
     const uint16_t* __restrict__ act, int T, int64_t ldx, const int32_t* __restrict__ perm,
-    void* __restrict__ Y, int64_t ldy) {
+    void* __restrict__ Y, int64_t ldy, LR lowrank) {
   constexpr int CPR = SPW * 4;                 // 16-byte value chunks per row
   constexpr int VBYTES = 16 * CPR * 16;        // values region per wave
   constexpr int IBYTES = 16 * SPW * 8;         // index region per wave
@@ -279,6 +283,7 @@ __global__ __launch_bounds__(kWaves * 64) void spmm_decode_lds_kernel(
     const int t = li;
     const int r = R0 + lq * 4;
     if (t < T && r < R) {
+      if constexpr (std::is_same_v<LR, LowRank>) lowrank_columns4<DT>(lowrank, t, r, sum);
       const bool vec_ok = (ldy & 3) == 0 && r + 3 < R;
       if constexpr (OUT == NM_F32) {
         float* y = static_cast<float*>(Y) + int64_t(t) * ldy + r;
@@ -311,11 +316,11 @@ __global__ __launch_bounds__(kWaves * 64) void spmm_decode_lds_kernel(
 // is multiplied: each wave keeps one accumulator tile per block, and the
 // partial tiles of all blocks are summed across waves once, at the end (in
 // LDS reused from the staging area), in a fixed wave order.
-template <int DT, int OUT, bool PERM, int SPW, int NBLK>
+template <int DT, int OUT, bool PERM, int SPW, int NBLK, class LR>
 __global__ __launch_bounds__(kWaves * 64, 1) void spmm_decode_stream_kernel(
     const uint16_t* __restrict__ values, const uint32_t* __restrict__ idx, int R, int K,
     const uint16_t* __restrict__ act, int T, int64_t ldx, const int32_t* __restrict__ perm,
-    void* __restrict__ Y, int64_t ldy, int rows_per_wg) {
+    void* __restrict__ Y, int64_t ldy, int rows_per_wg, LR lowrank) {
   constexpr int CPR = SPW * 4;
   constexpr int VBYTES = 16 * CPR * 16;
   constexpr int IBYTES = 16 * SPW * 8;
@@ -484,6 +489,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void spmm_decode_stream_kernel(
     const int t = li;
     const int r = row_begin + b * 16 + lq * 4;
     if (t < T && r < row_end) {
+      if constexpr (std::is_same_v<LR, LowRank>) lowrank_columns4<DT>(lowrank, t, r, sum);
       const bool vec_ok = (ldy & 3) == 0 && r + 3 < row_end;
       if constexpr (OUT == NM_F32) {
         float* y = static_cast<float*>(Y) + int64_t(t) * ldy + r;
@@ -504,20 +510,20 @@ __global__ __launch_bounds__(kWaves * 64, 1) void spmm_decode_stream_kernel(
   }
 }
 
-template <int DT, int OUT, bool PERM, int SPW, int NBLK>
-hipError_t launch_dec_stream_n(const SpmmArgs& a, hipStream_t s, int grid, int rows_per_wg) {
+template <int DT, int OUT, bool PERM, int SPW, int NBLK, class LR>
+hipError_t launch_dec_stream_n(const SpmmArgs& a, const LR& lr, hipStream_t s, int grid, int rows_per_wg) {
   constexpr int lds = 2 * kWaves * (16 * SPW * 4 * 16 + 16 * SPW * 8);
-  auto kern = spmm_decode_stream_kernel<DT, OUT, PERM, SPW, NBLK>;
+  auto kern = spmm_decode_stream_kernel<DT, OUT, PERM, SPW, NBLK, LR>;
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), lds); e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(kWaves * 64), lds, s, a.values, a.idx, int(a.R),
-                     int(a.K), a.act, int(a.T), a.ldx, a.perm, a.Y, a.ldy, rows_per_wg);
+                     int(a.K), a.act, int(a.T), a.ldx, a.perm, a.Y, a.ldy, rows_per_wg, lr);
   return hipGetLastError();
 }
 
 // One workgroup per CU while that keeps a workgroup's rows within 8 blocks of
 // 16; more rows than that take more workgroups.
-template <int DT, int OUT, bool PERM, int SPW>
-hipError_t launch_dec_stream(const SpmmArgs& a, hipStream_t s) {
+template <int DT, int OUT, bool PERM, int SPW, class LR>
+hipError_t launch_dec_stream(const SpmmArgs& a, const LR& lr, hipStream_t s) {
   const int cus = device_cu_count();
   const int64_t blocks16 = (a.R + 15) / 16;
   int64_t grid = blocks16 < cus ? blocks16 : cus;
@@ -528,70 +534,74 @@ hipError_t launch_dec_stream(const SpmmArgs& a, hipStream_t s) {
   const int nblk = int((even + 15) / 16);
   const int rows_per_wg = int(even);
   switch (nblk) {
-    case 1: return launch_dec_stream_n<DT, OUT, PERM, SPW, 1>(a, s, int(grid), rows_per_wg);
-    case 2: return launch_dec_stream_n<DT, OUT, PERM, SPW, 2>(a, s, int(grid), rows_per_wg);
-    case 3: return launch_dec_stream_n<DT, OUT, PERM, SPW, 3>(a, s, int(grid), rows_per_wg);
-    case 4: return launch_dec_stream_n<DT, OUT, PERM, SPW, 4>(a, s, int(grid), rows_per_wg);
-    case 5: return launch_dec_stream_n<DT, OUT, PERM, SPW, 5>(a, s, int(grid), rows_per_wg);
-    case 6: return launch_dec_stream_n<DT, OUT, PERM, SPW, 6>(a, s, int(grid), rows_per_wg);
-    case 7: return launch_dec_stream_n<DT, OUT, PERM, SPW, 7>(a, s, int(grid), rows_per_wg);
-    default: return launch_dec_stream_n<DT, OUT, PERM, SPW, 8>(a, s, int(grid), rows_per_wg);
+    case 1: return launch_dec_stream_n<DT, OUT, PERM, SPW, 1>(a, lr, s, int(grid), rows_per_wg);
+    case 2: return launch_dec_stream_n<DT, OUT, PERM, SPW, 2>(a, lr, s, int(grid), rows_per_wg);
+    case 3: return launch_dec_stream_n<DT, OUT, PERM, SPW, 3>(a, lr, s, int(grid), rows_per_wg);
+    case 4: return launch_dec_stream_n<DT, OUT, PERM, SPW, 4>(a, lr, s, int(grid), rows_per_wg);
+    case 5: return launch_dec_stream_n<DT, OUT, PERM, SPW, 5>(a, lr, s, int(grid), rows_per_wg);
+    case 6: return launch_dec_stream_n<DT, OUT, PERM, SPW, 6>(a, lr, s, int(grid), rows_per_wg);
+    case 7: return launch_dec_stream_n<DT, OUT, PERM, SPW, 7>(a, lr, s, int(grid), rows_per_wg);
+    default: return launch_dec_stream_n<DT, OUT, PERM, SPW, 8>(a, lr, s, int(grid), rows_per_wg);
   }
 }
 
-template <int DT, int OUT, bool PERM, int SPW>
-hipError_t launch_dec_lds(const SpmmArgs& a, hipStream_t s) {
+template <int DT, int OUT, bool PERM, int SPW, class LR>
+hipError_t launch_dec_lds(const SpmmArgs& a, const LR& lr, hipStream_t s) {
   const int64_t blocks = (a.R + 15) / 16;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((spmm_decode_lds_kernel<DT, OUT, PERM, SPW>), dim3(unsigned(blocks)),
+  hipLaunchKernelGGL((spmm_decode_lds_kernel<DT, OUT, PERM, SPW, LR>), dim3(unsigned(blocks)),
                      dim3(kWaves * 64), 0, s, a.values, a.idx, int(a.R), int(a.K), a.act, int(a.T),
-                     a.ldx, a.perm, a.Y, a.ldy);
+                     a.ldx, a.perm, a.Y, a.ldy, lr);
   return hipGetLastError();
 }
 
-template <int P, int DT, int OUT, bool PERM, int RB, int SPW>
-hipError_t launch_dec(const SpmmArgs& a, hipStream_t s) {
+template <int P, int DT, int OUT, bool PERM, int RB, int SPW, class LR>
+hipError_t launch_dec(const SpmmArgs& a, const LR& lr, hipStream_t s) {
   const int64_t blocks = (a.R + RB * 16 - 1) / (RB * 16);
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((spmm_decode_kernel<P, DT, OUT, PERM, RB, SPW>), dim3(unsigned(blocks)),
+  hipLaunchKernelGGL((spmm_decode_kernel<P, DT, OUT, PERM, RB, SPW, LR>), dim3(unsigned(blocks)),
                      dim3(kWaves * 64), 0, s, a.values, a.idx, int(a.R), int(a.K), a.idx_row_words,
-                     a.act, int(a.T), a.ldx, a.perm, a.Y, a.ldy);
+                     a.act, int(a.T), a.ldx, a.perm, a.Y, a.ldy, lr);
   return hipGetLastError();
 }
 
 // K steps per wave: the smallest instantiated SPW with 8 * SPW * 64 >= K.
-template <int P, int DT, int OUT, bool PERM, int RB>
-hipError_t pick_spw(const SpmmArgs& a, hipStream_t s) {
+template <int P, int DT, int OUT, bool PERM, int RB, class LR>
+hipError_t pick_spw(const SpmmArgs& a, const LR& lr, hipStream_t s) {
   const int64_t steps = (a.K + 63) / 64;
-  if (steps <= 8 * 2) return launch_dec<P, DT, OUT, PERM, RB, 2>(a, s);
-  if (steps <= 8 * 4) return launch_dec<P, DT, OUT, PERM, RB, 4>(a, s);
-  if (steps <= 8 * 8) return launch_dec<P, DT, OUT, PERM, RB, 8>(a, s);
+  if (steps <= 8 * 2) return launch_dec<P, DT, OUT, PERM, RB, 2>(a, lr, s);
+  if (steps <= 8 * 4) return launch_dec<P, DT, OUT, PERM, RB, 4>(a, lr, s);
+  if (steps <= 8 * 8) return launch_dec<P, DT, OUT, PERM, RB, 8>(a, lr, s);
   return hipErrorInvalidValue;  // caller checks decode_applies
 }
 
-template <int P, int DT, int OUT, bool PERM>
-hipError_t pick_rb(const SpmmArgs& a, hipStream_t s) {
+template <int P, int DT, int OUT, bool PERM, class LR>
+hipError_t pick_rb(const SpmmArgs& a, const LR& lr, hipStream_t s) {
   if constexpr (P == 0) {
     const int64_t steps = (a.K + 63) / 64;
     if (a.K % 128 == 0) {
-      if (steps <= 8 * 2) return launch_dec_lds<DT, OUT, PERM, 2>(a, s);
-      if (steps <= 8 * 4) return launch_dec_lds<DT, OUT, PERM, 4>(a, s);
-      if (a.R >= 16 * 256) return launch_dec_stream<DT, OUT, PERM, 8>(a, s);
-      return launch_dec_lds<DT, OUT, PERM, 8>(a, s);
+      if (steps <= 8 * 2) return launch_dec_lds<DT, OUT, PERM, 2>(a, lr, s);
+      if (steps <= 8 * 4) return launch_dec_lds<DT, OUT, PERM, 4>(a, lr, s);
+      if (a.R >= 16 * 256) return launch_dec_stream<DT, OUT, PERM, 8>(a, lr, s);
+      return launch_dec_lds<DT, OUT, PERM, 8>(a, lr, s);
     }
   }
   // Two row blocks per workgroup halve the activation re-reads when enough
   // workgroups remain to cover the chip.
-  if (a.T > 4 && a.R >= 2 * 16 * 256) return pick_spw<P, DT, OUT, PERM, 2>(a, s);
-  return pick_spw<P, DT, OUT, PERM, 1>(a, s);
+  if (a.T > 4 && a.R >= 2 * 16 * 256) return pick_spw<P, DT, OUT, PERM, 2>(a, lr, s);
+  return pick_spw<P, DT, OUT, PERM, 1>(a, lr, s);
 }
 
 template <int P, int DT>
 hipError_t pick_out(const SpmmArgs& a, hipStream_t s) {
+  if (a.lowrank)   // never through the map
+    return a.out_dtype == NM_F32 ? pick_rb<P, DT, NM_F32, false>(a, *a.lowrank, s)
+                                 : pick_rb<P, DT, DT, false>(a, *a.lowrank, s);
   const bool perm = a.perm != nullptr;
+  const NoLowRank lr{};
   if (a.out_dtype == NM_F32)
-    return perm ? pick_rb<P, DT, NM_F32, true>(a, s) : pick_rb<P, DT, NM_F32, false>(a, s);
-  return perm ? pick_rb<P, DT, DT, true>(a, s) : pick_rb<P, DT, DT, false>(a, s);
+    return perm ? pick_rb<P, DT, NM_F32, true>(a, lr, s) : pick_rb<P, DT, NM_F32, false>(a, lr, s);
+  return perm ? pick_rb<P, DT, DT, true>(a, lr, s) : pick_rb<P, DT, DT, false>(a, lr, s);
 }
 
 template <int P>

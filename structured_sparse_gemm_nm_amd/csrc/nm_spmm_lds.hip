@@ -34,6 +34,7 @@
 // ring's fill nor the epilogue's stores leave the MFMAs idle between tiles.
 #include "nm_device.h"
 #include "nm_internal.h"
+#include "nm_lowrank.h"
 
 #include <type_traits>
 
@@ -72,11 +73,11 @@ struct TileMap {
   }
 };
 
-template <int DT, int OUT>
+template <int DT, int OUT, class LR>
 __global__ __launch_bounds__(256, 1) void spmm_lds_kernel(
     const uint16_t* __restrict__ values, const uint32_t* __restrict__ idx, int R, int K,
     const uint16_t* __restrict__ act, int T, int64_t ldx, void* __restrict__ Y, int64_t ldy,
-    TileMap tm) {
+    TileMap tm, LR lowrank) {
   constexpr int FR = 8, FT = kBT / 32;
   extern __shared__ __align__(16) unsigned char smem[];
   unsigned char* bbuf = smem;                              // [kNS][kStageB]
@@ -387,6 +388,18 @@ __global__ __launch_bounds__(256, 1) void spmm_lds_kernel(
       body(integral_constant<int, -2>{}, s + 1, 0, 0, a1, x1, b1, a0, x0, b0);
     }
 
+    // ---- the low-rank term, a token fragment at a time (its loads are waited
+    // for along with the next tile's, already in flight)
+    if constexpr (std::is_same_v<LR, LowRank>) {
+#pragma unroll
+      for (int j = 0; j < FT; ++j)
+        lowrank_term<DT, false, FR>(lowrank, T0 + wt * (kBT / 2) + j * 16, R0 + wr * 128,
+                                    [&](int f, const f32x4& d, bool mine) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[f][j][e] = mine ? acc[f][j][e] + d[e] : acc[f][j][e];
+        });
+    }
+
     // ---- epilogue
     stores_behind = R0 + kBR <= R && T0 + kBT <= T;
     if constexpr (OUT == NM_F32) {
@@ -505,8 +518,8 @@ __global__ __launch_bounds__(256, 1) void spmm_lds_kernel(
   }
 }
 
-template <int DT, int OUT>
-hipError_t launch_lds(const SpmmArgs& a, hipStream_t s) {
+template <int DT, int OUT, class LR>
+hipError_t launch_lds(const SpmmArgs& a, const LR& lowrank, hipStream_t s) {
   const int tilesR = int((a.R + kBR - 1) / kBR);
   const int tilesT = int((a.T + kBT - 1) / kBT);
   const int64_t ntiles = int64_t(tilesR) * tilesT;
@@ -531,10 +544,10 @@ hipError_t launch_lds(const SpmmArgs& a, hipStream_t s) {
   if (a.R * a.K <= (int64_t(4) << 20)) tm.group_r = tilesR;
   tm.ntiles = int(ntiles);
   tm.grid = int(walk && ntiles > cus ? cus : ntiles);
-  auto kern = spmm_lds_kernel<DT, OUT>;
+  auto kern = spmm_lds_kernel<DT, OUT, LR>;
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), kLds); e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3(unsigned(tm.grid)), dim3(256), kLds, s, a.values, a.idx, int(a.R),
-                     int(a.K), a.act, int(a.T), a.ldx, a.Y, a.ldy, tm);
+                     int(a.K), a.act, int(a.T), a.ldx, a.Y, a.ldy, tm, lowrank);
   return hipGetLastError();
 }
 
@@ -551,10 +564,15 @@ bool spmm_lds_applies(const SpmmArgs& a) {
   return device_max_lds() >= kLds;
 }
 
-hipError_t launch_spmm_lds(const SpmmArgs& a, hipStream_t s) {
+template <class LR>
+static hipError_t launch_lds_lr(const SpmmArgs& a, const LR& lowrank, hipStream_t s) {
   if (a.dtype == NM_F16)
-    return a.out_dtype == NM_F32 ? launch_lds<NM_F16, NM_F32>(a, s) : launch_lds<NM_F16, NM_F16>(a, s);
-  return a.out_dtype == NM_F32 ? launch_lds<NM_BF16, NM_F32>(a, s) : launch_lds<NM_BF16, NM_BF16>(a, s);
+    return a.out_dtype == NM_F32 ? launch_lds<NM_F16, NM_F32>(a, lowrank, s) : launch_lds<NM_F16, NM_F16>(a, lowrank, s);
+  return a.out_dtype == NM_F32 ? launch_lds<NM_BF16, NM_F32>(a, lowrank, s) : launch_lds<NM_BF16, NM_BF16>(a, lowrank, s);
+}
+
+hipError_t launch_spmm_lds(const SpmmArgs& a, hipStream_t s) {
+  return a.lowrank ? launch_lds_lr(a, *a.lowrank, s) : launch_lds_lr(a, NoLowRank{}, s);
 }
 
 }  // namespace nm

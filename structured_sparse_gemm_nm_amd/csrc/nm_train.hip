@@ -25,6 +25,7 @@
 // reads per operand, without a transposing copy.
 #include "nm_device.h"
 #include "nm_internal.h"
+#include "nm_lowrank.h"
 
 #include <algorithm>
 #include <type_traits>
@@ -136,12 +137,12 @@ __device__ inline void dx_expand(const DxPack& d, uint32_t ishift, uint32_t (&o)
   }
 }
 
-template <int P, int DT, int OUT>
+template <int P, int DT, int OUT, class LR>
 __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restrict__ values, uint32_t values_bytes,
                                                       const uint32_t* __restrict__ idx, uint32_t idx_bytes, int R,
                                                       int K, int idx_row_words, const uint16_t* __restrict__ G,
                                                       int T, int64_t ldg, void* __restrict__ dX, int64_t lddx,
-                                                      int tilesK, int tilesT, int group) {
+                                                      int tilesK, int tilesT, int group, LR lowrank) {
   constexpr int N = pat_n(P), M = pat_m(P);
   constexpr int B = P == 2 ? 3 : 2;  // index bits per survivor
   extern __shared__ __align__(16) unsigned char smem[];
@@ -304,6 +305,16 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
   }
   if (c < nchunks) step(std::integral_constant<int, 0>{}, c);
   wait_vmcnt<0>();
+
+  // ---- the low-rank term, a token fragment at a time
+  if constexpr (std::is_same_v<LR, LowRank>) {
+#pragma unroll
+    for (int tf = 0; tf < 4; ++tf)
+      lowrank_term<DT, true, 4>(lowrank, T0 + wt * 64 + tf * 16, K0 + wk * 64, [&](int f, const f32x4& d, bool mine) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[f][tf][e] = mine ? acc[f][tf][e] + d[e] : acc[f][tf][e];
+      });
+  }
 
   // ---- epilogue: lane (t = li, quarter q) holds rows 4q..4q+3 (k) of
   // column t of each fragment: 16 (fp32) or 8 (half) contiguous bytes of dX
@@ -583,22 +594,26 @@ hipError_t launch_dw_dt(const TrainArgs& a, hipStream_t s) {
   return a.dtype == NM_F16 ? launch_dw_out<P, NM_F16>(a, s) : launch_dw_out<P, NM_BF16>(a, s);
 }
 
-template <int P, int DT, int OUT>
-hipError_t launch_dx_cfg(const TrainArgs& a, hipStream_t s) {
+template <int P, int DT, int OUT, class LR>
+hipError_t launch_dx_cfg(const TrainArgs& a, const LR& lowrank, hipStream_t s) {
   const int64_t tilesK = (a.K + kDxBK - 1) / kDxBK, tilesT = (a.T + kDxBT - 1) / kDxBT;
   if (tilesK * tilesT > 0x7FFFFFFF) return hipErrorInvalidValue;
-  auto kern = spmm_dx_kernel<P, DT, OUT>;
+  auto kern = spmm_dx_kernel<P, DT, OUT, LR>;
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), kDxLds); e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3(unsigned(tilesK * tilesT)), dim3(256), kDxLds, s, a.values,
                      uint32_t(a.values_bytes), a.idx, uint32_t(a.idx_bytes), int(a.R), int(a.K),
                      int(a.idx_row_words), a.G, int(a.T), a.ldg, a.out, a.ldo, int(tilesK), int(tilesT),
-                     pick_group(tilesK, tilesT, double(pat_n(P)) / pat_m(P), 1.0));
+                     pick_group(tilesK, tilesT, double(pat_n(P)) / pat_m(P), 1.0), lowrank);
   return hipGetLastError();
 }
 
 template <int P, int DT>
 hipError_t launch_dx_out(const TrainArgs& a, hipStream_t s) {
-  return a.out_dtype == NM_F32 ? launch_dx_cfg<P, DT, NM_F32>(a, s) : launch_dx_cfg<P, DT, DT>(a, s);
+  if (a.lowrank)
+    return a.out_dtype == NM_F32 ? launch_dx_cfg<P, DT, NM_F32>(a, *a.lowrank, s)
+                                 : launch_dx_cfg<P, DT, DT>(a, *a.lowrank, s);
+  return a.out_dtype == NM_F32 ? launch_dx_cfg<P, DT, NM_F32>(a, NoLowRank{}, s)
+                               : launch_dx_cfg<P, DT, DT>(a, NoLowRank{}, s);
 }
 
 template <int P>

@@ -68,12 +68,12 @@ def adapter_bwd(values=P, idx=2 * P, R=64, K=64, n=2, m=4, dt=nm.NM_BF16, G=11 *
 
 
 def test_adapter_errors():
-    for name in ("values", "idx", "act", "ids", "A", "B", "scale", "xa", "Y"):
-        assert adapter(**{name: None}) == NULL, name
+    for name in ("values", "idx", "act", "ids", "A", "B", "scale", "xa", "Y", "ws"):
+        assert adapter(**{name: None, "T": 40}) == NULL, name
     assert adapter(dt=nm.NM_I8) == UNSUPPORTED and adapter(od=nm.NM_F16) == UNSUPPORTED and adapter(n=3) == UNSUPPORTED
     assert adapter(r=0) == SHAPE and adapter(r=257) == SHAPE and adapter(na=-1) == SHAPE and adapter(na=65536) == SHAPE
     assert adapter(T=(1 << 24) + 1) == SHAPE and adapter(T=-1) == SHAPE and adapter(K=40, ldx=40) == SHAPE
-    assert adapter(R=1 << 23, ldy=1 << 23) == SHAPE
+    assert adapter(R=1 << 23, ldy=1 << 23) == SHAPE and adapter(ldx=1 << 24) == SHAPE
     assert adapter(ldx=56) == STRIDE and adapter(ldy=63) == STRIDE and adapter(ldx=68) == ALIGN
     assert adapter(A=5 * P + 8) == ALIGN and adapter(ids=4 * P + 2) == ALIGN and adapter(xa=8 * P + 4) == ALIGN
     assert adapter(Y=3 * P) == ALIAS and adapter(xa=9 * P) == ALIAS and adapter(Y=7 * P) == ALIAS
@@ -93,10 +93,13 @@ def test_adapter_bwd_errors():
 
 def test_adapter_workspace_sizes():
     b = ctypes.c_size_t()
-    for f in (nm.lib().nm_adapter_spmm_workspace_size, nm.lib().nm_adapter_spmm_bwd_workspace_size):
-        assert f(64, 64, 2, 4, nm.NM_BF16, 16, 3, 8, nm.NM_BF16, ctypes.byref(b)) == OK
-        assert f(64, 64, 2, 4, nm.NM_BF16, 16, 3, 8, nm.NM_F16, ctypes.byref(b)) == UNSUPPORTED
-        assert f(64, 64, 2, 4, nm.NM_BF16, 16, 3, 8, nm.NM_BF16, None) == NULL
+    fwd, bwd = nm.lib().nm_adapter_spmm_workspace_size, nm.lib().nm_adapter_spmm_bwd_workspace_size
+    ref = ctypes.byref(b)
+    assert fwd(64, 64, 2, 4, nm.NM_BF16, 40, 64, 3, 8, nm.NM_BF16, ref) == OK and b.value == 40 * 64 * 4
+    assert fwd(64, 64, 2, 4, nm.NM_BF16, 40, 64, 3, 8, nm.NM_F32, ref) == OK and b.value == 0
+    assert bwd(64, 64, 2, 4, nm.NM_BF16, 40, 3, 8, nm.NM_BF16, ref) == OK and b.value == 40 * 8 * 4
+    assert fwd(64, 64, 2, 4, nm.NM_BF16, 40, 64, 3, 8, nm.NM_F16, ref) == UNSUPPORTED
+    assert bwd(64, 64, 2, 4, nm.NM_BF16, 40, 3, 8, nm.NM_BF16, None) == NULL
 
 
 def xent(x=P, T=4, H=64, ldx=64, w=2 * P, V=100, ldw=64, dt=nm.NM_BF16, labels=3 * P, loss=4 * P, lse=5 * P, ws=6 * P,
