@@ -9,10 +9,10 @@
 //   dx_t    = W_nm^T g_t + A_a^T u[t]      (expand)
 //   dA_a    = sum_{t in a} u[t] x_t^T,   dB_a = s_a sum_{t in a} g_t xa[t]^T.
 //
-// Tokens of an adapter are found where they lie: a 16-token fragment is
+// Tokens of an adapter are found where they lie: a tile of 64 tokens is
 // multiplied once for every adapter that occurs in it, and each token keeps its
 // own adapter's result.  Requests whose tokens are adjacent cost one product a
-// fragment; any other order is right and costs up to 16.
+// tile, two where they meet; any other order is right and costs more.
 //
 // The shrunk activations are fp32 (nothing between the two products is
 // rounded to 16 bits).  All three kernels are bound by reading what they
@@ -20,113 +20,104 @@
 // expand; the adapters themselves are small.  The expand step costs no pass of
 // its own where the shared product's kernel holds its tile in registers and
 // adds the term there (few tokens, 2:4 prefill, and dx).
+#include "nm_gemm_nt.h"
 #include "nm_internal.h"
 #include "nm_lowrank.h"
 
+#include <algorithm>
+
 namespace nm {
 namespace {
-
-// Offset past every descriptor here: a load from it returns zeros.
-constexpr uint32_t kDeadOff = 0xFFFFFFF0u;
 
 __device__ inline u32x4 load16(__amdgpu_buffer_rsrc_t rsrc, uint32_t off) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0));
 }
 
 // ---------------------------------------------------------------------------
-// Shrink: V[t][j] = s_a sum_c M_a[j][c] Z[t][c] for 16 tokens x RF*16 ranks.
-// A workgroup of 16 waves splits the columns: wave w takes the 64-column steps
-// w, w + 16, ..., U of them at a time so that their loads are in flight
-// together, and the waves' partial tiles are added in LDS in wave order.  16
-// tokens a workgroup keeps enough workgroups for short batches; Z is read once
-// (rank tiles past the first reread it from L2).
-// TRANS: M_a is stored [C][r] (B), else [r][C] (A).
+// Shrink: V[t][j] = s_a sum_c M_a[j][c] Z[t][c], M as [n][r][C].
+// The product of a 64-token tile with one adapter's 32 or 64 ranks is far too
+// small for the chip, so its columns are split over blockIdx.y and the shares,
+// part[split][t][j], are added in order by adapter_join_kernel.  Loading whole
+// 128-byte lines into LDS (gemm_nt) matters more than the few operations: with
+// operand fragments loaded straight into registers (16 rows of 64 bytes an
+// instruction) 2048 tokens x 4096, rank 32, took 13 us in place of SHRINK_US.
+// Several adapters in a tile are dealt to blockIdx.z in turn.
 // ---------------------------------------------------------------------------
-constexpr int kShrinkWaves = 16;
+struct ShrinkArgs {
+  const int32_t* ids;
+  const uint16_t* M;
+  const uint16_t* Z;
+  int64_t ldz;
+  int n, T, C, r, csplit;   // a split takes csplit columns (a multiple of 64)
+  float* part;              // [splits][T][r]
+};
 
-template <int DT, bool TRANS, int RF, int U>
-__global__ __launch_bounds__(kShrinkWaves * 64) void adapter_shrink_kernel(
-    const int32_t* __restrict__ ids, int n, const uint16_t* __restrict__ M, const float* __restrict__ scale,
-    const uint16_t* __restrict__ Z, int64_t ldz, int T, int C, int r, float* __restrict__ V) {
-  __shared__ f32x4 part[kShrinkWaves][RF][64];
-  const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int t0 = blockIdx.x * 16, r0 = blockIdx.y * (RF * 16);
-  const int t = t0 + li;
-  const int id = t < T ? ids[t] : -1;
-  const bool valid = uint32_t(id) < uint32_t(n);
+template <int DT, class C>
+__global__ __launch_bounds__(C::THREADS) void adapter_shrink_kernel(ShrinkArgs p, int rank_tiles) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  static_assert(C::BN == 64, "a lane a token");
+  const int tt = blockIdx.x / rank_tiles, tr = blockIdx.x - tt * rank_tiles;
+  const int t = tt * 64 + (threadIdx.x & 63);
+  const int id = t < p.T ? p.ids[t] : -1;
   // every wave holds the same ids, so the loop and its barriers are uniform
-  uint32_t todo = uint32_t(__ballot(valid)) & 0xFFFFu;
-  if (wave < RF && !valid && t < T) {   // no adapter: zeros
+  uint64_t todo = __ballot(uint32_t(id) < uint32_t(p.n));
+  const int c0 = blockIdx.y * p.csplit, K = min(p.C - c0, p.csplit);
+  float* part = p.part + int64_t(blockIdx.y) * p.T * p.r;
+  for (uint32_t turn = 0; todo; ++turn) {
+    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+    const uint64_t mine = __ballot(id == a);
+    todo &= ~mine;
+    if (turn % gridDim.z != blockIdx.z) continue;
+    gemm_nt<DT, C>(p.M + int64_t(a) * p.r * p.C + c0, p.C, p.r, p.Z + c0, p.ldz, p.T, K, tr, tt, smem,
+                   [&](auto& acc, int wm, int wn, int li, int lq) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int j = r0 + wave * 16 + lq * 4 + e;
-      if (j < r) V[int64_t(t) * r + j] = 0.f;
-    }
-  }
-  const int last = min(t0 + 16, T) - 1;
-  const __amdgpu_buffer_rsrc_t rz = make_rsrc(Z + int64_t(t0) * ldz, uint32_t((int64_t(last - t0) * ldz + C) * 2));
-  const uint32_t zrow = uint32_t(min(t, last) - t0) * uint32_t(ldz) * 2u;
-  const int steps = (C + 63) / 64;
-  while (todo) {
-    const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
-    const bool mine = id == a;
-    todo &= ~uint32_t(__ballot(mine));
-    const __amdgpu_buffer_rsrc_t rm = make_rsrc(M + int64_t(a) * r * C, uint32_t(r) * uint32_t(C) * 2u);
-    f32x4 acc[RF];
+      for (int j = 0; j < C::FN; ++j) {
+        const int k = wn * C::FN * 16 + j * 16 + li;
+        if (!((mine >> k) & 1u)) continue;
+        float* row = part + int64_t(tt * 64 + k) * p.r;
 #pragma unroll
-    for (int f = 0; f < RF; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int s = wave; s < steps; s += kShrinkWaves * U) {
-      u32x4 z[U][2], m[U][2][RF];
+        for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c = (s + u * kShrinkWaves) * 64 + h * 32 + lq * 8;
-          const bool in = c < C;    // C is a multiple of 8
-          z[u][h] = load16(rz, in ? zrow + uint32_t(c) * 2u : kDeadOff);
-#pragma unroll
-          for (int f = 0; f < RF; ++f) {
-            const int j = min(r0 + f * 16 + li, r - 1);   // rows past r: results not stored
-            if constexpr (TRANS) {
-              const uint32_t at = (uint32_t(c) * uint32_t(r) + uint32_t(j)) * 2u;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b16(
-                    rm, in ? at + uint32_t(2 * e) * uint32_t(r) * 2u : kDeadOff, 0, 0);
-                const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b16(
-                    rm, in ? at + uint32_t(2 * e + 1) * uint32_t(r) * 2u : kDeadOff, 0, 0);
-                m[u][h][f][e] = lo | (hi << 16);
-              }
-            } else {
-              m[u][h][f] = load16(rm, in ? (uint32_t(j) * uint32_t(C) + uint32_t(c)) * 2u : kDeadOff);
-            }
+          for (int e = 0; e < 4; ++e) {
+            const int q = tr * C::BM + wm * C::FM * 16 + i * 16 + 4 * lq + e;
+            if (q < p.r) row[q] = acc[i][j][e];
           }
-        }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int f = 0; f < RF; ++f) acc[f] = mfma32<DT>(m[u][h][f], z[u][h], acc[f]);
-    }
-#pragma unroll
-    for (int f = 0; f < RF; ++f) part[wave][f][lane] = acc[f];
-    __syncthreads();
-    if (wave < RF) {
-      f32x4 sum = part[0][wave][lane];
-#pragma unroll
-      for (int w = 1; w < kShrinkWaves; ++w) sum += part[w][wave][lane];
-      const float sc = scale ? scale[a] : 1.f;
-      if (mine && t < T) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = r0 + wave * 16 + lq * 4 + e;
-          if (j < r) V[int64_t(t) * r + j] = sum[e] * sc;
-        }
       }
-    }
-    __syncthreads();   // part is free for the next adapter
+    });
+  }
+}
+
+__global__ __launch_bounds__(256) void adapter_join_kernel(const float* __restrict__ part, int splits,
+                                                           const int32_t* __restrict__ ids, int n,
+                                                           const float* __restrict__ scale, int T, int r,
+                                                           float* __restrict__ V) {
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, all = int64_t(T) * r;
+  if (i >= all) return;
+  const int a = ids[i / r];
+  float v = 0.f;
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) v += part[s * all + i];
+  V[i] = uint32_t(a) < uint32_t(n) ? (scale ? v * scale[a] : v) : 0.f;   // no adapter: zeros
+}
+
+// Mt[a][j][c] = M[a][c][j]: B's columns along the reduction of the backward
+// pass's shrink.  A workgroup takes 64 columns c and 32 ranks.
+__global__ __launch_bounds__(256) void adapter_transpose_kernel(const uint16_t* __restrict__ M, int C, int r,
+                                                                uint16_t* __restrict__ Mt) {
+  __shared__ uint16_t tile[32][64 + 2];
+  const int c0 = blockIdx.x * 64, j0 = blockIdx.y * 32;
+  const uint16_t* m = M + int64_t(blockIdx.z) * C * r;
+  uint16_t* mt = Mt + int64_t(blockIdx.z) * C * r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = (threadIdx.x >> 5) + 8 * i, j = threadIdx.x & 31;
+    if (c0 + c < C && j0 + j < r) tile[j][c] = m[int64_t(c0 + c) * r + j0 + j];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int j = (threadIdx.x >> 6) + 4 * i, c = threadIdx.x & 63;
+    if (c0 + c < C && j0 + j < r) mt[int64_t(j0 + j) * C + c0 + c] = tile[j][c];
   }
 }
 
@@ -136,6 +127,7 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void adapter_shrink_kernel(
 template <int DT>
 __global__ __launch_bounds__(256) void adapter_dots_kernel(const int32_t* __restrict__ ids, int n,
                                                            const uint16_t* __restrict__ M,
+                                                           const float* __restrict__ scale,
                                                            const uint16_t* __restrict__ Z, int64_t ldz, int T, int C,
                                                            int r, float* __restrict__ V) {
   const int lane = threadIdx.x & 63;
@@ -154,6 +146,7 @@ __global__ __launch_bounds__(256) void adapter_dots_kernel(const int32_t* __rest
         z[i] = load16(rz, uint32_t(c0 + (i * 64 + lane) * 8) * 2u);
         m[i] = load16(rm, uint32_t(c0 + (i * 64 + lane) * 8) * 2u);
       }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -163,6 +156,7 @@ __global__ __launch_bounds__(256) void adapter_dots_kernel(const int32_t* __rest
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+    if (scale) sum *= scale[a];
   }
   if (lane == 0) V[dot] = sum;
 }
@@ -171,7 +165,7 @@ __global__ __launch_bounds__(256) void adapter_dots_kernel(const int32_t* __rest
 // Expand: Y[t][c] = base[t][c] + (low-rank term), base fp32 (Y itself or a
 // workspace).  A wave takes 16 tokens x 64 columns.
 // ---------------------------------------------------------------------------
-template <int DT, bool TRANS, int OUT>
+template <int DT, int OUT>
 __global__ __launch_bounds__(256) void adapter_expand_kernel(LowRank p, const float* base, int64_t ldb, void* Y,
                                                              int64_t ldy) {
   const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
@@ -189,10 +183,7 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(LowRank p, const fl
     else
       for (int e = 0; e < 4 && c + e < p.C; ++e) acc[f][e] = b[e];
   }
-  lowrank_term<DT, TRANS, 4>(p, t0, c0, [&](int f, const f32x4& d, bool mine) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[f][e] = mine ? acc[f][e] + d[e] : acc[f][e];
-  });
+  lowrank_add<DT, false, 4, 1>(p, t0, c0, [&](int f, int) -> f32x4& { return acc[f]; });
   if (t >= p.T) return;
 #pragma unroll
   for (int f = 0; f < 4; ++f) {
@@ -287,6 +278,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void adapter_grad_kernel(GradArgs 
 #pragma unroll
           for (int j = 0; j < CF; ++j) x[j][e] = z.Z[t * z.ldz + min(c0 + j * 16 + li, C - 1)];
         }
+        __builtin_amdgcn_sched_barrier(0);
         u32x4 vp[RF][3];
 #pragma unroll
         for (int i = 0; i < RF; ++i) {
@@ -346,35 +338,65 @@ __global__ __launch_bounds__(kGradWaves * 64) void adapter_grad_kernel(GradArgs 
 // row would be read by too many waves.
 constexpr int64_t kFewTokens = 16;
 
-template <int DT, bool TRANS>
-hipError_t shrink(const int32_t* ids, int64_t n, const uint16_t* M, const float* scale, const uint16_t* Z, int64_t ldz,
-                  int64_t T, int64_t C, int64_t r, float* V, hipStream_t s) {
-  if constexpr (!TRANS) {
-    if (T <= kFewTokens) {
-      hipLaunchKernelGGL((adapter_dots_kernel<DT>), dim3(unsigned((T * r + 3) / 4)), dim3(256), 0, s, ids, int(n), M, Z,
-                         ldz, int(T), int(C), int(r), V);
-      return hipGetLastError();
-    }
-  }
-  auto go = [&](auto kern, int rf) {
-    hipLaunchKernelGGL(kern, dim3(unsigned((T + 15) / 16), unsigned((r + rf * 16 - 1) / (rf * 16))),
-                       dim3(kShrinkWaves * 64), 0, s, ids, int(n), M, scale, Z, ldz, int(T), int(C), int(r), V);
-    return hipGetLastError();
-  };
-  // as many steps in flight as the 128 registers of a 1024-thread workgroup hold
-  if (r <= 16) return go(adapter_shrink_kernel<DT, TRANS, 1, 4>, 1);
-  if (r <= 32) return go(adapter_shrink_kernel<DT, TRANS, 2, TRANS ? 2 : 4>, 2);
-  return go(adapter_shrink_kernel<DT, TRANS, 4, TRANS ? 1 : 2>, 4);
+using ShrinkTile32 = GemmTile<32, 64, 2, 2, 4>;   // ranks x tokens, 48 KB: three workgroups a CU
+using ShrinkTile64 = GemmTile<64, 64, 4, 1, 4>;
+
+// Splits of the shrink's columns and their width: enough workgroups to cover
+// the chip twice, shares of at least 256 columns.
+struct ShrinkPlan {
+  int64_t splits, csplit;
+};
+ShrinkPlan shrink_plan(int64_t T, int64_t C, int64_t r) {
+  if (C == 0) return {0, 64};   // an empty sum
+  const int64_t tiles = (T + 63) / 64 * (r <= 32 ? 1 : (r + 63) / 64);
+  const int64_t want = std::min<int64_t>(std::max<int64_t>(512 / tiles, 1), std::max<int64_t>(C / 256, 1));
+  const int64_t csplit = ((C + want - 1) / want + 63) / 64 * 64;
+  return {(C + csplit - 1) / csplit, csplit};
 }
 
-template <int DT, bool TRANS>
+// Bytes of the shrink's shares (0: none are kept).
+size_t shrink_bytes(int64_t T, int64_t C, int64_t r) {
+  return T <= kFewTokens ? 0 : size_t(shrink_plan(T, C, r).splits) * size_t(T) * size_t(r) * 4;
+}
+
+template <int DT, class C>
+hipError_t launch_shrink(const ShrinkArgs& p, int64_t splits, hipStream_t s) {
+  auto kern = adapter_shrink_kernel<DT, C>;
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), C::LDS); e != hipSuccess) return e;
+  const int rank_tiles = (p.r + C::BM - 1) / C::BM;
+  // two adapters of a tile at a time, where there can be two
+  hipLaunchKernelGGL(kern, dim3(unsigned((p.T + 63) / 64 * rank_tiles), unsigned(splits), p.n > 1 ? 2u : 1u),
+                     dim3(C::THREADS), C::LDS, s, p, rank_tiles);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t shrink(const int32_t* ids, int64_t n, const uint16_t* M, const float* scale, const uint16_t* Z, int64_t ldz,
+                  int64_t T, int64_t C, int64_t r, float* part, float* V, hipStream_t s) {
+  if (T <= kFewTokens) {
+    hipLaunchKernelGGL((adapter_dots_kernel<DT>), dim3(unsigned((T * r + 3) / 4)), dim3(256), 0, s, ids, int(n), M,
+                       scale, Z, ldz, int(T), int(C), int(r), V);
+    return hipGetLastError();
+  }
+  const ShrinkPlan pl = shrink_plan(T, C, r);
+  const ShrinkArgs p{ids, M, Z, ldz, int(n), int(T), int(C), int(r), int(pl.csplit), part};
+  hipError_t e = hipSuccess;
+  if (n > 0 && pl.splits > 0)
+    e = r <= 32 ? launch_shrink<DT, ShrinkTile32>(p, pl.splits, s) : launch_shrink<DT, ShrinkTile64>(p, pl.splits, s);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(adapter_join_kernel, dim3(unsigned((T * r + 255) / 256)), dim3(256), 0, s, part, int(pl.splits),
+                     ids, int(n), scale, int(T), int(r), V);
+  return hipGetLastError();
+}
+
+template <int DT>
 hipError_t expand(const LowRank& p, const float* base, int64_t ldb, void* Y, int64_t ldy, int out_dtype,
                   hipStream_t s) {
   const dim3 grid(unsigned((p.T + 15) / 16), unsigned((p.C + 255) / 256));
   if (out_dtype == NM_F32)
-    hipLaunchKernelGGL((adapter_expand_kernel<DT, TRANS, NM_F32>), grid, dim3(256), 0, s, p, base, ldb, Y, ldy);
+    hipLaunchKernelGGL((adapter_expand_kernel<DT, NM_F32>), grid, dim3(256), 0, s, p, base, ldb, Y, ldy);
   else
-    hipLaunchKernelGGL((adapter_expand_kernel<DT, TRANS, DT>), grid, dim3(256), 0, s, p, base, ldb, Y, ldy);
+    hipLaunchKernelGGL((adapter_expand_kernel<DT, DT>), grid, dim3(256), 0, s, p, base, ldb, Y, ldy);
   return hipGetLastError();
 }
 
@@ -388,8 +410,10 @@ hipError_t gradients(GradArgs g, int64_t n, hipStream_t s) {
                        dim3(kGradWaves * 64), 0, s, g);
     return hipGetLastError();
   };
-  if (g.r <= 16) return go(adapter_grad_kernel<DT, 1, 4>, 1, 4);
-  if (g.r <= 32) return go(adapter_grad_kernel<DT, 2, 4>, 2, 4);
+  // 128 columns a workgroup where that still covers the chip, else 64
+  const bool wide = (int64_t(g.a.C) + g.b.C) / 128 * n >= 256;
+  if (g.r <= 16) return wide ? go(adapter_grad_kernel<DT, 1, 8>, 1, 8) : go(adapter_grad_kernel<DT, 1, 4>, 1, 4);
+  if (g.r <= 32) return wide ? go(adapter_grad_kernel<DT, 2, 8>, 2, 8) : go(adapter_grad_kernel<DT, 2, 4>, 2, 4);
   return go(adapter_grad_kernel<DT, 4, 4>, 4, 4);
 }
 
@@ -397,9 +421,15 @@ hipError_t gradients(GradArgs g, int64_t n, hipStream_t s) {
 // few-token family (T <= 16) and the all-LDS family (prefill, 2:4).
 bool fused_forward(const SpmmArgs& b) { return spmm_decode_applies(b) || spmm_lds_applies(b); }
 
+// Parts of the workspaces, each on 256 bytes.
+size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
 template <int DT>
 hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
-  hipError_t e = shrink<DT, false>(a.ids, a.n, a.A, nullptr, a.base.act, a.base.ldx, a.base.T, a.base.K, a.r, a.xa, s);
+  const int64_t T = a.base.T;
+  char* ws = static_cast<char*>(a.workspace);
+  hipError_t e = shrink<DT>(a.ids, a.n, a.A, nullptr, a.base.act, a.base.ldx, T, a.base.K, a.r,
+                            reinterpret_cast<float*>(ws), a.xa, s);
   if (e != hipSuccess || a.base.R == 0) return e;
   LowRank p;
   p.ids = a.ids;
@@ -408,31 +438,43 @@ hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
   p.V = a.xa;
   p.n = int(a.n);
   p.r = int(a.r);
-  p.T = int(a.base.T);
+  p.T = int(T);
   p.C = int(a.base.R);
   SpmmArgs b = a.base;
   if (fused_forward(b)) {
     b.lowrank = &p;
     return spmm_decode_applies(b) ? launch_spmm_decode(b, s) : launch_spmm_lds(b, s);
   }
-  // the product in fp32, in Y itself or in the workspace; then the low-rank term
+  // the product in fp32, in Y itself or in the workspace (where the shares are
+  // no longer needed); then the low-rank term
   if (a.base.out_dtype != NM_F32) {
-    b.Y = a.workspace;
+    b.Y = ws;
     b.ldy = a.base.R;
     b.out_dtype = NM_F32;
   }
   e = launch_spmm(b, s);
   if (e != hipSuccess) return e;
-  return expand<DT, false>(p, static_cast<const float*>(b.Y), b.ldy, a.base.Y, a.base.ldy, a.base.out_dtype, s);
+  return expand<DT>(p, static_cast<const float*>(b.Y), b.ldy, a.base.Y, a.base.ldy, a.base.out_dtype, s);
 }
 
 template <int DT>
 hipError_t backward_dt(const AdapterBwdArgs& a, hipStream_t s) {
   TrainArgs d = a.dx;
-  float* u = static_cast<float*>(a.workspace);
+  char* ws = static_cast<char*>(a.workspace);
+  float* u = reinterpret_cast<float*>(ws);
+  uint16_t* bt = reinterpret_cast<uint16_t*>(ws + padded(size_t(d.T) * a.r * 4));
+  float* part = reinterpret_cast<float*>(ws + padded(size_t(d.T) * a.r * 4) + padded(size_t(a.n) * a.r * d.R * 2));
   hipError_t e = hipSuccess;
-  if (d.T > 0) e = shrink<DT, true>(a.ids, a.n, a.B, a.scale, d.G, d.ldg, d.T, d.R, a.r, u, s);
-  if (e != hipSuccess) return e;
+  if (d.T > 0) {
+    if (a.n > 0 && d.R > 0) {
+      hipLaunchKernelGGL(adapter_transpose_kernel, dim3(unsigned((d.R + 63) / 64), unsigned((a.r + 31) / 32),
+                                                        unsigned(a.n)),
+                         dim3(256), 0, s, a.B, int(d.R), int(a.r), bt);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    e = shrink<DT>(a.ids, a.n, bt, a.scale, d.G, d.ldg, d.T, d.R, a.r, part, u, s);
+    if (e != hipSuccess) return e;
+  }
   if (d.out && d.T > 0) {
     LowRank p;
     p.ids = a.ids;
@@ -454,11 +496,14 @@ hipError_t backward_dt(const AdapterBwdArgs& a, hipStream_t s) {
 
 }  // namespace
 
-size_t adapter_workspace(const SpmmArgs& base) {
-  return base.out_dtype == NM_F32 || fused_forward(base) ? 0 : size_t(base.T) * size_t(base.R) * 4;
+size_t adapter_workspace(const SpmmArgs& base, int64_t r) {
+  const size_t y = base.out_dtype == NM_F32 || fused_forward(base) ? 0 : size_t(base.T) * size_t(base.R) * 4;
+  return std::max(shrink_bytes(base.T, base.K, r), y);
 }
 
-size_t adapter_bwd_workspace(int64_t T, int64_t r) { return size_t(T) * size_t(r) * 4; }
+size_t adapter_bwd_workspace(int64_t R, int64_t T, int64_t n, int64_t r) {
+  return padded(size_t(T) * r * 4) + padded(size_t(n) * r * R * 2) + shrink_bytes(T, R, r);
+}
 
 hipError_t launch_adapter(const AdapterArgs& a, hipStream_t s) {
   return a.base.dtype == NM_F16 ? forward_dt<NM_F16>(a, s) : forward_dt<NM_BF16>(a, s);

@@ -200,8 +200,8 @@ struct AdapterBwdArgs {
 };
 constexpr int64_t kAdapterMaxRank = 256, kAdapterMaxCount = 65535;
 constexpr int64_t kAdapterMaxTokens = int64_t(1) << 24, kAdapterMaxWidth = int64_t(1) << 22;   // grid limits
-size_t adapter_workspace(const SpmmArgs& base);   // pointers are not looked at
-size_t adapter_bwd_workspace(int64_t T, int64_t r);
+size_t adapter_workspace(const SpmmArgs& base, int64_t r);   // pointers are not looked at
+size_t adapter_bwd_workspace(int64_t R, int64_t T, int64_t n, int64_t r);
 hipError_t launch_adapter(const AdapterArgs& a, hipStream_t s);
 hipError_t launch_adapter_bwd(const AdapterBwdArgs& a, hipStream_t s);
 

@@ -139,48 +139,66 @@ __device__ inline void lowrank_columns4(const LowRank& p, int t, int c, f32x4& s
   for (int e = 0; e < 4; ++e) sum[e] += s * d[e];
 }
 
-// Calls add(f, d, mine) for every adapter that occurs among tokens t0 .. t0+15
-// and every fragment f < F (columns c0 + 16 f ..): d the fragment of the term, in
-// the matrix cores' result layout (lane (t, q): columns 4q .. 4q+3 of token t),
-// mine true where the lane's token uses that adapter.  The term of a token
-// that does not use the adapter is whatever the product gives, Inf and NaN
-// among it, so callers select on `mine` and never multiply by a mask.
-// Columns past C reread column C - 1.
-template <int DT, bool TRANS, int F, typename Add>
-__device__ inline void lowrank_term(const LowRank& p, int t0, int c0, Add&& add) {
+// acc(f, n) += the term, for F column fragments from c0 and NT token fragments
+// (16 NT <= 64 tokens) from t0, in the matrix cores' result layout (lane (i, q):
+// columns 4q .. 4q+3 of token i).  Every adapter that occurs among the tokens
+// takes one round: its operands are loaded once for all of them (one round for
+// a request's adjacent tokens, two where requests meet, 64 at worst).  With one
+// adapter the product accumulates in place; with several, each token takes the
+// sum of its own adapter's round by selection, never by a mask's product, so
+// Inf and NaN stay with their adapter's tokens.  The scale goes into V (one
+// fp32 rounding).  Columns past C and tokens past T reread the last one.
+template <int DT, bool TRANS, int F, int NT, typename Acc>
+__device__ inline void lowrank_add(const LowRank& p, int t0, int c0, Acc&& acc) {
   const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
-  const int t = t0 + li;
-  const int id = t < p.T ? p.ids[t] : -1;
-  uint32_t todo = uint32_t(__ballot(uint32_t(id) < uint32_t(p.n))) & 0xFFFFu;
-  const float* vrow = p.V + int64_t(min(t, p.T - 1)) * p.r;
+  if (t0 >= p.T) return;
+  const int id = p.ids[min(t0 + lane % (16 * NT), p.T - 1)];
+  uint64_t todo = __ballot(uint32_t(id) < uint32_t(p.n));
   while (todo) {
-    const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
-    const bool mine = id == a;
-    todo &= ~uint32_t(__ballot(mine));
+    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+    const uint64_t mine = __ballot(id == a);
+    todo &= ~mine;
     const uint16_t* Ma = p.M + int64_t(a) * p.r * p.C;
-    f32x4 d[F];
-#pragma unroll
-    for (int f = 0; f < F; ++f) d[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const float s = p.scale ? p.scale[a] : 1.f;
     for (int j = 0; j < p.r; j += 32) {
       const int j0 = j + 8 * lq;
-      float v[8];
-      load_v8(vrow, j0, p.r, v);
-      u32x4 vp[3];
-      split8(v, vp);
+      float v[NT][8];
+      u32x4 raw[F];
 #pragma unroll
-      for (int f = 0; f < F; ++f) {
-        const int c = min(c0 + 16 * f + li, p.C - 1);
-        u32x4 mp[operand_count<DT>()];
-        operand_parts<DT>(lowrank_operand<TRANS>(Ma, c, p.C, j0, p.r), mp);
-        d[f] = mfma_parts(mp, vp, d[f]);
+      for (int n = 0; n < NT; ++n) load_v8(p.V + int64_t(min(t0 + 16 * n + li, p.T - 1)) * p.r, j0, p.r, v[n]);
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+        raw[f] = lowrank_operand<TRANS>(Ma, min(c0 + 16 * f + li, p.C - 1), p.C, j0, p.r);
+      __builtin_amdgcn_sched_barrier(0);   // every load above in flight before the first use
+      u32x4 vp[NT][3];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[n][e] *= s;
+        split8(v[n], vp[n]);
       }
-    }
-    const float s = p.scale ? p.scale[a] : 1.f;
+      if (mine == ~uint64_t(0)) {
 #pragma unroll
-    for (int f = 0; f < F; ++f) {
+        for (int f = 0; f < F; ++f) {
+          u32x4 mp[operand_count<DT>()];
+          operand_parts<DT>(raw[f], mp);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) d[f][e] *= s;
-      add(f, d[f], mine);
+          for (int n = 0; n < NT; ++n) acc(f, n) = mfma_parts(mp, vp[n], acc(f, n));
+        }
+      } else {
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          u32x4 mp[operand_count<DT>()];
+          operand_parts<DT>(raw[f], mp);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const bool sel = (mine >> (16 * n + li)) & 1u;
+            const f32x4 d = mfma_parts(mp, vp[n], f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc(f, n)[e] = sel ? acc(f, n)[e] + d[e] : acc(f, n)[e];
+          }
+        }
+      }
     }
   }
 }

@@ -388,16 +388,14 @@ __global__ __launch_bounds__(256, 1) void spmm_lds_kernel(
       body(integral_constant<int, -2>{}, s + 1, 0, 0, a1, x1, b1, a0, x0, b0);
     }
 
-    // ---- the low-rank term, a token fragment at a time (its loads are waited
-    // for along with the next tile's, already in flight)
+    // ---- the low-rank term (its loads are waited for along with the next
+    // tile's, already in flight)
     if constexpr (std::is_same_v<LR, LowRank>) {
+      // in two halves: the next tile's fragments already take their registers
 #pragma unroll
-      for (int j = 0; j < FT; ++j)
-        lowrank_term<DT, false, FR>(lowrank, T0 + wt * (kBT / 2) + j * 16, R0 + wr * 128,
-                                    [&](int f, const f32x4& d, bool mine) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[f][j][e] = mine ? acc[f][j][e] + d[e] : acc[f][j][e];
-        });
+      for (int i = 0; i < FR; i += FR / 2)
+        lowrank_add<DT, false, FR / 2, FT>(lowrank, T0 + wt * (kBT / 2), R0 + wr * 128 + i * 16,
+                                           [&](int f, int n) -> f32x4& { return acc[i + f][n]; });
     }
 
     // ---- epilogue

@@ -306,15 +306,9 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
   if (c < nchunks) step(std::integral_constant<int, 0>{}, c);
   wait_vmcnt<0>();
 
-  // ---- the low-rank term, a token fragment at a time
-  if constexpr (std::is_same_v<LR, LowRank>) {
-#pragma unroll
-    for (int tf = 0; tf < 4; ++tf)
-      lowrank_term<DT, true, 4>(lowrank, T0 + wt * 64 + tf * 16, K0 + wk * 64, [&](int f, const f32x4& d, bool mine) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[f][tf][e] = mine ? acc[f][tf][e] + d[e] : acc[f][tf][e];
-      });
-  }
+  // ---- the low-rank term
+  if constexpr (std::is_same_v<LR, LowRank>)
+    lowrank_add<DT, true, 4, 4>(lowrank, T0 + wt * 64, K0 + wk * 64, [&](int f, int n) -> f32x4& { return acc[f][n]; });
 
   // ---- epilogue: lane (t = li, quarter q) holds rows 4q..4q+3 (k) of
   // column t of each fragment: 16 (fp32) or 8 (half) contiguous bytes of dX

@@ -285,6 +285,20 @@ def test_views_streams_and_empty():
     assert torch.equal(y1, nm.nm_spmm(d["values"], d["idx"], d["act"], c.K)) and not xa1.any()
 
 
+def test_no_rows():
+    # R == 0: nothing to write but xa; gradients through no rows are zeros
+    log("adapter R=0")
+    c = Case(64, 320, 40, 9, 3, "bf16")
+    d, G = c.dev()
+    e = dict(d, values=d["values"][:0], idx=d["idx"][:0], B=d["B"][:, :0].contiguous())
+    y, xa = nm.nm_adapter_spmm(**e, K=c.K)
+    _, ref = nm.nm_adapter_spmm(**d, K=c.K)
+    dx, dA, dB = nm.nm_adapter_spmm_bwd(G=G[:, :0], xa=xa, **e, K=c.K)
+    torch.cuda.synchronize()
+    assert y.shape == (40, 0) and torch.equal(xa, ref)
+    assert not dx.any() and not dA.any() and dB.shape == (3, 0, 9)
+
+
 def test_binding_refusals():
     c = Case(264, 320, 10, 9, 3, "bf16")
     d, G = c.dev()
