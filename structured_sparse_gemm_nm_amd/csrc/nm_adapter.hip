@@ -25,6 +25,7 @@
 #include "nm_lowrank.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace nm {
 namespace {
@@ -210,9 +211,13 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(LowRank p, const fl
 // RF*16 ranks and CF*16 columns.  The tokens are gone through 4096 at a time:
 // the workgroup marks each 32-token chunk's tokens of the adapter in LDS, the
 // chunks that hold any are dealt to the waves in turn, and in the end the
-// waves' tiles are added in a fixed order.  Tokens of other adapters enter as
-// zeros selected in both operands, so an Inf or NaN among them reaches nothing.
-// An adapter without tokens gets zeros.
+// waves' tiles are added in a fixed order.  The reduction runs over the rows of
+// Z, so a wave brings its chunk's tile into LDS (16 bytes a lane, rows as they
+// lie) and takes the operands out by transpose reads: picking them 2 bytes a
+// lane from memory spent 13 of 21 us issuing loads (2048 tokens, 4 adapters of
+// rank 32 on 4096 x 4096; GRAD_US now).  Tokens of other adapters enter as zeros
+// selected in both operands, so an Inf or NaN among them reaches nothing.  An
+// adapter without tokens gets zeros.
 // ---------------------------------------------------------------------------
 constexpr int kGradWaves = 8;
 constexpr int kGradSpan = 4096, kGradChunks = kGradSpan / 32;
@@ -231,9 +236,20 @@ struct GradArgs {
   GradSide a, b;        // dA, written [r][C]; dB, written [C][r]
 };
 
+// A wave's staged tile: token row t starts at P t + 128 (t >> 3 & 1) + 128 (t >> 4)
+// with P = 32 bytes past the row, so that the transpose reads of 32 lanes (rows
+// 8g + j) fall in distinct banks.
+template <int CF>
+struct GradTile {
+  static constexpr int PITCH = CF * 32 + 32;
+  __host__ __device__ static constexpr int row(int t) { return t * PITCH + (((t >> 3) & 1) + (t >> 4)) * 128; }
+  static constexpr int BYTES = (row(31) + CF * 32 + 15) / 16 * 16;
+};
+
 template <int DT, int RF, int CF>
 __global__ __launch_bounds__(kGradWaves * 64) void adapter_grad_kernel(GradArgs g) {
-  __shared__ f32x4 part[kGradWaves / 2][RF * CF][64];
+  using Tile = GradTile<CF>;
+  extern __shared__ __align__(16) unsigned char smem[];   // the waves' tiles; in the end their sums
   __shared__ uint32_t mark[kGradChunks];
   const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -241,67 +257,89 @@ __global__ __launch_bounds__(kGradWaves * 64) void adapter_grad_kernel(GradArgs 
   const GradSide& z = rank_minor ? g.b : g.a;
   const int c0 = (blockIdx.x - (rank_minor ? g.a.tiles : 0)) * (CF * 16), r0 = blockIdx.y * (RF * 16), a = blockIdx.z;
   const int r = g.r, C = z.C;
+  unsigned char* tile = smem + wave * Tile::BYTES;
   f32x4 acc[RF][CF];
 #pragma unroll
   for (int i = 0; i < RF; ++i)
 #pragma unroll
     for (int j = 0; j < CF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // this lane's piece of a row of the tile, and its row among those of a load
+  constexpr int PPR = CF * 2, RPL = 64 / PPR;   // 16-byte pieces a row, rows a load
+  const int piece = lane % PPR, prow = lane / PPR;
+  const bool inside = c0 + piece * 8 < C;       // C is a multiple of 8
+  // transpose reads: lane 16g + 4j + e reads token rows 8g + j and 8g + j + 4
+  const int tr_row = 8 * (lane >> 4) + ((lane >> 2) & 3);
+  const int tr_lo = Tile::row(tr_row) + 8 * (lane & 3), tr_hi = Tile::row(tr_row + 4) + 8 * (lane & 3);
 
   for (int64_t base = 0; base < g.T; base += kGradSpan) {
     __syncthreads();                      // the marks of the span before are read
 #pragma unroll
     for (int i = 0; i < kGradSpan / (kGradWaves * 64); ++i) {
-      const int k = (i * kGradWaves + wave) * 64 + lane;
-      const int64_t t = base + k;
+      const int64_t t = base + (i * kGradWaves + wave) * 64 + lane;
       const uint64_t in = __ballot(t < g.T && g.ids[t < g.T ? t : 0] == a);
       if (lane < 2) mark[(i * kGradWaves + wave) * 2 + lane] = uint32_t(in >> (32 * lane));
     }
     __syncthreads();
     // chunks that hold a token of the adapter, as two 64-bit maps
-    uint64_t some[2] = {__ballot(mark[lane] != 0), __ballot(mark[64 + lane] != 0)};
+    const uint64_t some[2] = {__ballot(mark[lane] != 0), __ballot(mark[64 + lane] != 0)};
     int turn = 0;
     for (int half = 0; half < 2; ++half) {
       for (uint64_t left = some[half]; left; left &= left - 1, ++turn) {
         if (turn % kGradWaves != wave) continue;
         const int chunk = half * 64 + __builtin_ctzll(left);
-        const uint32_t mine = (mark[chunk] >> (8 * lq)) & 0xFFu;   // this lane's 8 tokens
-        const int64_t t0 = base + chunk * 32 + 8 * lq;
+        const uint32_t mine = mark[chunk];
+        const int64_t t0 = base + chunk * 32;
         // loads are unconditional (tokens past T reread the last) and
         // selected afterwards, so that all are in flight together
         float v[RF][8];
-        uint32_t x[CF][8];
+        u32x4 x[32 / RPL];
+#pragma unroll
+        for (int k = 0; k < 32 / RPL; ++k) {
+          const int64_t t = min(t0 + k * RPL + prow, int64_t(g.T) - 1);
+          x[k] = inside ? *reinterpret_cast<const u32x4*>(z.Z + t * z.ldz + c0 + piece * 8) : u32x4{0u, 0u, 0u, 0u};
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int64_t t = t0 + e < g.T ? t0 + e : g.T - 1;
+          const int64_t t = min(t0 + 8 * lq + e, int64_t(g.T) - 1);
 #pragma unroll
           for (int i = 0; i < RF; ++i) v[i][e] = z.V[t * r + min(r0 + i * 16 + li, r - 1)];
-#pragma unroll
-          for (int j = 0; j < CF; ++j) x[j][e] = z.Z[t * z.ldz + min(c0 + j * 16 + li, C - 1)];
         }
         __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int k = 0; k < 32 / RPL; ++k) {
+          const int row = k * RPL + prow;
+          const bool sel = (mine >> row) & 1u;
+          u32x4 w;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = sel ? x[k][e] : 0u;
+          *reinterpret_cast<u32x4*>(tile + Tile::row(row) + piece * 16) = w;
+        }
         u32x4 vp[RF][3];
 #pragma unroll
         for (int i = 0; i < RF; ++i) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[i][e] = (mine >> e) & 1u ? v[i][e] : 0.f;
+          for (int e = 0; e < 8; ++e) v[i][e] = (mine >> (8 * lq + e)) & 1u ? v[i][e] : 0.f;
           split8(v[i], vp[i]);
         }
+        // a wave's LDS operations are carried out in order: no barrier
+        wait_lgkm0();
+        asm volatile("" ::: "memory");
 #pragma unroll
         for (int j = 0; j < CF; ++j) {
-          u32x4 raw, zp[operand_count<DT>()];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            raw[e] = ((mine >> (2 * e)) & 1u ? x[j][2 * e] : 0u) |
-                     ((mine >> (2 * e + 1)) & 1u ? x[j][2 * e + 1] << 16 : 0u);
-          operand_parts<DT>(raw, zp);
+          const u32x2 lo = lds_read_tr(tile + tr_lo + 32 * j), hi = lds_read_tr(tile + tr_hi + 32 * j);
+          u32x4 zp[operand_count<DT>()];
+          operand_parts<DT>(u32x4{lo[0], lo[1], hi[0], hi[1]}, zp);
 #pragma unroll
           for (int i = 0; i < RF; ++i) acc[i][j] = mfma_parts(vp[i], zp, acc[i][j]);
         }
+        wait_lgkm0();
+        asm volatile("" ::: "memory");   // the next chunk's writes stay behind these reads
       }
     }
   }
   __syncthreads();
   // waves 4..7 onto 0..3, 2..3 onto 0..1, 1 onto 0
+  f32x4 (*part)[RF * CF][64] = reinterpret_cast<f32x4 (*)[RF * CF][64]>(smem);
 #pragma unroll
   for (int half = kGradWaves / 2; half > 0; half >>= 1) {
     if (wave >= half && wave < 2 * half) {
@@ -402,19 +440,26 @@ hipError_t expand(const LowRank& p, const float* base, int64_t ldb, void* Y, int
 
 template <int DT>
 hipError_t gradients(GradArgs g, int64_t n, hipStream_t s) {
-  auto go = [&](auto kern, int rf, int cf) {
-    g.a.tiles = (g.a.C + cf * 16 - 1) / (cf * 16);
-    g.b.tiles = (g.b.C + cf * 16 - 1) / (cf * 16);
-    hipLaunchKernelGGL(kern, dim3(unsigned(g.a.tiles + g.b.tiles), unsigned((g.r + rf * 16 - 1) / (rf * 16)),
+  auto go = [&](auto kern, auto rfc, auto cfc) {
+    constexpr int RF = decltype(rfc)::value, CF = decltype(cfc)::value;
+    constexpr int lds = std::max(kGradWaves * GradTile<CF>::BYTES, kGradWaves / 2 * RF * CF * 1024);
+    if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), lds); e != hipSuccess) return e;
+    g.a.tiles = (g.a.C + CF * 16 - 1) / (CF * 16);
+    g.b.tiles = (g.b.C + CF * 16 - 1) / (CF * 16);
+    hipLaunchKernelGGL(kern, dim3(unsigned(g.a.tiles + g.b.tiles), unsigned((g.r + RF * 16 - 1) / (RF * 16)),
                                   unsigned(n)),
-                       dim3(kGradWaves * 64), 0, s, g);
+                       dim3(kGradWaves * 64), lds, s, g);
     return hipGetLastError();
   };
+  using one = std::integral_constant<int, 1>;
+  using two = std::integral_constant<int, 2>;
+  using four = std::integral_constant<int, 4>;
+  using eight = std::integral_constant<int, 8>;
   // 128 columns a workgroup where that still covers the chip, else 64
   const bool wide = (int64_t(g.a.C) + g.b.C) / 128 * n >= 256;
-  if (g.r <= 16) return wide ? go(adapter_grad_kernel<DT, 1, 8>, 1, 8) : go(adapter_grad_kernel<DT, 1, 4>, 1, 4);
-  if (g.r <= 32) return wide ? go(adapter_grad_kernel<DT, 2, 8>, 2, 8) : go(adapter_grad_kernel<DT, 2, 4>, 2, 4);
-  return go(adapter_grad_kernel<DT, 4, 4>, 4, 4);
+  if (g.r <= 16) return wide ? go(adapter_grad_kernel<DT, 1, 8>, one{}, eight{}) : go(adapter_grad_kernel<DT, 1, 4>, one{}, four{});
+  if (g.r <= 32) return wide ? go(adapter_grad_kernel<DT, 2, 8>, two{}, eight{}) : go(adapter_grad_kernel<DT, 2, 4>, two{}, four{});
+  return go(adapter_grad_kernel<DT, 4, 4>, four{}, four{});
 }
 
 // Whether the shared product's kernel adds the low-rank term itself: the

@@ -128,6 +128,16 @@ __device__ inline void dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_byte*)lds_dst, 16, int(voff), int(soff), 0, 0);
 }
 
+// One LDS transpose read (ds_read_b64_tr_b16): 4 halves a lane, exchanged within
+// each group of 16 lanes (lane 16g + 4a + b receives element b of what lane
+// 16g + 4j + a read, j = 0..3).
+typedef short v4s __attribute__((ext_vector_type(4)));
+
+__device__ inline u32x2 lds_read_tr(const unsigned char* p) {
+  const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(p));
+  return __builtin_bit_cast(u32x2, v);
+}
+
 // XCD-aware order of a 1-D grid: the hardware deals workgroups to the 8 XCDs
 // round robin, so workgroup p runs on XCD p % 8.  Of the largest multiple of 8
 // workgroups each XCD is given a contiguous run of logical tiles instead; the

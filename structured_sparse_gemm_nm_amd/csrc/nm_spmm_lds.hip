@@ -388,10 +388,9 @@ __global__ __launch_bounds__(256, 1) void spmm_lds_kernel(
       body(integral_constant<int, -2>{}, s + 1, 0, 0, a1, x1, b1, a0, x0, b0);
     }
 
-    // ---- the low-rank term (its loads are waited for along with the next
-    // tile's, already in flight)
+    // ---- the low-rank term, in two halves (the next tile's fragments already
+    // take their registers)
     if constexpr (std::is_same_v<LR, LowRank>) {
-      // in two halves: the next tile's fragments already take their registers
 #pragma unroll
       for (int i = 0; i < FR; i += FR / 2)
         lowrank_add<DT, false, FR / 2, FT>(lowrank, T0 + wt * (kBT / 2), R0 + wr * 128 + i * 16,

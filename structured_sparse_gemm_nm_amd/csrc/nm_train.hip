@@ -33,13 +33,6 @@
 namespace nm {
 namespace {
 
-typedef short v4s __attribute__((ext_vector_type(4)));
-
-__device__ inline u32x2 lds_read_tr(const unsigned char* p) {
-  const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(p));
-  return __builtin_bit_cast(u32x2, v);
-}
-
 constexpr int pat_n(int P) { return P == 0 ? 2 : 1; }
 constexpr int pat_m(int P) { return P == 2 ? 8 : 4; }
 
