@@ -88,37 +88,62 @@ __global__ __launch_bounds__(C::THREADS) void adapter_shrink_kernel(ShrinkArgs p
   }
 }
 
+// V = s times the sum of the shares, in order, and P = f V in parts (f the
+// adapter's scale if it belongs to the next product): a thread an element.
+// Tokens without an adapter get zeros in V; nothing reads their P.
 __global__ __launch_bounds__(256) void adapter_join_kernel(const float* __restrict__ part, int splits,
                                                            const int32_t* __restrict__ ids, int n,
-                                                           const float* __restrict__ scale, int T, int r,
-                                                           float* __restrict__ V) {
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, all = int64_t(T) * r;
-  if (i >= all) return;
-  const int a = ids[i / r];
+                                                           const float* __restrict__ now,
+                                                           const float* __restrict__ next, int T, int r,
+                                                           float* __restrict__ V, uint16_t* __restrict__ P) {
+  const int r8 = (r + 7) & ~7;
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= int64_t(T) * r8) return;
+  const int64_t t = i / r8, at = t * r + (i - t * r8), all = int64_t(T) * r;
+  const int j = int(i - t * r8), a = ids[t];
   float v = 0.f;
+  if (j < r) {
 #pragma unroll 8
-  for (int s = 0; s < splits; ++s) v += part[s * all + i];
-  V[i] = uint32_t(a) < uint32_t(n) ? (scale ? v * scale[a] : v) : 0.f;   // no adapter: zeros
+    for (int s = 0; s < splits; ++s) v += part[s * all + at];
+    const bool some = uint32_t(a) < uint32_t(n);
+    v = some ? (now ? v * now[a] : v) : 0.f;
+    V[at] = v;
+    if (some && next) v *= next[a];
+  }
+  store_parts(P + t * 3 * r8, r8, j, v);
 }
 
-// Mt[a][j][c] = M[a][c][j]: B's columns along the reduction of the backward
-// pass's shrink.  A workgroup takes 64 columns c and 32 ranks.
-__global__ __launch_bounds__(256) void adapter_transpose_kernel(const uint16_t* __restrict__ M, int C, int r,
-                                                                uint16_t* __restrict__ Mt) {
-  __shared__ uint16_t tile[32][64 + 2];
-  const int c0 = blockIdx.x * 64, j0 = blockIdx.y * 32;
-  const uint16_t* m = M + int64_t(blockIdx.z) * C * r;
-  uint16_t* mt = Mt + int64_t(blockIdx.z) * C * r;
+// Mt[a][j][c] = M[a][c][j] for M [n][C][r]: B's columns along the reduction of
+// the backward pass's shrink, and (with the roles of C and r exchanged) A's
+// ranks along that of its expand; one launch does both, the first tiles B's.
+// A workgroup takes 64 of the long and 32 of the short index.
+struct TransposeSide {
+  const uint16_t* M;
+  uint16_t* Mt;
+  int rows, cols;       // of M
+  int tiles;            // workgroups
+};
+
+__global__ __launch_bounds__(256) void adapter_transpose_kernel(TransposeSide first, TransposeSide second) {
+  __shared__ uint16_t tile[64][64 + 2];
+  const bool two = int(blockIdx.x) >= first.tiles;
+  const TransposeSide& s = two ? second : first;
+  const int b = blockIdx.x - (two ? first.tiles : 0), across = (s.cols + 63) / 64;
+  const int r0 = b / across * 64, c0 = b % across * 64;
+  const int64_t each = int64_t(s.rows) * s.cols;
+  const uint16_t* m = s.M + blockIdx.y * each;
+  uint16_t* mt = s.Mt + blockIdx.y * each;
+  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = (threadIdx.x >> 5) + 8 * i, j = threadIdx.x & 31;
-    if (c0 + c < C && j0 + j < r) tile[j][c] = m[int64_t(c0 + c) * r + j0 + j];
+  for (int i = 0; i < 16; ++i) {
+    const int row = r0 + y + 4 * i, col = c0 + x;
+    tile[y + 4 * i][x] = m[int64_t(min(row, s.rows - 1)) * s.cols + min(col, s.cols - 1)];
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int j = (threadIdx.x >> 6) + 4 * i, c = threadIdx.x & 63;
-    if (c0 + c < C && j0 + j < r) mt[int64_t(j0 + j) * C + c0 + c] = tile[j][c];
+  for (int i = 0; i < 16; ++i) {
+    const int col = c0 + y + 4 * i, row = r0 + x;
+    if (col < s.cols && row < s.rows) mt[int64_t(col) * s.rows + row] = tile[x][y + 4 * i];
   }
 }
 
@@ -128,9 +153,10 @@ __global__ __launch_bounds__(256) void adapter_transpose_kernel(const uint16_t* 
 template <int DT>
 __global__ __launch_bounds__(256) void adapter_dots_kernel(const int32_t* __restrict__ ids, int n,
                                                            const uint16_t* __restrict__ M,
-                                                           const float* __restrict__ scale,
+                                                           const float* __restrict__ now,
+                                                           const float* __restrict__ next,
                                                            const uint16_t* __restrict__ Z, int64_t ldz, int T, int C,
-                                                           int r, float* __restrict__ V) {
+                                                           int r, float* __restrict__ V, uint16_t* __restrict__ P) {
   const int lane = threadIdx.x & 63;
   const int dot = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (dot >= T * r) return;
@@ -157,9 +183,16 @@ __global__ __launch_bounds__(256) void adapter_dots_kernel(const int32_t* __rest
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
-    if (scale) sum *= scale[a];
+    if (now) sum *= now[a];
   }
-  if (lane == 0) V[dot] = sum;
+  if (lane != 0) return;
+  V[dot] = sum;
+  if (!P) return;
+  const int r8 = (r + 7) & ~7;
+  uint16_t* row = P + int64_t(t) * 3 * r8;
+  store_parts(row, r8, j, next && uint32_t(a) < uint32_t(n) ? sum * next[a] : sum);
+  if (j == r - 1)
+    for (int k = r; k < r8; ++k) store_parts(row, r8, k, 0.f);
 }
 
 // ---------------------------------------------------------------------------
@@ -184,7 +217,7 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(LowRank p, const fl
     else
       for (int e = 0; e < 4 && c + e < p.C; ++e) acc[f][e] = b[e];
   }
-  lowrank_add<DT, false, 4, 1>(p, t0, c0, [&](int f, int) -> f32x4& { return acc[f]; });
+  lowrank_add<DT, 4, 1>(p, lowrank_ids<1>(p, t0), t0, c0, [&](int f, int) -> f32x4& { return acc[f]; });
   if (t >= p.T) return;
 #pragma unroll
   for (int f = 0; f < 4; ++f) {
@@ -408,12 +441,14 @@ hipError_t launch_shrink(const ShrinkArgs& p, int64_t splits, hipStream_t s) {
   return hipGetLastError();
 }
 
+// V = now_a M Z and its parts for the next product, next_a V (P null: not wanted).
 template <int DT>
-hipError_t shrink(const int32_t* ids, int64_t n, const uint16_t* M, const float* scale, const uint16_t* Z, int64_t ldz,
-                  int64_t T, int64_t C, int64_t r, float* part, float* V, hipStream_t s) {
+hipError_t shrink(const int32_t* ids, int64_t n, const uint16_t* M, const float* now, const float* next,
+                  const uint16_t* Z, int64_t ldz, int64_t T, int64_t C, int64_t r, float* part, float* V, uint16_t* P,
+                  hipStream_t s) {
   if (T <= kFewTokens) {
     hipLaunchKernelGGL((adapter_dots_kernel<DT>), dim3(unsigned((T * r + 3) / 4)), dim3(256), 0, s, ids, int(n), M,
-                       scale, Z, ldz, int(T), int(C), int(r), V);
+                       now, next, Z, ldz, int(T), int(C), int(r), V, P);
     return hipGetLastError();
   }
   const ShrinkPlan pl = shrink_plan(T, C, r);
@@ -422,8 +457,8 @@ hipError_t shrink(const int32_t* ids, int64_t n, const uint16_t* M, const float*
   if (n > 0 && pl.splits > 0)
     e = r <= 32 ? launch_shrink<DT, ShrinkTile32>(p, pl.splits, s) : launch_shrink<DT, ShrinkTile64>(p, pl.splits, s);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(adapter_join_kernel, dim3(unsigned((T * r + 255) / 256)), dim3(256), 0, s, part, int(pl.splits),
-                     ids, int(n), scale, int(T), int(r), V);
+  hipLaunchKernelGGL(adapter_join_kernel, dim3(unsigned((T * ((r + 7) / 8 * 8) + 255) / 256)), dim3(256), 0, s, part,
+                     int(pl.splits), ids, int(n), now, next, int(T), int(r), V, P);
   return hipGetLastError();
 }
 
@@ -468,19 +503,25 @@ bool fused_forward(const SpmmArgs& b) { return spmm_decode_applies(b) || spmm_ld
 
 // Parts of the workspaces, each on 256 bytes.
 size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
+size_t parts_bytes(int64_t T, int64_t r) { return padded(size_t(T) * 3 * ((r + 7) / 8 * 8) * 2); }
 
 template <int DT>
 hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
   const int64_t T = a.base.T;
+  // the few-token family multiplies V itself
+  const bool few = spmm_decode_applies(a.base);
   char* ws = static_cast<char*>(a.workspace);
-  hipError_t e = shrink<DT>(a.ids, a.n, a.A, nullptr, a.base.act, a.base.ldx, T, a.base.K, a.r,
-                            reinterpret_cast<float*>(ws), a.xa, s);
+  uint16_t* P = few ? nullptr : reinterpret_cast<uint16_t*>(ws);
+  char* rest = ws + (few ? 0 : parts_bytes(T, a.r));   // the shares, and when they are joined the fp32 product
+  hipError_t e = shrink<DT>(a.ids, a.n, a.A, nullptr, a.scale, a.base.act, a.base.ldx, T, a.base.K, a.r,
+                            reinterpret_cast<float*>(rest), a.xa, P, s);
   if (e != hipSuccess || a.base.R == 0) return e;
   LowRank p;
   p.ids = a.ids;
   p.M = a.B;
   p.scale = a.scale;
   p.V = a.xa;
+  p.P = P;
   p.n = int(a.n);
   p.r = int(a.r);
   p.T = int(T);
@@ -488,12 +529,10 @@ hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
   SpmmArgs b = a.base;
   if (fused_forward(b)) {
     b.lowrank = &p;
-    return spmm_decode_applies(b) ? launch_spmm_decode(b, s) : launch_spmm_lds(b, s);
+    return few ? launch_spmm_decode(b, s) : launch_spmm_lds(b, s);
   }
-  // the product in fp32, in Y itself or in the workspace (where the shares are
-  // no longer needed); then the low-rank term
   if (a.base.out_dtype != NM_F32) {
-    b.Y = ws;
+    b.Y = rest;
     b.ldy = a.base.R;
     b.out_dtype = NM_F32;
   }
@@ -502,29 +541,51 @@ hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
   return expand<DT>(p, static_cast<const float*>(b.Y), b.ldy, a.base.Y, a.base.ldy, a.base.out_dtype, s);
 }
 
+// The backward pass's workspace: u, its parts, B and A transposed, the shares.
+struct BwdParts {
+  size_t u, p, bt, at, part, total;
+};
+BwdParts bwd_parts(int64_t R, int64_t K, int64_t T, int64_t n, int64_t r) {
+  BwdParts b;
+  b.u = 0;
+  b.p = b.u + padded(size_t(T) * r * 4);
+  b.bt = b.p + parts_bytes(T, r);
+  b.at = b.bt + padded(size_t(n) * r * R * 2);
+  b.part = b.at + padded(size_t(n) * r * K * 2);
+  b.total = b.part + shrink_bytes(T, R, r);
+  return b;
+}
+
 template <int DT>
 hipError_t backward_dt(const AdapterBwdArgs& a, hipStream_t s) {
   TrainArgs d = a.dx;
+  const BwdParts w = bwd_parts(d.R, d.K, d.T, a.n, a.r);
   char* ws = static_cast<char*>(a.workspace);
-  float* u = reinterpret_cast<float*>(ws);
-  uint16_t* bt = reinterpret_cast<uint16_t*>(ws + padded(size_t(d.T) * a.r * 4));
-  float* part = reinterpret_cast<float*>(ws + padded(size_t(d.T) * a.r * 4) + padded(size_t(a.n) * a.r * d.R * 2));
+  float* u = reinterpret_cast<float*>(ws + w.u);
+  uint16_t* P = reinterpret_cast<uint16_t*>(ws + w.p);
+  uint16_t* bt = reinterpret_cast<uint16_t*>(ws + w.bt);
+  uint16_t* at = reinterpret_cast<uint16_t*>(ws + w.at);
   hipError_t e = hipSuccess;
   if (d.T > 0) {
-    if (a.n > 0 && d.R > 0) {
-      hipLaunchKernelGGL(adapter_transpose_kernel, dim3(unsigned((d.R + 63) / 64), unsigned((a.r + 31) / 32),
-                                                        unsigned(a.n)),
-                         dim3(256), 0, s, a.B, int(d.R), int(a.r), bt);
+    if (a.n > 0) {
+      auto tiles = [](int64_t rows, int64_t cols) { return int((rows + 63) / 64 * ((cols + 63) / 64)); };
+      const TransposeSide tb{a.B, bt, int(d.R), int(a.r), tiles(d.R, a.r)};
+      const TransposeSide ta{a.A, at, int(a.r), int(d.K), d.out ? tiles(a.r, d.K) : 0};
+      if (tb.tiles + ta.tiles > 0)
+        hipLaunchKernelGGL(adapter_transpose_kernel, dim3(unsigned(tb.tiles + ta.tiles), unsigned(a.n)), dim3(256), 0,
+                           s, tb, ta);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    e = shrink<DT>(a.ids, a.n, bt, a.scale, d.G, d.ldg, d.T, d.R, a.r, part, u, s);
+    e = shrink<DT>(a.ids, a.n, bt, a.scale, nullptr, d.G, d.ldg, d.T, d.R, a.r, reinterpret_cast<float*>(ws + w.part),
+                   u, P, s);
     if (e != hipSuccess) return e;
   }
   if (d.out && d.T > 0) {
     LowRank p;
     p.ids = a.ids;
-    p.M = a.A;
+    p.M = at;
     p.V = u;
+    p.P = P;
     p.n = int(a.n);
     p.r = int(a.r);
     p.T = int(d.T);
@@ -542,12 +603,13 @@ hipError_t backward_dt(const AdapterBwdArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t adapter_workspace(const SpmmArgs& base, int64_t r) {
+  if (spmm_decode_applies(base)) return 0;
   const size_t y = base.out_dtype == NM_F32 || fused_forward(base) ? 0 : size_t(base.T) * size_t(base.R) * 4;
-  return std::max(shrink_bytes(base.T, base.K, r), y);
+  return parts_bytes(base.T, r) + std::max(shrink_bytes(base.T, base.K, r), y);
 }
 
-size_t adapter_bwd_workspace(int64_t R, int64_t T, int64_t n, int64_t r) {
-  return padded(size_t(T) * r * 4) + padded(size_t(n) * r * R * 2) + shrink_bytes(T, R, r);
+size_t adapter_bwd_workspace(int64_t R, int64_t K, int64_t T, int64_t n, int64_t r) {
+  return bwd_parts(R, K, T, n, r).total;
 }
 
 hipError_t launch_adapter(const AdapterArgs& a, hipStream_t s) {

@@ -1068,7 +1068,7 @@ nm_status nm_adapter_spmm_bwd_workspace_size(int64_t R, int64_t K, int n, int m,
   nm_status st = check_adapter(R, K, n, m, dtype, T, adapters, rank, out_dtype);
   if (st != NM_OK) return st;
   if (!bytes) return fail(NM_ERR_NULL, "bytes must be non-NULL");
-  *bytes = nm::adapter_bwd_workspace(R, T, adapters, rank);
+  *bytes = nm::adapter_bwd_workspace(R, K, T, adapters, rank);
   return ok();
 }
 
@@ -1092,7 +1092,7 @@ nm_status nm_adapter_spmm_bwd(const void* values, const uint32_t* idx, int64_t R
       !aligned16(B) || !aligned16(dX) || !aligned16(dA) || !aligned16(dB) || !aligned16(workspace) ||
       !aligned_to(adapter, 4) || !aligned_to(scale, 4))
     return fail(NM_ERR_ALIGN, "device pointers must be 16-byte aligned (adapter and scale: 4)");
-  const size_t need = nm::adapter_bwd_workspace(R, T, adapters, rank);
+  const size_t need = nm::adapter_bwd_workspace(R, K, T, adapters, rank);
   if (T > 0 && workspace_bytes < need)
     return fail(NM_ERR_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
   const Sizes z = sizes_of(R, K, n, m, dtype);

@@ -31,12 +31,14 @@ hipError_t launch_decompress_i8(const uint8_t* values, const uint32_t* idx, int6
                                 int64_t idx_row_words, uint8_t* W, int64_t ldw, hipStream_t s);
 
 // The low-rank term s_a sum_j M_a[c][j] V[t][j], a = ids[t], of a product's
-// columns c (nm_lowrank.h).
+// columns c (nm_lowrank.h).  The few-token kernels read V and scale, the
+// matrix-core kernels P.
 struct LowRank {
   const int32_t* ids = nullptr;   // [T]: the token's adapter; outside [0, n): none
-  const uint16_t* M = nullptr;    // [n][C][r], or [n][r][C] where the user says so
+  const uint16_t* M = nullptr;    // [n][C][r]
   const float* scale = nullptr;   // [n], or null: 1
   const float* V = nullptr;       // [T][r]
+  const uint16_t* P = nullptr;    // [T][3][r8]: s_a V in three bf16 parts, zeros from r to r8 (r rounded up to 8)
   int n = 0, r = 0, T = 0;
   int C = 0;                      // columns of the product
 };
@@ -80,7 +82,7 @@ struct TrainArgs {
   void* out;               // dX [T, K] (ldo) or dW [R, S] (contiguous)
   int64_t ldo;
   int out_dtype;           // NM_F32 or dtype
-  const LowRank* lowrank = nullptr;   // dX only: added in the epilogue, M as [n][r][K]
+  const LowRank* lowrank = nullptr;   // dX only: added in the epilogue
 };
 hipError_t launch_spmm_dx(const TrainArgs& a, hipStream_t s);
 hipError_t launch_spmm_dw(const TrainArgs& a, hipStream_t s);
@@ -201,7 +203,7 @@ struct AdapterBwdArgs {
 constexpr int64_t kAdapterMaxRank = 256, kAdapterMaxCount = 65535;
 constexpr int64_t kAdapterMaxTokens = int64_t(1) << 24, kAdapterMaxWidth = int64_t(1) << 22;   // grid limits
 size_t adapter_workspace(const SpmmArgs& base, int64_t r);   // pointers are not looked at
-size_t adapter_bwd_workspace(int64_t R, int64_t T, int64_t n, int64_t r);
+size_t adapter_bwd_workspace(int64_t R, int64_t K, int64_t T, int64_t n, int64_t r);
 hipError_t launch_adapter(const AdapterArgs& a, hipStream_t s);
 hipError_t launch_adapter_bwd(const AdapterBwdArgs& a, hipStream_t s);
 

@@ -67,32 +67,42 @@ __device__ inline f32x4 mfma_parts(const u32x4 (&a)[NA], const u32x4 (&b)[NB], f
   return acc;
 }
 
-// Operand lane (row c, quarter q) of M: elements j0 .. j0 + 7 (zeros past r).
-// TRANS: M is [r][C], the lane's elements lie C apart.
-template <bool TRANS>
-__device__ inline u32x4 lowrank_operand(const uint16_t* Ma, int c, int64_t C, int j0, int r) {
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (j0 >= r) return v;
-  if constexpr (TRANS) {
-    const uint16_t* p = Ma + int64_t(j0) * C + c;
+// s V as P's parts, the form the matrix cores take it in: part k of element j
+// at row[k * r8 + j].
+__device__ inline void store_parts(uint16_t* row, int r8, int j, float f) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t x = j0 + e < r ? p[int64_t(e) * C] : 0u;
-      v[e >> 1] |= x << (16 * (e & 1));
-    }
-  } else {
-    const uint16_t* p = Ma + int64_t(c) * r + j0;
-    if ((r & 7) == 0) {
-      v = *reinterpret_cast<const u32x4*>(p);
-    } else {
+  for (int k = 0; k < 3; ++k) {
+    const uint16_t h = to_half_bits<NM_BF16>(f);
+    row[k * r8 + j] = h;
+    f -= half_to_f32<NM_BF16>(h);
+    f = fabsf(f) < __builtin_inff() ? f : 0.f;   // what is not finite stays in the first part alone
+  }
+}
+
+// Offset past every descriptor here: a load from it returns zeros.
+constexpr uint32_t kLowRankDead = 0xFFFFFFF0u;
+
+// Operand lane (row c, quarter q) of an adapter's M (its descriptor): elements
+// j0 .. j0 + 7, zeros past r.  No branch over the lanes, so that a tile's loads
+// are issued together.
+__device__ inline u32x4 lowrank_operand(__amdgpu_buffer_rsrc_t rm, int c, int j0, int r) {
+  const uint32_t at = (uint32_t(c) * uint32_t(r) + uint32_t(j0)) * 2u;
+  if ((r & 7) == 0)
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rm, j0 < r ? at : kLowRankDead, 0, 0));
+  u32x4 v;   // rows not on 16 bytes: element by element
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t x = j0 + e < r ? p[e] : 0u;
-        v[e >> 1] |= x << (16 * (e & 1));
-      }
-    }
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b16(rm, j0 + 2 * e < r ? at + 4u * e : kLowRankDead, 0, 0);
+    const uint32_t hi =
+        __builtin_amdgcn_raw_buffer_load_b16(rm, j0 + 2 * e + 1 < r ? at + 4u * e + 2u : kLowRankDead, 0, 0);
+    v[e] = lo | (hi << 16);
   }
   return v;
+}
+
+// An adapter's M.
+__device__ inline __amdgpu_buffer_rsrc_t lowrank_rsrc(const LowRank& p, int a) {
+  return make_rsrc(p.M + int64_t(a) * p.r * p.C, uint32_t(p.r) * uint32_t(p.C) * 2u);
 }
 
 // Elements j0 .. j0 + 7 of a row of r floats, zeros past r.
@@ -113,13 +123,13 @@ __device__ inline void load_v8(const float* row, int j0, int r, float (&v)[8]) {
 // sum[e] += s_a sum_j M_a[c + e][j] V[t][j] for 4 columns of one token, on the
 // vector ALUs: for few tokens, where every token has its own adapter and a
 // matrix-core fragment would hold one column of use.  Columns past C reread
-// column C - 1.  M as [n][C][r].
+// column C - 1.
 template <int DT>
 __device__ inline void lowrank_columns4(const LowRank& p, int t, int c, f32x4& sum) {
   const int a = p.ids[t];
   if (uint32_t(a) >= uint32_t(p.n)) return;
   const float s = p.scale ? p.scale[a] : 1.f;
-  const uint16_t* Ma = p.M + int64_t(a) * p.r * p.C;
+  const __amdgpu_buffer_rsrc_t rm = lowrank_rsrc(p, a);
   const float* vrow = p.V + int64_t(t) * p.r;
   f32x4 d = {0.f, 0.f, 0.f, 0.f};
   for (int j = 0; j < p.r; j += 8) {
@@ -127,7 +137,7 @@ __device__ inline void lowrank_columns4(const LowRank& p, int t, int c, f32x4& s
     load_v8(vrow, j, p.r, v);
     u32x4 m[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) m[e] = lowrank_operand<false>(Ma, min(c + e, p.C - 1), p.C, j, p.r);
+    for (int e = 0; e < 4; ++e) m[e] = lowrank_operand(rm, min(c + e, p.C - 1), j, p.r);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -139,44 +149,50 @@ __device__ inline void lowrank_columns4(const LowRank& p, int t, int c, f32x4& s
   for (int e = 0; e < 4; ++e) sum[e] += s * d[e];
 }
 
+// The adapters of a tile of 16 NT tokens, a lane a token (tokens past T count
+// as the last); loaded early by the kernels that add the term late.
+template <int NT>
+__device__ inline int lowrank_ids(const LowRank& p, int t0) {
+  return p.ids[min(t0 + int(threadIdx.x & 63) % (16 * NT), p.T - 1)];
+}
+
 // acc(f, n) += the term, for F column fragments from c0 and NT token fragments
 // (16 NT <= 64 tokens) from t0, in the matrix cores' result layout (lane (i, q):
-// columns 4q .. 4q+3 of token i).  Every adapter that occurs among the tokens
-// takes one round: its operands are loaded once for all of them (one round for
-// a request's adjacent tokens, two where requests meet, 64 at worst).  With one
-// adapter the product accumulates in place; with several, each token takes the
-// sum of its own adapter's round by selection, never by a mask's product, so
-// Inf and NaN stay with their adapter's tokens.  The scale goes into V (one
-// fp32 rounding).  Columns past C and tokens past T reread the last one.
-template <int DT, bool TRANS, int F, int NT, typename Acc>
-__device__ inline void lowrank_add(const LowRank& p, int t0, int c0, Acc&& acc) {
+// columns 4q .. 4q+3 of token i); id from lowrank_ids.  Every adapter that
+// occurs among the tokens takes one round: its operands are loaded once for all
+// of them (one round for a request's adjacent tokens, two where requests meet,
+// 64 at worst).  With one adapter the product accumulates in place; with
+// several, each token takes the sum of its own adapter's round by selection,
+// never by a mask's product, so Inf and NaN stay with their adapter's tokens.
+// Columns past C and tokens past T reread the last one.
+template <int DT, int F, int NT, typename Acc>
+__device__ inline void lowrank_add(const LowRank& p, int id, int t0, int c0, Acc&& acc) {
   const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
   if (t0 >= p.T) return;
-  const int id = p.ids[min(t0 + lane % (16 * NT), p.T - 1)];
+  const int r8 = (p.r + 7) & ~7;
+  const int rows = min(16 * NT, p.T - t0);
+  const __amdgpu_buffer_rsrc_t rp = make_rsrc(p.P + int64_t(t0) * 3 * r8, uint32_t(rows) * 3u * uint32_t(r8) * 2u);
   uint64_t todo = __ballot(uint32_t(id) < uint32_t(p.n));
   while (todo) {
     const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
     const uint64_t mine = __ballot(id == a);
     todo &= ~mine;
-    const uint16_t* Ma = p.M + int64_t(a) * p.r * p.C;
-    const float s = p.scale ? p.scale[a] : 1.f;
+    const __amdgpu_buffer_rsrc_t rm = lowrank_rsrc(p, a);
     for (int j = 0; j < p.r; j += 32) {
       const int j0 = j + 8 * lq;
-      float v[NT][8];
-      u32x4 raw[F];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) load_v8(p.V + int64_t(min(t0 + 16 * n + li, p.T - 1)) * p.r, j0, p.r, v[n]);
-#pragma unroll
-      for (int f = 0; f < F; ++f)
-        raw[f] = lowrank_operand<TRANS>(Ma, min(c0 + 16 * f + li, p.C - 1), p.C, j0, p.r);
-      __builtin_amdgcn_sched_barrier(0);   // every load above in flight before the first use
-      u32x4 vp[NT][3];
+      u32x4 vp[NT][3], raw[F];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
+        const uint32_t at = (uint32_t(min(16 * n + li, rows - 1)) * 3u * uint32_t(r8) + uint32_t(j0)) * 2u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[n][e] *= s;
-        split8(v[n], vp[n]);
+        for (int k = 0; k < 3; ++k)
+          vp[n][k] = __builtin_bit_cast(
+              u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                         rp, j0 < p.r ? at + uint32_t(k) * uint32_t(r8) * 2u : kLowRankDead, 0, 0));
       }
+#pragma unroll
+      for (int f = 0; f < F; ++f) raw[f] = lowrank_operand(rm, min(c0 + 16 * f + li, p.C - 1), j0, p.r);
+      __builtin_amdgcn_sched_barrier(0);   // every load above in flight before the first use
       if (mine == ~uint64_t(0)) {
 #pragma unroll
         for (int f = 0; f < F; ++f) {

@@ -357,6 +357,8 @@ __global__ __launch_bounds__(256, 1) void spmm_lds_kernel(
   read_frags(0, 0, 0, a0, x0, b0);
 
   while (true) {
+    [[maybe_unused]] int ids = 0;
+    if constexpr (std::is_same_v<LR, LowRank>) ids = lowrank_ids<FT>(lowrank, T0 + wt * (kBT / 2));
 #pragma unroll
     for (int i = 0; i < FR; ++i)
 #pragma unroll
@@ -393,8 +395,8 @@ __global__ __launch_bounds__(256, 1) void spmm_lds_kernel(
     if constexpr (std::is_same_v<LR, LowRank>) {
 #pragma unroll
       for (int i = 0; i < FR; i += FR / 2)
-        lowrank_add<DT, false, FR / 2, FT>(lowrank, T0 + wt * (kBT / 2), R0 + wr * 128 + i * 16,
-                                           [&](int f, int n) -> f32x4& { return acc[i + f][n]; });
+        lowrank_add<DT, FR / 2, FT>(lowrank, ids, T0 + wt * (kBT / 2), R0 + wr * 128 + i * 16,
+                                    [&](int f, int n) -> f32x4& { return acc[i + f][n]; });
     }
 
     // ---- epilogue

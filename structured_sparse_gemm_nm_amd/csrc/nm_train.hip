@@ -246,6 +246,8 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
     pack_offsets(chunk, vo, i0, i1);
     dx_load<P>(d, rv, ri, vo, i0, i1);
   };
+  [[maybe_unused]] int ids = 0;
+  if constexpr (std::is_same_v<LR, LowRank>) ids = lowrank_ids<4>(lowrank, T0 + wt * 64);
   load_g(0, gs[0]);
   load_pack(0, pk[0]);
   load_g(1, gs[1]);
@@ -301,7 +303,7 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
 
   // ---- the low-rank term
   if constexpr (std::is_same_v<LR, LowRank>)
-    lowrank_add<DT, true, 4, 4>(lowrank, T0 + wt * 64, K0 + wk * 64, [&](int f, int n) -> f32x4& { return acc[f][n]; });
+    lowrank_add<DT, 4, 4>(lowrank, ids, T0 + wt * 64, K0 + wk * 64, [&](int f, int n) -> f32x4& { return acc[f][n]; });
 
   // ---- epilogue: lane (t = li, quarter q) holds rows 4q..4q+3 (k) of
   // column t of each fragment: 16 (fp32) or 8 (half) contiguous bytes of dX
