@@ -160,8 +160,8 @@ def _torch_dtype(code: int):
 
 
 def _stream_ptr(device) -> int:
-    torch = _torch()
-    return int(torch.cuda.current_stream(device).cuda_stream)
+    # torch.cuda.current_stream(device).cuda_stream without the Stream object (1.7 us a call)
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
 def _require_cuda(*ts):
@@ -654,14 +654,14 @@ def _row_stride(t):
 
 
 def _vector(t, name, size, dtype, device):
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != (size,) or not t.is_contiguous()
+    if t is not None and (t.dtype != dtype or t.shape != (size,) or not t.is_contiguous()
                           or t.device != device):
         raise ValueError(f"{name} must be a contiguous {dtype} [{size}] tensor on {device}")
 
 
 def _matrix(t, name, rows, cols, dtype, device):
     _row_major(t, name)
-    if t.dtype != dtype or tuple(t.shape) != (rows, cols) or t.device != device:
+    if t.dtype != dtype or t.shape != (rows, cols) or t.device != device:
         raise ValueError(f"{name} must be a [{rows}, {cols}] {dtype} tensor on {device}")
 
 
@@ -726,22 +726,45 @@ def nm_layernorm_bwd(dy, x, mean, rstd, weight=None, out_dtype=None, affine: boo
 # low-rank adapters beside a shared projection
 # --------------------------------------------------------------------------
 
-def _check_adapters(values, idx, act, adapter, A, B, scale, K, n, m, dt):
-    """Tensors of both passes; returns (R, T, adapters, rank)."""
+def _check_adapters(values, idx, act, adapter, A, B, scale, K, n, m):
+    """Tensors of both passes; returns (R, T, adapters, rank).  One decoded token spends
+    longer here than on the GPU, so this checks plain attributes once each."""
     torch = _torch()
     R, T = values.shape[0], act.shape[0]
-    _check_packed(values, idx, R, K, n, m, dt)
-    _matrix(act, "act", T, K, values.dtype, values.device)
-    _vector(adapter, "adapter", T, torch.int32, values.device)
-    if A.dim() != 3 or A.shape[2] != K or A.dtype != values.dtype or not A.is_contiguous() \
-            or A.device != values.device:
-        raise ValueError(f"A must be a contiguous [adapters, rank, {K}] {values.dtype} tensor on {values.device}")
+    dt, dev = values.dtype, values.device
+    if (n, m) not in PATTERNS:
+        nm_packed_sizes(R, K, n, m)     # raises
+    S = K // m * n
+    words = (S * (3 if m == 8 else 2) + 31) // 32
+    if values.shape != (R, S) or not values.is_contiguous():
+        raise ValueError(f"values must be a contiguous [{R}, {S}] tensor, got {tuple(values.shape)}")
+    if idx.dtype != torch.int32 or idx.shape != (R, words) or not idx.is_contiguous():
+        raise ValueError(f"idx must be a contiguous int32 [{R}, {words}] tensor, got {idx.dtype} {tuple(idx.shape)}")
+    _matrix(act, "act", T, K, dt, dev)
+    _vector(adapter, "adapter", T, torch.int32, dev)
+    if A.dim() != 3 or A.shape[2] != K or A.dtype != dt or not A.is_contiguous() or A.device != dev:
+        raise ValueError(f"A must be a contiguous [adapters, rank, {K}] {dt} tensor on {dev}")
     na, r = A.shape[0], A.shape[1]
-    if tuple(B.shape) != (na, R, r) or B.dtype != values.dtype or not B.is_contiguous() or B.device != values.device:
-        raise ValueError(f"B must be a contiguous [{na}, {R}, {r}] {values.dtype} tensor on {values.device}")
-    _vector(scale, "scale", na, torch.float32, values.device)
-    _require_cuda(values, idx, act, adapter, A, B, scale)
+    if B.shape != (na, R, r) or B.dtype != dt or not B.is_contiguous() or B.device != dev:
+        raise ValueError(f"B must be a contiguous [{na}, {R}, {r}] {dt} tensor on {dev}")
+    _vector(scale, "scale", na, torch.float32, dev)
+    if idx.device != dev:
+        raise ValueError("values and idx must be on one device")
+    _require_cuda(values)
     return R, T, na, r
+
+
+def _adapter_out_dtype(values, out_dtype):
+    """(dtype codes of the weights and the output, the output's torch dtype)."""
+    torch = _torch()
+    dt = _dtype_code(values)
+    if dt not in (NM_F16, NM_BF16):
+        raise TypeError("adapters take float16 or bfloat16 weights")
+    if out_dtype is None or out_dtype == torch.float32:
+        return dt, NM_F32, torch.float32
+    if out_dtype != values.dtype:
+        raise TypeError("out_dtype must be float32 or the weights' dtype")
+    return dt, dt, out_dtype
 
 
 def _workspace(size_of, *args, device):
@@ -758,13 +781,12 @@ def nm_adapter_spmm(values, idx, act, adapter, A, B, scale, K: int, n: int = 2, 
     xa float32, kept for nm_adapter_spmm_bwd."""
     torch = _torch()
     _row_major(act, "act")
-    dt = _dtype_code(values)
-    od = _train_out_dtype(torch, dt, out_dtype)
-    R, T, na, r = _check_adapters(values, idx, act, adapter, A, B, scale, K, n, m, dt)
+    dt, od, otype = _adapter_out_dtype(values, out_dtype)
+    R, T, na, r = _check_adapters(values, idx, act, adapter, A, B, scale, K, n, m)
     if out is not None:
-        _matrix(out, "out", T, R, _torch_dtype(od), act.device)
+        _matrix(out, "out", T, R, otype, act.device)
     else:
-        out = torch.empty((T, R), dtype=_torch_dtype(od), device=act.device)
+        out = torch.empty((T, R), dtype=otype, device=act.device)
     if xa is None:
         xa = torch.empty((T, r), dtype=torch.float32, device=act.device)
     elif xa.dtype != torch.float32 or tuple(xa.shape) != (T, r) or not xa.is_contiguous() or xa.device != act.device:
@@ -785,18 +807,17 @@ def nm_adapter_spmm_bwd(values, idx, G, act, xa, adapter, A, B, scale, K: int, n
     token uses."""
     torch = _torch()
     _row_major(act, "act")
-    dt = _dtype_code(values)
-    od = _train_out_dtype(torch, dt, out_dtype)
-    R, T, na, r = _check_adapters(values, idx, act, adapter, A, B, scale, K, n, m, dt)
+    dt, od, otype = _adapter_out_dtype(values, out_dtype)
+    R, T, na, r = _check_adapters(values, idx, act, adapter, A, B, scale, K, n, m)
     _matrix(G, "G", T, R, values.dtype, values.device)
     if xa.dtype != torch.float32 or tuple(xa.shape) != (T, r) or not xa.is_contiguous() or xa.device != act.device:
         raise ValueError(f"xa must be a contiguous float32 [{T}, {r}] tensor on {act.device}")
     if not need_dx:
         out = None
     elif out is not None:
-        _matrix(out, "out", T, K, _torch_dtype(od), act.device)
+        _matrix(out, "out", T, K, otype, act.device)
     else:
-        out = torch.empty((T, K), dtype=_torch_dtype(od), device=act.device)
+        out = torch.empty((T, K), dtype=otype, device=act.device)
     dA = torch.empty((na, r, K), dtype=torch.float32, device=act.device)
     dB = torch.empty((na, R, r), dtype=torch.float32, device=act.device)
     L = lib()

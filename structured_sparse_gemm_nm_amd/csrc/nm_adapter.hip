@@ -88,29 +88,48 @@ __global__ __launch_bounds__(C::THREADS) void adapter_shrink_kernel(ShrinkArgs p
   }
 }
 
-// V = s times the sum of the shares, in order, and P = f V in parts (f the
-// adapter's scale if it belongs to the next product): a thread an element.
-// Tokens without an adapter get zeros in V; nothing reads their P.
-__global__ __launch_bounds__(256) void adapter_join_kernel(const float* __restrict__ part, int splits,
-                                                           const int32_t* __restrict__ ids, int n,
-                                                           const float* __restrict__ now,
-                                                           const float* __restrict__ next, int T, int r,
-                                                           float* __restrict__ V, uint16_t* __restrict__ P) {
+// One of the join's jobs: value = now_a sum of `splits` shares [T][r], in
+// order; zero for a token without an adapter.  Written where wanted: the fp32
+// value; next_a value in three bf16 parts, [T][3][r8] for the products over
+// ranks (lowrank_add) and [3][r][ldt] for those over tokens (the gradients).
+struct JoinJob {
+  const float* part;
+  int splits;
+  const float* now;     // or null: 1
+  const float* next;    // or null: 1
+  float* V;
+  uint16_t* P;
+  uint16_t* PT;
+};
+
+// A thread an element (j runs to r8, where P holds zeros); blockIdx.y is the job.
+__global__ __launch_bounds__(256) void adapter_join_kernel(JoinJob first, JoinJob second,
+                                                           const int32_t* __restrict__ ids, int n, int T, int r,
+                                                           int ldt) {
+  const JoinJob& q = blockIdx.y ? second : first;
   const int r8 = (r + 7) & ~7;
   const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (i >= int64_t(T) * r8) return;
-  const int64_t t = i / r8, at = t * r + (i - t * r8), all = int64_t(T) * r;
-  const int j = int(i - t * r8), a = ids[t];
+  const int64_t t = i / r8, all = int64_t(T) * r;
+  const int j = int(i - t * r8);
   float v = 0.f;
   if (j < r) {
+    const int64_t at = t * r + j;
+    const int a = ids[t];
 #pragma unroll 8
-    for (int s = 0; s < splits; ++s) v += part[s * all + at];
+    for (int s = 0; s < q.splits; ++s) v += q.part[s * all + at];
     const bool some = uint32_t(a) < uint32_t(n);
-    v = some ? (now ? v * now[a] : v) : 0.f;
-    V[at] = v;
-    if (some && next) v *= next[a];
+    v = some ? (q.now ? v * q.now[a] : v) : 0.f;
+    if (q.V) q.V[at] = v;
+    if (some && q.next) v *= q.next[a];
   }
-  store_parts(P + t * 3 * r8, r8, j, v);
+  uint16_t h[3];
+  split3(v, h);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    if (q.P) q.P[(t * 3 + k) * r8 + j] = h[k];
+    if (q.PT && j < r) q.PT[(int64_t(k) * r + j) * ldt + t] = h[k];
+  }
 }
 
 // Mt[a][j][c] = M[a][c][j] for M [n][C][r]: B's columns along the reduction of
@@ -154,9 +173,8 @@ template <int DT>
 __global__ __launch_bounds__(256) void adapter_dots_kernel(const int32_t* __restrict__ ids, int n,
                                                            const uint16_t* __restrict__ M,
                                                            const float* __restrict__ now,
-                                                           const float* __restrict__ next,
                                                            const uint16_t* __restrict__ Z, int64_t ldz, int T, int C,
-                                                           int r, float* __restrict__ V, uint16_t* __restrict__ P) {
+                                                           int r, float* __restrict__ V) {
   const int lane = threadIdx.x & 63;
   const int dot = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (dot >= T * r) return;
@@ -185,14 +203,7 @@ __global__ __launch_bounds__(256) void adapter_dots_kernel(const int32_t* __rest
     for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
     if (now) sum *= now[a];
   }
-  if (lane != 0) return;
-  V[dot] = sum;
-  if (!P) return;
-  const int r8 = (r + 7) & ~7;
-  uint16_t* row = P + int64_t(t) * 3 * r8;
-  store_parts(row, r8, j, next && uint32_t(a) < uint32_t(n) ? sum * next[a] : sum);
-  if (j == r - 1)
-    for (int k = r; k < r8; ++k) store_parts(row, r8, k, 0.f);
+  if (lane == 0) V[dot] = sum;
 }
 
 // ---------------------------------------------------------------------------
@@ -238,26 +249,26 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(LowRank p, const fl
 }
 
 // ---------------------------------------------------------------------------
-// Gradients: D_a[j][c] = s_a sum_{t in a} V[t][j] Z[t][c], written [r][C] (dA,
-// Z = x, V = u) or [C][r] (dB, Z = g, V = xa); one launch does both, the first
+// Gradients: D_a[j][c] = sum_{t in a} V[t][j] Z[t][c], written [r][C] (dA, Z =
+// x, V = u) or [C][r] (dB, Z = g, V = s xa); one launch does both, the first
 // column tiles dA's, the rest dB's.  A workgroup of 8 waves owns one adapter,
 // RF*16 ranks and CF*16 columns.  The tokens are gone through 4096 at a time:
-// the workgroup marks each 32-token chunk's tokens of the adapter in LDS, the
-// chunks that hold any are dealt to the waves in turn, and in the end the
-// waves' tiles are added in a fixed order.  The reduction runs over the rows of
-// Z, so a wave brings its chunk's tile into LDS (16 bytes a lane, rows as they
-// lie) and takes the operands out by transpose reads: picking them 2 bytes a
-// lane from memory spent 13 of 21 us issuing loads (2048 tokens, 4 adapters of
-// rank 32 on 4096 x 4096; GRAD_US now).  Tokens of other adapters enter as zeros
-// selected in both operands, so an Inf or NaN among them reaches nothing.  An
-// adapter without tokens gets zeros.
+// the workgroup marks each 32-token chunk's tokens of the adapter in LDS and
+// lists the chunks that hold any; the waves take them in turn, each loading its
+// next chunk while it multiplies one, and in the end the waves' tiles are added
+// in a fixed order.  The reduction runs over the rows of Z, so a wave brings
+// its chunk's tile into LDS (16 bytes a lane, rows as they lie) and takes the
+// operands out by transpose reads; V's parts lie along the tokens already (16
+// bytes a lane and part).  Picking Z's operands 2 bytes a lane from memory, or
+// V's 4, is bound by issuing loads (GRAD_US).  Tokens of other adapters are
+// selected to zero in both operands, so an Inf or NaN among them reaches
+// nothing.  An adapter without tokens gets zeros.
 // ---------------------------------------------------------------------------
 constexpr int kGradWaves = 8;
 constexpr int kGradSpan = 4096, kGradChunks = kGradSpan / 32;
 
 struct GradSide {
-  const float* scale;   // or null: 1
-  const float* V;       // [T][r]
+  const uint16_t* VT;   // [3][r][ldt]: V's parts
   const uint16_t* Z;    // [T][C]
   int64_t ldz;
   int C, tiles;
@@ -265,7 +276,7 @@ struct GradSide {
 };
 struct GradArgs {
   const int32_t* ids;
-  int T, r;
+  int T, r, ldt;        // ldt: T rounded up to 32
   GradSide a, b;        // dA, written [r][C]; dB, written [C][r]
 };
 
@@ -284,6 +295,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void adapter_grad_kernel(GradArgs 
   using Tile = GradTile<CF>;
   extern __shared__ __align__(16) unsigned char smem[];   // the waves' tiles; in the end their sums
   __shared__ uint32_t mark[kGradChunks];
+  __shared__ uint8_t list[kGradChunks];
   const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool rank_minor = int(blockIdx.x) >= g.a.tiles;
@@ -304,6 +316,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void adapter_grad_kernel(GradArgs 
   const int tr_row = 8 * (lane >> 4) + ((lane >> 2) & 3);
   const int tr_lo = Tile::row(tr_row) + 8 * (lane & 3), tr_hi = Tile::row(tr_row + 4) + 8 * (lane & 3);
 
+  bool any = false;                       // the same in every wave
   for (int64_t base = 0; base < g.T; base += kGradSpan) {
     __syncthreads();                      // the marks of the span before are read
 #pragma unroll
@@ -313,68 +326,81 @@ __global__ __launch_bounds__(kGradWaves * 64) void adapter_grad_kernel(GradArgs 
       if (lane < 2) mark[(i * kGradWaves + wave) * 2 + lane] = uint32_t(in >> (32 * lane));
     }
     __syncthreads();
-    // chunks that hold a token of the adapter, as two 64-bit maps
+    // the chunks that hold a token of the adapter, listed in order
     const uint64_t some[2] = {__ballot(mark[lane] != 0), __ballot(mark[64 + lane] != 0)};
-    int turn = 0;
-    for (int half = 0; half < 2; ++half) {
-      for (uint64_t left = some[half]; left; left &= left - 1, ++turn) {
-        if (turn % kGradWaves != wave) continue;
-        const int chunk = half * 64 + __builtin_ctzll(left);
-        const uint32_t mine = mark[chunk];
-        const int64_t t0 = base + chunk * 32;
-        // loads are unconditional (tokens past T reread the last) and
-        // selected afterwards, so that all are in flight together
-        float v[RF][8];
-        u32x4 x[32 / RPL];
-#pragma unroll
-        for (int k = 0; k < 32 / RPL; ++k) {
-          const int64_t t = min(t0 + k * RPL + prow, int64_t(g.T) - 1);
-          x[k] = inside ? *reinterpret_cast<const u32x4*>(z.Z + t * z.ldz + c0 + piece * 8) : u32x4{0u, 0u, 0u, 0u};
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int64_t t = min(t0 + 8 * lq + e, int64_t(g.T) - 1);
-#pragma unroll
-          for (int i = 0; i < RF; ++i) v[i][e] = z.V[t * r + min(r0 + i * 16 + li, r - 1)];
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int k = 0; k < 32 / RPL; ++k) {
-          const int row = k * RPL + prow;
-          const bool sel = (mine >> row) & 1u;
-          u32x4 w;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = sel ? x[k][e] : 0u;
-          *reinterpret_cast<u32x4*>(tile + Tile::row(row) + piece * 16) = w;
-        }
-        u32x4 vp[RF][3];
-#pragma unroll
-        for (int i = 0; i < RF; ++i) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[i][e] = (mine >> (8 * lq + e)) & 1u ? v[i][e] : 0.f;
-          split8(v[i], vp[i]);
-        }
-        // a wave's LDS operations are carried out in order: no barrier
-        wait_lgkm0();
-        asm volatile("" ::: "memory");
-#pragma unroll
-        for (int j = 0; j < CF; ++j) {
-          const u32x2 lo = lds_read_tr(tile + tr_lo + 32 * j), hi = lds_read_tr(tile + tr_hi + 32 * j);
-          u32x4 zp[operand_count<DT>()];
-          operand_parts<DT>(u32x4{lo[0], lo[1], hi[0], hi[1]}, zp);
-#pragma unroll
-          for (int i = 0; i < RF; ++i) acc[i][j] = mfma_parts(vp[i], zp, acc[i][j]);
-        }
-        wait_lgkm0();
-        asm volatile("" ::: "memory");   // the next chunk's writes stay behind these reads
-      }
+    const int count = __builtin_popcountll(some[0]) + __builtin_popcountll(some[1]);
+    if (wave < 2) {
+      const uint64_t below = some[wave] & ((uint64_t(1) << lane) - 1);
+      if ((some[wave] >> lane) & 1u)
+        list[__builtin_popcountll(below) + (wave ? __builtin_popcountll(some[0]) : 0)] = uint8_t(wave * 64 + lane);
     }
+    __syncthreads();
+    // chunk i's rows of Z and V; loads are unconditional (tokens past T reread
+    // the last) and selected when used, so that all are in flight together
+    auto load = [&](int i, u32x4 (&x)[32 / RPL], u32x4 (&v)[RF][3]) {
+      const int64_t t0 = base + list[i] * 32;
+#pragma unroll
+      for (int k = 0; k < 32 / RPL; ++k) {
+        const int64_t t = min(t0 + k * RPL + prow, int64_t(g.T) - 1);
+        x[k] = *reinterpret_cast<const u32x4*>(z.Z + t * z.ldz + (inside ? c0 + piece * 8 : 0));
+      }
+#pragma unroll
+      for (int i = 0; i < RF; ++i)
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          v[i][k] = *reinterpret_cast<const u32x4*>(
+              z.VT + (int64_t(k) * r + min(r0 + i * 16 + li, r - 1)) * g.ldt + t0 + 8 * lq);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    u32x4 x[32 / RPL], v[RF][3];
+    if (wave < count) load(wave, x, v);
+    for (int i = wave; i < count; i += kGradWaves) {
+      const uint32_t mine = mark[list[i]];
+#pragma unroll
+      for (int k = 0; k < 32 / RPL; ++k) {
+        const int row = k * RPL + prow;
+        const bool sel = inside && ((mine >> row) & 1u);
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = sel ? x[k][e] : 0u;
+        *reinterpret_cast<u32x4*>(tile + Tile::row(row) + piece * 16) = w;
+      }
+      // this lane's 8 tokens (8 lq ..) as a mask of halves
+      uint32_t keep[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        keep[e] = ((mine >> (8 * lq + 2 * e)) & 1u ? 0xFFFFu : 0u) |
+                  ((mine >> (8 * lq + 2 * e + 1)) & 1u ? 0xFFFF0000u : 0u);
+      u32x4 vp[RF][3];
+#pragma unroll
+      for (int q = 0; q < RF; ++q)
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) vp[q][k][e] = v[q][k][e] & keep[e];
+      __builtin_amdgcn_sched_barrier(0);
+      // x and v are used up: the next chunk's rows arrive while this one is multiplied
+      if (i + kGradWaves < count) load(i + kGradWaves, x, v);
+      // a wave's LDS operations are carried out in order: no barrier
+      wait_lgkm0();
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int j = 0; j < CF; ++j) {
+        const u32x2 lo = lds_read_tr(tile + tr_lo + 32 * j), hi = lds_read_tr(tile + tr_hi + 32 * j);
+        u32x4 zp[operand_count<DT>()];
+        operand_parts<DT>(u32x4{lo[0], lo[1], hi[0], hi[1]}, zp);
+#pragma unroll
+        for (int q = 0; q < RF; ++q) acc[q][j] = mfma_parts(vp[q], zp, acc[q][j]);
+      }
+      wait_lgkm0();
+      asm volatile("" ::: "memory");   // the next chunk's writes stay behind these reads
+    }
+    any |= count > 0;
   }
-  __syncthreads();
   // waves 4..7 onto 0..3, 2..3 onto 0..1, 1 onto 0
   f32x4 (*part)[RF * CF][64] = reinterpret_cast<f32x4 (*)[RF * CF][64]>(smem);
-#pragma unroll
-  for (int half = kGradWaves / 2; half > 0; half >>= 1) {
+  if (any) __syncthreads();               // every wave is done with its tile
+  for (int half = any ? kGradWaves / 2 : 0; half > 0; half >>= 1) {
     if (wave >= half && wave < 2 * half) {
 #pragma unroll
       for (int i = 0; i < RF; ++i)
@@ -391,7 +417,6 @@ __global__ __launch_bounds__(kGradWaves * 64) void adapter_grad_kernel(GradArgs 
     __syncthreads();
   }
   if (wave != 0) return;
-  const float s = z.scale ? z.scale[a] : 1.f;
   float* out = z.out + int64_t(a) * r * C;
 #pragma unroll
   for (int i = 0; i < RF; ++i)
@@ -399,9 +424,13 @@ __global__ __launch_bounds__(kGradWaves * 64) void adapter_grad_kernel(GradArgs 
     for (int j = 0; j < CF; ++j) {
       const int c = c0 + j * 16 + li, q = r0 + i * 16 + lq * 4;
       if (c >= C) continue;
+      if (rank_minor && (r & 3) == 0) {
+        if (q < r) *reinterpret_cast<f32x4*>(out + int64_t(c) * r + q) = acc[i][j];
+        continue;
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (q + e < r) out[rank_minor ? int64_t(c) * r + q + e : int64_t(q + e) * C + c] = acc[i][j][e] * s;
+        if (q + e < r) out[rank_minor ? int64_t(c) * r + q + e : int64_t(q + e) * C + c] = acc[i][j][e];
     }
 }
 
@@ -441,25 +470,39 @@ hipError_t launch_shrink(const ShrinkArgs& p, int64_t splits, hipStream_t s) {
   return hipGetLastError();
 }
 
-// V = now_a M Z and its parts for the next product, next_a V (P null: not wanted).
+hipError_t join(const JoinJob& first, const JoinJob* second, const int32_t* ids, int64_t n, int64_t T, int64_t r,
+                int64_t ldt, hipStream_t s) {
+  hipLaunchKernelGGL(adapter_join_kernel, dim3(unsigned((T * ((r + 7) / 8 * 8) + 255) / 256), second ? 2u : 1u),
+                     dim3(256), 0, s, first, second ? *second : first, ids, int(n), int(T), int(r), int(ldt));
+  return hipGetLastError();
+}
+
+// now_a M Z as `out` wants it (out.V is written in any case; out.part and
+// out.splits are filled in here), and a second job along with it.
 template <int DT>
-hipError_t shrink(const int32_t* ids, int64_t n, const uint16_t* M, const float* now, const float* next,
-                  const uint16_t* Z, int64_t ldz, int64_t T, int64_t C, int64_t r, float* part, float* V, uint16_t* P,
-                  hipStream_t s) {
+hipError_t shrink(const int32_t* ids, int64_t n, const uint16_t* M, const uint16_t* Z, int64_t ldz, int64_t T, int64_t C,
+                  int64_t r, float* part, JoinJob out, const JoinJob* second, int64_t ldt, hipStream_t s) {
   if (T <= kFewTokens) {
     hipLaunchKernelGGL((adapter_dots_kernel<DT>), dim3(unsigned((T * r + 3) / 4)), dim3(256), 0, s, ids, int(n), M,
-                       now, next, Z, ldz, int(T), int(C), int(r), V, P);
-    return hipGetLastError();
+                       out.now, Z, ldz, int(T), int(C), int(r), out.V);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    if (!out.P && !out.PT && !second) return hipSuccess;
+    out.part = out.V;     // whole and scaled already
+    out.V = nullptr;
+    out.splits = 1;
+    out.now = nullptr;
+    return join(out, second, ids, n, T, r, ldt, s);
   }
   const ShrinkPlan pl = shrink_plan(T, C, r);
   const ShrinkArgs p{ids, M, Z, ldz, int(n), int(T), int(C), int(r), int(pl.csplit), part};
-  hipError_t e = hipSuccess;
-  if (n > 0 && pl.splits > 0)
-    e = r <= 32 ? launch_shrink<DT, ShrinkTile32>(p, pl.splits, s) : launch_shrink<DT, ShrinkTile64>(p, pl.splits, s);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(adapter_join_kernel, dim3(unsigned((T * ((r + 7) / 8 * 8) + 255) / 256)), dim3(256), 0, s, part,
-                     int(pl.splits), ids, int(n), now, next, int(T), int(r), V, P);
-  return hipGetLastError();
+  if (n > 0 && pl.splits > 0) {
+    const hipError_t e =
+        r <= 32 ? launch_shrink<DT, ShrinkTile32>(p, pl.splits, s) : launch_shrink<DT, ShrinkTile64>(p, pl.splits, s);
+    if (e != hipSuccess) return e;
+  }
+  out.part = part;
+  out.splits = int(pl.splits);
+  return join(out, second, ids, n, T, r, ldt, s);
 }
 
 template <int DT>
@@ -492,8 +535,10 @@ hipError_t gradients(GradArgs g, int64_t n, hipStream_t s) {
   using eight = std::integral_constant<int, 8>;
   // 128 columns a workgroup where that still covers the chip, else 64
   const bool wide = (int64_t(g.a.C) + g.b.C) / 128 * n >= 256;
-  if (g.r <= 16) return wide ? go(adapter_grad_kernel<DT, 1, 8>, one{}, eight{}) : go(adapter_grad_kernel<DT, 1, 4>, one{}, four{});
-  if (g.r <= 32) return wide ? go(adapter_grad_kernel<DT, 2, 8>, two{}, eight{}) : go(adapter_grad_kernel<DT, 2, 4>, two{}, four{});
+  if (g.r <= 16)
+    return wide ? go(adapter_grad_kernel<DT, 1, 8>, one{}, eight{}) : go(adapter_grad_kernel<DT, 1, 4>, one{}, four{});
+  if (g.r <= 32)
+    return wide ? go(adapter_grad_kernel<DT, 2, 8>, two{}, eight{}) : go(adapter_grad_kernel<DT, 2, 4>, two{}, four{});
   return go(adapter_grad_kernel<DT, 4, 4>, four{}, four{});
 }
 
@@ -513,8 +558,9 @@ hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
   char* ws = static_cast<char*>(a.workspace);
   uint16_t* P = few ? nullptr : reinterpret_cast<uint16_t*>(ws);
   char* rest = ws + (few ? 0 : parts_bytes(T, a.r));   // the shares, and when they are joined the fp32 product
-  hipError_t e = shrink<DT>(a.ids, a.n, a.A, nullptr, a.scale, a.base.act, a.base.ldx, T, a.base.K, a.r,
-                            reinterpret_cast<float*>(rest), a.xa, P, s);
+  const JoinJob out{nullptr, 0, nullptr, a.scale, a.xa, P, nullptr};
+  hipError_t e = shrink<DT>(a.ids, a.n, a.A, a.base.act, a.base.ldx, T, a.base.K, a.r, reinterpret_cast<float*>(rest),
+                            out, nullptr, 0, s);
   if (e != hipSuccess || a.base.R == 0) return e;
   LowRank p;
   p.ids = a.ids;
@@ -541,15 +587,20 @@ hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
   return expand<DT>(p, static_cast<const float*>(b.Y), b.ldy, a.base.Y, a.base.ldy, a.base.out_dtype, s);
 }
 
-// The backward pass's workspace: u, its parts, B and A transposed, the shares.
+// The backward pass's workspace: u, its parts, u's and s xa's parts along the
+// tokens, B and A transposed, the shares.
 struct BwdParts {
-  size_t u, p, bt, at, part, total;
+  int64_t ldt;
+  size_t u, p, ut, xt, bt, at, part, total;
 };
 BwdParts bwd_parts(int64_t R, int64_t K, int64_t T, int64_t n, int64_t r) {
   BwdParts b;
+  b.ldt = (T + 31) / 32 * 32;
   b.u = 0;
   b.p = b.u + padded(size_t(T) * r * 4);
-  b.bt = b.p + parts_bytes(T, r);
+  b.ut = b.p + parts_bytes(T, r);
+  b.xt = b.ut + padded(size_t(b.ldt) * r * 6);
+  b.bt = b.xt + padded(size_t(b.ldt) * r * 6);
   b.at = b.bt + padded(size_t(n) * r * R * 2);
   b.part = b.at + padded(size_t(n) * r * K * 2);
   b.total = b.part + shrink_bytes(T, R, r);
@@ -563,6 +614,8 @@ hipError_t backward_dt(const AdapterBwdArgs& a, hipStream_t s) {
   char* ws = static_cast<char*>(a.workspace);
   float* u = reinterpret_cast<float*>(ws + w.u);
   uint16_t* P = reinterpret_cast<uint16_t*>(ws + w.p);
+  uint16_t* ut = reinterpret_cast<uint16_t*>(ws + w.ut);
+  uint16_t* xt = reinterpret_cast<uint16_t*>(ws + w.xt);
   uint16_t* bt = reinterpret_cast<uint16_t*>(ws + w.bt);
   uint16_t* at = reinterpret_cast<uint16_t*>(ws + w.at);
   hipError_t e = hipSuccess;
@@ -576,8 +629,10 @@ hipError_t backward_dt(const AdapterBwdArgs& a, hipStream_t s) {
                            s, tb, ta);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    e = shrink<DT>(a.ids, a.n, bt, a.scale, nullptr, d.G, d.ldg, d.T, d.R, a.r, reinterpret_cast<float*>(ws + w.part),
-                   u, P, s);
+    const JoinJob mine{nullptr, 0, a.scale, nullptr, u, P, ut};
+    const JoinJob other{a.xa, 1, a.scale, nullptr, nullptr, nullptr, xt};
+    e = shrink<DT>(a.ids, a.n, bt, d.G, d.ldg, d.T, d.R, a.r, reinterpret_cast<float*>(ws + w.part), mine, &other, w.ldt,
+                   s);
     if (e != hipSuccess) return e;
   }
   if (d.out && d.T > 0) {
@@ -595,8 +650,8 @@ hipError_t backward_dt(const AdapterBwdArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (a.n == 0) return e;
-  GradArgs g{a.ids, int(d.T), int(a.r), GradSide{nullptr, u, d.act, d.ldx, int(d.K), 0, a.dA},
-             GradSide{a.scale, a.xa, d.G, d.ldg, int(d.R), 0, a.dB}};
+  const GradArgs g{a.ids, int(d.T), int(a.r), int(w.ldt), GradSide{ut, d.act, d.ldx, int(d.K), 0, a.dA},
+                   GradSide{xt, d.G, d.ldg, int(d.R), 0, a.dB}};
   return gradients<DT>(g, a.n, s);
 }
 

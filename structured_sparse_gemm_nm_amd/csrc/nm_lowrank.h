@@ -67,14 +67,12 @@ __device__ inline f32x4 mfma_parts(const u32x4 (&a)[NA], const u32x4 (&b)[NB], f
   return acc;
 }
 
-// s V as P's parts, the form the matrix cores take it in: part k of element j
-// at row[k * r8 + j].
-__device__ inline void store_parts(uint16_t* row, int r8, int j, float f) {
+// One float in three bf16 parts.
+__device__ inline void split3(float f, uint16_t (&h)[3]) {
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    const uint16_t h = to_half_bits<NM_BF16>(f);
-    row[k * r8 + j] = h;
-    f -= half_to_f32<NM_BF16>(h);
+    h[k] = to_half_bits<NM_BF16>(f);
+    f -= half_to_f32<NM_BF16>(h[k]);
     f = fabsf(f) < __builtin_inff() ? f : 0.f;   // what is not finite stays in the first part alone
   }
 }
