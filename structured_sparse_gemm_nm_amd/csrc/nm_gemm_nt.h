@@ -17,6 +17,8 @@
 
 #include "nm_device.h"
 
+#include <type_traits>
+
 namespace nm {
 
 template <int BM_, int BN_, int WM_, int WN_, int NS_>
@@ -125,6 +127,145 @@ __device__ inline void gemm_nt(const uint16_t* P, int64_t ldp, int M, const uint
   };
   for (int s = 0; s < steps - 1; ++s) step(s, false);
   step(steps - 1, rem < 64);
+  wait_vmcnt<0>();
+  wait_lgkm0();
+  barrier_no_fence();
+  epi(acc, wm, wn, li, lq);
+}
+
+// The same product for large shapes: 256 x 256 tiles by 8 waves of 128 x 64,
+// two a SIMD, software-pipelined.  With fragments read right before their MFMAs
+// both waves of a SIMD leave each barrier at the same time and wait for the
+// same LDS port (2048 x 32003 x 4096 fp16 with the softmax epilogue: 479 us).
+// Here they go through two register sets: while one half step (32 k) is
+// multiplied the next half's fragments are read and the loads of the step after
+// next are issued between the MFMAs, in eight chunks a half that scheduling
+// barriers keep in order (425 us, 1.26 PFLOP/s; the library's product alone
+// takes 458).  Two stages of 64 k; a step's stage is free once its second half
+// is in registers, at mid-step, where the one barrier a step stands:
+//   first half   MFMAs on set 0 (s, 0);  reads (s, 1) into set 1;
+//   barrier      step s+1 has landed, stage s is free;
+//   second half  MFMAs on set 1;  reads (s+1, 0) into set 0;  loads step s+2.
+// (4 waves of 128 x 128 read a third fewer LDS bytes, but alone on its SIMD a
+// wave covers none of another's waits: 558 us.)
+struct GemmTilePiped {
+  static constexpr int BM = 256, BN = 256, WM = 2, WN = 4, THREADS = 512, FM = 8, FN = 4;
+  static constexpr int STAGE = (BM + BN) * 128, LDS = 2 * STAGE;
+};
+
+template <int DT, class C, class Epi>
+__device__ inline void gemm_nt_piped(const uint16_t* P, int64_t ldp, int M, const uint16_t* Q, int64_t ldq, int N, int K,
+                                    int tm, int tn, unsigned char* smem, Epi&& epi) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 15, lq = lane >> 4;
+  const int wm = wave >> 2, wn = wave & 3;
+  const int m0 = tm * C::BM, n0 = tn * C::BN;
+  const int steps = (K + 63) >> 6;
+  const int rem = K - (steps - 1) * 64;
+
+  const __amdgpu_buffer_rsrc_t rp = make_rsrc(P + int64_t(m0) * ldp);
+  const __amdgpu_buffer_rsrc_t rq = make_rsrc(Q + int64_t(n0) * ldq);
+  // loads j = 0..3: rows (wave*4 + j)*8 + lane/8 of P, 4..7 the same of Q
+  const uint32_t chunk = uint32_t((lane & 7) ^ ((lane >> 3) & 7));
+  uint32_t off[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int row = (wave * 4 + j) * 8 + (lane >> 3);
+    off[j] = uint32_t(min(row, M - 1 - m0)) * uint32_t(ldp) * 2u + chunk * 16u;
+    off[4 + j] = uint32_t(min(row, N - 1 - n0)) * uint32_t(ldq) * 2u + chunk * 16u;
+  }
+  // past the end: again the last step, into a stage nothing reads any more
+  auto issue = [&](int j, int s, uint32_t back, unsigned char* st) {
+    dma16(j < 4 ? rp : rq, off[j] - back, uint32_t(s) * 128u,
+          st + (j < 4 ? 0 : C::BM * 128) + (wave * 4 + (j & 3)) * 1024);
+  };
+  auto last_back = [&](int s) { return s == steps - 1 && int(chunk) * 8 >= rem ? chunk * 16u : 0u; };
+
+  f32x4 acc[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // fragment i of the wave's rows, half h: its address differs from fragment
+  // 0's by a constant (16 rows apart the swizzle is the same)
+  const int prow = wm * 128 + li, qrow = wn * 64 + li;
+  int pa[2], qa[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    pa[h] = (prow * 8 + ((4 * h + lq) ^ (prow & 7))) * 16;
+    qa[h] = C::BM * 128 + (qrow * 8 + ((4 * h + lq) ^ (qrow & 7))) * 16;
+  }
+  auto read_p = [&](const unsigned char* st, int h, int i) {
+    return *reinterpret_cast<const u32x4*>(st + pa[h] + i * 2048);
+  };
+  auto read_q = [&](const unsigned char* st, int h, int j) {
+    return *reinterpret_cast<const u32x4*>(st + qa[h] + j * 2048);
+  };
+  u32x4 a0[8], b0[4], a1[8], b1[4];
+
+  // One half step: MFMAs on (ca, cb); with READ, fragments of half rh of stage
+  // rst into (na, nb); with LOAD, the 8 loads of step ls into stage lst.
+  auto half = [&](auto read_c, auto load_c, const u32x4 (&ca)[8], const u32x4 (&cb)[4], u32x4 (&na)[8], u32x4 (&nb)[4],
+                  const unsigned char* rst, int rh, int ls, uint32_t back, unsigned char* lst) {
+    constexpr bool READ = decltype(read_c)::value, LOAD = decltype(load_c)::value;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      // reads in the first four chunks (the next half needs them right at its
+      // start), loads spread over all eight
+      if (READ && k < 4) {
+        nb[k] = read_q(rst, rh, k);
+        na[2 * k] = read_p(rst, rh, 2 * k);
+        na[2 * k + 1] = read_p(rst, rh, 2 * k + 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[k][j] = mfma32<DT>(ca[k], cb[j], acc[k][j]);
+      if constexpr (LOAD) issue(k, ls, back, lst);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  using yes = std::integral_constant<bool, true>;
+  using no = std::integral_constant<bool, false>;
+  // the last step's chunks past K: zeros on both sides
+  auto trim = [&](u32x4 (&a)[8], u32x4 (&b)[4], int h) {
+    if ((4 * h + lq) * 8 < rem) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a[i] = u32x4{0u, 0u, 0u, 0u};
+      if (i < 4) b[i] = a[i];
+    }
+  };
+
+  // step 0 in stage 0, step 1 in stage 1, (0, 0) in set 0
+#pragma unroll
+  for (int j = 0; j < 8; ++j) issue(j, 0, last_back(0), smem);
+  const int s1 = min(1, steps - 1);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) issue(j, s1, last_back(s1), smem + C::STAGE);
+  wait_vmcnt<8>();
+  barrier_no_fence();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a0[i] = read_p(smem, 0, i);
+    if (i < 4) b0[i] = read_q(smem, 0, i);
+  }
+  // every step but the last in the loop, which then holds no branch
+  for (int s = 0; s < steps - 1; ++s) {
+    unsigned char* here = smem + (s & 1) * C::STAGE;
+    unsigned char* next = smem + ((s & 1) ^ 1) * C::STAGE;
+    half(yes{}, no{}, a0, b0, a1, b1, here, 1, 0, 0u, nullptr);
+    wait_vmcnt<0>();
+    wait_lgkm0();
+    barrier_no_fence();
+    const int ls = min(s + 2, steps - 1);
+    half(yes{}, yes{}, a1, b1, a0, b0, next, 0, ls, last_back(ls), here);
+  }
+  if (rem < 64) trim(a0, b0, 0);
+  half(yes{}, no{}, a0, b0, a1, b1, smem + ((steps - 1) & 1) * C::STAGE, 1, 0, 0u, nullptr);
+  if (rem < 64) trim(a1, b1, 1);
+  half(no{}, no{}, a1, b1, a0, b0, nullptr, 0, 0, 0u, nullptr);
   wait_vmcnt<0>();
   wait_lgkm0();
   barrier_no_fence();

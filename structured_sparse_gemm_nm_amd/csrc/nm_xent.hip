@@ -24,17 +24,51 @@
 #include "nm_internal.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace nm {
 namespace {
 
 constexpr float kInf = __builtin_inff();
 
-// 256 x 256 tiles, 8 waves of 128 x 64; for few tokens, narrow tiles with a
-// deeper ring (the product is then a stream of W)
-using TileBig = GemmTile<256, 256, 2, 4, 2>;
+// For few tokens, narrow tiles with a deeper ring (the product is then a stream
+// of W).
+using TileBig = GemmTilePiped;
 using Tile64 = GemmTile<128, 64, 4, 1, 4>;
 using Tile16 = GemmTile<128, 16, 4, 1, 6>;
+
+// The product of tile type C.
+template <int DT, class C, class... Args>
+__device__ inline void product_tile(Args&&... args) {
+  if constexpr (std::is_same_v<C, GemmTilePiped>) gemm_nt_piped<DT, C>(static_cast<Args&&>(args)...);
+  else gemm_nt<DT, C>(static_cast<Args&&>(args)...);
+}
+
+// A piped tile's 16-bit results leave through LDS, a wave its own 128 x 64, so
+// that every store writes whole 128- or 256-byte runs (straight from the result
+// layout a store covers 16 rows of 32 bytes).  Rows are padded by 16 bytes.
+constexpr int kRowsN = 128 * 2 + 16, kRowsM = 64 * 2 + 16;   // bytes of a row: by n (128 m), by m (64 n)
+constexpr int kOutBytes = 128 * kRowsM;                      // a wave's area (64 * kRowsN is less)
+constexpr int kOutLds = 8 * kOutBytes;
+static_assert(64 * kRowsN <= kOutBytes && kOutLds >= GemmTilePiped::LDS && kOutLds <= 160 * 1024, "LDS areas");
+
+// Fragment (i, j)'s 4 consecutive m of the lane's n, as two words, into the
+// area by n.
+__device__ inline void put_by_n(unsigned char* area, int i, int j, int li, int lq, uint32_t lo, uint32_t hi) {
+  *reinterpret_cast<u32x2*>(area + (j * 16 + li) * kRowsN + (i * 16 + 4 * lq) * 2) = u32x2{lo, hi};
+}
+
+// The same into the area by m: neighbouring lanes (n, n + 1) exchange halves, so
+// that each writes two whole words.
+__device__ inline void put_by_m(unsigned char* area, int i, int j, int li, int lq, uint32_t lo, uint32_t hi) {
+  const bool odd = li & 1;
+  const uint32_t got = uint32_t(__builtin_amdgcn_update_dpp(0, int(odd ? lo : hi), 0xB1, 0xF, 0xF, false));
+  const uint32_t own = odd ? hi : lo;          // rows m, m + 1 (even lane) or m + 2, m + 3 (odd)
+  const uint32_t first = odd ? got : own, second = odd ? own : got;
+  unsigned char* p = area + (i * 16 + 4 * lq + (odd ? 2 : 0)) * kRowsM + (j * 16 + (li & ~1)) * 2;
+  *reinterpret_cast<uint32_t*>(p) = (first & 0xFFFFu) | (second << 16);
+  *reinterpret_cast<uint32_t*>(p + kRowsM) = (first >> 16) | (second & 0xFFFF0000u);
+}
 
 // exp(m - top) for parts of a sum: 0 for an empty part (m = -inf).
 __device__ inline float part_weight(float m, float top) { return m == -kInf ? 0.f : __expf(m - top); }
@@ -57,7 +91,7 @@ __global__ __launch_bounds__(C::THREADS) void xent_stats_kernel(XentArgsDev p, f
   extern __shared__ __align__(16) unsigned char smem[];
   int tv, tt;
   grouped_tile(xcd_tile(blockIdx.x, gridDim.x), tilesV, tilesT, group, tv, tt);
-  gemm_nt<DT, C>(p.w, p.ldw, p.V, p.x, p.ldx, p.T, p.H, tv, tt, smem, [&](auto& acc, int wm, int wn, int li, int lq) {
+  product_tile<DT, C>(p.w, p.ldw, p.V, p.x, p.ldx, p.T, p.H, tv, tt, smem, [&](auto& acc, int wm, int wn, int li, int lq) {
     float2* red = reinterpret_cast<float2*>(smem);   // [WM][BN]
     const int v0 = tv * C::BM + wm * C::FM * 16 + 4 * lq;
 #pragma unroll
@@ -206,42 +240,67 @@ __global__ __launch_bounds__(C::THREADS) void xent_dlogits_kernel(XentBwdDev p, 
   int tv, tt;
   grouped_tile(xcd_tile(blockIdx.x, gridDim.x), tilesV, tilesT, group, tv, tt);
   const uint16_t* w = p.a.w + int64_t(p.v0) * p.a.ldw;
-  gemm_nt<DT, C>(w, p.a.ldw, p.vn, p.a.x, p.a.ldx, p.a.T, p.a.H, tv, tt, smem,
+  product_tile<DT, C>(w, p.a.ldw, p.vn, p.a.x, p.a.ldx, p.a.T, p.a.H, tv, tt, smem,
                  [&](auto& acc, int wm, int wn, int li, int lq) {
     const float G = *p.largest;
-    const int vb = tv * C::BM + wm * C::FM * 16 + 4 * lq;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    unsigned char* area = smem + wave * kOutBytes;
+    const int v0 = tv * C::BM + wm * 128, t0 = tt * C::BN + wn * 64;   // the wave's corner
+    // q, scaled for its 16-bit type, in place of the logits
+    float ratio[C::FN];
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) {
-      const int t = tt * C::BN + wn * C::FN * 16 + j * 16 + li;
+      const int t = t0 + j * 16 + li;
       const bool live = t < p.a.T;
       const int label = live ? p.a.labels[t] : -1;
       const bool counted = uint32_t(label) < uint32_t(p.a.V);
       const float lse = live ? p.lse[t] : 0.f;
       // g == G gives exactly 1; G == 0 (no gradient at all) gives 0
-      const float ratio = counted && G != 0.f ? p.dloss[t] / G : 0.f;
+      ratio[j] = counted && G != 0.f ? p.dloss[t] / G : 0.f;
       const int mine = label - p.v0;
 #pragma unroll
-      for (int i = 0; i < C::FM; ++i) {
-        const int v = vb + i * 16;
-        float d[4];
+      for (int i = 0; i < C::FM; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float q = __expf(acc[i][j][e] - lse) - (v + e == mine ? 1.f : 0.f);
-          d[e] = counted && v + e < p.vn ? kOperandScale<DT> * q : 0.f;
+          const int v = v0 + i * 16 + 4 * lq + e;
+          const float q = __expf(acc[i][j][e] - lse) - (v == mine ? 1.f : 0.f);
+          acc[i][j][e] = counted && v < p.vn ? kOperandScale<DT> * q : 0.f;
         }
-        if (v >= p.vpad) continue;     // vpad is a multiple of 4
-        if (p.d && live)
-          *reinterpret_cast<uint2*>(p.d + int64_t(t) * p.ldd + v) =
-              make_uint2(pack_half2<DT>(d[0], d[1]), pack_half2<DT>(d[2], d[3]));
-        if (p.dt && t < p.ldt) {
-          const uint32_t lo = pack_half2<DT>(ratio * d[0], ratio * d[1]);
-          const uint32_t hi = pack_half2<DT>(ratio * d[2], ratio * d[3]);
-          uint16_t* q = p.dt + int64_t(v) * p.ldt + t;
-          q[0] = uint16_t(lo);
-          q[p.ldt] = uint16_t(lo >> 16);
-          q[2 * p.ldt] = uint16_t(hi);
-          q[3 * p.ldt] = uint16_t(hi >> 16);
-        }
+    }
+    if (p.d) {
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+          put_by_n(area, i, j, li, lq, pack_half2<DT>(acc[i][j][0], acc[i][j][1]),
+                   pack_half2<DT>(acc[i][j][2], acc[i][j][3]));
+      wait_lgkm0();
+      asm volatile("" ::: "memory");
+      const int v = v0 + (lane & 15) * 8;      // vpad is a multiple of 64: whole pieces
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int n = k * 4 + (lane >> 4), t = t0 + n;
+        const u32x4 w = *reinterpret_cast<const u32x4*>(area + n * kRowsN + (lane & 15) * 16);
+        if (t < p.a.T && v < p.vpad) *reinterpret_cast<u32x4*>(p.d + int64_t(t) * p.ldd + v) = w;
+      }
+      wait_lgkm0();
+      asm volatile("" ::: "memory");
+    }
+    if (p.dt) {
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+          put_by_m(area, i, j, li, lq, pack_half2<DT>(ratio[j] * acc[i][j][0], ratio[j] * acc[i][j][1]),
+                   pack_half2<DT>(ratio[j] * acc[i][j][2], ratio[j] * acc[i][j][3]));
+      wait_lgkm0();
+      asm volatile("" ::: "memory");
+      const int t = t0 + (lane & 7) * 8;       // ldt is a multiple of 64
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int m = k * 8 + (lane >> 3), v = v0 + m;
+        const u32x4 w = *reinterpret_cast<const u32x4*>(area + m * kRowsM + (lane & 7) * 16);
+        if (v < p.vpad && t < p.ldt) *reinterpret_cast<u32x4*>(p.dt + int64_t(v) * p.ldt + t) = w;
       }
     }
   });
@@ -266,27 +325,54 @@ __global__ __launch_bounds__(C::THREADS) void xent_product_kernel(XentProduct p,
   grouped_tile(xcd_tile(blockIdx.x, gridDim.x), tilesM, tilesN, group, tm, tn);
   const int k0 = blockIdx.y * p.ksplit;
   const int K = min(p.K - k0, p.ksplit);
-  gemm_nt<DT, C>(p.P + k0, p.ldp, p.M, p.Q + k0, p.ldq, p.N, K, tm, tn, smem,
+  product_tile<DT, C>(p.P + k0, p.ldp, p.M, p.Q + k0, p.ldq, p.N, K, tm, tn, smem,
                  [&](auto& acc, int wm, int wn, int li, int lq) {
     const float down = (p.largest ? *p.largest : 1.f) / kOperandScale<DT>;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int m0 = tm * C::BM + wm * 128, n0 = tn * C::BN + wn * 64;   // the wave's corner
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j) {
-      const int n = tn * C::BN + wn * C::FN * 16 + j * 16 + li;
-      if (n >= p.N) continue;
+    for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-      for (int i = 0; i < C::FM; ++i) {
-        const int m = tm * C::BM + wm * C::FM * 16 + i * 16 + 4 * lq;
-        if (m >= p.M) continue;        // M is a multiple of 8
-        f32x4 v = acc[i][j];
+      for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] *= down;
-        if constexpr (OUT == NM_F32) {
+        for (int e = 0; e < 4; ++e) acc[i][j][e] *= down;
+    if constexpr (OUT == NM_F32) {
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) {
+        const int n = n0 + j * 16 + li;
+        if (n >= p.N) continue;
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) {
+          const int m = m0 + i * 16 + 4 * lq;
+          if (m >= p.M) continue;        // M is a multiple of 8
           float* o = static_cast<float*>(p.out) + blockIdx.y * p.split_stride + int64_t(n) * p.ldo + m;
+          f32x4 v = acc[i][j];
           if (p.add) v += *reinterpret_cast<const f32x4*>(o);
           *reinterpret_cast<f32x4*>(o) = v;
-        } else {
-          uint16_t* o = static_cast<uint16_t*>(p.out) + int64_t(n) * p.ldo + m;
-          *reinterpret_cast<uint2*>(o) = make_uint2(pack_half2<OUT>(v[0], v[1]), pack_half2<OUT>(v[2], v[3]));
+        }
+      }
+    } else {
+      unsigned char* area = smem + wave * kOutBytes;
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+          put_by_n(area, i, j, li, lq, pack_half2<OUT>(acc[i][j][0], acc[i][j][1]),
+                   pack_half2<OUT>(acc[i][j][2], acc[i][j][3]));
+      wait_lgkm0();
+      asm volatile("" ::: "memory");
+      const int m = m0 + (lane & 15) * 8;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int r = k * 4 + (lane >> 4), n = n0 + r;
+        const u32x4 w = *reinterpret_cast<const u32x4*>(area + r * kRowsN + (lane & 15) * 16);
+        if (n >= p.N || m >= p.M) continue;
+        uint16_t* o = static_cast<uint16_t*>(p.out) + int64_t(n) * p.ldo + m;
+        if ((p.ldo & 7) == 0) {
+          __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(o));   // not read again here: leave the caches to the operands
+        } else {                         // rows on 8 bytes
+          *reinterpret_cast<u32x2*>(o) = u32x2{w[0], w[1]};
+          *reinterpret_cast<u32x2*>(o + 4) = u32x2{w[2], w[3]};
         }
       }
     }
@@ -324,10 +410,12 @@ template <class C, typename Kern, typename Args, typename... Rest>
 hipError_t launch_tiles(Kern kern, const Args& args, int64_t tilesA, int64_t tilesB, int64_t splits, hipStream_t s,
                         Rest... rest) {
   if (tilesA * tilesB * C::THREADS > 0xFFFFFFFFll) return hipErrorInvalidValue;
-  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), C::LDS); e != hipSuccess) return e;
+  // (the kernels that write through LDS take piped tiles only)
+  constexpr int lds = std::is_same_v<C, GemmTilePiped> ? kOutLds : C::LDS;
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), lds); e != hipSuccess) return e;
   // an XCD's run of tiles covers about 4 tiles of A by what fits of B
   const int group = int(std::min<int64_t>(tilesA, 4));
-  hipLaunchKernelGGL(kern, dim3(unsigned(tilesA * tilesB), unsigned(splits)), dim3(C::THREADS), C::LDS, s, args,
+  hipLaunchKernelGGL(kern, dim3(unsigned(tilesA * tilesB), unsigned(splits)), dim3(C::THREADS), lds, s, args,
                      rest..., int(tilesA), int(tilesB), group);
   return hipGetLastError();
 }
