@@ -44,31 +44,52 @@ __device__ inline void product_tile(Args&&... args) {
   else gemm_nt<DT, C>(static_cast<Args&&>(args)...);
 }
 
-// A piped tile's 16-bit results leave through LDS, a wave its own 128 x 64, so
-// that every store writes whole 128- or 256-byte runs (straight from the result
-// layout a store covers 16 rows of 32 bytes).  Rows are padded by 16 bytes.
-constexpr int kRowsN = 128 * 2 + 16, kRowsM = 64 * 2 + 16;   // bytes of a row: by n (128 m), by m (64 n)
-constexpr int kOutBytes = 128 * kRowsM;                      // a wave's area (64 * kRowsN is less)
-constexpr int kOutLds = 8 * kOutBytes;
-static_assert(64 * kRowsN <= kOutBytes && kOutLds >= GemmTilePiped::LDS && kOutLds <= 160 * 1024, "LDS areas");
+// A tile's 16-bit results leave through LDS, a wave its own part, so that every
+// store writes whole lines (straight from the result layout a store covers 16
+// rows of 32 bytes).  The wave's area holds rows by n (of its m) or by m (of
+// its n), padded by 16 bytes.
+template <class C>
+struct OutArea {
+  static constexpr int MW = C::FM * 16, NW = C::FN * 16;           // the wave's part
+  static constexpr int ROW_N = MW * 2 + 16, ROW_M = NW * 2 + 16;   // bytes of a row
+  static constexpr int BYTES = NW * ROW_N > MW * ROW_M ? NW * ROW_N : MW * ROW_M;
+  static constexpr int ALL = C::WM * C::WN * BYTES;
+  static constexpr int LDS = ALL > C::LDS ? ALL : C::LDS;          // of a kernel that uses it
+  static_assert(LDS <= 160 * 1024, "fits a workgroup");
 
-// Fragment (i, j)'s 4 consecutive m of the lane's n, as two words, into the
-// area by n.
-__device__ inline void put_by_n(unsigned char* area, int i, int j, int li, int lq, uint32_t lo, uint32_t hi) {
-  *reinterpret_cast<u32x2*>(area + (j * 16 + li) * kRowsN + (i * 16 + 4 * lq) * 2) = u32x2{lo, hi};
-}
-
-// The same into the area by m: neighbouring lanes (n, n + 1) exchange halves, so
-// that each writes two whole words.
-__device__ inline void put_by_m(unsigned char* area, int i, int j, int li, int lq, uint32_t lo, uint32_t hi) {
-  const bool odd = li & 1;
-  const uint32_t got = uint32_t(__builtin_amdgcn_update_dpp(0, int(odd ? lo : hi), 0xB1, 0xF, 0xF, false));
-  const uint32_t own = odd ? hi : lo;          // rows m, m + 1 (even lane) or m + 2, m + 3 (odd)
-  const uint32_t first = odd ? got : own, second = odd ? own : got;
-  unsigned char* p = area + (i * 16 + 4 * lq + (odd ? 2 : 0)) * kRowsM + (j * 16 + (li & ~1)) * 2;
-  *reinterpret_cast<uint32_t*>(p) = (first & 0xFFFFu) | (second << 16);
-  *reinterpret_cast<uint32_t*>(p + kRowsM) = (first >> 16) | (second & 0xFFFF0000u);
-}
+  // Fragment (i, j)'s 4 consecutive m of the lane's n, as two words, by n.
+  __device__ static void put_by_n(unsigned char* area, int i, int j, int li, int lq, uint32_t lo, uint32_t hi) {
+    *reinterpret_cast<u32x2*>(area + (j * 16 + li) * ROW_N + (i * 16 + 4 * lq) * 2) = u32x2{lo, hi};
+  }
+  // By m: neighbouring lanes (n, n + 1) exchange halves, so that each writes
+  // two whole words.
+  __device__ static void put_by_m(unsigned char* area, int i, int j, int li, int lq, uint32_t lo, uint32_t hi) {
+    const bool odd = li & 1;
+    const uint32_t got = uint32_t(__builtin_amdgcn_update_dpp(0, int(odd ? lo : hi), 0xB1, 0xF, 0xF, false));
+    const uint32_t own = odd ? hi : lo;          // rows m, m + 1 (even lane) or m + 2, m + 3 (odd)
+    const uint32_t first = odd ? got : own, second = odd ? own : got;
+    unsigned char* p = area + (i * 16 + 4 * lq + (odd ? 2 : 0)) * ROW_M + (j * 16 + (li & ~1)) * 2;
+    *reinterpret_cast<uint32_t*>(p) = (first & 0xFFFFu) | (second << 16);
+    *reinterpret_cast<uint32_t*>(p + ROW_M) = (first >> 16) | (second & 0xFFFF0000u);
+  }
+  // Calls out(row, first column, 8 values) for the area's rows, 16 bytes a lane.
+  template <bool BY_N, class Out>
+  __device__ static void take(const unsigned char* area, Out&& out) {
+    constexpr int ROWS = BY_N ? NW : MW, PIECES = (BY_N ? MW : NW) / 8, PITCH = BY_N ? ROW_N : ROW_M;
+    constexpr int PER = 64 / PIECES;             // rows a pass
+    static_assert(64 % PIECES == 0 && ROWS % PER == 0, "whole passes");
+    const int lane = threadIdx.x & 63, piece = lane % PIECES;
+    wait_lgkm0();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < ROWS / PER; ++k) {
+      const int row = k * PER + lane / PIECES;
+      out(row, piece * 8, *reinterpret_cast<const u32x4*>(area + row * PITCH + piece * 16));
+    }
+    wait_lgkm0();
+    asm volatile("" ::: "memory");
+  }
+};
 
 // exp(m - top) for parts of a sum: 0 for an empty part (m = -inf).
 __device__ inline float part_weight(float m, float top) { return m == -kInf ? 0.f : __expf(m - top); }
@@ -243,9 +264,9 @@ __global__ __launch_bounds__(C::THREADS) void xent_dlogits_kernel(XentBwdDev p, 
   product_tile<DT, C>(w, p.a.ldw, p.vn, p.a.x, p.a.ldx, p.a.T, p.a.H, tv, tt, smem,
                  [&](auto& acc, int wm, int wn, int li, int lq) {
     const float G = *p.largest;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    unsigned char* area = smem + wave * kOutBytes;
-    const int v0 = tv * C::BM + wm * 128, t0 = tt * C::BN + wn * 64;   // the wave's corner
+    using Area = OutArea<C>;
+    unsigned char* area = smem + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * Area::BYTES;
+    const int v0 = tv * C::BM + wm * Area::MW, t0 = tt * C::BN + wn * Area::NW;   // the wave's corner
     // q, scaled for its 16-bit type, in place of the logits
     float ratio[C::FN];
 #pragma unroll
@@ -272,36 +293,26 @@ __global__ __launch_bounds__(C::THREADS) void xent_dlogits_kernel(XentBwdDev p, 
       for (int j = 0; j < C::FN; ++j)
 #pragma unroll
         for (int i = 0; i < C::FM; ++i)
-          put_by_n(area, i, j, li, lq, pack_half2<DT>(acc[i][j][0], acc[i][j][1]),
-                   pack_half2<DT>(acc[i][j][2], acc[i][j][3]));
-      wait_lgkm0();
-      asm volatile("" ::: "memory");
-      const int v = v0 + (lane & 15) * 8;      // vpad is a multiple of 64: whole pieces
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int n = k * 4 + (lane >> 4), t = t0 + n;
-        const u32x4 w = *reinterpret_cast<const u32x4*>(area + n * kRowsN + (lane & 15) * 16);
-        if (t < p.a.T && v < p.vpad) *reinterpret_cast<u32x4*>(p.d + int64_t(t) * p.ldd + v) = w;
-      }
-      wait_lgkm0();
-      asm volatile("" ::: "memory");
+          Area::put_by_n(area, i, j, li, lq, pack_half2<DT>(acc[i][j][0], acc[i][j][1]),
+                         pack_half2<DT>(acc[i][j][2], acc[i][j][3]));
+      // vpad is a multiple of 64: whole pieces
+      Area::template take<true>(area, [&](int n, int m, const u32x4& w) {
+        if (t0 + n < p.a.T && v0 + m < p.vpad)
+          *reinterpret_cast<u32x4*>(p.d + int64_t(t0 + n) * p.ldd + v0 + m) = w;
+      });
     }
     if (p.dt) {
 #pragma unroll
       for (int j = 0; j < C::FN; ++j)
 #pragma unroll
         for (int i = 0; i < C::FM; ++i)
-          put_by_m(area, i, j, li, lq, pack_half2<DT>(ratio[j] * acc[i][j][0], ratio[j] * acc[i][j][1]),
-                   pack_half2<DT>(ratio[j] * acc[i][j][2], ratio[j] * acc[i][j][3]));
-      wait_lgkm0();
-      asm volatile("" ::: "memory");
-      const int t = t0 + (lane & 7) * 8;       // ldt is a multiple of 64
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int m = k * 8 + (lane >> 3), v = v0 + m;
-        const u32x4 w = *reinterpret_cast<const u32x4*>(area + m * kRowsM + (lane & 7) * 16);
-        if (v < p.vpad && t < p.ldt) *reinterpret_cast<u32x4*>(p.dt + int64_t(v) * p.ldt + t) = w;
-      }
+          Area::put_by_m(area, i, j, li, lq, pack_half2<DT>(ratio[j] * acc[i][j][0], ratio[j] * acc[i][j][1]),
+                         pack_half2<DT>(ratio[j] * acc[i][j][2], ratio[j] * acc[i][j][3]));
+      // so is ldt
+      Area::template take<false>(area, [&](int m, int n, const u32x4& w) {
+        if (v0 + m < p.vpad && t0 + n < p.ldt)
+          *reinterpret_cast<u32x4*>(p.dt + int64_t(v0 + m) * p.ldt + t0 + n) = w;
+      });
     }
   });
 }
@@ -328,8 +339,8 @@ __global__ __launch_bounds__(C::THREADS) void xent_product_kernel(XentProduct p,
   product_tile<DT, C>(p.P + k0, p.ldp, p.M, p.Q + k0, p.ldq, p.N, K, tm, tn, smem,
                  [&](auto& acc, int wm, int wn, int li, int lq) {
     const float down = (p.largest ? *p.largest : 1.f) / kOperandScale<DT>;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int m0 = tm * C::BM + wm * 128, n0 = tn * C::BN + wn * 64;   // the wave's corner
+    using Area = OutArea<C>;
+    const int m0 = tm * C::BM + wm * Area::MW, n0 = tn * C::BN + wn * Area::NW;   // the wave's corner
 #pragma unroll
     for (int j = 0; j < C::FN; ++j)
 #pragma unroll
@@ -352,21 +363,16 @@ __global__ __launch_bounds__(C::THREADS) void xent_product_kernel(XentProduct p,
         }
       }
     } else {
-      unsigned char* area = smem + wave * kOutBytes;
+      unsigned char* area = smem + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * Area::BYTES;
 #pragma unroll
       for (int j = 0; j < C::FN; ++j)
 #pragma unroll
         for (int i = 0; i < C::FM; ++i)
-          put_by_n(area, i, j, li, lq, pack_half2<OUT>(acc[i][j][0], acc[i][j][1]),
-                   pack_half2<OUT>(acc[i][j][2], acc[i][j][3]));
-      wait_lgkm0();
-      asm volatile("" ::: "memory");
-      const int m = m0 + (lane & 15) * 8;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int r = k * 4 + (lane >> 4), n = n0 + r;
-        const u32x4 w = *reinterpret_cast<const u32x4*>(area + r * kRowsN + (lane & 15) * 16);
-        if (n >= p.N || m >= p.M) continue;
+          Area::put_by_n(area, i, j, li, lq, pack_half2<OUT>(acc[i][j][0], acc[i][j][1]),
+                         pack_half2<OUT>(acc[i][j][2], acc[i][j][3]));
+      Area::template take<true>(area, [&](int r, int c, const u32x4& w) {
+        const int n = n0 + r, m = m0 + c;
+        if (n >= p.N || m >= p.M) return;
         uint16_t* o = static_cast<uint16_t*>(p.out) + int64_t(n) * p.ldo + m;
         if ((p.ldo & 7) == 0) {
           __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(o));   // not read again here: leave the caches to the operands
@@ -374,9 +380,119 @@ __global__ __launch_bounds__(C::THREADS) void xent_product_kernel(XentProduct p,
           *reinterpret_cast<u32x2*>(o) = u32x2{w[0], w[1]};
           *reinterpret_cast<u32x2*>(o + 4) = u32x2{w[2], w[3]};
         }
-      }
+      });
     }
   });
+}
+
+// dx for few tokens: acc[split][t][h] = sum over the split's v of q[t][v] w[v][h].
+// The product is a stream of W, whose rows lie along h, not along the
+// reduction: transposing W first, as the large products do, would read and
+// write it once more.  A workgroup of 8 waves owns TF*16 tokens and 128
+// columns; its waves take the split's 32-row chunks in turn, bring each into
+// LDS (16 bytes a lane) and take the operands out by transpose reads, the next
+// chunk's rows arriving meanwhile; in the end the waves' tiles are added in a
+// fixed order.
+struct FewDx {
+  const uint16_t* w;    // the piece's rows [vn][H], ldw
+  const uint16_t* d;    // q [T][ldd], zeros from vn to vpad
+  int64_t ldw, ldd;
+  int T, H, vn, vpad, vsplit;   // a split takes vsplit rows (a multiple of 32)
+  float* acc;           // [splits][T][H]
+  bool add;
+};
+constexpr int kFewWaves = 8;
+constexpr int kFewPitch = 128 * 2 + 32;
+__host__ __device__ constexpr int few_row(int v) { return v * kFewPitch + (((v >> 3) & 1) + (v >> 4)) * 128; }
+constexpr int kFewTile = few_row(31) + 256;
+static_assert(kFewTile % 16 == 0, "aligned tiles");
+
+template <int DT, int TF>
+__global__ __launch_bounds__(kFewWaves * 64) void xent_dx_few_kernel(FewDx p) {
+  constexpr int LDS = kFewWaves * kFewTile > kFewWaves / 2 * TF * 8 * 1024 ? kFewWaves * kFewTile
+                                                                             : kFewWaves / 2 * TF * 8 * 1024;
+  __shared__ __align__(16) unsigned char smem[LDS];
+  const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h0 = blockIdx.x * 128;
+  const int v0 = blockIdx.y * p.vsplit, v1 = min(v0 + p.vsplit, p.vpad);
+  unsigned char* tile = smem + wave * kFewTile;
+  const int piece = lane & 15, prow = lane >> 4;
+  const int col = h0 + piece * 8 < p.H ? h0 + piece * 8 : 0;   // columns past H: results not stored
+  const int tr_row = 8 * (lane >> 4) + ((lane >> 2) & 3);
+  const int tr_lo = few_row(tr_row) + 8 * (lane & 3), tr_hi = few_row(tr_row + 4) + 8 * (lane & 3);
+  f32x4 acc[TF][8];
+#pragma unroll
+  for (int i = 0; i < TF; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  u32x4 x[8], q[TF];
+  auto load = [&](int v) {   // rows past vn reread the last one and meet zeros of q
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      x[k] = *reinterpret_cast<const u32x4*>(p.w + int64_t(min(v + k * 4 + prow, p.vn - 1)) * p.ldw + col);
+#pragma unroll
+    for (int i = 0; i < TF; ++i)
+      q[i] = *reinterpret_cast<const u32x4*>(p.d + int64_t(min(i * 16 + li, p.T - 1)) * p.ldd + v + 8 * lq);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int v = v0 + wave * 32;
+  if (v < v1) load(v);
+  for (; v < v1; v += kFewWaves * 32) {
+    u32x4 a[TF];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) *reinterpret_cast<u32x4*>(tile + few_row(k * 4 + prow) + piece * 16) = x[k];
+#pragma unroll
+    for (int i = 0; i < TF; ++i) a[i] = q[i];
+    __builtin_amdgcn_sched_barrier(0);
+    if (v + kFewWaves * 32 < v1) load(v + kFewWaves * 32);
+    wait_lgkm0();            // a wave's LDS operations are carried out in order: no barrier
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const u32x2 lo = lds_read_tr(tile + tr_lo + 32 * j), hi = lds_read_tr(tile + tr_hi + 32 * j);
+      const u32x4 b = {lo[0], lo[1], hi[0], hi[1]};
+      // D[h][t]: the lane holds 4 consecutive h of token li
+#pragma unroll
+      for (int i = 0; i < TF; ++i) acc[i][j] = mfma32<DT>(b, a[i], acc[i][j]);
+    }
+    wait_lgkm0();
+    asm volatile("" ::: "memory");   // the next chunk's writes stay behind these reads
+  }
+  f32x4 (*part)[TF * 8][64] = reinterpret_cast<f32x4 (*)[TF * 8][64]>(smem);
+  for (int half = kFewWaves / 2; half > 0; half >>= 1) {
+    __syncthreads();         // the tiles, then the sums of the round before, are read
+    if (wave >= half && wave < 2 * half) {
+#pragma unroll
+      for (int i = 0; i < TF; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) part[wave - half][i * 8 + j][lane] = acc[i][j];
+    }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int i = 0; i < TF; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] += part[wave][i * 8 + j][lane];
+    }
+  }
+  if (wave != 0) return;
+#pragma unroll
+  for (int i = 0; i < TF; ++i) {
+    const int t = i * 16 + li;
+    if (t >= p.T) continue;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int h = h0 + j * 16 + 4 * lq;
+      if (h >= p.H) continue;      // H is a multiple of 8
+      float* o = p.acc + (int64_t(blockIdx.y) * p.T + t) * p.H + h;
+      f32x4 r;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] = acc[i][j][e] * (1.f / kOperandScale<DT>);
+      if (p.add) r += *reinterpret_cast<const f32x4*>(o);
+      *reinterpret_cast<f32x4*>(o) = r;
+    }
+  }
 }
 
 // dx = g times the sum of the splits' fp32 shares, in order, rounded once.  A
@@ -410,8 +526,7 @@ template <class C, typename Kern, typename Args, typename... Rest>
 hipError_t launch_tiles(Kern kern, const Args& args, int64_t tilesA, int64_t tilesB, int64_t splits, hipStream_t s,
                         Rest... rest) {
   if (tilesA * tilesB * C::THREADS > 0xFFFFFFFFll) return hipErrorInvalidValue;
-  // (the kernels that write through LDS take piped tiles only)
-  constexpr int lds = std::is_same_v<C, GemmTilePiped> ? kOutLds : C::LDS;
+  constexpr int lds = OutArea<C>::LDS;
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), lds); e != hipSuccess) return e;
   // an XCD's run of tiles covers about 4 tiles of A by what fits of B
   const int group = int(std::min<int64_t>(tilesA, 4));
@@ -447,6 +562,10 @@ hipError_t forward_dt(const XentArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Up to this many tokens the products are streams of W: narrow tiles, and dx
+// without a transposed W (T = 64 on 32000 x 4096: FEW_US).
+constexpr int64_t kFewTokens = 64;
+
 // Where the backward pass keeps things in its workspace (bytes).
 struct BwdPlan {
   int64_t piece, ldt, ldd, splits, ksplit;
@@ -463,8 +582,9 @@ BwdPlan plan_bwd(int64_t T, int64_t V, int64_t H, bool dx, bool dw) {
   const int64_t pieces = (V + most - 1) / most;
   p.piece = up_to((V + pieces - 1) / pieces, 256);
   p.ldd = p.piece;
-  // dx has few tiles: its reduction is split until the chip is covered
-  const int64_t tiles = ((T + 255) / 256) * ((H + 255) / 256);
+  // dx has few tiles: its reduction is split until the chip is covered (for few
+  // tokens twice, with tiles of all tokens by 128)
+  const int64_t tiles = T <= kFewTokens ? ((H + 127) / 128 + 1) / 2 : ((T + 255) / 256) * ((H + 255) / 256);
   p.splits = std::min<int64_t>(std::max<int64_t>(256 / tiles, 1), std::max<int64_t>(p.piece / 512, 1));
   p.ksplit = up_to((p.piece + p.splits - 1) / p.splits, 64);
   p.splits = (p.piece + p.ksplit - 1) / p.ksplit;
@@ -478,7 +598,7 @@ BwdPlan plan_bwd(int64_t T, int64_t V, int64_t H, bool dx, bool dw) {
   p.xt = take(dw ? size_t(H) * p.ldt * 2 : 0);
   p.dt = take(dw ? size_t(p.piece) * p.ldt * 2 : 0);
   p.d = take(dx ? size_t(T) * p.ldd * 2 : 0);
-  p.wt = take(dx ? size_t(H) * p.ldd * 2 : 0);
+  p.wt = take(dx && T > kFewTokens ? size_t(H) * p.ldd * 2 : 0);
   p.acc = take(dx ? size_t(p.splits) * T * H * 4 : 0);
   p.total = at;
   return p;
@@ -525,15 +645,26 @@ hipError_t backward_dt(const XentArgs& a, hipStream_t s) {
     b.v0 = int(v0);
     b.vn = int(vn);
     b.vpad = int(vpad);
-    using C = TileBig;
-    e = launch_tiles<C>(xent_dlogits_kernel<DT, C>, b, (vpad + C::BM - 1) / C::BM, (pl.ldt + C::BN - 1) / C::BN, 1, s);
-    if (e != hipSuccess) return e;
-    if (a.dx) {
+    auto dlogits = [&](auto tile) {
+      using C = decltype(tile);
+      return launch_tiles<C>(xent_dlogits_kernel<DT, C>, b, (vpad + C::BM - 1) / C::BM, (pl.ldt + C::BN - 1) / C::BN, 1,
+                             s);
+    };
+    if ((e = a.T <= kFewTokens ? dlogits(Tile64{}) : dlogits(TileBig{})) != hipSuccess) return e;
+    const int64_t splits = (vpad + pl.ksplit - 1) / pl.ksplit;
+    if (a.dx && a.T <= kFewTokens) {
+      const FewDx p{a.w + v0 * a.ldw, b.d, a.ldw, pl.ldd, int(a.T), int(a.H), int(vn), int(vpad), int(pl.ksplit), acc,
+                    v0 > 0};
+      const dim3 grid(unsigned((a.H + 127) / 128), unsigned(splits));
+      if (a.T <= 16) hipLaunchKernelGGL((xent_dx_few_kernel<DT, 1>), grid, dim3(kFewWaves * 64), 0, s, p);
+      else hipLaunchKernelGGL((xent_dx_few_kernel<DT, 4>), grid, dim3(kFewWaves * 64), 0, s, p);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    } else if (a.dx) {
       if ((e = transpose(a.w + v0 * a.ldw, a.ldw, vn, a.H, nullptr, 0, wt, pl.ldd, s)) != hipSuccess) return e;
       XentProduct p{wt, b.d, pl.ldd, pl.ldd, int(a.H), int(a.T), int(vpad), int(pl.ksplit), nullptr, acc, a.H,
                     a.T * a.H, v0 > 0};
       // (a last piece shorter than the others may need fewer splits: the rest keep their sums)
-      if ((e = product<DT>(p, NM_F32, (vpad + pl.ksplit - 1) / pl.ksplit, s)) != hipSuccess) return e;
+      if ((e = product<DT>(p, NM_F32, splits, s)) != hipSuccess) return e;
     }
     if (a.dw) {
       const size_t es = a.dw_dtype == NM_F32 ? 4 : 2;
