@@ -83,33 +83,61 @@ __device__ inline void store_piece(void* row, int c, int H, const float* f) {
   }
 }
 
+// Sum over a wave, the same bits in every lane: shifts within rows of 16 lanes,
+// then row totals passed on, all on the vector ALUs (six LDS permutes a sum
+// would take longer than a short row's arithmetic), and lane 63's total read
+// back as a scalar.
+template <int CTRL, int ROWS>
+__device__ inline float dpp_add(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xF, true));
+}
 __device__ inline float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  v = dpp_add<0x111, 0xF>(v);   // row_shr 1, 2, 4, 8
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);   // row_bcast 15 into rows 1 and 3
+  v = dpp_add<0x143, 0xC>(v);   // row_bcast 31 into rows 2 and 3
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
-// Sums of a and b over the TPR threads of a row, the same bits in every
+// Sums of N values over the TPR threads of a row, the same bits in every
 // thread: each wave sums itself, the waves' sums are added in wave order.
 // `slot` alternates between two LDS areas, so one barrier a call suffices (a
 // wave can be at most one call ahead of the slowest).
-template <int TPR>
-__device__ inline void row_sum2(float& a, float& b, float2 (*part)[16], int& slot) {
-  a = wave_sum(a);
-  b = wave_sum(b);
+template <int TPR, int N>
+__device__ inline void row_sum(float (&v)[N], float (*part)[16][2], int& slot) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
   if constexpr (TPR > 64) {
     constexpr int W = TPR / 64;
     const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) part[slot][wave] = make_float2(a, b);
-    __syncthreads();
-    a = 0.f;
-    b = 0.f;
+    if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      a += part[slot][w].x;
-      b += part[slot][w].y;
+      for (int i = 0; i < N; ++i) part[slot][wave][i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) v[i] += part[slot][w][i];
     }
     slot ^= 1;
+  }
+}
+
+// use(e) for the elements of the piece at column c that lie before H: without
+// a test an element where the whole piece does.
+template <int V, typename Use>
+__device__ inline void each_inside(int c, int H, Use&& use) {
+  if (c + V <= H) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) use(e);
+  } else if (c < H) {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (c + e < H) use(e);
   }
 }
 
@@ -124,7 +152,7 @@ __global__ __launch_bounds__(block_of(TPR)) void layernorm_kernel(const void* __
                                                                   float* __restrict__ mean, float* __restrict__ rstd) {
   constexpr int V = Elem<DT>::V, NV = EPT / V, E = Elem<DT>::SIZE;
   constexpr int ROWS = block_of(TPR) / TPR;
-  __shared__ float2 part[2][16];
+  __shared__ float part[2][16][2];
   const int lane = threadIdx.x % TPR;
   u32x4 wr[NV], br[NV];
 #pragma unroll
@@ -134,31 +162,36 @@ __global__ __launch_bounds__(block_of(TPR)) void layernorm_kernel(const void* __
     if (bias) br[j] = load_piece<DT>(bias, c, H);
   }
   int slot = 0;
-  // TPR > 64: the rows of a workgroup's loop are the same for every wave, so
-  // its barriers are met by all
-  for (int64_t t = int64_t(blockIdx.x) * ROWS + threadIdx.x / TPR; t < T; t += int64_t(gridDim.x) * ROWS) {
-    const char* row = static_cast<const char*>(x) + t * ldx * E;
-    u32x4 raw[NV];
+  // A group walks its rows, the next one's loads issued before the current
+  // one's sums.  TPR > 64: the rows of a workgroup's loop are the same for every
+  // wave, so its barriers are met by all.
+  const int64_t stride = int64_t(gridDim.x) * ROWS;
+  int64_t t = int64_t(blockIdx.x) * ROWS + threadIdx.x / TPR;
+  auto load_row = [&](int64_t r, u32x4 (&v)[NV]) {
+    const char* row = static_cast<const char*>(x) + r * ldx * E;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) raw[j] = load_piece<DT>(row, (j * TPR + lane) * V, H);
-    float s = 0.f, unused = 0.f;
+    for (int j = 0; j < NV; ++j) v[j] = load_piece<DT>(row, (j * TPR + lane) * V, H);
+  };
+  u32x4 raw[NV], ahead[NV];
+  if (t < T) load_row(t, raw);
+  for (; t < T; t += stride) {
+    if (t + stride < T) load_row(t + stride, ahead);
+    float sum[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < V; ++e) s += elem<DT>(raw[j], e);
-    row_sum2<TPR>(s, unused, part, slot);
-    const float mu = s / float(H);
-    float q = 0.f;
+      for (int e = 0; e < V; ++e) sum[0] += elem<DT>(raw[j], e);
+    row_sum<TPR>(sum, part, slot);
+    const float mu = sum[0] / float(H);
+    float q[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
+      each_inside<V>((j * TPR + lane) * V, H, [&](int e) {
         const float d = elem<DT>(raw[j], e) - mu;
-        if ((j * TPR + lane) * V + e < H) q += d * d;
-      }
-    unused = 0.f;
-    row_sum2<TPR>(q, unused, part, slot);
-    const float rs = 1.f / sqrtf(q / float(H) + eps);
+        q[0] += d * d;
+      });
+    row_sum<TPR>(q, part, slot);
+    const float rs = 1.f / sqrtf(q[0] / float(H) + eps);
     if (mean && lane == 0) {
       mean[t] = mu;
       rstd[t] = rs;
@@ -175,6 +208,8 @@ __global__ __launch_bounds__(block_of(TPR)) void layernorm_kernel(const void* __
       }
       store_piece<DT>(out, (j * TPR + lane) * V, H, f);
     }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) raw[j] = ahead[j];
   }
 }
 
@@ -186,31 +221,29 @@ __global__ __launch_bounds__(1024) void layernorm_long_kernel(const void* __rest
                                                               void* __restrict__ y, int64_t ldy,
                                                               float* __restrict__ mean, float* __restrict__ rstd) {
   constexpr int V = Elem<DT>::V, E = Elem<DT>::SIZE;
-  __shared__ float2 part[2][16];
+  __shared__ float part[2][16][2];
   int slot = 0;
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
     const char* row = static_cast<const char*>(x) + t * ldx * E;
     char* out = static_cast<char*>(y) + t * ldy * E;
-    float s = 0.f, unused = 0.f;
+    float sum[1] = {0.f};
     for (int c = threadIdx.x * V; c < H; c += 1024 * V) {
       const u32x4 v = load_piece<DT>(row, c, H);
 #pragma unroll
-      for (int e = 0; e < V; ++e) s += elem<DT>(v, e);
+      for (int e = 0; e < V; ++e) sum[0] += elem<DT>(v, e);
     }
-    row_sum2<1024>(s, unused, part, slot);
-    const float mu = s / float(H);
-    float q = 0.f;
+    row_sum<1024>(sum, part, slot);
+    const float mu = sum[0] / float(H);
+    float q[1] = {0.f};
     for (int c = threadIdx.x * V; c < H; c += 1024 * V) {
       const u32x4 v = load_piece<DT>(row, c, H);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
+      each_inside<V>(c, H, [&](int e) {
         const float d = elem<DT>(v, e) - mu;
-        if (c + e < H) q += d * d;
-      }
+        q[0] += d * d;
+      });
     }
-    unused = 0.f;
-    row_sum2<1024>(q, unused, part, slot);
-    const float rs = 1.f / sqrtf(q / float(H) + eps);
+    row_sum<1024>(q, part, slot);
+    const float rs = 1.f / sqrtf(q[0] / float(H) + eps);
     if (mean && threadIdx.x == 0) {
       mean[t] = mu;
       rstd[t] = rs;
@@ -245,7 +278,7 @@ __global__ __launch_bounds__(block_of(TPR)) void layernorm_bwd_kernel(
     void* __restrict__ dx, int64_t lddx, float* __restrict__ part_wb) {
   constexpr int V = Elem<DT>::V, NV = EPT / V, E = Elem<DT>::SIZE;
   constexpr int ROWS = block_of(TPR) / TPR;
-  __shared__ float2 part[2][16];
+  __shared__ float part[2][16][2];
   const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const int G = gridDim.x * ROWS;
   const float inv_h = 1.f / float(H);
@@ -278,25 +311,20 @@ __global__ __launch_bounds__(block_of(TPR)) void layernorm_bwd_kernel(
     u32x4 xn[NV], gn[NV];
     float mn = 0.f, rn = 0.f;
     if (t + G < T) load_row(t + G, xn, gn, mn, rn);
-    float c1 = 0.f, c2 = 0.f;
+    float c[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        // past H dy is zero, and xh takes no part in any sum but through it
+      each_inside<V>((j * TPR + lane) * V, H, [&](int e) {
         const float g = elem<DT>(gr[j], e);
         const float xh = (elem<DT>(xr[j], e) - mu) * rs;
         const float p = weight ? g * elem<DT>(wr[j], e) : g;
-        if ((j * TPR + lane) * V + e < H) {
-          c1 += p;
-          c2 += p * xh;
-          aw[j * V + e] += g * xh;
-          ab[j * V + e] += g;
-        }
-      }
-    row_sum2<TPR>(c1, c2, part, slot);
-    c1 *= inv_h;
-    c2 *= inv_h;
+        c[0] += p;
+        c[1] += p * xh;
+        aw[j * V + e] += g * xh;
+        ab[j * V + e] += g;
+      });
+    row_sum<TPR>(c, part, slot);
+    const float c1 = c[0] * inv_h, c2 = c[1] * inv_h;
     char* out = static_cast<char*>(dx) + t * lddx * E;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -359,14 +387,14 @@ __global__ __launch_bounds__(1024) void layernorm_bwd_long_kernel(
     const float* __restrict__ mean, const float* __restrict__ rstd, const void* __restrict__ weight,
     void* __restrict__ dx, int64_t lddx) {
   constexpr int V = Elem<DT>::V, E = Elem<DT>::SIZE;
-  __shared__ float2 part[2][16];
+  __shared__ float part[2][16][2];
   int slot = 0;
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
     const char* xrow = static_cast<const char*>(x) + t * ldx * E;
     const char* grow = static_cast<const char*>(dy) + t * ldg * E;
     char* out = static_cast<char*>(dx) + t * lddx * E;
     const float mu = mean[t], rs = rstd[t];
-    float c1 = 0.f, c2 = 0.f;
+    float sum[2] = {0.f, 0.f};
     auto each = [&](auto&& use) {
       for (int c = threadIdx.x * V; c < H; c += 1024 * V) {
         const u32x4 xv = load_piece<DT>(xrow, c, H), gv = load_piece<DT>(grow, c, H);
@@ -382,16 +410,13 @@ __global__ __launch_bounds__(1024) void layernorm_bwd_long_kernel(
       }
     };
     each([&](int c, const float* p, const float* xh) {
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        if (c + e < H) {
-          c1 += p[e];
-          c2 += p[e] * xh[e];
-        }
+      each_inside<V>(c, H, [&](int e) {
+        sum[0] += p[e];
+        sum[1] += p[e] * xh[e];
+      });
     });
-    row_sum2<1024>(c1, c2, part, slot);
-    c1 /= float(H);
-    c2 /= float(H);
+    row_sum<1024>(sum, part, slot);
+    const float c1 = sum[0] / float(H), c2 = sum[1] / float(H);
     each([&](int c, const float* p, const float* xh) {
       float f[V];
 #pragma unroll
@@ -471,10 +496,21 @@ Shape row_shape(int64_t H) {
 // Workgroups of a forward pass or of a long-row kernel; past this many they walk.
 unsigned row_grid(int64_t n) { return unsigned(n < (int64_t(1) << 20) ? n : int64_t(1) << 20); }
 
+// Workgroups of the forward pass: one a row group while they all fit the chip
+// at once (2048 threads a CU), past that the fewest rounds, evenly filled, so
+// that a group's next row arrives while it works on one (12608 x 768 fp16: 13.6
+// us with a workgroup every 4 rows and sums by LDS permutes, 12.4 now; 8192 x
+// 4096 bf16: 26.6, now 23.7, 5.7 TB/s).
+unsigned fwd_grid(int64_t groups, int threads) {
+  const int64_t resident = int64_t(256) * 2048 / threads;
+  const int64_t rounds = (groups + resident - 1) / resident;
+  return unsigned(rounds <= 1 ? groups : (groups + rounds - 1) / rounds);
+}
+
 template <int DT, int TPR, int EPT>
 hipError_t fwd_cfg(const LayerNormArgs& a, hipStream_t s) {
   constexpr int ROWS = block_of(TPR) / TPR;
-  hipLaunchKernelGGL((layernorm_kernel<DT, TPR, EPT>), dim3(row_grid((a.T + ROWS - 1) / ROWS)), dim3(block_of(TPR)), 0,
+  hipLaunchKernelGGL((layernorm_kernel<DT, TPR, EPT>), dim3(fwd_grid((a.T + ROWS - 1) / ROWS, block_of(TPR))), dim3(block_of(TPR)), 0,
                      s, a.x, int(a.T), int(a.H), a.ldx, a.weight, a.bias, a.eps, a.y, a.ldy, a.mean_out, a.rstd_out);
   return hipGetLastError();
 }

@@ -34,6 +34,7 @@ constexpr float kInf = __builtin_inff();
 // For few tokens, narrow tiles with a deeper ring (the product is then a stream
 // of W).
 using TileBig = GemmTilePiped;
+using Tile128 = GemmTile<128, 128, 2, 2, 4>;
 using Tile64 = GemmTile<128, 64, 4, 1, 4>;
 using Tile16 = GemmTile<128, 16, 4, 1, 6>;
 
@@ -414,7 +415,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void xent_dx_few_kernel(FewDx p) {
   __shared__ __align__(16) unsigned char smem[LDS];
   const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int h0 = blockIdx.x * 128;
+  const int h0 = blockIdx.x * 128, t0 = blockIdx.z * (TF * 16);
   const int v0 = blockIdx.y * p.vsplit, v1 = min(v0 + p.vsplit, p.vpad);
   unsigned char* tile = smem + wave * kFewTile;
   const int piece = lane & 15, prow = lane >> 4;
@@ -433,7 +434,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void xent_dx_few_kernel(FewDx p) {
       x[k] = *reinterpret_cast<const u32x4*>(p.w + int64_t(min(v + k * 4 + prow, p.vn - 1)) * p.ldw + col);
 #pragma unroll
     for (int i = 0; i < TF; ++i)
-      q[i] = *reinterpret_cast<const u32x4*>(p.d + int64_t(min(i * 16 + li, p.T - 1)) * p.ldd + v + 8 * lq);
+      q[i] = *reinterpret_cast<const u32x4*>(p.d + int64_t(min(t0 + i * 16 + li, p.T - 1)) * p.ldd + v + 8 * lq);
     __builtin_amdgcn_sched_barrier(0);
   };
   int v = v0 + wave * 32;
@@ -479,7 +480,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void xent_dx_few_kernel(FewDx p) {
   if (wave != 0) return;
 #pragma unroll
   for (int i = 0; i < TF; ++i) {
-    const int t = i * 16 + li;
+    const int t = t0 + i * 16 + li;
     if (t >= p.T) continue;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -539,7 +540,21 @@ XentArgsDev dev_args(const XentArgs& a) {
   return XentArgsDev{a.x, a.w, a.labels, a.ldx, a.ldw, int(a.T), int(a.V), int(a.H)};
 }
 
-int64_t stats_tile_v(int64_t T) { return T <= 64 ? 128 : 256; }
+// Tiles of a product over words and tokens: as wide as so few tokens are, with
+// 128 words (more workgroups); past 128 tokens the 256 x 256 tiles, whose
+// operands are read half as often (T = 512 on 32000 x 4096, forward: 110 us
+// against 190 with 128 x 128; T = 128: 81 against 55), unless they would leave
+// half the chip idle (T = 200 on 4000 x 1024: 28 us against 20).
+template <class Use>
+auto with_tile(int64_t T, int64_t words, Use&& use) {
+  if (T <= 16) return use(Tile16{});
+  if (T <= 64) return use(Tile64{});
+  if (T <= 128 || (T + 255) / 256 * ((words + 255) / 256) <= 128) return use(Tile128{});
+  return use(TileBig{});
+}
+int64_t stats_tile_v(int64_t T, int64_t V) {
+  return with_tile(T, V, [](auto tile) { return int64_t(decltype(tile)::BM); });
+}
 
 template <int DT, class C>
 hipError_t stats(const XentArgs& a, float2* part, float* at_label, hipStream_t s) {
@@ -549,22 +564,21 @@ hipError_t stats(const XentArgs& a, float2* part, float* at_label, hipStream_t s
 
 template <int DT>
 hipError_t forward_dt(const XentArgs& a, hipStream_t s) {
-  const int64_t tilesV = (a.V + stats_tile_v(a.T) - 1) / stats_tile_v(a.T);
+  const int64_t tilesV = (a.V + stats_tile_v(a.T, a.V) - 1) / stats_tile_v(a.T, a.V);
   float2* part = static_cast<float2*>(a.workspace);
   float* at_label = reinterpret_cast<float*>(part + tilesV * a.T);
-  hipError_t e;
-  if (a.T <= 16) e = stats<DT, Tile16>(a, part, at_label, s);
-  else if (a.T <= 64) e = stats<DT, Tile64>(a, part, at_label, s);
-  else e = stats<DT, TileBig>(a, part, at_label, s);
+  const hipError_t e =
+      with_tile(a.T, a.V, [&](auto tile) { return stats<DT, decltype(tile)>(a, part, at_label, s); });
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(xent_join_kernel, dim3(unsigned((a.T + 63) / 64)), dim3(1024), 0, s, part, at_label, a.labels,
                      int(tilesV), int(a.T), int(a.V), a.loss, a.lse_out);
   return hipGetLastError();
 }
 
-// Up to this many tokens the products are streams of W: narrow tiles, and dx
-// without a transposed W (T = 64 on 32000 x 4096: FEW_US).
-constexpr int64_t kFewTokens = 64;
+// Up to this many tokens dx is a stream of W as it lies, past it a product with
+// W transposed (forward and backward on 32000 x 4096: T = 128 331 us against
+// 427, T = 200 545 against 519).
+constexpr int64_t kFewTokens = 128;
 
 // Where the backward pass keeps things in its workspace (bytes).
 struct BwdPlan {
@@ -645,17 +659,18 @@ hipError_t backward_dt(const XentArgs& a, hipStream_t s) {
     b.v0 = int(v0);
     b.vn = int(vn);
     b.vpad = int(vpad);
-    auto dlogits = [&](auto tile) {
+    // (ldt is a multiple of 64, which the narrowest tile here has to cover)
+    e = with_tile(std::max<int64_t>(a.T, 17), vpad, [&](auto tile) {
       using C = decltype(tile);
       return launch_tiles<C>(xent_dlogits_kernel<DT, C>, b, (vpad + C::BM - 1) / C::BM, (pl.ldt + C::BN - 1) / C::BN, 1,
                              s);
-    };
-    if ((e = a.T <= kFewTokens ? dlogits(Tile64{}) : dlogits(TileBig{})) != hipSuccess) return e;
+    });
+    if (e != hipSuccess) return e;
     const int64_t splits = (vpad + pl.ksplit - 1) / pl.ksplit;
     if (a.dx && a.T <= kFewTokens) {
       const FewDx p{a.w + v0 * a.ldw, b.d, a.ldw, pl.ldd, int(a.T), int(a.H), int(vn), int(vpad), int(pl.ksplit), acc,
                     v0 > 0};
-      const dim3 grid(unsigned((a.H + 127) / 128), unsigned(splits));
+      const dim3 grid(unsigned((a.H + 127) / 128), unsigned(splits), unsigned((a.T + 63) / 64));
       if (a.T <= 16) hipLaunchKernelGGL((xent_dx_few_kernel<DT, 1>), grid, dim3(kFewWaves * 64), 0, s, p);
       else hipLaunchKernelGGL((xent_dx_few_kernel<DT, 4>), grid, dim3(kFewWaves * 64), 0, s, p);
       if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -690,7 +705,7 @@ hipError_t backward_dt(const XentArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t xent_workspace(int64_t T, int64_t V) {
-  const int64_t tilesV = (V + stats_tile_v(T) - 1) / stats_tile_v(T);
+  const int64_t tilesV = (V + stats_tile_v(T, V) - 1) / stats_tile_v(T, V);
   return size_t(tilesV) * T * 8 + size_t(T) * 4;
 }
 
