@@ -92,7 +92,7 @@ KERNEL_SOURCES = {
     "hybrid": ["nm_hybrid.hip", "nm_select.h"],
     "host": ["nm_hosts.hip"],
     "train": ["nm_train.hip", "nm_lowrank.h"],
-    "adapter": ["nm_adapter.hip", "nm_lowrank.h", "nm_gemm_nt.h"],
+    "adapter": ["nm_adapter.hip", "nm_lowrank.h"],
     "layernorm": ["nm_layernorm.hip"],
     "xent": ["nm_xent.hip", "nm_gemm_nt.h"],
 }

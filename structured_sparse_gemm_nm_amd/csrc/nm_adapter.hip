@@ -20,7 +20,6 @@
 // expand; the adapters themselves are small.  The expand step costs no pass of
 // its own where the shared product's kernel holds its tile in registers and
 // adds the term there (few tokens, 2:4 prefill, and dx).
-#include "nm_gemm_nt.h"
 #include "nm_internal.h"
 #include "nm_lowrank.h"
 
@@ -34,108 +33,176 @@ __device__ inline u32x4 load16(__amdgpu_buffer_rsrc_t rsrc, uint32_t off) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0));
 }
 
-// ---------------------------------------------------------------------------
-// Shrink: V[t][j] = s_a sum_c M_a[j][c] Z[t][c], M as [n][r][C].
-// The product of a 64-token tile with one adapter's 32 or 64 ranks is far too
-// small for the chip, so its columns are split over blockIdx.y and the shares,
-// part[split][t][j], are added in order by adapter_join_kernel.  Loading whole
-// 128-byte lines into LDS (gemm_nt) matters more than the few operations: with
-// operand fragments loaded straight into registers (16 rows of 64 bytes an
-// instruction) 2048 tokens x 4096, rank 32, took 13 us in place of SHRINK_US.
-// Several adapters in a tile are dealt to blockIdx.z in turn.
-// ---------------------------------------------------------------------------
-struct ShrinkArgs {
-  const int32_t* ids;
-  const uint16_t* M;
-  const uint16_t* Z;
-  int64_t ldz;
-  int n, T, C, r, csplit;   // a split takes csplit columns (a multiple of 64)
-  float* part;              // [splits][T][r]
-};
-
-template <int DT, class C>
-__global__ __launch_bounds__(C::THREADS) void adapter_shrink_kernel(ShrinkArgs p, int rank_tiles) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  static_assert(C::BN == 64, "a lane a token");
-  const int tt = blockIdx.x / rank_tiles, tr = blockIdx.x - tt * rank_tiles;
-  const int t = tt * 64 + (threadIdx.x & 63);
-  const int id = t < p.T ? p.ids[t] : -1;
-  // every wave holds the same ids, so the loop and its barriers are uniform
-  uint64_t todo = __ballot(uint32_t(id) < uint32_t(p.n));
-  const int c0 = blockIdx.y * p.csplit, K = min(p.C - c0, p.csplit);
-  float* part = p.part + int64_t(blockIdx.y) * p.T * p.r;
-  for (uint32_t turn = 0; todo; ++turn) {
-    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-    const uint64_t mine = __ballot(id == a);
-    todo &= ~mine;
-    if (turn % gridDim.z != blockIdx.z) continue;
-    gemm_nt<DT, C>(p.M + int64_t(a) * p.r * p.C + c0, p.C, p.r, p.Z + c0, p.ldz, p.T, K, tr, tt, smem,
-                   [&](auto& acc, int wm, int wn, int li, int lq) {
-#pragma unroll
-      for (int j = 0; j < C::FN; ++j) {
-        const int k = wn * C::FN * 16 + j * 16 + li;
-        if (!((mine >> k) & 1u)) continue;
-        float* row = part + int64_t(tt * 64 + k) * p.r;
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int q = tr * C::BM + wm * C::FM * 16 + i * 16 + 4 * lq + e;
-            if (q < p.r) row[q] = acc[i][j][e];
-          }
-      }
-    });
-  }
-}
-
-// One of the join's jobs: value = now_a sum of `splits` shares [T][r], in
-// order; zero for a token without an adapter.  Written where wanted: the fp32
-// value; next_a value in three bf16 parts, [T][3][r8] for the products over
-// ranks (lowrank_add) and [3][r][ldt] for those over tokens (the gradients).
-struct JoinJob {
-  const float* part;
-  int splits;
-  const float* now;     // or null: 1
-  const float* next;    // or null: 1
+// What is written of shrunk values V [T][r]: the fp32 value, and next_a V in
+// three bf16 parts, P [T][3][r8] for the products over ranks (lowrank_add) and
+// PT [3][r][ldt] for those over tokens (the gradients).  Each may be null.
+struct ShrunkOut {
+  const float* next;    // the adapter's factor in the parts, or null: 1
   float* V;
   uint16_t* P;
   uint16_t* PT;
+  int ldt;
 };
 
-// A thread an element (j runs to r8, where P holds zeros); blockIdx.y is the job.
-__global__ __launch_bounds__(256) void adapter_join_kernel(JoinJob first, JoinJob second,
-                                                           const int32_t* __restrict__ ids, int n, int T, int r,
-                                                           int ldt) {
-  const JoinJob& q = blockIdx.y ? second : first;
+// Element j < r8 of token t, whose adapter is a (or none: zeros).
+__device__ inline void put_shrunk(const ShrunkOut& o, int64_t t, int j, int r, bool some, int a, float v) {
   const int r8 = (r + 7) & ~7;
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= int64_t(T) * r8) return;
-  const int64_t t = i / r8, all = int64_t(T) * r;
-  const int j = int(i - t * r8);
-  float v = 0.f;
-  if (j < r) {
-    const int64_t at = t * r + j;
-    const int a = ids[t];
-#pragma unroll 8
-    for (int s = 0; s < q.splits; ++s) v += q.part[s * all + at];
-    const bool some = uint32_t(a) < uint32_t(n);
-    v = some ? (q.now ? v * q.now[a] : v) : 0.f;
-    if (q.V) q.V[at] = v;
-    if (some && q.next) v *= q.next[a];
-  }
+  v = some && j < r ? v : 0.f;
+  if (o.V && j < r) o.V[t * r + j] = v;
+  if (!o.P && !o.PT) return;
+  if (some && o.next) v *= o.next[a];
   uint16_t h[3];
   split3(v, h);
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    if (q.P) q.P[(t * 3 + k) * r8 + j] = h[k];
-    if (q.PT && j < r) q.PT[(int64_t(k) * r + j) * ldt + t] = h[k];
+    if (o.P) o.P[(t * 3 + k) * r8 + j] = h[k];
+    if (o.PT && j < r) o.PT[(int64_t(k) * r + j) * o.ldt + t] = h[k];
+  }
+}
+
+// The parts of a V that is already there: a thread an element.
+__device__ inline void parts_of(const float* V, const ShrunkOut& o, const int32_t* ids, int n, int T, int r,
+                                int64_t i) {
+  const int r8 = (r + 7) & ~7;
+  if (i >= int64_t(T) * r8) return;
+  const int64_t t = i / r8;
+  const int j = int(i - t * r8), a = ids[t];
+  put_shrunk(o, t, j, r, uint32_t(a) < uint32_t(n), a, j < r ? V[t * r + j] : 0.f);
+}
+__global__ __launch_bounds__(256) void adapter_parts_kernel(const float* __restrict__ V, ShrunkOut out,
+                                                            const int32_t* __restrict__ ids, int n, int T, int r) {
+  parts_of(V, out, ids, n, T, r, int64_t(blockIdx.x) * 256 + threadIdx.x);
+}
+
+// ---------------------------------------------------------------------------
+// Shrink: V[t][j] = now_a sum_c M_a[j][c] Z[t][c], M as [n][r][C].
+// A workgroup of 8 waves takes 16 tokens and RF*16 ranks: 16 tokens, so that
+// few of them make many workgroups.  The columns are dealt to the waves in
+// 64-wide steps; each wave brings its own steps' rows, whole 128-byte lines,
+// straight into its own ring of LDS stages and needs no barrier until the
+// waves' tiles are added, in wave order.  (Fragments loaded straight into
+// registers, 16 rows of 64 bytes an instruction, took 13 us for 2048 tokens x
+// 4096 at rank 32; tiles of 64 tokens with the columns split over workgroups
+// and a second kernel to add the shares 10 + 5; this SHRINK_US.)
+// Several adapters in a tile are dealt to blockIdx.z in turn.
+// ---------------------------------------------------------------------------
+constexpr int kShrinkWaves = 8;
+
+template <int RF>
+struct ShrinkRing {
+  static constexpr int ROWS = (1 + RF) * 16, STAGE = ROWS * 128, LOADS = ROWS / 8;
+  static constexpr int NS = RF == 1 ? 4 : 3;    // 16 KB or 18 KB a wave
+  static constexpr int LDS = kShrinkWaves * NS * STAGE;
+};
+
+template <int DT, int RF>
+__global__ __launch_bounds__(kShrinkWaves * 64) void adapter_shrink_kernel(
+    const int32_t* __restrict__ ids, int n, const uint16_t* __restrict__ M, const float* __restrict__ now,
+    const uint16_t* __restrict__ Z, int64_t ldz, int T, int C, int r, ShrunkOut out) {
+  using Ring = ShrinkRing<RF>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t0 = blockIdx.x * 16, r0 = blockIdx.y * (RF * 16);
+  const int t = t0 + li;
+  const int id = t < T ? ids[t] : -1;
+  const bool valid = uint32_t(id) < uint32_t(n);
+  // every wave holds the same ids, so the loop and its barriers are uniform
+  uint32_t todo = uint32_t(__ballot(valid)) & 0xFFFFu;
+  if (blockIdx.z == 0 && wave < RF && !valid && t < T) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = r0 + wave * 16 + lq * 4 + e;
+      if (j < ((r + 7) & ~7)) put_shrunk(out, t, j, r, false, 0, 0.f);
+    }
+  }
+  unsigned char* ring = smem + wave * (Ring::NS * Ring::STAGE);
+  f32x4 (*part)[RF][64] = reinterpret_cast<f32x4 (*)[RF][64]>(smem);
+  const int steps = (C + 63) >> 6, rem = C - (steps - 1) * 64;
+  const int mine_steps = wave < steps ? (steps - 1 - wave) / kShrinkWaves + 1 : 0;
+  // loads j: rows 8 j + lane / 8 of the tokens (j = 0, 1), then of the ranks
+  const uint32_t chunk = uint32_t((lane & 7) ^ ((lane >> 3) & 7));
+  const __amdgpu_buffer_rsrc_t rz = make_rsrc(Z + int64_t(t0) * ldz);
+  uint32_t off[Ring::LOADS];
+#pragma unroll
+  for (int j = 0; j < Ring::LOADS; ++j) {
+    const int row = 8 * j + (lane >> 3);
+    off[j] = (j < 2 ? uint32_t(min(row, T - 1 - t0)) * uint32_t(ldz)
+                    : uint32_t(min(r0 + row - 16, r - 1)) * uint32_t(C)) * 2u + chunk * 16u;
+  }
+  for (uint32_t turn = 0; todo; ++turn) {
+    const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+    const bool sel = id == a;
+    todo &= ~uint32_t(__ballot(sel));
+    if (turn % gridDim.z != blockIdx.z) continue;
+    const __amdgpu_buffer_rsrc_t rm = make_rsrc(M + int64_t(a) * r * C, uint32_t(r) * uint32_t(C) * 2u);
+    // this wave's i-th step into stage i % NS; past its last step that step
+    // again, into a stage nothing reads any more; chunks past C reread the
+    // step's first one
+    auto issue = [&](int i) {
+      const int s = wave + min(i, mine_steps - 1) * kShrinkWaves;
+      unsigned char* st = ring + i % Ring::NS * Ring::STAGE;
+      const uint32_t back = s == steps - 1 && int(chunk) * 8 >= rem ? chunk * 16u : 0u;
+#pragma unroll
+      for (int j = 0; j < Ring::LOADS; ++j) dma16(j < 2 ? rz : rm, off[j] - back, uint32_t(s) * 128u, st + j * 1024);
+    };
+    f32x4 acc[RF];
+#pragma unroll
+    for (int f = 0; f < RF; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (mine_steps > 0) {
+#pragma unroll
+      for (int i = 0; i < Ring::NS - 1; ++i) issue(i);
+      for (int i = 0; i < mine_steps; ++i) {
+        wait_lgkm0();                                    // the stage about to be refilled has been read
+        asm volatile("" ::: "memory");
+        issue(i + Ring::NS - 1);
+        wait_vmcnt<(Ring::NS - 1) * Ring::LOADS>();      // step i has landed
+        asm volatile("" ::: "memory");
+        const unsigned char* st = ring + i % Ring::NS * Ring::STAGE;
+        const bool tail = wave + i * kShrinkWaves == steps - 1;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = 4 * h + lq;
+          u32x4 z = *reinterpret_cast<const u32x4*>(st + (li * 8 + (c ^ (li & 7))) * 16);
+          u32x4 m[RF];
+#pragma unroll
+          for (int f = 0; f < RF; ++f)
+            m[f] = *reinterpret_cast<const u32x4*>(st + ((16 + f * 16 + li) * 8 + (c ^ (li & 7))) * 16);
+          if (tail && c * 8 >= rem) {
+            z = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int f = 0; f < RF; ++f) m[f] = u32x4{0u, 0u, 0u, 0u};
+          }
+#pragma unroll
+          for (int f = 0; f < RF; ++f) acc[f] = mfma32<DT>(m[f], z, acc[f]);
+        }
+      }
+      wait_vmcnt<0>();
+      wait_lgkm0();
+    }
+    __syncthreads();                                     // every wave is done with its ring
+#pragma unroll
+    for (int f = 0; f < RF; ++f) part[wave][f][lane] = acc[f];
+    __syncthreads();
+    if (wave < RF && sel && t < T) {
+      f32x4 sum = part[0][wave][lane];
+#pragma unroll
+      for (int w = 1; w < kShrinkWaves; ++w) sum += part[w][wave][lane];
+      const float sc = now ? now[a] : 1.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = r0 + wave * 16 + lq * 4 + e;
+        if (j < ((r + 7) & ~7)) put_shrunk(out, t, j, r, true, a, sum[e] * sc);
+      }
+    }
+    __syncthreads();                                     // part is read
   }
 }
 
 // Mt[a][j][c] = M[a][c][j] for M [n][C][r]: B's columns along the reduction of
 // the backward pass's shrink, and (with the roles of C and r exchanged) A's
-// ranks along that of its expand; one launch does both, the first tiles B's.
-// A workgroup takes 64 of the long and 32 of the short index.
+// ranks along that of its expand.  One launch prepares the backward pass: the
+// first tiles transpose B, the next A, the rest take xa apart.
 struct TransposeSide {
   const uint16_t* M;
   uint16_t* Mt;
@@ -143,8 +210,22 @@ struct TransposeSide {
   int tiles;            // workgroups
 };
 
-__global__ __launch_bounds__(256) void adapter_transpose_kernel(TransposeSide first, TransposeSide second) {
+struct PartsJob {
+  const float* V;
+  ShrunkOut out;
+  const int32_t* ids;
+  int n, T, r;
+};
+
+__global__ __launch_bounds__(256) void adapter_prepare_kernel(TransposeSide first, TransposeSide second,
+                                                              PartsJob parts) {
   __shared__ uint16_t tile[64][64 + 2];
+  const int third = int(blockIdx.x) - first.tiles - second.tiles;
+  if (third >= 0) {     // the parts of xa (one adapter index does them)
+    if (blockIdx.y == 0)
+      parts_of(parts.V, parts.out, parts.ids, parts.n, parts.T, parts.r, int64_t(third) * 256 + threadIdx.x);
+    return;
+  }
   const bool two = int(blockIdx.x) >= first.tiles;
   const TransposeSide& s = two ? second : first;
   const int b = blockIdx.x - (two ? first.tiles : 0), across = (s.cols + 63) / 64;
@@ -397,112 +478,67 @@ __global__ __launch_bounds__(kGradWaves * 64) void adapter_grad_kernel(GradArgs 
     }
     any |= count > 0;
   }
-  // waves 4..7 onto 0..3, 2..3 onto 0..1, 1 onto 0
+  // the waves' tiles into LDS; then each wave adds up, in wave order, and writes
+  // every 8th fragment
   f32x4 (*part)[RF * CF][64] = reinterpret_cast<f32x4 (*)[RF * CF][64]>(smem);
-  if (any) __syncthreads();               // every wave is done with its tile
-  for (int half = any ? kGradWaves / 2 : 0; half > 0; half >>= 1) {
-    if (wave >= half && wave < 2 * half) {
+  if (any) {
+    __syncthreads();                      // every wave is done with its staged tile
 #pragma unroll
-      for (int i = 0; i < RF; ++i)
+    for (int i = 0; i < RF; ++i)
 #pragma unroll
-        for (int j = 0; j < CF; ++j) part[wave - half][i * CF + j][lane] = acc[i][j];
-    }
-    __syncthreads();
-    if (wave < half) {
-#pragma unroll
-      for (int i = 0; i < RF; ++i)
-#pragma unroll
-        for (int j = 0; j < CF; ++j) acc[i][j] += part[wave][i * CF + j][lane];
-    }
+      for (int j = 0; j < CF; ++j) part[wave][i * CF + j][lane] = acc[i][j];
     __syncthreads();
   }
-  if (wave != 0) return;
   float* out = z.out + int64_t(a) * r * C;
+  for (int f = wave; f < RF * CF; f += kGradWaves) {
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    if (any) {
 #pragma unroll
-  for (int i = 0; i < RF; ++i)
-#pragma unroll
-    for (int j = 0; j < CF; ++j) {
-      const int c = c0 + j * 16 + li, q = r0 + i * 16 + lq * 4;
-      if (c >= C) continue;
-      if (rank_minor && (r & 3) == 0) {
-        if (q < r) *reinterpret_cast<f32x4*>(out + int64_t(c) * r + q) = acc[i][j];
-        continue;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (q + e < r) out[rank_minor ? int64_t(c) * r + q + e : int64_t(q + e) * C + c] = acc[i][j][e];
+      for (int w = 0; w < kGradWaves; ++w) sum += part[w][f][lane];
     }
+    const int i = f / CF, j = f - i * CF;
+    const int c = c0 + j * 16 + li, q = r0 + i * 16 + lq * 4;
+    if (c >= C) continue;
+    if (rank_minor && (r & 3) == 0) {
+      if (q < r) *reinterpret_cast<f32x4*>(out + int64_t(c) * r + q) = sum;
+      continue;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (q + e < r) out[rank_minor ? int64_t(c) * r + q + e : int64_t(q + e) * C + c] = sum[e];
+  }
 }
 
 // Up to this many tokens a wave computes one number of V: past it, a token's
 // row would be read by too many waves.
 constexpr int64_t kFewTokens = 16;
 
-using ShrinkTile32 = GemmTile<32, 64, 2, 2, 4>;   // ranks x tokens, 48 KB: three workgroups a CU
-using ShrinkTile64 = GemmTile<64, 64, 4, 1, 4>;
+int64_t round8(int64_t r) { return (r + 7) / 8 * 8; }
 
-// Splits of the shrink's columns and their width: enough workgroups to cover
-// the chip twice, shares of at least 256 columns.
-struct ShrinkPlan {
-  int64_t splits, csplit;
-};
-ShrinkPlan shrink_plan(int64_t T, int64_t C, int64_t r) {
-  if (C == 0) return {0, 64};   // an empty sum
-  const int64_t tiles = (T + 63) / 64 * (r <= 32 ? 1 : (r + 63) / 64);
-  const int64_t want = std::min<int64_t>(std::max<int64_t>(512 / tiles, 1), std::max<int64_t>(C / 256, 1));
-  const int64_t csplit = ((C + want - 1) / want + 63) / 64 * 64;
-  return {(C + csplit - 1) / csplit, csplit};
-}
-
-// Bytes of the shrink's shares (0: none are kept).
-size_t shrink_bytes(int64_t T, int64_t C, int64_t r) {
-  return T <= kFewTokens ? 0 : size_t(shrink_plan(T, C, r).splits) * size_t(T) * size_t(r) * 4;
-}
-
-template <int DT, class C>
-hipError_t launch_shrink(const ShrinkArgs& p, int64_t splits, hipStream_t s) {
-  auto kern = adapter_shrink_kernel<DT, C>;
-  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), C::LDS); e != hipSuccess) return e;
-  const int rank_tiles = (p.r + C::BM - 1) / C::BM;
-  // two adapters of a tile at a time, where there can be two
-  hipLaunchKernelGGL(kern, dim3(unsigned((p.T + 63) / 64 * rank_tiles), unsigned(splits), p.n > 1 ? 2u : 1u),
-                     dim3(C::THREADS), C::LDS, s, p, rank_tiles);
-  return hipGetLastError();
-}
-
-hipError_t join(const JoinJob& first, const JoinJob* second, const int32_t* ids, int64_t n, int64_t T, int64_t r,
-                int64_t ldt, hipStream_t s) {
-  hipLaunchKernelGGL(adapter_join_kernel, dim3(unsigned((T * ((r + 7) / 8 * 8) + 255) / 256), second ? 2u : 1u),
-                     dim3(256), 0, s, first, second ? *second : first, ids, int(n), int(T), int(r), int(ldt));
-  return hipGetLastError();
-}
-
-// now_a M Z as `out` wants it (out.V is written in any case; out.part and
-// out.splits are filled in here), and a second job along with it.
+// now_a M Z as `out` wants it (out.V is written in any case).
 template <int DT>
-hipError_t shrink(const int32_t* ids, int64_t n, const uint16_t* M, const uint16_t* Z, int64_t ldz, int64_t T, int64_t C,
-                  int64_t r, float* part, JoinJob out, const JoinJob* second, int64_t ldt, hipStream_t s) {
+hipError_t shrink(const int32_t* ids, int64_t n, const uint16_t* M, const float* now, const uint16_t* Z, int64_t ldz,
+                  int64_t T, int64_t C, int64_t r, const ShrunkOut& out, hipStream_t s) {
   if (T <= kFewTokens) {
     hipLaunchKernelGGL((adapter_dots_kernel<DT>), dim3(unsigned((T * r + 3) / 4)), dim3(256), 0, s, ids, int(n), M,
-                       out.now, Z, ldz, int(T), int(C), int(r), out.V);
+                       now, Z, ldz, int(T), int(C), int(r), out.V);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    if (!out.P && !out.PT && !second) return hipSuccess;
-    out.part = out.V;     // whole and scaled already
-    out.V = nullptr;
-    out.splits = 1;
-    out.now = nullptr;
-    return join(out, second, ids, n, T, r, ldt, s);
+    if (!out.P && !out.PT) return hipSuccess;
+    ShrunkOut rest = out;
+    rest.V = nullptr;
+    hipLaunchKernelGGL(adapter_parts_kernel, dim3(unsigned((T * round8(r) + 255) / 256)), dim3(256), 0, s, out.V, rest,
+                       ids, int(n), int(T), int(r));
+    return hipGetLastError();
   }
-  const ShrinkPlan pl = shrink_plan(T, C, r);
-  const ShrinkArgs p{ids, M, Z, ldz, int(n), int(T), int(C), int(r), int(pl.csplit), part};
-  if (n > 0 && pl.splits > 0) {
-    const hipError_t e =
-        r <= 32 ? launch_shrink<DT, ShrinkTile32>(p, pl.splits, s) : launch_shrink<DT, ShrinkTile64>(p, pl.splits, s);
-    if (e != hipSuccess) return e;
-  }
-  out.part = part;
-  out.splits = int(pl.splits);
-  return join(out, second, ids, n, T, r, ldt, s);
+  auto go = [&](auto kern, int rf, int lds) {
+    if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), lds); e != hipSuccess) return e;
+    // two adapters of a tile at a time, where there can be two
+    hipLaunchKernelGGL(kern, dim3(unsigned((T + 15) / 16), unsigned((r + rf * 16 - 1) / (rf * 16)), n > 1 ? 2u : 1u),
+                       dim3(kShrinkWaves * 64), lds, s, ids, int(n), M, now, Z, ldz, int(T), int(C), int(r), out);
+    return hipGetLastError();
+  };
+  return r <= 16 ? go(adapter_shrink_kernel<DT, 1>, 1, ShrinkRing<1>::LDS)
+                 : go(adapter_shrink_kernel<DT, 2>, 2, ShrinkRing<2>::LDS);
 }
 
 template <int DT>
@@ -520,7 +556,7 @@ template <int DT>
 hipError_t gradients(GradArgs g, int64_t n, hipStream_t s) {
   auto go = [&](auto kern, auto rfc, auto cfc) {
     constexpr int RF = decltype(rfc)::value, CF = decltype(cfc)::value;
-    constexpr int lds = std::max(kGradWaves * GradTile<CF>::BYTES, kGradWaves / 2 * RF * CF * 1024);
+    constexpr int lds = std::max(kGradWaves * GradTile<CF>::BYTES, kGradWaves * RF * CF * 1024);
     if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), lds); e != hipSuccess) return e;
     g.a.tiles = (g.a.C + CF * 16 - 1) / (CF * 16);
     g.b.tiles = (g.b.C + CF * 16 - 1) / (CF * 16);
@@ -548,7 +584,7 @@ bool fused_forward(const SpmmArgs& b) { return spmm_decode_applies(b) || spmm_ld
 
 // Parts of the workspaces, each on 256 bytes.
 size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
-size_t parts_bytes(int64_t T, int64_t r) { return padded(size_t(T) * 3 * ((r + 7) / 8 * 8) * 2); }
+size_t parts_bytes(int64_t T, int64_t r) { return padded(size_t(T) * 3 * round8(r) * 2); }
 
 template <int DT>
 hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
@@ -557,10 +593,8 @@ hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
   const bool few = spmm_decode_applies(a.base);
   char* ws = static_cast<char*>(a.workspace);
   uint16_t* P = few ? nullptr : reinterpret_cast<uint16_t*>(ws);
-  char* rest = ws + (few ? 0 : parts_bytes(T, a.r));   // the shares, and when they are joined the fp32 product
-  const JoinJob out{nullptr, 0, nullptr, a.scale, a.xa, P, nullptr};
-  hipError_t e = shrink<DT>(a.ids, a.n, a.A, a.base.act, a.base.ldx, T, a.base.K, a.r, reinterpret_cast<float*>(rest),
-                            out, nullptr, 0, s);
+  const ShrunkOut out{a.scale, a.xa, P, nullptr, 0};
+  hipError_t e = shrink<DT>(a.ids, a.n, a.A, nullptr, a.base.act, a.base.ldx, T, a.base.K, a.r, out, s);
   if (e != hipSuccess || a.base.R == 0) return e;
   LowRank p;
   p.ids = a.ids;
@@ -578,7 +612,7 @@ hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
     return few ? launch_spmm_decode(b, s) : launch_spmm_lds(b, s);
   }
   if (a.base.out_dtype != NM_F32) {
-    b.Y = rest;
+    b.Y = ws + parts_bytes(T, a.r);
     b.ldy = a.base.R;
     b.out_dtype = NM_F32;
   }
@@ -588,10 +622,10 @@ hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
 }
 
 // The backward pass's workspace: u, its parts, u's and s xa's parts along the
-// tokens, B and A transposed, the shares.
+// tokens, B and A transposed.
 struct BwdParts {
   int64_t ldt;
-  size_t u, p, ut, xt, bt, at, part, total;
+  size_t u, p, ut, xt, bt, at, total;
 };
 BwdParts bwd_parts(int64_t R, int64_t K, int64_t T, int64_t n, int64_t r) {
   BwdParts b;
@@ -602,8 +636,7 @@ BwdParts bwd_parts(int64_t R, int64_t K, int64_t T, int64_t n, int64_t r) {
   b.xt = b.ut + padded(size_t(b.ldt) * r * 6);
   b.bt = b.xt + padded(size_t(b.ldt) * r * 6);
   b.at = b.bt + padded(size_t(n) * r * R * 2);
-  b.part = b.at + padded(size_t(n) * r * K * 2);
-  b.total = b.part + shrink_bytes(T, R, r);
+  b.total = b.at + padded(size_t(n) * r * K * 2);
   return b;
 }
 
@@ -624,15 +657,12 @@ hipError_t backward_dt(const AdapterBwdArgs& a, hipStream_t s) {
       auto tiles = [](int64_t rows, int64_t cols) { return int((rows + 63) / 64 * ((cols + 63) / 64)); };
       const TransposeSide tb{a.B, bt, int(d.R), int(a.r), tiles(d.R, a.r)};
       const TransposeSide ta{a.A, at, int(a.r), int(d.K), d.out ? tiles(a.r, d.K) : 0};
-      if (tb.tiles + ta.tiles > 0)
-        hipLaunchKernelGGL(adapter_transpose_kernel, dim3(unsigned(tb.tiles + ta.tiles), unsigned(a.n)), dim3(256), 0,
-                           s, tb, ta);
+      const PartsJob xp{a.xa, ShrunkOut{a.scale, nullptr, nullptr, xt, int(w.ldt)}, a.ids, int(a.n), int(d.T), int(a.r)};
+      const int64_t blocks = tb.tiles + ta.tiles + (d.T * round8(a.r) + 255) / 256;
+      hipLaunchKernelGGL(adapter_prepare_kernel, dim3(unsigned(blocks), unsigned(a.n)), dim3(256), 0, s, tb, ta, xp);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    const JoinJob mine{nullptr, 0, a.scale, nullptr, u, P, ut};
-    const JoinJob other{a.xa, 1, a.scale, nullptr, nullptr, nullptr, xt};
-    e = shrink<DT>(a.ids, a.n, bt, d.G, d.ldg, d.T, d.R, a.r, reinterpret_cast<float*>(ws + w.part), mine, &other, w.ldt,
-                   s);
+    e = shrink<DT>(a.ids, a.n, bt, a.scale, d.G, d.ldg, d.T, d.R, a.r, ShrunkOut{nullptr, u, P, ut, int(w.ldt)}, s);
     if (e != hipSuccess) return e;
   }
   if (d.out && d.T > 0) {
@@ -660,7 +690,7 @@ hipError_t backward_dt(const AdapterBwdArgs& a, hipStream_t s) {
 size_t adapter_workspace(const SpmmArgs& base, int64_t r) {
   if (spmm_decode_applies(base)) return 0;
   const size_t y = base.out_dtype == NM_F32 || fused_forward(base) ? 0 : size_t(base.T) * size_t(base.R) * 4;
-  return parts_bytes(base.T, r) + std::max(shrink_bytes(base.T, base.K, r), y);
+  return parts_bytes(base.T, r) + y;
 }
 
 size_t adapter_bwd_workspace(int64_t R, int64_t K, int64_t T, int64_t n, int64_t r) {
