@@ -120,32 +120,65 @@ __device__ inline void load_v8(const float* row, int j0, int r, float (&v)[8]) {
 
 // sum[e] += s_a sum_j M_a[c + e][j] V[t][j] for 4 columns of one token, on the
 // vector ALUs: for few tokens, where every token has its own adapter and a
-// matrix-core fragment would hold one column of use.  Columns past C reread
-// column C - 1.
+// matrix-core fragment would hold one column of use.  The token's adapter is
+// loaded with the kernel's first loads, the first 16 ranks' operands while its
+// waves still join their partial sums (11008 x 4096, 16 tokens of rank 16, the
+// whole call: 19.2 us with all of it loaded at the end, 16.7 so).  Columns past
+// C reread column C - 1.
 template <int DT>
-__device__ inline void lowrank_columns4(const LowRank& p, int t, int c, f32x4& sum) {
-  const int a = p.ids[t];
-  if (uint32_t(a) >= uint32_t(p.n)) return;
-  const float s = p.scale ? p.scale[a] : 1.f;
-  const __amdgpu_buffer_rsrc_t rm = lowrank_rsrc(p, a);
-  const float* vrow = p.V + int64_t(t) * p.r;
-  f32x4 d = {0.f, 0.f, 0.f, 0.f};
-  for (int j = 0; j < p.r; j += 8) {
-    float v[8];
-    load_v8(vrow, j, p.r, v);
-    u32x4 m[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) m[e] = lowrank_operand(rm, min(c + e, p.C - 1), j, p.r);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        // past r both are zero
-        d[e] += half_to_f32<DT>((m[e][q >> 1] >> (16 * (q & 1))) & 0xFFFFu) * v[q];
+struct LowRankFew {
+  int a = -1;           // none
+  float s;
+  u32x4 m[2][4];
+  float v[2][8];
+
+  __device__ void adapter(const LowRank& p, int t) {
+    if (t < p.T) a = p.ids[t];
   }
+  __device__ void load8(const LowRank& p, int t, int c, int j, u32x4 (&mm)[4], float (&vv)[8]) const {
+    load_v8(p.V + int64_t(t) * p.r, j, p.r, vv);
+    const uint16_t* Ma = p.M + int64_t(a) * p.r * p.C;   // the lanes' adapters differ: plain addresses
 #pragma unroll
-  for (int e = 0; e < 4; ++e) sum[e] += s * d[e];
-}
+    for (int e = 0; e < 4; ++e) {
+      const uint16_t* row = Ma + int64_t(min(c + e, p.C - 1)) * p.r + j;
+      if ((p.r & 7) == 0) {
+        mm[e] = *reinterpret_cast<const u32x4*>(row);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          mm[e][q] = (j + 2 * q < p.r ? uint32_t(row[2 * q]) : 0u) |
+                     (j + 2 * q + 1 < p.r ? uint32_t(row[2 * q + 1]) << 16 : 0u);
+      }
+    }
+  }
+  __device__ void load(const LowRank& p, int t, int c) {
+    if (uint32_t(a) >= uint32_t(p.n)) {
+      a = -1;
+      return;
+    }
+    s = p.scale ? p.scale[a] : 1.f;
+    load8(p, t, c, 0, m[0], v[0]);
+    if (p.r > 8) load8(p, t, c, 8, m[1], v[1]);
+  }
+  __device__ void add(const LowRank& p, int t, int c, f32x4& sum) {
+    if (a < 0) return;
+    f32x4 d = {0.f, 0.f, 0.f, 0.f};
+    auto dot8 = [&](const u32x4 (&mm)[4], const float (&vv)[8]) {   // past r both are zero
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) d[e] += half_to_f32<DT>((mm[e][q >> 1] >> (16 * (q & 1))) & 0xFFFFu) * vv[q];
+    };
+    dot8(m[0], v[0]);
+    if (p.r > 8) dot8(m[1], v[1]);
+    for (int j = 16; j < p.r; j += 8) {
+      load8(p, t, c, j, m[0], v[0]);
+      dot8(m[0], v[0]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += s * d[e];
+  }
+};
 
 // The adapters of a tile of 16 NT tokens, a lane a token (tokens past T count
 // as the last); loaded early by the kernels that add the term late.

@@ -148,6 +148,11 @@ __global__ __launch_bounds__(kWaves * 64) void spmm_decode_kernel(
   const int R0 = blockIdx.x * (RB * 16);
   const int64_t S = int64_t(K) / pat_m(P) * pat_n(P);
   const int s0 = wave * SPW;  // first K step of this wave
+  constexpr bool kLowRank = std::is_same_v<LR, LowRank>;
+  [[maybe_unused]] LowRankFew<DT> few;
+  if constexpr (kLowRank) {
+    if (wave < RB) few.adapter(lowrank, li);
+  }
 
   AFrag af[SPW][RB];
   u32x8 bf[SPW];
@@ -173,6 +178,9 @@ __global__ __launch_bounds__(kWaves * 64) void spmm_decode_kernel(
   }
 #pragma unroll
   for (int i = 0; i < RB; ++i) part[wave][i][lane] = acc[i];
+  if constexpr (kLowRank) {
+    if (wave < RB) few.load(lowrank, li, R0 + wave * 16 + lq * 4);
+  }
   __syncthreads();
   // wave i < RB sums the 8 partials of fragment i in wave order
   if (wave < RB) {
@@ -182,7 +190,7 @@ __global__ __launch_bounds__(kWaves * 64) void spmm_decode_kernel(
     const int t = li;
     const int r = R0 + wave * 16 + lq * 4;
     if (t < T && r < R) {
-      if constexpr (std::is_same_v<LR, LowRank>) lowrank_columns4<DT>(lowrank, t, r, sum);
+      if constexpr (kLowRank) few.add(lowrank, t, r, sum);
       const bool vec_ok = (ldy & 3) == 0 && r + 3 < R;
       if constexpr (OUT == NM_F32) {
         float* y = static_cast<float*>(Y) + int64_t(t) * ldy + r;
@@ -232,6 +240,11 @@ __global__ __launch_bounds__(kWaves * 64) void spmm_decode_lds_kernel(
   const int nsteps = (K + 63) >> 6;
   unsigned char* vst = stage[wave];
   unsigned char* ist = stage[wave] + VBYTES;
+  constexpr bool kLowRank = std::is_same_v<LR, LowRank>;
+  [[maybe_unused]] LowRankFew<DT> few;
+  if constexpr (kLowRank) {
+    if (wave == 0) few.adapter(lowrank, li);
+  }
 
   // values: instruction j covers slots [j*64, j*64 + 64) = 64/CPR rows
 #pragma unroll
@@ -275,6 +288,9 @@ __global__ __launch_bounds__(kWaves * 64) void spmm_decode_lds_kernel(
     acc = smfmac<DT>(a, bf[u], acc, ix);
   }
   part[wave][lane] = acc;
+  if constexpr (kLowRank) {
+    if (wave == 0) few.load(lowrank, li, R0 + lq * 4);
+  }
   __syncthreads();
   if (wave == 0) {
     f32x4 sum = part[0][lane];
@@ -283,7 +299,7 @@ __global__ __launch_bounds__(kWaves * 64) void spmm_decode_lds_kernel(
     const int t = li;
     const int r = R0 + lq * 4;
     if (t < T && r < R) {
-      if constexpr (std::is_same_v<LR, LowRank>) lowrank_columns4<DT>(lowrank, t, r, sum);
+      if constexpr (kLowRank) few.add(lowrank, t, r, sum);
       const bool vec_ok = (ldy & 3) == 0 && r + 3 < R;
       if constexpr (OUT == NM_F32) {
         float* y = static_cast<float*>(Y) + int64_t(t) * ldy + r;
@@ -341,6 +357,13 @@ __global__ __launch_bounds__(kWaves * 64, 1) void spmm_decode_stream_kernel(
   const int row_end = min(R, row_begin + rows_per_wg);
   if (row_begin >= row_end) return;  // uniform over the workgroup
   constexpr int nblk = NBLK;
+  // (NBLK <= 8 blocks, at most one a wave to finish)
+  static_assert(NBLK <= kWaves, "a block a wave");
+  constexpr bool kLowRank = std::is_same_v<LR, LowRank>;
+  [[maybe_unused]] LowRankFew<DT> few;
+  if constexpr (kLowRank) {
+    if (wave < nblk) few.adapter(lowrank, li);
+  }
   const int S = K >> 1;
   const int irow_bytes = K >> 3;
   const int s0 = wave * SPW;
@@ -481,6 +504,9 @@ __global__ __launch_bounds__(kWaves * 64, 1) void spmm_decode_stream_kernel(
   __syncthreads();
 #pragma unroll
   for (int b = 0; b < NBLK; ++b) part[wave][b][lane] = acc[b];
+  if constexpr (kLowRank) {
+    if (wave < nblk) few.load(lowrank, li, row_begin + wave * 16 + lq * 4);
+  }
   __syncthreads();
   for (int b = wave; b < nblk; b += kWaves) {
     f32x4 sum = part[0][b][lane];
@@ -489,7 +515,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void spmm_decode_stream_kernel(
     const int t = li;
     const int r = row_begin + b * 16 + lq * 4;
     if (t < T && r < row_end) {
-      if constexpr (std::is_same_v<LR, LowRank>) lowrank_columns4<DT>(lowrank, t, r, sum);
+      if constexpr (kLowRank) few.add(lowrank, t, r, sum);
       const bool vec_ok = (ldy & 3) == 0 && r + 3 < row_end;
       if constexpr (OUT == NM_F32) {
         float* y = static_cast<float*>(Y) + int64_t(t) * ldy + r;
