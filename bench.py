@@ -88,11 +88,12 @@ CSRC = os.path.join(ROOT, "structured_sparse_gemm_nm_amd", "csrc")
 # header.  Counters taken on one family stay valid while only another changes.
 KERNEL_SOURCES = {
     "spmm": ["nm_spmm.hip", "nm_spmm_lds.hip", "nm_spmm_lds_nm.hip", "nm_spmm_decode.hip",
-             "nm_spmm_pipe.hip", "nm_spmm_resident.hip", "nm_permute.hip", "nm_int8.hip", "nm_lowrank.h"],
+             "nm_spmm_pipe.hip", "nm_spmm_resident.hip", "nm_permute.hip", "nm_int8.hip", "nm_lowrank.h",
+             "nm_widen.h"],
     "hybrid": ["nm_hybrid.hip", "nm_select.h"],
     "host": ["nm_hosts.hip"],
     "train": ["nm_train.hip", "nm_lowrank.h"],
-    "adapter": ["nm_adapter.hip", "nm_lowrank.h"],
+    "adapter": ["nm_adapter.hip", "nm_adapter_product.hip", "nm_lowrank.h", "nm_widen.h"],
     "layernorm": ["nm_layernorm.hip"],
     "xent": ["nm_xent.hip", "nm_gemm_nt.h"],
 }

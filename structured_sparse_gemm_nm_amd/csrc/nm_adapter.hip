@@ -288,12 +288,12 @@ __global__ __launch_bounds__(256) void adapter_dots_kernel(const int32_t* __rest
 }
 
 // ---------------------------------------------------------------------------
-// Expand: Y[t][c] = base[t][c] + (low-rank term), base fp32 (Y itself or a
-// workspace).  A wave takes 16 tokens x 64 columns.
+// Expand: Y[t][c] = sum of the base's shares, in order, + (low-rank term); the
+// base fp32 (Y itself or a workspace).  A wave takes 16 tokens x 64 columns.
 // ---------------------------------------------------------------------------
 template <int DT, int OUT>
-__global__ __launch_bounds__(256) void adapter_expand_kernel(LowRank p, const float* base, int64_t ldb, void* Y,
-                                                             int64_t ldy) {
+__global__ __launch_bounds__(256) void adapter_expand_kernel(LowRank p, const float* base, int64_t ldb, int splits,
+                                                             void* Y, int64_t ldy) {
   const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t0 = blockIdx.x * 16, c0 = blockIdx.y * 256 + wave * 64;
@@ -304,10 +304,12 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(LowRank p, const fl
     acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int c = c0 + 16 * f + 4 * lq;
     if (t >= p.T) continue;
-    const float* b = base + int64_t(t) * ldb + c;
-    if ((ldb & 3) == 0 && c + 3 < p.C) acc[f] = *reinterpret_cast<const f32x4*>(b);
-    else
-      for (int e = 0; e < 4 && c + e < p.C; ++e) acc[f][e] = b[e];
+    for (int z = 0; z < splits; ++z) {
+      const float* b = base + (int64_t(z) * p.T + t) * ldb + c;
+      if ((ldb & 3) == 0 && c + 3 < p.C) acc[f] += *reinterpret_cast<const f32x4*>(b);
+      else
+        for (int e = 0; e < 4 && c + e < p.C; ++e) acc[f][e] += b[e];
+    }
   }
   lowrank_add<DT, 4, 1>(p, lowrank_ids<1>(p, t0), t0, c0, [&](int f, int) -> f32x4& { return acc[f]; });
   if (t >= p.T) return;
@@ -543,13 +545,15 @@ hipError_t shrink(const int32_t* ids, int64_t n, const uint16_t* M, const float*
 }
 
 template <int DT>
-hipError_t expand(const LowRank& p, const float* base, int64_t ldb, void* Y, int64_t ldy, int out_dtype,
-                  hipStream_t s) {
+hipError_t expand(const LowRank& p, const float* base, int64_t ldb, int64_t splits, void* Y, int64_t ldy,
+                  int out_dtype, hipStream_t s) {
   const dim3 grid(unsigned((p.T + 15) / 16), unsigned((p.C + 255) / 256));
   if (out_dtype == NM_F32)
-    hipLaunchKernelGGL((adapter_expand_kernel<DT, NM_F32>), grid, dim3(256), 0, s, p, base, ldb, Y, ldy);
+    hipLaunchKernelGGL((adapter_expand_kernel<DT, NM_F32>), grid, dim3(256), 0, s, p, base, ldb,
+                       int(splits), Y, ldy);
   else
-    hipLaunchKernelGGL((adapter_expand_kernel<DT, DT>), grid, dim3(256), 0, s, p, base, ldb, Y, ldy);
+    hipLaunchKernelGGL((adapter_expand_kernel<DT, DT>), grid, dim3(256), 0, s, p, base, ldb,
+                       int(splits), Y, ldy);
   return hipGetLastError();
 }
 
@@ -579,9 +583,16 @@ hipError_t gradients(GradArgs g, int64_t n, hipStream_t s) {
   return go(adapter_grad_kernel<DT, 4, 4>, four{}, four{});
 }
 
-// Whether the shared product's kernel adds the low-rank term itself: the
-// few-token family (T <= 16) and the all-LDS family (prefill, 2:4).
-bool fused_forward(const SpmmArgs& b) { return spmm_decode_applies(b) || spmm_lds_applies(b); }
+// How the shared product is computed: by the few-token family (T <= 16) or the
+// all-LDS family (2:4 prefill), which add the low-rank term themselves; in
+// shares; or by whatever nm_spmm chooses, in fp32.  The last two leave the term
+// to the expand kernel.
+enum class Route { kFew, kPrefill, kShares, kPlain };
+Route route(const SpmmArgs& b) {
+  if (spmm_decode_applies(b)) return Route::kFew;
+  if (adapter_product_applies(b)) return Route::kShares;
+  return spmm_lds_applies(b) ? Route::kPrefill : Route::kPlain;
+}
 
 // Parts of the workspaces, each on 256 bytes.
 size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
@@ -590,8 +601,8 @@ size_t parts_bytes(int64_t T, int64_t r) { return padded(size_t(T) * 3 * round8(
 template <int DT>
 hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
   const int64_t T = a.base.T;
-  // the few-token family multiplies V itself
-  const bool few = spmm_decode_applies(a.base);
+  const Route way = route(a.base);
+  const bool few = way == Route::kFew;   // that family multiplies V itself
   char* ws = static_cast<char*>(a.workspace);
   uint16_t* P = few ? nullptr : reinterpret_cast<uint16_t*>(ws);
   const ShrunkOut out{a.scale, a.xa, P, nullptr, 0};
@@ -608,18 +619,27 @@ hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
   p.T = int(T);
   p.C = int(a.base.R);
   SpmmArgs b = a.base;
-  if (fused_forward(b)) {
+  if (few || way == Route::kPrefill) {
     b.lowrank = &p;
     return few ? launch_spmm_decode(b, s) : launch_spmm_lds(b, s);
   }
-  if (a.base.out_dtype != NM_F32) {
-    b.Y = ws + parts_bytes(T, a.r);
-    b.ldy = a.base.R;
+  float* base = reinterpret_cast<float*>(ws + parts_bytes(T, a.r));
+  int64_t ldb = a.base.R, splits = 1;
+  if (way == Route::kShares) {
+    splits = adapter_product_splits(b);
+    e = launch_adapter_product(b, base, s);
+  } else {
+    if (a.base.out_dtype == NM_F32) {
+      base = static_cast<float*>(a.base.Y);
+      ldb = a.base.ldy;
+    }
+    b.Y = base;
+    b.ldy = ldb;
     b.out_dtype = NM_F32;
+    e = launch_spmm(b, s);
   }
-  e = launch_spmm(b, s);
   if (e != hipSuccess) return e;
-  return expand<DT>(p, static_cast<const float*>(b.Y), b.ldy, a.base.Y, a.base.ldy, a.base.out_dtype, s);
+  return expand<DT>(p, base, ldb, splits, a.base.Y, a.base.ldy, a.base.out_dtype, s);
 }
 
 // The backward pass's workspace: u, its parts, u's and s xa's parts along the
@@ -689,9 +709,13 @@ hipError_t backward_dt(const AdapterBwdArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t adapter_workspace(const SpmmArgs& base, int64_t r) {
-  if (spmm_decode_applies(base)) return 0;
-  const size_t y = base.out_dtype == NM_F32 || fused_forward(base) ? 0 : size_t(base.T) * size_t(base.R) * 4;
-  return parts_bytes(base.T, r) + y;
+  const size_t y = size_t(base.T) * size_t(base.R) * 4;
+  switch (route(base)) {
+    case Route::kFew: return 0;
+    case Route::kPrefill: return parts_bytes(base.T, r);
+    case Route::kShares: return parts_bytes(base.T, r) + size_t(adapter_product_splits(base)) * y;
+    default: return parts_bytes(base.T, r) + (base.out_dtype == NM_F32 ? 0 : y);
+  }
 }
 
 size_t adapter_bwd_workspace(int64_t R, int64_t K, int64_t T, int64_t n, int64_t r) {

@@ -96,6 +96,7 @@ def test_adapter_workspace_sizes():
     fwd, bwd = nm.lib().nm_adapter_spmm_workspace_size, nm.lib().nm_adapter_spmm_bwd_workspace_size
     ref = ctypes.byref(b)
     assert fwd(64, 64, 2, 4, nm.NM_BF16, 40, 64, 3, 8, nm.NM_BF16, ref) == OK and b.value >= 40 * 64 * 4
+    assert fwd(64, 64, 2, 4, nm.NM_BF16, 40, 64, 3, 8, nm.NM_F32, ref) == OK and b.value >= 40 * 3 * 8 * 2
     assert fwd(64, 64, 2, 4, nm.NM_BF16, 9, 64, 3, 8, nm.NM_F32, ref) == OK and b.value == 0
     assert bwd(64, 64, 2, 4, nm.NM_BF16, 40, 3, 8, nm.NM_BF16, ref) == OK and b.value >= 40 * 8 * 4
     assert fwd(64, 64, 2, 4, nm.NM_BF16, 40, 64, 3, 8, nm.NM_F16, ref) == UNSUPPORTED

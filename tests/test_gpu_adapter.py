@@ -127,6 +127,28 @@ def test_patterns(n, m, T):
     c.check_backward()
 
 
+# the shared product in shares of K: one tile and several, a last step of 32,
+# more steps than waves, 16 tokens of a K past the few-token family; and shapes
+# of as few tokens whose K is too short to share out
+@pytest.mark.parametrize("R,K,T,n,m", [(33, 2080, 17, 2, 4), (32, 64, 20, 2, 4), (250, 96, 40, 2, 4),
+                                       (5, 8224, 16, 2, 4), (300, 4160, 33, 2, 4), (100, 1056, 65, 1, 4),
+                                       (301, 8192, 64, 1, 4), (48, 4128, 9, 1, 4), (250, 2112, 129, 1, 8),
+                                       (37, 6208, 16, 1, 8), (64, 128, 31, 1, 8)])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_product_in_shares(R, K, T, n, m, dt):
+    log(f"adapter shares R={R} K={K} T={T} {n}:{m} {dt}")
+    c = Case(R, K, T, 7, 3, dt, n, m)
+    c.check_forward()
+    # activations inside a wider buffer of NaN: nothing past K is used
+    d, _ = c.dev()
+    X = torch.full((T, K + 64), float("nan"), dtype=torch_dtype(dt), device="cuda")
+    X[:, :K] = d["act"]
+    y, _ = nm.nm_adapter_spmm(**d, K=K, n=n, m=m)
+    y2, _ = nm.nm_adapter_spmm(**dict(d, act=X[:, :K]), K=K, n=n, m=m)
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2)
+
+
 @pytest.mark.parametrize("R,K,T,r,na", [(64, 64, 1, 1, 1), (304, 224, 3, 5, 4), (136, 1056, 50, 17, 3),
                                         (520, 256, 333, 64, 5), (72, 96, 200, 100, 2), (256, 512, 129, 32, 1)])
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
