@@ -289,32 +289,43 @@ __global__ __launch_bounds__(256) void adapter_dots_kernel(const int32_t* __rest
 
 // ---------------------------------------------------------------------------
 // Expand: Y[t][c] = sum of the base's shares, in order, + (low-rank term); the
-// base fp32 (Y itself or a workspace).  A wave takes 16 tokens x 64 columns.
+// base fp32 (Y itself or a workspace).  A wave takes 16 tokens x F*16 columns.
 // ---------------------------------------------------------------------------
-template <int DT, int OUT>
+template <int DT, int OUT, int F>
 __global__ __launch_bounds__(256) void adapter_expand_kernel(LowRank p, const float* base, int64_t ldb, int splits,
                                                              void* Y, int64_t ldy) {
   const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int t0 = blockIdx.x * 16, c0 = blockIdx.y * 256 + wave * 64;
-  const int t = t0 + li;
-  f32x4 acc[4];
+  const int t0 = blockIdx.x * 16, c0 = (blockIdx.y * 4 + wave) * (F * 16);
+  if (c0 >= p.C) return;
+  const int t = t0 + li, tr = min(t, p.T - 1);
+  const int id = lowrank_ids<1>(p, t0);
+  f32x4 acc[F];
 #pragma unroll
-  for (int f = 0; f < 4; ++f) {
-    acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int c = c0 + 16 * f + 4 * lq;
-    if (t >= p.T) continue;
+  for (int f = 0; f < F; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if ((ldb & 3) == 0) {
+    // rows on 16 bytes: pieces that start before C end before ldb
+#pragma unroll 4
     for (int z = 0; z < splits; ++z) {
-      const float* b = base + (int64_t(z) * p.T + t) * ldb + c;
-      if ((ldb & 3) == 0 && c + 3 < p.C) acc[f] += *reinterpret_cast<const f32x4*>(b);
-      else
-        for (int e = 0; e < 4 && c + e < p.C; ++e) acc[f][e] += b[e];
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const int c = min(c0 + 16 * f + 4 * lq, (p.C - 1) & ~3);
+        acc[f] += *reinterpret_cast<const f32x4*>(base + (int64_t(z) * p.T + tr) * ldb + c);
+      }
+    }
+  } else {
+    for (int z = 0; z < splits; ++z) {
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[f][e] += base[(int64_t(z) * p.T + tr) * ldb + min(c0 + 16 * f + 4 * lq + e, p.C - 1)];
     }
   }
-  lowrank_add<DT, 4, 1>(p, lowrank_ids<1>(p, t0), t0, c0, [&](int f, int) -> f32x4& { return acc[f]; });
+  lowrank_add<DT, F, 1>(p, id, t0, c0, [&](int f, int) -> f32x4& { return acc[f]; });
   if (t >= p.T) return;
 #pragma unroll
-  for (int f = 0; f < 4; ++f) {
+  for (int f = 0; f < F; ++f) {
     const int c = c0 + 16 * f + 4 * lq;
     if constexpr (OUT == NM_F32) {
       float* y = static_cast<float*>(Y) + int64_t(t) * ldy + c;
@@ -547,14 +558,16 @@ hipError_t shrink(const int32_t* ids, int64_t n, const uint16_t* M, const float*
 template <int DT>
 hipError_t expand(const LowRank& p, const float* base, int64_t ldb, int64_t splits, void* Y, int64_t ldy,
                   int out_dtype, hipStream_t s) {
-  const dim3 grid(unsigned((p.T + 15) / 16), unsigned((p.C + 255) / 256));
+  auto go = [&](auto kern, int f) {
+    hipLaunchKernelGGL(kern, dim3(unsigned((p.T + 15) / 16), unsigned((p.C + f * 64 - 1) / (f * 64))), dim3(256), 0, s,
+                       p, base, ldb, int(splits), Y, ldy);
+    return hipGetLastError();
+  };
+  // 64 columns a wave where that still covers the chip, else 16
+  const bool wide = (int64_t(p.T) + 15) / 16 * ((p.C + 255) / 256) >= 256;
   if (out_dtype == NM_F32)
-    hipLaunchKernelGGL((adapter_expand_kernel<DT, NM_F32>), grid, dim3(256), 0, s, p, base, ldb,
-                       int(splits), Y, ldy);
-  else
-    hipLaunchKernelGGL((adapter_expand_kernel<DT, DT>), grid, dim3(256), 0, s, p, base, ldb,
-                       int(splits), Y, ldy);
-  return hipGetLastError();
+    return wide ? go(adapter_expand_kernel<DT, NM_F32, 4>, 4) : go(adapter_expand_kernel<DT, NM_F32, 1>, 1);
+  return wide ? go(adapter_expand_kernel<DT, DT, 4>, 4) : go(adapter_expand_kernel<DT, DT, 1>, 1);
 }
 
 template <int DT>
@@ -627,6 +640,7 @@ hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
   int64_t ldb = a.base.R, splits = 1;
   if (way == Route::kShares) {
     splits = adapter_product_splits(b);
+    ldb = adapter_product_ld(b);
     e = launch_adapter_product(b, base, s);
   } else {
     if (a.base.out_dtype == NM_F32) {
@@ -713,7 +727,8 @@ size_t adapter_workspace(const SpmmArgs& base, int64_t r) {
   switch (route(base)) {
     case Route::kFew: return 0;
     case Route::kPrefill: return parts_bytes(base.T, r);
-    case Route::kShares: return parts_bytes(base.T, r) + size_t(adapter_product_splits(base)) * y;
+    case Route::kShares:
+      return parts_bytes(base.T, r) + size_t(adapter_product_splits(base)) * size_t(base.T) * adapter_product_ld(base) * 4;
     default: return parts_bytes(base.T, r) + (base.out_dtype == NM_F32 ? 0 : y);
   }
 }

