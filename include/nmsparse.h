@@ -85,7 +85,9 @@ typedef enum { NM_F16 = 0, NM_BF16 = 1, NM_F32 = 2, NM_I8 = 3, NM_I32 = 4, NM_FP
  * per-call nm_spmm_variant and gives nm_spmm_perm a caller-owned workspace in
  * place of memory the library allocated; 201 adds the hybrid tiles
  * (nm_hybrid_*), the training products (nm_spmm_dx, nm_spmm_dw) and the
- * block / diagonal structures (nm_block_*, nm_diag_*). */
+ * block / diagonal structures (nm_block_*, nm_diag_*).  Layer norm, the adapters
+ * and cross entropy (nm_layernorm*, nm_adapter_*, nm_xent*) only add entry
+ * points and came under 201. */
 int nm_version(void);
 
 /* Short fixed text for a status code (never NULL). */

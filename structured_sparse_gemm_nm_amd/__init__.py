@@ -7,7 +7,8 @@ and the current HIP stream.  There is no CPU fallback: if the library is
 missing every call raises.
 
 Function names follow the C ABI: nm_compress, nm_decompress, nm_spmm,
-nm_spmm_perm, nm_packed_sizes.
+nm_spmm_perm, nm_packed_sizes, and so on to the operators beside a projection:
+nm_layernorm, nm_adapter_spmm, nm_xent and their _bwd.
 """
 from __future__ import annotations
 
