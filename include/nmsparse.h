@@ -468,7 +468,9 @@ nm_status nm_layernorm_bwd(const void* dy, int64_t ldg, const void* x, int64_t l
  *              overwritten: an adapter without tokens gets zeros.
  *   workspace  device, the bytes of the matching _workspace_size, 16-byte aligned.
  * xa and u stay fp32; between the two low-rank products they enter the matrix
- * cores as three bf16 parts, which hold their 24 bits.  Inf or NaN in one token or adapter reaches the outputs of that token or adapter only.
+ * cores as three bf16 parts, which hold their 24 bits.  Inf or NaN in one token
+ * or adapter reaches the outputs of that token or adapter only (there an Inf may
+ * turn to NaN: it meets the parts that are zero).
  * T <= 2^24, R and K <= 2^22.  Pointers 16-byte aligned (adapter, scale: 4),
  * ldx and ldg multiples of 8 below 2^24; outputs and workspace must not overlap anything
  * (NM_ERR_ALIAS).  Stream-ordered; nothing is allocated or synchronised.
