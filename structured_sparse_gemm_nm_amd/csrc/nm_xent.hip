@@ -224,20 +224,23 @@ __global__ __launch_bounds__(256) void xent_transpose_kernel(const uint16_t* __r
   }
 }
 
-// The largest |dloss| of a counted token.
+// The larger of two magnitudes, NaN if either is (fmaxf drops a NaN, and dW with it).
+__device__ inline float larger(float a, float b) { return a >= b || a != a ? a : b; }
+
+// The largest |dloss| of a counted token; NaN if one holds NaN, so that dW does.
 __global__ __launch_bounds__(1024) void xent_largest_kernel(const float* __restrict__ dloss,
                                                             const int32_t* __restrict__ labels, int T, int V,
                                                             float* __restrict__ largest) {
   __shared__ float red[16];
   float m = 0.f;
   for (int t = threadIdx.x; t < T; t += 1024)
-    if (uint32_t(labels[t]) < uint32_t(V)) m = fmaxf(m, fabsf(dloss[t]));
+    if (uint32_t(labels[t]) < uint32_t(V)) m = larger(m, fabsf(dloss[t]));
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  for (int o = 32; o > 0; o >>= 1) m = larger(m, __shfl_xor(m, o));
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
   __syncthreads();
   if (threadIdx.x != 0) return;
-  for (int w = 1; w < 16; ++w) m = fmaxf(m, red[w]);
+  for (int w = 1; w < 16; ++w) m = larger(m, red[w]);
   *largest = m;
 }
 
@@ -508,9 +511,10 @@ __global__ __launch_bounds__(256) void xent_finish_kernel(const float* __restric
     f32x4 v = *reinterpret_cast<const f32x4*>(acc + i);
     for (int z = 1; z < splits; ++z) v += *reinterpret_cast<const f32x4*>(acc + z * all + i);
     const int64_t t = i / H, h = i - t * H;
-    const float g = uint32_t(labels[t]) < uint32_t(V) ? dloss[t] : 0.f;
+    const bool counted = uint32_t(labels[t]) < uint32_t(V);
+    const float g = counted ? dloss[t] : 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] *= g;
+    for (int e = 0; e < 4; ++e) v[e] = counted ? v[e] * g : 0.f;   // by selection: W may hold Inf or NaN
     if constexpr (OUT == NM_F32) {
       *reinterpret_cast<f32x4*>(static_cast<float*>(out) + t * ldo + h) = v;
     } else {

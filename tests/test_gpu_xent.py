@@ -218,6 +218,45 @@ def test_f16_gradients_of_any_size(scale):
     assert torch.equal(a2, a * scale) and torch.equal(b2, b * scale) and not zx.any() and not zw.any()
 
 
+@pytest.mark.parametrize("which", ["one", "all"])
+def test_nan_in_dloss_is_not_lost(which):
+    # a NaN upstream gradient of a counted token reaches its dx and every entry of dW,
+    # also where it is the only kind of gradient there is
+    log(f"xent nan dloss {which}")
+    T, V, H = 40, 300, 64
+    x, w, labels, g = inputs(T, V, H, "bf16")
+    labels[:2] = 5, -100
+    if which == "one":
+        g[0] = np.nan
+    else:
+        g[:] = np.nan
+    X, W = to_dev(x, "bf16"), to_dev(w, "bf16")
+    lab, gd = torch.from_numpy(labels).cuda(), torch.from_numpy(g).cuda()
+    _, lse = nm.nm_xent(X, W, lab)
+    dx, dw = nm.nm_xent_bwd(X, W, lab, lse, gd)
+    torch.cuda.synchronize()
+    bad = torch.from_numpy(np.isnan(g) & (labels >= 0)).cuda()
+    assert dw.isnan().all() and dx[bad].isnan().all()
+    assert dx[~bad].isfinite().all() and not dx[1].any()
+
+
+def test_ignored_token_has_no_gradient_whatever_the_head_holds():
+    # an Inf or NaN in a word's row: the counted tokens' gradients are lost, an ignored
+    # token's stays zero
+    log("xent ignored token, bad word")
+    for T in (40, 200):
+        V, H = 300, 64
+        x, w, labels, g = inputs(T, V, H, "bf16")
+        labels[3] = -100
+        X, W = to_dev(x, "bf16"), to_dev(w, "bf16")
+        W[7, 5], W[290, 9] = float("nan"), float("inf")
+        lab, gd = torch.from_numpy(labels).cuda(), torch.from_numpy(g).cuda()
+        loss, lse = nm.nm_xent(X, W, lab)
+        dx, _ = nm.nm_xent_bwd(X, W, lab, lse, gd)
+        torch.cuda.synchronize()
+        assert not dx[lab < 0].any() and not loss[lab < 0].any()
+
+
 def test_gradient_against_differences():
     # L = sum g loss along a random direction of x, by central differences with
     # steps exact in fp16: 2 sum |g| (bound on loss) / 2h of rounding, and h^2 / 6 of
