@@ -12,7 +12,8 @@
 // (activations in whole 128-byte lines, packed values, index words), without a
 // barrier until the waves' tiles are added in wave order.
 // (4096 x 4096, 64 tokens, 2:4 bf16: 11.7 us, the register-prefetch kernel 37;
-// 4096 x 11008, 16 tokens: 13, the generic kernel 92.)
+// 4096 x 11008, 16 tokens: 13, the generic kernel 92.  The whole call for 261
+// tokens, 531 x 2848 1:8: 35 us, with the generic kernel 90.)
 // Operand layouts and the 1:4 / 1:8 widening are those of nm_spmm.hip.
 #include "nm_internal.h"
 #include "nm_widen.h"
@@ -27,8 +28,8 @@ constexpr int kWaves = 4, kRows = 32, kNS = 3;
 template <int P, int TB>
 struct Stage {
   static constexpr int ACT = TB * 2048;                 // [TB*16 tokens][128 bytes]
-  static constexpr int VLOADS = P == 0 ? 2 : 1;
-  static constexpr int VAL = VLOADS * 1024;             // [32 rows][64, 32 or 16 bytes]
+  static constexpr int VLOADS = P == 1 ? 1 : 2;
+  static constexpr int VAL = P == 2 ? 512 : VLOADS * 1024;   // [32 rows][64, 32 or 16 bytes]
   static constexpr int BYTES = ACT + VAL + 256;         // + index words, 8 (1:4: 4) bytes a row
   static constexpr int LOADS = TB * 2 + VLOADS + 1;
   static constexpr int RING = kWaves * kNS * BYTES;
@@ -51,7 +52,7 @@ __global__ __launch_bounds__(kWaves * 64) void adapter_product_kernel(const uint
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int R0 = blockIdx.x * kRows, T0 = blockIdx.y * (TB * 16);
   const int S = K / pat_m(P) * pat_n(P);
-  const int steps = (K + 63) >> 6, rem = K - (steps - 1) * 64;   // 64, or 32 (2:4 and 1:4)
+  const int steps = (K + 63) >> 6, rem = K - (steps - 1) * 64;   // 64 or 32
   const int first = blockIdx.z * kWaves + wave, stride = gridDim.z * kWaves;
   const int count = first < steps ? (steps - 1 - first) / stride + 1 : 0;
 
@@ -65,14 +66,16 @@ __global__ __launch_bounds__(kWaves * 64) void adapter_product_kernel(const uint
   for (int j = 0; j < TB * 2; ++j)
     aoff[j] = uint32_t(min(j * 8 + (lane >> 3), T - 1 - T0)) * uint32_t(ldx) * 2u + chunk * 16u;
   // values: 2:4 slot (row, quarter) at row*4 + (q ^ ((row >> 1) & 3)); 1:4 two
-  // 16-byte pieces a row, 1:8 one (the upper lanes repeat the lower ones)
+  // 16-byte pieces a row; 1:8 four of 4 bytes (its rows lie on 8 bytes where K is
+  // an odd multiple of 32, and a short last step holds half of 16)
+  constexpr uint32_t vbytes = P == 2 ? 4u : 16u;
   uint32_t voff[St::VLOADS], vpiece[St::VLOADS];
 #pragma unroll
   for (int j = 0; j < St::VLOADS; ++j) {
     const int slot = j * 64 + lane;
-    const int row = P == 0 ? slot >> 2 : P == 1 ? slot >> 1 : slot & 31;
-    vpiece[j] = P == 0 ? uint32_t((slot & 3) ^ ((row >> 1) & 3)) : P == 1 ? uint32_t(slot & 1) : 0u;
-    voff[j] = uint32_t(min(row, R - 1 - R0)) * uint32_t(S) * 2u + vpiece[j] * 16u;
+    const int row = P == 1 ? slot >> 1 : slot >> 2;
+    vpiece[j] = P == 0 ? uint32_t((slot & 3) ^ ((row >> 1) & 3)) : uint32_t(slot & (P == 1 ? 1 : 3));
+    voff[j] = uint32_t(min(row, R - 1 - R0)) * uint32_t(S) * 2u + vpiece[j] * vbytes;
   }
   // index words: 2:4 and 1:8 two a row, 1:4 one (repeated)
   const int irow = P == 1 ? lane & 31 : lane >> 1;
@@ -90,11 +93,12 @@ __global__ __launch_bounds__(kWaves * 64) void adapter_product_kernel(const uint
 #pragma unroll
     for (int j = 0; j < TB * 2; ++j) dma16(ra, aoff[j] - back, uint32_t(s) * 128u, st + j * 1024);
     constexpr uint32_t vstep = P == 0 ? 64u : P == 1 ? 32u : 16u;
-    constexpr int vk = P == 0 ? 16 : P == 1 ? 32 : 64;     // K positions of a 16-byte piece
+    constexpr int vk = P == 1 ? 32 : 16;     // K positions of a piece
 #pragma unroll
     for (int j = 0; j < St::VLOADS; ++j) {
-      const uint32_t vback = tail && int(vpiece[j]) * vk >= rem ? vpiece[j] * 16u : 0u;
-      dma16(rv, voff[j] - vback, uint32_t(s) * vstep, st + St::ACT + j * 1024);
+      const uint32_t vback = tail && int(vpiece[j]) * vk >= rem ? vpiece[j] * vbytes : 0u;
+      if constexpr (P == 2) dma4(rv, voff[j] - vback + uint32_t(s) * vstep, st + St::ACT + j * 256);
+      else dma16(rv, voff[j] - vback, uint32_t(s) * vstep, st + St::ACT + j * 1024);
     }
     const int word = P == 0 ? 2 * s + (lane & 1) : P == 1 ? s : ((24 * s) >> 5) + (lane & 1);
     dma4(ri, ioff + uint32_t(min(word, words - 1)) * 4u, st + St::ACT + St::VAL);
@@ -220,13 +224,13 @@ int64_t adapter_product_splits(const SpmmArgs& a) {
   return std::max<int64_t>(std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), steps / (4 * kWaves)), 1);
 }
 
-// Shapes it takes (a short last step leaves whole 16-byte pieces of values: K a
-// multiple of 32, of 64 for 1:8; grid limits), and among them those where it is
+// Shapes it takes (a short last step leaves whole pieces of values: K a multiple
+// of 32; grid limits), and among them those where it is
 // the fastest: a K of at least 16 steps (shorter ones leave nothing to share
 // out) and prefill tiles, 256 x 128 (1:4 and 1:8: 128 x 64), that cover less
 // than a quarter (a half) of the chip.
 bool adapter_product_applies(const SpmmArgs& a) {
-  if (a.R < 1 || a.T < 1 || a.K < 1024 || a.K % (a.m == 8 ? 64 : 32) != 0 || a.T > (int64_t(1) << 20)) return false;
+  if (a.R < 1 || a.T < 1 || a.K < 1024 || a.K % 32 != 0 || a.T > (int64_t(1) << 20)) return false;
   const int64_t wide = (a.R + 255) / 256 * ((a.T + 127) / 128), narrow = (a.R + 127) / 128 * ((a.T + 63) / 64);
   if (spmm_lds_applies(a)) return wide < 64;
   if (spmm_lds_nm_applies(a)) return narrow < 128;

@@ -148,6 +148,13 @@ def test_product_in_shares(R, K, T, n, m, dt):
     torch.cuda.synchronize()
     assert torch.equal(y, y2)
 
+# 1:8 with K an odd multiple of 32: rows of values on 8 bytes, a last step of 4 values
+@pytest.mark.parametrize("R,K,T", [(33, 1056, 17), (531, 2848, 261), (100, 4128, 9), (32, 1120, 64)])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_product_in_shares_of_short_rows(R, K, T, dt):
+    log(f"adapter shares R={R} K={K} T={T} 1:8 {dt}")
+    Case(R, K, T, 12, 3, dt, 1, 8).check_forward()
+
 
 @pytest.mark.parametrize("R,K,T,r,na", [(64, 64, 1, 1, 1), (304, 224, 3, 5, 4), (136, 1056, 50, 17, 3),
                                         (520, 256, 333, 64, 5), (72, 96, 200, 100, 2), (256, 512, 129, 32, 1)])
