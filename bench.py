@@ -93,7 +93,7 @@ KERNEL_SOURCES = {
     "hybrid": ["nm_hybrid.hip", "nm_select.h"],
     "host": ["nm_hosts.hip"],
     "train": ["nm_train.hip", "nm_lowrank.h"],
-    "adapter": ["nm_adapter.hip", "nm_adapter_product.hip", "nm_lowrank.h", "nm_widen.h"],
+    "adapter": ["nm_adapter.hip", "nm_adapter_product.hip", "nm_lowrank.h", "nm_piece.h", "nm_widen.h"],
     "layernorm": ["nm_layernorm.hip"],
     "xent": ["nm_xent.hip", "nm_gemm_nt.h"],
 }

@@ -22,6 +22,7 @@
 // adds the term there (few tokens, 2:4 prefill, and dx).
 #include "nm_internal.h"
 #include "nm_lowrank.h"
+#include "nm_piece.h"
 
 #include <algorithm>
 #include <type_traits>
@@ -289,11 +290,12 @@ __global__ __launch_bounds__(256) void adapter_dots_kernel(const int32_t* __rest
 
 // ---------------------------------------------------------------------------
 // Expand: Y[t][c] = sum of the base's shares, in order, + (low-rank term); the
-// base fp32 (Y itself or a workspace).  A wave takes 16 tokens x F*16 columns.
+// base fp32 (Y itself or a workspace).  A wave takes 16 tokens x F*16 columns;
+// `readable` columns of a row of the base may be read.
 // ---------------------------------------------------------------------------
 template <int DT, int OUT, int F>
-__global__ __launch_bounds__(256) void adapter_expand_kernel(LowRank p, const float* base, int64_t ldb, int splits,
-                                                             void* Y, int64_t ldy) {
+__global__ __launch_bounds__(256) void adapter_expand_kernel(LowRank p, const float* base, int64_t ldb,
+                                                             int64_t readable, int splits, void* Y, int64_t ldy) {
   const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t0 = blockIdx.x * 16, c0 = (blockIdx.y * 4 + wave) * (F * 16);
@@ -303,13 +305,12 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(LowRank p, const fl
   f32x4 acc[F];
 #pragma unroll
   for (int f = 0; f < F; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if ((ldb & 3) == 0) {
-    // rows on 16 bytes: pieces that start before C end before ldb
+  if (whole_pieces(c0, F * 16, p.C, ldb, readable)) {
 #pragma unroll 4
     for (int z = 0; z < splits; ++z) {
 #pragma unroll
       for (int f = 0; f < F; ++f) {
-        const int c = min(c0 + 16 * f + 4 * lq, (p.C - 1) & ~3);
+        const int c = piece_start(c0 + 16 * f + 4 * lq, p.C);
         acc[f] += *reinterpret_cast<const f32x4*>(base + (int64_t(z) * p.T + tr) * ldb + c);
       }
     }
@@ -556,11 +557,11 @@ hipError_t shrink(const int32_t* ids, int64_t n, const uint16_t* M, const float*
 }
 
 template <int DT>
-hipError_t expand(const LowRank& p, const float* base, int64_t ldb, int64_t splits, void* Y, int64_t ldy,
-                  int out_dtype, hipStream_t s) {
+hipError_t expand(const LowRank& p, const float* base, int64_t ldb, int64_t readable, int64_t splits, void* Y,
+                  int64_t ldy, int out_dtype, hipStream_t s) {
   auto go = [&](auto kern, int f) {
     hipLaunchKernelGGL(kern, dim3(unsigned((p.T + 15) / 16), unsigned((p.C + f * 64 - 1) / (f * 64))), dim3(256), 0, s,
-                       p, base, ldb, int(splits), Y, ldy);
+                       p, base, ldb, readable, int(splits), Y, ldy);
     return hipGetLastError();
   };
   // 64 columns a wave where that still covers the chip, else 16
@@ -637,10 +638,10 @@ hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
     return few ? launch_spmm_decode(b, s) : launch_spmm_lds(b, s);
   }
   float* base = reinterpret_cast<float*>(ws + parts_bytes(T, a.r));
-  int64_t ldb = a.base.R, splits = 1;
+  int64_t ldb = a.base.R, readable = ldb, splits = 1;   // in Y's last row nothing follows column R
   if (way == Route::kShares) {
     splits = adapter_product_splits(b);
-    ldb = adapter_product_ld(b);
+    ldb = readable = adapter_product_ld(b);
     e = launch_adapter_product(b, base, s);
   } else {
     if (a.base.out_dtype == NM_F32) {
@@ -653,7 +654,7 @@ hipError_t forward_dt(const AdapterArgs& a, hipStream_t s) {
     e = launch_spmm(b, s);
   }
   if (e != hipSuccess) return e;
-  return expand<DT>(p, base, ldb, splits, a.base.Y, a.base.ldy, a.base.out_dtype, s);
+  return expand<DT>(p, base, ldb, readable, splits, a.base.Y, a.base.ldy, a.base.out_dtype, s);
 }
 
 // The backward pass's workspace: u, its parts, u's and s xa's parts along the
