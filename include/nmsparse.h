@@ -509,9 +509,10 @@ nm_status nm_adapter_spmm_bwd(const void* values, const uint32_t* idx, int64_t R
  *              pass: for the same choice of dx and dw), 16-byte aligned.
  * Logits, statistics and sums are fp32.  The backward pass walks the vocabulary
  * in pieces and computes the logits again; softmax - onehot (for dw: times dloss
- * over its largest magnitude) is rounded to the inputs' 16-bit type before its
- * two products, relative 2^-8 in bf16, 2^-11 in fp16 an element; dloss itself
- * multiplies the fp32 results.
+ * over its largest magnitude) enters its two products in the inputs' 16-bit type:
+ * rounded once for a 16-bit dx or dw (relative 2^-8 in bf16, 2^-11 in fp16 an
+ * element), in two parts that add up to it to 2^-16 or 2^-22 for an fp32 one,
+ * which costs that product twice.  dloss itself multiplies the fp32 results.
  * T <= 2^22, V <= 2^24, H <= 2^20.  Matrices and workspace 16-byte aligned, vectors 4;
  * outputs and workspace must not overlap anything (NM_ERR_ALIAS).
  * Stream-ordered; nothing is allocated or synchronised.

@@ -868,7 +868,8 @@ def nm_xent(x, w, labels, ignore_index: int = -100):
 def nm_xent_bwd(x, w, labels, lse, dloss, ignore_index: int = -100, out_dtype=None, need_dx: bool = True,
                 need_dw: bool = True):
     """(dx [T, H], dw [V, H]) of nm_xent from dloss = dL/dloss (float32 [T]) and the lse it returned;
-    float32 unless out_dtype names the dtype of x.  need_dx / need_dw False leave one out (None)."""
+    float32 unless out_dtype names the dtype of x (float32 keeps softmax - onehot in two 16-bit parts,
+    and takes each product twice).  need_dx / need_dw False leave one out (None)."""
     torch = _torch()
     T, V, H, dt = _check_xent(x, w, labels, ignore_index)
     _vector(lse, "lse", T, torch.float32, x.device)

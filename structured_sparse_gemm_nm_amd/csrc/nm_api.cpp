@@ -1209,7 +1209,7 @@ nm_status nm_xent_bwd_workspace_size(int64_t T, int64_t V, int64_t H, int dtype,
   nm_status st = check_xent(T, V, H, dtype);
   if (st != NM_OK) return st;
   if (!bytes) return fail(NM_ERR_NULL, "bytes must be non-NULL");
-  *bytes = nm::xent_bwd_workspace(T, V, H, need_dx != 0, need_dw != 0);
+  *bytes = nm::xent_bwd_workspace(T, V, H, need_dx ? 2 : 0, need_dw ? 2 : 0);   // enough for either type
   return ok();
 }
 
@@ -1232,7 +1232,7 @@ nm_status nm_xent_bwd(const void* x, int64_t T, int64_t H, int64_t ldx, const vo
   if (!aligned16(x) || !aligned16(w) || !aligned16(dx) || !aligned16(dw) || !aligned16(workspace) ||
       !aligned_to(labels, 4) || !aligned_to(lse, 4) || !aligned_to(dloss, 4))
     return fail(NM_ERR_ALIGN, "matrices and workspace must be 16-byte aligned, vectors 4-byte");
-  const size_t need = nm::xent_bwd_workspace(T, V, H, dx != nullptr, dw != nullptr);
+  const size_t need = nm::xent_bwd_workspace(T, V, H, dx ? 1 + (dx_dtype == NM_F32) : 0, dw ? 1 + (dw_dtype == NM_F32) : 0);
   if (workspace_bytes < need)
     return fail(NM_ERR_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
   const size_t tb = size_t(T) * 4;

@@ -231,7 +231,8 @@ struct XentArgs {
 };
 constexpr int64_t kXentMaxTokens = int64_t(1) << 22, kXentMaxVocab = int64_t(1) << 24, kXentMaxH = int64_t(1) << 20;
 size_t xent_workspace(int64_t T, int64_t V);
-size_t xent_bwd_workspace(int64_t T, int64_t V, int64_t H, bool dx, bool dw);
+// dx, dw: 0 not wanted, 1 in the inputs' type, 2 in fp32.
+size_t xent_bwd_workspace(int64_t T, int64_t V, int64_t H, int dx, int dw);
 hipError_t launch_xent(const XentArgs& a, hipStream_t s);
 hipError_t launch_xent_bwd(const XentArgs& a, hipStream_t s);
 

@@ -20,6 +20,12 @@
 // q itself; g q rounded as a whole would give every label's entry, all near -g,
 // the same rounding error (4e-3 of dW measured, against 2e-3 now).  fp16 holds
 // the operands times 2^14, so that probabilities down to 2^-38 are not flushed.
+// An output of 16 bits takes the operand rounded once (its own rounding is as
+// large: 2048 x 32000 x 4096 bf16, dx and dW 1.667e-3 from the exact ones, 1.662e-3
+// with fp32 operands).  An fp32 output would show it (1.3e-4 there, 6e-4 at 7
+// tokens), so it takes the operand in two parts that add up to q to 2^-16 (bf16)
+// or 2^-22 (fp16) and a product of each (9e-7 and 1.5e-6; the backward pass of that
+// size with both outputs in fp32 2.67 ms, in bf16 1.47).
 #include "nm_gemm_nt.h"
 #include "nm_internal.h"
 
@@ -248,6 +254,13 @@ __global__ __launch_bounds__(1024) void xent_largest_kernel(const float* __restr
 template <int DT>
 constexpr float kOperandScale = DT == NM_F16 ? 16384.f : 1.f;
 
+// What is left of f after its rounding to 16 bits; nothing of what is not finite.
+template <int DT>
+__device__ inline float rest(float f) {
+  const float r = f - half_to_f32<DT>(to_half_bits<DT>(f));
+  return fabsf(r) < kInf ? r : 0.f;
+}
+
 struct XentBwdDev {
   XentArgsDev a;
   const float* lse;
@@ -255,6 +268,8 @@ struct XentBwdDev {
   const float* largest; // of |dloss|
   uint16_t* d;          // q [T][ldd], or null
   uint16_t* dt;         // q g / G, transposed: [piece][ldt], or null
+  uint16_t* d_rest;     // what rounding left of them, or null
+  uint16_t* dt_rest;
   int64_t ldd, ldt;
   int v0, vn, vpad;     // the piece: rows v0 .. v0 + vn of W, padded to vpad
 };
@@ -293,30 +308,38 @@ __global__ __launch_bounds__(C::THREADS) void xent_dlogits_kernel(XentBwdDev p, 
         }
     }
     if (p.d) {
+      auto write = [&](uint16_t* d, auto&& part) {
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j)
+        for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-          Area::put_by_n(area, i, j, li, lq, pack_half2<DT>(acc[i][j][0], acc[i][j][1]),
-                         pack_half2<DT>(acc[i][j][2], acc[i][j][3]));
-      // vpad is a multiple of 64: whole pieces
-      Area::template take<true>(area, [&](int n, int m, const u32x4& w) {
-        if (t0 + n < p.a.T && v0 + m < p.vpad)
-          *reinterpret_cast<u32x4*>(p.d + int64_t(t0 + n) * p.ldd + v0 + m) = w;
-      });
+          for (int i = 0; i < C::FM; ++i)
+            Area::put_by_n(area, i, j, li, lq, pack_half2<DT>(part(acc[i][j][0]), part(acc[i][j][1])),
+                           pack_half2<DT>(part(acc[i][j][2]), part(acc[i][j][3])));
+        // vpad is a multiple of 64: whole pieces
+        Area::template take<true>(area, [&](int n, int m, const u32x4& w) {
+          if (t0 + n < p.a.T && v0 + m < p.vpad) *reinterpret_cast<u32x4*>(d + int64_t(t0 + n) * p.ldd + v0 + m) = w;
+        });
+      };
+      write(p.d, [](float f) { return f; });
+      if (p.d_rest) write(p.d_rest, [](float f) { return rest<DT>(f); });
     }
     if (p.dt) {
+      auto write = [&](uint16_t* dt, auto&& part) {
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j)
+        for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-          Area::put_by_m(area, i, j, li, lq, pack_half2<DT>(ratio[j] * acc[i][j][0], ratio[j] * acc[i][j][1]),
-                         pack_half2<DT>(ratio[j] * acc[i][j][2], ratio[j] * acc[i][j][3]));
-      // so is ldt
-      Area::template take<false>(area, [&](int m, int n, const u32x4& w) {
-        if (v0 + m < p.vpad && t0 + n < p.ldt)
-          *reinterpret_cast<u32x4*>(p.dt + int64_t(v0 + m) * p.ldt + t0 + n) = w;
-      });
+          for (int i = 0; i < C::FM; ++i)
+            Area::put_by_m(area, i, j, li, lq,
+                           pack_half2<DT>(part(ratio[j] * acc[i][j][0]), part(ratio[j] * acc[i][j][1])),
+                           pack_half2<DT>(part(ratio[j] * acc[i][j][2]), part(ratio[j] * acc[i][j][3])));
+        // so is ldt
+        Area::template take<false>(area, [&](int m, int n, const u32x4& w) {
+          if (v0 + m < p.vpad && t0 + n < p.ldt)
+            *reinterpret_cast<u32x4*>(dt + int64_t(v0 + m) * p.ldt + t0 + n) = w;
+        });
+      };
+      write(p.dt, [](float f) { return f; });
+      if (p.dt_rest) write(p.dt_rest, [](float f) { return rest<DT>(f); });
     }
   });
 }
@@ -587,13 +610,14 @@ constexpr int64_t kFewTokens = 128;
 // Where the backward pass keeps things in its workspace (bytes).
 struct BwdPlan {
   int64_t piece, ldt, ldd, splits, ksplit;
-  size_t xt, wt, d, dt, acc, largest, total;
+  size_t xt, wt, d, dt, d_rest, dt_rest, acc, largest, total;
 };
 
-// The vocabulary is cut into pieces of at most 2^26 logits (128 MB in each
-// order): large enough that dx's fp32 sums, read and written once a piece,
+// dx and dw: parts of their operand (0: not wanted, 2: an fp32 output).  The
+// vocabulary is cut into pieces of at most 2^26 logits (128 MB in each order and
+// part): large enough that dx's fp32 sums, read and written once a piece,
 // stay a few percent of its products.
-BwdPlan plan_bwd(int64_t T, int64_t V, int64_t H, bool dx, bool dw) {
+BwdPlan plan_bwd(int64_t T, int64_t V, int64_t H, int dx, int dw) {
   BwdPlan p;
   p.ldt = up_to(T, 64);
   const int64_t most = std::max<int64_t>((int64_t(1) << 26) / std::max<int64_t>(p.ldt, 1) / 256 * 256, 256);
@@ -617,6 +641,8 @@ BwdPlan plan_bwd(int64_t T, int64_t V, int64_t H, bool dx, bool dw) {
   p.dt = take(dw ? size_t(p.piece) * p.ldt * 2 : 0);
   p.d = take(dx ? size_t(T) * p.ldd * 2 : 0);
   p.wt = take(dx && T > kFewTokens ? size_t(H) * p.ldd * 2 : 0);
+  p.dt_rest = take(dw > 1 ? size_t(p.piece) * p.ldt * 2 : 0);
+  p.d_rest = take(dx > 1 ? size_t(T) * p.ldd * 2 : 0);
   p.acc = take(dx ? size_t(p.splits) * T * H * 4 : 0);
   p.total = at;
   return p;
@@ -639,7 +665,8 @@ hipError_t product(const XentProduct& p, int out_dtype, int64_t splits, hipStrea
 
 template <int DT>
 hipError_t backward_dt(const XentArgs& a, hipStream_t s) {
-  const BwdPlan pl = plan_bwd(a.T, a.V, a.H, a.dx != nullptr, a.dw != nullptr);
+  const bool dx2 = a.dx && a.dx_dtype == NM_F32, dw2 = a.dw && a.dw_dtype == NM_F32;
+  const BwdPlan pl = plan_bwd(a.T, a.V, a.H, a.dx ? 1 + dx2 : 0, a.dw ? 1 + dw2 : 0);
   char* ws = static_cast<char*>(a.workspace);
   float* largest = reinterpret_cast<float*>(ws + pl.largest);
   uint16_t* xt = reinterpret_cast<uint16_t*>(ws + pl.xt);
@@ -656,6 +683,8 @@ hipError_t backward_dt(const XentArgs& a, hipStream_t s) {
   b.largest = largest;
   b.d = a.dx ? reinterpret_cast<uint16_t*>(ws + pl.d) : nullptr;
   b.dt = a.dw ? reinterpret_cast<uint16_t*>(ws + pl.dt) : nullptr;
+  b.d_rest = dx2 ? reinterpret_cast<uint16_t*>(ws + pl.d_rest) : nullptr;
+  b.dt_rest = dw2 ? reinterpret_cast<uint16_t*>(ws + pl.dt_rest) : nullptr;
   b.ldd = pl.ldd;
   b.ldt = pl.ldt;
   for (int64_t v0 = 0; v0 < a.V; v0 += pl.piece) {
@@ -671,25 +700,37 @@ hipError_t backward_dt(const XentArgs& a, hipStream_t s) {
     });
     if (e != hipSuccess) return e;
     const int64_t splits = (vpad + pl.ksplit - 1) / pl.ksplit;
+    // each product once for the rounded operand and, where there is one, once more for what it left
     if (a.dx && a.T <= kFewTokens) {
-      const FewDx p{a.w + v0 * a.ldw, b.d, a.ldw, pl.ldd, int(a.T), int(a.H), int(vn), int(vpad), int(pl.ksplit), acc,
-                    v0 > 0};
+      FewDx p{a.w + v0 * a.ldw, b.d, a.ldw, pl.ldd, int(a.T), int(a.H), int(vn), int(vpad), int(pl.ksplit), acc, v0 > 0};
       const dim3 grid(unsigned((a.H + 127) / 128), unsigned(splits), unsigned((a.T + 63) / 64));
-      if (a.T <= 16) hipLaunchKernelGGL((xent_dx_few_kernel<DT, 1>), grid, dim3(kFewWaves * 64), 0, s, p);
-      else hipLaunchKernelGGL((xent_dx_few_kernel<DT, 4>), grid, dim3(kFewWaves * 64), 0, s, p);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
+      auto go = [&] {
+        if (a.T <= 16) hipLaunchKernelGGL((xent_dx_few_kernel<DT, 1>), grid, dim3(kFewWaves * 64), 0, s, p);
+        else hipLaunchKernelGGL((xent_dx_few_kernel<DT, 4>), grid, dim3(kFewWaves * 64), 0, s, p);
+        return hipGetLastError();
+      };
+      if ((e = go()) != hipSuccess) return e;
+      p.d = b.d_rest;
+      p.add = true;
+      if (dx2 && (e = go()) != hipSuccess) return e;
     } else if (a.dx) {
       if ((e = transpose(a.w + v0 * a.ldw, a.ldw, vn, a.H, nullptr, 0, wt, pl.ldd, s)) != hipSuccess) return e;
       XentProduct p{wt, b.d, pl.ldd, pl.ldd, int(a.H), int(a.T), int(vpad), int(pl.ksplit), nullptr, acc, a.H,
                     a.T * a.H, v0 > 0};
       // (a last piece shorter than the others may need fewer splits: the rest keep their sums)
       if ((e = product<DT>(p, NM_F32, splits, s)) != hipSuccess) return e;
+      p.Q = b.d_rest;
+      p.add = true;
+      if (dx2 && (e = product<DT>(p, NM_F32, splits, s)) != hipSuccess) return e;
     }
     if (a.dw) {
-      const size_t es = a.dw_dtype == NM_F32 ? 4 : 2;
+      const size_t es = dw2 ? 4 : 2;
       XentProduct p{xt, b.dt, pl.ldt, pl.ldt, int(a.H), int(vn), int(pl.ldt), int(pl.ldt), largest,
                     static_cast<char*>(a.dw) + size_t(v0) * a.lddw * es, a.lddw, 0, false};
       if ((e = product<DT>(p, a.dw_dtype, 1, s)) != hipSuccess) return e;
+      p.Q = b.dt_rest;
+      p.add = true;
+      if (dw2 && (e = product<DT>(p, a.dw_dtype, 1, s)) != hipSuccess) return e;
     }
   }
   if (a.dx) {
@@ -713,7 +754,7 @@ size_t xent_workspace(int64_t T, int64_t V) {
   return size_t(tilesV) * T * 8 + size_t(T) * 4;
 }
 
-size_t xent_bwd_workspace(int64_t T, int64_t V, int64_t H, bool dx, bool dw) {
+size_t xent_bwd_workspace(int64_t T, int64_t V, int64_t H, int dx, int dw) {
   return T == 0 ? 0 : plan_bwd(T, V, H, dx, dw).total;
 }
 
