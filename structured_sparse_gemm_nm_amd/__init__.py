@@ -161,8 +161,11 @@ def _torch_dtype(code: int):
 
 
 def _stream_ptr(device) -> int:
-    # torch.cuda.current_stream(device).cuda_stream without the Stream object (1.7 us a call)
-    return _torch()._C._cuda_getCurrentRawStream(device.index)
+    # torch.cuda.current_stream(device).cuda_stream, without the Stream object (1.7 us a call) where
+    # this torch has the private call for it
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return int(raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream)
 
 
 def _require_cuda(*ts):
