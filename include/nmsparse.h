@@ -512,8 +512,13 @@ nm_status nm_adapter_spmm_bwd(const void* values, const uint32_t* idx, int64_t R
  * over its largest magnitude) enters its two products in the inputs' 16-bit type:
  * rounded once for a 16-bit dx or dw (relative 2^-8 in bf16, 2^-11 in fp16 an
  * element), in two parts that add up to it to 2^-16 or 2^-22 for an fp32 one,
- * which costs that product twice.  dloss itself multiplies the fp32 results.
- * T <= 2^22, V <= 2^24, H <= 2^20.  Matrices and workspace 16-byte aligned, vectors 4;
+ * which costs that product twice.  fp16 operands are held in steps of 2^-38, so
+ * below 2^-28 an element has an absolute error of up to 2^-39 instead: for dw that
+ * is 2^-39 of the largest |dloss|, and tokens whose dloss is far below the largest
+ * keep fewer bits there (not in dx, and not in bf16, which has fp32's range).
+ * dloss itself multiplies the fp32 results.
+ * T <= 2^22, V <= 2^24, H <= 2^20 and ceil(T / 16) ceil(V / 128) <= 2^26 (T x V up
+ * to 2^37; NM_ERR_SHAPE past it).  Matrices and workspace 16-byte aligned, vectors 4;
  * outputs and workspace must not overlap anything (NM_ERR_ALIAS).
  * Stream-ordered; nothing is allocated or synchronised.
  */

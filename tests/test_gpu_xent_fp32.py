@@ -95,3 +95,28 @@ def test_each_output_has_its_own_type(T, dt):
     assert torch.equal(hf[1], ff[1]) and torch.equal(fh[1], hh[1])
     assert torch.equal(nm.nm_xent_bwd(X, W, lab, lse, gd, need_dw=False)[0], ff[0])
     assert torch.equal(nm.nm_xent_bwd(X, W, lab, lse, gd, need_dx=False)[1], ff[1])
+
+
+@pytest.mark.parametrize("T", [40, 200])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_dloss_of_many_magnitudes(T, dt):
+    # dloss from 1 down to 2^-44: dx keeps its relative bound whatever a token's share
+    # (dloss multiplies it last); fp16 dw adds 2^-39 of the largest dloss an element,
+    # bf16 dw nothing
+    log(f"xent dloss magnitudes T={T} {dt}")
+    V, H = 500, 64
+    x, w, labels, _ = inputs(T, V, H, dt)
+    labels[:] = np.arange(T) * 3 % V                # words that only one or two tokens name
+    g = (2.0 ** -(44.0 * np.arange(T) / (T - 1))).astype(np.float32)
+    X, W = to_dev(x, dt), to_dev(w, dt)
+    lab, gd = torch.from_numpy(labels).cuda(), torch.from_numpy(g).cuda()
+    _, lse = nm.nm_xent(X, W, lab)
+    dx, dw = nm.nm_xent_bwd(X, W, lab, lse, gd)
+    torch.cuda.synchronize()
+    g = g.astype(np.float64)
+    rx, rw = L.xent_bwd_ref(f64(x, dt), f64(w, dt), labels, g)
+    # a token at a time: q's own steps of 2^-38 (fp16) are of its g
+    bx = np.concatenate([bounds(f64(x, dt)[t:t + 1], f64(w, dt), labels[t:t + 1], g[t:t + 1], dt)[0] for t in range(T)])
+    _, bw = bounds(f64(x, dt), f64(w, dt), labels, g, dt)
+    within(host(dx), rx, bx)
+    within(host(dw), rw, bw)
