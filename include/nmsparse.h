@@ -433,8 +433,9 @@ nm_status nm_diag_spmm(const void* values, const int32_t* offsets, int64_t D, in
  * Statistics and sums are fp32 (the variance taken about the mean), outputs are
  * rounded once.  Pointers need the alignment of their element only, leading
  * dimensions are free.  Outputs must not overlap inputs or each other
- * (NM_ERR_ALIAS).  A token holding Inf or NaN gives NaN in its own row and in
- * dw / db.
+ * (NM_ERR_ALIAS).  An x that holds Inf or NaN gives NaN in its own row of y and dx
+ * and in all of dw, not in db; a dy that does, in its own row of dx (any weight not
+ * zero) and in its columns of dw and db.
  */
 nm_status nm_layernorm(const void* x, int64_t T, int64_t H, int64_t ldx, int dtype, const void* weight,
                        const void* bias, float eps, void* y, int64_t ldy, float* mean, float* rstd, void* stream);
