@@ -471,7 +471,10 @@ nm_status nm_layernorm_bwd(const void* dy, int64_t ldg, const void* x, int64_t l
  * xa and u stay fp32; between the two low-rank products they enter the matrix
  * cores as three bf16 parts, which hold their 24 bits.  Inf or NaN in one token
  * or adapter reaches the outputs of that token or adapter only (there an Inf may
- * turn to NaN: it meets the parts that are zero).
+ * turn to NaN: it meets the parts that are zero).  Equal calls give equal bits; a
+ * token's last bits can change with its neighbours (the kernel goes by T, and the
+ * term is summed onto the product where a tile's tokens share one adapter, apart
+ * from it where they do not).
  * T <= 2^24, R and K <= 2^22.  Pointers 16-byte aligned (adapter, scale: 4),
  * ldx and ldg multiples of 8 below 2^24; outputs and workspace must not overlap anything
  * (NM_ERR_ALIAS).  Stream-ordered; nothing is allocated or synchronised.

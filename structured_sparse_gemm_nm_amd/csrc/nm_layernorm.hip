@@ -527,8 +527,10 @@ hipError_t fwd_dt(const LayerNormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Workgroups of the backward pass (= rows of partial sums): enough to keep
-// every CU's loads in flight, few enough that the partial sums stay small.
+// Workgroups of the backward pass (= rows of partial sums): two a CU, to keep its
+// loads in flight.  Their partial sums, 8 H bytes each, written and read once, are
+// small beside many rows (8192 x 4096 bf16: 16.8 MB beside 67 of dx) and as large as
+// dx beside few (1999 x 1543 fp16: 6.3 MB beside 6.2, of the pass's 13 + 4 us).
 int64_t bwd_groups(int64_t T, int64_t H) {
   const Shape sh = row_shape(H);
   const int64_t rows = sh.tpr == 64 ? 4 : 1;

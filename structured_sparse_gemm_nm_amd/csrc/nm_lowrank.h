@@ -194,7 +194,8 @@ __device__ inline int lowrank_ids(const LowRank& p, int t0) {
 // of them (one round for a request's adjacent tokens, two where requests meet,
 // 64 at worst).  With one adapter the product accumulates in place; with
 // several, each token takes the sum of its own adapter's round by selection,
-// never by a mask's product, so Inf and NaN stay with their adapter's tokens.
+// never by a mask's product, so Inf and NaN stay with their adapter's tokens (the
+// two differ in rounding: a token's last bit depends on its neighbours' adapters).
 // Columns past C and tokens past T reread the last one.
 template <int DT, int F, int NT, typename Acc>
 __device__ inline void lowrank_add(const LowRank& p, int id, int t0, int c0, Acc&& acc) {
