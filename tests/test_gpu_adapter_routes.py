@@ -74,3 +74,13 @@ def test_wide_gradients(R, K, T, r, na, dt):
 def test_backward_of_many_tiles(n, m):
     log(f"adapter backward tiles {n}:{m}")
     Case(1096, 672, 700, 24, 4, "bf16", n, m).check_backward()
+
+
+# the largest ranks: several rounds of 16 (few tokens), 32 (the term) and 64 (gradients)
+@pytest.mark.parametrize("T,r", [(9, 256), (40, 256), (300, 129), (130, 200)])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_largest_ranks(T, r, dt):
+    log(f"adapter rank {r} T={T} {dt}")
+    c = Case(264, 384, T, r, 3, dt)
+    c.check_forward()
+    c.check_backward()
