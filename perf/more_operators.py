@@ -183,6 +183,9 @@ def prepare(case, seed):
         for g in s["grads"]:
             s["out"].append(s["flat"][g.dtype][at[g.dtype]: at[g.dtype] + g.numel()].view(g.shape))
             at[g.dtype] += g.numel()
+        if own:     # a training loop's gradients keep their tensors, and it keeps their list
+            import structured_sparse_gemm_nm_amd as nm
+            s["list"] = nm.nm_grad_list(s["grads"], s["out"])
         return s
     T, K = case["T"], case["K"]
     # activations or weights of differing rows, with a few outlying columns
@@ -271,9 +274,12 @@ def _mx_split(x):
 
 
 def _mx_pack(x):
+    """The codes two a byte, and the exponent bytes in panels of eight: block i of
+    row r at [i // 8, r, i % 8], zeros behind the last."""
     code, byte = _mx_split(x)
     code = code.view(x.shape[0], -1, 2)
-    return (code[:, :, 0] | (code[:, :, 1] << 4)).to(torch.uint8), byte.to(torch.uint8)
+    byte = torch.nn.functional.pad(byte, (0, -byte.shape[1] % 8)).view(x.shape[0], -1, 8).transpose(0, 1)
+    return (code[:, :, 0] | (code[:, :, 1] << 4)).to(torch.uint8), byte.to(torch.uint8).contiguous()
 
 
 def _mx_values(code, byte):
@@ -285,8 +291,9 @@ def _mx_values(code, byte):
     return (mag * _pow2(half) * _pow2(e - half)).view(code.shape[0], -1)
 
 
-def _mx_unpack(q, byte):
+def _mx_unpack(q, panels):
     code = torch.stack([q & 15, q >> 4], 2).view(q.shape[0], -1, BLOCK).int()
+    byte = panels.transpose(0, 1).reshape(q.shape[0], -1)[:, : code.shape[1]]
     return _mx_values(code, byte)
 
 
@@ -350,7 +357,7 @@ def _mx_own(s):
 
 def _clip_own(s):
     import structured_sparse_gemm_nm_amd as nm
-    norm, _ = nm.nm_grad_clip(s["grads"], s["case"]["max_norm"], eps=EPS, out=s["out"])
+    norm, _ = nm.nm_grad_clip(s["list"], s["case"]["max_norm"], eps=EPS)
     return [norm, *s["flat"].values()]
 
 
@@ -459,7 +466,9 @@ def _mx_exact(s):
     x = _mx_round_exact(s)
     grid = torch.tensor(E2M1 + tuple(-v for v in E2M1), dtype=torch.float64, device="cuda")
 
-    def weight(q, byte):
+    def weight(q, panels):
+        block = torch.arange(q.shape[1] * 2 // BLOCK, device="cuda")
+        byte = panels[block // 8, :, block % 8].t()
         w = torch.empty((q.shape[0], q.shape[1] * 2), dtype=torch.float64, device="cuda")
         w[:, 0::2], w[:, 1::2] = grid[(q % 16).long()], grid[(q // 16).long()]
         return w * _pow2(byte.int() - 127, torch.float64).repeat_interleave(BLOCK, 1)
