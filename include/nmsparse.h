@@ -86,8 +86,9 @@ typedef enum { NM_F16 = 0, NM_BF16 = 1, NM_F32 = 2, NM_I8 = 3, NM_I32 = 4, NM_FP
  * place of memory the library allocated; 201 adds the hybrid tiles
  * (nm_hybrid_*), the training products (nm_spmm_dx, nm_spmm_dw) and the
  * block / diagonal structures (nm_block_*, nm_diag_*).  Layer norm, the adapters
- * and cross entropy (nm_layernorm*, nm_adapter_*, nm_xent*) only add entry
- * points and came under 201. */
+ * and cross entropy (nm_layernorm*, nm_adapter_*, nm_xent*), and the products
+ * grouped by expert, the 4-bit format and the gradients' norm (nm_group_*, nm_mx_*,
+ * nm_grad_*) only add entry points and came under 201. */
 int nm_version(void);
 
 /* Short fixed text for a status code (never NULL). */
@@ -536,6 +537,116 @@ nm_status nm_xent_bwd(const void* x, int64_t T, int64_t H, int64_t ldx, const vo
                       int dtype, const int32_t* labels, const float* lse, const float* dloss, void* dx, int64_t lddx,
                       int dx_dtype, void* dw, int64_t lddw, int dw_dtype, void* workspace, size_t workspace_bytes,
                       void* stream);
+
+/*
+ * Products grouped by expert: a layer of E experts, each with its own packed N:M
+ * weight of R x K, over tokens ordered by expert.  Expert e owns the rows
+ * offsets[e] <= t < offsets[e+1] of act, Y, G and dX:
+ *   nm_group_spmm:     Y[t][r]  = sum_k W_e[r][k] act[t][k]           (nm_spmm),
+ *   nm_group_spmm_dx:  dX[t][k] = sum_r G[t][r] W_e[r][k]             (nm_spmm_dx),
+ *   nm_group_spmm_dw:  dW[e][r][s] = sum_t G[t][r] act[t][k(r, s)]    (nm_spmm_dw).
+ *   values, idx   E packed weights one after the other (each as nm_packed_sizes
+ *                 says), 16-bit types;  dW  E packed gradients likewise.
+ *   offsets       device int32 [E + 1], ascending, 0 <= offsets[0], offsets[E] <=
+ *                 T; read on the device, so a captured graph follows them.  An
+ *                 expert may own no rows (its dW is zeros).  Rows before
+ *                 offsets[0] and from offsets[E] on belong to none: they are not
+ *                 read, and stay as they were in Y and dX.  Offsets that break the
+ *                 rule are clamped into [0, T] and to ascend one by one: wrong
+ *                 values, but no access outside the arrays.
+ *   act, Y, G, dX as nm_spmm and nm_spmm_dx (ldx, ldg below 2^23); out_dtype NM_F32
+ *                 or the input dtype.  dX and dW need R % 8 == 0 and K % 32 == 0.
+ *   workspace     device, the bytes of the matching _workspace_size, 16-byte aligned
+ *                 (dW needs none).
+ * Products and sums are fp32, outputs rounded once.  Equal calls give equal bits; the
+ * kernel goes by T / min(T, E), so a token's last bits can change with T and E.  Inf
+ * or NaN in one row reaches the outputs of its expert's row (dW: of its expert) only.
+ * 1 <= E <= 65535, T <= 2^24, R and K <= 2^22; NM_ERR_SHAPE as in nm_spmm_dx and
+ * nm_spmm_dw for one expert's arrays, and for T x ldg or T x ldx of 4 GiB in dW.
+ * Outputs and workspace must not overlap anything (NM_ERR_ALIAS).  Stream-ordered;
+ * nothing is allocated or synchronised.
+ */
+nm_status nm_group_spmm_workspace_size(int64_t E, int64_t R, int64_t K, int n, int m, int dtype, int64_t T,
+                                       int out_dtype, size_t* bytes);
+nm_status nm_group_spmm(const void* values, const uint32_t* idx, int64_t E, int64_t R, int64_t K, int n, int m,
+                        int dtype, const void* act, int64_t T, int64_t ldx, const int32_t* offsets, void* Y,
+                        int64_t ldy, int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+nm_status nm_group_spmm_dx_workspace_size(int64_t E, int64_t T, size_t* bytes);
+nm_status nm_group_spmm_dx(const void* values, const uint32_t* idx, int64_t E, int64_t R, int64_t K, int n, int m,
+                           int dtype, const void* G, int64_t T, int64_t ldg, const int32_t* offsets, void* dX,
+                           int64_t lddx, int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+nm_status nm_group_spmm_dw(const uint32_t* idx, int64_t E, int64_t R, int64_t K, int n, int m, int dtype, const void* G,
+                           int64_t T, int64_t ldg, const void* act, int64_t ldx, const int32_t* offsets, void* dW,
+                           int out_dtype, void* stream);
+
+/*
+ * Microscaled 4-bit floats: a row's values in blocks of 32, each value a sign and
+ * one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (E2M1) times the block's power of two (E8M0):
+ * 4.25 bits a value.
+ *   q      [T][K/2] bytes: value 2i of a row in the low four bits of byte i, value
+ *          2i + 1 in the high four (bit 3 the sign, bits 0..2 the magnitude's number
+ *          in the list above);
+ *   scale  [ceil(K/256)][T][8] bytes: byte b of a block means 2^(b - 127), 255 NaN;
+ *          block i of row t is scale[i / 8][t][i % 8].  The eight bytes of a row's
+ *          256 columns lie together and the rows after one another (a product's tile
+ *          then reads one run); those past K in the last panel are written as 0 and
+ *          not looked at.
+ * nm_mx_quantize: the exponent of a block is that of its largest magnitude less 2
+ *   (not below 2^-127; a block of zeros has byte 0), each value goes to the nearest
+ *   representable one, ties to the even mantissa, magnitudes above 6 in the block's
+ *   scale to 6.  A block that holds Inf or NaN becomes NaN.
+ *   x      device [T, K] row-major, ldx >= K, NM_F16, NM_BF16 or NM_F32, aligned to
+ *          its element; K % 32 == 0.
+ * nm_mx_dequantize: y [T, K] (ldy >= K; NM_F16, NM_BF16 or NM_F32), the values,
+ *   rounded once where the type does not hold them.
+ * nm_mx_gemm: Y[t][r] = sum_k x[t][k] w[r][k] of two quantised operands.
+ *   wq, wscale  E weights of R rows one after the other, each as above (E = 1
+ *               without offsets);  xq, xscale  T rows.
+ *   offsets     device int32 [E + 1] or NULL: rows ordered by expert, as in
+ *               nm_group_spmm.
+ *   Y           device [T, R] row-major, ldy >= R, NM_F32, NM_F16 or NM_BF16.
+ * Products are exact, sums fp32, outputs rounded once.  T <= 2^24, R and K <= 2^22,
+ * an operand's scales below 4 GiB.  Device pointers 16-byte aligned (x, y: their
+ * element; offsets: 4); outputs and workspace must not overlap anything
+ * (NM_ERR_ALIAS).  Stream-ordered; nothing is allocated or synchronised.
+ */
+nm_status nm_mx_sizes(int64_t T, int64_t K, size_t* q_bytes, size_t* scale_bytes);
+nm_status nm_mx_quantize(const void* x, int64_t T, int64_t K, int64_t ldx, int dtype, uint8_t* q, uint8_t* scale,
+                         void* stream);
+nm_status nm_mx_dequantize(const uint8_t* q, const uint8_t* scale, int64_t T, int64_t K, void* y, int64_t ldy,
+                           int dtype, void* stream);
+nm_status nm_mx_gemm_workspace_size(int64_t E, int64_t R, int64_t K, int64_t T, int grouped, int out_dtype,
+                                    size_t* bytes);
+nm_status nm_mx_gemm(const uint8_t* wq, const uint8_t* wscale, int64_t E, int64_t R, int64_t K, const uint8_t* xq,
+                     const uint8_t* xscale, int64_t T, const int32_t* offsets, void* Y, int64_t ldy, int out_dtype,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Global norm of the gradients in many tensors, and their clipping:
+ *   norm = (sum over every element of every tensor of g^2)^(1/2),
+ *   out_i = g_i min(1, max_norm / (norm + eps)).
+ *   grads, out  host arrays of `tensors` device addresses; counts, dtypes their
+ *               numbers of elements and types (host; NM_F16, NM_BF16 or NM_F32, a
+ *               list may mix them; out_i has the type of g_i).  Read before the call
+ *               returns.  Tensors are contiguous and aligned to their element; an
+ *               empty one (count 0) may be NULL.
+ *   out         grads itself, or single addresses equal to theirs, scale in place.
+ *   norm        device fp32 [1];  workspace  device, nm_grad_workspace_size bytes,
+ *               16-byte aligned.
+ * Squares are summed in 64 bits, so that neither large nor small gradients leave the
+ * range; each out_i is rounded once.  A NaN anywhere makes norm and every out_i NaN; an
+ * Inf makes norm Inf, itself NaN and everything else 0 (max_norm finite).  A norm + eps
+ * of 0 scales by 1.  Equal calls give equal bits.
+ * tensors <= 16384, counts <= 2^36; max_norm >= 0 (Inf: no limit), eps >= 0
+ * (NM_ERR_SHAPE).  Nothing written may overlap anything else (NM_ERR_ALIAS): a tensor
+ * named twice in place among them.  Stream-ordered; nothing is allocated or synchronised.
+ */
+nm_status nm_grad_workspace_size(int64_t tensors, size_t* bytes);
+nm_status nm_grad_norm(const void* const* grads, const int64_t* counts, const int* dtypes, int64_t tensors, float* norm,
+                       void* workspace, size_t workspace_bytes, void* stream);
+nm_status nm_grad_clip(const void* const* grads, const int64_t* counts, const int* dtypes, int64_t tensors,
+                       double max_norm, double eps, void* const* out, float* norm, void* workspace,
+                       size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

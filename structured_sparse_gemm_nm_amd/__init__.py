@@ -8,10 +8,12 @@ missing every call raises.
 
 Function names follow the C ABI: nm_compress, nm_decompress, nm_spmm,
 nm_spmm_perm, nm_packed_sizes, and so on to the operators beside a projection:
-nm_layernorm, nm_adapter_spmm, nm_xent and their _bwd.
+nm_layernorm, nm_adapter_spmm, nm_xent and their _bwd, nm_group_spmm (_dx, _dw),
+nm_mx_quantize, nm_mx_gemm, nm_grad_norm and nm_grad_clip.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -20,7 +22,9 @@ __all__ = ["NM_OK", "NM_F16", "NM_BF16", "NM_F32", "NM_I8", "NM_I32", "NM_FP8", 
            "nm_spmm_perm_workspace_size", "nm_spmm_perm_static", "nm_check_perm", "nm_spmm_dx", "nm_spmm_dw",
            "nm_hybrid_layout", "nm_hybrid_compress", "nm_hybrid_spmm", "nm_block_structure", "nm_block_compress",
            "nm_block_spmm", "nm_diag_compress", "nm_diag_spmm", "nm_layernorm", "nm_layernorm_bwd", "nm_adapter_spmm",
-           "nm_adapter_spmm_bwd", "nm_xent", "nm_xent_bwd", "PATTERNS"]
+           "nm_adapter_spmm_bwd", "nm_xent", "nm_xent_bwd", "nm_group_spmm", "nm_group_spmm_dx", "nm_group_spmm_dw",
+           "nm_mx_quantize", "nm_mx_dequantize", "nm_mx_gemm", "GradList", "nm_grad_list", "nm_grad_norm",
+           "nm_grad_clip", "PATTERNS"]
 
 NM_OK = 0
 NM_F16, NM_BF16, NM_F32, NM_I8, NM_I32, NM_FP8 = 0, 1, 2, 3, 4, 5
@@ -123,6 +127,24 @@ def lib() -> ctypes.CDLL:
     L.nm_xent_bwd_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32, ctypes.POINTER(sz)]
     L.nm_xent_bwd.restype = i32
     L.nm_xent_bwd.argtypes = [vp, i64, i64, i64, vp, i64, i64, i32, vp, vp, vp, vp, i64, i32, vp, i64, i32, vp, sz, vp]
+    f64 = ctypes.c_double
+    L.nm_group_spmm_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32, i64, i32, ctypes.POINTER(sz)]
+    L.nm_group_spmm.argtypes = [vp, vp, i64, i64, i64, i32, i32, i32, vp, i64, i64, vp, vp, i64, i32, vp, sz, vp]
+    L.nm_group_spmm_dx_workspace_size.argtypes = [i64, i64, ctypes.POINTER(sz)]
+    L.nm_group_spmm_dx.argtypes = [vp, vp, i64, i64, i64, i32, i32, i32, vp, i64, i64, vp, vp, i64, i32, vp, sz, vp]
+    L.nm_group_spmm_dw.argtypes = [vp, i64, i64, i64, i32, i32, i32, vp, i64, i64, vp, i64, vp, vp, i32, vp]
+    L.nm_mx_sizes.argtypes = [i64, i64, ctypes.POINTER(sz), ctypes.POINTER(sz)]
+    L.nm_mx_quantize.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp]
+    L.nm_mx_dequantize.argtypes = [vp, vp, i64, i64, vp, i64, i32, vp]
+    L.nm_mx_gemm_workspace_size.argtypes = [i64, i64, i64, i64, i32, i32, ctypes.POINTER(sz)]
+    L.nm_mx_gemm.argtypes = [vp, vp, i64, i64, i64, vp, vp, i64, vp, vp, i64, i32, vp, sz, vp]
+    L.nm_grad_workspace_size.argtypes = [i64, ctypes.POINTER(sz)]
+    L.nm_grad_norm.argtypes = [vp, vp, vp, i64, vp, vp, sz, vp]
+    L.nm_grad_clip.argtypes = [vp, vp, vp, i64, f64, f64, vp, vp, vp, sz, vp]
+    for name in ("nm_group_spmm_workspace_size", "nm_group_spmm", "nm_group_spmm_dx_workspace_size", "nm_group_spmm_dx",
+                 "nm_group_spmm_dw", "nm_mx_sizes", "nm_mx_quantize", "nm_mx_dequantize", "nm_mx_gemm_workspace_size",
+                 "nm_mx_gemm", "nm_grad_workspace_size", "nm_grad_norm", "nm_grad_clip"):
+        getattr(L, name).restype = i32
     _lib = L
     return L
 
@@ -888,3 +910,305 @@ def nm_xent_bwd(x, w, labels, lse, dloss, ignore_index: int = -100, out_dtype=No
                          lse.data_ptr(), dloss.data_ptr(), _ptr(dx), H, od, _ptr(dw), H, od, _ptr(ws), need,
                          _stream_ptr(x.device)))
     return dx, dw
+
+
+# --------------------------------------------------------------------------
+# products grouped by expert over packed weights
+# --------------------------------------------------------------------------
+
+def _on(device):
+    """Makes `device` the current one for a launch (nothing to do where it is)."""
+    torch = _torch()
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _check_offsets(offsets, E, device):
+    torch = _torch()
+    if offsets.dtype != torch.int32 or offsets.shape != (E + 1,) or not offsets.is_contiguous() \
+            or offsets.device != device:
+        raise ValueError(f"offsets must be a contiguous int32 [{E + 1}] tensor on {device}")
+
+
+def _check_experts(idx, act, offsets, K, n, m):
+    """(E, R, T, dtype code) of index words [E, R, words] beside rows `act` (act or G)."""
+    torch = _torch()
+    if idx.dim() != 3 or act.dim() != 2:
+        raise ValueError("idx must be [experts, R, words] and the rows a matrix")
+    E, R = idx.shape[0], idx.shape[1]
+    dt = _dtype_code(act)
+    if dt not in (NM_F16, NM_BF16):
+        raise TypeError("grouped products take float16 or bfloat16 weights")
+    if (n, m) not in PATTERNS or K < 16 or K % 16:
+        nm_packed_sizes(R, K, n, m, dt)     # raises
+    words = (K // m * n * (3 if m == 8 else 2) + 31) // 32
+    if idx.dtype != torch.int32 or idx.shape[2] != words or not idx.is_contiguous() or idx.device != act.device:
+        raise ValueError(f"idx must be a contiguous int32 [{E}, {R}, {words}] tensor on {act.device}")
+    _check_offsets(offsets, E, act.device)
+    _require_cuda(act)
+    return E, R, act.shape[0], dt
+
+
+def _check_expert_values(values, E, R, K, n, m, like):
+    S = K // m * n
+    if values.shape != (E, R, S) or values.dtype != like.dtype or not values.is_contiguous() \
+            or values.device != like.device:
+        raise ValueError(f"values must be a contiguous [{E}, {R}, {S}] {like.dtype} tensor on {like.device}")
+
+
+def _group_out(out, rows, cols, dt, out_dtype, like):
+    torch = _torch()
+    if out_dtype not in (None, torch.float32, like.dtype):
+        raise TypeError("out_dtype must be float32 or the weights' dtype")
+    od, otype = (dt, like.dtype) if out_dtype == like.dtype else (NM_F32, torch.float32)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=otype, device=like.device)
+    else:
+        _matrix(out, "out", rows, cols, otype, like.device)
+    return out, od
+
+
+def nm_group_spmm(values, idx, act, offsets, K: int, n: int = 2, m: int = 4, out_dtype=None, out=None):
+    """Y [T, R]: Y[t] = W_e act[t] for the rows offsets[e] <= t < offsets[e + 1] of expert e.
+    values [E, R, K n / m], idx int32 [E, R, words]: E packed weights; act [T, K]; offsets int32
+    [E + 1], on the device.  Rows of no expert stay as they were (in a fresh Y: undefined)."""
+    _row_major(act, "act")
+    E, R, T, dt = _check_experts(idx, act, offsets, K, n, m)
+    _check_expert_values(values, E, R, K, n, m, act)
+    _matrix(act, "act", T, K, values.dtype, values.device)
+    L = lib()
+    with _on(act.device):
+        out, od = _group_out(out, T, R, dt, out_dtype, act)
+        ws, need = _workspace(L.nm_group_spmm_workspace_size, E, R, K, n, m, dt, T, od, device=act.device)
+        _check(L.nm_group_spmm(values.data_ptr(), idx.data_ptr(), E, R, K, n, m, dt, act.data_ptr(), T, _row_stride(act),
+                               offsets.data_ptr(), out.data_ptr(), _row_stride(out), od, _ptr(ws), need,
+                               _stream_ptr(act.device)))
+    return out
+
+
+def nm_group_spmm_dx(values, idx, G, offsets, K: int, n: int = 2, m: int = 4, out_dtype=None, out=None):
+    """dX [T, K] of nm_group_spmm from G = dL/dY [T, R]: dX[t] = W_e^T G[t]."""
+    _row_major(G, "G")
+    E, R, T, dt = _check_experts(idx, G, offsets, K, n, m)
+    _check_expert_values(values, E, R, K, n, m, G)
+    _matrix(G, "G", T, R, values.dtype, values.device)
+    L = lib()
+    with _on(G.device):
+        out, od = _group_out(out, T, K, dt, out_dtype, G)
+        ws, need = _workspace(L.nm_group_spmm_dx_workspace_size, E, T, device=G.device)
+        _check(L.nm_group_spmm_dx(values.data_ptr(), idx.data_ptr(), E, R, K, n, m, dt, G.data_ptr(), T, _row_stride(G),
+                                  offsets.data_ptr(), out.data_ptr(), _row_stride(out), od, _ptr(ws), need,
+                                  _stream_ptr(G.device)))
+    return out
+
+
+def nm_group_spmm_dw(idx, G, act, offsets, K: int, n: int = 2, m: int = 4, out_dtype=None, out=None):
+    """dW [E, R, K n / m] of nm_group_spmm: the gradient of every stored survivor of every expert
+    (zeros for an expert without rows)."""
+    torch = _torch()
+    _row_major(G, "G")
+    _row_major(act, "act")
+    E, R, T, dt = _check_experts(idx, G, offsets, K, n, m)
+    _matrix(G, "G", T, R, act.dtype, act.device)
+    _matrix(act, "act", T, K, G.dtype, G.device)
+    S = K // m * n
+    L = lib()
+    with _on(G.device):
+        flat = out.view(E * R, S) if out is not None and out.shape == (E, R, S) and out.is_contiguous() else out
+        flat, od = _group_out(flat, E * R, S, dt, out_dtype, G)
+        if not flat.is_contiguous():
+            raise ValueError(f"out must be a contiguous [{E}, {R}, {S}] tensor")
+        _check(L.nm_group_spmm_dw(idx.data_ptr(), E, R, K, n, m, dt, G.data_ptr(), T, _row_stride(G), act.data_ptr(),
+                                  _row_stride(act), offsets.data_ptr(), flat.data_ptr(), od, _stream_ptr(G.device)))
+    return out if out is not None else flat.view(E, R, S)
+
+
+# --------------------------------------------------------------------------
+# microscaled 4-bit floats
+# --------------------------------------------------------------------------
+
+def _mx_shapes(T, K):
+    if K < 32 or K % 32:
+        raise ValueError(f"K = {K} is not a positive multiple of 32")
+    return (T, K // 2), ((K + 255) // 256, T, 8)
+
+
+def nm_mx_quantize(x):
+    """(q, scale) of x [T, K] or E weights [E, R, K] (float16, bfloat16 or float32): 4-bit values, two a
+    byte, uint8 [T, K / 2], and a power of two for every 32 of a row, uint8 [ceil(K / 256), T, 8] (block i
+    of row t at [i // 8, t, i % 8]); a leading axis of experts stays in front of both."""
+    torch = _torch()
+    _require_cuda(x)
+    dt = _norm_code(x)
+    if x.dim() not in (2, 3) or x.stride(-1) != 1:
+        raise ValueError("x must be [T, K] or [experts, R, K] with unit stride along its rows")
+    lead, (T, K) = tuple(x.shape[:-2]), x.shape[-2:]
+    qs, ss = _mx_shapes(T, K)
+    with _on(x.device):
+        q = torch.empty(lead + qs, dtype=torch.uint8, device=x.device)
+        scale = torch.empty(lead + ss, dtype=torch.uint8, device=x.device)
+        stream = _stream_ptr(x.device)
+        for e in range(lead[0] if lead else 1):
+            xe, qe, se = (x[e], q[e], scale[e]) if lead else (x, q, scale)
+            _check(lib().nm_mx_quantize(xe.data_ptr(), T, K, _row_stride(xe), dt, qe.data_ptr(), se.data_ptr(), stream))
+    return q, scale
+
+
+def nm_mx_dequantize(q, scale, dtype=None):
+    """The values [T, K] (float32 unless dtype names bfloat16 or float16) of nm_mx_quantize's q, scale;
+    [E, R, K] of a stack of weights."""
+    torch = _torch()
+    _require_cuda(q)
+    dtype = dtype or torch.float32
+    dt = _norm_code(torch.empty(0, dtype=dtype))
+    if q.dim() not in (2, 3):
+        raise ValueError("q must be [T, K / 2] or [experts, R, K / 2]")
+    lead, T, K = tuple(q.shape[:-2]), q.shape[-2], 2 * q.shape[-1]
+    _check_mx(q, scale, lead, T, K, "q", "scale", q.device)
+    with _on(q.device):
+        y = torch.empty(lead + (T, K), dtype=dtype, device=q.device)
+        stream = _stream_ptr(q.device)
+        for e in range(lead[0] if lead else 1):
+            ye, qe, se = (y[e], q[e], scale[e]) if lead else (y, q, scale)
+            _check(lib().nm_mx_dequantize(qe.data_ptr(), se.data_ptr(), T, K, ye.data_ptr(), K, dt, stream))
+    return y
+
+
+def _check_mx(q, scale, lead, T, K, name_q, name_s, device):
+    torch = _torch()
+    qs, ss = _mx_shapes(T, K)
+    for t, name, shape in ((q, name_q, lead + qs), (scale, name_s, lead + ss)):
+        if t.dtype != torch.uint8 or t.shape != shape or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{name} must be a contiguous uint8 {list(shape)} tensor on {device}")
+
+
+def nm_mx_gemm(wq, wscale, xq, xscale, offsets=None, out_dtype=None, out=None):
+    """Y [T, R] = x w^T of two operands that nm_mx_quantize made: wq [R, K / 2], xq [T, K / 2].  With
+    offsets (int32 [E + 1], on the device) wq is [E, R, K / 2], and the rows offsets[e] <= t <
+    offsets[e + 1] of x meet weight e; rows of no expert stay as they were.  float32, or out_dtype."""
+    torch = _torch()
+    if xq.dim() != 2 or wq.dim() != (2 if offsets is None else 3):
+        raise ValueError("xq must be [T, K / 2] and wq [R, K / 2] (with offsets [experts, R, K / 2])")
+    T, K, R = xq.shape[0], 2 * xq.shape[1], wq.shape[-2]
+    E = 1 if offsets is None else wq.shape[0]
+    _check_mx(xq, xscale, (), T, K, "xq", "xscale", xq.device)
+    _check_mx(wq, wscale, () if offsets is None else (E,), R, K, "wq", "wscale", xq.device)
+    if offsets is not None:
+        _check_offsets(offsets, E, xq.device)
+    _require_cuda(xq)
+    otype = out_dtype or torch.float32
+    od = NM_F32 if otype == torch.float32 else NM_BF16 if otype == torch.bfloat16 else NM_F16
+    if otype not in (torch.float32, torch.bfloat16, torch.float16):
+        raise TypeError(f"out_dtype must be float32, bfloat16 or float16, not {otype}")
+    L = lib()
+    with _on(xq.device):
+        if out is None:
+            out = torch.empty((T, R), dtype=otype, device=xq.device)
+        else:
+            _matrix(out, "out", T, R, otype, xq.device)
+        ws, need = _workspace(L.nm_mx_gemm_workspace_size, E, R, K, T, int(offsets is not None), od, device=xq.device)
+        _check(L.nm_mx_gemm(wq.data_ptr(), wscale.data_ptr(), E, R, K, xq.data_ptr(), xscale.data_ptr(), T,
+                            _ptr(offsets), out.data_ptr(), _row_stride(out), od, _ptr(ws), need,
+                            _stream_ptr(xq.device)))
+    return out
+
+
+# --------------------------------------------------------------------------
+# global norm of gradients, and clipping
+# --------------------------------------------------------------------------
+
+class GradList:
+    """Gradients to be measured or clipped together, and where the clipped ones go
+    (in place unless `out` names as many tensors of the same sizes and types).
+
+    A training loop whose gradients keep their tensors makes one and passes it to
+    nm_grad_norm and nm_grad_clip every step: the tensors are checked here, once, and
+    a call only asks each for its address (a tensor that has been given other memory
+    since is noticed, and the list checked again)."""
+
+    def __init__(self, grads, out=None):
+        self.grads, self.out = list(grads), None if out is None else list(out)
+        self._lay_out()
+
+    def _lay_out(self):
+        torch = _torch()
+        outs = self.grads if self.out is None else self.out
+        if len(outs) != len(self.grads):
+            raise ValueError(f"{len(outs)} outputs for {len(self.grads)} gradients")
+        self.device = self.grads[0].device if self.grads else torch.device("cuda", torch.cuda.current_device())
+        codes = {torch.float32: NM_F32, torch.bfloat16: NM_BF16, torch.float16: NM_F16}
+        dtypes = []
+        for g, o in zip(self.grads, outs):
+            code = codes.get(g.dtype)
+            if code is None:
+                raise TypeError(f"gradients are float16, bfloat16 or float32, got {g.dtype}")
+            for t in (g, o):
+                if not t.is_cuda:
+                    raise ValueError("tensors must be on a HIP device (no CPU path)")
+                if t.dtype != g.dtype or t.shape != g.shape or t.device != self.device or not t.is_contiguous():
+                    raise ValueError(f"gradients and outputs must be contiguous, on {self.device}, an output of its "
+                                     "gradient's shape and dtype")
+            dtypes.append(code)
+        n = len(self.grads)
+        # held, so that the memory behind an unchanged address is the same memory
+        self._storage = [t.untyped_storage() for t in (*self.grads, *outs)]
+        self._addresses = self._ask()
+        self._grads = (ctypes.c_void_p * n)(*self._addresses[:n])
+        self._outs = (ctypes.c_void_p * n)(*self._addresses[-n:]) if n else self._grads
+        self._counts = (ctypes.c_int64 * n)(*(g.numel() for g in self.grads))
+        self._dtypes = (ctypes.c_int * n)(*dtypes)
+        b = ctypes.c_size_t()
+        _check(lib().nm_grad_workspace_size(n, ctypes.byref(b)))
+        self._need = b.value
+
+    def _ask(self):
+        return [t.data_ptr() for t in self.grads] + ([] if self.out is None else [t.data_ptr() for t in self.out])
+
+    def _arrays(self):
+        if self._ask() != self._addresses:
+            self._lay_out()
+        return self._grads, self._counts, self._dtypes, len(self.grads)
+
+
+def nm_grad_list(grads, out=None) -> GradList:
+    """The gradients (float16, bfloat16 or float32, contiguous, mixed as they come) as a list that
+    nm_grad_norm and nm_grad_clip take without checking it again."""
+    return GradList(grads, out)
+
+
+def _grad_workspace(grads):
+    torch = _torch()
+    return torch.empty(grads._need, dtype=torch.uint8, device=grads.device), grads._need
+
+
+def nm_grad_norm(grads):
+    """The norm of all gradients together (a float32 scalar tensor): the square root of the sum of
+    every element's square.  grads: tensors, or a GradList."""
+    torch = _torch()
+    grads = grads if isinstance(grads, GradList) else GradList(grads)
+    arrays = grads._arrays()
+    with _on(grads.device):
+        norm = torch.empty((), dtype=torch.float32, device=grads.device)
+        ws, need = _grad_workspace(grads)
+        _check(lib().nm_grad_norm(*arrays, norm.data_ptr(), ws.data_ptr(), need, _stream_ptr(grads.device)))
+    return norm
+
+
+def nm_grad_clip(grads, max_norm: float, eps: float = 1e-6, out=None):
+    """(norm, outputs): every gradient times min(1, max_norm / (norm + eps)), in place or into `out`
+    (tensors of the gradients' shapes and types); norm as nm_grad_norm gives it.  grads: tensors, or a
+    GradList (which names its outputs itself)."""
+    torch = _torch()
+    if isinstance(grads, GradList):
+        if out is not None:
+            raise ValueError("a GradList names its outputs itself")
+    else:
+        grads = GradList(grads, out)
+    arrays = grads._arrays()
+    with _on(grads.device):
+        norm = torch.empty((), dtype=torch.float32, device=grads.device)
+        ws, need = _grad_workspace(grads)
+        _check(lib().nm_grad_clip(*arrays, max_norm, eps, grads._outs, norm.data_ptr(), ws.data_ptr(), need,
+                                  _stream_ptr(grads.device)))
+    return norm, (grads.grads if grads.out is None else grads.out)

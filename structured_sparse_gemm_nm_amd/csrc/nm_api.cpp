@@ -2,8 +2,10 @@
 //
 // Every check runs on the host before the first HIP call, so argument errors
 // never touch the device and can be tested without a GPU.
-#include <cstdio>
+#include <algorithm>
+#include <cmath>
 #include <cstdarg>
+#include <cstdio>
 #include <map>
 #include <mutex>
 #include <set>
@@ -1260,6 +1262,405 @@ nm_status nm_xent_bwd(const void* x, int64_t T, int64_t H, int64_t ldx, const vo
   a.dw_dtype = dw_dtype;
   a.workspace = workspace;
   return hip_status(nm::launch_xent_bwd(a, static_cast<hipStream_t>(stream)), "nm_xent_bwd launch");
+}
+
+// Shared checks of the products grouped by expert: one expert's packed weight
+// (16-bit), the counts, the output type and the offsets.
+static nm_status check_group(int64_t E, int64_t R, int64_t K, int n, int m, int dtype, int64_t T, int out_dtype) {
+  nm_status st = check_format(R, K, n, m, dtype);
+  if (st != NM_OK) return st;
+  if (dtype != NM_F16 && dtype != NM_BF16) return fail(NM_ERR_UNSUPPORTED, "grouped products take fp16 or bf16 weights");
+  if (out_dtype != NM_F32 && out_dtype != dtype)
+    return fail(NM_ERR_UNSUPPORTED, "out_dtype %d must be NM_F32 or the input dtype", out_dtype);
+  if (E < 1 || E > nm::kGroupMaxExperts)
+    return fail(NM_ERR_SHAPE, "E = %lld out of range [1, %lld]", (long long)E, (long long)nm::kGroupMaxExperts);
+  if (T < 0 || T > nm::kGroupMaxTokens) return fail(NM_ERR_SHAPE, "T = %lld out of range [0, 2^24]", (long long)T);
+  if (R > nm::kGroupMaxWidth || K > nm::kGroupMaxWidth)
+    return fail(NM_ERR_SHAPE, "R = %lld or K = %lld above 2^22", (long long)R, (long long)K);
+  return NM_OK;
+}
+
+// A 16-bit operand's leading dimension: rows on 16 bytes, 128 of them in 32-bit offsets.
+static nm_status check_group_ld(const char* name, int64_t ld, int64_t T, int64_t W) {
+  nm_status st = check_ld(name, ld, T, W);
+  if (st != NM_OK) return st;
+  if (ld >= nm::kGroupMaxLd) return fail(NM_ERR_SHAPE, "%s of 2^23 or more", name);
+  if (ld % 8) return fail(NM_ERR_ALIGN, "%s = %lld is not a multiple of 8", name, (long long)ld);
+  return NM_OK;
+}
+
+static nm_status check_workspace(const void* workspace, size_t have, size_t need) {
+  if (need > 0 && !workspace) return fail(NM_ERR_NULL, "workspace must be non-NULL");
+  if (have < need) return fail(NM_ERR_SHAPE, "workspace of %zu bytes, %zu needed", have, need);
+  if (need > 0 && !aligned16(workspace)) return fail(NM_ERR_ALIGN, "workspace must be 16-byte aligned");
+  return NM_OK;
+}
+
+static nm::SpmmArgs group_base(int64_t R, int64_t K, int n, int m, int dtype, int64_t T, int64_t ldx, int out_dtype) {
+  return adapter_base(R, K, n, m, dtype, T, ldx, out_dtype);
+}
+
+nm_status nm_group_spmm_workspace_size(int64_t E, int64_t R, int64_t K, int n, int m, int dtype, int64_t T,
+                                       int out_dtype, size_t* bytes) {
+  nm_status st = check_group(E, R, K, n, m, dtype, T, out_dtype);
+  if (st != NM_OK) return st;
+  if (!bytes) return fail(NM_ERR_NULL, "bytes must be non-NULL");
+  *bytes = T == 0 || R == 0 ? 0 : nm::group_workspace(group_base(R, K, n, m, dtype, T, K, out_dtype), E);
+  return ok();
+}
+
+nm_status nm_group_spmm(const void* values, const uint32_t* idx, int64_t E, int64_t R, int64_t K, int n, int m,
+                        int dtype, const void* act, int64_t T, int64_t ldx, const int32_t* offsets, void* Y,
+                        int64_t ldy, int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  nm_status st = check_group(E, R, K, n, m, dtype, T, out_dtype);
+  if (st != NM_OK) return st;
+  if ((st = check_group_ld("ldx", ldx, T, K)) != NM_OK || (st = check_ld("ldy", ldy, T, R)) != NM_OK) return st;
+  if (T == 0 || R == 0) return ok();
+  if (!values || !idx || !act || !offsets || !Y)
+    return fail(NM_ERR_NULL, "values, idx, act, offsets and Y must be non-NULL");
+  if (!aligned16(values) || !aligned16(idx) || !aligned16(act) || !aligned16(Y) || !aligned_to(offsets, 4))
+    return fail(NM_ERR_ALIGN, "device pointers must be 16-byte aligned (offsets: 4)");
+  nm::GroupArgs a;
+  a.base = group_base(R, K, n, m, dtype, T, ldx, out_dtype);
+  const size_t need = nm::group_workspace(a.base, E);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
+  const Sizes z = sizes_of(R, K, n, m, dtype);
+  const Span in[] = {{values, size_t(E) * z.values_bytes}, {idx, size_t(E) * z.idx_bytes},
+                     {act, extent(T, K, ldx, 2)}, {offsets, size_t(E + 1) * 4}};
+  const Span out[] = {{Y, extent(T, R, ldy, elt_bytes(out_dtype))}, {workspace, need}};
+  if ((st = check_alias(in, out)) != NM_OK) return st;
+  a.base.values = static_cast<const uint16_t*>(values);
+  a.base.idx = idx;
+  a.base.act = static_cast<const uint16_t*>(act);
+  a.base.Y = Y;
+  a.base.ldy = ldy;
+  a.offsets = offsets;
+  a.E = E;
+  a.workspace = workspace;
+  return hip_status(nm::launch_group(a, static_cast<hipStream_t>(stream)), "nm_group_spmm launch");
+}
+
+nm_status nm_group_spmm_dx_workspace_size(int64_t E, int64_t T, size_t* bytes) {
+  if (E < 1 || E > nm::kGroupMaxExperts || T < 0 || T > nm::kGroupMaxTokens)
+    return fail(NM_ERR_SHAPE, "E = %lld or T = %lld out of range", (long long)E, (long long)T);
+  if (!bytes) return fail(NM_ERR_NULL, "bytes must be non-NULL");
+  *bytes = T == 0 ? 0 : nm::group_dx_workspace(T, E);
+  return ok();
+}
+
+nm_status nm_group_spmm_dx(const void* values, const uint32_t* idx, int64_t E, int64_t R, int64_t K, int n, int m,
+                           int dtype, const void* G, int64_t T, int64_t ldg, const int32_t* offsets, void* dX,
+                           int64_t lddx, int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  nm_status st = check_group(E, R, K, n, m, dtype, T, out_dtype);
+  if (st != NM_OK) return st;
+  if ((st = check_train(R, K, n, m, dtype, T, ldg, out_dtype)) != NM_OK) return st;
+  if ((st = check_group_ld("ldg", ldg, T, R)) != NM_OK || (st = check_ld("lddx", lddx, T, K)) != NM_OK) return st;
+  if (T == 0) return ok();
+  if (!offsets || !dX || (R > 0 && (!values || !idx || !G)))
+    return fail(NM_ERR_NULL, "values, idx, G, offsets and dX must be non-NULL");
+  if (!aligned16(values) || !aligned16(idx) || !aligned16(G) || !aligned16(dX) || !aligned_to(offsets, 4))
+    return fail(NM_ERR_ALIGN, "device pointers must be 16-byte aligned (offsets: 4)");
+  const size_t need = nm::group_dx_workspace(T, E);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
+  const Sizes z = sizes_of(R, K, n, m, dtype);
+  if (z.values_bytes >= (size_t(1) << 32) || z.idx_bytes >= (size_t(1) << 32))
+    return fail(NM_ERR_SHAPE, "one expert's packed W of 4 GiB or more");
+  const Span in[] = {{values, size_t(E) * z.values_bytes}, {idx, size_t(E) * z.idx_bytes},
+                     {G, extent(T, R, ldg, 2)}, {offsets, size_t(E + 1) * 4}};
+  const Span out[] = {{dX, extent(T, K, lddx, elt_bytes(out_dtype))}, {workspace, need}};
+  if ((st = check_alias(in, out)) != NM_OK) return st;
+  nm::TrainArgs a{};
+  a.values = static_cast<const uint16_t*>(values);
+  a.values_bytes = z.values_bytes;
+  a.idx = idx;
+  a.idx_bytes = z.idx_bytes;
+  a.R = R;
+  a.K = K;
+  a.n = n;
+  a.m = m;
+  a.dtype = dtype;
+  a.idx_row_words = z.words;
+  a.G = static_cast<const uint16_t*>(G);
+  a.T = T;
+  a.ldg = ldg;
+  a.out = dX;
+  a.ldo = lddx;
+  a.out_dtype = out_dtype;
+  a.offsets = offsets;
+  a.experts = E;
+  a.table = workspace;
+  return hip_status(nm::launch_spmm_dx(a, static_cast<hipStream_t>(stream)), "nm_group_spmm_dx launch");
+}
+
+nm_status nm_group_spmm_dw(const uint32_t* idx, int64_t E, int64_t R, int64_t K, int n, int m, int dtype, const void* G,
+                           int64_t T, int64_t ldg, const void* act, int64_t ldx, const int32_t* offsets, void* dW,
+                           int out_dtype, void* stream) {
+  nm_status st = check_group(E, R, K, n, m, dtype, T, out_dtype);
+  if (st != NM_OK) return st;
+  if ((st = check_train(R, K, n, m, dtype, T, ldg, out_dtype)) != NM_OK) return st;
+  if ((st = check_group_ld("ldg", ldg, T, R)) != NM_OK || (st = check_group_ld("ldx", ldx, T, K)) != NM_OK) return st;
+  if (R == 0) return ok();
+  if (!idx || !offsets || !dW || (T > 0 && (!G || !act)))
+    return fail(NM_ERR_NULL, "idx, G, act, offsets and dW must be non-NULL");
+  if (!aligned16(idx) || !aligned16(G) || !aligned16(act) || !aligned16(dW) || !aligned_to(offsets, 4))
+    return fail(NM_ERR_ALIGN, "device pointers must be 16-byte aligned (offsets: 4)");
+  if (T * ldg * 2 >= (int64_t(1) << 32) || T * ldx * 2 >= (int64_t(1) << 32))
+    return fail(NM_ERR_SHAPE, "G or act of 4 GiB or more");
+  const Sizes z = sizes_of(R, K, n, m, dtype);
+  if (z.idx_bytes >= (size_t(1) << 32)) return fail(NM_ERR_SHAPE, "one expert's index words of 4 GiB or more");
+  const Span in[] = {{idx, size_t(E) * z.idx_bytes}, {G, extent(T, R, ldg, 2)}, {act, extent(T, K, ldx, 2)},
+                     {offsets, size_t(E + 1) * 4}};
+  const Span out[] = {{dW, size_t(E) * size_t(R) * size_t(z.S) * elt_bytes(out_dtype)}};
+  if ((st = check_alias(in, out)) != NM_OK) return st;
+  nm::TrainArgs a{};
+  a.idx = idx;
+  a.idx_bytes = z.idx_bytes;
+  a.R = R;
+  a.K = K;
+  a.n = n;
+  a.m = m;
+  a.dtype = dtype;
+  a.idx_row_words = z.words;
+  a.G = static_cast<const uint16_t*>(G);
+  a.T = T;
+  a.ldg = ldg;
+  a.act = static_cast<const uint16_t*>(act);
+  a.ldx = ldx;
+  a.out = dW;
+  a.out_dtype = out_dtype;
+  a.offsets = offsets;
+  a.experts = E;
+  return hip_status(nm::launch_spmm_dw(a, static_cast<hipStream_t>(stream)), "nm_group_spmm_dw launch");
+}
+
+// Shared checks of the 4-bit format: rows and columns of a quantised matrix.
+static nm_status check_mx(const char* rows_name, int64_t rows, int64_t K) {
+  if (rows < 0 || rows > nm::kMxMaxRows)
+    return fail(NM_ERR_SHAPE, "%s = %lld out of range [0, 2^24]", rows_name, (long long)rows);
+  if (K < 32 || K > nm::kGroupMaxWidth || K % 32)
+    return fail(NM_ERR_SHAPE, "K = %lld is not a multiple of 32 in [32, 2^22]", (long long)K);
+  return NM_OK;
+}
+
+static nm_status check_mx_float(int dtype) {
+  if (dtype != NM_F16 && dtype != NM_BF16 && dtype != NM_F32)
+    return fail(NM_ERR_UNSUPPORTED, "dtype %d is not NM_F16, NM_BF16 or NM_F32", dtype);
+  return NM_OK;
+}
+
+static size_t mx_scale_bytes(int64_t rows, int64_t K) { return size_t((K + 255) / 256) * size_t(rows) * 8; }
+
+nm_status nm_mx_sizes(int64_t T, int64_t K, size_t* q_bytes, size_t* scale_bytes) {
+  nm_status st = check_mx("T", T, K);
+  if (st != NM_OK) return st;
+  if (q_bytes) *q_bytes = size_t(T) * size_t(K / 2);
+  if (scale_bytes) *scale_bytes = mx_scale_bytes(T, K);
+  return ok();
+}
+
+nm_status nm_mx_quantize(const void* x, int64_t T, int64_t K, int64_t ldx, int dtype, uint8_t* q, uint8_t* scale,
+                         void* stream) {
+  nm_status st = check_mx("T", T, K);
+  if (st != NM_OK || (st = check_mx_float(dtype)) != NM_OK || (st = check_ld("ldx", ldx, T, K)) != NM_OK) return st;
+  if (T == 0) return ok();
+  if (!x || !q || !scale) return fail(NM_ERR_NULL, "x, q and scale must be non-NULL");
+  const size_t e = elt_bytes(dtype);
+  if (!aligned_to(x, e) || !aligned16(q) || !aligned16(scale))
+    return fail(NM_ERR_ALIGN, "q and scale must be 16-byte aligned, x to its element");
+  const Span in[] = {{x, extent(T, K, ldx, e)}};
+  const Span out[] = {{q, size_t(T) * size_t(K / 2)}, {scale, mx_scale_bytes(T, K)}};
+  if ((st = check_alias(in, out)) != NM_OK) return st;
+  nm::MxQuantArgs a;
+  a.T = T;
+  a.K = K;
+  a.ldx = ldx;
+  a.dtype = dtype;
+  a.x = x;
+  a.q = q;
+  a.scale = scale;
+  return hip_status(nm::launch_mx_quantize(a, static_cast<hipStream_t>(stream)), "nm_mx_quantize launch");
+}
+
+nm_status nm_mx_dequantize(const uint8_t* q, const uint8_t* scale, int64_t T, int64_t K, void* y, int64_t ldy,
+                           int dtype, void* stream) {
+  nm_status st = check_mx("T", T, K);
+  if (st != NM_OK || (st = check_mx_float(dtype)) != NM_OK || (st = check_ld("ldy", ldy, T, K)) != NM_OK) return st;
+  if (T == 0) return ok();
+  if (!y || !q || !scale) return fail(NM_ERR_NULL, "q, scale and y must be non-NULL");
+  const size_t e = elt_bytes(dtype);
+  if (!aligned_to(y, e) || !aligned16(q) || !aligned16(scale))
+    return fail(NM_ERR_ALIGN, "q and scale must be 16-byte aligned, y to its element");
+  const Span in[] = {{q, size_t(T) * size_t(K / 2)}, {scale, mx_scale_bytes(T, K)}};
+  const Span out[] = {{y, extent(T, K, ldy, e)}};
+  if ((st = check_alias(in, out)) != NM_OK) return st;
+  nm::MxQuantArgs a;
+  a.T = T;
+  a.K = K;
+  a.ldx = ldy;
+  a.dtype = dtype;
+  a.q = const_cast<uint8_t*>(q);
+  a.scale = const_cast<uint8_t*>(scale);
+  a.y = y;
+  return hip_status(nm::launch_mx_dequantize(a, static_cast<hipStream_t>(stream)), "nm_mx_dequantize launch");
+}
+
+static nm_status check_mx_gemm(int64_t E, int64_t R, int64_t K, int64_t T, bool grouped, int out_dtype) {
+  nm_status st = check_mx("R", R, K);
+  if (st != NM_OK || (st = check_mx("T", T, K)) != NM_OK || (st = check_mx_float(out_dtype)) != NM_OK) return st;
+  if (R > nm::kGroupMaxWidth) return fail(NM_ERR_SHAPE, "R = %lld above 2^22", (long long)R);
+  if (E < 1 || E > nm::kGroupMaxExperts || (!grouped && E != 1))
+    return fail(NM_ERR_SHAPE, "E = %lld out of range (1 without offsets, else [1, %lld])", (long long)E,
+                (long long)nm::kGroupMaxExperts);
+  // 32-bit offsets into one operand's scales
+  if (mx_scale_bytes(R, K) >= (size_t(1) << 32) || mx_scale_bytes(T, K) >= (size_t(1) << 32))
+    return fail(NM_ERR_SHAPE, "scales of 4 GiB or more");
+  return NM_OK;
+}
+
+nm_status nm_mx_gemm_workspace_size(int64_t E, int64_t R, int64_t K, int64_t T, int grouped, int out_dtype,
+                                    size_t* bytes) {
+  nm_status st = check_mx_gemm(E, R, K, T, grouped != 0, out_dtype);
+  if (st != NM_OK) return st;
+  if (!bytes) return fail(NM_ERR_NULL, "bytes must be non-NULL");
+  *bytes = T == 0 || R == 0 ? 0 : nm::mx_workspace(E, R, K, T, grouped != 0);
+  return ok();
+}
+
+nm_status nm_mx_gemm(const uint8_t* wq, const uint8_t* wscale, int64_t E, int64_t R, int64_t K, const uint8_t* xq,
+                     const uint8_t* xscale, int64_t T, const int32_t* offsets, void* Y, int64_t ldy, int out_dtype,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  nm_status st = check_mx_gemm(E, R, K, T, offsets != nullptr, out_dtype);
+  if (st != NM_OK || (st = check_ld("ldy", ldy, T, R)) != NM_OK) return st;
+  if (T == 0 || R == 0) return ok();
+  if (!wq || !wscale || !xq || !xscale || !Y)
+    return fail(NM_ERR_NULL, "wq, wscale, xq, xscale and Y must be non-NULL");
+  if (!aligned16(wq) || !aligned16(wscale) || !aligned16(xq) || !aligned16(xscale) || !aligned16(Y) ||
+      !aligned_to(offsets, 4))
+    return fail(NM_ERR_ALIGN, "device pointers must be 16-byte aligned (offsets: 4)");
+  const size_t need = nm::mx_workspace(E, R, K, T, offsets != nullptr);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
+  const Span in[] = {{wq, size_t(E) * size_t(R) * size_t(K / 2)}, {wscale, size_t(E) * mx_scale_bytes(R, K)},
+                     {xq, size_t(T) * size_t(K / 2)}, {xscale, mx_scale_bytes(T, K)},
+                     {offsets, offsets ? size_t(E + 1) * 4 : 0}};
+  const Span out[] = {{Y, extent(T, R, ldy, elt_bytes(out_dtype))}, {workspace, need}};
+  if ((st = check_alias(in, out)) != NM_OK) return st;
+  nm::MxArgs a;
+  a.wq = wq;
+  a.ws = wscale;
+  a.xq = xq;
+  a.xs = xscale;
+  a.offsets = offsets;
+  a.E = E;
+  a.R = R;
+  a.K = K;
+  a.T = T;
+  a.ldy = ldy;
+  a.Y = Y;
+  a.out_dtype = out_dtype;
+  a.workspace = workspace;
+  return hip_status(nm::launch_mx_gemm(a, static_cast<hipStream_t>(stream)), "nm_mx_gemm launch");
+}
+
+nm_status nm_grad_workspace_size(int64_t tensors, size_t* bytes) {
+  if (tensors < 0 || tensors > nm::kGradMaxTensors)
+    return fail(NM_ERR_SHAPE, "tensors = %lld out of range [0, %lld]", (long long)tensors,
+                (long long)nm::kGradMaxTensors);
+  if (!bytes) return fail(NM_ERR_NULL, "bytes must be non-NULL");
+  *bytes = nm::grad_workspace(tensors);
+  return ok();
+}
+
+// A written range and the tensor it belongs to.
+struct Written {
+  uintptr_t begin, end;
+  int32_t tensor;
+};
+
+// The lists of a norm (out NULL) or a clipping: their types and counts, and that
+// nothing written overlaps anything else, but for a tensor scaled in place.
+static nm_status check_grads(const void* const* grads, const int64_t* counts, const int* dtypes, int64_t tensors,
+                             void* const* out, const float* norm, const void* workspace, size_t workspace_bytes) {
+  if (tensors < 0 || tensors > nm::kGradMaxTensors)
+    return fail(NM_ERR_SHAPE, "tensors = %lld out of range [0, %lld]", (long long)tensors,
+                (long long)nm::kGradMaxTensors);
+  if (!norm || (tensors > 0 && (!grads || !counts || !dtypes)))
+    return fail(NM_ERR_NULL, "grads, counts, dtypes and norm must be non-NULL");
+  nm_status st = check_workspace(workspace, workspace_bytes, nm::grad_workspace(tensors));
+  if (st != NM_OK) return st;
+  if (!aligned_to(norm, 4)) return fail(NM_ERR_ALIGN, "norm must be 4-byte aligned");
+  Written w[nm::kGradMaxTensors + 2];   // 400 KB of the caller's stack
+  int64_t written = 0;
+  auto add = [&](const void* p, size_t bytes, int32_t tensor) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+    w[written++] = Written{b, b + bytes, tensor};
+  };
+  add(norm, 4, -1);
+  add(workspace, nm::grad_workspace(tensors), -1);
+  for (int64_t i = 0; i < tensors; ++i) {
+    if (dtypes[i] != NM_F16 && dtypes[i] != NM_BF16 && dtypes[i] != NM_F32)
+      return fail(NM_ERR_UNSUPPORTED, "tensor %lld: dtype %d is not NM_F16, NM_BF16 or NM_F32", (long long)i, dtypes[i]);
+    if (counts[i] < 0 || counts[i] > nm::kGradMaxCount)
+      return fail(NM_ERR_SHAPE, "tensor %lld: count %lld out of range [0, 2^36]", (long long)i, (long long)counts[i]);
+    if (counts[i] == 0) continue;
+    const size_t e = elt_bytes(dtypes[i]);
+    if (!grads[i] || (out && !out[i])) return fail(NM_ERR_NULL, "tensor %lld is NULL", (long long)i);
+    if (!aligned_to(grads[i], e) || (out && !aligned_to(out[i], e)))
+      return fail(NM_ERR_ALIGN, "tensor %lld is not aligned to its element", (long long)i);
+    if (out) add(out[i], size_t(counts[i]) * e, int32_t(i));
+  }
+  auto before = [](const Written& a, const Written& b) { return a.begin < b.begin; };
+  if (!std::is_sorted(w, w + written, before)) std::sort(w, w + written, before);
+  for (int64_t i = 1; i < written; ++i)
+    if (w[i].begin < w[i - 1].end) return fail(NM_ERR_ALIAS, "outputs, norm or workspace overlap each other");
+  for (int64_t i = 0; i < tensors; ++i) {
+    if (counts[i] == 0) continue;
+    const uintptr_t b = reinterpret_cast<uintptr_t>(grads[i]), end = b + size_t(counts[i]) * elt_bytes(dtypes[i]);
+    // the written ranges do not overlap, so the last one that begins before `end` decides
+    const Written* p = std::lower_bound(w, w + written, Written{end, 0, 0}, before);
+    if (p == w) continue;
+    --p;
+    if (p->end > b && !(p->tensor == int32_t(i) && p->begin == b))
+      return fail(NM_ERR_ALIAS, "tensor %lld overlaps an output of another, norm or workspace", (long long)i);
+  }
+  return NM_OK;
+}
+
+nm_status nm_grad_norm(const void* const* grads, const int64_t* counts, const int* dtypes, int64_t tensors, float* norm,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  nm_status st = check_grads(grads, counts, dtypes, tensors, nullptr, norm, workspace, workspace_bytes);
+  if (st != NM_OK) return st;
+  nm::GradArgs a;
+  a.grads = grads;
+  a.counts = counts;
+  a.dtypes = dtypes;
+  a.tensors = tensors;
+  a.norm = norm;
+  a.workspace = workspace;
+  return hip_status(nm::launch_grad(a, static_cast<hipStream_t>(stream)), "nm_grad_norm launch");
+}
+
+nm_status nm_grad_clip(const void* const* grads, const int64_t* counts, const int* dtypes, int64_t tensors,
+                       double max_norm, double eps, void* const* out, float* norm, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (!(max_norm >= 0.0) || !(eps >= 0.0) || std::isinf(eps))
+    return fail(NM_ERR_SHAPE, "max_norm = %g or eps = %g is negative or not a number", max_norm, eps);
+  if (tensors > 0 && !out) return fail(NM_ERR_NULL, "out must be non-NULL (grads for in place)");
+  nm_status st = check_grads(grads, counts, dtypes, tensors, out, norm, workspace, workspace_bytes);
+  if (st != NM_OK) return st;
+  nm::GradArgs a;
+  a.grads = grads;
+  a.out = out;
+  a.counts = counts;
+  a.dtypes = dtypes;
+  a.tensors = tensors;
+  a.clip = true;
+  a.in_place = true;
+  for (int64_t i = 0; i < tensors && a.in_place; ++i) a.in_place = counts[i] == 0 || out[i] == grads[i];
+  a.max_norm = max_norm;
+  a.eps = eps;
+  a.norm = norm;
+  a.workspace = workspace;
+  return hip_status(nm::launch_grad(a, static_cast<hipStream_t>(stream)), "nm_grad_clip launch");
 }
 
 }  // extern "C"

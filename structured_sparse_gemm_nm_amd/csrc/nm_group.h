@@ -1,0 +1,63 @@
+// Token tiles of rows ordered by expert: expert e owns rows offsets[e] ..
+// offsets[e+1]-1 of T, and each expert's rows are cut into tiles of BT tokens of
+// their own.  The offsets lie on the device, so the host knows only how many
+// tiles there can be; which they are is found on the device, by every workgroup
+// for itself (group_find: a few dependent loads, for kernels that are over in
+// microseconds) or once for all by group_tiles_kernel (kernels whose workgroups
+// walk many tiles).
+//
+// Offsets that do not ascend or leave [0, T] are clamped one by one
+// (nm_offsets.h), so no access leaves the arrays, whatever they hold.
+#pragma once
+
+#include "nm_device.h"
+#include "nm_offsets.h"
+
+namespace nm {
+
+// A tile's expert and its first token and the end of the expert's rows.
+struct GroupTile {
+  int e, t0, t1;
+};
+
+__device__ inline void group_range(const int32_t* __restrict__ offsets, int e, int T, int& lo, int& hi) {
+  lo = rows_lo(offsets[e], T);
+  hi = rows_hi(offsets[e + 1], lo, T);
+}
+
+// Tile number `tile` by the whole wave (64 experts at a time); false past the last.
+__device__ inline bool group_find(const int32_t* __restrict__ offsets, int E, int T, int BT, int tile, GroupTile& g) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    int lo = 0, hi = 0;
+    if (e0 + lane < E) group_range(offsets, e0 + lane, T, lo, hi);
+    const int tiles = (hi - lo + BT - 1) / BT;
+    int sum = tiles;   // inclusive prefix
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int up = __shfl_up(sum, o, 64);
+      if (lane >= o) sum = tile_sum(sum, up);
+    }
+    const uint64_t past = __ballot(before + sum > tile);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      const int start = before + (at > 0 ? __builtin_amdgcn_readlane(sum, at - 1) : 0);
+      g.e = e0 + at;
+      g.t0 = __builtin_amdgcn_readlane(lo, at) + (tile - start) * BT;
+      g.t1 = __builtin_amdgcn_readlane(hi, at);
+      return true;
+    }
+    before = tile_sum(before, __builtin_amdgcn_readlane(sum, 63));
+  }
+  return false;
+}
+
+// The tiles as a table in a workspace: its size, and the launch that fills it
+// (nm_group.hip).  Entry 0 holds the count, entries 1 .. count the tiles (e, t0,
+// t1, 0); at most max_tiles of them.
+inline size_t group_table_bytes(int64_t max_tiles) { return size_t(max_tiles + 1) * 16; }
+hipError_t launch_group_tiles(const int32_t* offsets, int64_t E, int64_t T, int BT, int64_t max_tiles, int4* table,
+                              hipStream_t s);
+
+}  // namespace nm

@@ -1,0 +1,416 @@
+// Products of packed N:M weights grouped by expert: Y[t] = W_e act[t] for the rows
+// t of expert e, rows ordered by expert (nm_group.h).  Operand layouts and the
+// widening of 1:4 and 1:8 rows to the 2:4 operand are those of nm_spmm.hip.
+#include "nm_group.h"
+
+#include "nm_internal.h"
+#include "nm_widen.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace nm {
+namespace {
+
+// ---------------------------------------------------------------------------
+// The table of token tiles (nm_group.h), by one workgroup: a prefix sum of the
+// experts' tile counts, 1024 experts at a time, then every thread looks up the
+// expert of its share of the tiles.
+// ---------------------------------------------------------------------------
+constexpr int kTableThreads = 1024;
+
+__global__ __launch_bounds__(kTableThreads) void group_tiles_kernel(const int32_t* __restrict__ offsets, int E, int T,
+                                                                    int BT, int max_tiles, int4* __restrict__ table) {
+  __shared__ int start[kTableThreads + 1], wsum[kTableThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int before = 0;
+  for (int e0 = 0; e0 < E; e0 += kTableThreads) {
+    int lo = 0, hi = 0;
+    if (e0 + tid < E) group_range(offsets, e0 + tid, T, lo, hi);
+    const int tiles = (hi - lo + BT - 1) / BT;
+    int sum = tiles;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int up = __shfl_up(sum, o, 64);
+      if (lane >= o) sum = tile_sum(sum, up);
+    }
+    if (lane == 63) wsum[wave] = sum;
+    __syncthreads();
+    int base = before;
+    for (int w = 0; w < wave; ++w) base = tile_sum(base, wsum[w]);
+    const int up = __shfl_up(sum, 1, 64);
+    start[tid] = tile_sum(base, lane > 0 ? up : 0);
+    if (tid == kTableThreads - 1) start[kTableThreads] = tile_sum(base, sum);
+    __syncthreads();
+    const int end = min(start[kTableThreads], max_tiles);
+    for (int i = before + tid; i < end; i += kTableThreads) {
+      int a = 0, b = kTableThreads;   // the last expert that starts at or before tile i
+      while (b - a > 1) {
+        const int m = (a + b) >> 1;
+        if (start[m] <= i) a = m;
+        else b = m;
+      }
+      int l, h;
+      group_range(offsets, e0 + a, T, l, h);
+      table[1 + i] = make_int4(e0 + a, l + (i - start[a]) * BT, h, 0);
+    }
+    before = start[kTableThreads];
+    __syncthreads();
+  }
+  if (tid == 0) table[0] = make_int4(min(before, max_tiles), 0, 0, 0);
+}
+
+struct GroupDims {
+  int E, R, K, T, words, tilesR;
+  int64_t ldx, ldy;
+};
+
+template <int DT, int OUT>
+__device__ inline void store4(void* Y, int64_t o, bool whole, int left, const f32x4& v) {
+  if constexpr (OUT == NM_F32) {
+    float* y = static_cast<float*>(Y) + o;
+    if (whole) *reinterpret_cast<f32x4*>(y) = v;
+    else for (int e = 0; e < 4 && e < left; ++e) y[e] = v[e];
+  } else {
+    uint16_t* y = static_cast<uint16_t*>(Y) + o;
+    const u32x2 h = {pack_half2<DT>(v[0], v[1]), pack_half2<DT>(v[2], v[3])};
+    if (whole) *reinterpret_cast<u32x2*>(y) = h;
+    else for (int e = 0; e < 4 && e < left; ++e) y[e] = uint16_t(h[e >> 1] >> (16 * (e & 1)));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows an expert: bound by streaming the packed weights of the experts that
+// have any.  A workgroup of 8 waves owns 16 rows of one expert's weight and up to
+// 16 NT of its tokens; the waves take contiguous shares of K, issue the loads of
+// U steps before multiplying them, and the partial tiles are added in wave order.
+// ---------------------------------------------------------------------------
+constexpr int kFewWaves = 8;
+
+template <int P, int DT, int OUT, int NT>
+__global__ __launch_bounds__(kFewWaves * 64) void group_few_kernel(const uint16_t* __restrict__ values,
+                                                                   const uint32_t* __restrict__ idx,
+                                                                   const uint16_t* __restrict__ act,
+                                                                   const int32_t* __restrict__ offsets, GroupDims d,
+                                                                   void* __restrict__ Y) {
+  __shared__ f32x4 part[kFewWaves][NT][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 15, lq = lane >> 4;
+  const int tile = blockIdx.x / d.tilesR;
+  const int r0 = (blockIdx.x - tile * d.tilesR) * 16;
+  GroupTile g;
+  if (!group_find(offsets, d.E, d.T, 16 * NT, tile, g)) return;
+  const int64_t S = int64_t(d.K) / pat_m(P) * pat_n(P);
+  values += int64_t(g.e) * d.R * S;
+  idx += int64_t(g.e) * d.R * d.words;
+  const uint16_t* x = act + int64_t(g.t0) * d.ldx;
+  const int toks = min(16 * NT, g.t1 - g.t0);
+  const int steps = (d.K + 63) >> 6;
+  const int share = (steps + kFewWaves - 1) / kFewWaves;
+  const int s_end = min(steps, (wave + 1) * share);
+
+  f32x4 acc[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  constexpr int U = NT == 1 ? 8 : NT == 2 ? 4 : 2;
+  for (int s0 = wave * share; s0 < s_end; s0 += U) {
+    AFrag a[U];
+    u32x8 b[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int s = s0 + u;
+      load_afrag<P>(a[u], values, idx, S, d.words, s < s_end ? r0 + li : d.R, d.R, d.K, s, lq);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int t = j * 16 + li;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = s * 64 + h * 32 + lq * 8;
+          u32x4 v = {0u, 0u, 0u, 0u};
+          if (s < s_end && t < toks && k < d.K) v = *reinterpret_cast<const u32x4*>(x + int64_t(t) * d.ldx + k);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) b[u][j][4 * h + e] = v[e];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      u32x4 w;
+      uint32_t ix;
+      widen<P>(a[u], w, ix);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[j] = smfmac<DT>(w, b[u][j], acc[j], ix);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j) part[wave][j][lane] = acc[j];
+  __syncthreads();
+  if (wave >= NT) return;
+  f32x4 sum = part[0][wave][lane];
+#pragma unroll
+  for (int w = 1; w < kFewWaves; ++w) sum += part[w][wave][lane];
+  const int t = wave * 16 + li, r = r0 + lq * 4;
+  if (t >= toks || r >= d.R) return;
+  store4<DT, OUT>(Y, int64_t(g.t0 + t) * d.ldy + r, (d.ldy & 3) == 0 && r + 3 < d.R, d.R - r, sum);
+}
+
+// ---------------------------------------------------------------------------
+// Any shape: 128 rows x BT tokens by 4 waves (2 x 2), K in steps of 64.  Each
+// thread loads its share of a step two steps ahead into registers (zeros past the
+// edges of W, of K and of the expert's rows), widens it to the 2:4 operand, and
+// writes it to a double-buffered stage in LDS, so every pattern runs the same
+// products.  One barrier a step publishes one stage and retires the other.
+// ---------------------------------------------------------------------------
+constexpr int kBR = 128;
+constexpr int kStageA = kBR * 64, kStageI = kBR * 8;
+constexpr uint32_t kDeadOff = 0xFFFFFFF0u;   // no descriptor covers it: reads zeros
+
+template <int P, int DT, int OUT, int BT>
+__global__ __launch_bounds__(256, 2) void group_tile_kernel(const uint16_t* __restrict__ values,
+                                                            const uint32_t* __restrict__ idx,
+                                                            const uint16_t* __restrict__ act,
+                                                            const int4* __restrict__ table, GroupDims d,
+                                                            void* __restrict__ Y) {
+  constexpr int FR = 4, FT = BT / 32;
+  constexpr int kStageB = BT * 128, kStage = kStageA + kStageI + kStageB;
+  constexpr int PB = BT / 32;   // 16-byte pieces of the tokens a thread loads a step
+  __shared__ __align__(16) unsigned char smem[2 * kStage];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 15, lq = lane >> 4;
+  const int wr = wave >> 1, wt = wave & 1;
+  const int ntiles = table[0].x;
+  const int b0 = blockIdx.x;
+  const int tt = b0 / d.tilesR, tr = b0 - tt * d.tilesR;
+  if (tt >= ntiles) return;
+  const int4 g = table[1 + tt];
+  const int r0 = tr * kBR;
+  const int rows = min(kBR, d.R - r0), toks = min(BT, g.z - g.y);
+  const int64_t S = int64_t(d.K) / pat_m(P) * pat_n(P);
+  const __amdgpu_buffer_rsrc_t rv = make_rsrc(values + (int64_t(g.x) * d.R + r0) * S, uint32_t(rows * S * 2));
+  const __amdgpu_buffer_rsrc_t ri =
+      make_rsrc(idx + (int64_t(g.x) * d.R + r0) * d.words, uint32_t(int64_t(rows) * d.words * 4));
+  const __amdgpu_buffer_rsrc_t rx =
+      make_rsrc(act + int64_t(g.y) * d.ldx, uint32_t((int64_t(toks - 1) * d.ldx + d.K) * 2));
+  const int steps = (d.K + 63) >> 6;
+
+  // this thread's share of W: 32 columns (half wh of the step) of row wrow
+  const int wrow = tid >> 1, wh = tid & 1;
+  constexpr int VB = P == 0 ? 32 : P == 1 ? 16 : 8;   // bytes of values of 32 columns
+  struct Share {
+    uint32_t v[VB / 4];
+    uint32_t w0, w1;
+    u32x4 x[PB];
+  };
+  const uint32_t vbase = uint32_t(wrow * S * 2), ibase = uint32_t(wrow * d.words * 4);
+  uint32_t xoff[PB];
+  int xcol[PB];
+#pragma unroll
+  for (int j = 0; j < PB; ++j) {
+    const int slot = j * 256 + tid, tok = slot >> 3, c = (slot & 7) ^ (tok & 7);
+    xoff[j] = tok < toks ? uint32_t(tok) * uint32_t(d.ldx) * 2u + uint32_t(c) * 16u : kDeadOff;
+    xcol[j] = c * 8;
+  }
+  auto load = [&](int s, Share& o) {
+    const int k = s * 64 + wh * 32;
+    const bool on = s < steps && wrow < rows && k < d.K, on2 = on && k + 16 < d.K;
+    const uint32_t v0 = vbase + uint32_t(s * 2 + wh) * VB;
+    if constexpr (P == 0) {
+      const u32x4 a = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rv, on ? v0 : kDeadOff, 0, 0));
+      const u32x4 b =
+          __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rv, on2 ? v0 + 16u : kDeadOff, 0, 0));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o.v[e] = a[e], o.v[4 + e] = b[e];
+      o.w0 = __builtin_amdgcn_raw_buffer_load_b32(ri, on ? ibase + uint32_t(s * 2 + wh) * 4u : kDeadOff, 0, 0);
+    } else if constexpr (P == 1) {
+      const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rv, on ? v0 : kDeadOff, 0, 0));
+      const u32x2 b =
+          __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rv, on2 ? v0 + 8u : kDeadOff, 0, 0));
+      o.v[0] = a[0], o.v[1] = a[1], o.v[2] = b[0], o.v[3] = b[1];
+      o.w0 = __builtin_amdgcn_raw_buffer_load_b32(ri, on ? ibase + uint32_t(s) * 4u : kDeadOff, 0, 0);
+    } else {
+      o.v[0] = __builtin_amdgcn_raw_buffer_load_b32(rv, on ? v0 : kDeadOff, 0, 0);
+      o.v[1] = __builtin_amdgcn_raw_buffer_load_b32(rv, on2 ? v0 + 4u : kDeadOff, 0, 0);
+      const int bit = 24 * s + 12 * wh, w = bit >> 5;
+      o.w0 = __builtin_amdgcn_raw_buffer_load_b32(ri, on ? ibase + uint32_t(w) * 4u : kDeadOff, 0, 0);
+      // (the row's last word holds every bit it needs: the next one is not looked at)
+      o.w1 = __builtin_amdgcn_raw_buffer_load_b32(ri, on ? ibase + uint32_t(min(w + 1, d.words - 1)) * 4u : kDeadOff, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < PB; ++j) {
+      const bool live = s < steps && s * 64 + xcol[j] < d.K && xoff[j] != kDeadOff;
+      o.x[j] = __builtin_bit_cast(
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, live ? xoff[j] + uint32_t(s) * 128u : kDeadOff, 0, 0));
+    }
+  };
+  auto stage = [&](int s, const Share& o) {
+    unsigned char* st = smem + (s & 1) * kStage;
+    uint32_t v[8], ix;
+    if constexpr (P == 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = o.v[e];
+      ix = o.w0;
+    } else if constexpr (P == 1) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (o.v[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+      uint32_t y = (o.w0 >> (16 * wh)) & 0xFFFFu;   // eight 2-bit positions, each to a nibble p | p << 2
+      y = (y | (y << 8)) & 0x00FF00FFu;
+      y = (y | (y << 4)) & 0x0F0F0F0Fu;
+      y = (y | (y << 2)) & 0x33333333u;
+      ix = y * 5u;
+    } else {
+      const uint32_t bits = uint32_t((uint64_t(o.w0) | uint64_t(o.w1) << 32) >> ((24 * s + 12 * wh) & 31));
+      ix = 0u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t h = (o.v[e >> 1] >> (16 * (e & 1))) & 0xFFFFu, p = (bits >> (3 * e)) & 7u;
+        v[2 * e] = p < 4u ? h : 0u;
+        v[2 * e + 1] = p < 4u ? 0u : h;
+        ix |= ((p & 3u) * 5u) << (8 * e + (p < 4u ? 0 : 4));
+      }
+    }
+    const int sw = (wrow >> 1) & 3;
+    *reinterpret_cast<u32x4*>(st + (wrow * 4 + ((2 * wh) ^ sw)) * 16) = u32x4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<u32x4*>(st + (wrow * 4 + ((2 * wh + 1) ^ sw)) * 16) = u32x4{v[4], v[5], v[6], v[7]};
+    *reinterpret_cast<uint32_t*>(st + kStageA + wrow * 8 + wh * 4) = ix;
+#pragma unroll
+    for (int j = 0; j < PB; ++j) *reinterpret_cast<u32x4*>(st + kStageA + kStageI + (j * 256 + tid) * 16) = o.x[j];
+  };
+
+  f32x4 acc[FR][FT];
+#pragma unroll
+  for (int i = 0; i < FR; ++i)
+#pragma unroll
+    for (int j = 0; j < FT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  Share sh[2];
+  load(0, sh[0]);
+  load(1, sh[1]);
+  stage(0, sh[0]);
+  load(2, sh[0]);
+  auto step = [&](auto par_c, int s) {
+    constexpr int PAR = decltype(par_c)::value;
+    wait_lgkm0();
+    barrier_no_fence();
+    const unsigned char* st = smem + PAR * kStage;
+    u32x4 a[FR];
+    uint32_t ix[FR];
+    u32x8 b[FT];
+#pragma unroll
+    for (int i = 0; i < FR; ++i) {
+      const int row = wr * 64 + i * 16 + li;
+      a[i] = *reinterpret_cast<const u32x4*>(st + (row * 4 + (lq ^ ((row >> 1) & 3))) * 16);
+      ix[i] = *reinterpret_cast<const uint16_t*>(st + kStageA + row * 8 + lq * 2);
+    }
+#pragma unroll
+    for (int j = 0; j < FT; ++j) {
+      const int tok = wt * (BT / 2) + j * 16 + li;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(st + kStageA + kStageI + (tok * 8 + ((lq + 4 * h) ^ (tok & 7))) * 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[j][4 * h + e] = v[e];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < FR; ++i)
+#pragma unroll
+      for (int j = 0; j < FT; ++j) acc[i][j] = smfmac<DT>(a[i], b[j], acc[i][j], ix[i]);
+    if (s + 1 < steps) stage(s + 1, sh[PAR ^ 1]);
+    load(s + 3, sh[PAR ^ 1]);
+  };
+  int s = 0;
+  for (; s + 1 < steps; s += 2) {
+    step(std::integral_constant<int, 0>{}, s);
+    step(std::integral_constant<int, 1>{}, s + 1);
+  }
+  if (s < steps) step(std::integral_constant<int, 0>{}, s);
+  wait_vmcnt<0>();
+
+  const bool vec = (d.ldy & 3) == 0;
+#pragma unroll
+  for (int i = 0; i < FR; ++i) {
+    const int r = wr * 64 + i * 16 + lq * 4;
+#pragma unroll
+    for (int j = 0; j < FT; ++j) {
+      const int t = wt * (BT / 2) + j * 16 + li;
+      if (t < toks && r < rows)
+        store4<DT, OUT>(Y, int64_t(g.y + t) * d.ldy + r0 + r, vec && r + 3 < rows, rows - r, acc[i][j]);
+    }
+  }
+}
+
+GroupDims dims_of(const GroupArgs& a, int rows) {
+  GroupDims d;
+  d.E = int(a.E);
+  d.R = int(a.base.R);
+  d.K = int(a.base.K);
+  d.T = int(a.base.T);
+  d.words = int(a.base.idx_row_words);
+  d.tilesR = int((a.base.R + rows - 1) / rows);
+  d.ldx = a.base.ldx;
+  d.ldy = a.base.ldy;
+  return d;
+}
+
+template <int P, int DT, int OUT, int NT>
+hipError_t launch_few(const GroupArgs& a, hipStream_t s) {
+  const GroupDims d = dims_of(a, 16);
+  const int64_t grid = group_max_tiles(a.base.T, a.E, 16 * NT) * d.tilesR;
+  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((group_few_kernel<P, DT, OUT, NT>), dim3(unsigned(grid)), dim3(kFewWaves * 64), 0, s,
+                     a.base.values, a.base.idx, a.base.act, a.offsets, d, a.base.Y);
+  return hipGetLastError();
+}
+
+template <int P, int DT, int OUT, int BT>
+hipError_t launch_tile(const GroupArgs& a, hipStream_t s) {
+  const GroupDims d = dims_of(a, kBR);
+  const int64_t tiles = group_max_tiles(a.base.T, a.E, BT);
+  if (tiles * d.tilesR > 0x7FFFFFFF) return hipErrorInvalidValue;
+  int4* table = static_cast<int4*>(a.workspace);
+  if (hipError_t e = launch_group_tiles(a.offsets, a.E, a.base.T, BT, tiles, table, s); e != hipSuccess) return e;
+  hipLaunchKernelGGL((group_tile_kernel<P, DT, OUT, BT>), dim3(unsigned(tiles * d.tilesR)), dim3(256), 0, s,
+                     a.base.values, a.base.idx, a.base.act, table, d, a.base.Y);
+  return hipGetLastError();
+}
+
+// Tokens an expert has on average, of the experts that can have any.
+int64_t mean_rows(int64_t T, int64_t E) { return T / std::max<int64_t>(1, std::min(T, E)); }
+
+template <int P, int DT, int OUT>
+hipError_t pick_kernel(const GroupArgs& a, hipStream_t s) {
+  const int64_t mean = mean_rows(a.base.T, a.E);
+  if (mean <= 8) return launch_few<P, DT, OUT, 1>(a, s);
+  if (mean <= 24) return launch_few<P, DT, OUT, 2>(a, s);
+  if (mean <= 64) return launch_tile<P, DT, OUT, 64>(a, s);
+  return launch_tile<P, DT, OUT, 128>(a, s);
+}
+
+template <int P>
+hipError_t pick_type(const GroupArgs& a, hipStream_t s) {
+  const bool f32 = a.base.out_dtype == NM_F32;
+  if (a.base.dtype == NM_F16) return f32 ? pick_kernel<P, NM_F16, NM_F32>(a, s) : pick_kernel<P, NM_F16, NM_F16>(a, s);
+  return f32 ? pick_kernel<P, NM_BF16, NM_F32>(a, s) : pick_kernel<P, NM_BF16, NM_BF16>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_group_tiles(const int32_t* offsets, int64_t E, int64_t T, int BT, int64_t max_tiles, int4* table,
+                              hipStream_t s) {
+  hipLaunchKernelGGL(group_tiles_kernel, dim3(1), dim3(kTableThreads), 0, s, offsets, int(E), int(T), BT,
+                     int(max_tiles), table);
+  return hipGetLastError();
+}
+
+size_t group_workspace(const SpmmArgs& base, int64_t E) { return group_table_bytes(group_max_tiles(base.T, E, 64)); }
+
+size_t group_dx_workspace(int64_t T, int64_t E) { return group_table_bytes(spmm_dx_max_tiles(T, E)); }
+
+hipError_t launch_group(const GroupArgs& a, hipStream_t s) {
+  if (a.base.n == 2) return pick_type<0>(a, s);
+  return a.base.m == 4 ? pick_type<1>(a, s) : pick_type<2>(a, s);
+}
+
+}  // namespace nm

@@ -83,7 +83,14 @@ struct TrainArgs {
   int64_t ldo;
   int out_dtype;           // NM_F32 or dtype
   const LowRank* lowrank = nullptr;   // dX only: added in the epilogue
+  // Products grouped by expert: expert e's tokens are rows offsets[e] ..
+  // offsets[e+1]-1 (null: one weight); the sizes above are one expert's, the
+  // arrays `experts` of them in a row; table: dX's workspace (nm_group.h).
+  const int32_t* offsets = nullptr;
+  int64_t experts = 0;
+  void* table = nullptr;
 };
+int64_t spmm_dx_max_tiles(int64_t T, int64_t E);
 hipError_t launch_spmm_dx(const TrainArgs& a, hipStream_t s);
 hipError_t launch_spmm_dw(const TrainArgs& a, hipStream_t s);
 
@@ -265,6 +272,65 @@ struct LayerNormArgs {
 size_t layernorm_bwd_workspace(int64_t T, int64_t H);
 hipError_t launch_layernorm(const LayerNormArgs& a, hipStream_t s);
 hipError_t launch_layernorm_bwd(const LayerNormArgs& a, hipStream_t s);
+
+// Products grouped by expert (nm_group.hip): base holds one expert's sizes, its
+// pointers those of the first expert.
+struct GroupArgs {
+  SpmmArgs base{};
+  const int32_t* offsets = nullptr;   // [E + 1]
+  int64_t E = 0;
+  void* workspace = nullptr;          // group_workspace bytes
+};
+constexpr int64_t kGroupMaxExperts = 65535;
+constexpr int64_t kGroupMaxTokens = int64_t(1) << 24, kGroupMaxWidth = int64_t(1) << 22;
+constexpr int64_t kGroupMaxLd = int64_t(1) << 23;   // 128 rows of it stay in 32-bit offsets
+size_t group_workspace(const SpmmArgs& base, int64_t E);   // pointers are not looked at
+size_t group_dx_workspace(int64_t T, int64_t E);
+hipError_t launch_group(const GroupArgs& a, hipStream_t s);
+
+// Microscaled 4-bit floats (nm_mx.hip).
+struct MxQuantArgs {
+  int64_t T = 0, K = 0, ldx = 0;
+  int dtype = 0;
+  const void* x = nullptr;      // quantise: [T, K], ldx
+  uint8_t* q = nullptr;         // [T][K / 2]
+  uint8_t* scale = nullptr;     // [ceil(K / 256)][T][8]
+  void* y = nullptr;            // dequantise: [T, K], ldx
+};
+struct MxArgs {
+  const uint8_t* wq = nullptr;  // [E][R][K / 2]
+  const uint8_t* ws = nullptr;  // [E][ceil(K / 256)][R][8]
+  const uint8_t* xq = nullptr;  // [T][K / 2]
+  const uint8_t* xs = nullptr;  // [ceil(K / 256)][T][8]
+  const int32_t* offsets = nullptr;   // [E + 1], or null: one weight
+  int64_t E = 1, R = 0, K = 0, T = 0, ldy = 0;
+  void* Y = nullptr;            // [T, R], ldy
+  int out_dtype = 0;
+  void* workspace = nullptr;    // mx_workspace bytes
+};
+constexpr int64_t kMxMaxRows = int64_t(1) << 24;
+hipError_t launch_mx_quantize(const MxQuantArgs& a, hipStream_t s);
+hipError_t launch_mx_dequantize(const MxQuantArgs& a, hipStream_t s);
+size_t mx_workspace(int64_t E, int64_t R, int64_t K, int64_t T, bool grouped);
+hipError_t launch_mx_gemm(const MxArgs& a, hipStream_t s);
+
+// Global norm of gradients and clipping (nm_grad.hip).  The arrays are the
+// host's, `tensors` long; counts of zero are passed over.
+struct GradArgs {
+  const void* const* grads = nullptr;
+  void* const* out = nullptr;         // clip: where each one goes (grads, in place)
+  const int64_t* counts = nullptr;
+  const int* dtypes = nullptr;
+  int64_t tensors = 0;
+  bool clip = false, in_place = false;
+  double max_norm = 0.0, eps = 0.0;
+  float* norm = nullptr;
+  void* workspace = nullptr;          // grad_workspace bytes
+};
+constexpr int64_t kGradMaxTensors = 16384;
+constexpr int64_t kGradMaxCount = int64_t(1) << 36;   // elements a tensor: a launch's chunks stay below 2^31
+size_t grad_workspace(int64_t tensors);
+hipError_t launch_grad(const GradArgs& a, hipStream_t s);
 
 // Device properties and per-kernel launch set-up, kept per device and safe to
 // call from several host threads (nm_api.cpp).

@@ -24,6 +24,7 @@
 // decompressed W for dX, G and act for dW) feed the MFMA through two such
 // reads per operand, without a transposing copy.
 #include "nm_device.h"
+#include "nm_group.h"
 #include "nm_internal.h"
 #include "nm_lowrank.h"
 
@@ -32,6 +33,19 @@
 
 namespace nm {
 namespace {
+
+// In the place of the experts' rows: one weight for all tokens.
+struct NoGroup {};
+// dX: the tiles' table, and from one expert's values (index words) to the next.
+struct GroupDx {
+  const int4* table;
+  int64_t values_stride, idx_stride;
+};
+// dW: the experts' rows, from one's index words to the next, and its gradient (bytes).
+struct GroupDw {
+  const int32_t* offsets;
+  int64_t idx_stride, dw_stride;
+};
 
 constexpr int pat_n(int P) { return P == 0 ? 2 : 1; }
 constexpr int pat_m(int P) { return P == 2 ? 8 : 4; }
@@ -130,12 +144,12 @@ __device__ inline void dx_expand(const DxPack& d, uint32_t ishift, uint32_t (&o)
   }
 }
 
-template <int P, int DT, int OUT, class LR>
+template <int P, int DT, int OUT, class LR, class GR>
 __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restrict__ values, uint32_t values_bytes,
                                                       const uint32_t* __restrict__ idx, uint32_t idx_bytes, int R,
                                                       int K, int idx_row_words, const uint16_t* __restrict__ G,
                                                       int T, int64_t ldg, void* __restrict__ dX, int64_t lddx,
-                                                      int tilesK, int tilesT, int group, LR lowrank) {
+                                                      int tilesK, int tilesT, int group, LR lowrank, GR experts) {
   constexpr int N = pat_n(P), M = pat_m(P);
   constexpr int B = P == 2 ? 3 : 2;  // index bits per survivor
   extern __shared__ __align__(16) unsigned char smem[];
@@ -144,7 +158,16 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
 
   int tk, tt;
   grouped_tile(xcd_tile(blockIdx.x, gridDim.x), tilesK, tilesT, group, tk, tt);
-  const int K0 = tk * kDxBK, T0 = tt * kDxBT;
+  const int K0 = tk * kDxBK;
+  int T0 = tt * kDxBT;
+  if constexpr (std::is_same_v<GR, GroupDx>) {   // the tile's expert, its tokens up to T
+    if (tt >= experts.table[0].x) return;
+    const int4 g = experts.table[1 + tt];
+    values += g.x * experts.values_stride;
+    idx += g.x * experts.idx_stride;
+    T0 = g.y;
+    T = g.z;
+  }
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wk = wave >> 1, wt = wave & 1;
@@ -372,18 +395,33 @@ constexpr int kDwStage = kDwActTile + kDwGTile;
 constexpr int kDwLds = 2 * kDwStage;
 static_assert(kDwActTile % 16 == 0 && kDwGTile % 16 == 0, "16-byte aligned tiles");
 
-template <int P, int DT, int OUT>
+template <int P, int DT, int OUT, class GR>
 __global__ __launch_bounds__(256, 2) void spmm_dw_kernel(const uint32_t* __restrict__ idx, uint32_t idx_bytes, int R,
                                                       int K, int idx_row_words, const uint16_t* __restrict__ G,
                                                       int T, int64_t ldg, const uint16_t* __restrict__ act,
                                                       int64_t ldx, void* __restrict__ dW, int tilesK, int tilesR,
-                                                      int group) {
+                                                      int group, GR experts) {
   constexpr int N = pat_n(P), M = pat_m(P);
   constexpr int B = P == 2 ? 3 : 2;
   extern __shared__ __align__(16) unsigned char smem[];
 
+  int block = blockIdx.x, blocks = gridDim.x;
+  if constexpr (std::is_same_v<GR, GroupDw>) {
+    // the expert's tokens, index words and gradient; its tiles are dealt to all
+    // the XCDs, so that experts of many tokens do not fall to one of them
+    blocks = tilesK * tilesR;
+    const int e = block / blocks;
+    block -= e * blocks;
+    int lo, hi;
+    group_range(experts.offsets, e, T, lo, hi);
+    act += int64_t(lo) * ldx;
+    G += int64_t(lo) * ldg;
+    T = hi - lo;
+    idx += e * experts.idx_stride;
+    dW = static_cast<unsigned char*>(dW) + e * experts.dw_stride;
+  }
   int tk, tr;
-  grouped_tile(xcd_tile(blockIdx.x, gridDim.x), tilesK, tilesR, group, tk, tr);
+  grouped_tile(xcd_tile(block, blocks), tilesK, tilesR, group, tk, tr);
   const int K0 = tk * kDwBK, R0 = tr * kDwBR;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -565,12 +603,18 @@ template <int P, int DT, int OUT>
 hipError_t launch_dw_cfg(const TrainArgs& a, hipStream_t s) {
   const int64_t tilesK = (a.K + kDwBK - 1) / kDwBK, tilesR = (a.R + kDwBR - 1) / kDwBR;
   if (tilesK * tilesR > 0x7FFFFFFF) return hipErrorInvalidValue;
-  auto kern = spmm_dw_kernel<P, DT, OUT>;
-  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), kDwLds); e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3(unsigned(tilesK * tilesR)), dim3(256), kDwLds, s, a.idx, uint32_t(a.idx_bytes),
-                     int(a.R), int(a.K), int(a.idx_row_words), a.G, int(a.T), a.ldg, a.act, a.ldx, a.out,
-                     int(tilesK), int(tilesR), pick_group(tilesK, tilesR, 2.0, 1.0));
-  return hipGetLastError();
+  auto launch = [&](auto experts, int64_t grid) {
+    auto kern = spmm_dw_kernel<P, DT, OUT, decltype(experts)>;
+    if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), kDwLds); e != hipSuccess) return e;
+    hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(256), kDwLds, s, a.idx, uint32_t(a.idx_bytes), int(a.R),
+                       int(a.K), int(a.idx_row_words), a.G, int(a.T), a.ldg, a.act, a.ldx, a.out, int(tilesK),
+                       int(tilesR), pick_group(tilesK, tilesR, 2.0, 1.0), experts);
+    return hipGetLastError();
+  };
+  if (!a.offsets) return launch(NoGroup{}, tilesK * tilesR);
+  const int64_t grid = tilesK * tilesR * a.experts;
+  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  return launch(GroupDw{a.offsets, a.R * a.idx_row_words, a.R * (a.K / a.m * a.n) * (OUT == NM_F32 ? 4 : 2)}, grid);
 }
 
 template <int P, int DT>
@@ -583,26 +627,32 @@ hipError_t launch_dw_dt(const TrainArgs& a, hipStream_t s) {
   return a.dtype == NM_F16 ? launch_dw_out<P, NM_F16>(a, s) : launch_dw_out<P, NM_BF16>(a, s);
 }
 
-template <int P, int DT, int OUT, class LR>
-hipError_t launch_dx_cfg(const TrainArgs& a, const LR& lowrank, hipStream_t s) {
-  const int64_t tilesK = (a.K + kDxBK - 1) / kDxBK, tilesT = (a.T + kDxBT - 1) / kDxBT;
+template <int P, int DT, int OUT, class LR, class GR>
+hipError_t launch_dx_cfg(const TrainArgs& a, const LR& lowrank, const GR& experts, hipStream_t s) {
+  const int64_t tilesK = (a.K + kDxBK - 1) / kDxBK;
+  const int64_t tilesT = a.offsets ? group_max_tiles(a.T, a.experts, kDxBT) : (a.T + kDxBT - 1) / kDxBT;
   if (tilesK * tilesT > 0x7FFFFFFF) return hipErrorInvalidValue;
-  auto kern = spmm_dx_kernel<P, DT, OUT, LR>;
+  auto kern = spmm_dx_kernel<P, DT, OUT, LR, GR>;
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), kDxLds); e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3(unsigned(tilesK * tilesT)), dim3(256), kDxLds, s, a.values,
                      uint32_t(a.values_bytes), a.idx, uint32_t(a.idx_bytes), int(a.R), int(a.K),
                      int(a.idx_row_words), a.G, int(a.T), a.ldg, a.out, a.ldo, int(tilesK), int(tilesT),
-                     pick_group(tilesK, tilesT, double(pat_n(P)) / pat_m(P), 1.0), lowrank);
+                     pick_group(tilesK, tilesT, double(pat_n(P)) / pat_m(P), 1.0), lowrank, experts);
   return hipGetLastError();
 }
 
 template <int P, int DT>
 hipError_t launch_dx_out(const TrainArgs& a, hipStream_t s) {
+  const bool f32 = a.out_dtype == NM_F32;
   if (a.lowrank)
-    return a.out_dtype == NM_F32 ? launch_dx_cfg<P, DT, NM_F32>(a, *a.lowrank, s)
-                                 : launch_dx_cfg<P, DT, DT>(a, *a.lowrank, s);
-  return a.out_dtype == NM_F32 ? launch_dx_cfg<P, DT, NM_F32>(a, NoLowRank{}, s)
-                               : launch_dx_cfg<P, DT, DT>(a, NoLowRank{}, s);
+    return f32 ? launch_dx_cfg<P, DT, NM_F32>(a, *a.lowrank, NoGroup{}, s)
+               : launch_dx_cfg<P, DT, DT>(a, *a.lowrank, NoGroup{}, s);
+  if (a.offsets) {
+    const GroupDx g{static_cast<const int4*>(a.table), a.R * (a.K / a.m * a.n), a.R * a.idx_row_words};
+    return f32 ? launch_dx_cfg<P, DT, NM_F32>(a, NoLowRank{}, g, s) : launch_dx_cfg<P, DT, DT>(a, NoLowRank{}, g, s);
+  }
+  return f32 ? launch_dx_cfg<P, DT, NM_F32>(a, NoLowRank{}, NoGroup{}, s)
+             : launch_dx_cfg<P, DT, DT>(a, NoLowRank{}, NoGroup{}, s);
 }
 
 template <int P>
@@ -619,7 +669,14 @@ hipError_t launch_spmm_dw(const TrainArgs& a, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
+int64_t spmm_dx_max_tiles(int64_t T, int64_t E) { return group_max_tiles(T, E, kDxBT); }
+
 hipError_t launch_spmm_dx(const TrainArgs& a, hipStream_t s) {
+  if (a.offsets) {
+    const hipError_t e = launch_group_tiles(a.offsets, a.experts, a.T, kDxBT, spmm_dx_max_tiles(a.T, a.experts),
+                                            static_cast<int4*>(a.table), s);
+    if (e != hipSuccess) return e;
+  }
   if (a.n == 2 && a.m == 4) return launch_dx_dt<0>(a, s);
   if (a.n == 1 && a.m == 4) return launch_dx_dt<1>(a, s);
   if (a.n == 1 && a.m == 8) return launch_dx_dt<2>(a, s);
