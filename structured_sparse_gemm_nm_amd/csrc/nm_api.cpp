@@ -1522,7 +1522,7 @@ nm_status nm_mx_gemm_workspace_size(int64_t E, int64_t R, int64_t K, int64_t T, 
   nm_status st = check_mx_gemm(E, R, K, T, grouped != 0, out_dtype);
   if (st != NM_OK) return st;
   if (!bytes) return fail(NM_ERR_NULL, "bytes must be non-NULL");
-  *bytes = T == 0 || R == 0 ? 0 : nm::mx_workspace(E, R, K, T, grouped != 0);
+  *bytes = T == 0 || R == 0 ? 0 : nm::mx_workspace(E, R, T, grouped != 0);
   return ok();
 }
 
@@ -1537,7 +1537,7 @@ nm_status nm_mx_gemm(const uint8_t* wq, const uint8_t* wscale, int64_t E, int64_
   if (!aligned16(wq) || !aligned16(wscale) || !aligned16(xq) || !aligned16(xscale) || !aligned16(Y) ||
       !aligned_to(offsets, 4))
     return fail(NM_ERR_ALIGN, "device pointers must be 16-byte aligned (offsets: 4)");
-  const size_t need = nm::mx_workspace(E, R, K, T, offsets != nullptr);
+  const size_t need = nm::mx_workspace(E, R, T, offsets != nullptr);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
   const Span in[] = {{wq, size_t(E) * size_t(R) * size_t(K / 2)}, {wscale, size_t(E) * mx_scale_bytes(R, K)},
                      {xq, size_t(T) * size_t(K / 2)}, {xscale, mx_scale_bytes(T, K)},

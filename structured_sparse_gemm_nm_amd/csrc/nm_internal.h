@@ -311,7 +311,7 @@ struct MxArgs {
 constexpr int64_t kMxMaxRows = int64_t(1) << 24;
 hipError_t launch_mx_quantize(const MxQuantArgs& a, hipStream_t s);
 hipError_t launch_mx_dequantize(const MxQuantArgs& a, hipStream_t s);
-size_t mx_workspace(int64_t E, int64_t R, int64_t K, int64_t T, bool grouped);
+size_t mx_workspace(int64_t E, int64_t R, int64_t T, bool grouped);
 hipError_t launch_mx_gemm(const MxArgs& a, hipStream_t s);
 
 // Global norm of gradients and clipping (nm_grad.hip).  The arrays are the

@@ -14,6 +14,7 @@
 #include "nm_group.h"
 #include "nm_internal.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace nm {
@@ -246,6 +247,294 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx_few_kernel(const uint8_t* _
   }
 }
 
+// ---------------------------------------------------------------------------
+// Product for many tokens: BM rows of W x BN tokens a workgroup, both operands
+// staged in LDS by direct loads in steps of 256 columns (128 bytes a row), two
+// stages, fragments through two register sets: while one half step (128 columns,
+// one instruction deep) is multiplied, the next half's fragments are read and the
+// loads of the step after next are issued between the products, in chunks that
+// scheduling barriers keep in order.  A stage is free once its second half is in
+// registers, at mid-step, where the one barrier a step stands.
+//
+// Slot (row, 16-byte chunk c) of a stage sits at row*8 + (c ^ (row & 7)).  A chunk
+// is one block of 32 values.  The order of the reduction is free, so half h of a
+// step takes chunk 2q + h in lane quarter q: the two scale bytes a lane needs for
+// a row and step are neighbours, one 16-bit read, and the product's own byte
+// select picks the half's.  Two fragments' scales share a register.
+//
+// Columns past K (the last step's): chunks that reread chunk 0 and enter as zeros
+// with the scale 1, whatever the panel holds there.  Rows past R and tokens past
+// the tile's end reread the last one and are not stored.
+// ---------------------------------------------------------------------------
+template <int BM_, int BN_, int WM_, int WN_>
+struct MxTile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int WAVES = WM * WN, THREADS = WAVES * 64;
+  static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
+  static constexpr int DATA = (BM + BN) * 128, SCALES = (BM + BN) * 8;
+  static constexpr int STAGE = DATA + SCALES, LDS = 2 * STAGE;
+  static constexpr int LP = BM / 8 / WAVES, LQ = BN / 8 / WAVES;   // direct loads a wave issues a step
+  static constexpr int LS = (BM + BN) * 2 / THREADS;
+  static_assert(LP * 8 * WAVES == BM && LQ * 8 * WAVES == BN && LS * THREADS == (BM + BN) * 2, "whole loads");
+  static_assert((LP + LQ) % FM == 0 && LS <= FM && FM % 2 == 0 && FN % 2 == 0 && FN <= 2 * FM, "chunks of a half");
+};
+
+template <int N, int I = 0, class F>
+__device__ inline void static_for(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<N, I + 1>(f);
+  }
+}
+
+struct MxTileDims {
+  int R, K, T, tilesR, tilesT, group;
+  int64_t ldy;
+};
+
+template <int OUT, class C>
+__global__ __launch_bounds__(C::THREADS, 2) void mx_tile_kernel(
+    const uint8_t* __restrict__ wq, const uint8_t* __restrict__ ws, const uint8_t* __restrict__ xq,
+    const uint8_t* __restrict__ xs, const int4* __restrict__ table, MxTileDims d, void* __restrict__ Y) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 15, lq = lane >> 4;
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  int tt, tr;
+  grouped_tile(xcd_tile(blockIdx.x, gridDim.x), d.tilesT, d.tilesR, d.group, tt, tr);
+  GroupTile g{0, tt * C::BN, d.T};
+  if (table) {
+    if (tt >= table[0].x) return;
+    const int4 e = table[1 + tt];
+    g = GroupTile{e.x, e.y, e.z};
+  }
+  const int r0 = tr * C::BM;
+  const int row_bytes = d.K >> 1, steps = (d.K + 255) >> 8;
+  const int rem = d.K - (steps - 1) * 256;   // columns of the last step
+  const int rlast = min(C::BM, d.R - r0) - 1, tlast = min(C::BN, g.t1 - g.t0) - 1;
+
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(wq + (int64_t(g.e) * d.R + r0) * row_bytes);
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(xq + int64_t(g.t0) * row_bytes);
+  const __amdgpu_buffer_rsrc_t rws = make_rsrc(ws + (int64_t(g.e) * steps * d.R + r0) * 8);
+  const __amdgpu_buffer_rsrc_t rxs = make_rsrc(xs + int64_t(g.t0) * 8);
+
+  // direct loads: 0 .. LP-1 rows of W, then tokens, 8 rows each
+  const uint32_t chunk = uint32_t((lane & 7) ^ ((lane >> 3) & 7));
+  uint32_t off[C::LP + C::LQ];
+#pragma unroll
+  for (int j = 0; j < C::LP; ++j)
+    off[j] = uint32_t(min((wave * C::LP + j) * 8 + (lane >> 3), rlast)) * uint32_t(row_bytes) + chunk * 16u;
+#pragma unroll
+  for (int j = 0; j < C::LQ; ++j)
+    off[C::LP + j] = uint32_t(min((wave * C::LQ + j) * 8 + (lane >> 3), tlast)) * uint32_t(row_bytes) + chunk * 16u;
+  // and the scales, a dword (half a row's eight) a lane: whole waves of W's rows, then of tokens
+  uint32_t soff[C::LS];
+  bool s_is_w[C::LS];
+#pragma unroll
+  for (int j = 0; j < C::LS; ++j) {
+    const int row = (wave * C::LS + j) * 32 + (lane >> 1);
+    s_is_w[j] = (wave * C::LS + j) * 32 < C::BM;
+    soff[j] = uint32_t(s_is_w[j] ? min(row, rlast) : min(row - C::BM, tlast)) * 8u + uint32_t(lane & 1) * 4u;
+  }
+  const uint32_t wstep = uint32_t(d.R) * 8u, xstep = uint32_t(d.T) * 8u;
+
+  auto last_back = [&](int s) { return s == steps - 1 && int(chunk) * 32 >= rem ? chunk * 16u : 0u; };
+  auto issue = [&](auto j_c, int s, uint32_t back, unsigned char* st) {
+    constexpr int j = decltype(j_c)::value;
+    if constexpr (j < C::LP)
+      dma16(rw, off[j] - back, uint32_t(s) * 128u, st + (wave * C::LP + j) * 1024);
+    else
+      dma16(rx, off[j] - back, uint32_t(s) * 128u, st + C::BM * 128 + (wave * C::LQ + j - C::LP) * 1024);
+  };
+  auto issue_scale = [&](auto j_c, int s, unsigned char* st) {
+    constexpr int j = decltype(j_c)::value;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(s_is_w[j] ? rws : rxs, (lds_byte*)(st + C::DATA + (wave * C::LS + j) * 256), 4,
+                                             int(soff[j]), int(uint32_t(s) * (s_is_w[j] ? wstep : xstep)), 0, 0);
+  };
+
+  f32x4 acc[C::FM][C::FN];
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // fragment addresses: fragment i's differs from fragment 0's by a constant
+  const int prow = wm * C::FM * 16 + li, qrow = wn * C::FN * 16 + li;
+  int pa[2], qa[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    pa[h] = (prow * 8 + ((2 * lq + h) ^ (prow & 7))) * 16;
+    qa[h] = C::BM * 128 + (qrow * 8 + ((2 * lq + h) ^ (qrow & 7))) * 16;
+  }
+  const int psc = C::DATA + prow * 8 + 2 * lq, qsc = C::DATA + C::BM * 8 + qrow * 8 + 2 * lq;
+  auto read_p = [&](const unsigned char* st, int h, int i) {
+    return *reinterpret_cast<const u32x4*>(st + pa[h] + i * 2048);
+  };
+  auto read_q = [&](const unsigned char* st, int h, int j) {
+    return *reinterpret_cast<const u32x4*>(st + qa[h] + j * 2048);
+  };
+  auto read_pair = [&](const unsigned char* p) {   // two fragments' scales, 16 rows apart
+    const uint32_t lo = *reinterpret_cast<const uint16_t*>(p), hi = *reinterpret_cast<const uint16_t*>(p + 128);
+    return lo | hi << 16;
+  };
+
+  u32x4 a0[C::FM], b0[C::FN], a1[C::FM], b1[C::FN];
+  uint32_t sa[C::FM / 2], sb[C::FN / 2], na[C::FM / 2], nb[C::FN / 2];
+
+  // One half step: products on (ca, cb) with byte H of the scales; with READ,
+  // fragments of half RH of stage rst into (ra, rb), and for RH = 0 the scales of
+  // that stage; with LOAD, the loads of step ls into stage lst.
+  auto half = [&](auto h_c, auto read_c, auto load_c, const u32x4 (&ca)[C::FM], const u32x4 (&cb)[C::FN],
+                  u32x4 (&ra)[C::FM], u32x4 (&rb)[C::FN], const unsigned char* rst, int ls, uint32_t back,
+                  unsigned char* lst) {
+    constexpr int H = decltype(h_c)::value, RH = H ^ 1;
+    constexpr bool READ = decltype(read_c)::value, LOAD = decltype(load_c)::value;
+    static_for<C::FM>([&](auto k_c) {
+      constexpr int k = decltype(k_c)::value;
+      // reads in the first half of the chunks (the next half step needs them right
+      // at its start), loads spread over all
+      if constexpr (READ && k < C::FM / 2) {
+        constexpr int per = 2 * C::FN / C::FM;
+#pragma unroll
+        for (int j = 0; j < per; ++j) rb[k * per + j] = read_q(rst, RH, k * per + j);
+        ra[2 * k] = read_p(rst, RH, 2 * k);
+        ra[2 * k + 1] = read_p(rst, RH, 2 * k + 1);
+        if constexpr (RH == 0) {
+          na[k] = read_pair(rst + psc + k * 256);
+          if constexpr (k < C::FN / 2) nb[k] = read_pair(rst + qsc + k * 256);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      static_for<C::FN>([&](auto j_c) {
+        constexpr int j = decltype(j_c)::value;
+        acc[k][j] = mfma_fp4<(k & 1) * 2 + H, (j & 1) * 2 + H>(ca[k], cb[j], acc[k][j], sa[k / 2], sb[j / 2]);
+      });
+      if constexpr (LOAD) {
+        constexpr int per = (C::LP + C::LQ) / C::FM;
+        static_for<per>([&](auto u_c) {
+          issue(std::integral_constant<int, k * per + decltype(u_c)::value>{}, ls, back, lst);
+        });
+        if constexpr (k < C::LS) issue_scale(k_c, ls, lst);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  using yes = std::integral_constant<bool, true>;
+  using no = std::integral_constant<bool, false>;
+  using h0 = std::integral_constant<int, 0>;
+  using h1 = std::integral_constant<int, 1>;
+  auto take_scales = [&] {
+#pragma unroll
+    for (int i = 0; i < C::FM / 2; ++i) sa[i] = na[i];
+#pragma unroll
+    for (int j = 0; j < C::FN / 2; ++j) sb[j] = nb[j];
+  };
+  // the last step's chunks past K: zeros, and the scale 1 in half h's byte
+  auto trim = [&](u32x4 (&a)[C::FM], u32x4 (&b)[C::FN], int h) {
+    if ((2 * lq + h) * 32 < rem) return;
+    const uint32_t keep = h ? 0x00FF00FFu : 0xFF00FF00u, one = h ? 0x7F007F00u : 0x007F007Fu;
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) a[i] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) b[j] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < C::FM / 2; ++i) sa[i] = (sa[i] & keep) | one;
+#pragma unroll
+    for (int j = 0; j < C::FN / 2; ++j) sb[j] = (sb[j] & keep) | one;
+  };
+  auto load_all = [&](int s, unsigned char* st) {
+    const uint32_t back = last_back(s);
+    static_for<C::LP + C::LQ>([&](auto j_c) { issue(j_c, s, back, st); });
+    static_for<C::LS>([&](auto j_c) { issue_scale(j_c, s, st); });
+  };
+
+  // steps 0 and 1 in stages 0 and 1, the first half step in set 0
+  load_all(0, smem);
+  load_all(min(1, steps - 1), smem + C::STAGE);
+  wait_vmcnt<C::LP + C::LQ + C::LS>();
+  barrier_no_fence();
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i) a0[i] = read_p(smem, 0, i);
+#pragma unroll
+  for (int j = 0; j < C::FN; ++j) b0[j] = read_q(smem, 0, j);
+#pragma unroll
+  for (int i = 0; i < C::FM / 2; ++i) sa[i] = read_pair(smem + psc + i * 256);
+#pragma unroll
+  for (int j = 0; j < C::FN / 2; ++j) sb[j] = read_pair(smem + qsc + j * 256);
+  for (int s = 0; s < steps - 1; ++s) {
+    unsigned char* here = smem + (s & 1) * C::STAGE;
+    unsigned char* next = smem + ((s & 1) ^ 1) * C::STAGE;
+    half(h0{}, yes{}, no{}, a0, b0, a1, b1, here, 0, 0u, nullptr);
+    wait_vmcnt<0>();
+    wait_lgkm0();
+    barrier_no_fence();
+    const int ls = min(s + 2, steps - 1);   // past the end: the last step again, which nothing reads
+    half(h1{}, yes{}, yes{}, a1, b1, a0, b0, next, ls, last_back(ls), here);
+    take_scales();
+  }
+  if (rem < 256) trim(a0, b0, 0);
+  half(h0{}, yes{}, no{}, a0, b0, a1, b1, smem + ((steps - 1) & 1) * C::STAGE, 0, 0u, nullptr);
+  if (rem < 256) trim(a1, b1, 1);
+  half(h1{}, no{}, no{}, a1, b1, a0, b0, nullptr, 0, 0u, nullptr);
+  wait_vmcnt<0>();
+  wait_lgkm0();
+  barrier_no_fence();   // no load is in flight and no stage is read any more
+
+  const int wr0 = wm * C::FM * 16, wt0 = wn * C::FN * 16;   // the wave's corner in the tile
+  if constexpr (OUT == NM_F32) {
+    const bool vec = (d.ldy & 3) == 0;
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+      const int t = wt0 + j * 16 + li;
+      if (t > tlast) continue;
+      float* y = static_cast<float*>(Y) + int64_t(g.t0 + t) * d.ldy + r0;
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) {
+        const int r = wr0 + i * 16 + lq * 4;
+        if (vec && r + 3 <= rlast) *reinterpret_cast<f32x4*>(y + r) = acc[i][j];
+        else for (int e = 0; e < 4 && r + e <= rlast; ++e) y[r + e] = acc[i][j][e];
+      }
+    }
+  } else {
+    // 16-bit results pass through the wave's own part of LDS, token-major, and
+    // leave in whole runs of its FM*16 rows (chunk c of token t at c ^ t)
+    constexpr int CH = C::FM * 2;   // 16-byte chunks a token
+    unsigned char* mine = smem + wave * (C::FN * 16 * CH * 16);
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) {
+        const u32x2 h = {pack_half2<OUT>(acc[i][j][0], acc[i][j][1]), pack_half2<OUT>(acc[i][j][2], acc[i][j][3])};
+        const int t = j * 16 + li, c = (2 * i + (lq >> 1)) ^ (t & (CH - 1));
+        *reinterpret_cast<u32x2*>(mine + (t * CH + c) * 16 + (lq & 1) * 8) = h;
+      }
+    wait_lgkm0();
+    asm volatile("" ::: "memory");
+    const bool vec = (d.ldy & 7) == 0;
+    const int c = lane % CH, r = wr0 + c * 8;
+#pragma unroll
+    for (int it = 0; it < C::FN * 16 * CH / 64; ++it) {
+      const int t = it * (64 / CH) + lane / CH;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(mine + (t * CH + (c ^ (t & (CH - 1)))) * 16);
+      if (wt0 + t > tlast) continue;
+      uint16_t* y = static_cast<uint16_t*>(Y) + int64_t(g.t0 + wt0 + t) * d.ldy + r0 + r;
+      if (vec && r + 7 <= rlast) {
+        *reinterpret_cast<u32x4*>(y) = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t w = v[e >> 1];
+          if (r + e <= rlast) y[e] = uint16_t(w >> (16 * (e & 1)));
+        }
+      }
+    }
+  }
+}
+
+using MxLarge = MxTile<256, 256, 2, 4>;
+using MxMiddle = MxTile<128, 128, 2, 2>;
+
 inline unsigned grid_of(int64_t items) {
   const int64_t blocks = (items + 255) / 256;
   return unsigned(blocks < 65536 ? blocks : 65536);
@@ -285,12 +574,51 @@ hipError_t launch_few(const MxArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int OUT, class C>
+hipError_t launch_tiles(const MxArgs& a, hipStream_t s) {
+  const int64_t tilesR = (a.R + C::BM - 1) / C::BM;
+  const int64_t tilesT = a.offsets ? group_max_tiles(a.T, a.E, C::BN) : (a.T + C::BN - 1) / C::BN;
+  if (tilesR * tilesT > 0x7FFFFFFF) return hipErrorInvalidValue;
+  MxTileDims d;
+  d.R = int(a.R);
+  d.K = int(a.K);
+  d.T = int(a.T);
+  d.tilesR = int(tilesR);
+  d.tilesT = int(tilesT);
+  d.group = int(std::min<int64_t>(tilesT, 4));
+  d.ldy = a.ldy;
+  int4* table = a.offsets ? static_cast<int4*>(a.workspace) : nullptr;
+  if (table)
+    if (hipError_t e = launch_group_tiles(a.offsets, a.E, a.T, C::BN, tilesT, table, s); e != hipSuccess) return e;
+  auto kern = mx_tile_kernel<OUT, C>;
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), C::LDS); e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3(unsigned(tilesR * tilesT)), dim3(C::THREADS), C::LDS, s, a.wq, a.ws, a.xq, a.xs, table, d,
+                     a.Y);
+  return hipGetLastError();
+}
+
+// Which kernel: by the rows that a weight meets on average, and, where those fill
+// tiles, by whether the largest ones still give every compute unit one.
+enum class MxPick { few1, few2, few4, middle, large };
+
+MxPick pick(int64_t E, int64_t R, int64_t T, bool grouped) {
+  const int64_t weights = grouped ? std::min(E, T) : 1, rows = T / weights;
+  if (rows <= 16) return MxPick::few1;
+  if (rows <= 32) return MxPick::few2;
+  if (rows <= 64) return MxPick::few4;
+  const int64_t large = weights * ((rows + 255) / 256) * ((R + 255) / 256);
+  return large >= 256 ? MxPick::large : MxPick::middle;
+}
+
 template <int OUT>
 hipError_t gemm_out(const MxArgs& a, hipStream_t s) {
-  const int64_t per = a.T / (a.offsets && a.E < a.T ? a.E : a.offsets ? a.T : 1);
-  if (per <= 16) return launch_few<OUT, 1, 1>(a, s);
-  if (per <= 32) return launch_few<OUT, 1, 2>(a, s);
-  return launch_few<OUT, 2, 4>(a, s);
+  switch (pick(a.E, a.R, a.T, a.offsets != nullptr)) {
+    case MxPick::few1: return launch_few<OUT, 1, 1>(a, s);
+    case MxPick::few2: return launch_few<OUT, 1, 2>(a, s);
+    case MxPick::few4: return launch_few<OUT, 2, 4>(a, s);
+    case MxPick::middle: return launch_tiles<OUT, MxMiddle>(a, s);
+    default: return launch_tiles<OUT, MxLarge>(a, s);
+  }
 }
 
 }  // namespace
@@ -305,7 +633,11 @@ hipError_t launch_mx_dequantize(const MxQuantArgs& a, hipStream_t s) {
   return a.dtype == NM_F16 ? dequantize_dt<NM_F16>(a, s) : dequantize_dt<NM_BF16>(a, s);
 }
 
-size_t mx_workspace(int64_t E, int64_t R, int64_t K, int64_t T, bool grouped) { return 0; }
+size_t mx_workspace(int64_t E, int64_t R, int64_t T, bool grouped) {
+  const MxPick p = pick(E, R, T, grouped);
+  if (!grouped || (p != MxPick::middle && p != MxPick::large)) return 0;
+  return group_table_bytes(group_max_tiles(T, E, p == MxPick::middle ? MxMiddle::BN : MxLarge::BN));
+}
 
 hipError_t launch_mx_gemm(const MxArgs& a, hipStream_t s) {
   if (a.out_dtype == NM_F32) return gemm_out<NM_F32>(a, s);
