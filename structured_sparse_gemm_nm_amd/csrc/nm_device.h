@@ -123,6 +123,14 @@ __device__ inline __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t by
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, int(bytes), 0x00020000);
 }
 
+// The offset o (a multiple of 2 bytes) where `live`, and otherwise one that no
+// descriptor of less than 4 GiB covers, so that the load reads zeros.  By a mask: a
+// conditional is often compiled to a branch around the load, whose end waits for it.
+constexpr uint32_t kDeadOffset = 0xFFFFFFF0u;
+__device__ inline uint32_t live_offset(bool live, uint32_t o) {
+  return o | ((live ? 0u : ~0u) & kDeadOffset);
+}
+
 // 16 bytes per lane from base + voff + soff into LDS slot lds_dst + lane*16.
 __device__ inline void dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t soff, unsigned char* lds_dst) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_byte*)lds_dst, 16, int(voff), int(soff), 0, 0);

@@ -26,10 +26,13 @@ __device__ inline void group_range(const int32_t* __restrict__ offsets, int e, i
 }
 
 // Tile number `tile` by the whole wave (64 experts at a time); false past the last.
+// The results are the same in every lane and leave through readfirstlane: the
+// compiler does not see that through the loop, and a descriptor made from what it
+// takes to differ by lane is looped over lane by lane, a load at a time.
 __device__ inline bool group_find(const int32_t* __restrict__ offsets, int E, int T, int BT, int tile, GroupTile& g) {
   const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int e0 = 0; e0 < E; e0 += 64) {
+  int before = 0, e = -1, t0 = 0, t1 = 0;
+  for (int e0 = 0; e0 < E && e < 0; e0 += 64) {
     int lo = 0, hi = 0;
     if (e0 + lane < E) group_range(offsets, e0 + lane, T, lo, hi);
     const int tiles = (hi - lo + BT - 1) / BT;
@@ -43,14 +46,16 @@ __device__ inline bool group_find(const int32_t* __restrict__ offsets, int E, in
     if (past) {
       const int at = __builtin_ctzll(past);
       const int start = before + (at > 0 ? __builtin_amdgcn_readlane(sum, at - 1) : 0);
-      g.e = e0 + at;
-      g.t0 = __builtin_amdgcn_readlane(lo, at) + (tile - start) * BT;
-      g.t1 = __builtin_amdgcn_readlane(hi, at);
-      return true;
+      e = e0 + at;
+      t0 = __builtin_amdgcn_readlane(lo, at) + (tile - start) * BT;
+      t1 = __builtin_amdgcn_readlane(hi, at);
     }
     before = tile_sum(before, __builtin_amdgcn_readlane(sum, 63));
   }
-  return false;
+  g.e = __builtin_amdgcn_readfirstlane(e);
+  g.t0 = __builtin_amdgcn_readfirstlane(t0);
+  g.t1 = __builtin_amdgcn_readfirstlane(t1);
+  return g.e >= 0;
 }
 
 // The tiles as a table in a workspace: its size, and the launch that fills it

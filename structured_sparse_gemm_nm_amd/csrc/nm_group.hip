@@ -81,78 +81,212 @@ __device__ inline void store4(void* Y, int64_t o, bool whole, int left, const f3
 
 // ---------------------------------------------------------------------------
 // Few rows an expert: bound by streaming the packed weights of the experts that
-// have any.  A workgroup of 8 waves owns 16 rows of one expert's weight and up to
-// 16 NT of its tokens; the waves take contiguous shares of K, issue the loads of
-// U steps before multiplying them, and the partial tiles are added in wave order.
+// have any.  A wave owns 16 RB rows of one expert's weight and up to 16 NT of its
+// tokens; the 8 waves of a workgroup take KS shares of K (in wave order added in
+// LDS) and 8 / KS blocks of rows, KS so that the waves fill the chip.
+//
+// The order of the reduction is free, as long as both operands keep it: so a lane
+// quarter takes a run of consecutive columns that makes whole 16-byte loads of
+// packed values whatever the pattern, and one load of their index bits:
+//   2:4  32 columns (2 x 16 bytes, 32 bits), a unit of 128 columns in 2 products;
+//   1:4  32 columns (16 bytes, 16 bits), the same;
+//   1:8  64 columns (16 bytes, 24 bits), a unit of 256 columns in 4 products.
+// (One 64-column step a load, 8 or 4 bytes a lane, ran 41 experts of 2816 x 2048 in
+// 1:4 in 94 us.)  Product p of a unit takes columns 16p .. 16p+15 of each quarter's
+// run.  Loads of U units go out before the first product.
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8;
 
-template <int P, int DT, int OUT, int NT>
+template <int P>
+struct FewUnit {
+  static constexpr int RUN = P == 2 ? 64 : 32;     // columns of a lane quarter
+  static constexpr int COLS = 4 * RUN, PRODUCTS = RUN / 16;
+  static constexpr int WORDS = P == 0 ? 8 : 4;     // packed values of a run
+  uint32_t v[WORDS];
+  uint32_t i0, i1;                                 // index bits (1:8: the two words that hold them)
+};
+
+// A lane's run of columns k .. k + RUN - 1 of a row, zeros past K and where `on` is
+// false.  Offsets past an edge are selected to lie outside the descriptors, not
+// branched on: behind branches the loads of a unit waited for those before them.
+// WIDE: K is a multiple of RUN, a run's values come whole; otherwise 16 columns a load.
+
+template <int P, bool WIDE>
+__device__ inline void load_unit(FewUnit<P>& f, __amdgpu_buffer_rsrc_t rv, __amdgpu_buffer_rsrc_t ri, uint32_t vrow,
+                                 uint32_t irow, int words, int k, int K, bool on) {
+  using F = FewUnit<P>;
+  on &= k < K;
+  const uint32_t v0 = vrow + uint32_t(k / pat_m(P) * pat_n(P)) * 2u;
+  if constexpr (P == 0 || WIDE) {
+#pragma unroll
+    for (int q = 0; q < F::WORDS / 4; ++q) {
+      const bool live = on & ((P != 0) | (k + 16 * q < K));
+      const u32x4 t = __builtin_bit_cast(
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(rv, live_offset(live, v0 + 16u * q), 0, 0));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f.v[4 * q + e] = t[e];
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < F::PRODUCTS; ++q) {
+      const bool live = on & (k + 16 * q < K);
+      if constexpr (P == 1) {
+        const u32x2 t = __builtin_bit_cast(
+            u32x2, __builtin_amdgcn_raw_buffer_load_b64(rv, live_offset(live, v0 + 8u * q), 0, 0));
+        f.v[2 * q] = t[0];
+        f.v[2 * q + 1] = t[1];
+      } else {
+        f.v[q] = __builtin_amdgcn_raw_buffer_load_b32(rv, live_offset(live, v0 + 4u * q), 0, 0);
+      }
+    }
+  }
+  if constexpr (P == 0) {
+    f.i0 = __builtin_amdgcn_raw_buffer_load_b32(ri, live_offset(on, irow + uint32_t(k >> 5) * 4u), 0, 0);
+  } else if constexpr (P == 1) {
+    f.i0 = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(ri, live_offset(on, irow + uint32_t(k >> 5) * 2u), 0, 0));
+  } else {   // 24 bits from bit 24 (k / 64) on; past the row's last word nothing is needed
+    const int w = (k >> 6) * 24 >> 5;
+    f.i0 = __builtin_amdgcn_raw_buffer_load_b32(ri, live_offset(on, irow + uint32_t(w) * 4u), 0, 0);
+    f.i1 = __builtin_amdgcn_raw_buffer_load_b32(ri, live_offset(on, irow + uint32_t(min(w + 1, words - 1)) * 4u), 0, 0);
+  }
+}
+
+// The 2:4 operand of product p.
+template <int P>
+__device__ inline void unit_operand(const FewUnit<P>& f, int k, int p, u32x4& a, uint32_t& ix) {
+  if constexpr (P == 0) {
+    a = u32x4{f.v[4 * p], f.v[4 * p + 1], f.v[4 * p + 2], f.v[4 * p + 3]};
+    ix = (f.i0 >> (16 * p)) & 0xFFFFu;
+  } else if constexpr (P == 1) {
+    AFrag t;
+    t.v[0] = f.v[2 * p];
+    t.v[1] = f.v[2 * p + 1];
+    t.ib = (f.i0 >> (8 * p)) & 0xFFu;
+    widen<1>(t, a, ix);
+  } else {
+    AFrag t;
+    t.v[0] = f.v[p];
+    t.v[1] = f.i0;
+    t.v[2] = f.i1;
+    t.ib = uint32_t((((k >> 6) * 24) & 31) + 6 * p);
+    widen<2>(t, a, ix);
+  }
+}
+
+template <int P, int DT, int OUT, int RB, int NT, int U, bool WIDE>
 __global__ __launch_bounds__(kFewWaves * 64) void group_few_kernel(const uint16_t* __restrict__ values,
                                                                    const uint32_t* __restrict__ idx,
                                                                    const uint16_t* __restrict__ act,
                                                                    const int32_t* __restrict__ offsets, GroupDims d,
-                                                                   void* __restrict__ Y) {
-  __shared__ f32x4 part[kFewWaves][NT][64];
+                                                                   int ks, void* __restrict__ Y) {
+  using F = FewUnit<P>;
+  __shared__ f32x4 part[kFewWaves][RB * NT][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lq = lane >> 4;
-  const int tile = blockIdx.x / d.tilesR;
-  const int r0 = (blockIdx.x - tile * d.tilesR) * 16;
+  const int tile = __builtin_amdgcn_readfirstlane(blockIdx.x / d.tilesR);
+  // its share of K and its rows (ks is a power of two)
+  const int share = wave & (ks - 1);
+  const int r0 = (((int(blockIdx.x) - tile * d.tilesR) * kFewWaves + wave - share) >> __builtin_ctz(ks)) * (16 * RB);
   GroupTile g;
   if (!group_find(offsets, d.E, d.T, 16 * NT, tile, g)) return;
   const int64_t S = int64_t(d.K) / pat_m(P) * pat_n(P);
-  values += int64_t(g.e) * d.R * S;
-  idx += int64_t(g.e) * d.R * d.words;
-  const uint16_t* x = act + int64_t(g.t0) * d.ldx;
   const int toks = min(16 * NT, g.t1 - g.t0);
-  const int steps = (d.K + 63) >> 6;
-  const int share = (steps + kFewWaves - 1) / kFewWaves;
-  const int s_end = min(steps, (wave + 1) * share);
+  // (clamping to two sides is a vector operation: back to a scalar for the descriptors)
+  const int rows = __builtin_amdgcn_readfirstlane(max(min(16 * RB, d.R - r0), 0));
+  const uint32_t vbytes = uint32_t(S * 2), ibytes = uint32_t(d.words) * 4u;
+  const int64_t first = int64_t(g.e) * d.R + r0;
+  const __amdgpu_buffer_rsrc_t rv = make_rsrc(values + first * S, uint32_t(rows) * vbytes);
+  const __amdgpu_buffer_rsrc_t ri = make_rsrc(idx + first * d.words, uint32_t(rows) * ibytes);
+  const __amdgpu_buffer_rsrc_t rx =
+      make_rsrc(act + int64_t(g.t0) * d.ldx, uint32_t((int64_t(toks - 1) * d.ldx + d.K) * 2));
+  const int units = (d.K + F::COLS - 1) / F::COLS;
+  const int per = (units + ks - 1) / ks;
+  const int u_end = min(units, (share + 1) * per);
 
-  f32x4 acc[NT];
+  f32x4 acc[RB][NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  constexpr int U = NT == 1 ? 8 : NT == 2 ? 4 : 2;
-  for (int s0 = wave * share; s0 < s_end; s0 += U) {
-    AFrag a[U];
-    u32x8 b[U][NT];
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  struct Batch {
+    F a[U][RB];
+    u32x8 b[U][F::PRODUCTS][NT];
+  };
+  auto load = [&](int u0, Batch& s) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int s = s0 + u;
-      load_afrag<P>(a[u], values, idx, S, d.words, s < s_end ? r0 + li : d.R, d.R, d.K, s, lq);
+      const int k = (u0 + u) * F::COLS + lq * F::RUN;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int t = j * 16 + li;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int k = s * 64 + h * 32 + lq * 8;
-          u32x4 v = {0u, 0u, 0u, 0u};
-          if (s < s_end && t < toks && k < d.K) v = *reinterpret_cast<const u32x4*>(x + int64_t(t) * d.ldx + k);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) b[u][j][4 * h + e] = v[e];
-        }
+      for (int i = 0; i < RB; ++i) {
+        const int r = i * 16 + li;
+        load_unit<P, WIDE>(s.a[u][i], rv, ri, uint32_t(r) * vbytes, uint32_t(r) * ibytes, d.words, k, d.K,
+                           (u0 + u < u_end) & (r < rows));
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      u32x4 w;
-      uint32_t ix;
-      widen<P>(a[u], w, ix);
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[j] = smfmac<DT>(w, b[u][j], acc[j], ix);
-    }
+      for (int p = 0; p < F::PRODUCTS; ++p)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int t = j * 16 + li;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // the product's columns 32h + 8 lq .. +7: half of a quarter's 16
+            const int k = (u0 + u) * F::COLS + (2 * h + (lq >> 1)) * F::RUN + 16 * p + 8 * (lq & 1);
+            const bool live = (u0 + u < u_end) & (t < toks) & (k < d.K);
+            const u32x4 v = __builtin_bit_cast(
+                u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                           rx, live_offset(live, (uint32_t(t) * uint32_t(d.ldx) + uint32_t(k)) * 2u), 0, 0));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s.b[u][p][j][4 * h + e] = v[e];
+          }
+        }
+  };
+  auto multiply = [&](int u0, const Batch& s) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int p = 0; p < F::PRODUCTS; ++p)
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+          u32x4 w;
+          uint32_t ix;
+          unit_operand<P>(s.a[u][i], (u0 + u) * F::COLS + lq * F::RUN, p, w, ix);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) acc[i][j] = smfmac<DT>(w, s.b[u][p][j], acc[i][j], ix);
+        }
+  };
+  for (int u = share * per; u < u_end; u += U) {
+    Batch b;
+    load(u, b);
+    __builtin_amdgcn_sched_barrier(0);   // every load goes out before the first product
+    multiply(u, b);
+  }
+  auto store = [&](int f, int first, const f32x4& sum) {   // fragment f of the rows from `first` on
+    const int t = (f % NT) * 16 + li, r = first + (f / NT) * 16 + lq * 4;
+    if (t < toks && r < d.R)
+      store4<DT, OUT>(Y, int64_t(g.t0 + t) * d.ldy + r, (d.ldy & 3) == 0 && r + 3 < d.R, d.R - r, sum);
+  };
+  if (ks == 1) {
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) store(i * NT + j, r0, acc[i][j]);
+    return;
   }
 #pragma unroll
-  for (int j = 0; j < NT; ++j) part[wave][j][lane] = acc[j];
-  __syncthreads();
-  if (wave >= NT) return;
-  f32x4 sum = part[0][wave][lane];
+  for (int i = 0; i < RB; ++i)
 #pragma unroll
-  for (int w = 1; w < kFewWaves; ++w) sum += part[w][wave][lane];
-  const int t = wave * 16 + li, r = r0 + lq * 4;
-  if (t >= toks || r >= d.R) return;
-  store4<DT, OUT>(Y, int64_t(g.t0 + t) * d.ldy + r, (d.ldy & 3) == 0 && r + 3 < d.R, d.R - r, sum);
+    for (int j = 0; j < NT; ++j) part[wave][i * NT + j][lane] = acc[i][j];
+  __syncthreads();
+  for (int f = share; f < RB * NT; f += ks) {
+    const int w0 = wave - share;
+    f32x4 sum = part[w0][f][lane];
+    for (int w = 1; w < ks; ++w) sum += part[w0 + w][f][lane];
+    store(f, r0, sum);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -164,8 +298,6 @@ __global__ __launch_bounds__(kFewWaves * 64) void group_few_kernel(const uint16_
 // ---------------------------------------------------------------------------
 constexpr int kBR = 128;
 constexpr int kStageA = kBR * 64, kStageI = kBR * 8;
-constexpr uint32_t kDeadOff = 0xFFFFFFF0u;   // no descriptor covers it: reads zeros
-
 template <int P, int DT, int OUT, int BT>
 __global__ __launch_bounds__(256, 2) void group_tile_kernel(const uint16_t* __restrict__ values,
                                                             const uint32_t* __restrict__ idx,
@@ -209,39 +341,39 @@ __global__ __launch_bounds__(256, 2) void group_tile_kernel(const uint16_t* __re
 #pragma unroll
   for (int j = 0; j < PB; ++j) {
     const int slot = j * 256 + tid, tok = slot >> 3, c = (slot & 7) ^ (tok & 7);
-    xoff[j] = tok < toks ? uint32_t(tok) * uint32_t(d.ldx) * 2u + uint32_t(c) * 16u : kDeadOff;
+    xoff[j] = live_offset(tok < toks, uint32_t(tok) * uint32_t(d.ldx) * 2u + uint32_t(c) * 16u);
     xcol[j] = c * 8;
   }
   auto load = [&](int s, Share& o) {
     const int k = s * 64 + wh * 32;
-    const bool on = s < steps && wrow < rows && k < d.K, on2 = on && k + 16 < d.K;
+    const bool on = (s < steps) & (wrow < rows) & (k < d.K), on2 = on & (k + 16 < d.K);
     const uint32_t v0 = vbase + uint32_t(s * 2 + wh) * VB;
     if constexpr (P == 0) {
-      const u32x4 a = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rv, on ? v0 : kDeadOff, 0, 0));
+      const u32x4 a = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rv, live_offset(on, v0), 0, 0));
       const u32x4 b =
-          __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rv, on2 ? v0 + 16u : kDeadOff, 0, 0));
+          __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rv, live_offset(on2, v0 + 16u), 0, 0));
 #pragma unroll
       for (int e = 0; e < 4; ++e) o.v[e] = a[e], o.v[4 + e] = b[e];
-      o.w0 = __builtin_amdgcn_raw_buffer_load_b32(ri, on ? ibase + uint32_t(s * 2 + wh) * 4u : kDeadOff, 0, 0);
+      o.w0 = __builtin_amdgcn_raw_buffer_load_b32(ri, live_offset(on, ibase + uint32_t(s * 2 + wh) * 4u), 0, 0);
     } else if constexpr (P == 1) {
-      const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rv, on ? v0 : kDeadOff, 0, 0));
+      const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rv, live_offset(on, v0), 0, 0));
       const u32x2 b =
-          __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rv, on2 ? v0 + 8u : kDeadOff, 0, 0));
+          __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rv, live_offset(on2, v0 + 8u), 0, 0));
       o.v[0] = a[0], o.v[1] = a[1], o.v[2] = b[0], o.v[3] = b[1];
-      o.w0 = __builtin_amdgcn_raw_buffer_load_b32(ri, on ? ibase + uint32_t(s) * 4u : kDeadOff, 0, 0);
+      o.w0 = __builtin_amdgcn_raw_buffer_load_b32(ri, live_offset(on, ibase + uint32_t(s) * 4u), 0, 0);
     } else {
-      o.v[0] = __builtin_amdgcn_raw_buffer_load_b32(rv, on ? v0 : kDeadOff, 0, 0);
-      o.v[1] = __builtin_amdgcn_raw_buffer_load_b32(rv, on2 ? v0 + 4u : kDeadOff, 0, 0);
+      o.v[0] = __builtin_amdgcn_raw_buffer_load_b32(rv, live_offset(on, v0), 0, 0);
+      o.v[1] = __builtin_amdgcn_raw_buffer_load_b32(rv, live_offset(on2, v0 + 4u), 0, 0);
       const int bit = 24 * s + 12 * wh, w = bit >> 5;
-      o.w0 = __builtin_amdgcn_raw_buffer_load_b32(ri, on ? ibase + uint32_t(w) * 4u : kDeadOff, 0, 0);
+      o.w0 = __builtin_amdgcn_raw_buffer_load_b32(ri, live_offset(on, ibase + uint32_t(w) * 4u), 0, 0);
       // (the row's last word holds every bit it needs: the next one is not looked at)
-      o.w1 = __builtin_amdgcn_raw_buffer_load_b32(ri, on ? ibase + uint32_t(min(w + 1, d.words - 1)) * 4u : kDeadOff, 0, 0);
+      o.w1 = __builtin_amdgcn_raw_buffer_load_b32(ri, live_offset(on, ibase + uint32_t(min(w + 1, d.words - 1)) * 4u), 0, 0);
     }
 #pragma unroll
     for (int j = 0; j < PB; ++j) {
-      const bool live = s < steps && s * 64 + xcol[j] < d.K && xoff[j] != kDeadOff;
+      const bool live = (s < steps) & (s * 64 + xcol[j] < d.K) & (xoff[j] < kDeadOffset);
       o.x[j] = __builtin_bit_cast(
-          u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, live ? xoff[j] + uint32_t(s) * 128u : kDeadOff, 0, 0));
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, live_offset(live, xoff[j] + uint32_t(s) * 128u), 0, 0));
     }
   };
   auto stage = [&](int s, const Share& o) {
@@ -354,13 +486,20 @@ GroupDims dims_of(const GroupArgs& a, int rows) {
   return d;
 }
 
-template <int P, int DT, int OUT, int NT>
+template <int P, int DT, int OUT, int RB, int NT, int U>
 hipError_t launch_few(const GroupArgs& a, hipStream_t s) {
-  const GroupDims d = dims_of(a, 16);
+  const int64_t experts = std::min(a.base.T, a.E);
+  // shares of K while the waves fit the chip a few times over, but none below two units
+  const int64_t blocks = (a.base.R + 16 * RB - 1) / (16 * RB), units = a.base.K / FewUnit<P>::COLS;
+  int ks = 1;
+  while (ks < kFewWaves && experts * blocks * ks < 16 * 1024 && units >= 2 * ks) ks *= 2;
+  const GroupDims d = dims_of(a, 16 * RB * (kFewWaves / ks));
   const int64_t grid = group_max_tiles(a.base.T, a.E, 16 * NT) * d.tilesR;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((group_few_kernel<P, DT, OUT, NT>), dim3(unsigned(grid)), dim3(kFewWaves * 64), 0, s,
-                     a.base.values, a.base.idx, a.base.act, a.offsets, d, a.base.Y);
+  const bool wide = P == 0 || a.base.K % FewUnit<P>::RUN == 0;
+  const auto kern = wide ? group_few_kernel<P, DT, OUT, RB, NT, U, true> : group_few_kernel<P, DT, OUT, RB, NT, U, P == 0>;
+  hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(kFewWaves * 64), 0, s, a.base.values, a.base.idx, a.base.act,
+                     a.offsets, d, ks, a.base.Y);
   return hipGetLastError();
 }
 
@@ -382,8 +521,11 @@ int64_t mean_rows(int64_t T, int64_t E) { return T / std::max<int64_t>(1, std::m
 template <int P, int DT, int OUT>
 hipError_t pick_kernel(const GroupArgs& a, hipStream_t s) {
   const int64_t mean = mean_rows(a.base.T, a.E);
-  if (mean <= 8) return launch_few<P, DT, OUT, 1>(a, s);
-  if (mean <= 24) return launch_few<P, DT, OUT, 2>(a, s);
+  // 64 rows a wave (the tokens are read a quarter as often) where that leaves waves enough
+  if (mean <= 8)
+    return std::min(a.base.T, a.E) * a.base.R >= 12288 ? launch_few<P, DT, OUT, 4, 1, 1>(a, s)
+                                                       : launch_few<P, DT, OUT, 1, 1, 2>(a, s);
+  if (mean <= 24) return launch_few<P, DT, OUT, 4, 2, 1>(a, s);
   if (mean <= 64) return launch_tile<P, DT, OUT, 64>(a, s);
   return launch_tile<P, DT, OUT, 128>(a, s);
 }

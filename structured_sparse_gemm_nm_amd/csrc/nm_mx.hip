@@ -144,9 +144,11 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* __re
 }
 
 // ---------------------------------------------------------------------------
-// Product for few tokens (and any other shape): a workgroup of 8 waves owns
-// 16 RB rows x 16 NT tokens, the waves take shares of K, operands go straight
-// into registers, and the partial tiles are added in wave order.
+// Product for few tokens: bound by streaming the weight.  A wave owns 16 RB rows x
+// 16 NT tokens; the 8 waves of a workgroup take KS shares of K (added in wave order
+// in LDS) and 8 / KS blocks of rows.  Operands go straight into registers: a lane
+// quarter takes 64 consecutive columns of a panel (two blocks, 32 bytes of values,
+// 2 of scales) for two products, so rows are read in whole 128-byte lines.
 // ---------------------------------------------------------------------------
 struct MxDims {
   int E, R, K, T, tilesR;
@@ -154,96 +156,132 @@ struct MxDims {
 };
 
 constexpr int kFewWaves = 8;
-constexpr uint32_t kDead = 0xFFFFFFF0u;   // no descriptor covers it: reads zeros
 
-template <int OUT, int RB, int NT>
+template <int OUT, int RB, int NT, int U>
 __global__ __launch_bounds__(kFewWaves * 64) void mx_few_kernel(const uint8_t* __restrict__ wq,
                                                                 const uint8_t* __restrict__ ws,
                                                                 const uint8_t* __restrict__ xq,
                                                                 const uint8_t* __restrict__ xs,
-                                                                const int32_t* __restrict__ offsets, MxDims d,
+                                                                const int32_t* __restrict__ offsets, MxDims d, int ks,
                                                                 void* __restrict__ Y) {
   __shared__ f32x4 part[kFewWaves][RB * NT][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lq = lane >> 4;
-  const int tile = blockIdx.x / d.tilesR;
-  const int r0 = (blockIdx.x - tile * d.tilesR) * (16 * RB);
+  const int tile = __builtin_amdgcn_readfirstlane(blockIdx.x / d.tilesR);
+  // its share of K and its rows (ks is a power of two)
+  const int share = wave & (ks - 1);
+  const int r0 = (((int(blockIdx.x) - tile * d.tilesR) * kFewWaves + wave - share) >> __builtin_ctz(ks)) * (16 * RB);
   GroupTile g{0, tile * 16 * NT, d.T};
   if (offsets && !group_find(offsets, d.E, d.T, 16 * NT, tile, g)) return;
-  const int row_bytes = d.K >> 1, panels = (d.K + 255) >> 8, blocks = d.K >> 5;
-  const int rows = min(16 * RB, d.R - r0), toks = min(16 * NT, g.t1 - g.t0);
-  const __amdgpu_buffer_rsrc_t rw =
-      make_rsrc(wq + (int64_t(g.e) * d.R + r0) * row_bytes, uint32_t(rows) * uint32_t(row_bytes));
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(xq + int64_t(g.t0) * row_bytes, uint32_t(toks) * uint32_t(row_bytes));
-  const uint8_t* sw = ws + (int64_t(g.e) * panels * d.R + r0) * 8;
-  const uint8_t* sx = xs + int64_t(g.t0) * 8;
-  const int64_t wstep = int64_t(d.R) * 8, xstep = int64_t(d.T) * 8;   // bytes from a panel to the next
+  const int row_bytes = d.K >> 1, panels = (d.K + 255) >> 8;
+  const int toks = min(16 * NT, g.t1 - g.t0);
+  // (clamping to two sides is a vector operation: back to a scalar for the descriptors)
+  const int rows = __builtin_amdgcn_readfirstlane(max(min(16 * RB, d.R - r0), 0));
+  // Loads past the rows, the tokens or K read zeros: their offsets are selected, not
+  // branched on (behind branches the loads of a unit waited for those before them).
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(wq + (int64_t(g.e) * d.R + r0) * row_bytes, uint32_t(rows * row_bytes));
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(xq + int64_t(g.t0) * row_bytes, uint32_t(toks * row_bytes));
+  const uint32_t wstep = uint32_t(d.R) * 8u, xstep = uint32_t(d.T) * 8u;   // from a panel's scales to the next's
+  const __amdgpu_buffer_rsrc_t rws = make_rsrc(ws + int64_t(g.e) * panels * wstep, uint32_t(panels) * wstep);
+  const __amdgpu_buffer_rsrc_t rxs = make_rsrc(xs, uint32_t(panels) * xstep);
+  const int per = (panels + ks - 1) / ks;
+  const int u_end = min(panels, (share + 1) * per);
 
-  const int steps = (d.K + 127) >> 7;
-  const int share = (steps + kFewWaves - 1) / kFewWaves;
-  const int s_end = min(steps, (wave + 1) * share);
   f32x4 acc[RB][NT];
 #pragma unroll
   for (int i = 0; i < RB; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  constexpr int U = 4 / (NT > 2 ? 2 : 1);
-  for (int s0 = wave * share; s0 < s_end; s0 += U) {
-    u32x4 a[U][RB], b[U][NT];
+  struct Batch {
+    u32x4 a[U][RB][2], b[U][NT][2];
     uint32_t sa[U][RB], sb[U][NT];
+  };
+  auto load = [&](int u0, Batch& s) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int block = (s0 + u) * 4 + lq;
-      const bool live = s0 + u < s_end && block < blocks;
-      const int64_t panel = block >> 3;
+      const int k = (u0 + u) * 256 + lq * 64;
+      const bool on0 = (u0 + u < u_end) & (k < d.K), on1 = on0 & (k + 32 < d.K);   // the two blocks
+      auto take = [&](__amdgpu_buffer_rsrc_t r, __amdgpu_buffer_rsrc_t rs, int row, bool on, uint32_t sc,
+                      u32x4 (&v)[2], uint32_t& scales) {
+        const uint32_t o = uint32_t(row * row_bytes + (k >> 1));
+        v[0] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, live_offset(on & on0, o), 0, 0));
+        v[1] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, live_offset(on & on1, o + 16u), 0, 0));
+        scales = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(rs, live_offset(on & on0, sc + 2u * lq), 0, 0));
+      };
 #pragma unroll
       for (int i = 0; i < RB; ++i) {
-        const int row = i * 16 + li;
-        const bool on = live && row < rows;
-        a[u][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                rw, on ? uint32_t(row * row_bytes + block * 16) : kDead, 0, 0));
-        sa[u][i] = on ? sw[panel * wstep + row * 8 + (block & 7)] : 0u;
+        const int r = i * 16 + li;
+        take(rw, rws, r, r < rows, uint32_t(u0 + u) * wstep + uint32_t(r0 + r) * 8u, s.a[u][i], s.sa[u][i]);
       }
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int t = j * 16 + li;
-        const bool on = live && t < toks;
-        b[u][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                rx, on ? uint32_t(t * row_bytes + block * 16) : kDead, 0, 0));
-        sb[u][j] = on ? sx[panel * xstep + t * 8 + (block & 7)] : 0u;
+        take(rx, rxs, t, t < toks, uint32_t(u0 + u) * xstep + uint32_t(g.t0 + t) * 8u, s.b[u][j], s.sb[u][j]);
       }
+    }
+  };
+  auto multiply = [&](int u0, Batch& s) {
+    // a block past K: zeros already, and the scale 1 whatever the panel holds there
+    if (d.K & 255) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if ((u0 + u) * 256 + lq * 64 + 32 >= d.K) {
+#pragma unroll
+          for (int i = 0; i < RB; ++i) s.sa[u][i] = (s.sa[u][i] & 0xFFu) | 0x7F00u;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) s.sb[u][j] = (s.sb[u][j] & 0xFFu) | 0x7F00u;
+        }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int i = 0; i < RB; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = mfma_fp4<0, 0>(a[u][i], b[u][j], acc[i][j], sa[u][i], sb[u][j]);
+        for (int j = 0; j < NT; ++j) {
+          acc[i][j] = mfma_fp4<0, 0>(s.a[u][i][0], s.b[u][j][0], acc[i][j], s.sa[u][i], s.sb[u][j]);
+          acc[i][j] = mfma_fp4<1, 1>(s.a[u][i][1], s.b[u][j][1], acc[i][j], s.sa[u][i], s.sb[u][j]);
+        }
+  };
+  for (int u = share * per; u < u_end; u += U) {
+    Batch b;
+    load(u, b);
+    __builtin_amdgcn_sched_barrier(0);   // every load goes out before the first product
+    multiply(u, b);
+  }
+  auto store = [&](int f, const f32x4& sum) {   // fragment f of the wave's rows
+    const int t = (f % NT) * 16 + li, r = r0 + (f / NT) * 16 + lq * 4;
+    if (t >= toks || r >= d.R) return;
+    const int64_t o = int64_t(g.t0 + t) * d.ldy + r;
+    const bool whole = (d.ldy & 3) == 0 && r + 3 < d.R;
+    if constexpr (OUT == NM_F32) {
+      float* y = static_cast<float*>(Y) + o;
+      if (whole) *reinterpret_cast<f32x4*>(y) = sum;
+      else for (int e = 0; e < 4 && r + e < d.R; ++e) y[e] = sum[e];
+    } else {
+      uint16_t* y = static_cast<uint16_t*>(Y) + o;
+      const u32x2 h = {pack_half2<OUT>(sum[0], sum[1]), pack_half2<OUT>(sum[2], sum[3])};
+      if (whole) *reinterpret_cast<u32x2*>(y) = h;
+      else for (int e = 0; e < 4 && r + e < d.R; ++e) y[e] = uint16_t(h[e >> 1] >> (16 * (e & 1)));
+    }
+  };
+  if (ks == 1) {
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) store(i * NT + j, acc[i][j]);
+    return;
   }
 #pragma unroll
   for (int i = 0; i < RB; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) part[wave][i * NT + j][lane] = acc[i][j];
   __syncthreads();
-  if (wave >= RB * NT) return;
-  f32x4 sum = part[0][wave][lane];
-#pragma unroll
-  for (int w = 1; w < kFewWaves; ++w) sum += part[w][wave][lane];
-  const int t = (wave % NT) * 16 + li, r = (wave / NT) * 16 + lq * 4;
-  if (t >= toks || r >= rows) return;
-  const int64_t o = int64_t(g.t0 + t) * d.ldy + r0 + r;
-  const bool whole = (d.ldy & 3) == 0 && r + 3 < rows;
-  if constexpr (OUT == NM_F32) {
-    float* y = static_cast<float*>(Y) + o;
-    if (whole) *reinterpret_cast<f32x4*>(y) = sum;
-    else for (int e = 0; e < 4 && r + e < rows; ++e) y[e] = sum[e];
-  } else {
-    uint16_t* y = static_cast<uint16_t*>(Y) + o;
-    const u32x2 h = {pack_half2<OUT>(sum[0], sum[1]), pack_half2<OUT>(sum[2], sum[3])};
-    if (whole) *reinterpret_cast<u32x2*>(y) = h;
-    else for (int e = 0; e < 4 && r + e < rows; ++e) y[e] = uint16_t(h[e >> 1] >> (16 * (e & 1)));
+  for (int f = share; f < RB * NT; f += ks) {
+    const int w0 = wave - share;
+    f32x4 sum = part[w0][f][lane];
+    for (int w = 1; w < ks; ++w) sum += part[w0 + w][f][lane];
+    store(f, sum);
   }
 }
 
@@ -558,19 +596,26 @@ hipError_t dequantize_dt(const MxQuantArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int OUT, int RB, int NT>
+template <int OUT, int RB, int NT, int U>
 hipError_t launch_few(const MxArgs& a, hipStream_t s) {
   MxDims d;
   d.E = int(a.E);
   d.R = int(a.R);
   d.K = int(a.K);
   d.T = int(a.T);
-  d.tilesR = int((a.R + 16 * RB - 1) / (16 * RB));
   d.ldy = a.ldy;
+  // shares of K: until there are 16 waves a compute unit, but none below two panels
+  // (11008 x 4096, 7 tokens, 1 / 2 / 4 / 8 shares: 15.6 / 10.1 / 9.7 / 8.4 us)
+  const int64_t weights = a.offsets ? std::min(a.E, a.T) : 1, tiles = (a.T / weights + 16 * NT - 1) / (16 * NT);
+  const int64_t blocks = (a.R + 16 * RB - 1) / (16 * RB), panels = (a.K + 255) / 256;
+  int ks = 1;
+  while (ks < kFewWaves && weights * tiles * blocks * ks < 16 * 256 && panels >= 2 * ks) ks *= 2;
+  const int64_t rows = 16 * RB * (kFewWaves / ks);
+  d.tilesR = int((a.R + rows - 1) / rows);
   const int64_t tilesT = a.offsets ? group_max_tiles(a.T, a.E, 16 * NT) : (a.T + 16 * NT - 1) / (16 * NT);
   if (tilesT * d.tilesR > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((mx_few_kernel<OUT, RB, NT>), dim3(unsigned(tilesT * d.tilesR)), dim3(kFewWaves * 64), 0, s, a.wq,
-                     a.ws, a.xq, a.xs, a.offsets, d, a.Y);
+  hipLaunchKernelGGL((mx_few_kernel<OUT, RB, NT, U>), dim3(unsigned(tilesT * d.tilesR)), dim3(kFewWaves * 64), 0, s, a.wq,
+                     a.ws, a.xq, a.xs, a.offsets, d, ks, a.Y);
   return hipGetLastError();
 }
 
@@ -613,9 +658,9 @@ MxPick pick(int64_t E, int64_t R, int64_t T, bool grouped) {
 template <int OUT>
 hipError_t gemm_out(const MxArgs& a, hipStream_t s) {
   switch (pick(a.E, a.R, a.T, a.offsets != nullptr)) {
-    case MxPick::few1: return launch_few<OUT, 1, 1>(a, s);
-    case MxPick::few2: return launch_few<OUT, 1, 2>(a, s);
-    case MxPick::few4: return launch_few<OUT, 2, 4>(a, s);
+    case MxPick::few1: return launch_few<OUT, 1, 1, 2>(a, s);
+    case MxPick::few2: return launch_few<OUT, 4, 2, 1>(a, s);
+    case MxPick::few4: return launch_few<OUT, 4, 4, 1>(a, s);
     case MxPick::middle: return launch_tiles<OUT, MxMiddle>(a, s);
     default: return launch_tiles<OUT, MxLarge>(a, s);
   }
