@@ -527,6 +527,13 @@ hipError_t pick_kernel(const GroupArgs& a, hipStream_t s) {
                                                        : launch_few<P, DT, OUT, 1, 1, 2>(a, s);
   if (mean <= 24) return launch_few<P, DT, OUT, 4, 2, 1>(a, s);
   if (mean <= 64) return launch_tile<P, DT, OUT, 64>(a, s);
+  if (P == 0 && spmm_lds_applies(a.base)) {
+    const int64_t tiles = group_max_tiles(a.base.T, a.E, spmm_lds_tile());
+    int4* table = static_cast<int4*>(a.workspace);
+    if (hipError_t e = launch_group_tiles(a.offsets, a.E, a.base.T, spmm_lds_tile(), tiles, table, s); e != hipSuccess)
+      return e;
+    return launch_spmm_lds_group(a.base, table, int(tiles), s);
+  }
   return launch_tile<P, DT, OUT, 128>(a, s);
 }
 

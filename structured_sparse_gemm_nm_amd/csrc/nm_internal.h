@@ -124,6 +124,9 @@ hipError_t launch_spmm_resident(const SpmmArgs& a, hipStream_t s);
 // All-LDS 2:4 kernel (nm_spmm_lds.hip) and the shapes it takes.
 bool spmm_lds_applies(const SpmmArgs& a);
 hipError_t launch_spmm_lds(const SpmmArgs& a, hipStream_t s);
+// The same of experts' rows (nm_group.h): a table of tiles of spmm_lds_tile() tokens.
+int spmm_lds_tile();
+hipError_t launch_spmm_lds_group(const SpmmArgs& a, const int4* table, int max_tiles, hipStream_t s);
 
 // All-LDS 1:4 / 1:8 kernel with 128 x 64 tiles (nm_spmm_lds_nm.hip) and the
 // shapes it takes.

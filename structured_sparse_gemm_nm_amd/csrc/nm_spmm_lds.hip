@@ -33,6 +33,7 @@
 // already load and read the first steps of the following one, so neither the
 // ring's fill nor the epilogue's stores leave the MFMAs idle between tiles.
 #include "nm_device.h"
+#include "nm_group.h"
 #include "nm_internal.h"
 #include "nm_lowrank.h"
 
@@ -59,7 +60,7 @@ constexpr int kRowRotate8 = 0x128;
 
 struct TileMap {
   int tilesR, tilesT, group_r, ntiles, grid;
-  __device__ void rt(int i, int& R0, int& T0) const {
+  __device__ void rt(int i, int& R0, int& tt) const {
     const int round = i / grid, p = i - round * grid;
     int q = p;
     if ((grid & 7) == 0 && (round + 1) * grid <= ntiles) q = (p & 7) * (grid >> 3) + (p >> 3);
@@ -69,15 +70,36 @@ struct TileMap {
     const int rem = b - grp * per_group;
     const int rows_in_grp = min(group_r, tilesR - grp * group_r);
     R0 = (grp * group_r + rem % rows_in_grp) * kBR;
-    T0 = (rem / rows_in_grp) * kBT;
+    tt = rem / rows_in_grp;
   }
 };
 
-template <int DT, int OUT, class LR>
+// Token tile tt of one weight: tokens from t0 on, below t1.
+struct OneWeight {
+  int T;
+  __device__ int tiles(int tilesT) const { return tilesT; }
+  __device__ GroupTile at(int tt) const { return GroupTile{0, tt * kBT, T}; }
+};
+// Of the experts' rows (nm_group.h): from the table, by scalar loads, which leave the
+// vector-memory counter that the ring goes by alone.
+struct ExpertTiles {
+  typedef const __attribute__((address_space(4))) u32x4* constant_ptr;
+  const int4* table;
+  __device__ int tiles(int) const { return int(((constant_ptr)table)[0][0]); }
+  __device__ GroupTile at(int tt) const {
+    const u32x4 e = ((constant_ptr)table)[1 + tt];
+    return GroupTile{int(e[0]), int(e[1]), int(e[2])};
+  }
+};
+
+template <int DT, int OUT, class LR, class GR>
 __global__ __launch_bounds__(256, 1) void spmm_lds_kernel(
     const uint16_t* __restrict__ values, const uint32_t* __restrict__ idx, int R, int K,
-    const uint16_t* __restrict__ act, int T, int64_t ldx, void* __restrict__ Y, int64_t ldy,
+    const uint16_t* __restrict__ act, GR rows, int64_t ldx, void* __restrict__ Y, int64_t ldy,
     TileMap tm, LR lowrank) {
+  tm.tilesT = rows.tiles(tm.tilesT);
+  tm.ntiles = tm.tilesR * tm.tilesT;
+  if (int(blockIdx.x) >= tm.ntiles) return;   // (the host knows only how many tiles there can be)
   constexpr int FR = 8, FT = kBT / 32;
   extern __shared__ __align__(16) unsigned char smem[];
   unsigned char* bbuf = smem;                              // [kNS][kStageB]
@@ -114,10 +136,12 @@ __global__ __launch_bounds__(256, 1) void spmm_lds_kernel(
     __amdgpu_buffer_rsrc_t a, b, i;
     uint32_t boff[4], aoff[4], ioff[4];
   };
-  auto make_src = [&](int R0, int T0, Src& o) {
+  auto make_src = [&](int R0, const GroupTile& g, Src& o) {
+    const int T0 = g.t0, T = g.t1;
+    const int64_t row = int64_t(g.e) * R + R0;
     o.b = make_rsrc(act + int64_t(T0) * ldx);
-    o.a = make_rsrc(values + int64_t(R0) * S);
-    o.i = make_rsrc(reinterpret_cast<const unsigned char*>(idx) + int64_t(R0) * irow_bytes);
+    o.a = make_rsrc(values + row * S);
+    o.i = make_rsrc(reinterpret_cast<const unsigned char*>(idx) + row * irow_bytes);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int slot = (wave * 4 + j) * 64 + lane;
@@ -219,14 +243,16 @@ __global__ __launch_bounds__(256, 1) void spmm_lds_kernel(
   // reads of the steps after it belong to the next tile, so a tile starts
   // with its first steps already in flight.
   int tile = blockIdx.x;
-  int R0, T0, nR0 = 0, nT0 = 0;
-  tm.rt(tile, R0, T0);
+  int R0, nR0 = 0, tt;
+  tm.rt(tile, R0, tt);
+  GroupTile g_cur = rows.at(tt), g_nxt = g_cur;
   Src cur, nxt;
-  make_src(R0, T0, cur);
+  make_src(R0, g_cur, cur);
   bool has_next = tile + tm.grid < tm.ntiles;
   if (has_next) {
-    tm.rt(tile + tm.grid, nR0, nT0);
-    make_src(nR0, nT0, nxt);
+    tm.rt(tile + tm.grid, nR0, tt);
+    g_nxt = rows.at(tt);
+    make_src(nR0, g_nxt, nxt);
   } else {
     nxt = cur;
   }
@@ -357,6 +383,7 @@ __global__ __launch_bounds__(256, 1) void spmm_lds_kernel(
   read_frags(0, 0, 0, a0, x0, b0);
 
   while (true) {
+    const int T0 = g_cur.t0, T = g_cur.t1;
     [[maybe_unused]] int ids = 0;
     if constexpr (std::is_same_v<LR, LowRank>) ids = lowrank_ids<FT>(lowrank, T0 + wt * (kBT / 2));
 #pragma unroll
@@ -505,22 +532,23 @@ __global__ __launch_bounds__(256, 1) void spmm_lds_kernel(
     }
     tile += tm.grid;
     R0 = nR0;
-    T0 = nT0;
+    g_cur = g_nxt;
     cur = nxt;
     g += nsteps;
     qb += nblocks;
     has_next = tile + tm.grid < tm.ntiles;
     if (has_next) {
-      tm.rt(tile + tm.grid, nR0, nT0);
-      make_src(nR0, nT0, nxt);
+      tm.rt(tile + tm.grid, nR0, tt);
+      g_nxt = rows.at(tt);
+      make_src(nR0, g_nxt, nxt);
     }
   }
 }
 
-template <int DT, int OUT, class LR>
-hipError_t launch_lds(const SpmmArgs& a, const LR& lowrank, hipStream_t s) {
+// tilesT: the token tiles, or, of experts' rows, as many as there can be.
+template <int DT, int OUT, class LR, class GR>
+hipError_t launch_lds(const SpmmArgs& a, const LR& lowrank, const GR& rows, int tilesT, hipStream_t s) {
   const int tilesR = int((a.R + kBR - 1) / kBR);
-  const int tilesT = int((a.T + kBT - 1) / kBT);
   const int64_t ntiles = int64_t(tilesR) * tilesT;
   if (ntiles > 0x7FFFFFFF) return hipErrorInvalidValue;
   const int cus = device_cu_count();
@@ -543,10 +571,10 @@ hipError_t launch_lds(const SpmmArgs& a, const LR& lowrank, hipStream_t s) {
   if (a.R * a.K <= (int64_t(4) << 20)) tm.group_r = tilesR;
   tm.ntiles = int(ntiles);
   tm.grid = int(walk && ntiles > cus ? cus : ntiles);
-  auto kern = spmm_lds_kernel<DT, OUT, LR>;
+  auto kern = spmm_lds_kernel<DT, OUT, LR, GR>;
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), kLds); e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3(unsigned(tm.grid)), dim3(256), kLds, s, a.values, a.idx, int(a.R),
-                     int(a.K), a.act, int(a.T), a.ldx, a.Y, a.ldy, tm, lowrank);
+                     int(a.K), a.act, rows, a.ldx, a.Y, a.ldy, tm, lowrank);
   return hipGetLastError();
 }
 
@@ -563,15 +591,26 @@ bool spmm_lds_applies(const SpmmArgs& a) {
   return device_max_lds() >= kLds;
 }
 
-template <class LR>
-static hipError_t launch_lds_lr(const SpmmArgs& a, const LR& lowrank, hipStream_t s) {
+template <class LR, class GR>
+static hipError_t launch_lds_type(const SpmmArgs& a, const LR& lowrank, const GR& rows, int tilesT, hipStream_t s) {
+  const bool f32 = a.out_dtype == NM_F32;
   if (a.dtype == NM_F16)
-    return a.out_dtype == NM_F32 ? launch_lds<NM_F16, NM_F32>(a, lowrank, s) : launch_lds<NM_F16, NM_F16>(a, lowrank, s);
-  return a.out_dtype == NM_F32 ? launch_lds<NM_BF16, NM_F32>(a, lowrank, s) : launch_lds<NM_BF16, NM_BF16>(a, lowrank, s);
+    return f32 ? launch_lds<NM_F16, NM_F32>(a, lowrank, rows, tilesT, s)
+               : launch_lds<NM_F16, NM_F16>(a, lowrank, rows, tilesT, s);
+  return f32 ? launch_lds<NM_BF16, NM_F32>(a, lowrank, rows, tilesT, s)
+             : launch_lds<NM_BF16, NM_BF16>(a, lowrank, rows, tilesT, s);
 }
 
 hipError_t launch_spmm_lds(const SpmmArgs& a, hipStream_t s) {
-  return a.lowrank ? launch_lds_lr(a, *a.lowrank, s) : launch_lds_lr(a, NoLowRank{}, s);
+  const OneWeight rows{int(a.T)};
+  const int tilesT = int((a.T + kBT - 1) / kBT);
+  return a.lowrank ? launch_lds_type(a, *a.lowrank, rows, tilesT, s) : launch_lds_type(a, NoLowRank{}, rows, tilesT, s);
+}
+
+// The same product of experts' rows, table filled for tiles of spmm_lds_tile() tokens.
+int spmm_lds_tile() { return kBT; }
+hipError_t launch_spmm_lds_group(const SpmmArgs& a, const int4* table, int max_tiles, hipStream_t s) {
+  return launch_lds_type(a, NoLowRank{}, ExpertTiles{table}, max_tiles, s);
 }
 
 }  // namespace nm
