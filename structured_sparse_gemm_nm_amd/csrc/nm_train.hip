@@ -533,51 +533,84 @@ __global__ __launch_bounds__(256, 2) void spmm_dw_kernel(const uint32_t* __restr
   wait_vmcnt<0>();
 
   // ---- epilogue: lane (r = li of the fragment, quarter q) holds D rows
-  // 4q..4q+3, columns k..k+3 of W's row r
+  // 4q..4q+3, columns k..k+3 of W's row r.  The wave's 128 columns of a row are VPR
+  // stored values and up to four index words, which every quarter loads; a fragment
+  // of 16 rows at a time is gathered in the wave's own part of LDS and leaves in
+  // whole rows (written from the lanes, a row's 128 or 256 bytes went out in pieces
+  // of 4 or 8, its index words came in two a fragment: 16 experts of 4096 x 2048,
+  // 8192 tokens, 232 us).
+  constexpr int VPR = 128 * N / M, ELT = OUT == NM_F32 ? 4 : 2;
+  constexpr int ROW = VPR * ELT, PITCH = ROW + 16;
+  constexpr int PIECE = P == 2 && ELT == 2 ? 8 : 16;   // bytes a store: whole 32 columns' worth
+  constexpr int IW = P == 0 ? 4 : 2;                   // index words of 128 columns
+  static_assert(4 * 16 * PITCH <= kDwLds, "the waves' gather areas");
+  wait_lgkm0();
+  barrier_no_fence();   // every wave is done with the stages
+  unsigned char* mine = smem + wave * (16 * PITCH);
+  const int kw = K0 + wk * 128;                        // the wave's first column
+  const int wbit = kw / M * N * B, w0 = wbit >> 5;     // (1:8: at bit 0 or 16 of a word)
+  const __amdgpu_buffer_rsrc_t ri = make_rsrc(idx, idx_bytes);
+  uint32_t iw[kDwFR][IW];
 #pragma unroll
   for (int rf = 0; rf < kDwFR; ++rf) {
     const int r = R0 + wr * 64 + rf * 16 + li;
 #pragma unroll
+    for (int e = 0; e < IW; ++e)
+      iw[rf][e] = __builtin_amdgcn_raw_buffer_load_b32(
+          ri, live_offset((r < R) & (w0 + e < idx_row_words), (uint32_t(r) * uint32_t(idx_row_words) + uint32_t(w0 + e)) * 4u),
+          0, 0);
+  }
+  const int valid = min(128, K - kw) * N / M;          // stored values of the row inside W (none: 0 or less)
+#pragma unroll
+  for (int rf = 0; rf < kDwFR; ++rf) {
+#pragma unroll
     for (int kf = 0; kf < kDwFK; ++kf) {
-      const int k = K0 + wk * 128 + kf * 16 + lq * 4;
-      if (r >= R || k >= K) continue;
       const f32x4 v = acc[kf][rf];
-      const int g = k / M;                          // the group holding k .. k+3
-      const int64_t sg = int64_t(g) * N;            // its first survivor
-      const int64_t bit = sg * B;
-      const uint32_t* irow = idx + int64_t(r) * idx_row_words;
-      const int64_t w = bit >> 5;
-      const uint64_t pair = uint64_t(irow[w]) |
-                            (w + 1 < idx_row_words ? uint64_t(irow[w + 1]) << 32 : uint64_t(0));
-      const uint32_t bits = uint32_t(pair >> (bit & 31));
       auto pick = [&](uint32_t p) {   // D value at in-lane column p (0..3)
         return p == 0 ? v[0] : p == 1 ? v[1] : p == 2 ? v[2] : v[3];
       };
-      const int64_t o = int64_t(r) * S + sg;
       if constexpr (P == 0) {
+        const uint32_t bits = iw[rf][kf >> 1] >> (16 * (kf & 1) + 4 * lq);
         const float x0 = pick(bits & 3u), x1 = pick((bits >> 2) & 3u);
-        if constexpr (OUT == NM_F32) {
-          float* y = static_cast<float*>(dW) + o;
-          y[0] = x0;
-          y[1] = x1;
-        } else {
-          *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(dW) + o) = pack_half2<DT>(x0, x1);
-        }
+        unsigned char* o = mine + li * PITCH + (kf * 4 + lq) * 2 * ELT;
+        if constexpr (OUT == NM_F32) *reinterpret_cast<f32x2_t*>(o) = f32x2_t{x0, x1};
+        else *reinterpret_cast<uint32_t*>(o) = pack_half2<DT>(x0, x1);
       } else {
-        const uint32_t pos = bits & (M - 1);
-        // 1:8: the survivor is in this lane's half of the group of eight only
-        // when its position's high bit matches the half
-        const bool mine = P == 1 || int(pos >> 2) == ((k % M) >> 2);
-        if (mine) {
+        // 1:4: a group a lane; 1:8: a group two lanes, of which the one whose half
+        // holds the survivor writes it
+        const int g = P == 1 ? kf * 4 + lq : kf * 2 + (lq >> 1);
+        uint32_t pos;
+        if constexpr (P == 1) {
+          pos = (iw[rf][kf >> 2] >> (8 * (kf & 3) + 2 * lq)) & 3u;
+        } else {
+          const uint64_t both = uint64_t(iw[rf][0]) | uint64_t(iw[rf][1]) << 32;
+          pos = uint32_t(both >> ((wbit & 31) + 3 * g)) & 7u;
+        }
+        if (P == 1 || int(pos >> 2) == (lq & 1)) {
           const float x = pick(pos & 3u);
-          if constexpr (OUT == NM_F32) {
-            static_cast<float*>(dW)[o] = x;
-          } else {
-            static_cast<uint16_t*>(dW)[o] = uint16_t(pack_half2<DT>(x, 0.f));
-          }
+          unsigned char* o = mine + li * PITCH + g * ELT;
+          if constexpr (OUT == NM_F32) *reinterpret_cast<float*>(o) = x;
+          else *reinterpret_cast<uint16_t*>(o) = uint16_t(pack_half2<DT>(x, 0.f));
         }
       }
     }
+    wait_lgkm0();
+    asm volatile("" ::: "memory");
+    constexpr int LPR = ROW / PIECE;   // lanes a row
+    constexpr int PASSES = (16 * LPR + 63) / 64;
+#pragma unroll
+    for (int it = 0; it < PASSES; ++it) {
+      const int slot = it * 64 + lane, row = slot / LPR, c = slot % LPR;
+      const int r = R0 + wr * 64 + rf * 16 + row;
+      if (r >= R || (c + 1) * (PIECE / ELT) > valid) continue;
+      unsigned char* o = static_cast<unsigned char*>(dW) + (int64_t(r) * S + kw / M * N) * ELT + c * PIECE;
+      if constexpr (PIECE == 16)
+        *reinterpret_cast<u32x4*>(o) = *reinterpret_cast<const u32x4*>(mine + row * PITCH + c * 16);
+      else
+        *reinterpret_cast<u32x2*>(o) = *reinterpret_cast<const u32x2*>(mine + row * PITCH + c * 8);
+    }
+    wait_lgkm0();   // read before the next fragment is gathered
+    asm volatile("" ::: "memory");
   }
 }
 
@@ -637,7 +670,10 @@ hipError_t launch_dx_cfg(const TrainArgs& a, const LR& lowrank, const GR& expert
   hipLaunchKernelGGL(kern, dim3(unsigned(tilesK * tilesT)), dim3(256), kDxLds, s, a.values,
                      uint32_t(a.values_bytes), a.idx, uint32_t(a.idx_bytes), int(a.R), int(a.K),
                      int(a.idx_row_words), a.G, int(a.T), a.ldg, a.out, a.ldo, int(tilesK), int(tilesT),
-                     pick_group(tilesK, tilesT, double(pat_n(P)) / pat_m(P), 1.0), lowrank, experts);
+                     // every column tile of an expert's tokens together: its weight is shared by few token
+                     // tiles only (16 experts of 4096 x 2048, 8192 tokens: 237 us with a single weight's order)
+                     a.offsets ? int(tilesK) : pick_group(tilesK, tilesT, double(pat_n(P)) / pat_m(P), 1.0), lowrank,
+                     experts);
   return hipGetLastError();
 }
 
