@@ -13,8 +13,8 @@ nm_mx_quantize, nm_mx_gemm, nm_grad_norm and nm_grad_clip.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 
 __all__ = ["NM_OK", "NM_F16", "NM_BF16", "NM_F32", "NM_I8", "NM_I32", "NM_FP8", "NMError", "lib", "lib_path",
@@ -916,171 +916,236 @@ def nm_xent_bwd(x, w, labels, lse, dloss, ignore_index: int = -100, out_dtype=No
 # products grouped by expert over packed weights
 # --------------------------------------------------------------------------
 
-def _on(device):
-    """Makes `device` the current one for a launch (nothing to do where it is)."""
-    torch = _torch()
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+# A few generated tokens spend longer in these functions than on the GPU, so they check plain
+# attributes once each, keep the sizes of workspaces by the numbers they follow from, and leave
+# the current device alone where it is the tensors'.
+
+_CODES = {}
+
+
+def _codes():
+    """torch dtype -> code of the types that the grouped products, the 4-bit floats and the gradients' norm
+    take or give."""
+    if not _CODES:
+        torch = _torch()
+        _CODES.update({torch.float16: NM_F16, torch.bfloat16: NM_BF16, torch.float32: NM_F32})
+    return _CODES
+
+
+def _elsewhere(device) -> bool:
+    """Whether `device` is not the current one (a launch on its stream needs it to be)."""
+    return _torch().cuda.current_device() != device.index
+
+
+def _need(size_of, *args) -> int:
+    b = ctypes.c_size_t()
+    _check(size_of(*args, ctypes.byref(b)))
+    return b.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _group_need(E, R, K, n, m, dt, T, od):
+    return _need(lib().nm_group_spmm_workspace_size, E, R, K, n, m, dt, T, od)
+
+
+@functools.lru_cache(maxsize=4096)
+def _group_dx_need(E, T):
+    return _need(lib().nm_group_spmm_dx_workspace_size, E, T)
+
+
+@functools.lru_cache(maxsize=4096)
+def _mx_need(E, R, K, T, grouped, od):
+    return _need(lib().nm_mx_gemm_workspace_size, E, R, K, T, grouped, od)
+
+
+def _scratch(need, like):
+    """(tensor to keep until the launch, its address) of a workspace."""
+    if not need:
+        return None, None
+    ws = like.new_empty(need, dtype=_torch().uint8)
+    return ws, ws.data_ptr()
 
 
 def _check_offsets(offsets, E, device):
-    torch = _torch()
-    if offsets.dtype != torch.int32 or offsets.shape != (E + 1,) or not offsets.is_contiguous() \
+    if offsets.dtype != _torch().int32 or offsets.shape != (E + 1,) or not offsets.is_contiguous() \
             or offsets.device != device:
         raise ValueError(f"offsets must be a contiguous int32 [{E + 1}] tensor on {device}")
 
 
-def _check_experts(idx, act, offsets, K, n, m):
-    """(E, R, T, dtype code) of index words [E, R, words] beside rows `act` (act or G)."""
+def _check_experts(idx, rows, name, width, offsets, K, n, m, out_dtype):
+    """(E, R, T, leading dimension, type's code, output's code) of index words [E, R, words] beside `rows`
+    (act or G) [T, width or, where that is None, R]."""
     torch = _torch()
-    if idx.dim() != 3 or act.dim() != 2:
-        raise ValueError("idx must be [experts, R, words] and the rows a matrix")
-    E, R = idx.shape[0], idx.shape[1]
-    dt = _dtype_code(act)
-    if dt not in (NM_F16, NM_BF16):
-        raise TypeError("grouped products take float16 or bfloat16 weights")
+    if idx.dim() != 3 or rows.dim() != 2:
+        raise ValueError(f"idx must be [experts, R, words] and {name} a matrix")
+    E, R, w = idx.shape
+    dt, dev = _codes().get(rows.dtype, NM_F32), rows.device
+    if dt == NM_F32:
+        raise TypeError(f"grouped products take float16 or bfloat16 weights, {name} is {rows.dtype}")
     if (n, m) not in PATTERNS or K < 16 or K % 16:
         nm_packed_sizes(R, K, n, m, dt)     # raises
     words = (K // m * n * (3 if m == 8 else 2) + 31) // 32
-    if idx.dtype != torch.int32 or idx.shape[2] != words or not idx.is_contiguous() or idx.device != act.device:
-        raise ValueError(f"idx must be a contiguous int32 [{E}, {R}, {words}] tensor on {act.device}")
-    _check_offsets(offsets, E, act.device)
-    _require_cuda(act)
-    return E, R, act.shape[0], dt
+    if w != words or idx.dtype != torch.int32 or not idx.is_contiguous() or idx.device != dev:
+        raise ValueError(f"idx must be a contiguous int32 [{E}, {R}, {words}] tensor on {dev}")
+    _check_offsets(offsets, E, dev)
+    T, cols = rows.shape
+    if cols != (R if width is None else width) or rows.stride(1) != 1:
+        raise ValueError(f"{name} must be [T, {R if width is None else width}] with unit stride along its rows")
+    if not rows.is_cuda:
+        raise ValueError("tensors must be on a HIP device (no CPU path)")
+    if out_dtype is None or out_dtype == torch.float32:
+        od = NM_F32
+    elif out_dtype == rows.dtype:
+        od = dt
+    else:
+        raise TypeError("out_dtype must be float32 or the weights' dtype")
+    return E, R, T, (rows.stride(0) if T > 1 else cols), dt, od
 
 
-def _check_expert_values(values, E, R, K, n, m, like):
-    S = K // m * n
+def _check_expert_values(values, E, R, S, like):
     if values.shape != (E, R, S) or values.dtype != like.dtype or not values.is_contiguous() \
             or values.device != like.device:
         raise ValueError(f"values must be a contiguous [{E}, {R}, {S}] {like.dtype} tensor on {like.device}")
 
 
-def _group_out(out, rows, cols, dt, out_dtype, like):
+def _rows_out(out, rows, cols, od, like):
+    """(output, its leading dimension): a fresh one, or the caller's, checked."""
     torch = _torch()
-    if out_dtype not in (None, torch.float32, like.dtype):
-        raise TypeError("out_dtype must be float32 or the weights' dtype")
-    od, otype = (dt, like.dtype) if out_dtype == like.dtype else (NM_F32, torch.float32)
     if out is None:
-        out = torch.empty((rows, cols), dtype=otype, device=like.device)
-    else:
-        _matrix(out, "out", rows, cols, otype, like.device)
-    return out, od
+        return (like.new_empty((rows, cols)) if _codes().get(like.dtype) == od
+                else like.new_empty((rows, cols), dtype=_torch_dtype(od))), cols
+    _matrix(out, "out", rows, cols, _torch_dtype(od), like.device)
+    return out, _row_stride(out)
 
 
 def nm_group_spmm(values, idx, act, offsets, K: int, n: int = 2, m: int = 4, out_dtype=None, out=None):
     """Y [T, R]: Y[t] = W_e act[t] for the rows offsets[e] <= t < offsets[e + 1] of expert e.
     values [E, R, K n / m], idx int32 [E, R, words]: E packed weights; act [T, K]; offsets int32
     [E + 1], on the device.  Rows of no expert stay as they were (in a fresh Y: undefined)."""
-    _row_major(act, "act")
-    E, R, T, dt = _check_experts(idx, act, offsets, K, n, m)
-    _check_expert_values(values, E, R, K, n, m, act)
-    _matrix(act, "act", T, K, values.dtype, values.device)
-    L = lib()
-    with _on(act.device):
-        out, od = _group_out(out, T, R, dt, out_dtype, act)
-        ws, need = _workspace(L.nm_group_spmm_workspace_size, E, R, K, n, m, dt, T, od, device=act.device)
-        _check(L.nm_group_spmm(values.data_ptr(), idx.data_ptr(), E, R, K, n, m, dt, act.data_ptr(), T, _row_stride(act),
-                               offsets.data_ptr(), out.data_ptr(), _row_stride(out), od, _ptr(ws), need,
-                               _stream_ptr(act.device)))
+    E, R, T, ldx, dt, od = _check_experts(idx, act, "act", K, offsets, K, n, m, out_dtype)
+    _check_expert_values(values, E, R, K // m * n, act)
+    dev = act.device
+    if _elsewhere(dev):
+        with _torch().cuda.device(dev):
+            return nm_group_spmm(values, idx, act, offsets, K, n, m, out_dtype, out)
+    out, ldy = _rows_out(out, T, R, od, act)
+    need = _group_need(E, R, K, n, m, dt, T, od)
+    ws, at = _scratch(need, act)
+    _check(lib().nm_group_spmm(values.data_ptr(), idx.data_ptr(), E, R, K, n, m, dt, act.data_ptr(), T, ldx,
+                               offsets.data_ptr(), out.data_ptr(), ldy, od, at, need, _stream_ptr(dev)))
     return out
 
 
 def nm_group_spmm_dx(values, idx, G, offsets, K: int, n: int = 2, m: int = 4, out_dtype=None, out=None):
     """dX [T, K] of nm_group_spmm from G = dL/dY [T, R]: dX[t] = W_e^T G[t]."""
-    _row_major(G, "G")
-    E, R, T, dt = _check_experts(idx, G, offsets, K, n, m)
-    _check_expert_values(values, E, R, K, n, m, G)
-    _matrix(G, "G", T, R, values.dtype, values.device)
-    L = lib()
-    with _on(G.device):
-        out, od = _group_out(out, T, K, dt, out_dtype, G)
-        ws, need = _workspace(L.nm_group_spmm_dx_workspace_size, E, T, device=G.device)
-        _check(L.nm_group_spmm_dx(values.data_ptr(), idx.data_ptr(), E, R, K, n, m, dt, G.data_ptr(), T, _row_stride(G),
-                                  offsets.data_ptr(), out.data_ptr(), _row_stride(out), od, _ptr(ws), need,
-                                  _stream_ptr(G.device)))
+    E, R, T, ldg, dt, od = _check_experts(idx, G, "G", None, offsets, K, n, m, out_dtype)
+    _check_expert_values(values, E, R, K // m * n, G)
+    dev = G.device
+    if _elsewhere(dev):
+        with _torch().cuda.device(dev):
+            return nm_group_spmm_dx(values, idx, G, offsets, K, n, m, out_dtype, out)
+    out, lddx = _rows_out(out, T, K, od, G)
+    need = _group_dx_need(E, T)
+    ws, at = _scratch(need, G)
+    _check(lib().nm_group_spmm_dx(values.data_ptr(), idx.data_ptr(), E, R, K, n, m, dt, G.data_ptr(), T, ldg,
+                                  offsets.data_ptr(), out.data_ptr(), lddx, od, at, need, _stream_ptr(dev)))
     return out
 
 
 def nm_group_spmm_dw(idx, G, act, offsets, K: int, n: int = 2, m: int = 4, out_dtype=None, out=None):
     """dW [E, R, K n / m] of nm_group_spmm: the gradient of every stored survivor of every expert
     (zeros for an expert without rows)."""
-    torch = _torch()
-    _row_major(G, "G")
-    _row_major(act, "act")
-    E, R, T, dt = _check_experts(idx, G, offsets, K, n, m)
-    _matrix(G, "G", T, R, act.dtype, act.device)
-    _matrix(act, "act", T, K, G.dtype, G.device)
-    S = K // m * n
-    L = lib()
-    with _on(G.device):
-        flat = out.view(E * R, S) if out is not None and out.shape == (E, R, S) and out.is_contiguous() else out
-        flat, od = _group_out(flat, E * R, S, dt, out_dtype, G)
-        if not flat.is_contiguous():
-            raise ValueError(f"out must be a contiguous [{E}, {R}, {S}] tensor")
-        _check(L.nm_group_spmm_dw(idx.data_ptr(), E, R, K, n, m, dt, G.data_ptr(), T, _row_stride(G), act.data_ptr(),
-                                  _row_stride(act), offsets.data_ptr(), flat.data_ptr(), od, _stream_ptr(G.device)))
-    return out if out is not None else flat.view(E, R, S)
+    E, R, T, ldg, dt, od = _check_experts(idx, G, "G", None, offsets, K, n, m, out_dtype)
+    dev = G.device
+    _matrix(act, "act", T, K, G.dtype, dev)
+    if _elsewhere(dev):
+        with _torch().cuda.device(dev):
+            return nm_group_spmm_dw(idx, G, act, offsets, K, n, m, out_dtype, out)
+    shape = (E, R, K // m * n)
+    if out is None:
+        out = G.new_empty(shape, dtype=_torch_dtype(od))
+    elif out.shape != shape or out.dtype != _torch_dtype(od) or not out.is_contiguous() or out.device != dev:
+        raise ValueError(f"out must be a contiguous {list(shape)} {_torch_dtype(od)} tensor on {dev}")
+    _check(lib().nm_group_spmm_dw(idx.data_ptr(), E, R, K, n, m, dt, G.data_ptr(), T, ldg, act.data_ptr(),
+                                  _row_stride(act), offsets.data_ptr(), out.data_ptr(), od, _stream_ptr(dev)))
+    return out
 
 
 # --------------------------------------------------------------------------
 # microscaled 4-bit floats
 # --------------------------------------------------------------------------
 
-def _mx_shapes(T, K):
-    if K < 32 or K % 32:
-        raise ValueError(f"K = {K} is not a positive multiple of 32")
-    return (T, K // 2), ((K + 255) // 256, T, 8)
-
-
 def nm_mx_quantize(x):
     """(q, scale) of x [T, K] or E weights [E, R, K] (float16, bfloat16 or float32): 4-bit values, two a
     byte, uint8 [T, K / 2], and a power of two for every 32 of a row, uint8 [ceil(K / 256), T, 8] (block i
     of row t at [i // 8, t, i % 8]); a leading axis of experts stays in front of both."""
     torch = _torch()
-    _require_cuda(x)
-    dt = _norm_code(x)
-    if x.dim() not in (2, 3) or x.stride(-1) != 1:
-        raise ValueError("x must be [T, K] or [experts, R, K] with unit stride along its rows")
-    lead, (T, K) = tuple(x.shape[:-2]), x.shape[-2:]
-    qs, ss = _mx_shapes(T, K)
-    with _on(x.device):
-        q = torch.empty(lead + qs, dtype=torch.uint8, device=x.device)
-        scale = torch.empty(lead + ss, dtype=torch.uint8, device=x.device)
-        stream = _stream_ptr(x.device)
-        for e in range(lead[0] if lead else 1):
-            xe, qe, se = (x[e], q[e], scale[e]) if lead else (x, q, scale)
-            _check(lib().nm_mx_quantize(xe.data_ptr(), T, K, _row_stride(xe), dt, qe.data_ptr(), se.data_ptr(), stream))
+    dt = _codes().get(x.dtype)
+    if dt is None:
+        raise TypeError(f"4-bit floats are made from float16, bfloat16 or float32, got {x.dtype}")
+    if not x.is_cuda:
+        raise ValueError("tensors must be on a HIP device (no CPU path)")
+    dev = x.device
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nm_mx_quantize(x)
+    if x.dim() == 3:
+        E, R, K = x.shape
+        q = x.new_empty((E, R, K // 2), dtype=torch.uint8)
+        scale = q.new_empty((E, (K + 255) // 256, R, 8))
+        for e in range(E):
+            _quantize(x[e], dt, q[e], scale[e], dev)
+        return q, scale
+    if x.dim() != 2:
+        raise ValueError("x must be [T, K] or [experts, R, K]")
+    T, K = x.shape
+    q = x.new_empty((T, K // 2), dtype=torch.uint8)
+    scale = q.new_empty(((K + 255) // 256, T, 8))
+    _quantize(x, dt, q, scale, dev)
     return q, scale
+
+
+def _quantize(x, dt, q, scale, dev):
+    T, K = x.shape
+    if x.stride(1) != 1:
+        raise ValueError("x must have unit stride along its rows")
+    _check(lib().nm_mx_quantize(x.data_ptr(), T, K, x.stride(0) if T > 1 else K, dt, q.data_ptr(), scale.data_ptr(),
+                                _stream_ptr(dev)))
 
 
 def nm_mx_dequantize(q, scale, dtype=None):
     """The values [T, K] (float32 unless dtype names bfloat16 or float16) of nm_mx_quantize's q, scale;
     [E, R, K] of a stack of weights."""
     torch = _torch()
-    _require_cuda(q)
     dtype = dtype or torch.float32
-    dt = _norm_code(torch.empty(0, dtype=dtype))
+    dt = _codes().get(dtype)
+    if dt is None:
+        raise TypeError(f"4-bit floats become float16, bfloat16 or float32, not {dtype}")
     if q.dim() not in (2, 3):
         raise ValueError("q must be [T, K / 2] or [experts, R, K / 2]")
-    lead, T, K = tuple(q.shape[:-2]), q.shape[-2], 2 * q.shape[-1]
-    _check_mx(q, scale, lead, T, K, "q", "scale", q.device)
-    with _on(q.device):
-        y = torch.empty(lead + (T, K), dtype=dtype, device=q.device)
-        stream = _stream_ptr(q.device)
-        for e in range(lead[0] if lead else 1):
-            ye, qe, se = (y[e], q[e], scale[e]) if lead else (y, q, scale)
-            _check(lib().nm_mx_dequantize(qe.data_ptr(), se.data_ptr(), T, K, ye.data_ptr(), K, dt, stream))
+    dev = q.device
+    _check_mx(q, scale, "q", "scale", dev)
+    if not q.is_cuda:
+        raise ValueError("tensors must be on a HIP device (no CPU path)")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nm_mx_dequantize(q, scale, dtype)
+    T, K = q.shape[-2], 2 * q.shape[-1]
+    y = q.new_empty(q.shape[:-1] + (K,), dtype=dtype)
+    for qe, se, ye in ((q, scale, y),) if q.dim() == 2 else zip(q, scale, y):
+        _check(lib().nm_mx_dequantize(qe.data_ptr(), se.data_ptr(), T, K, ye.data_ptr(), K, dt, _stream_ptr(dev)))
     return y
 
 
-def _check_mx(q, scale, lead, T, K, name_q, name_s, device):
-    torch = _torch()
-    qs, ss = _mx_shapes(T, K)
-    for t, name, shape in ((q, name_q, lead + qs), (scale, name_s, lead + ss)):
-        if t.dtype != torch.uint8 or t.shape != shape or not t.is_contiguous() or t.device != device:
-            raise ValueError(f"{name} must be a contiguous uint8 {list(shape)} tensor on {device}")
+def _check_mx(q, scale, name_q, name_s, device):
+    """An operand's two tensors: q [.., T, K / 2] and its scales."""
+    u8 = _torch().uint8
+    *lead, T, half = q.shape
+    if q.dtype != u8 or half < 16 or half % 16 or not q.is_contiguous() or q.device != device:
+        raise ValueError(f"{name_q} must be a contiguous uint8 [.., T, K / 2] tensor on {device}, K a multiple of 32")
+    shape = (*lead, (half + 127) // 128, T, 8)
+    if scale.dtype != u8 or scale.shape != shape or not scale.is_contiguous() or scale.device != device:
+        raise ValueError(f"{name_s} must be a contiguous uint8 {list(shape)} tensor on {device}")
 
 
 def nm_mx_gemm(wq, wscale, xq, xscale, offsets=None, out_dtype=None, out=None):
@@ -1088,29 +1153,29 @@ def nm_mx_gemm(wq, wscale, xq, xscale, offsets=None, out_dtype=None, out=None):
     offsets (int32 [E + 1], on the device) wq is [E, R, K / 2], and the rows offsets[e] <= t <
     offsets[e + 1] of x meet weight e; rows of no expert stay as they were.  float32, or out_dtype."""
     torch = _torch()
-    if xq.dim() != 2 or wq.dim() != (2 if offsets is None else 3):
+    dev = xq.device
+    grouped = offsets is not None
+    if xq.dim() != 2 or wq.dim() != 2 + grouped or wq.shape[-1] != xq.shape[1]:
         raise ValueError("xq must be [T, K / 2] and wq [R, K / 2] (with offsets [experts, R, K / 2])")
+    _check_mx(xq, xscale, "xq", "xscale", dev)
+    _check_mx(wq, wscale, "wq", "wscale", dev)
     T, K, R = xq.shape[0], 2 * xq.shape[1], wq.shape[-2]
-    E = 1 if offsets is None else wq.shape[0]
-    _check_mx(xq, xscale, (), T, K, "xq", "xscale", xq.device)
-    _check_mx(wq, wscale, () if offsets is None else (E,), R, K, "wq", "wscale", xq.device)
-    if offsets is not None:
-        _check_offsets(offsets, E, xq.device)
-    _require_cuda(xq)
-    otype = out_dtype or torch.float32
-    od = NM_F32 if otype == torch.float32 else NM_BF16 if otype == torch.bfloat16 else NM_F16
-    if otype not in (torch.float32, torch.bfloat16, torch.float16):
-        raise TypeError(f"out_dtype must be float32, bfloat16 or float16, not {otype}")
-    L = lib()
-    with _on(xq.device):
-        if out is None:
-            out = torch.empty((T, R), dtype=otype, device=xq.device)
-        else:
-            _matrix(out, "out", T, R, otype, xq.device)
-        ws, need = _workspace(L.nm_mx_gemm_workspace_size, E, R, K, T, int(offsets is not None), od, device=xq.device)
-        _check(L.nm_mx_gemm(wq.data_ptr(), wscale.data_ptr(), E, R, K, xq.data_ptr(), xscale.data_ptr(), T,
-                            _ptr(offsets), out.data_ptr(), _row_stride(out), od, _ptr(ws), need,
-                            _stream_ptr(xq.device)))
+    E = wq.shape[0] if grouped else 1
+    if grouped:
+        _check_offsets(offsets, E, dev)
+    od = NM_F32 if out_dtype is None else _codes().get(out_dtype)
+    if od is None:
+        raise TypeError(f"out_dtype must be float32, bfloat16 or float16, not {out_dtype}")
+    if not xq.is_cuda:
+        raise ValueError("tensors must be on a HIP device (no CPU path)")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nm_mx_gemm(wq, wscale, xq, xscale, offsets, out_dtype, out)
+    out, ldy = _rows_out(out, T, R, od, xq)
+    need = _mx_need(E, R, K, T, int(grouped), od)
+    ws, at = _scratch(need, xq)
+    _check(lib().nm_mx_gemm(wq.data_ptr(), wscale.data_ptr(), E, R, K, xq.data_ptr(), xscale.data_ptr(), T,
+                            _ptr(offsets), out.data_ptr(), ldy, od, at, need, _stream_ptr(dev)))
     return out
 
 
@@ -1137,7 +1202,7 @@ class GradList:
         if len(outs) != len(self.grads):
             raise ValueError(f"{len(outs)} outputs for {len(self.grads)} gradients")
         self.device = self.grads[0].device if self.grads else torch.device("cuda", torch.cuda.current_device())
-        codes = {torch.float32: NM_F32, torch.bfloat16: NM_BF16, torch.float16: NM_F16}
+        codes = _codes()
         dtypes = []
         for g, o in zip(self.grads, outs):
             code = codes.get(g.dtype)
@@ -1153,17 +1218,16 @@ class GradList:
         n = len(self.grads)
         # held, so that the memory behind an unchanged address is the same memory
         self._storage = [t.untyped_storage() for t in (*self.grads, *outs)]
+        self._tensors = self.grads + ([] if self.out is None else self.out)
         self._addresses = self._ask()
         self._grads = (ctypes.c_void_p * n)(*self._addresses[:n])
         self._outs = (ctypes.c_void_p * n)(*self._addresses[-n:]) if n else self._grads
         self._counts = (ctypes.c_int64 * n)(*(g.numel() for g in self.grads))
         self._dtypes = (ctypes.c_int * n)(*dtypes)
-        b = ctypes.c_size_t()
-        _check(lib().nm_grad_workspace_size(n, ctypes.byref(b)))
-        self._need = b.value
+        self._need = _need(lib().nm_grad_workspace_size, n)
 
     def _ask(self):
-        return [t.data_ptr() for t in self.grads] + ([] if self.out is None else [t.data_ptr() for t in self.out])
+        return list(map(_torch().Tensor.data_ptr, self._tensors))
 
     def _arrays(self):
         if self._ask() != self._addresses:
@@ -1177,38 +1241,35 @@ def nm_grad_list(grads, out=None) -> GradList:
     return GradList(grads, out)
 
 
-def _grad_workspace(grads):
+def _grad_call(grads, device, call):
+    """norm of a launch on the list's device: call(norm's address, workspace, its bytes, stream)."""
     torch = _torch()
-    return torch.empty(grads._need, dtype=torch.uint8, device=grads.device), grads._need
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return _grad_call(grads, device, call)
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    ws = torch.empty(grads._need, dtype=torch.uint8, device=device)
+    _check(call(norm.data_ptr(), ws.data_ptr(), grads._need, _stream_ptr(device)))
+    return norm
 
 
 def nm_grad_norm(grads):
     """The norm of all gradients together (a float32 scalar tensor): the square root of the sum of
     every element's square.  grads: tensors, or a GradList."""
-    torch = _torch()
     grads = grads if isinstance(grads, GradList) else GradList(grads)
     arrays = grads._arrays()
-    with _on(grads.device):
-        norm = torch.empty((), dtype=torch.float32, device=grads.device)
-        ws, need = _grad_workspace(grads)
-        _check(lib().nm_grad_norm(*arrays, norm.data_ptr(), ws.data_ptr(), need, _stream_ptr(grads.device)))
-    return norm
+    return _grad_call(grads, grads.device, lambda *at: lib().nm_grad_norm(*arrays, *at))
 
 
 def nm_grad_clip(grads, max_norm: float, eps: float = 1e-6, out=None):
     """(norm, outputs): every gradient times min(1, max_norm / (norm + eps)), in place or into `out`
     (tensors of the gradients' shapes and types); norm as nm_grad_norm gives it.  grads: tensors, or a
     GradList (which names its outputs itself)."""
-    torch = _torch()
-    if isinstance(grads, GradList):
-        if out is not None:
-            raise ValueError("a GradList names its outputs itself")
-    else:
+    if not isinstance(grads, GradList):
         grads = GradList(grads, out)
+    elif out is not None:
+        raise ValueError("a GradList names its outputs itself")
     arrays = grads._arrays()
-    with _on(grads.device):
-        norm = torch.empty((), dtype=torch.float32, device=grads.device)
-        ws, need = _grad_workspace(grads)
-        _check(lib().nm_grad_clip(*arrays, max_norm, eps, grads._outs, norm.data_ptr(), ws.data_ptr(), need,
-                                  _stream_ptr(grads.device)))
+    norm = _grad_call(grads, grads.device,
+                      lambda *at: lib().nm_grad_clip(*arrays, max_norm, eps, grads._outs, *at))
     return norm, (grads.grads if grads.out is None else grads.out)
