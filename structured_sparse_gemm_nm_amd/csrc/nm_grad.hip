@@ -28,22 +28,29 @@ constexpr int kVecs = kChunkBytes / 16 / kThreads;   // 16-byte vectors a thread
 // 16 bytes at any element's address.
 typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 
-// Tensors of one launch: addresses, counts, first chunks and types.
+// Tensors of one launch, in as few bytes as hold them: kernel arguments end at 4 KB,
+// and every launch costs 3 us of the host's time.
 template <int N, bool OUT>
 struct Batch {
   const void* p[N];
   void* out[OUT ? N : 1];
-  int64_t n[N];
   uint32_t start[N + 1];   // first chunk; start[count] is the launch's number of chunks
+  uint16_t tail[N];        // elements of the last chunk, less one
   uint8_t dtype[N];
   int count;
 };
-// Kernel arguments stay below 4 KB.
-constexpr int kNormTensors = 180, kClipTensors = 132;
+constexpr int kNormTensors = 262, kClipTensors = 170;
 using NormBatch = Batch<kNormTensors, false>;
 using ClipBatch = Batch<kClipTensors, true>;
-static_assert(int64_t(kNormTensors) * (kGradMaxCount / (32768 / 4)) < 0x7FFFFFFF, "chunks of a launch");
+static_assert(int64_t(kNormTensors) * (kGradMaxCount / (kChunkBytes / 4)) < 0xFFFF0000, "chunks of a launch");
 static_assert(sizeof(NormBatch) <= 3968 && sizeof(ClipBatch) <= 3968, "kernel argument size");
+
+constexpr int chunk_elements(int dtype) { return kChunkBytes / (dtype == NM_F32 ? 4 : 2); }
+
+template <class B>
+__device__ inline int64_t count_of(const B& b, int t) {
+  return int64_t(b.start[t + 1] - b.start[t] - 1) * chunk_elements(b.dtype[t]) + b.tail[t] + 1;
+}
 
 template <class B>
 __device__ inline int find(const B& b, uint32_t chunk) {
@@ -140,7 +147,7 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const NormBatch b, 
     while (c >= b.start[t + 1]) ++t;
     const int64_t local = int64_t(c - b.start[t]);
     const void* p = b.p[t];
-    const int64_t n = b.n[t];
+    const int64_t n = count_of(b, t);
     const int dt = b.dtype[t];
     if (dt == NM_F32) s += chunk_squares<NM_F32>(p, n, local);
     else if (dt == NM_BF16) s += chunk_squares<NM_BF16>(p, n, local);
@@ -221,7 +228,7 @@ __global__ __launch_bounds__(kThreads) void grad_clip_kernel(const ClipBatch b, 
     const int64_t local = int64_t(c - b.start[t]);
     const void* p = b.p[t];
     void* o = b.out[t];
-    const int64_t n = b.n[t];
+    const int64_t n = count_of(b, t);
     const int dt = b.dtype[t];
     if (dt == NM_F32) chunk_scale<NM_F32>(p, o, n, local, pre, coef);
     else if (dt == NM_BF16) chunk_scale<NM_BF16>(p, o, n, local, pre, coef);
@@ -236,11 +243,6 @@ __global__ __launch_bounds__(kThreads) void grad_clip_kernel(const ClipBatch b, 
 constexpr int kMaxGrid = 2048;
 constexpr int kSelfSum = 4096;   // partial sums a clipping workgroup still adds itself
 
-inline int64_t chunks_of(int64_t n, int dtype) {
-  const int64_t e = kChunkBytes / (dtype == NM_F32 ? 4 : 2);
-  return (n + e - 1) / e;
-}
-
 // Fills b with the tensors from i on (empty ones are left out), up to its size;
 // returns the next tensor.
 template <class B, int N>
@@ -252,9 +254,10 @@ int64_t fill(B& b, const GradArgs& a, int64_t i) {
     const int k = b.count++;
     b.p[k] = a.grads[i];
     if constexpr (sizeof(b.out) > sizeof(void*)) b.out[k] = a.out[i];
-    b.n[k] = a.counts[i];
+    const int64_t per = chunk_elements(a.dtypes[i]), chunks = (a.counts[i] + per - 1) / per;
+    b.tail[k] = uint16_t(a.counts[i] - (chunks - 1) * per - 1);
     b.dtype[k] = uint8_t(a.dtypes[i]);
-    b.start[k + 1] = b.start[k] + uint32_t(chunks_of(a.counts[i], a.dtypes[i]));   // below 2^31: kGradMaxCount
+    b.start[k + 1] = b.start[k] + uint32_t(chunks);   // below 2^32: kGradMaxCount
   }
   return i;
 }

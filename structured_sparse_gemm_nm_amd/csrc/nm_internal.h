@@ -331,7 +331,7 @@ struct GradArgs {
   void* workspace = nullptr;          // grad_workspace bytes
 };
 constexpr int64_t kGradMaxTensors = 16384;
-constexpr int64_t kGradMaxCount = int64_t(1) << 36;   // elements a tensor: a launch's chunks stay below 2^31
+constexpr int64_t kGradMaxCount = int64_t(1) << 36;   // elements a tensor: a launch's chunks stay below 2^32
 size_t grad_workspace(int64_t tensors);
 hipError_t launch_grad(const GradArgs& a, hipStream_t s);
 
