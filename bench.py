@@ -89,13 +89,16 @@ CSRC = os.path.join(ROOT, "structured_sparse_gemm_nm_amd", "csrc")
 KERNEL_SOURCES = {
     "spmm": ["nm_spmm.hip", "nm_spmm_lds.hip", "nm_spmm_lds_nm.hip", "nm_spmm_decode.hip",
              "nm_spmm_pipe.hip", "nm_spmm_resident.hip", "nm_permute.hip", "nm_int8.hip", "nm_lowrank.h",
-             "nm_widen.h"],
+             "nm_widen.h", "nm_group.h", "nm_offsets.h"],
     "hybrid": ["nm_hybrid.hip", "nm_select.h"],
     "host": ["nm_hosts.hip"],
-    "train": ["nm_train.hip", "nm_lowrank.h"],
+    "train": ["nm_train.hip", "nm_lowrank.h", "nm_group.h", "nm_offsets.h"],
     "adapter": ["nm_adapter.hip", "nm_adapter_product.hip", "nm_lowrank.h", "nm_piece.h", "nm_widen.h"],
     "layernorm": ["nm_layernorm.hip"],
     "xent": ["nm_xent.hip", "nm_gemm_nt.h"],
+    "group": ["nm_group.hip", "nm_group.h", "nm_offsets.h", "nm_widen.h"],
+    "mx": ["nm_mx.hip", "nm_group.h", "nm_offsets.h"],
+    "grad": ["nm_grad.hip"],
 }
 SHARED_SOURCES = ["nm_device.h", "nm_internal.h", "nm_api.cpp"]
 

@@ -65,4 +65,38 @@ inline size_t group_table_bytes(int64_t max_tiles) { return size_t(max_tiles + 1
 hipError_t launch_group_tiles(const int32_t* offsets, int64_t E, int64_t T, int BT, int64_t max_tiles, int4* table,
                               hipStream_t s);
 
+// Kernels of one tile a workgroup look for it themselves where the experts are few
+// (under a microsecond for 64, behind the other workgroups' work; the table is a
+// launch of 4 us before them), and read the table where they are many.
+constexpr int64_t kFindExperts = 256;
+struct GroupRows {
+  const int32_t* offsets;   // null: one weight for all rows
+  const int4* table;        // null: look for the tile
+  int E;
+  __device__ bool tile(int tt, int T, int BT, GroupTile& g) const {
+    if (!offsets) {
+      g = GroupTile{0, tt * BT, T};
+      return true;
+    }
+    if (!table) return group_find(offsets, E, T, BT, tt, g);
+    if (tt >= table[0].x) return false;
+    const int4 e = table[1 + tt];
+    g = GroupTile{e.x, e.y, e.z};
+    return true;
+  }
+};
+
+// The rows of a launch of tiles of BT tokens, its table (if any) filled in `workspace`
+// of group_rows_bytes.
+inline size_t group_rows_bytes(int64_t E, int64_t max_tiles) {
+  return E > kFindExperts ? group_table_bytes(max_tiles) : 0;
+}
+inline hipError_t group_rows(const int32_t* offsets, int64_t E, int64_t T, int BT, int64_t max_tiles, void* workspace,
+                             hipStream_t s, GroupRows& rows) {
+  rows = GroupRows{offsets, nullptr, int(E)};
+  if (!offsets || E <= kFindExperts) return hipSuccess;
+  rows.table = static_cast<int4*>(workspace);
+  return launch_group_tiles(offsets, E, T, BT, max_tiles, static_cast<int4*>(workspace), s);
+}
+
 }  // namespace nm

@@ -21,7 +21,7 @@ constexpr int kTableThreads = 1024;
 
 __global__ __launch_bounds__(kTableThreads) void group_tiles_kernel(const int32_t* __restrict__ offsets, int E, int T,
                                                                     int BT, int max_tiles, int4* __restrict__ table) {
-  __shared__ int start[kTableThreads + 1], wsum[kTableThreads / 64];
+  __shared__ int start[kTableThreads + 1], first[kTableThreads], last[kTableThreads], wsum[kTableThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int before = 0;
   for (int e0 = 0; e0 < E; e0 += kTableThreads) {
@@ -35,6 +35,8 @@ __global__ __launch_bounds__(kTableThreads) void group_tiles_kernel(const int32_
       if (lane >= o) sum = tile_sum(sum, up);
     }
     if (lane == 63) wsum[wave] = sum;
+    first[tid] = lo;
+    last[tid] = hi;
     __syncthreads();
     int base = before;
     for (int w = 0; w < wave; ++w) base = tile_sum(base, wsum[w]);
@@ -50,9 +52,7 @@ __global__ __launch_bounds__(kTableThreads) void group_tiles_kernel(const int32_
         if (start[m] <= i) a = m;
         else b = m;
       }
-      int l, h;
-      group_range(offsets, e0 + a, T, l, h);
-      table[1 + i] = make_int4(e0 + a, l + (i - start[a]) * BT, h, 0);
+      table[1 + i] = make_int4(e0 + a, first[a] + (i - start[a]) * BT, last[a], 0);
     }
     before = start[kTableThreads];
     __syncthreads();
@@ -302,8 +302,7 @@ template <int P, int DT, int OUT, int BT>
 __global__ __launch_bounds__(256, 2) void group_tile_kernel(const uint16_t* __restrict__ values,
                                                             const uint32_t* __restrict__ idx,
                                                             const uint16_t* __restrict__ act,
-                                                            const int4* __restrict__ table, GroupDims d,
-                                                            void* __restrict__ Y) {
+                                                            GroupRows experts, GroupDims d, void* __restrict__ Y) {
   constexpr int FR = 4, FT = BT / 32;
   constexpr int kStageB = BT * 128, kStage = kStageA + kStageI + kStageB;
   constexpr int PB = BT / 32;   // 16-byte pieces of the tokens a thread loads a step
@@ -312,19 +311,18 @@ __global__ __launch_bounds__(256, 2) void group_tile_kernel(const uint16_t* __re
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lq = lane >> 4;
   const int wr = wave >> 1, wt = wave & 1;
-  const int ntiles = table[0].x;
   const int b0 = blockIdx.x;
   const int tt = b0 / d.tilesR, tr = b0 - tt * d.tilesR;
-  if (tt >= ntiles) return;
-  const int4 g = table[1 + tt];
+  GroupTile g;
+  if (!experts.tile(tt, d.T, BT, g)) return;
   const int r0 = tr * kBR;
-  const int rows = min(kBR, d.R - r0), toks = min(BT, g.z - g.y);
+  const int rows = min(kBR, d.R - r0), toks = min(BT, g.t1 - g.t0);
   const int64_t S = int64_t(d.K) / pat_m(P) * pat_n(P);
-  const __amdgpu_buffer_rsrc_t rv = make_rsrc(values + (int64_t(g.x) * d.R + r0) * S, uint32_t(rows * S * 2));
+  const __amdgpu_buffer_rsrc_t rv = make_rsrc(values + (int64_t(g.e) * d.R + r0) * S, uint32_t(rows * S * 2));
   const __amdgpu_buffer_rsrc_t ri =
-      make_rsrc(idx + (int64_t(g.x) * d.R + r0) * d.words, uint32_t(int64_t(rows) * d.words * 4));
+      make_rsrc(idx + (int64_t(g.e) * d.R + r0) * d.words, uint32_t(int64_t(rows) * d.words * 4));
   const __amdgpu_buffer_rsrc_t rx =
-      make_rsrc(act + int64_t(g.y) * d.ldx, uint32_t((int64_t(toks - 1) * d.ldx + d.K) * 2));
+      make_rsrc(act + int64_t(g.t0) * d.ldx, uint32_t((int64_t(toks - 1) * d.ldx + d.K) * 2));
   const int steps = (d.K + 63) >> 6;
 
   // this thread's share of W: 32 columns (half wh of the step) of row wrow
@@ -468,7 +466,7 @@ __global__ __launch_bounds__(256, 2) void group_tile_kernel(const uint16_t* __re
     for (int j = 0; j < FT; ++j) {
       const int t = wt * (BT / 2) + j * 16 + li;
       if (t < toks && r < rows)
-        store4<DT, OUT>(Y, int64_t(g.y + t) * d.ldy + r0 + r, vec && r + 3 < rows, rows - r, acc[i][j]);
+        store4<DT, OUT>(Y, int64_t(g.t0 + t) * d.ldy + r0 + r, vec && r + 3 < rows, rows - r, acc[i][j]);
     }
   }
 }
@@ -508,40 +506,51 @@ hipError_t launch_tile(const GroupArgs& a, hipStream_t s) {
   const GroupDims d = dims_of(a, kBR);
   const int64_t tiles = group_max_tiles(a.base.T, a.E, BT);
   if (tiles * d.tilesR > 0x7FFFFFFF) return hipErrorInvalidValue;
-  int4* table = static_cast<int4*>(a.workspace);
-  if (hipError_t e = launch_group_tiles(a.offsets, a.E, a.base.T, BT, tiles, table, s); e != hipSuccess) return e;
+  GroupRows rows;
+  if (hipError_t e = group_rows(a.offsets, a.E, a.base.T, BT, tiles, a.workspace, s, rows); e != hipSuccess) return e;
   hipLaunchKernelGGL((group_tile_kernel<P, DT, OUT, BT>), dim3(unsigned(tiles * d.tilesR)), dim3(256), 0, s,
-                     a.base.values, a.base.idx, a.base.act, table, d, a.base.Y);
+                     a.base.values, a.base.idx, a.base.act, rows, d, a.base.Y);
   return hipGetLastError();
 }
 
 // Tokens an expert has on average, of the experts that can have any.
 int64_t mean_rows(int64_t T, int64_t E) { return T / std::max<int64_t>(1, std::min(T, E)); }
 
-template <int P, int DT, int OUT>
-hipError_t pick_kernel(const GroupArgs& a, hipStream_t s) {
-  const int64_t mean = mean_rows(a.base.T, a.E);
+// Which kernel: by the rows an expert has on average, of those that can have any.
+enum class Pick { few1, few1_wide, few2, tile64, tile128, lds };
+
+Pick pick(const SpmmArgs& b, int64_t E) {
+  const int64_t mean = mean_rows(b.T, E);
   // 64 rows a wave (the tokens are read a quarter as often) where that leaves waves enough
-  if (mean <= 8)
-    return std::min(a.base.T, a.E) * a.base.R >= 12288 ? launch_few<P, DT, OUT, 4, 1, 1>(a, s)
-                                                       : launch_few<P, DT, OUT, 1, 1, 2>(a, s);
-  if (mean <= 24) return launch_few<P, DT, OUT, 4, 2, 1>(a, s);
-  if (mean <= 64) return launch_tile<P, DT, OUT, 64>(a, s);
-  if (P == 0 && spmm_lds_applies(a.base)) {
-    const int64_t tiles = group_max_tiles(a.base.T, a.E, spmm_lds_tile());
-    int4* table = static_cast<int4*>(a.workspace);
-    if (hipError_t e = launch_group_tiles(a.offsets, a.E, a.base.T, spmm_lds_tile(), tiles, table, s); e != hipSuccess)
-      return e;
-    return launch_spmm_lds_group(a.base, table, int(tiles), s);
+  if (mean <= 8) return std::min(b.T, E) * b.R >= 12288 ? Pick::few1_wide : Pick::few1;
+  if (mean <= 24) return Pick::few2;
+  if (mean <= 64) return Pick::tile64;
+  // (by numbers alone: the workspace's size is asked for without a device)
+  return b.n == 2 && b.K % 128 == 0 && b.R >= 256 ? Pick::lds : Pick::tile128;
+}
+
+template <int P, int DT, int OUT>
+hipError_t launch_pick(const GroupArgs& a, hipStream_t s) {
+  switch (pick(a.base, a.E)) {
+    case Pick::few1: return launch_few<P, DT, OUT, 1, 1, 2>(a, s);
+    case Pick::few1_wide: return launch_few<P, DT, OUT, 4, 1, 1>(a, s);
+    case Pick::few2: return launch_few<P, DT, OUT, 4, 2, 1>(a, s);
+    case Pick::tile64: return launch_tile<P, DT, OUT, 64>(a, s);
+    case Pick::tile128: return launch_tile<P, DT, OUT, 128>(a, s);
+    default: break;
   }
-  return launch_tile<P, DT, OUT, 128>(a, s);
+  const int64_t tiles = group_max_tiles(a.base.T, a.E, spmm_lds_tile());
+  int4* table = static_cast<int4*>(a.workspace);
+  if (hipError_t e = launch_group_tiles(a.offsets, a.E, a.base.T, spmm_lds_tile(), tiles, table, s); e != hipSuccess)
+    return e;
+  return launch_spmm_lds_group(a.base, table, int(tiles), s);
 }
 
 template <int P>
 hipError_t pick_type(const GroupArgs& a, hipStream_t s) {
   const bool f32 = a.base.out_dtype == NM_F32;
-  if (a.base.dtype == NM_F16) return f32 ? pick_kernel<P, NM_F16, NM_F32>(a, s) : pick_kernel<P, NM_F16, NM_F16>(a, s);
-  return f32 ? pick_kernel<P, NM_BF16, NM_F32>(a, s) : pick_kernel<P, NM_BF16, NM_BF16>(a, s);
+  if (a.base.dtype == NM_F16) return f32 ? launch_pick<P, NM_F16, NM_F32>(a, s) : launch_pick<P, NM_F16, NM_F16>(a, s);
+  return f32 ? launch_pick<P, NM_BF16, NM_F32>(a, s) : launch_pick<P, NM_BF16, NM_BF16>(a, s);
 }
 
 }  // namespace
@@ -553,9 +562,16 @@ hipError_t launch_group_tiles(const int32_t* offsets, int64_t E, int64_t T, int 
   return hipGetLastError();
 }
 
-size_t group_workspace(const SpmmArgs& base, int64_t E) { return group_table_bytes(group_max_tiles(base.T, E, 64)); }
+size_t group_workspace(const SpmmArgs& base, int64_t E) {
+  switch (pick(base, E)) {
+    case Pick::tile64: return group_rows_bytes(E, group_max_tiles(base.T, E, 64));
+    case Pick::tile128: return group_rows_bytes(E, group_max_tiles(base.T, E, 128));
+    case Pick::lds: return group_table_bytes(group_max_tiles(base.T, E, spmm_lds_tile()));
+    default: return 0;
+  }
+}
 
-size_t group_dx_workspace(int64_t T, int64_t E) { return group_table_bytes(spmm_dx_max_tiles(T, E)); }
+size_t group_dx_workspace(int64_t T, int64_t E) { return group_rows_bytes(E, spmm_dx_max_tiles(T, E)); }
 
 hipError_t launch_group(const GroupArgs& a, hipStream_t s) {
   if (a.base.n == 2) return pick_type<0>(a, s);

@@ -333,7 +333,7 @@ struct MxTileDims {
 template <int OUT, class C>
 __global__ __launch_bounds__(C::THREADS, 2) void mx_tile_kernel(
     const uint8_t* __restrict__ wq, const uint8_t* __restrict__ ws, const uint8_t* __restrict__ xq,
-    const uint8_t* __restrict__ xs, const int4* __restrict__ table, MxTileDims d, void* __restrict__ Y) {
+    const uint8_t* __restrict__ xs, GroupRows experts, MxTileDims d, void* __restrict__ Y) {
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -341,12 +341,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void mx_tile_kernel(
   const int wm = wave / C::WN, wn = wave % C::WN;
   int tt, tr;
   grouped_tile(xcd_tile(blockIdx.x, gridDim.x), d.tilesT, d.tilesR, d.group, tt, tr);
-  GroupTile g{0, tt * C::BN, d.T};
-  if (table) {
-    if (tt >= table[0].x) return;
-    const int4 e = table[1 + tt];
-    g = GroupTile{e.x, e.y, e.z};
-  }
+  GroupTile g;
+  if (!experts.tile(tt, d.T, C::BN, g)) return;
   const int r0 = tr * C::BM;
   const int row_bytes = d.K >> 1, steps = (d.K + 255) >> 8;
   const int rem = d.K - (steps - 1) * 256;   // columns of the last step
@@ -632,12 +628,11 @@ hipError_t launch_tiles(const MxArgs& a, hipStream_t s) {
   d.tilesT = int(tilesT);
   d.group = int(std::min<int64_t>(tilesT, 4));
   d.ldy = a.ldy;
-  int4* table = a.offsets ? static_cast<int4*>(a.workspace) : nullptr;
-  if (table)
-    if (hipError_t e = launch_group_tiles(a.offsets, a.E, a.T, C::BN, tilesT, table, s); e != hipSuccess) return e;
+  GroupRows rows;
+  if (hipError_t e = group_rows(a.offsets, a.E, a.T, C::BN, tilesT, a.workspace, s, rows); e != hipSuccess) return e;
   auto kern = mx_tile_kernel<OUT, C>;
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), C::LDS); e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3(unsigned(tilesR * tilesT)), dim3(C::THREADS), C::LDS, s, a.wq, a.ws, a.xq, a.xs, table, d,
+  hipLaunchKernelGGL(kern, dim3(unsigned(tilesR * tilesT)), dim3(C::THREADS), C::LDS, s, a.wq, a.ws, a.xq, a.xs, rows, d,
                      a.Y);
   return hipGetLastError();
 }
@@ -681,7 +676,7 @@ hipError_t launch_mx_dequantize(const MxQuantArgs& a, hipStream_t s) {
 size_t mx_workspace(int64_t E, int64_t R, int64_t T, bool grouped) {
   const MxPick p = pick(E, R, T, grouped);
   if (!grouped || (p != MxPick::middle && p != MxPick::large)) return 0;
-  return group_table_bytes(group_max_tiles(T, E, p == MxPick::middle ? MxMiddle::BN : MxLarge::BN));
+  return group_rows_bytes(E, group_max_tiles(T, E, p == MxPick::middle ? MxMiddle::BN : MxLarge::BN));
 }
 
 hipError_t launch_mx_gemm(const MxArgs& a, hipStream_t s) {

@@ -36,9 +36,9 @@ namespace {
 
 // In the place of the experts' rows: one weight for all tokens.
 struct NoGroup {};
-// dX: the tiles' table, and from one expert's values (index words) to the next.
+// dX: the tiles, and from one expert's values (index words) to the next.
 struct GroupDx {
-  const int4* table;
+  GroupRows rows;
   int64_t values_stride, idx_stride;
 };
 // dW: the experts' rows, from one's index words to the next, and its gradient (bytes).
@@ -73,11 +73,24 @@ constexpr int pat_m(int P) { return P == 2 ? 8 : 4; }
 // LDS two workgroups share a compute unit, each covering the other's barrier
 // and epilogue.
 // ---------------------------------------------------------------------------
-constexpr int kDxBK = 128, kDxBT = 128, kDxRC = 64;
-constexpr int kDxGStage = kDxBT * kDxRC * 2;     // 16 KB
-constexpr int kDxWRow = kDxBK * 2 + 32;          // 288 bytes: padded row of the W tile
-constexpr int kDxWTile = kDxRC * kDxWRow;        // 18 KB
-constexpr int kDxLds = 2 * kDxGStage + 2 * kDxWTile;
+// WIDE: 256 k x 128 t in chunks of 32 rows (a wave 128 x 64): the same products a
+// barrier, a quarter fewer LDS bytes for each, which is what bounds the kernel where
+// its tiles fill the chip.
+constexpr int kDxBT = 128;
+template <bool WIDE>
+struct DxTile {
+  static constexpr int BK = WIDE ? 256 : 128, RC = WIDE ? 32 : 64;
+  static constexpr int FK = BK / 32;              // a wave's fragments along k
+  static constexpr int CPR = RC / 8;              // 16-byte pieces of a token's chunk of G
+  static constexpr int NG = kDxBT * CPR / 256;    // of them a thread loads
+  static constexpr int GStage = kDxBT * RC * 2;
+  static constexpr int WRow = BK * 2 + 32;        // padded row of the W tile
+  static constexpr int WTile = RC * WRow;
+  static constexpr int LDS = 2 * GStage + 2 * WTile;
+  __device__ static int piece(int tok, int c) {   // the slot of piece c of a token
+    return tok * CPR + (WIDE ? c ^ ((tok >> 1) & 3) : c ^ (tok & 7));
+  }
+};
 
 // One thread's packed share of a chunk: values of 32 columns of one row
 // (2:4 16 values, 1:4 8, 1:8 4) and the two index words holding its bits.
@@ -144,35 +157,36 @@ __device__ inline void dx_expand(const DxPack& d, uint32_t ishift, uint32_t (&o)
   }
 }
 
-template <int P, int DT, int OUT, class LR, class GR>
+template <int P, int DT, int OUT, bool WIDE, class LR, class GR>
 __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restrict__ values, uint32_t values_bytes,
                                                       const uint32_t* __restrict__ idx, uint32_t idx_bytes, int R,
                                                       int K, int idx_row_words, const uint16_t* __restrict__ G,
                                                       int T, int64_t ldg, void* __restrict__ dX, int64_t lddx,
                                                       int tilesK, int tilesT, int group, LR lowrank, GR experts) {
+  using C = DxTile<WIDE>;
   constexpr int N = pat_n(P), M = pat_m(P);
   constexpr int B = P == 2 ? 3 : 2;  // index bits per survivor
   extern __shared__ __align__(16) unsigned char smem[];
-  unsigned char* gbuf = smem;                          // [2][16 KB]
-  unsigned char* wbuf = smem + 2 * kDxGStage;          // [2][64][288 B]
+  unsigned char* gbuf = smem;                          // [2][GStage]
+  unsigned char* wbuf = smem + 2 * C::GStage;          // [2][RC][WRow]
 
   int tk, tt;
   grouped_tile(xcd_tile(blockIdx.x, gridDim.x), tilesK, tilesT, group, tk, tt);
-  const int K0 = tk * kDxBK;
+  const int K0 = tk * C::BK;
   int T0 = tt * kDxBT;
   if constexpr (std::is_same_v<GR, GroupDx>) {   // the tile's expert, its tokens up to T
-    if (tt >= experts.table[0].x) return;
-    const int4 g = experts.table[1 + tt];
-    values += g.x * experts.values_stride;
-    idx += g.x * experts.idx_stride;
-    T0 = g.y;
-    T = g.z;
+    GroupTile g;
+    if (!experts.rows.tile(tt, T, kDxBT, g)) return;
+    values += g.e * experts.values_stride;
+    idx += g.e * experts.idx_stride;
+    T0 = g.t0;
+    T = g.t1;
   }
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wk = wave >> 1, wt = wave & 1;
   const int li = lane & 15, lq = lane >> 4;
-  const int nchunks = (R + kDxRC - 1) / kDxRC;
+  const int nchunks = (R + C::RC - 1) / C::RC;
   const int64_t S = int64_t(K) * N / M;
 
   // G: descriptor over the tile's token rows (rows past T reread row T - 1;
@@ -182,38 +196,37 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
   const int tlast = min(T0 + kDxBT, T) - 1;
   const __amdgpu_buffer_rsrc_t rg =
       make_rsrc(G + int64_t(T0) * ldg, uint32_t((int64_t(tlast - T0) * ldg + R) * 2));
-  // this thread's 4 pieces of a chunk: LDS slot gslot[j] = (wave*4 + j)*64 +
-  // lane, holding (token, 16-byte chunk c) of the tile
-  uint32_t goff[4];
-  int gcol[4];
+  // this thread's pieces of a chunk: LDS slot (wave*NG + j)*64 + lane, holding
+  // (token, 16-byte piece c) of the tile (a piece's slot is its own inverse)
+  uint32_t goff[C::NG];
+  int gcol[C::NG];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int slot = (wave * 4 + j) * 64 + lane;
-    const int tok = slot >> 3;
-    const int c = (slot & 7) ^ (tok & 7);
+  for (int j = 0; j < C::NG; ++j) {
+    const int slot = (wave * C::NG + j) * 64 + lane;
+    const int tok = slot / C::CPR;
+    const int c = C::piece(tok, slot % C::CPR) % C::CPR;
     const int t = min(T0 + tok, T - 1) - T0;
     goff[j] = uint32_t(t) * uint32_t(ldg) * 2u + uint32_t(c) * 16u;
     gcol[j] = c * 8;
   }
-  auto load_g = [&](int chunk, u32x4 (&gr)[4]) {
-    const int r0 = chunk * kDxRC;
+  auto load_g = [&](int chunk, u32x4 (&gr)[C::NG]) {
+    const int r0 = chunk * C::RC;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < C::NG; ++j) {
       // a piece past R (or of a chunk past the last) reads zeros
       const bool live = chunk < nchunks && r0 + gcol[j] < R;
       gr[j] = __builtin_bit_cast(
           u32x4, __builtin_amdgcn_raw_buffer_load_b128(rg, live ? goff[j] + uint32_t(r0) * 2u : kDeadOff, 0, 0));
     }
   };
-  auto write_g = [&](int stage, const u32x4 (&gr)[4]) {
+  auto write_g = [&](int stage, const u32x4 (&gr)[C::NG]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<u32x4*>(gbuf + stage * kDxGStage + ((wave * 4 + j) * 64 + lane) * 16) = gr[j];
+    for (int j = 0; j < C::NG; ++j)
+      *reinterpret_cast<u32x4*>(gbuf + stage * C::GStage + ((wave * C::NG + j) * 64 + lane) * 16) = gr[j];
   };
 
-  // W: this thread decompresses row (tid >> 2) of the chunk, columns
-  // K0 + 32 (tid & 3) .. +31
-  const int wr = tid >> 2, wc = tid & 3;
+  // W: this thread decompresses 32 columns of a row of the chunk
+  const int wr = tid / (C::BK / 32), wc = tid % (C::BK / 32);
   const __amdgpu_buffer_rsrc_t rv = make_rsrc(values, values_bytes);
   const __amdgpu_buffer_rsrc_t ri = make_rsrc(idx, idx_bytes);
   const int kc = K0 + 32 * wc;                      // first column of the segment
@@ -224,7 +237,7 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
   // row's last word then holds every bit the segment needs)
   const int64_t w0 = bit0 >> 5, w1 = min(w0 + 1, int64_t(idx_row_words) - 1);
   auto pack_offsets = [&](int chunk, uint32_t& voff, uint32_t& ioff0, uint32_t& ioff1) {
-    const int64_t row = int64_t(chunk) * kDxRC + wr;
+    const int64_t row = int64_t(chunk) * C::RC + wr;
     const bool live = chunk < nchunks && row < R && kc < K;
     voff = live ? uint32_t((row * S + s0) * 2) : kDeadOff;
     ioff0 = live ? uint32_t((row * idx_row_words + w0) * 4) : kDeadOff;
@@ -233,15 +246,15 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
   auto decompress = [&](const DxPack& d, int buf) {
     uint32_t o[16];
     dx_expand<P>(d, ishift, o);
-    unsigned char* dst = wbuf + buf * kDxWTile + wr * kDxWRow + wc * 64;
+    unsigned char* dst = wbuf + buf * C::WTile + wr * C::WRow + wc * 64;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       *reinterpret_cast<u32x4*>(dst + 16 * q) = u32x4{o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]};
   };
 
-  f32x4 acc[4][4];
+  f32x4 acc[C::FK][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < C::FK; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
@@ -250,20 +263,20 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
   const int tr_row = 8 * (lane >> 4) + ((lane >> 2) & 3), tr_col = 4 * (lane & 3);
   auto read_a = [&](int buf, int h, int kf) {
     const unsigned char* base =
-        wbuf + buf * kDxWTile + (32 * h + tr_row) * kDxWRow + (wk * 64 + kf * 16 + tr_col) * 2;
-    const u32x2 lo = lds_read_tr(base), hi = lds_read_tr(base + 4 * kDxWRow);
+        wbuf + buf * C::WTile + (32 * h + tr_row) * C::WRow + (wk * (C::BK / 2) + kf * 16 + tr_col) * 2;
+    const u32x2 lo = lds_read_tr(base), hi = lds_read_tr(base + 4 * C::WRow);
     return u32x4{lo[0], lo[1], hi[0], hi[1]};
   };
   auto read_b = [&](int slot, int h, int tf) {
     const int tok = wt * 64 + tf * 16 + li;
     const int c = 4 * h + lq;
-    return *reinterpret_cast<const u32x4*>(gbuf + slot * kDxGStage + (tok * 8 + (c ^ (tok & 7))) * 16);
+    return *reinterpret_cast<const u32x4*>(gbuf + slot * C::GStage + C::piece(tok, c) * 16);
   };
 
   // ---- prologue: chunks 0 and 1 in registers, chunk 0 staged and
   // decompressed, chunk 2 in registers
   DxPack pk[2];
-  u32x4 gs[2][4];
+  u32x4 gs[2][C::NG];
   auto load_pack = [&](int chunk, DxPack& d) {
     uint32_t vo, i0, i1;
     pack_offsets(chunk, vo, i0, i1);
@@ -290,18 +303,18 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
   auto step = [&](auto par_c, int c) {
     constexpr int PAR = decltype(par_c)::value;
     DxPack& nextp = pk[PAR ^ 1];
-    u32x4 (&nextg)[4] = gs[PAR ^ 1];
+    u32x4 (&nextg)[C::NG] = gs[PAR ^ 1];
     wait_lgkm0();
     barrier_no_fence();
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      u32x4 a[4], b[4];
+    for (int h = 0; h < C::RC / 32; ++h) {
+      u32x4 a[C::FK], b[4];
 #pragma unroll
-      for (int kf = 0; kf < 4; ++kf) a[kf] = read_a(PAR, h, kf);
+      for (int kf = 0; kf < C::FK; ++kf) a[kf] = read_a(PAR, h, kf);
 #pragma unroll
       for (int tf = 0; tf < 4; ++tf) b[tf] = read_b(PAR, h, tf);
 #pragma unroll
-      for (int kf = 0; kf < 4; ++kf)
+      for (int kf = 0; kf < C::FK; ++kf)
 #pragma unroll
         for (int tf = 0; tf < 4; ++tf) acc[kf][tf] = mfma32<DT>(a[kf], b[tf], acc[kf][tf]);
     }
@@ -326,37 +339,50 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
 
   // ---- the low-rank term
   if constexpr (std::is_same_v<LR, LowRank>)
-    lowrank_add<DT, 4, 4>(lowrank, ids, T0 + wt * 64, K0 + wk * 64, [&](int f, int n) -> f32x4& { return acc[f][n]; });
+    lowrank_add<DT, C::FK, 4>(lowrank, ids, T0 + wt * 64, K0 + wk * (C::BK / 2), [&](int f, int n) -> f32x4& { return acc[f][n]; });
 
-  // ---- epilogue: lane (t = li, quarter q) holds rows 4q..4q+3 (k) of
-  // column t of each fragment: 16 (fp32) or 8 (half) contiguous bytes of dX
-  const bool vec_ok = OUT == NM_F32 ? (lddx & 3) == 0 : (lddx & 3) == 0;
+  // ---- epilogue: lane (t = li, quarter q) holds rows 4q..4q+3 (k) of column t of
+  // each fragment.  A fragment of 16 tokens at a time is gathered in the wave's own
+  // part of LDS and leaves in runs of the wave's BK / 2 columns (from the lanes a
+  // token's columns would go out in pieces of 32 or 64 bytes).
+  constexpr int ELT = OUT == NM_F32 ? 4 : 2, RUN = C::BK / 2 * ELT, PITCH = RUN + 16, LPR = RUN / 16;
+  static_assert(4 * 16 * PITCH <= C::LDS, "the waves' gather areas");
+  wait_lgkm0();
+  barrier_no_fence();   // every wave is done with the stages
+  unsigned char* mine = smem + wave * (16 * PITCH);
+  const int kw = K0 + wk * (C::BK / 2);
+  const bool vec_ok = (lddx * ELT) % 16 == 0;
 #pragma unroll
-  for (int kf = 0; kf < 4; ++kf) {
-    const int k = K0 + wk * 64 + kf * 16 + lq * 4;
+  for (int tf = 0; tf < 4; ++tf) {
 #pragma unroll
-    for (int tf = 0; tf < 4; ++tf) {
-      const int t = T0 + wt * 64 + tf * 16 + li;
-      if (t >= T || k >= K) continue;
+    for (int kf = 0; kf < C::FK; ++kf) {
       const f32x4 v = acc[kf][tf];
-      if constexpr (OUT == NM_F32) {
-        float* y = static_cast<float*>(dX) + int64_t(t) * lddx + k;
-        if (vec_ok && k + 3 < K) {
-          *reinterpret_cast<f32x4*>(y) = v;
-        } else {
-          for (int e = 0; e < 4 && k + e < K; ++e) y[e] = v[e];
-        }
+      unsigned char* o = mine + li * PITCH + (kf * 16 + lq * 4) * ELT;
+      if constexpr (OUT == NM_F32) *reinterpret_cast<f32x4*>(o) = v;
+      else *reinterpret_cast<u32x2*>(o) = u32x2{pack_half2<DT>(v[0], v[1]), pack_half2<DT>(v[2], v[3])};
+    }
+    wait_lgkm0();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int it = 0; it < 16 * LPR / 64; ++it) {
+      const int slot = it * 64 + lane, row = slot / LPR, c = slot % LPR;
+      const int t = T0 + wt * 64 + tf * 16 + row, k = kw + c * (16 / ELT);
+      if (t >= T || k >= K) continue;   // (K is a multiple of 32: a piece is in or out)
+      const u32x4 v = *reinterpret_cast<const u32x4*>(mine + row * PITCH + c * 16);
+      unsigned char* y = static_cast<unsigned char*>(dX) + (int64_t(t) * lddx + k) * ELT;
+      if (vec_ok) {
+        *reinterpret_cast<u32x4*>(y) = v;
       } else {
-        uint16_t* y = static_cast<uint16_t*>(dX) + int64_t(t) * lddx + k;
-        const uint32_t p0 = pack_half2<DT>(v[0], v[1]), p1 = pack_half2<DT>(v[2], v[3]);
-        if (vec_ok && k + 3 < K) {
-          *reinterpret_cast<uint2*>(y) = make_uint2(p0, p1);
-        } else {
-          const uint16_t hh[4] = {uint16_t(p0), uint16_t(p0 >> 16), uint16_t(p1), uint16_t(p1 >> 16)};
-          for (int e = 0; e < 4 && k + e < K; ++e) y[e] = hh[e];
+#pragma unroll
+        for (int e = 0; e < 16 / ELT; ++e) {
+          const uint32_t w = v[e * ELT / 4];
+          if constexpr (ELT == 4) reinterpret_cast<uint32_t*>(y)[e] = w;
+          else reinterpret_cast<uint16_t*>(y)[e] = uint16_t(w >> (16 * (e & 1)));
         }
       }
     }
+    wait_lgkm0();   // read before the next fragment is gathered
+    asm volatile("" ::: "memory");
   }
 }
 
@@ -660,14 +686,15 @@ hipError_t launch_dw_dt(const TrainArgs& a, hipStream_t s) {
   return a.dtype == NM_F16 ? launch_dw_out<P, NM_F16>(a, s) : launch_dw_out<P, NM_BF16>(a, s);
 }
 
-template <int P, int DT, int OUT, class LR, class GR>
-hipError_t launch_dx_cfg(const TrainArgs& a, const LR& lowrank, const GR& experts, hipStream_t s) {
-  const int64_t tilesK = (a.K + kDxBK - 1) / kDxBK;
+template <int P, int DT, int OUT, bool WIDE, class LR, class GR>
+hipError_t launch_dx_tile(const TrainArgs& a, const LR& lowrank, const GR& experts, hipStream_t s) {
+  using C = DxTile<WIDE>;
+  const int64_t tilesK = (a.K + C::BK - 1) / C::BK;
   const int64_t tilesT = a.offsets ? group_max_tiles(a.T, a.experts, kDxBT) : (a.T + kDxBT - 1) / kDxBT;
   if (tilesK * tilesT > 0x7FFFFFFF) return hipErrorInvalidValue;
-  auto kern = spmm_dx_kernel<P, DT, OUT, LR, GR>;
-  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), kDxLds); e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3(unsigned(tilesK * tilesT)), dim3(256), kDxLds, s, a.values,
+  auto kern = spmm_dx_kernel<P, DT, OUT, WIDE, LR, GR>;
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), C::LDS); e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3(unsigned(tilesK * tilesT)), dim3(256), C::LDS, s, a.values,
                      uint32_t(a.values_bytes), a.idx, uint32_t(a.idx_bytes), int(a.R), int(a.K),
                      int(a.idx_row_words), a.G, int(a.T), a.ldg, a.out, a.ldo, int(tilesK), int(tilesT),
                      // every column tile of an expert's tokens together: its weight is shared by few token
@@ -677,6 +704,16 @@ hipError_t launch_dx_cfg(const TrainArgs& a, const LR& lowrank, const GR& expert
   return hipGetLastError();
 }
 
+// Wide tiles where they still give every compute unit two workgroups.
+template <int P, int DT, int OUT, class LR, class GR>
+hipError_t launch_dx_cfg(const TrainArgs& a, const LR& lowrank, const GR& experts, hipStream_t s) {
+  if constexpr (std::is_same_v<LR, NoLowRank>) {   // (the low-rank term's registers are spilled by wide tiles)
+    const int64_t tiles = (a.K + 255) / 256 * ((a.T + kDxBT - 1) / kDxBT);
+    if (tiles >= 512) return launch_dx_tile<P, DT, OUT, true>(a, lowrank, experts, s);
+  }
+  return launch_dx_tile<P, DT, OUT, false>(a, lowrank, experts, s);
+}
+
 template <int P, int DT>
 hipError_t launch_dx_out(const TrainArgs& a, hipStream_t s) {
   const bool f32 = a.out_dtype == NM_F32;
@@ -684,7 +721,9 @@ hipError_t launch_dx_out(const TrainArgs& a, hipStream_t s) {
     return f32 ? launch_dx_cfg<P, DT, NM_F32>(a, *a.lowrank, NoGroup{}, s)
                : launch_dx_cfg<P, DT, DT>(a, *a.lowrank, NoGroup{}, s);
   if (a.offsets) {
-    const GroupDx g{static_cast<const int4*>(a.table), a.R * (a.K / a.m * a.n), a.R * a.idx_row_words};
+    GroupDx g{{}, a.R * (a.K / a.m * a.n), a.R * a.idx_row_words};
+    const hipError_t e = group_rows(a.offsets, a.experts, a.T, kDxBT, spmm_dx_max_tiles(a.T, a.experts), a.table, s, g.rows);
+    if (e != hipSuccess) return e;
     return f32 ? launch_dx_cfg<P, DT, NM_F32>(a, NoLowRank{}, g, s) : launch_dx_cfg<P, DT, DT>(a, NoLowRank{}, g, s);
   }
   return f32 ? launch_dx_cfg<P, DT, NM_F32>(a, NoLowRank{}, NoGroup{}, s)
@@ -698,6 +737,8 @@ hipError_t launch_dx_dt(const TrainArgs& a, hipStream_t s) {
 
 }  // namespace
 
+int64_t spmm_dx_max_tiles(int64_t T, int64_t E) { return group_max_tiles(T, E, kDxBT); }
+
 hipError_t launch_spmm_dw(const TrainArgs& a, hipStream_t s) {
   if (a.n == 2 && a.m == 4) return launch_dw_dt<0>(a, s);
   if (a.n == 1 && a.m == 4) return launch_dw_dt<1>(a, s);
@@ -705,14 +746,7 @@ hipError_t launch_spmm_dw(const TrainArgs& a, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
-int64_t spmm_dx_max_tiles(int64_t T, int64_t E) { return group_max_tiles(T, E, kDxBT); }
-
 hipError_t launch_spmm_dx(const TrainArgs& a, hipStream_t s) {
-  if (a.offsets) {
-    const hipError_t e = launch_group_tiles(a.offsets, a.experts, a.T, kDxBT, spmm_dx_max_tiles(a.T, a.experts),
-                                            static_cast<int4*>(a.table), s);
-    if (e != hipSuccess) return e;
-  }
   if (a.n == 2 && a.m == 4) return launch_dx_dt<0>(a, s);
   if (a.n == 1 && a.m == 4) return launch_dx_dt<1>(a, s);
   if (a.n == 1 && a.m == 8) return launch_dx_dt<2>(a, s);

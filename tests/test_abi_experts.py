@@ -38,7 +38,9 @@ def test_group_errors(call):
     assert call(idx=None) == NULL and call(off=None) == NULL and call(off=4 * P + 2) == ALIGN
     assert call(idx=2 * P + 4) == ALIGN
     if call is not group_dw:
-        assert call(ws=None) == NULL and call(wsb=16) == SHAPE and call(ws=6 * P + 8) == ALIGN and call(ws=P) == ALIAS
+        many = dict(E=300, T=30000)          # enough experts for a table
+        assert call(ws=None, **many) == NULL and call(wsb=16, **many) == SHAPE
+        assert call(ws=6 * P + 8, **many) == ALIGN and call(ws=P, **many) == ALIAS
         assert call(values=None) == NULL and call(values=P + 8) == ALIGN
 
 
@@ -64,12 +66,14 @@ def test_group_workspace_sizes():
     b = ctypes.c_size_t()
     ref = ctypes.byref(b)
     f = nm.lib().nm_group_spmm_workspace_size
-    assert f(8, 64, 64, 2, 4, nm.NM_BF16, 1000, nm.NM_F32, ref) == OK and 0 < b.value < 1 << 16
+    assert f(300, 64, 64, 2, 4, nm.NM_BF16, 30000, nm.NM_F32, ref) == OK and 0 < b.value < 1 << 16
+    assert f(8, 512, 256, 2, 4, nm.NM_BF16, 1000, nm.NM_F32, ref) == OK and 0 < b.value < 1 << 16
+    assert f(8, 64, 64, 2, 4, nm.NM_BF16, 8, nm.NM_F32, ref) == OK and b.value == 0
     assert f(8, 64, 64, 2, 4, nm.NM_BF16, 0, nm.NM_F32, ref) == OK and b.value == 0
     assert f(0, 64, 64, 2, 4, nm.NM_BF16, 10, nm.NM_F32, ref) == SHAPE
     assert f(8, 64, 64, 2, 4, nm.NM_BF16, 10, nm.NM_F32, None) == NULL
     g = nm.lib().nm_group_spmm_dx_workspace_size
-    assert g(8, 1000, ref) == OK and 0 < b.value < 1 << 16
+    assert g(300, 1000, ref) == OK and 0 < b.value < 1 << 16 and g(8, 1000, ref) == OK and b.value == 0
     assert g(8, -1, ref) == SHAPE and g(1 << 20, 5, ref) == SHAPE and g(8, 10, None) == NULL
 
 

@@ -265,3 +265,19 @@ def test_one_expert_is_the_plain_product():
     assert torch.equal(dx, pdx) and torch.equal(dw[0], pdw)
     _, size, _ = E.group_ref(c.values, c.idx, 512, 2, 4, c.act, c.offsets, "bf16")
     assert (np.abs((y - py).double().cpu().numpy()) <= 2 * 256 * 2.0 ** -23 * size).all()
+
+
+@pytest.mark.parametrize("pat", PAT)
+def test_wide_gradient_tiles(pat):
+    """Rows enough for the wide tiles of dX, with edges in rows, columns and the reduction."""
+    log(f"group wide dX {pat}")
+    Case([7001, 0, 9003, 1, 6100], 72, 544, pat, "bf16", behind=3).backward("bf16")
+
+
+@pytest.mark.parametrize("R,K", [(520, 256), (300, 640), (1000, 1152)])
+@pytest.mark.parametrize("dt,out", [("bf16", "bf16"), ("f16", "f32")])
+def test_large_forward_walks_tiles(R, K, dt, out):
+    """2:4 rows enough that workgroups walk from tile to tile, across experts; 640 columns, where each
+    tile has its own workgroup."""
+    log(f"group walked tiles R={R} K={K} {dt} {out}")
+    Case([9000, 1, 0, 6500, 130, 2999], R, K, (2, 4), dt, before=2, behind=5).forward(out, 1 if out == "f32" else 8)
