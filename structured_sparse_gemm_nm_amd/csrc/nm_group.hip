@@ -526,7 +526,10 @@ Pick pick(const SpmmArgs& b, int64_t E) {
   if (mean <= 24) return Pick::few2;
   if (mean <= 64) return Pick::tile64;
   // (by numbers alone: the workspace's size is asked for without a device)
-  return b.n == 2 && b.K % 128 == 0 && b.R >= 256 ? Pick::lds : Pick::tile128;
+  if (b.n == 2 && b.K % 128 == 0 && b.R >= 256) return Pick::lds;
+  // tiles of 128 tokens where there is one for every compute unit
+  const int64_t tiles = (b.R + kBR - 1) / kBR * ((b.T + 127) / 128);
+  return tiles >= 256 ? Pick::tile128 : Pick::tile64;
 }
 
 template <int P, int DT, int OUT>

@@ -73,24 +73,11 @@ constexpr int pat_m(int P) { return P == 2 ? 8 : 4; }
 // LDS two workgroups share a compute unit, each covering the other's barrier
 // and epilogue.
 // ---------------------------------------------------------------------------
-// WIDE: 256 k x 128 t in chunks of 32 rows (a wave 128 x 64): the same products a
-// barrier, a quarter fewer LDS bytes for each, which is what bounds the kernel where
-// its tiles fill the chip.
-constexpr int kDxBT = 128;
-template <bool WIDE>
-struct DxTile {
-  static constexpr int BK = WIDE ? 256 : 128, RC = WIDE ? 32 : 64;
-  static constexpr int FK = BK / 32;              // a wave's fragments along k
-  static constexpr int CPR = RC / 8;              // 16-byte pieces of a token's chunk of G
-  static constexpr int NG = kDxBT * CPR / 256;    // of them a thread loads
-  static constexpr int GStage = kDxBT * RC * 2;
-  static constexpr int WRow = BK * 2 + 32;        // padded row of the W tile
-  static constexpr int WTile = RC * WRow;
-  static constexpr int LDS = 2 * GStage + 2 * WTile;
-  __device__ static int piece(int tok, int c) {   // the slot of piece c of a token
-    return tok * CPR + (WIDE ? c ^ ((tok >> 1) & 3) : c ^ (tok & 7));
-  }
-};
+constexpr int kDxBK = 128, kDxBT = 128, kDxRC = 64;
+constexpr int kDxGStage = kDxBT * kDxRC * 2;     // 16 KB
+constexpr int kDxWRow = kDxBK * 2 + 32;          // 288 bytes: padded row of the W tile
+constexpr int kDxWTile = kDxRC * kDxWRow;        // 18 KB
+constexpr int kDxLds = 2 * kDxGStage + 2 * kDxWTile;
 
 // One thread's packed share of a chunk: values of 32 columns of one row
 // (2:4 16 values, 1:4 8, 1:8 4) and the two index words holding its bits.
@@ -99,18 +86,15 @@ struct DxPack {
   uint32_t i0, i1;
 };
 
-// Offset that no descriptor here covers: a load from it returns zeros.
-constexpr uint32_t kDeadOff = 0xFFFFFFF0u;
-
 template <int P>
 __device__ inline void dx_load(DxPack& d, __amdgpu_buffer_rsrc_t rv, __amdgpu_buffer_rsrc_t ri, uint32_t voff,
                                uint32_t ioff0, uint32_t ioff1) {
   if constexpr (P == 0) {
     d.v0 = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rv, voff, 0, 0));
-    // a dead share stays dead: kDeadOff + 16 would wrap to offset 0, and row
+    // a dead share stays dead: kDeadOffset + 16 would wrap to offset 0, and row
     // 0's values with zero index bits expand (two halves OR'ed into one
     // position) into arbitrary bits, Inf and NaN among them
-    const uint32_t voff1 = voff == kDeadOff ? kDeadOff : voff + 16u;
+    const uint32_t voff1 = voff == kDeadOffset ? kDeadOffset : voff + 16u;
     d.v1 = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rv, voff1, 0, 0));
   } else if constexpr (P == 1) {
     d.v0 = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rv, voff, 0, 0));
@@ -122,57 +106,56 @@ __device__ inline void dx_load(DxPack& d, __amdgpu_buffer_rsrc_t rv, __amdgpu_bu
   d.i1 = __builtin_amdgcn_raw_buffer_load_b32(ri, ioff1, 0, 0);
 }
 
-// The 32 dense halves (16 dwords) of a thread's row segment from its packed
-// share; ishift is the position of its first index bit in word i0.
-template <int P>
-__device__ inline void dx_expand(const DxPack& d, uint32_t ishift, uint32_t (&o)[16]) {
+// Quarter q (8 columns, 4 dwords) of a thread's row segment from its packed share;
+// ishift is the position of the segment's first index bit in word i0.
+template <int P, int q>
+__device__ inline void dx_expand(const DxPack& d, uint32_t ishift, u32x4& o) {
   const uint64_t bits = (uint64_t(d.i1) << 32 | d.i0) >> ishift;
-  if constexpr (P == 0) {  // 8 groups of 4, two values each
-    const uint32_t v[8] = {d.v0[0], d.v0[1], d.v0[2], d.v0[3], d.v1[0], d.v1[1], d.v1[2], d.v1[3]};
+  if constexpr (P == 0) {  // 2 groups of 4, two values each
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
+    for (int e = 0; e < 2; ++e) {
+      constexpr int g0 = 2 * q;
+      const int g = g0 + e;
+      const uint32_t v = g < 4 ? d.v0[g & 3] : d.v1[g & 3];
       const uint32_t p0 = uint32_t(bits >> (4 * g)) & 3u, p1 = uint32_t(bits >> (4 * g + 2)) & 3u;
-      const uint64_t w = (uint64_t(v[g] & 0xFFFFu) << (16 * p0)) | (uint64_t(v[g] >> 16) << (16 * p1));
-      o[2 * g] = uint32_t(w);
-      o[2 * g + 1] = uint32_t(w >> 32);
+      const uint64_t w = (uint64_t(v & 0xFFFFu) << (16 * p0)) | (uint64_t(v >> 16) << (16 * p1));
+      o[2 * e] = uint32_t(w);
+      o[2 * e + 1] = uint32_t(w >> 32);
     }
-  } else if constexpr (P == 1) {  // 8 groups of 4, one value each
+  } else if constexpr (P == 1) {  // 2 groups of 4, one value each
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
+    for (int e = 0; e < 2; ++e) {
+      const int g = 2 * q + e;
       const uint32_t h = (d.v0[g >> 1] >> (16 * (g & 1))) & 0xFFFFu;
       const uint32_t p = uint32_t(bits >> (2 * g)) & 3u;
       const uint64_t w = uint64_t(h) << (16 * p);
-      o[2 * g] = uint32_t(w);
-      o[2 * g + 1] = uint32_t(w >> 32);
+      o[2 * e] = uint32_t(w);
+      o[2 * e + 1] = uint32_t(w >> 32);
     }
-  } else {  // 4 groups of 8, one value each
+  } else {  // a group of 8, one value
+    const uint32_t h = (d.v0[q >> 1] >> (16 * (q & 1))) & 0xFFFFu;
+    const uint32_t p = uint32_t(bits >> (3 * q)) & 7u;
+    const uint32_t x = h << (16 * (p & 1));
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const uint32_t h = (d.v0[g >> 1] >> (16 * (g & 1))) & 0xFFFFu;
-      const uint32_t p = uint32_t(bits >> (3 * g)) & 7u;
-      const uint32_t x = h << (16 * (p & 1));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[4 * g + e] = (p >> 1) == uint32_t(e) ? x : 0u;
-    }
+    for (int e = 0; e < 4; ++e) o[e] = (p >> 1) == uint32_t(e) ? x : 0u;
   }
 }
 
-template <int P, int DT, int OUT, bool WIDE, class LR, class GR>
+template <int P, int DT, int OUT, class LR, class GR>
 __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restrict__ values, uint32_t values_bytes,
                                                       const uint32_t* __restrict__ idx, uint32_t idx_bytes, int R,
                                                       int K, int idx_row_words, const uint16_t* __restrict__ G,
                                                       int T, int64_t ldg, void* __restrict__ dX, int64_t lddx,
                                                       int tilesK, int tilesT, int group, LR lowrank, GR experts) {
-  using C = DxTile<WIDE>;
   constexpr int N = pat_n(P), M = pat_m(P);
   constexpr int B = P == 2 ? 3 : 2;  // index bits per survivor
   extern __shared__ __align__(16) unsigned char smem[];
-  unsigned char* gbuf = smem;                          // [2][GStage]
-  unsigned char* wbuf = smem + 2 * C::GStage;          // [2][RC][WRow]
+  unsigned char* gbuf = smem;                          // [2][16 KB]
+  unsigned char* wbuf = smem + 2 * kDxGStage;          // [2][64][288 B]
 
   int tk, tt;
   grouped_tile(xcd_tile(blockIdx.x, gridDim.x), tilesK, tilesT, group, tk, tt);
-  const int K0 = tk * C::BK;
+  const int K0 = tk * kDxBK;
   int T0 = tt * kDxBT;
   if constexpr (std::is_same_v<GR, GroupDx>) {   // the tile's expert, its tokens up to T
     GroupTile g;
@@ -186,7 +169,7 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wk = wave >> 1, wt = wave & 1;
   const int li = lane & 15, lq = lane >> 4;
-  const int nchunks = (R + C::RC - 1) / C::RC;
+  const int nchunks = (R + kDxRC - 1) / kDxRC;
   const int64_t S = int64_t(K) * N / M;
 
   // G: descriptor over the tile's token rows (rows past T reread row T - 1;
@@ -198,35 +181,30 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
       make_rsrc(G + int64_t(T0) * ldg, uint32_t((int64_t(tlast - T0) * ldg + R) * 2));
   // this thread's pieces of a chunk: LDS slot (wave*NG + j)*64 + lane, holding
   // (token, 16-byte piece c) of the tile (a piece's slot is its own inverse)
-  uint32_t goff[C::NG];
-  int gcol[C::NG];
+  uint32_t goff[4];
+  int gcol[4];
 #pragma unroll
-  for (int j = 0; j < C::NG; ++j) {
-    const int slot = (wave * C::NG + j) * 64 + lane;
-    const int tok = slot / C::CPR;
-    const int c = C::piece(tok, slot % C::CPR) % C::CPR;
+  for (int j = 0; j < 4; ++j) {
+    const int slot = (wave * 4 + j) * 64 + lane;
+    const int tok = slot >> 3;
+    const int c = (slot & 7) ^ (tok & 7);
     const int t = min(T0 + tok, T - 1) - T0;
     goff[j] = uint32_t(t) * uint32_t(ldg) * 2u + uint32_t(c) * 16u;
     gcol[j] = c * 8;
   }
-  auto load_g = [&](int chunk, u32x4 (&gr)[C::NG]) {
-    const int r0 = chunk * C::RC;
-#pragma unroll
-    for (int j = 0; j < C::NG; ++j) {
-      // a piece past R (or of a chunk past the last) reads zeros
-      const bool live = chunk < nchunks && r0 + gcol[j] < R;
-      gr[j] = __builtin_bit_cast(
-          u32x4, __builtin_amdgcn_raw_buffer_load_b128(rg, live ? goff[j] + uint32_t(r0) * 2u : kDeadOff, 0, 0));
-    }
+  auto load_g = [&](int chunk, u32x4 (&gr)[4], int j) {
+    const int r0 = chunk * kDxRC;
+    // a piece past R (or of a chunk past the last) reads zeros
+    const bool live = (chunk < nchunks) & (r0 + gcol[j] < R);
+    gr[j] = __builtin_bit_cast(
+        u32x4, __builtin_amdgcn_raw_buffer_load_b128(rg, live_offset(live, goff[j] + uint32_t(r0) * 2u), 0, 0));
   };
-  auto write_g = [&](int stage, const u32x4 (&gr)[C::NG]) {
-#pragma unroll
-    for (int j = 0; j < C::NG; ++j)
-      *reinterpret_cast<u32x4*>(gbuf + stage * C::GStage + ((wave * C::NG + j) * 64 + lane) * 16) = gr[j];
+  auto write_g = [&](int stage, const u32x4 (&gr)[4], int j) {
+    *reinterpret_cast<u32x4*>(gbuf + stage * kDxGStage + ((wave * 4 + j) * 64 + lane) * 16) = gr[j];
   };
 
   // W: this thread decompresses 32 columns of a row of the chunk
-  const int wr = tid / (C::BK / 32), wc = tid % (C::BK / 32);
+  const int wr = tid >> 2, wc = tid & 3;
   const __amdgpu_buffer_rsrc_t rv = make_rsrc(values, values_bytes);
   const __amdgpu_buffer_rsrc_t ri = make_rsrc(idx, idx_bytes);
   const int kc = K0 + 32 * wc;                      // first column of the segment
@@ -237,24 +215,23 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
   // row's last word then holds every bit the segment needs)
   const int64_t w0 = bit0 >> 5, w1 = min(w0 + 1, int64_t(idx_row_words) - 1);
   auto pack_offsets = [&](int chunk, uint32_t& voff, uint32_t& ioff0, uint32_t& ioff1) {
-    const int64_t row = int64_t(chunk) * C::RC + wr;
-    const bool live = chunk < nchunks && row < R && kc < K;
-    voff = live ? uint32_t((row * S + s0) * 2) : kDeadOff;
-    ioff0 = live ? uint32_t((row * idx_row_words + w0) * 4) : kDeadOff;
-    ioff1 = live ? uint32_t((row * idx_row_words + w1) * 4) : kDeadOff;
+    const int64_t row = int64_t(chunk) * kDxRC + wr;
+    const bool live = (chunk < nchunks) & (row < R) & (kc < K);
+    voff = live_offset(live, uint32_t((row * S + s0) * 2));
+    ioff0 = live_offset(live, uint32_t((row * idx_row_words + w0) * 4));
+    ioff1 = live_offset(live, uint32_t((row * idx_row_words + w1) * 4));
   };
-  auto decompress = [&](const DxPack& d, int buf) {
-    uint32_t o[16];
-    dx_expand<P>(d, ishift, o);
-    unsigned char* dst = wbuf + buf * C::WTile + wr * C::WRow + wc * 64;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<u32x4*>(dst + 16 * q) = u32x4{o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]};
+  // 8 columns (quarter q) of the segment, 16 bytes of the tile's row
+  auto decompress = [&](const DxPack& d, int buf, auto q_c) {
+    constexpr int q = decltype(q_c)::value;
+    u32x4 o;
+    dx_expand<P, q>(d, ishift, o);
+    *reinterpret_cast<u32x4*>(wbuf + buf * kDxWTile + wr * kDxWRow + wc * 64 + 16 * q) = o;
   };
 
-  f32x4 acc[C::FK][4];
+  f32x4 acc[4][4];
 #pragma unroll
-  for (int i = 0; i < C::FK; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
@@ -263,20 +240,20 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
   const int tr_row = 8 * (lane >> 4) + ((lane >> 2) & 3), tr_col = 4 * (lane & 3);
   auto read_a = [&](int buf, int h, int kf) {
     const unsigned char* base =
-        wbuf + buf * C::WTile + (32 * h + tr_row) * C::WRow + (wk * (C::BK / 2) + kf * 16 + tr_col) * 2;
-    const u32x2 lo = lds_read_tr(base), hi = lds_read_tr(base + 4 * C::WRow);
+        wbuf + buf * kDxWTile + (32 * h + tr_row) * kDxWRow + (wk * (kDxBK / 2) + kf * 16 + tr_col) * 2;
+    const u32x2 lo = lds_read_tr(base), hi = lds_read_tr(base + 4 * kDxWRow);
     return u32x4{lo[0], lo[1], hi[0], hi[1]};
   };
   auto read_b = [&](int slot, int h, int tf) {
     const int tok = wt * 64 + tf * 16 + li;
     const int c = 4 * h + lq;
-    return *reinterpret_cast<const u32x4*>(gbuf + slot * C::GStage + C::piece(tok, c) * 16);
+    return *reinterpret_cast<const u32x4*>(gbuf + slot * kDxGStage + (tok * 8 + (c ^ (tok & 7))) * 16);
   };
 
   // ---- prologue: chunks 0 and 1 in registers, chunk 0 staged and
   // decompressed, chunk 2 in registers
   DxPack pk[2];
-  u32x4 gs[2][C::NG];
+  u32x4 gs[2][4];
   auto load_pack = [&](int chunk, DxPack& d) {
     uint32_t vo, i0, i1;
     pack_offsets(chunk, vo, i0, i1);
@@ -284,46 +261,69 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
   };
   [[maybe_unused]] int ids = 0;
   if constexpr (std::is_same_v<LR, LowRank>) ids = lowrank_ids<4>(lowrank, T0 + wt * 64);
-  load_g(0, gs[0]);
+  using std::integral_constant;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) load_g(0, gs[0], j);
   load_pack(0, pk[0]);
-  load_g(1, gs[1]);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) load_g(1, gs[1], j);
   load_pack(1, pk[1]);
-  decompress(pk[0], 0);
-  write_g(0, gs[0]);
-  load_g(2, gs[0]);
+  decompress(pk[0], 0, integral_constant<int, 0>{});
+  decompress(pk[0], 0, integral_constant<int, 1>{});
+  decompress(pk[0], 0, integral_constant<int, 2>{});
+  decompress(pk[0], 0, integral_constant<int, 3>{});
+#pragma unroll
+  for (int j = 0; j < 4; ++j) write_g(0, gs[0], j);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) load_g(2, gs[0], j);
   load_pack(2, pk[0]);
 
   // Step c (parity PAR = c & 1, a compile-time constant: the loop is unrolled
   // by two so the register sets alternate without copies): the barrier
   // publishes G stage PAR and W tile PAR, written in step c-1 (or the
   // prologue), and retires stage and tile PAR ^ 1, read in step c-1.  The step
-  // multiplies chunk c, then stages chunk c+1 from register sets (c+1) & 1
-  // into stage and tile PAR ^ 1 and loads chunk c+3 into those sets.  Past the
-  // last chunk the loads read zeros (dead offsets).
+  // multiplies chunk c, stages chunk c+1 from register sets (c+1) & 1 into
+  // stage and tile PAR ^ 1 and loads chunk c+3 into those sets.  Past the
+  // last chunk the loads read zeros (dead offsets), and so are staged.
+  // Eight slots of four products, which scheduling barriers keep in order: in the
+  // first four a quarter of the next chunk is decompressed behind the products and
+  // the second half's fragments are read, in the last four G is staged and the
+  // loads go out (one after the other, products, decompression and stage writes
+  // took the sum of their times).
   auto step = [&](auto par_c, int c) {
     constexpr int PAR = decltype(par_c)::value;
     DxPack& nextp = pk[PAR ^ 1];
-    u32x4 (&nextg)[C::NG] = gs[PAR ^ 1];
+    u32x4 (&nextg)[4] = gs[PAR ^ 1];
     wait_lgkm0();
     barrier_no_fence();
+    u32x4 a0[4], b0[4], a1[4], b1[4];
 #pragma unroll
-    for (int h = 0; h < C::RC / 32; ++h) {
-      u32x4 a[C::FK], b[4];
-#pragma unroll
-      for (int kf = 0; kf < C::FK; ++kf) a[kf] = read_a(PAR, h, kf);
-#pragma unroll
-      for (int tf = 0; tf < 4; ++tf) b[tf] = read_b(PAR, h, tf);
-#pragma unroll
-      for (int kf = 0; kf < C::FK; ++kf)
-#pragma unroll
-        for (int tf = 0; tf < 4; ++tf) acc[kf][tf] = mfma32<DT>(a[kf], b[tf], acc[kf][tf]);
+    for (int f = 0; f < 4; ++f) {
+      b0[f] = read_b(PAR, 0, f);
+      a0[f] = read_a(PAR, 0, f);
     }
-    if (c + 1 < nchunks) {
-      decompress(nextp, PAR ^ 1);
-      write_g(PAR ^ 1, nextg);
-    }
-    load_g(c + 3, nextg);
+    auto slot = [&](auto k_c) {
+      constexpr int k = decltype(k_c)::value;
+      a1[k] = read_a(PAR, 1, k);
+      b1[k] = read_b(PAR, 1, k);
+#pragma unroll
+      for (int tf = 0; tf < 4; ++tf) acc[k][tf] = mfma32<DT>(a0[k], b0[tf], acc[k][tf]);
+      decompress(nextp, PAR ^ 1, k_c);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    slot(integral_constant<int, 0>{});
+    slot(integral_constant<int, 1>{});
+    slot(integral_constant<int, 2>{});
+    slot(integral_constant<int, 3>{});
     load_pack(c + 3, nextp);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int tf = 0; tf < 4; ++tf) acc[k][tf] = mfma32<DT>(a1[k], b1[tf], acc[k][tf]);
+      write_g(PAR ^ 1, nextg, k);
+      load_g(c + 3, nextg, k);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
   // whole pairs in the loop and an odd last chunk after it: a pair cut short
   // inside the loop would give the back edge a path on which the other
@@ -339,23 +339,23 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
 
   // ---- the low-rank term
   if constexpr (std::is_same_v<LR, LowRank>)
-    lowrank_add<DT, C::FK, 4>(lowrank, ids, T0 + wt * 64, K0 + wk * (C::BK / 2), [&](int f, int n) -> f32x4& { return acc[f][n]; });
+    lowrank_add<DT, 4, 4>(lowrank, ids, T0 + wt * 64, K0 + wk * (kDxBK / 2), [&](int f, int n) -> f32x4& { return acc[f][n]; });
 
   // ---- epilogue: lane (t = li, quarter q) holds rows 4q..4q+3 (k) of column t of
   // each fragment.  A fragment of 16 tokens at a time is gathered in the wave's own
   // part of LDS and leaves in runs of the wave's BK / 2 columns (from the lanes a
   // token's columns would go out in pieces of 32 or 64 bytes).
-  constexpr int ELT = OUT == NM_F32 ? 4 : 2, RUN = C::BK / 2 * ELT, PITCH = RUN + 16, LPR = RUN / 16;
-  static_assert(4 * 16 * PITCH <= C::LDS, "the waves' gather areas");
+  constexpr int ELT = OUT == NM_F32 ? 4 : 2, RUN = kDxBK / 2 * ELT, PITCH = RUN + 16, LPR = RUN / 16;
+  static_assert(4 * 16 * PITCH <= kDxLds, "the waves' gather areas");
   wait_lgkm0();
   barrier_no_fence();   // every wave is done with the stages
   unsigned char* mine = smem + wave * (16 * PITCH);
-  const int kw = K0 + wk * (C::BK / 2);
+  const int kw = K0 + wk * (kDxBK / 2);
   const bool vec_ok = (lddx * ELT) % 16 == 0;
 #pragma unroll
   for (int tf = 0; tf < 4; ++tf) {
 #pragma unroll
-    for (int kf = 0; kf < C::FK; ++kf) {
+    for (int kf = 0; kf < 4; ++kf) {
       const f32x4 v = acc[kf][tf];
       unsigned char* o = mine + li * PITCH + (kf * 16 + lq * 4) * ELT;
       if constexpr (OUT == NM_F32) *reinterpret_cast<f32x4*>(o) = v;
@@ -485,13 +485,13 @@ __global__ __launch_bounds__(256, 2) void spmm_dw_kernel(const uint32_t* __restr
     for (int j = 0; j < 4; ++j) {
       const bool live = t0 + arow[j] < T;      // false for every chunk past the last
       v[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                           ra, live ? aoff[j] + uint32_t(t0) * uint32_t(ldx) * 2u : kDeadOff, 0, 0));
+                                           ra, live_offset(live, aoff[j] + uint32_t(t0) * uint32_t(ldx) * 2u), 0, 0));
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const bool live = t0 + grow[j] < T;
       v[4 + j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                               rg, live ? goff[j] + uint32_t(t0) * uint32_t(ldg) * 2u : kDeadOff, 0, 0));
+                                               rg, live_offset(live, goff[j] + uint32_t(t0) * uint32_t(ldg) * 2u), 0, 0));
     }
   };
   auto write_chunk = [&](int stage, const u32x4 (&v)[6]) {
@@ -686,15 +686,14 @@ hipError_t launch_dw_dt(const TrainArgs& a, hipStream_t s) {
   return a.dtype == NM_F16 ? launch_dw_out<P, NM_F16>(a, s) : launch_dw_out<P, NM_BF16>(a, s);
 }
 
-template <int P, int DT, int OUT, bool WIDE, class LR, class GR>
-hipError_t launch_dx_tile(const TrainArgs& a, const LR& lowrank, const GR& experts, hipStream_t s) {
-  using C = DxTile<WIDE>;
-  const int64_t tilesK = (a.K + C::BK - 1) / C::BK;
+template <int P, int DT, int OUT, class LR, class GR>
+hipError_t launch_dx_cfg(const TrainArgs& a, const LR& lowrank, const GR& experts, hipStream_t s) {
+  const int64_t tilesK = (a.K + kDxBK - 1) / kDxBK;
   const int64_t tilesT = a.offsets ? group_max_tiles(a.T, a.experts, kDxBT) : (a.T + kDxBT - 1) / kDxBT;
   if (tilesK * tilesT > 0x7FFFFFFF) return hipErrorInvalidValue;
-  auto kern = spmm_dx_kernel<P, DT, OUT, WIDE, LR, GR>;
-  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), C::LDS); e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3(unsigned(tilesK * tilesT)), dim3(256), C::LDS, s, a.values,
+  auto kern = spmm_dx_kernel<P, DT, OUT, LR, GR>;
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), kDxLds); e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3(unsigned(tilesK * tilesT)), dim3(256), kDxLds, s, a.values,
                      uint32_t(a.values_bytes), a.idx, uint32_t(a.idx_bytes), int(a.R), int(a.K),
                      int(a.idx_row_words), a.G, int(a.T), a.ldg, a.out, a.ldo, int(tilesK), int(tilesT),
                      // every column tile of an expert's tokens together: its weight is shared by few token
@@ -702,16 +701,6 @@ hipError_t launch_dx_tile(const TrainArgs& a, const LR& lowrank, const GR& exper
                      a.offsets ? int(tilesK) : pick_group(tilesK, tilesT, double(pat_n(P)) / pat_m(P), 1.0), lowrank,
                      experts);
   return hipGetLastError();
-}
-
-// Wide tiles where they still give every compute unit two workgroups.
-template <int P, int DT, int OUT, class LR, class GR>
-hipError_t launch_dx_cfg(const TrainArgs& a, const LR& lowrank, const GR& experts, hipStream_t s) {
-  if constexpr (std::is_same_v<LR, NoLowRank>) {   // (the low-rank term's registers are spilled by wide tiles)
-    const int64_t tiles = (a.K + 255) / 256 * ((a.T + kDxBT - 1) / kDxBT);
-    if (tiles >= 512) return launch_dx_tile<P, DT, OUT, true>(a, lowrank, experts, s);
-  }
-  return launch_dx_tile<P, DT, OUT, false>(a, lowrank, experts, s);
 }
 
 template <int P, int DT>
