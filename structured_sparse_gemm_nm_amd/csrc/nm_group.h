@@ -58,6 +58,20 @@ __device__ inline bool group_find(const int32_t* __restrict__ offsets, int E, in
   return g.e >= 0;
 }
 
+// How many tiles there are, by the whole wave.
+__device__ inline int group_count(const int32_t* __restrict__ offsets, int E, int T, int BT) {
+  const int lane = threadIdx.x & 63;
+  int sum = 0;
+  for (int e = lane; e < E; e += 64) {
+    int lo, hi;
+    group_range(offsets, e, T, lo, hi);
+    sum = tile_sum(sum, (hi - lo + BT - 1) / BT);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) sum = tile_sum(sum, __shfl_xor(sum, o, 64));
+  return __builtin_amdgcn_readfirstlane(sum);
+}
+
 // The tiles as a table in a workspace: its size, and the launch that fills it
 // (nm_group.hip).  Entry 0 holds the count, entries 1 .. count the tiles (e, t0,
 // t1, 0); at most max_tiles of them.

@@ -290,6 +290,219 @@ __global__ __launch_bounds__(kFewWaves * 64) void group_few_kernel(const uint16_
 }
 
 // ---------------------------------------------------------------------------
+// The same for rows of whole 16-byte pieces and K <= 4096: one workgroup a compute
+// unit streams the weights without a pause.  The kernel above spends most of a
+// workgroup's life waiting (the search, two round trips to memory, the sum over its
+// waves); here a workgroup takes a run of one tile's rows, its waves keep their
+// shares of the tokens in registers and fetch packed rows by direct loads into rings
+// of D stages in LDS of their own: a stage is refilled as soon as its fragments are
+// in registers.
+//
+// A unit is 16 rows x 128 bytes of values (2:4 128, 1:4 256, 1:8 512 columns), two
+// loads of 8 whole rows' lines each, and their index words; slot (row, 16-byte
+// piece c) of a unit at row*8 + (c ^ (row & 7)).  A stage is KU units.  As above a
+// lane quarter's run is 16 values, so the products differ only in the widening.
+// Of the 8 waves KS share K and 8 / KS take rows of their own; the KS partial tiles
+// are added in wave order through LDS, one barrier a step.
+// ---------------------------------------------------------------------------
+template <int N, int I = 0, class F>
+__device__ inline void static_for(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<N, I + 1>(f);
+  }
+}
+
+template <int P, int KU>
+struct Stream {
+  static constexpr int RUN = P == 0 ? 32 : P == 1 ? 64 : 128;   // columns of a lane quarter
+  static constexpr int COLS = 4 * RUN, PRODUCTS = RUN / 16;
+  static constexpr int IWORDS = P == 2 ? 6 : 4;                 // index words of a row's unit
+  static constexpr int ILOADS = P == 2 ? 2 : 1;
+  static constexpr int UNIT = 2048 + ILOADS * 256, STAGE = KU * UNIT;
+  static constexpr int LOADS = KU * (2 + ILOADS);               // a wave's direct loads a stage
+  static constexpr int PART = 2 * kFewWaves * 64 * 16;
+  static constexpr int D = (160 * 1024 - PART) / (kFewWaves * STAGE) < 8 ? (160 * 1024 - PART) / (kFewWaves * STAGE) : 8;
+  static constexpr int LDS = kFewWaves * D * STAGE + PART;
+  static_assert(D >= 2 && D * LOADS < 64, "stages, and a count of their loads");
+};
+
+template <int P, int DT, int OUT, int KU>
+__global__ __launch_bounds__(kFewWaves * 64, 2) void group_stream_kernel(const uint16_t* __restrict__ values,
+                                                                         const uint32_t* __restrict__ idx,
+                                                                         const uint16_t* __restrict__ act,
+                                                                         const int32_t* __restrict__ offsets,
+                                                                         GroupDims d, int max_tiles, int ks,
+                                                                         void* __restrict__ Y) {
+  using C = Stream<P, KU>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  f32x4* part = reinterpret_cast<f32x4*>(smem + kFewWaves * C::D * C::STAGE);   // [2][waves][64]
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 15, lq = lane >> 4;
+  unsigned char* ring = smem + wave * (C::D * C::STAGE);
+  const int share = wave & (ks - 1), rg = kFewWaves >> __builtin_ctz(ks);   // row groups; the wave's:
+  const int mine = wave >> __builtin_ctz(ks);
+  const int row_bytes = d.K / pat_m(P) * pat_n(P) * 2, idx_bytes = d.words * 4;
+  const int rsteps = (d.R + 16 * rg - 1) / (16 * rg);   // steps of 16 rows a group over all rows
+  const int unit0 = share * KU;
+
+  // Parts of a tile's rows: enough that every workgroup has one, or, of many tiles,
+  // so many that the last round is nearly full.
+  const int tiles = min(group_count(offsets, d.E, d.T, 16), max_tiles), grid = gridDim.x;
+  int parts = 1;
+  if (2 * tiles <= grid) {
+    parts = tiles > 0 ? min(grid / tiles, rsteps) : 1;
+  } else {
+    int best = 0x7FFFFFFF;
+    for (int w = 1; w <= min(8, rsteps); ++w) {
+      const int cost = ((tiles * w + grid - 1) / grid) * ((rsteps + w - 1) / w + 3);   // (3: a start's worth of steps)
+      if (cost < best) best = cost, parts = w;
+    }
+  }
+  for (int job = blockIdx.x; job < tiles * parts; job += grid) {
+    GroupTile g;
+    if (!group_find(offsets, d.E, d.T, 16, job / parts, g)) return;
+    const int p = job % parts;
+    const int step0 = __builtin_amdgcn_readfirstlane(int(int64_t(rsteps) * p / parts));
+    const int n = __builtin_amdgcn_readfirstlane(int(int64_t(rsteps) * (p + 1) / parts)) - step0;
+    const int toks = g.t1 - g.t0 < 16 ? g.t1 - g.t0 : 16;
+    const __amdgpu_buffer_rsrc_t rv =
+        make_rsrc(reinterpret_cast<const unsigned char*>(values) + int64_t(g.e) * d.R * row_bytes);
+    const __amdgpu_buffer_rsrc_t ri = make_rsrc(idx + int64_t(g.e) * d.R * d.words);
+    const __amdgpu_buffer_rsrc_t rx =
+        make_rsrc(act + int64_t(g.t0) * d.ldx, uint32_t((int64_t(toks - 1) * d.ldx + d.K) * 2));
+
+    // step i's rows; rows past R reread the last one, pieces and words past K the row's first
+    auto issue = [&](int i, int slot) {
+      const int r0 = ((step0 + i) * rg + mine) * 16;
+      unsigned char* st = ring + slot * C::STAGE;
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int row = j * 8 + (lane >> 3), c = (lane & 7) ^ (row & 7);
+          const int at = (unit0 + u) * 128 + c * 16;
+          dma16(rv, uint32_t(min(r0 + row, d.R - 1)) * uint32_t(row_bytes) + uint32_t(at < row_bytes ? at : 0), 0u,
+                st + u * C::UNIT + j * 1024);
+        }
+#pragma unroll
+        for (int j = 0; j < C::ILOADS; ++j) {
+          const int s = min(j * 64 + lane, 16 * C::IWORDS - 1), row = s / C::IWORDS;
+          const int at = (unit0 + u) * C::IWORDS + s % C::IWORDS;
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(
+              ri, (lds_byte*)(st + u * C::UNIT + 2048 + j * 256), 4,
+              int(uint32_t(min(r0 + row, d.R - 1)) * uint32_t(idx_bytes) + uint32_t(at < d.words ? at : 0) * 4u), 0, 0, 0);
+        }
+      }
+    };
+    // the tokens' operands of the wave's units, kept over all steps
+    u32x8 b[KU][C::PRODUCTS];
+    auto load_tokens = [&] {
+#pragma unroll
+      for (int u = 0; u < KU; ++u)
+#pragma unroll
+        for (int q = 0; q < C::PRODUCTS; ++q)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int k = (unit0 + u) * C::COLS + (2 * h + (lq >> 1)) * C::RUN + 16 * q + 8 * (lq & 1);
+            const bool live = (li < toks) & (k < d.K);
+            const u32x4 v = __builtin_bit_cast(
+                u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                           rx, live_offset(live, (uint32_t(li) * uint32_t(d.ldx) + uint32_t(k)) * 2u), 0, 0));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[u][q][4 * h + e] = v[e];
+          }
+    };
+#pragma unroll
+    for (int s = 0; s < C::D; ++s)
+      if (s < n) issue(s, s);
+    load_tokens();
+
+    int slot = 0;
+    for (int i = 0; i < n; ++i) {
+      // stage i has landed once at most the loads of the stages after it remain
+      // (tokens and stores issued since only make the wait stricter)
+      const int behind = min(n - 1 - i, C::D - 1);
+      static_for<C::D>([&](auto c) {
+        if (behind == decltype(c)::value) wait_vmcnt<decltype(c)::value * C::LOADS>();
+      });
+      asm volatile("" ::: "memory");
+      const unsigned char* st = ring + slot * C::STAGE;
+      u32x4 v[KU][2];
+      uint32_t w0[KU], w1[KU];
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+        const unsigned char* un = st + u * C::UNIT;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          v[u][x] = *reinterpret_cast<const u32x4*>(un + (li * 8 + ((2 * lq + x) ^ (li & 7))) * 16);
+        // the run's 32 index bits (1:8: 48, from bit 0 or 16 of two words)
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(
+            un + 2048 + (P == 2 ? li * 24 + (3 * lq >> 1) * 4 : li * 16 + lq * 4));
+        w0[u] = w[0];
+        w1[u] = 0u;
+        if constexpr (P == 2) w1[u] = w[1];
+      }
+      wait_lgkm0();
+      asm volatile("" ::: "memory");
+      if (i + C::D < n) issue(i + C::D, slot);
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if ((unit0 + u) * 128 + (2 * lq + x) * 16 >= row_bytes) v[u][x] = u32x4{0u, 0u, 0u, 0u};   // past K
+        uint64_t bits = w0[u];
+        if constexpr (P == 2) bits = (bits | uint64_t(w1[u]) << 32) >> (16 * (lq & 1));
+#pragma unroll
+        for (int q = 0; q < C::PRODUCTS; ++q) {
+          u32x4 a;
+          uint32_t ix;
+          if constexpr (P == 0) {
+            a = v[u][q];
+            ix = uint32_t(bits >> (16 * q)) & 0xFFFFu;
+          } else {
+            AFrag t;
+            if constexpr (P == 1) {
+              t.v[0] = v[u][q >> 1][2 * (q & 1)];
+              t.v[1] = v[u][q >> 1][2 * (q & 1) + 1];
+              t.ib = uint32_t(bits >> (8 * q)) & 0xFFu;
+            } else {
+              t.v[0] = v[u][q >> 2][q & 3];
+              t.v[1] = uint32_t(bits >> (6 * q)) & 63u;
+              t.v[2] = 0u;
+              t.ib = 0u;
+            }
+            widen<P>(t, a, ix);
+          }
+          acc = smfmac<DT>(a, b[u][q], acc, ix);
+        }
+      }
+      const int r = ((step0 + i) * rg + mine) * 16 + lq * 4;
+      const bool inside = li < toks && r < d.R;
+      const int64_t o = int64_t(g.t0 + li) * d.ldy + r;
+      const bool whole = (d.ldy & 3) == 0 && r + 3 < d.R;
+      if (ks == 1) {
+        if (inside) store4<DT, OUT>(Y, o, whole, d.R - r, acc);
+      } else {
+        f32x4* buf = part + (i & 1) * (kFewWaves * 64);
+        buf[wave * 64 + lane] = acc;
+        wait_lgkm0();
+        barrier_no_fence();   // (the other buffer's sums were read before this one was written)
+        if (share == (i & (ks - 1))) {
+          f32x4 sum = buf[(wave - share) * 64 + lane];
+          for (int w = 1; w < ks; ++w) sum += buf[(wave - share + w) * 64 + lane];
+          if (inside) store4<DT, OUT>(Y, o, whole, d.R - r, sum);
+        }
+      }
+      slot = slot == C::D - 1 ? 0 : slot + 1;
+    }
+    if (ks > 1) barrier_no_fence();   // the last sums are read before the next job's are written
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Any shape: 128 rows x BT tokens by 4 waves (2 x 2), K in steps of 64.  Each
 // thread loads its share of a step two steps ahead into registers (zeros past the
 // edges of W, of K and of the expert's rows), widens it to the 2:4 operand, and
@@ -501,6 +714,30 @@ hipError_t launch_few(const GroupArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Units a wave of the streaming kernel keeps its tokens for: as many as its registers
+// hold (fewer, in more shares of K, mean more sums: 41 experts of 2816 x 2048 in 1:4
+// with 1 / 2 / 4 units 34.6 / 27.1 / 28.1 us).
+constexpr int stream_units(int P) { return P == 0 ? 4 : 2; }
+int stream_shares(const SpmmArgs& b) {
+  const int P = b.n == 2 ? 0 : b.m == 4 ? 1 : 2;
+  const int64_t cols = 128 << P;   // of a unit
+  int ks = 1;
+  while (ks * stream_units(P) * cols < b.K) ks *= 2;
+  return ks;
+}
+
+template <int P, int DT, int OUT, int KU>
+hipError_t launch_stream(const GroupArgs& a, hipStream_t s) {
+  using C = Stream<P, KU>;
+  static_assert(C::COLS == 128 << P, "a unit's columns");
+  const int ks = stream_shares(a.base);
+  const auto kern = group_stream_kernel<P, DT, OUT, KU>;
+  if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), C::LDS); e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3(unsigned(device_cu_count())), dim3(kFewWaves * 64), C::LDS, s, a.base.values, a.base.idx,
+                     a.base.act, a.offsets, dims_of(a, 16), int(group_max_tiles(a.base.T, a.E, 16)), ks, a.base.Y);
+  return hipGetLastError();
+}
+
 template <int P, int DT, int OUT, int BT>
 hipError_t launch_tile(const GroupArgs& a, hipStream_t s) {
   const GroupDims d = dims_of(a, kBR);
@@ -516,13 +753,27 @@ hipError_t launch_tile(const GroupArgs& a, hipStream_t s) {
 // Tokens an expert has on average, of the experts that can have any.
 int64_t mean_rows(int64_t T, int64_t E) { return T / std::max<int64_t>(1, std::min(T, E)); }
 
+// Whether the streaming kernel takes the weight (whole 16-byte pieces a row, K in its
+// waves' registers, one expert's packed bytes in 32-bit offsets) and has at least four
+// steps a workgroup to stream (2 experts of 4096 x 4096, two steps: 12.4 us against
+// 11.5; 4 experts 19.8 against 20.4; 8 experts 33.9 against 39.1).
+bool stream_applies(const SpmmArgs& b, int64_t E) {
+  const int64_t piece = b.n == 2 ? 16 : b.m == 4 ? 32 : 64, row_bytes = b.K / b.m * b.n * 2;
+  if (b.K % piece != 0 || b.K > 4096 || b.R * row_bytes >= (int64_t(1) << 32)) return false;
+  const int64_t rows = 16 * (kFewWaves / stream_shares(b));
+  return std::min(b.T, E) * ((b.R + rows - 1) / rows) >= 4 * 256;
+}
+
 // Which kernel: by the rows an expert has on average, of those that can have any.
-enum class Pick { few1, few1_wide, few2, tile64, tile128, lds };
+enum class Pick { stream, few1, few1_wide, few2, tile64, tile128, lds };
 
 Pick pick(const SpmmArgs& b, int64_t E) {
   const int64_t mean = mean_rows(b.T, E);
   // 64 rows a wave (the tokens are read a quarter as often) where that leaves waves enough
-  if (mean <= 8) return std::min(b.T, E) * b.R >= 12288 ? Pick::few1_wide : Pick::few1;
+  if (mean <= 8) {
+    if (stream_applies(b, E)) return Pick::stream;
+    return std::min(b.T, E) * b.R >= 12288 ? Pick::few1_wide : Pick::few1;
+  }
   if (mean <= 24) return Pick::few2;
   if (mean <= 64) return Pick::tile64;
   // (by numbers alone: the workspace's size is asked for without a device)
@@ -535,6 +786,7 @@ Pick pick(const SpmmArgs& b, int64_t E) {
 template <int P, int DT, int OUT>
 hipError_t launch_pick(const GroupArgs& a, hipStream_t s) {
   switch (pick(a.base, a.E)) {
+    case Pick::stream: return launch_stream<P, DT, OUT, stream_units(P)>(a, s);
     case Pick::few1: return launch_few<P, DT, OUT, 1, 1, 2>(a, s);
     case Pick::few1_wide: return launch_few<P, DT, OUT, 4, 1, 1>(a, s);
     case Pick::few2: return launch_few<P, DT, OUT, 4, 2, 1>(a, s);

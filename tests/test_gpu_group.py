@@ -4,8 +4,6 @@ Bounds: products of two 16-bit floats are exact in fp32; n of them summed in any
 order with unit 2^-23 (allowing round-toward-zero) are off by at most n 2^-23 of the
 sum of their magnitudes, plus half a step of the output's type.
 """
-import ctypes
-
 import numpy as np
 import pytest
 
@@ -31,14 +29,18 @@ def within(got, ref, size, terms, out):
 
 
 class Case:
-    def __init__(self, lengths, R, K, pat, dt, before=0, behind=0, pad=0, seed=0):
+    def __init__(self, lengths, R, K, pat, dt, before=0, behind=0, pad=0, seed=0, pack_on_gpu=False):
         self.n, self.m = pat
         self.R, self.K, self.dt = R, K, dt
         self.T = before + sum(lengths) + behind
         self.offsets = np.cumsum([before, *lengths]).astype(np.int32)
         seed = seed * 7919 + R * 31 + K + self.T
         w = nm_inputs.normal_half((len(lengths) * R, K), 0.05, dt, 90, 0, seed)
-        v, i = O.prune_pack(w, self.n, self.m)
+        if pack_on_gpu:      # large weights: the pack kernels have tests of their own
+            v, i = nm.nm_compress(to_dev(w, dt), self.n, self.m)
+            v, i = bits_of(v), i.cpu().numpy().view(np.uint32)
+        else:
+            v, i = O.prune_pack(w, self.n, self.m)
         self.values, self.idx = v.reshape(len(lengths), R, -1), i.reshape(len(lengths), R, -1)
         self.act = nm_inputs.normal_half((self.T, K), 1.0, dt, 90, 1, seed)
         self.g = nm_inputs.normal_half((self.T, R), 0.5, dt, 90, 2, seed)
@@ -281,3 +283,34 @@ def test_large_forward_walks_tiles(R, K, dt, out):
     tile has its own workgroup."""
     log(f"group walked tiles R={R} K={K} {dt} {out}")
     Case([9000, 1, 0, 6500, 130, 2999], R, K, (2, 4), dt, before=2, behind=5).forward(out, 1 if out == "f32" else 8)
+
+
+# many experts of few rows, enough steps that workgroups stream; K at and past a wave's units, whole
+# pieces and columns past K in every place, 1, 2, 4 and 8 shares of K
+@pytest.mark.parametrize("E_,R,K,pat", [(40, 4100, 48, (2, 4)), (64, 2100, 512, (2, 4)), (70, 1100, 528, (2, 4)),
+                                        (33, 1030, 1552, (2, 4)), (20, 900, 4096, (2, 4)), (64, 2100, 96, (1, 4)),
+                                        (64, 1100, 1056, (1, 4)), (40, 500, 3104, (1, 4)), (64, 2100, 64, (1, 8)),
+                                        (64, 1100, 1088, (1, 8)), (40, 500, 3136, (1, 8)), (300, 600, 128, (2, 4))])
+def test_streamed_experts(E_, R, K, pat):
+    log(f"group streamed E={E_} R={R} K={K} {pat}")
+    rng = np.random.default_rng(E_ + K)
+    lengths = rng.integers(0, 6, E_)
+    lengths[0], lengths[E_ // 2], lengths[-1] = 17, 0, 16      # two tiles, none, a full one
+    lengths = np.minimum(lengths, 17)
+    c = Case(lengths.tolist(), R, K, pat, "bf16" if E_ % 2 else "f16", before=1, behind=4, pad=8, pack_on_gpu=True)
+    c.d_act[:1], c.d_act[-4:] = float("nan"), float("nan")
+    c.forward("f32", 3)
+    c.forward("bf16" if E_ % 2 else "f16", 8)
+    # equal calls give equal bits, and broken offsets change nothing around the output
+    args = (c.d_values, c.d_idx, c.d_act)
+    ys = [torch.zeros((c.T, R), device="cuda") for _ in range(2)]
+    for y in ys:
+        nm.nm_group_spmm(*args, c.d_off, K, *pat, out=y)
+    whole = torch.full((c.T + 40, R + 4), 77.0, device="cuda")
+    bad = c.d_off.clone()
+    bad[1::2], bad[::2] = c.T + 9, -3
+    nm.nm_group_spmm(*args, bad, K, *pat, out=whole[20: 20 + c.T, :R])
+    torch.cuda.synchronize()
+    assert torch.equal(ys[0], ys[1])
+    w = whole.cpu().numpy()
+    assert (w[:20] == 77).all() and (w[20 + c.T:] == 77).all() and (w[:, R:] == 77).all()
