@@ -479,27 +479,26 @@ __global__ __launch_bounds__(256, 2) void spmm_dw_kernel(const uint32_t* __restr
     goff[j] = uint32_t(grow[j]) * uint32_t(ldg) * 2u + uint32_t(tid & 15) * 16u;
     gloff[j] = uint32_t(kDwActTile + dw_row(grow[j], 288) + (tid & 15) * 16);
   }
-  auto load_chunk = [&](int chunk, u32x4 (&v)[6]) {
+  // piece j of a chunk: 0 .. 3 act, 4 and 5 G
+  auto load_piece = [&](int chunk, u32x4 (&v)[6], int j) {
     const int t0 = chunk * kDwTC;
+    const bool is_act = j < 4;
+    const int row = is_act ? arow[j & 3] : grow[j & 1];
+    const bool live = t0 + row < T;      // false for every chunk past the last
+    const uint32_t o = is_act ? aoff[j & 3] + uint32_t(t0) * uint32_t(ldx) * 2u : goff[j & 1] + uint32_t(t0) * uint32_t(ldg) * 2u;
+    v[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(is_act ? ra : rg, live_offset(live, o), 0, 0));
+  };
+  auto load_chunk = [&](int chunk, u32x4 (&v)[6]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool live = t0 + arow[j] < T;      // false for every chunk past the last
-      v[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                           ra, live_offset(live, aoff[j] + uint32_t(t0) * uint32_t(ldx) * 2u), 0, 0));
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const bool live = t0 + grow[j] < T;
-      v[4 + j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                               rg, live_offset(live, goff[j] + uint32_t(t0) * uint32_t(ldg) * 2u), 0, 0));
-    }
+    for (int j = 0; j < 6; ++j) load_piece(chunk, v, j);
+  };
+  auto write_piece = [&](int stage, const u32x4 (&v)[6], int j) {
+    unsigned char* st = smem + stage * kDwStage;
+    *reinterpret_cast<u32x4*>(st + (j < 4 ? aloff[j & 3] : gloff[j & 1])) = v[j];
   };
   auto write_chunk = [&](int stage, const u32x4 (&v)[6]) {
-    unsigned char* st = smem + stage * kDwStage;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) *reinterpret_cast<u32x4*>(st + aloff[j]) = v[j];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) *reinterpret_cast<u32x4*>(st + gloff[j]) = v[4 + j];
+    for (int j = 0; j < 6; ++j) write_piece(stage, v, j);
   };
 
   // transpose reads: lane L = 16g + 4j + a reads token rows 8g + j and
@@ -534,17 +533,25 @@ __global__ __launch_bounds__(256, 2) void spmm_dw_kernel(const uint32_t* __restr
     wait_lgkm0();
     barrier_no_fence();
     const unsigned char* st = smem + PAR * kDwStage;
-    u32x4 a[kDwFK];
+    // Four slots of eight products, which scheduling barriers keep in order: the next
+    // slot's operand is read, and the next chunk staged and the one after its loads
+    // issued, behind the products (past the last chunk, zeros that nothing reads).
+    u32x4 a[kDwFK], b[2];
+    b[0] = read_tr(st, g_lo, g_hi, wr * 64);
 #pragma unroll
     for (int kf = 0; kf < kDwFK; ++kf) a[kf] = read_tr(st, a_lo, a_hi, wk * 128 + kf * 16);
 #pragma unroll
     for (int rf = 0; rf < kDwFR; ++rf) {
-      const u32x4 b = read_tr(st, g_lo, g_hi, wr * 64 + rf * 16);
+      if (rf + 1 < kDwFR) b[(rf + 1) & 1] = read_tr(st, g_lo, g_hi, wr * 64 + (rf + 1) * 16);
 #pragma unroll
-      for (int kf = 0; kf < kDwFK; ++kf) acc[kf][rf] = mfma32<DT>(a[kf], b, acc[kf][rf]);
+      for (int kf = 0; kf < kDwFK; ++kf) acc[kf][rf] = mfma32<DT>(a[kf], b[rf & 1], acc[kf][rf]);
+#pragma unroll
+      for (int j = rf; j < 6; j += 4) {
+        write_piece(PAR ^ 1, nextv, j);
+        load_piece(c + 3, nextv, j);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if (c + 1 < nchunks) write_chunk(PAR ^ 1, nextv);
-    load_chunk(c + 3, nextv);
   };
   // whole pairs in the loop and an odd last chunk after it: a pair cut short
   // inside the loop would give the back edge a path on which the other
