@@ -934,7 +934,17 @@ def _codes():
 
 def _elsewhere(device) -> bool:
     """Whether `device` is not the current one (a launch on its stream needs it to be)."""
-    return _torch().cuda.current_device() != device.index
+    return _cuda().current_device() != device.index
+
+
+_cuda_module = None
+
+
+def _cuda():
+    global _cuda_module
+    if _cuda_module is None:
+        _cuda_module = _torch().cuda
+    return _cuda_module
 
 
 def _need(size_of, *args) -> int:
@@ -1031,7 +1041,7 @@ def nm_group_spmm(values, idx, act, offsets, K: int, n: int = 2, m: int = 4, out
     out, ldy = _rows_out(out, T, R, od, act)
     need = _group_need(E, R, K, n, m, dt, T, od)
     ws, at = _scratch(need, act)
-    _check(lib().nm_group_spmm(values.data_ptr(), idx.data_ptr(), E, R, K, n, m, dt, act.data_ptr(), T, ldx,
+    _check((_lib or lib()).nm_group_spmm(values.data_ptr(), idx.data_ptr(), E, R, K, n, m, dt, act.data_ptr(), T, ldx,
                                offsets.data_ptr(), out.data_ptr(), ldy, od, at, need, _stream_ptr(dev)))
     return out
 
@@ -1047,7 +1057,7 @@ def nm_group_spmm_dx(values, idx, G, offsets, K: int, n: int = 2, m: int = 4, ou
     out, lddx = _rows_out(out, T, K, od, G)
     need = _group_dx_need(E, T)
     ws, at = _scratch(need, G)
-    _check(lib().nm_group_spmm_dx(values.data_ptr(), idx.data_ptr(), E, R, K, n, m, dt, G.data_ptr(), T, ldg,
+    _check((_lib or lib()).nm_group_spmm_dx(values.data_ptr(), idx.data_ptr(), E, R, K, n, m, dt, G.data_ptr(), T, ldg,
                                   offsets.data_ptr(), out.data_ptr(), lddx, od, at, need, _stream_ptr(dev)))
     return out
 
@@ -1066,7 +1076,7 @@ def nm_group_spmm_dw(idx, G, act, offsets, K: int, n: int = 2, m: int = 4, out_d
         out = G.new_empty(shape, dtype=_torch_dtype(od))
     elif out.shape != shape or out.dtype != _torch_dtype(od) or not out.is_contiguous() or out.device != dev:
         raise ValueError(f"out must be a contiguous {list(shape)} {_torch_dtype(od)} tensor on {dev}")
-    _check(lib().nm_group_spmm_dw(idx.data_ptr(), E, R, K, n, m, dt, G.data_ptr(), T, ldg, act.data_ptr(),
+    _check((_lib or lib()).nm_group_spmm_dw(idx.data_ptr(), E, R, K, n, m, dt, G.data_ptr(), T, ldg, act.data_ptr(),
                                   _row_stride(act), offsets.data_ptr(), out.data_ptr(), od, _stream_ptr(dev)))
     return out
 
@@ -1089,28 +1099,28 @@ def nm_mx_quantize(x):
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return nm_mx_quantize(x)
-    if x.dim() == 3:
-        E, R, K = x.shape
-        q = x.new_empty((E, R, K // 2), dtype=torch.uint8)
-        scale = q.new_empty((E, (K + 255) // 256, R, 8))
-        for e in range(E):
-            _quantize(x[e], dt, q[e], scale[e], dev)
+    L, u8 = _lib or lib(), torch.uint8
+    if x.dim() == 2:
+        T, K = x.shape
+        ldx, unit = x.stride()
+        q = x.new_empty((T, K // 2), dtype=u8)
+        scale = x.new_empty(((K + 255) // 256, T, 8), dtype=u8)
+        if unit != 1:
+            raise ValueError("x must have unit stride along its rows")
+        status = L.nm_mx_quantize(x.data_ptr(), T, K, ldx if T > 1 else K, dt, q.data_ptr(), scale.data_ptr(),
+                                  _stream_ptr(dev))
+        if status:
+            _check(status)
         return q, scale
-    if x.dim() != 2:
-        raise ValueError("x must be [T, K] or [experts, R, K]")
-    T, K = x.shape
-    q = x.new_empty((T, K // 2), dtype=torch.uint8)
-    scale = q.new_empty(((K + 255) // 256, T, 8))
-    _quantize(x, dt, q, scale, dev)
-    return q, scale
-
-
-def _quantize(x, dt, q, scale, dev):
-    T, K = x.shape
-    if x.stride(1) != 1:
-        raise ValueError("x must have unit stride along its rows")
-    _check(lib().nm_mx_quantize(x.data_ptr(), T, K, x.stride(0) if T > 1 else K, dt, q.data_ptr(), scale.data_ptr(),
+    if x.dim() != 3 or x.stride(2) != 1:
+        raise ValueError("x must be [T, K] or [experts, R, K] with unit stride along its rows")
+    E, R, K = x.shape
+    q = x.new_empty((E, R, K // 2), dtype=u8)
+    scale = x.new_empty((E, (K + 255) // 256, R, 8), dtype=u8)
+    for xe, qe, se in zip(x, q, scale):
+        _check(L.nm_mx_quantize(xe.data_ptr(), R, K, _row_stride(xe), dt, qe.data_ptr(), se.data_ptr(),
                                 _stream_ptr(dev)))
+    return q, scale
 
 
 def nm_mx_dequantize(q, scale, dtype=None):
@@ -1133,19 +1143,20 @@ def nm_mx_dequantize(q, scale, dtype=None):
     T, K = q.shape[-2], 2 * q.shape[-1]
     y = q.new_empty(q.shape[:-1] + (K,), dtype=dtype)
     for qe, se, ye in ((q, scale, y),) if q.dim() == 2 else zip(q, scale, y):
-        _check(lib().nm_mx_dequantize(qe.data_ptr(), se.data_ptr(), T, K, ye.data_ptr(), K, dt, _stream_ptr(dev)))
+        _check((_lib or lib()).nm_mx_dequantize(qe.data_ptr(), se.data_ptr(), T, K, ye.data_ptr(), K, dt, _stream_ptr(dev)))
     return y
 
 
 def _check_mx(q, scale, name_q, name_s, device):
     """An operand's two tensors: q [.., T, K / 2] and its scales."""
     u8 = _torch().uint8
-    *lead, T, half = q.shape
+    shape = q.shape
+    half = shape[-1]
     if q.dtype != u8 or half < 16 or half % 16 or not q.is_contiguous() or q.device != device:
         raise ValueError(f"{name_q} must be a contiguous uint8 [.., T, K / 2] tensor on {device}, K a multiple of 32")
-    shape = (*lead, (half + 127) // 128, T, 8)
-    if scale.dtype != u8 or scale.shape != shape or not scale.is_contiguous() or scale.device != device:
-        raise ValueError(f"{name_s} must be a contiguous uint8 {list(shape)} tensor on {device}")
+    want = shape[:-2] + ((half + 127) // 128, shape[-2], 8)
+    if scale.shape != want or scale.dtype != u8 or not scale.is_contiguous() or scale.device != device:
+        raise ValueError(f"{name_s} must be a contiguous uint8 {list(want)} tensor on {device}")
 
 
 def nm_mx_gemm(wq, wscale, xq, xscale, offsets=None, out_dtype=None, out=None):
@@ -1174,7 +1185,7 @@ def nm_mx_gemm(wq, wscale, xq, xscale, offsets=None, out_dtype=None, out=None):
     out, ldy = _rows_out(out, T, R, od, xq)
     need = _mx_need(E, R, K, T, int(grouped), od)
     ws, at = _scratch(need, xq)
-    _check(lib().nm_mx_gemm(wq.data_ptr(), wscale.data_ptr(), E, R, K, xq.data_ptr(), xscale.data_ptr(), T,
+    _check((_lib or lib()).nm_mx_gemm(wq.data_ptr(), wscale.data_ptr(), E, R, K, xq.data_ptr(), xscale.data_ptr(), T,
                             _ptr(offsets), out.data_ptr(), ldy, od, at, need, _stream_ptr(dev)))
     return out
 

@@ -314,3 +314,11 @@ def test_streamed_experts(E_, R, K, pat):
     assert torch.equal(ys[0], ys[1])
     w = whole.cpu().numpy()
     assert (w[:20] == 77).all() and (w[20 + c.T:] == 77).all() and (w[:, R:] == 77).all()
+
+
+@pytest.mark.parametrize("lengths", ["token", "few", "tile64"])
+@pytest.mark.parametrize("pat,K", [((2, 4), 8208), ((1, 4), 8240), ((1, 8), 12304)])
+def test_long_reductions(lengths, pat, K):
+    """K past what a streaming wave keeps, in multiples of 16 only."""
+    log(f"group long K={K} {pat} {lengths}")
+    Case(LENGTHS[lengths], 70, K, pat, "bf16").forward("f32")

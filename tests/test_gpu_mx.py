@@ -259,3 +259,43 @@ def test_empty_stacks_streams_and_graphs():
         want = serve()
         torch.cuda.synchronize()
         assert torch.equal(held, want)
+
+
+@pytest.mark.parametrize("T,R,K", [(3, 70, 9248), (40, 100, 8224), (300, 300, 11264)])
+def test_gemm_long(T, R, K):
+    log(f"mx gemm long {T}x{R}x{K}")
+    check_gemm(T, R, K, "f32")
+
+
+@pytest.mark.parametrize("E_,T", [(70, 90), (300, 500), (300, 30000)])
+def test_gemm_of_many_experts(E_, T):
+    """More experts than a wave looks at in one go; enough for a table of tiles; many rows."""
+    log(f"mx gemm experts={E_} T={T}")
+    R, K = 40, 64
+    lengths = np.bincount(np.random.default_rng(E_).integers(0, E_, T), minlength=E_)
+    lengths[3] = 0
+    T = int(lengths.sum())
+    off = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
+    w, wq, ws = operands(R, K, 3, E_)
+    x, xq, xs = operands(T, K, 4)
+    y = nm.nm_mx_gemm(wq, ws, xq, xs, torch.from_numpy(off).cuda())
+    torch.cuda.synchronize()
+    ids = np.repeat(np.arange(E_), lengths)
+    ref = np.einsum("tk,trk->tr", x, w[ids]) if T < 1000 else np.concatenate(
+        [x[off[e]: off[e + 1]] @ w[e].T for e in range(E_)])
+    size = np.concatenate([np.abs(x[off[e]: off[e + 1]]) @ np.abs(w[e]).T for e in range(E_)])
+    within(f64(y), ref, size, K, "f32")
+
+
+@pytest.mark.parametrize("T", [12, 300])
+@pytest.mark.parametrize("offsets", [[-5, 700, 3, 90], [400, 100, 300, 0], [0, 5, 2 ** 31 - 1, -2 ** 31], [0, 300, 0, 300]])
+def test_broken_offsets_stay_inside(offsets, T):
+    """Clamped (the rule is run over every small list by test_host_offsets); nothing around Y changes."""
+    log(f"mx broken offsets {offsets} T={T}")
+    w, wq, ws = operands(136, 160, 3, 3)
+    x, xq, xs = operands(T, 160, 4)
+    whole = torch.full((T + 600, 144), 77.0, device="cuda")
+    nm.nm_mx_gemm(wq, ws, xq, xs, torch.tensor(offsets, dtype=torch.int32, device="cuda"), out=whole[300: 300 + T, :136])
+    torch.cuda.synchronize()
+    got = whole.cpu().numpy()
+    assert (got[:300] == 77.0).all() and (got[300 + T:] == 77.0).all() and (got[:, 136:] == 77.0).all()
