@@ -556,10 +556,10 @@ nm_status nm_xent_bwd(const void* x, int64_t T, int64_t H, int64_t ldx, const vo
  *                 values, but no access outside the arrays.
  *   act, Y, G, dX as nm_spmm and nm_spmm_dx (ldx, ldg below 2^23); out_dtype NM_F32
  *                 or the input dtype.  dX and dW need R % 8 == 0 and K % 32 == 0.
- *   workspace     device, the bytes of the matching _workspace_size, 16-byte aligned
- *                 (dW needs none).
+ *   workspace     device, the bytes of the matching _workspace_size, 16-byte aligned.
  * Products and sums are fp32, outputs rounded once.  Equal calls give equal bits; the
- * kernel goes by T / min(T, E), so a token's last bits can change with T and E.  Inf
+ * kernel, and the shares a long reduction of few tiles is summed in, go by the sizes,
+ * so a token's last bits can change with T and E.  Inf
  * or NaN in one row reaches the outputs of its expert's row (dW: of its expert) only.
  * 1 <= E <= 65535, T <= 2^24, R and K <= 2^22; NM_ERR_SHAPE as in nm_spmm_dx and
  * nm_spmm_dw for one expert's arrays, and for T x ldg or T x ldx of 4 GiB in dW.
@@ -571,13 +571,14 @@ nm_status nm_group_spmm_workspace_size(int64_t E, int64_t R, int64_t K, int n, i
 nm_status nm_group_spmm(const void* values, const uint32_t* idx, int64_t E, int64_t R, int64_t K, int n, int m,
                         int dtype, const void* act, int64_t T, int64_t ldx, const int32_t* offsets, void* Y,
                         int64_t ldy, int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
-nm_status nm_group_spmm_dx_workspace_size(int64_t E, int64_t T, size_t* bytes);
+nm_status nm_group_spmm_dx_workspace_size(int64_t E, int64_t R, int64_t K, int64_t T, size_t* bytes);
 nm_status nm_group_spmm_dx(const void* values, const uint32_t* idx, int64_t E, int64_t R, int64_t K, int n, int m,
                            int dtype, const void* G, int64_t T, int64_t ldg, const int32_t* offsets, void* dX,
                            int64_t lddx, int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+nm_status nm_group_spmm_dw_workspace_size(int64_t E, int64_t R, int64_t K, int n, int m, int64_t T, size_t* bytes);
 nm_status nm_group_spmm_dw(const uint32_t* idx, int64_t E, int64_t R, int64_t K, int n, int m, int dtype, const void* G,
                            int64_t T, int64_t ldg, const void* act, int64_t ldx, const int32_t* offsets, void* dW,
-                           int out_dtype, void* stream);
+                           int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Microscaled 4-bit floats: a row's values in blocks of 32, each value a sign and

@@ -130,9 +130,10 @@ def lib() -> ctypes.CDLL:
     f64 = ctypes.c_double
     L.nm_group_spmm_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32, i64, i32, ctypes.POINTER(sz)]
     L.nm_group_spmm.argtypes = [vp, vp, i64, i64, i64, i32, i32, i32, vp, i64, i64, vp, vp, i64, i32, vp, sz, vp]
-    L.nm_group_spmm_dx_workspace_size.argtypes = [i64, i64, ctypes.POINTER(sz)]
+    L.nm_group_spmm_dx_workspace_size.argtypes = [i64, i64, i64, i64, ctypes.POINTER(sz)]
     L.nm_group_spmm_dx.argtypes = [vp, vp, i64, i64, i64, i32, i32, i32, vp, i64, i64, vp, vp, i64, i32, vp, sz, vp]
-    L.nm_group_spmm_dw.argtypes = [vp, i64, i64, i64, i32, i32, i32, vp, i64, i64, vp, i64, vp, vp, i32, vp]
+    L.nm_group_spmm_dw_workspace_size.argtypes = [i64, i64, i64, i32, i32, i64, ctypes.POINTER(sz)]
+    L.nm_group_spmm_dw.argtypes = [vp, i64, i64, i64, i32, i32, i32, vp, i64, i64, vp, i64, vp, vp, i32, vp, sz, vp]
     L.nm_mx_sizes.argtypes = [i64, i64, ctypes.POINTER(sz), ctypes.POINTER(sz)]
     L.nm_mx_quantize.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp]
     L.nm_mx_dequantize.argtypes = [vp, vp, i64, i64, vp, i64, i32, vp]
@@ -141,7 +142,7 @@ def lib() -> ctypes.CDLL:
     L.nm_grad_workspace_size.argtypes = [i64, ctypes.POINTER(sz)]
     L.nm_grad_norm.argtypes = [vp, vp, vp, i64, vp, vp, sz, vp]
     L.nm_grad_clip.argtypes = [vp, vp, vp, i64, f64, f64, vp, vp, vp, sz, vp]
-    for name in ("nm_group_spmm_workspace_size", "nm_group_spmm", "nm_group_spmm_dx_workspace_size", "nm_group_spmm_dx",
+    for name in ("nm_group_spmm_workspace_size", "nm_group_spmm", "nm_group_spmm_dx_workspace_size", "nm_group_spmm_dx", "nm_group_spmm_dw_workspace_size",
                  "nm_group_spmm_dw", "nm_mx_sizes", "nm_mx_quantize", "nm_mx_dequantize", "nm_mx_gemm_workspace_size",
                  "nm_mx_gemm", "nm_grad_workspace_size", "nm_grad_norm", "nm_grad_clip"):
         getattr(L, name).restype = i32
@@ -959,8 +960,13 @@ def _group_need(E, R, K, n, m, dt, T, od):
 
 
 @functools.lru_cache(maxsize=4096)
-def _group_dx_need(E, T):
-    return _need(lib().nm_group_spmm_dx_workspace_size, E, T)
+def _group_dw_need(E, R, K, n, m, T):
+    return _need(lib().nm_group_spmm_dw_workspace_size, E, R, K, n, m, T)
+
+
+@functools.lru_cache(maxsize=4096)
+def _group_dx_need(E, R, K, T):
+    return _need(lib().nm_group_spmm_dx_workspace_size, E, R, K, T)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -1055,7 +1061,7 @@ def nm_group_spmm_dx(values, idx, G, offsets, K: int, n: int = 2, m: int = 4, ou
         with _torch().cuda.device(dev):
             return nm_group_spmm_dx(values, idx, G, offsets, K, n, m, out_dtype, out)
     out, lddx = _rows_out(out, T, K, od, G)
-    need = _group_dx_need(E, T)
+    need = _group_dx_need(E, R, K, T)
     ws, at = _scratch(need, G)
     _check((_lib or lib()).nm_group_spmm_dx(values.data_ptr(), idx.data_ptr(), E, R, K, n, m, dt, G.data_ptr(), T, ldg,
                                   offsets.data_ptr(), out.data_ptr(), lddx, od, at, need, _stream_ptr(dev)))
@@ -1076,8 +1082,10 @@ def nm_group_spmm_dw(idx, G, act, offsets, K: int, n: int = 2, m: int = 4, out_d
         out = G.new_empty(shape, dtype=_torch_dtype(od))
     elif out.shape != shape or out.dtype != _torch_dtype(od) or not out.is_contiguous() or out.device != dev:
         raise ValueError(f"out must be a contiguous {list(shape)} {_torch_dtype(od)} tensor on {dev}")
+    need = _group_dw_need(E, R, K, n, m, T)
+    ws, at = _scratch(need, G)
     _check((_lib or lib()).nm_group_spmm_dw(idx.data_ptr(), E, R, K, n, m, dt, G.data_ptr(), T, ldg, act.data_ptr(),
-                                  _row_stride(act), offsets.data_ptr(), out.data_ptr(), od, _stream_ptr(dev)))
+                                  _row_stride(act), offsets.data_ptr(), out.data_ptr(), od, at, need, _stream_ptr(dev)))
     return out
 
 

@@ -1340,11 +1340,11 @@ nm_status nm_group_spmm(const void* values, const uint32_t* idx, int64_t E, int6
   return hip_status(nm::launch_group(a, static_cast<hipStream_t>(stream)), "nm_group_spmm launch");
 }
 
-nm_status nm_group_spmm_dx_workspace_size(int64_t E, int64_t T, size_t* bytes) {
-  if (E < 1 || E > nm::kGroupMaxExperts || T < 0 || T > nm::kGroupMaxTokens)
-    return fail(NM_ERR_SHAPE, "E = %lld or T = %lld out of range", (long long)E, (long long)T);
+nm_status nm_group_spmm_dx_workspace_size(int64_t E, int64_t R, int64_t K, int64_t T, size_t* bytes) {
+  nm_status st = check_group(E, R, K, 2, 4, NM_BF16, T, NM_F32);
+  if (st != NM_OK) return st;
   if (!bytes) return fail(NM_ERR_NULL, "bytes must be non-NULL");
-  *bytes = T == 0 ? 0 : nm::group_dx_workspace(T, E);
+  *bytes = T == 0 ? 0 : nm::group_dx_workspace(R, K, T, E);
   return ok();
 }
 
@@ -1360,7 +1360,7 @@ nm_status nm_group_spmm_dx(const void* values, const uint32_t* idx, int64_t E, i
     return fail(NM_ERR_NULL, "values, idx, G, offsets and dX must be non-NULL");
   if (!aligned16(values) || !aligned16(idx) || !aligned16(G) || !aligned16(dX) || !aligned_to(offsets, 4))
     return fail(NM_ERR_ALIGN, "device pointers must be 16-byte aligned (offsets: 4)");
-  const size_t need = nm::group_dx_workspace(T, E);
+  const size_t need = nm::group_dx_workspace(R, K, T, E);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
   const Sizes z = sizes_of(R, K, n, m, dtype);
   if (z.values_bytes >= (size_t(1) << 32) || z.idx_bytes >= (size_t(1) << 32))
@@ -1392,9 +1392,17 @@ nm_status nm_group_spmm_dx(const void* values, const uint32_t* idx, int64_t E, i
   return hip_status(nm::launch_spmm_dx(a, static_cast<hipStream_t>(stream)), "nm_group_spmm_dx launch");
 }
 
+nm_status nm_group_spmm_dw_workspace_size(int64_t E, int64_t R, int64_t K, int n, int m, int64_t T, size_t* bytes) {
+  nm_status st = check_group(E, R, K, n, m, NM_BF16, T, NM_F32);
+  if (st != NM_OK) return st;
+  if (!bytes) return fail(NM_ERR_NULL, "bytes must be non-NULL");
+  *bytes = nm::group_dw_workspace(R, K, K / m * n, T, E);
+  return ok();
+}
+
 nm_status nm_group_spmm_dw(const uint32_t* idx, int64_t E, int64_t R, int64_t K, int n, int m, int dtype, const void* G,
                            int64_t T, int64_t ldg, const void* act, int64_t ldx, const int32_t* offsets, void* dW,
-                           int out_dtype, void* stream) {
+                           int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
   nm_status st = check_group(E, R, K, n, m, dtype, T, out_dtype);
   if (st != NM_OK) return st;
   if ((st = check_train(R, K, n, m, dtype, T, ldg, out_dtype)) != NM_OK) return st;
@@ -1408,9 +1416,11 @@ nm_status nm_group_spmm_dw(const uint32_t* idx, int64_t E, int64_t R, int64_t K,
     return fail(NM_ERR_SHAPE, "G or act of 4 GiB or more");
   const Sizes z = sizes_of(R, K, n, m, dtype);
   if (z.idx_bytes >= (size_t(1) << 32)) return fail(NM_ERR_SHAPE, "one expert's index words of 4 GiB or more");
+  const size_t need = nm::group_dw_workspace(R, K, z.S, T, E);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
   const Span in[] = {{idx, size_t(E) * z.idx_bytes}, {G, extent(T, R, ldg, 2)}, {act, extent(T, K, ldx, 2)},
                      {offsets, size_t(E + 1) * 4}};
-  const Span out[] = {{dW, size_t(E) * size_t(R) * size_t(z.S) * elt_bytes(out_dtype)}};
+  const Span out[] = {{dW, size_t(E) * size_t(R) * size_t(z.S) * elt_bytes(out_dtype)}, {workspace, need}};
   if ((st = check_alias(in, out)) != NM_OK) return st;
   nm::TrainArgs a{};
   a.idx = idx;
@@ -1430,6 +1440,7 @@ nm_status nm_group_spmm_dw(const uint32_t* idx, int64_t E, int64_t R, int64_t K,
   a.out_dtype = out_dtype;
   a.offsets = offsets;
   a.experts = E;
+  a.table = workspace;
   return hip_status(nm::launch_spmm_dw(a, static_cast<hipStream_t>(stream)), "nm_group_spmm_dw launch");
 }
 

@@ -63,6 +63,8 @@ __global__ __launch_bounds__(kTableThreads) void group_tiles_kernel(const int32_
 struct GroupDims {
   int E, R, K, T, words, tilesR;
   int64_t ldx, ldy;
+  int share = 0;            // steps of K a workgroup takes (0: all), parts part_stride apart
+  int64_t part_stride = 0;
 };
 
 template <int DT, int OUT>
@@ -536,7 +538,13 @@ __global__ __launch_bounds__(256, 2) void group_tile_kernel(const uint16_t* __re
       make_rsrc(idx + (int64_t(g.e) * d.R + r0) * d.words, uint32_t(int64_t(rows) * d.words * 4));
   const __amdgpu_buffer_rsrc_t rx =
       make_rsrc(act + int64_t(g.t0) * d.ldx, uint32_t((int64_t(toks - 1) * d.ldx + d.K) * 2));
-  const int steps = (d.K + 63) >> 6;
+  // the steps this workgroup reduces over: all, or its share (an even number) of them
+  int first = 0, steps = (d.K + 63) >> 6;
+  if (d.share > 0) {
+    first = int(blockIdx.y) * d.share;
+    steps = min(steps, first + d.share);
+    Y = static_cast<float*>(Y) + int64_t(blockIdx.y) * d.part_stride;
+  }
 
   // this thread's share of W: 32 columns (half wh of the step) of row wrow
   const int wrow = tid >> 1, wh = tid & 1;
@@ -628,10 +636,10 @@ __global__ __launch_bounds__(256, 2) void group_tile_kernel(const uint16_t* __re
     for (int j = 0; j < FT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   Share sh[2];
-  load(0, sh[0]);
-  load(1, sh[1]);
-  stage(0, sh[0]);
-  load(2, sh[0]);
+  load(first, sh[0]);
+  load(first + 1, sh[1]);
+  stage(first, sh[0]);
+  load(first + 2, sh[0]);
   auto step = [&](auto par_c, int s) {
     constexpr int PAR = decltype(par_c)::value;
     wait_lgkm0();
@@ -663,7 +671,7 @@ __global__ __launch_bounds__(256, 2) void group_tile_kernel(const uint16_t* __re
     if (s + 1 < steps) stage(s + 1, sh[PAR ^ 1]);
     load(s + 3, sh[PAR ^ 1]);
   };
-  int s = 0;
+  int s = first;
   for (; s + 1 < steps; s += 2) {
     step(std::integral_constant<int, 0>{}, s);
     step(std::integral_constant<int, 1>{}, s + 1);
@@ -682,6 +690,22 @@ __global__ __launch_bounds__(256, 2) void group_tile_kernel(const uint16_t* __re
         store4<DT, OUT>(Y, int64_t(g.t0 + t) * d.ldy + r0 + r, vec && r + 3 < rows, rows - r, acc[i][j]);
     }
   }
+}
+
+// The parts of a shared reduction, added in their order.
+template <int OUT>
+__global__ __launch_bounds__(256) void group_join_kernel(const float* __restrict__ part, int n, int T, int C, int64_t ld,
+                                                         const int32_t* __restrict__ offsets, int E,
+                                                         void* __restrict__ out, int64_t ldo) {
+  int lo = 0, hi = T;
+  if (offsets) lo = rows_lo(offsets[0], T), hi = rows_hi(offsets[E], lo, T);
+  const int t = lo + int(blockIdx.x), c = (int(blockIdx.y) * 256 + int(threadIdx.x)) * 4;
+  if (t >= hi || c >= C) return;
+  const int64_t stride = int64_t(T) * ld;
+  const float* p = part + t * ld + c;
+  f32x4 sum = *reinterpret_cast<const f32x4*>(p);
+  for (int i = 1; i < n; ++i) sum += *reinterpret_cast<const f32x4*>(p + i * stride);
+  store4<OUT, OUT>(out, int64_t(t) * ldo + c, (ldo & 3) == 0 && c + 3 < C, C - c, sum);
 }
 
 GroupDims dims_of(const GroupArgs& a, int rows) {
@@ -738,6 +762,12 @@ hipError_t launch_stream(const GroupArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+int64_t part_ld(int64_t R) { return (R + 3) / 4 * 4; }   // rows on 16 bytes
+
+Shares tile_shares(const SpmmArgs& b, int64_t E, int BT) {
+  return group_shares((b.R + kBR - 1) / kBR * group_max_tiles(b.T, E, BT), (b.K + 63) / 64);
+}
+
 template <int P, int DT, int OUT, int BT>
 hipError_t launch_tile(const GroupArgs& a, hipStream_t s) {
   const GroupDims d = dims_of(a, kBR);
@@ -745,6 +775,20 @@ hipError_t launch_tile(const GroupArgs& a, hipStream_t s) {
   if (tiles * d.tilesR > 0x7FFFFFFF) return hipErrorInvalidValue;
   GroupRows rows;
   if (hipError_t e = group_rows(a.offsets, a.E, a.base.T, BT, tiles, a.workspace, s, rows); e != hipSuccess) return e;
+  const Shares sh = tile_shares(a.base, a.E, BT);
+  if (sh.n > 1) {
+    // partial sums behind the table, joined by a second launch
+    float* part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.workspace) + group_rows_bytes(a.E, tiles));
+    const int64_t ld = part_ld(a.base.R);
+    GroupDims p = d;
+    p.ldy = ld;
+    p.share = sh.size;
+    p.part_stride = a.base.T * ld;
+    hipLaunchKernelGGL((group_tile_kernel<P, DT, NM_F32, BT>), dim3(unsigned(tiles * d.tilesR), unsigned(sh.n)), dim3(256),
+                       0, s, a.base.values, a.base.idx, a.base.act, rows, p, static_cast<void*>(part));
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    return launch_group_join(part, sh.n, a.base.T, a.base.R, ld, a.offsets, int(a.E), a.base.Y, a.base.ldy, OUT, s);
+  }
   hipLaunchKernelGGL((group_tile_kernel<P, DT, OUT, BT>), dim3(unsigned(tiles * d.tilesR)), dim3(256), 0, s,
                      a.base.values, a.base.idx, a.base.act, rows, d, a.base.Y);
   return hipGetLastError();
@@ -777,7 +821,11 @@ Pick pick(const SpmmArgs& b, int64_t E) {
   if (mean <= 24) return Pick::few2;
   if (mean <= 64) return Pick::tile64;
   // (by numbers alone: the workspace's size is asked for without a device)
-  if (b.n == 2 && b.K % 128 == 0 && b.R >= 256) return Pick::lds;
+  // the single weight's large tiles and their table's launch where 96 of them fill the
+  // chip (8 experts of 1024 x 1024: 2048 tokens, 64 tiles, 20.4 us against 13.9 below;
+  // 16 experts of 1408 x 2048: 2048 tokens, 96 tiles, 29.4 against 36.4, 8192 tokens of
+  // 4096 x 2048, 1024 tiles, 108 against 180)
+  if (b.n == 2 && b.K % 128 == 0 && b.R >= 256 && (b.R + 255) / 256 * ((b.T + 127) / 128) >= 96) return Pick::lds;
   // tiles of 128 tokens where there is one for every compute unit
   const int64_t tiles = (b.R + kBR - 1) / kBR * ((b.T + 127) / 128);
   return tiles >= 256 ? Pick::tile128 : Pick::tile64;
@@ -817,16 +865,51 @@ hipError_t launch_group_tiles(const int32_t* offsets, int64_t E, int64_t T, int 
   return hipGetLastError();
 }
 
-size_t group_workspace(const SpmmArgs& base, int64_t E) {
-  switch (pick(base, E)) {
-    case Pick::tile64: return group_rows_bytes(E, group_max_tiles(base.T, E, 64));
-    case Pick::tile128: return group_rows_bytes(E, group_max_tiles(base.T, E, 128));
-    case Pick::lds: return group_table_bytes(group_max_tiles(base.T, E, spmm_lds_tile()));
-    default: return 0;
-  }
+// Shares of at least four steps, an even number of them each (the tiles' stages go by
+// a step's parity), while the workgroups fit the chip twice, and three or more of 32
+// steps or more: a step is a third to two thirds of a microsecond, the join a launch
+// and 2 to 4.  (One token of ten experts of 3184 x 480, dX, 4 tiles of 50 steps: 36.4 us
+// in one, 11.8 in shares.  2130 tokens of 12 experts of 160 x 2912, forward: 25.6 and
+// 20.5.  8192 tokens of 2 experts of 64 x 64, dW: 69.5 and 16.0.  Two shares: 2376
+// tokens of 2 experts of 520 x 2016, forward, 20.7 in one, 25.6 in two.)
+Shares group_shares(int64_t tiles, int64_t steps) {
+  Shares s;
+  if (tiles >= 256 || steps < 32) return s;
+  const int64_t most = std::min<int64_t>(std::min<int64_t>(512 / tiles, steps / 4), 16);
+  if (most < 3) return s;
+  s.size = int((steps + most - 1) / most + 1) & ~1;
+  s.n = int((steps + s.size - 1) / s.size);
+  return s;
 }
 
-size_t group_dx_workspace(int64_t T, int64_t E) { return group_rows_bytes(E, spmm_dx_max_tiles(T, E)); }
+hipError_t launch_group_join(const float* part, int n, int64_t T, int64_t C, int64_t ld, const int32_t* offsets, int E,
+                             void* out, int64_t ldo, int out_dtype, hipStream_t s) {
+  const dim3 grid(unsigned(T), unsigned((C + 1023) / 1024));
+  const auto kern = out_dtype == NM_F32 ? group_join_kernel<NM_F32>
+                    : out_dtype == NM_F16 ? group_join_kernel<NM_F16> : group_join_kernel<NM_BF16>;
+  hipLaunchKernelGGL(kern, grid, dim3(256), 0, s, part, n, int(T), int(C), ld, offsets, E, out, ldo);
+  return hipGetLastError();
+}
+
+size_t group_workspace(const SpmmArgs& base, int64_t E) {
+  const Pick p = pick(base, E);
+  if (p == Pick::lds) return group_table_bytes(group_max_tiles(base.T, E, spmm_lds_tile()));
+  if (p != Pick::tile64 && p != Pick::tile128) return 0;
+  const int BT = p == Pick::tile64 ? 64 : 128;
+  const Shares sh = tile_shares(base, E, BT);
+  return group_rows_bytes(E, group_max_tiles(base.T, E, BT)) +
+         (sh.n > 1 ? size_t(sh.n) * size_t(base.T) * size_t(part_ld(base.R)) * 4 : 0);
+}
+
+size_t group_dx_workspace(int64_t R, int64_t K, int64_t T, int64_t E) {
+  const Shares sh = spmm_dx_shares(R, K, T, E);
+  return group_rows_bytes(E, spmm_dx_max_tiles(T, E)) + (sh.n > 1 ? size_t(sh.n) * size_t(T) * size_t(K) * 4 : 0);
+}
+
+size_t group_dw_workspace(int64_t R, int64_t K, int64_t S, int64_t T, int64_t E) {
+  const int n = spmm_dw_shares(R, K, T, E);
+  return n > 1 ? size_t(n) * size_t(E) * size_t(R) * size_t(S) * 4 : 0;
+}
 
 hipError_t launch_group(const GroupArgs& a, hipStream_t s) {
   if (a.base.n == 2) return pick_type<0>(a, s);

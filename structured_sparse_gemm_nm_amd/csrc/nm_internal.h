@@ -88,9 +88,22 @@ struct TrainArgs {
   // arrays `experts` of them in a row; table: dX's workspace (nm_group.h).
   const int32_t* offsets = nullptr;
   int64_t experts = 0;
-  void* table = nullptr;
+  void* table = nullptr;   // the grouped products' workspace
+  int shares = 1;          // (set by the launch)
 };
 int64_t spmm_dx_max_tiles(int64_t T, int64_t E);
+// How a reduction is shared out where a product's tiles leave most of the chip idle
+// (nm_group.hip): n shares of `size` steps, each summed into a part of its own.
+struct Shares {
+  int n = 1, size = 0;
+};
+Shares group_shares(int64_t tiles, int64_t steps);
+Shares spmm_dx_shares(int64_t R, int64_t K, int64_t T, int64_t E);
+int spmm_dw_shares(int64_t R, int64_t K, int64_t T, int64_t E);
+// out[t][c] = sum of part[i][t][c] over i, rounded to out_dtype, for the rows of any
+// expert (every row: offsets NULL); ld a multiple of 4.
+hipError_t launch_group_join(const float* part, int n, int64_t T, int64_t C, int64_t ld, const int32_t* offsets, int E,
+                             void* out, int64_t ldo, int out_dtype, hipStream_t s);
 hipError_t launch_spmm_dx(const TrainArgs& a, hipStream_t s);
 hipError_t launch_spmm_dw(const TrainArgs& a, hipStream_t s);
 
@@ -288,7 +301,8 @@ constexpr int64_t kGroupMaxExperts = 65535;
 constexpr int64_t kGroupMaxTokens = int64_t(1) << 24, kGroupMaxWidth = int64_t(1) << 22;
 constexpr int64_t kGroupMaxLd = int64_t(1) << 23;   // 128 rows of it stay in 32-bit offsets
 size_t group_workspace(const SpmmArgs& base, int64_t E);   // pointers are not looked at
-size_t group_dx_workspace(int64_t T, int64_t E);
+size_t group_dx_workspace(int64_t R, int64_t K, int64_t T, int64_t E);
+size_t group_dw_workspace(int64_t R, int64_t K, int64_t S, int64_t T, int64_t E);
 hipError_t launch_group(const GroupArgs& a, hipStream_t s);
 
 // Microscaled 4-bit floats (nm_mx.hip).

@@ -37,14 +37,22 @@ namespace {
 // In the place of the experts' rows: one weight for all tokens.
 struct NoGroup {};
 // dX: the tiles, and from one expert's values (index words) to the next.
+// share > 0: workgroup y reduces over that many chunks of R and leaves fp32 sums
+// part_stride bytes from those before it.
 struct GroupDx {
   GroupRows rows;
   int64_t values_stride, idx_stride;
+  int share;
+  int64_t part_stride;
 };
 // dW: the experts' rows, from one's index words to the next, and its gradient (bytes).
+// shares > 1: workgroup y sums over a share of its expert's tokens and leaves it
+// part_stride bytes from the one before.
 struct GroupDw {
   const int32_t* offsets;
   int64_t idx_stride, dw_stride;
+  int shares;
+  int64_t part_stride;
 };
 
 constexpr int pat_n(int P) { return P == 0 ? 2 : 1; }
@@ -169,7 +177,15 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wk = wave >> 1, wt = wave & 1;
   const int li = lane & 15, lq = lane >> 4;
-  const int nchunks = (R + kDxRC - 1) / kDxRC;
+  // the chunks this workgroup reduces over: all, or its share of them
+  int first = 0, nchunks = (R + kDxRC - 1) / kDxRC;
+  if constexpr (std::is_same_v<GR, GroupDx>) {
+    if (experts.share > 0) {
+      first = int(blockIdx.y) * experts.share;
+      nchunks = min(nchunks, first + experts.share);
+      dX = static_cast<unsigned char*>(dX) + int64_t(blockIdx.y) * experts.part_stride;
+    }
+  }
   const int64_t S = int64_t(K) * N / M;
 
   // G: descriptor over the tile's token rows (rows past T reread row T - 1;
@@ -263,11 +279,11 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
   if constexpr (std::is_same_v<LR, LowRank>) ids = lowrank_ids<4>(lowrank, T0 + wt * 64);
   using std::integral_constant;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) load_g(0, gs[0], j);
-  load_pack(0, pk[0]);
+  for (int j = 0; j < 4; ++j) load_g(first, gs[0], j);
+  load_pack(first, pk[0]);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) load_g(1, gs[1], j);
-  load_pack(1, pk[1]);
+  for (int j = 0; j < 4; ++j) load_g(first + 1, gs[1], j);
+  load_pack(first + 1, pk[1]);
   decompress(pk[0], 0, integral_constant<int, 0>{});
   decompress(pk[0], 0, integral_constant<int, 1>{});
   decompress(pk[0], 0, integral_constant<int, 2>{});
@@ -275,8 +291,8 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
 #pragma unroll
   for (int j = 0; j < 4; ++j) write_g(0, gs[0], j);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) load_g(2, gs[0], j);
-  load_pack(2, pk[0]);
+  for (int j = 0; j < 4; ++j) load_g(first + 2, gs[0], j);
+  load_pack(first + 2, pk[0]);
 
   // Step c (parity PAR = c & 1, a compile-time constant: the loop is unrolled
   // by two so the register sets alternate without copies): the barrier
@@ -329,7 +345,7 @@ __global__ __launch_bounds__(256, 2) void spmm_dx_kernel(const uint16_t* __restr
   // inside the loop would give the back edge a path on which the other
   // register set holds the newest loads, and the compiler's waits before
   // every later write of a set would then drain both sets
-  int c = 0;
+  int c = first;
   for (; c + 1 < nchunks; c += 2) {
     step(std::integral_constant<int, 0>{}, c);
     step(std::integral_constant<int, 1>{}, c + 1);
@@ -440,6 +456,12 @@ __global__ __launch_bounds__(256, 2) void spmm_dw_kernel(const uint32_t* __restr
     block -= e * blocks;
     int lo, hi;
     group_range(experts.offsets, e, T, lo, hi);
+    if (experts.shares > 1) {
+      const int per = ((hi - lo + kDwTC - 1) / kDwTC + experts.shares - 1) / experts.shares * kDwTC;
+      lo = min(lo + int(blockIdx.y) * per, hi);   // shares <= 16 and T <= 2^24: no overflow
+      hi = min(lo + per, hi);
+      dW = static_cast<unsigned char*>(dW) + int64_t(blockIdx.y) * experts.part_stride;
+    }
     act += int64_t(lo) * ldx;
     G += int64_t(lo) * ldg;
     T = hi - lo;
@@ -670,9 +692,11 @@ hipError_t launch_dw_cfg(const TrainArgs& a, hipStream_t s) {
   const int64_t tilesK = (a.K + kDwBK - 1) / kDwBK, tilesR = (a.R + kDwBR - 1) / kDwBR;
   if (tilesK * tilesR > 0x7FFFFFFF) return hipErrorInvalidValue;
   auto launch = [&](auto experts, int64_t grid) {
+    unsigned shares = 1;
+    if constexpr (std::is_same_v<decltype(experts), GroupDw>) shares = unsigned(experts.shares);
     auto kern = spmm_dw_kernel<P, DT, OUT, decltype(experts)>;
     if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), kDwLds); e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(256), kDwLds, s, a.idx, uint32_t(a.idx_bytes), int(a.R),
+    hipLaunchKernelGGL(kern, dim3(unsigned(grid), shares), dim3(256), kDwLds, s, a.idx, uint32_t(a.idx_bytes), int(a.R),
                        int(a.K), int(a.idx_row_words), a.G, int(a.T), a.ldg, a.act, a.ldx, a.out, int(tilesK),
                        int(tilesR), pick_group(tilesK, tilesR, 2.0, 1.0), experts);
     return hipGetLastError();
@@ -680,11 +704,29 @@ hipError_t launch_dw_cfg(const TrainArgs& a, hipStream_t s) {
   if (!a.offsets) return launch(NoGroup{}, tilesK * tilesR);
   const int64_t grid = tilesK * tilesR * a.experts;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  return launch(GroupDw{a.offsets, a.R * a.idx_row_words, a.R * (a.K / a.m * a.n) * (OUT == NM_F32 ? 4 : 2)}, grid);
+  GroupDw g{a.offsets, a.R * a.idx_row_words, a.R * (a.K / a.m * a.n) * (OUT == NM_F32 ? 4 : 2), 1, 0};
+  if constexpr (OUT == NM_F32) {
+    if (a.shares > 1) {
+      g.shares = a.shares;
+      g.part_stride = a.experts * g.dw_stride;
+    }
+  }
+  return launch(g, grid);
 }
 
 template <int P, int DT>
 hipError_t launch_dw_out(const TrainArgs& a, hipStream_t s) {
+  const int64_t S = a.K / a.m * a.n;
+  const int n = a.offsets ? spmm_dw_shares(a.R, a.K, a.T, a.experts) : 1;
+  if (n > 1) {
+    // partial sums, joined by a second launch
+    TrainArgs part = a;
+    part.out = a.table;
+    part.shares = n;
+    if (hipError_t e = launch_dw_cfg<P, DT, NM_F32>(part, s); e != hipSuccess) return e;
+    return launch_group_join(static_cast<const float*>(a.table), n, a.experts * a.R, S, S, nullptr, 0, a.out, S,
+                             a.out_dtype, s);
+  }
   return a.out_dtype == NM_F32 ? launch_dw_cfg<P, DT, NM_F32>(a, s) : launch_dw_cfg<P, DT, DT>(a, s);
 }
 
@@ -698,9 +740,12 @@ hipError_t launch_dx_cfg(const TrainArgs& a, const LR& lowrank, const GR& expert
   const int64_t tilesK = (a.K + kDxBK - 1) / kDxBK;
   const int64_t tilesT = a.offsets ? group_max_tiles(a.T, a.experts, kDxBT) : (a.T + kDxBT - 1) / kDxBT;
   if (tilesK * tilesT > 0x7FFFFFFF) return hipErrorInvalidValue;
+  unsigned shares = 1;
+  if constexpr (std::is_same_v<GR, GroupDx>)
+    if (experts.share > 0) shares = unsigned(((a.R + kDxRC - 1) / kDxRC + experts.share - 1) / experts.share);
   auto kern = spmm_dx_kernel<P, DT, OUT, LR, GR>;
   if (hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kern), kDxLds); e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3(unsigned(tilesK * tilesT)), dim3(256), kDxLds, s, a.values,
+  hipLaunchKernelGGL(kern, dim3(unsigned(tilesK * tilesT), shares), dim3(256), kDxLds, s, a.values,
                      uint32_t(a.values_bytes), a.idx, uint32_t(a.idx_bytes), int(a.R), int(a.K),
                      int(a.idx_row_words), a.G, int(a.T), a.ldg, a.out, a.ldo, int(tilesK), int(tilesT),
                      // every column tile of an expert's tokens together: its weight is shared by few token
@@ -717,9 +762,21 @@ hipError_t launch_dx_out(const TrainArgs& a, hipStream_t s) {
     return f32 ? launch_dx_cfg<P, DT, NM_F32>(a, *a.lowrank, NoGroup{}, s)
                : launch_dx_cfg<P, DT, DT>(a, *a.lowrank, NoGroup{}, s);
   if (a.offsets) {
-    GroupDx g{{}, a.R * (a.K / a.m * a.n), a.R * a.idx_row_words};
-    const hipError_t e = group_rows(a.offsets, a.experts, a.T, kDxBT, spmm_dx_max_tiles(a.T, a.experts), a.table, s, g.rows);
-    if (e != hipSuccess) return e;
+    const int64_t tiles = spmm_dx_max_tiles(a.T, a.experts);
+    GroupDx g{{}, a.R * (a.K / a.m * a.n), a.R * a.idx_row_words, 0, 0};
+    if (hipError_t e = group_rows(a.offsets, a.experts, a.T, kDxBT, tiles, a.table, s, g.rows); e != hipSuccess) return e;
+    const Shares sh = spmm_dx_shares(a.R, a.K, a.T, a.experts);
+    if (sh.n > 1) {
+      // partial sums behind the table, joined by a second launch
+      TrainArgs part = a;
+      part.out = static_cast<unsigned char*>(a.table) + group_rows_bytes(a.experts, tiles);
+      part.ldo = a.K;
+      g.share = sh.size;
+      g.part_stride = a.T * a.K * 4;
+      if (hipError_t e = launch_dx_cfg<P, DT, NM_F32>(part, NoLowRank{}, g, s); e != hipSuccess) return e;
+      return launch_group_join(static_cast<const float*>(part.out), sh.n, a.T, a.K, a.K, a.offsets, int(a.experts), a.out,
+                               a.ldo, a.out_dtype, s);
+    }
     return f32 ? launch_dx_cfg<P, DT, NM_F32>(a, NoLowRank{}, g, s) : launch_dx_cfg<P, DT, DT>(a, NoLowRank{}, g, s);
   }
   return f32 ? launch_dx_cfg<P, DT, NM_F32>(a, NoLowRank{}, NoGroup{}, s)
@@ -734,6 +791,16 @@ hipError_t launch_dx_dt(const TrainArgs& a, hipStream_t s) {
 }  // namespace
 
 int64_t spmm_dx_max_tiles(int64_t T, int64_t E) { return group_max_tiles(T, E, kDxBT); }
+
+Shares spmm_dx_shares(int64_t R, int64_t K, int64_t T, int64_t E) {
+  return group_shares((K + kDxBK - 1) / kDxBK * spmm_dx_max_tiles(T, E), (R + kDxRC - 1) / kDxRC);
+}
+
+// dW's reduction is over an expert's tokens, of which the host knows the mean.
+int spmm_dw_shares(int64_t R, int64_t K, int64_t T, int64_t E) {
+  const int64_t tiles = (K + kDwBK - 1) / kDwBK * ((R + kDwBR - 1) / kDwBR) * E;
+  return group_shares(tiles, T / std::max<int64_t>(1, std::min(T, E)) / kDwTC).n;
+}
 
 hipError_t launch_spmm_dw(const TrainArgs& a, hipStream_t s) {
   if (a.n == 2 && a.m == 4) return launch_dw_dt<0>(a, s);

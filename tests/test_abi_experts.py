@@ -26,8 +26,8 @@ def group_dx(values=P, idx=2 * P, E=3, R=64, K=64, n=2, m=4, dt=nm.NM_BF16, G=3 
 
 
 def group_dw(idx=2 * P, E=3, R=64, K=64, n=2, m=4, dt=nm.NM_BF16, G=3 * P, T=4, ldg=64, act=7 * P, ldx=64, off=4 * P,
-             dW=5 * P, od=nm.NM_BF16):
-    return nm.lib().nm_group_spmm_dw(idx, E, R, K, n, m, dt, G, T, ldg, act, ldx, off, dW, od, None)
+             dW=5 * P, od=nm.NM_BF16, ws=6 * P, wsb=1 << 24):
+    return nm.lib().nm_group_spmm_dw(idx, E, R, K, n, m, dt, G, T, ldg, act, ldx, off, dW, od, ws, wsb, None)
 
 
 @pytest.mark.parametrize("call", [group, group_dx, group_dw])
@@ -60,6 +60,9 @@ def test_group_shapes_strides_and_aliases():
     assert group_dw(R=60) == SHAPE and group_dw(K=48) == SHAPE and group_dw(ldx=56) == STRIDE and group_dw(ldg=68) == ALIGN
     assert group_dw(T=1 << 20, ldg=1 << 12) == SHAPE and group_dw(dW=7 * P) == ALIAS and group_dw(dW=2 * P) == ALIAS
     assert group_dw(R=0, dW=None, idx=None) == OK
+    # many tokens, few tiles: partial sums
+    assert group_dw(T=8192, ws=None) == NULL and group_dw(T=8192, wsb=64) == SHAPE and group_dw(T=8192, ws=6 * P + 8) == ALIGN
+    assert group_dw(T=8192, ws=3 * P) == ALIAS
 
 
 def test_group_workspace_sizes():
@@ -67,14 +70,19 @@ def test_group_workspace_sizes():
     ref = ctypes.byref(b)
     f = nm.lib().nm_group_spmm_workspace_size
     assert f(300, 64, 64, 2, 4, nm.NM_BF16, 30000, nm.NM_F32, ref) == OK and 0 < b.value < 1 << 16
-    assert f(8, 512, 256, 2, 4, nm.NM_BF16, 1000, nm.NM_F32, ref) == OK and 0 < b.value < 1 << 16
+    assert f(8, 2048, 256, 2, 4, nm.NM_BF16, 2000, nm.NM_F32, ref) == OK and 0 < b.value < 1 << 16
     assert f(8, 64, 64, 2, 4, nm.NM_BF16, 8, nm.NM_F32, ref) == OK and b.value == 0
     assert f(8, 64, 64, 2, 4, nm.NM_BF16, 0, nm.NM_F32, ref) == OK and b.value == 0
     assert f(0, 64, 64, 2, 4, nm.NM_BF16, 10, nm.NM_F32, ref) == SHAPE
     assert f(8, 64, 64, 2, 4, nm.NM_BF16, 10, nm.NM_F32, None) == NULL
     g = nm.lib().nm_group_spmm_dx_workspace_size
-    assert g(300, 1000, ref) == OK and 0 < b.value < 1 << 16 and g(8, 1000, ref) == OK and b.value == 0
-    assert g(8, -1, ref) == SHAPE and g(1 << 20, 5, ref) == SHAPE and g(8, 10, None) == NULL
+    assert g(300, 64, 64, 1000, ref) == OK and 0 < b.value < 1 << 16 and g(8, 64, 64, 1000, ref) == OK and b.value == 0
+    assert g(8, 4096, 64, 100, ref) == OK and 2 * 100 * 64 * 4 <= b.value < 1 << 24       # in shares
+    w = nm.lib().nm_group_spmm_dw_workspace_size
+    assert w(8, 64, 64, 2, 4, 1000, ref) == OK and b.value == 0
+    assert w(2, 64, 64, 2, 4, 8192, ref) == OK and b.value == 16 * 2 * 64 * 32 * 4
+    assert w(2, 64, 64, 2, 4, -1, ref) == SHAPE and w(2, 64, 64, 3, 4, 5, ref) == UNSUPPORTED and w(2, 64, 64, 2, 4, 5, None) == NULL
+    assert g(8, 64, 64, -1, ref) == SHAPE and g(1 << 20, 64, 64, 5, ref) == SHAPE and g(8, 64, 64, 10, None) == NULL
 
 
 def quantize(x=P, T=4, K=64, ldx=64, dt=nm.NM_BF16, q=2 * P, s=3 * P):

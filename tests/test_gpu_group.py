@@ -97,6 +97,30 @@ def test_forward(lengths, pat, dt, out):
     Case(LENGTHS[lengths], 200, 192, pat, dt).forward(out)
 
 
+# few tiles and a long reduction: summed in shares, the last one shorter, joined in order
+@pytest.mark.parametrize("pat", PAT)
+@pytest.mark.parametrize("dt,out", [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f16", "f32")])
+@pytest.mark.parametrize("lengths,R,K", [([33, 2, 0, 90], 131, 2208), ([260, 0, 150], 72, 2080), ([70], 6, 8224)])
+def test_forward_in_shares(lengths, R, K, pat, dt, out):
+    log(f"group shares forward {lengths} {R} {K} {pat} {dt} {out}")
+    c = Case(lengths, R, K, pat, dt)
+    assert nm._group_need(len(lengths), R, K, *pat, nm.NM_BF16, c.T, nm.NM_F32) > 2 * 4 * c.T * R
+    c.forward(out)
+    c.forward(out, ldpad=3)
+
+
+@pytest.mark.parametrize("pat", PAT)
+@pytest.mark.parametrize("dt,out", [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f16", "f32")])
+@pytest.mark.parametrize("lengths,R,K", [([1, 0, 1], 2056, 96), ([33, 150, 0], 2216, 160), ([1100, 0, 2200], 72, 96),
+                                         ([2049], 136, 288)])
+def test_backward_in_shares(lengths, R, K, pat, dt, out):
+    log(f"group shares backward {lengths} {R} {K} {pat} {dt} {out}")
+    c = Case(lengths, R, K, pat, dt)
+    assert nm._group_dx_need(len(lengths), R, K, c.T) + nm._group_dw_need(len(lengths), R, K, *pat, c.T) > 0
+    c.backward(out)
+    c.backward(out, ldpad=8)
+
+
 # rows and columns at and past the tiles' edges; K of 16 and odd multiples of it
 @pytest.mark.parametrize("R,K", [(1, 16), (15, 48), (17, 64), (127, 80), (128, 128), (129, 144), (257, 1040), (96, 2064), (640, 512)])
 @pytest.mark.parametrize("pat", PAT)
@@ -252,6 +276,46 @@ def test_captured_and_replayed_with_other_offsets(lengths):
         torch.cuda.synchronize()
         for a, b, d in zip(held, held_other, want):
             assert torch.equal(a, d) and torch.equal(b, d)
+
+
+@pytest.mark.parametrize("T,R,K", [(700, 4104, 256), (130, 72, 2208), (96, 2216, 96), (3300, 72, 96)])
+def test_large_and_shared_products_follow_their_offsets(T, R, K):
+    """The large tiles' table and the parts of a shared reduction (forward, dX, dW): captured twice and replayed
+    with other offsets, broken ones among them; nothing around the outputs changes."""
+    log(f"group graph T={T} R={R} K={K}")
+    c = Case([T // 2, 0, T - T // 2], R, K, (2, 4), "bf16", before=1, behind=3)
+    dt = torch.bfloat16
+    outs = [[torch.full((c.T + 20, w + 8), 77.0, dtype=dt, device="cuda") for w in (R, K)] for _ in range(3)]
+
+    def all_three(o):
+        nm.nm_group_spmm(c.d_values, c.d_idx, c.d_act, c.d_off, K, out_dtype=dt, out=o[0][10: 10 + c.T, :R])
+        nm.nm_group_spmm_dx(c.d_values, c.d_idx, c.d_g, c.d_off, K, out_dtype=dt, out=o[1][10: 10 + c.T, :K])
+        return nm.nm_group_spmm_dw(c.d_idx, c.d_g, c.d_act, c.d_off, K, out_dtype=dt)
+    all_three(outs[2])
+    torch.cuda.synchronize()
+    graphs, held = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for graph, o in zip(graphs, outs):
+        with torch.cuda.graph(graph):
+            held.append(all_three(o))
+    for offsets in ([1, 1, 40, T], [0, T, T, T + 4], [5, 9, T, T], [9, 9, 9, 9], [T, 3, 700, -1], [-5, T + 99, 0, 50]):
+        for o in outs:
+            for y in o:
+                y.fill_(77.0)
+        c.d_off.copy_(torch.tensor(offsets, dtype=torch.int32))
+        for graph in graphs:
+            graph.replay()
+        want = all_three(outs[2])
+        torch.cuda.synchronize()
+        whole = offsets == sorted(offsets)
+        for k, cols in enumerate((R, K)):
+            for o in outs:
+                w = o[k].float()
+                assert (w[:10] == 77).all() and (w[10 + c.T:] == 77).all() and (w[:, cols:] == 77).all()
+                if whole:
+                    assert (w[10: 10 + offsets[0]] == 77).all() and (w[10 + offsets[-1]:] == 77).all()
+                    assert torch.equal(o[k], outs[2][k])
+        if whole:
+            assert torch.equal(held[0], want) and torch.equal(held[1], want)
 
 
 def test_one_expert_is_the_plain_product():
