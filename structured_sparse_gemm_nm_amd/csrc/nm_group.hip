@@ -874,7 +874,7 @@ hipError_t launch_group_tiles(const int32_t* offsets, int64_t E, int64_t T, int 
 // tokens of 2 experts of 520 x 2016, forward, 20.7 in one, 25.6 in two.)
 Shares group_shares(int64_t tiles, int64_t steps) {
   Shares s;
-  if (tiles >= 256 || steps < 32) return s;
+  if (tiles <= 0 || tiles >= 256 || steps < 32) return s;   // (none: a weight without rows)
   const int64_t most = std::min<int64_t>(std::min<int64_t>(512 / tiles, steps / 4), 16);
   if (most < 3) return s;
   s.size = int((steps + most - 1) / most + 1) & ~1;

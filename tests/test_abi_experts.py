@@ -85,6 +85,17 @@ def test_group_workspace_sizes():
     assert g(8, 64, 64, -1, ref) == SHAPE and g(1 << 20, 64, 64, 5, ref) == SHAPE and g(8, 64, 64, 10, None) == NULL
 
 
+def test_experts_without_rows_of_weight():
+    """R = 0 is a valid, empty weight however many tokens there are: nothing to share out."""
+    b = ctypes.c_size_t(1)
+    ref = ctypes.byref(b)
+    for T in (0, 1, 1 << 14, 1 << 24):
+        assert nm.lib().nm_group_spmm_dw_workspace_size(2, 0, 64, 2, 4, T, ref) == OK and b.value == 0
+        assert nm.lib().nm_group_spmm_workspace_size(2, 0, 64, 2, 4, nm.NM_BF16, T, nm.NM_F32, ref) == OK and b.value == 0
+        assert nm.lib().nm_group_spmm_dx_workspace_size(2, 0, 64, T, ref) == OK
+        assert group_dw(R=0, T=T, ldg=8, dW=None, idx=None) == OK
+
+
 def quantize(x=P, T=4, K=64, ldx=64, dt=nm.NM_BF16, q=2 * P, s=3 * P):
     return nm.lib().nm_mx_quantize(x, T, K, ldx, dt, q, s, None)
 
