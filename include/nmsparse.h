@@ -636,8 +636,8 @@ nm_status nm_mx_gemm(const uint8_t* wq, const uint8_t* wscale, int64_t E, int64_
  *               16-byte aligned.
  * Squares are summed in 64 bits, so that neither large nor small gradients leave the
  * range; each out_i is rounded once.  A NaN anywhere makes norm and every out_i NaN; an
- * Inf makes norm Inf, itself NaN and everything else 0 (max_norm finite).  A norm + eps
- * of 0 scales by 1.  Equal calls give equal bits.
+ * Inf makes norm Inf, itself NaN and everything else 0 (with max_norm Inf nothing is
+ * scaled).  A norm + eps of 0 scales by 1.  Equal calls give equal bits.
  * tensors <= 16384, counts <= 2^36; max_norm >= 0 (Inf: no limit), eps >= 0
  * (NM_ERR_SHAPE).  Nothing written may overlap anything else (NM_ERR_ALIAS): a tensor
  * named twice in place among them.  Stream-ordered; nothing is allocated or synchronised.

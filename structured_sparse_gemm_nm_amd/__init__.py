@@ -1206,7 +1206,7 @@ class GradList:
     """Gradients to be measured or clipped together, and where the clipped ones go
     (in place unless `out` names as many tensors of the same sizes and types).
 
-    A training loop whose gradients keep their tensors makes one and passes it to
+    A training loop whose gradients keep their tensors and sizes makes one and passes it to
     nm_grad_norm and nm_grad_clip every step: the tensors are checked here, once, and
     a call only asks each for its address (a tensor that has been given other memory
     since is noticed, and the list checked again)."""

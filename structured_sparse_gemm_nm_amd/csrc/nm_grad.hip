@@ -211,8 +211,9 @@ __global__ __launch_bounds__(kThreads) void grad_clip_kernel(const ClipBatch b, 
   __shared__ double red[kThreads / 64];
   const double norm = __builtin_sqrt(total_of<kThreads>(partial, slots, red));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = float(norm);
-  // a NaN norm gives a NaN factor; nothing to divide by gives 1
-  const double ratio = norm + eps == 0.0 ? 1.0 : max_norm / (norm + eps);
+  // a NaN norm gives a NaN factor; nothing to divide by, or no limit (Inf / Inf), gives 1
+  const bool one = norm + eps == 0.0 || (__builtin_isinf(max_norm) && __builtin_isinf(norm));
+  const double ratio = one ? 1.0 : max_norm / (norm + eps);
   // a factor that fp32 holds with fewer bits, beside gradients near its end, goes in two
   const bool tiny = ratio < 0x1p-64;
   const float pre = tiny ? 0x1p-64f : 1.f;

@@ -136,6 +136,22 @@ def test_nonfinite():
     assert torch.isnan(norm) and all(torch.isnan(o).all() for o in out)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_no_limit_scales_nothing(in_place):
+    """max_norm Inf is no limit, of an infinite norm too; a NaN still reaches everything."""
+    log(f"grad no limit {in_place}")
+    gs = grads(MIXED)
+    gs[4][77] = -float("inf")
+    before = [g.clone() for g in gs]
+    norm, out = nm.nm_grad_clip(gs, float("inf"), out=None if in_place else [torch.empty_like(g) for g in gs])
+    torch.cuda.synchronize()
+    assert float(norm) == float("inf") and all(torch.equal(o, b) for o, b in zip(out, before))
+    gs[0][3, 3] = float("nan")
+    norm, out = nm.nm_grad_clip(gs, float("inf"))
+    torch.cuda.synchronize()
+    assert torch.isnan(norm) and all(torch.isnan(o).all() for o in out)
+
+
 def test_nothing_to_clip_leaves_the_bits():
     log("grad untouched")
     gs = grads(MIXED)
