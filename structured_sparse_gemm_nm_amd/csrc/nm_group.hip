@@ -873,15 +873,19 @@ hipError_t launch_group_tiles(const int32_t* offsets, int64_t E, int64_t T, int 
 }
 
 // Shares of at least four steps, an even number of them each (the tiles' stages go by
-// a step's parity), while the workgroups fit the chip twice, and three or more of 32
-// steps or more: a step is a third to two thirds of a microsecond, the join a launch
+// a step's parity), while the workgroups fit the chip twice, and three or more: of 32
+// steps or more, or, where at most 64 tiles leave three quarters of the chip idle (and the
+// parts are small), of 16.  A step is a third to a whole microsecond, the join a launch
 // and 2 to 4.  (One token of ten experts of 3184 x 480, dX, 4 tiles of 50 steps: 36.4 us
 // in one, 11.8 in shares.  2130 tokens of 12 experts of 160 x 2912, forward: 25.6 and
 // 20.5.  8192 tokens of 2 experts of 64 x 64, dW: 69.5 and 16.0.  Two shares: 2376
-// tokens of 2 experts of 520 x 2016, forward, 20.7 in one, 25.6 in two.)
+// tokens of 2 experts of 520 x 2016, forward, 20.7 in one, 25.6 in two.  64 tokens of 4
+// experts of 1536 x 1024, dX, 32 tiles of 24 steps: 20.3 and 10.9; 200 tokens of 512 x
+// 1280, forward, 16 of 20: 11.5 and 8.7; 900 tokens of 1024 x 512, dW, 16 of 28: 21.0 and
+// 15.2; but 1333 tokens of 5 experts of 1000 x 1056, dX, 135 of 16: 15.7 and 23.1.)
 Shares group_shares(int64_t tiles, int64_t steps) {
   Shares s;
-  if (tiles <= 0 || tiles >= 256 || steps < 32) return s;   // (none: a weight without rows)
+  if (tiles <= 0 || tiles >= 256 || steps < (tiles <= 64 ? 16 : 32)) return s;   // (none: a weight without rows)
   const int64_t most = std::min<int64_t>(std::min<int64_t>(512 / tiles, steps / 4), 16);
   if (most < 3) return s;
   s.size = int((steps + most - 1) / most + 1) & ~1;

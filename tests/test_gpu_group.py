@@ -121,6 +121,32 @@ def test_backward_in_shares(lengths, R, K, pat, dt, out):
     c.backward(out, ldpad=8)
 
 
+# at most 64 tiles of 16 to 31 steps: in three or four shares; one step or one tile past that, in one
+@pytest.mark.parametrize("pat", PAT)
+@pytest.mark.parametrize("out", ["f16", "f32"])
+@pytest.mark.parametrize("lengths,R,K,shared", [([70, 0, 61], 133, 1040, True), ([200], 512, 1936, True),
+                                                ([130], 4104, 1040, False), ([200], 72, 960, False)])
+def test_forward_in_few_shares(lengths, R, K, shared, pat, out):
+    log(f"group few shares forward {lengths} {R} {K} {pat} {out}")
+    c = Case(lengths, R, K, pat, "f16")
+    need = nm._group_need(len(lengths), R, K, *pat, nm.NM_F16, c.T, nm.NM_F32)
+    assert need > 2 * 4 * c.T * R if shared else need == 0
+    c.forward(out)
+
+
+@pytest.mark.parametrize("pat", PAT)
+@pytest.mark.parametrize("out", ["f16", "f32"])
+@pytest.mark.parametrize("lengths,R,K,dx,dw", [([1, 0, 3], 1032, 96, True, False), ([33, 90], 1992, 1056, True, False),
+                                               ([520], 72, 96, False, True), ([300, 724], 1032, 288, True, True),
+                                               ([40], 1016, 2080, True, False), ([40], 952, 96, False, False)])
+def test_backward_in_few_shares(lengths, R, K, dx, dw, pat, out):
+    log(f"group few shares backward {lengths} {R} {K} {pat} {out}")
+    c = Case(lengths, R, K, pat, "f16")
+    assert (nm._group_dx_need(len(lengths), R, K, c.T) > 0) == dx
+    assert (nm._group_dw_need(len(lengths), R, K, *pat, c.T) > 0) == dw
+    c.backward(out)
+
+
 # rows and columns at and past the tiles' edges; K of 16 and odd multiples of it
 @pytest.mark.parametrize("R,K", [(1, 16), (15, 48), (17, 64), (127, 80), (128, 128), (129, 144), (257, 1040), (96, 2064), (640, 512)])
 @pytest.mark.parametrize("pat", PAT)
