@@ -600,6 +600,10 @@ nm_status nm_group_spmm_dw(const uint32_t* idx, int64_t E, int64_t R, int64_t K,
  *          its element; K % 32 == 0.
  * nm_mx_dequantize: y [T, K] (ldy >= K; NM_F16, NM_BF16 or NM_F32), the values,
  *   rounded once where the type does not hold them.
+ * nm_mx_quantize_stack, nm_mx_dequantize_stack: the same of E matrices [R, K], q and scale one matrix after the other (as nm_mx_gemm reads E weights),
+ *   x and y `stride` elements apart (x: any, 0 repeats one; y: no less than a matrix).
+ *   E <= 2^24; E = 0 does nothing.  With E = 1 for one matrix of such a stack, whose
+ *   scales begin on 8 bytes only.
  * nm_mx_gemm: Y[t][r] = sum_k x[t][k] w[r][k] of two quantised operands.
  *   wq, wscale  E weights of R rows one after the other, each as above (E = 1
  *               without offsets);  xq, xscale  T rows.
@@ -608,14 +612,19 @@ nm_status nm_group_spmm_dw(const uint32_t* idx, int64_t E, int64_t R, int64_t K,
  *   Y           device [T, R] row-major, ldy >= R, NM_F32, NM_F16 or NM_BF16.
  * Products are exact, sums fp32, outputs rounded once.  T <= 2^24, R and K <= 2^22,
  * an operand's scales below 4 GiB.  Device pointers 16-byte aligned (x, y: their
- * element; offsets: 4); outputs and workspace must not overlap anything
- * (NM_ERR_ALIAS).  Stream-ordered; nothing is allocated or synchronised.
+ * element; offsets: 4; the scales of nm_mx_gemm and of the _stack calls: 8); outputs
+ * and workspace must not overlap anything (NM_ERR_ALIAS).  Stream-ordered; nothing is
+ * allocated or synchronised.
  */
 nm_status nm_mx_sizes(int64_t T, int64_t K, size_t* q_bytes, size_t* scale_bytes);
 nm_status nm_mx_quantize(const void* x, int64_t T, int64_t K, int64_t ldx, int dtype, uint8_t* q, uint8_t* scale,
                          void* stream);
 nm_status nm_mx_dequantize(const uint8_t* q, const uint8_t* scale, int64_t T, int64_t K, void* y, int64_t ldy,
                            int dtype, void* stream);
+nm_status nm_mx_quantize_stack(const void* x, int64_t E, int64_t R, int64_t K, int64_t ldx, int64_t stride, int dtype,
+                               uint8_t* q, uint8_t* scale, void* stream);
+nm_status nm_mx_dequantize_stack(const uint8_t* q, const uint8_t* scale, int64_t E, int64_t R, int64_t K, void* y,
+                                 int64_t ldy, int64_t stride, int dtype, void* stream);
 nm_status nm_mx_gemm_workspace_size(int64_t E, int64_t R, int64_t K, int64_t T, int grouped, int out_dtype,
                                     size_t* bytes);
 nm_status nm_mx_gemm(const uint8_t* wq, const uint8_t* wscale, int64_t E, int64_t R, int64_t K, const uint8_t* xq,

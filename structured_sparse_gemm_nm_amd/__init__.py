@@ -137,13 +137,16 @@ def lib() -> ctypes.CDLL:
     L.nm_mx_sizes.argtypes = [i64, i64, ctypes.POINTER(sz), ctypes.POINTER(sz)]
     L.nm_mx_quantize.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp]
     L.nm_mx_dequantize.argtypes = [vp, vp, i64, i64, vp, i64, i32, vp]
+    L.nm_mx_quantize_stack.argtypes = [vp, i64, i64, i64, i64, i64, i32, vp, vp, vp]
+    L.nm_mx_dequantize_stack.argtypes = [vp, vp, i64, i64, i64, vp, i64, i64, i32, vp]
     L.nm_mx_gemm_workspace_size.argtypes = [i64, i64, i64, i64, i32, i32, ctypes.POINTER(sz)]
     L.nm_mx_gemm.argtypes = [vp, vp, i64, i64, i64, vp, vp, i64, vp, vp, i64, i32, vp, sz, vp]
     L.nm_grad_workspace_size.argtypes = [i64, ctypes.POINTER(sz)]
     L.nm_grad_norm.argtypes = [vp, vp, vp, i64, vp, vp, sz, vp]
     L.nm_grad_clip.argtypes = [vp, vp, vp, i64, f64, f64, vp, vp, vp, sz, vp]
     for name in ("nm_group_spmm_workspace_size", "nm_group_spmm", "nm_group_spmm_dx_workspace_size", "nm_group_spmm_dx", "nm_group_spmm_dw_workspace_size",
-                 "nm_group_spmm_dw", "nm_mx_sizes", "nm_mx_quantize", "nm_mx_dequantize", "nm_mx_gemm_workspace_size",
+                 "nm_group_spmm_dw", "nm_mx_sizes", "nm_mx_quantize", "nm_mx_dequantize", "nm_mx_quantize_stack",
+                 "nm_mx_dequantize_stack", "nm_mx_gemm_workspace_size",
                  "nm_mx_gemm", "nm_grad_workspace_size", "nm_grad_norm", "nm_grad_clip"):
         getattr(L, name).restype = i32
     _lib = L
@@ -1125,9 +1128,8 @@ def nm_mx_quantize(x):
     E, R, K = x.shape
     q = x.new_empty((E, R, K // 2), dtype=u8)
     scale = x.new_empty((E, (K + 255) // 256, R, 8), dtype=u8)
-    for xe, qe, se in zip(x, q, scale):
-        _check(L.nm_mx_quantize(xe.data_ptr(), R, K, _row_stride(xe), dt, qe.data_ptr(), se.data_ptr(),
-                                _stream_ptr(dev)))
+    _check(L.nm_mx_quantize_stack(x.data_ptr(), E, R, K, x.stride(1) if R > 1 else K, x.stride(0) if E > 1 else 0, dt,
+                                  q.data_ptr(), scale.data_ptr(), _stream_ptr(dev)))
     return q, scale
 
 
@@ -1148,10 +1150,11 @@ def nm_mx_dequantize(q, scale, dtype=None):
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return nm_mx_dequantize(q, scale, dtype)
-    T, K = q.shape[-2], 2 * q.shape[-1]
+    E, T, K = q.shape[0] if q.dim() == 3 else 1, q.shape[-2], 2 * q.shape[-1]
     y = q.new_empty(q.shape[:-1] + (K,), dtype=dtype)
-    for qe, se, ye in ((q, scale, y),) if q.dim() == 2 else zip(q, scale, y):
-        _check((_lib or lib()).nm_mx_dequantize(qe.data_ptr(), se.data_ptr(), T, K, ye.data_ptr(), K, dt, _stream_ptr(dev)))
+    # (of one matrix too: it may be an expert's of a stack, whose scales begin on 8 bytes)
+    _check((_lib or lib()).nm_mx_dequantize_stack(q.data_ptr(), scale.data_ptr(), E, T, K, y.data_ptr(), K, T * K, dt,
+                                                  _stream_ptr(dev)))
     return y
 
 

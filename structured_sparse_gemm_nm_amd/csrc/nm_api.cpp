@@ -1469,50 +1469,98 @@ nm_status nm_mx_sizes(int64_t T, int64_t K, size_t* q_bytes, size_t* scale_bytes
   return ok();
 }
 
-nm_status nm_mx_quantize(const void* x, int64_t T, int64_t K, int64_t ldx, int dtype, uint8_t* q, uint8_t* scale,
-                         void* stream) {
-  nm_status st = check_mx("T", T, K);
-  if (st != NM_OK || (st = check_mx_float(dtype)) != NM_OK || (st = check_ld("ldx", ldx, T, K)) != NM_OK) return st;
-  if (T == 0) return ok();
+// E matrices, `stride` elements of x (y) apart.
+static nm_status check_mx_stack(const char* rows_name, int64_t E, int64_t R, int64_t K, int dtype, const char* ld_name,
+                                int64_t ld, int64_t stride) {
+  nm_status st = check_mx(rows_name, R, K);
+  if (st != NM_OK || (st = check_mx_float(dtype)) != NM_OK || (st = check_ld(ld_name, ld, R, K)) != NM_OK) return st;
+  if (E < 0 || E > nm::kMxMaxRows) return fail(NM_ERR_SHAPE, "E = %lld out of range [0, 2^24]", (long long)E);
+  if (stride < 0) return fail(NM_ERR_STRIDE, "stride = %lld is negative", (long long)stride);
+  if (E > 0 && (stride > kMaxElems / E || R * K > kMaxElems / E))
+    return fail(NM_ERR_SHAPE, "a stack above 2^40 elements");
+  return NM_OK;
+}
+
+static size_t mx_stack_extent(int64_t E, int64_t R, int64_t K, int64_t ld, int64_t stride, size_t e) {
+  return size_t(E - 1) * size_t(stride) * e + extent(R, K, ld, e);
+}
+
+// An expert's scales are a multiple of 8 bytes long, so in a stack they begin on 8;
+// the kernels read them by the byte (nm_mx_gemm: two or four).
+static nm_status mx_quantize(const void* x, int64_t E, int64_t R, int64_t K, int64_t ldx, int64_t stride, int dtype,
+                             uint8_t* q, uint8_t* scale, size_t scale_align, hipStream_t s) {
+  if (E == 0 || R == 0) return ok();
   if (!x || !q || !scale) return fail(NM_ERR_NULL, "x, q and scale must be non-NULL");
   const size_t e = elt_bytes(dtype);
-  if (!aligned_to(x, e) || !aligned16(q) || !aligned16(scale))
-    return fail(NM_ERR_ALIGN, "q and scale must be 16-byte aligned, x to its element");
-  const Span in[] = {{x, extent(T, K, ldx, e)}};
-  const Span out[] = {{q, size_t(T) * size_t(K / 2)}, {scale, mx_scale_bytes(T, K)}};
-  if ((st = check_alias(in, out)) != NM_OK) return st;
+  if (!aligned_to(x, e) || !aligned16(q) || !aligned_to(scale, scale_align))
+    return fail(NM_ERR_ALIGN, "q must be 16-byte aligned, scale %zu, x to its element", scale_align);
+  const Span in[] = {{x, mx_stack_extent(E, R, K, ldx, stride, e)}};
+  const Span out[] = {{q, size_t(E) * size_t(R) * size_t(K / 2)}, {scale, size_t(E) * mx_scale_bytes(R, K)}};
+  if (nm_status st = check_alias(in, out); st != NM_OK) return st;
   nm::MxQuantArgs a;
-  a.T = T;
+  a.E = E;
+  a.T = R;
   a.K = K;
   a.ldx = ldx;
+  a.stride = stride;
   a.dtype = dtype;
   a.x = x;
   a.q = q;
   a.scale = scale;
-  return hip_status(nm::launch_mx_quantize(a, static_cast<hipStream_t>(stream)), "nm_mx_quantize launch");
+  return hip_status(nm::launch_mx_quantize(a, s), "nm_mx_quantize launch");
 }
 
-nm_status nm_mx_dequantize(const uint8_t* q, const uint8_t* scale, int64_t T, int64_t K, void* y, int64_t ldy,
-                           int dtype, void* stream) {
-  nm_status st = check_mx("T", T, K);
-  if (st != NM_OK || (st = check_mx_float(dtype)) != NM_OK || (st = check_ld("ldy", ldy, T, K)) != NM_OK) return st;
-  if (T == 0) return ok();
+nm_status nm_mx_quantize(const void* x, int64_t T, int64_t K, int64_t ldx, int dtype, uint8_t* q, uint8_t* scale,
+                         void* stream) {
+  nm_status st = check_mx_stack("T", 1, T, K, dtype, "ldx", ldx, 0);
+  if (st != NM_OK) return st;
+  return mx_quantize(x, 1, T, K, ldx, 0, dtype, q, scale, 16, static_cast<hipStream_t>(stream));
+}
+
+nm_status nm_mx_quantize_stack(const void* x, int64_t E, int64_t R, int64_t K, int64_t ldx, int64_t stride, int dtype,
+                               uint8_t* q, uint8_t* scale, void* stream) {
+  nm_status st = check_mx_stack("R", E, R, K, dtype, "ldx", ldx, stride);
+  if (st != NM_OK) return st;
+  return mx_quantize(x, E, R, K, ldx, stride, dtype, q, scale, 8, static_cast<hipStream_t>(stream));
+}
+
+static nm_status mx_dequantize(const uint8_t* q, const uint8_t* scale, size_t scale_align, int64_t E, int64_t R,
+                               int64_t K, void* y, int64_t ldy, int64_t stride, int dtype, hipStream_t s) {
+  if (E == 0 || R == 0) return ok();
   if (!y || !q || !scale) return fail(NM_ERR_NULL, "q, scale and y must be non-NULL");
   const size_t e = elt_bytes(dtype);
-  if (!aligned_to(y, e) || !aligned16(q) || !aligned16(scale))
-    return fail(NM_ERR_ALIGN, "q and scale must be 16-byte aligned, y to its element");
-  const Span in[] = {{q, size_t(T) * size_t(K / 2)}, {scale, mx_scale_bytes(T, K)}};
-  const Span out[] = {{y, extent(T, K, ldy, e)}};
-  if ((st = check_alias(in, out)) != NM_OK) return st;
+  if (!aligned_to(y, e) || !aligned16(q) || !aligned_to(scale, scale_align))
+    return fail(NM_ERR_ALIGN, "q must be 16-byte aligned, scale %zu, y to its element", scale_align);
+  const Span in[] = {{q, size_t(E) * size_t(R) * size_t(K / 2)}, {scale, size_t(E) * mx_scale_bytes(R, K)}};
+  const Span out[] = {{y, mx_stack_extent(E, R, K, ldy, stride, e)}};
+  if (nm_status st = check_alias(in, out); st != NM_OK) return st;
   nm::MxQuantArgs a;
-  a.T = T;
+  a.E = E;
+  a.T = R;
   a.K = K;
   a.ldx = ldy;
+  a.stride = stride;
   a.dtype = dtype;
   a.q = const_cast<uint8_t*>(q);
   a.scale = const_cast<uint8_t*>(scale);
   a.y = y;
-  return hip_status(nm::launch_mx_dequantize(a, static_cast<hipStream_t>(stream)), "nm_mx_dequantize launch");
+  return hip_status(nm::launch_mx_dequantize(a, s), "nm_mx_dequantize launch");
+}
+
+nm_status nm_mx_dequantize(const uint8_t* q, const uint8_t* scale, int64_t T, int64_t K, void* y, int64_t ldy,
+                           int dtype, void* stream) {
+  nm_status st = check_mx_stack("T", 1, T, K, dtype, "ldy", ldy, 0);
+  if (st != NM_OK) return st;
+  return mx_dequantize(q, scale, 16, 1, T, K, y, ldy, 0, dtype, static_cast<hipStream_t>(stream));
+}
+
+nm_status nm_mx_dequantize_stack(const uint8_t* q, const uint8_t* scale, int64_t E, int64_t R, int64_t K, void* y,
+                                 int64_t ldy, int64_t stride, int dtype, void* stream) {
+  nm_status st = check_mx_stack("R", E, R, K, dtype, "ldy", ldy, stride);
+  if (st != NM_OK) return st;
+  if (E > 1 && R > 0 && stride < (R - 1) * ldy + K)   // the matrices written would overlap
+    return fail(NM_ERR_STRIDE, "stride = %lld below one matrix", (long long)stride);
+  return mx_dequantize(q, scale, 8, E, R, K, y, ldy, stride, dtype, static_cast<hipStream_t>(stream));
 }
 
 static nm_status check_mx_gemm(int64_t E, int64_t R, int64_t K, int64_t T, bool grouped, int out_dtype) {
@@ -1545,9 +1593,9 @@ nm_status nm_mx_gemm(const uint8_t* wq, const uint8_t* wscale, int64_t E, int64_
   if (T == 0 || R == 0) return ok();
   if (!wq || !wscale || !xq || !xscale || !Y)
     return fail(NM_ERR_NULL, "wq, wscale, xq, xscale and Y must be non-NULL");
-  if (!aligned16(wq) || !aligned16(wscale) || !aligned16(xq) || !aligned16(xscale) || !aligned16(Y) ||
+  if (!aligned16(wq) || !aligned_to(wscale, 8) || !aligned16(xq) || !aligned_to(xscale, 8) || !aligned16(Y) ||
       !aligned_to(offsets, 4))
-    return fail(NM_ERR_ALIGN, "device pointers must be 16-byte aligned (offsets: 4)");
+    return fail(NM_ERR_ALIGN, "device pointers must be 16-byte aligned (scales: 8, offsets: 4)");
   const size_t need = nm::mx_workspace(E, R, T, offsets != nullptr);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
   const Span in[] = {{wq, size_t(E) * size_t(R) * size_t(K / 2)}, {wscale, size_t(E) * mx_scale_bytes(R, K)},

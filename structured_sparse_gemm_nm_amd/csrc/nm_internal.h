@@ -307,11 +307,13 @@ hipError_t launch_group(const GroupArgs& a, hipStream_t s);
 
 // Microscaled 4-bit floats (nm_mx.hip).
 struct MxQuantArgs {
+  int64_t E = 1;                // matrices, one after the other in q and scale
   int64_t T = 0, K = 0, ldx = 0;
+  int64_t stride = 0;           // elements from a matrix of x (y) to the next
   int dtype = 0;
   const void* x = nullptr;      // quantise: [T, K], ldx
-  uint8_t* q = nullptr;         // [T][K / 2]
-  uint8_t* scale = nullptr;     // [ceil(K / 256)][T][8]
+  uint8_t* q = nullptr;         // [E][T][K / 2]
+  uint8_t* scale = nullptr;     // [E][ceil(K / 256)][T][8]
   void* y = nullptr;            // dequantise: [T, K], ldx
 };
 struct MxArgs {

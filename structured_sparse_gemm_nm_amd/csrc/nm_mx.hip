@@ -38,17 +38,21 @@ __device__ inline f32x4 mfma_fp4(const u32x4& a, const u32x4& b, const f32x4& c,
 // that this one lies in [4, 8) (6 is the largest value: above it saturates), and
 // each value goes to the nearest of the eight magnitudes, ties to the even
 // mantissa.  Four lanes share a block, 8 values each.  A block that holds Inf or
-// NaN gets the exponent byte 255, which makes all of it NaN.
+// NaN gets the exponent byte 255, which makes all of it NaN.  Of a stack, workgroups
+// (.., e) take matrix e, `stride` elements of x (y) behind the one before.
 // Bound by its bytes: 2 (or 4) read and 17/32 written a value.  11008 x 4096 fp32:
 // 45 us, 4.6 TB/s.
 // ---------------------------------------------------------------------------
 template <int DT>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* __restrict__ x, int64_t T, int64_t K, int64_t ldx,
-                                                          bool vec, uint32_t* __restrict__ q,
+                                                          int64_t stride, bool vec, uint32_t* __restrict__ q,
                                                           uint8_t* __restrict__ scale) {
   const int64_t per_row = K / 8;   // shares of 8 values
   const int64_t panels = (K + 255) / 256;
   const int64_t total = T * panels * 32;   // whole panels: the last one's missing blocks get the byte 0
+  x = static_cast<const unsigned char*>(x) + blockIdx.y * stride * (DT == NM_F32 ? 4 : 2);
+  q += blockIdx.y * (T * per_row);
+  scale += blockIdx.y * (panels * T * 8);
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
     const int64_t t = i / (panels * 32), c = i - t * (panels * 32);
     float v[8];
@@ -108,9 +112,13 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* __restrict
 template <int DT>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint32_t* __restrict__ q,
                                                             const uint8_t* __restrict__ scale, int64_t T, int64_t K,
-                                                            void* __restrict__ y, int64_t ldy, bool vec) {
+                                                            void* __restrict__ y, int64_t ldy, int64_t stride,
+                                                            bool vec) {
   const int64_t per_row = K / 8;
   const int64_t total = T * per_row;
+  q += blockIdx.y * total;
+  scale += blockIdx.y * ((K + 255) / 256 * T * 8);
+  y = static_cast<unsigned char*>(y) + blockIdx.y * stride * (DT == NM_F32 ? 4 : 2);
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
     const int64_t t = i / per_row, c = i - t * per_row;
     const int64_t block = c >> 2;
@@ -581,21 +589,24 @@ inline unsigned grid_of(int64_t items) {
   return unsigned(blocks < 65536 ? blocks : 65536);
 }
 
+// Whether every row of every matrix at p begins on 16 bytes.
+inline bool rows_aligned(const MxQuantArgs& a, const void* p, int64_t e) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (a.ldx * e) % 16 == 0 && (a.E == 1 || (a.stride * e) % 16 == 0);
+}
+
 template <int DT>
 hipError_t quantize_dt(const MxQuantArgs& a, hipStream_t s) {
-  const int64_t e = DT == NM_F32 ? 4 : 2;
-  const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.ldx * e) % 16 == 0;
-  hipLaunchKernelGGL(mx_quantize_kernel<DT>, dim3(grid_of(a.T * ((a.K + 255) / 256) * 32)), dim3(256), 0, s, a.x, a.T,
-                     a.K, a.ldx, vec, reinterpret_cast<uint32_t*>(a.q), a.scale);
+  const bool vec = rows_aligned(a, a.x, DT == NM_F32 ? 4 : 2);
+  hipLaunchKernelGGL(mx_quantize_kernel<DT>, dim3(grid_of(a.T * ((a.K + 255) / 256) * 32), unsigned(a.E)), dim3(256), 0,
+                     s, a.x, a.T, a.K, a.ldx, a.stride, vec, reinterpret_cast<uint32_t*>(a.q), a.scale);
   return hipGetLastError();
 }
 
 template <int DT>
 hipError_t dequantize_dt(const MxQuantArgs& a, hipStream_t s) {
-  const int64_t e = DT == NM_F32 ? 4 : 2;
-  const bool vec = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && (a.ldx * e) % 16 == 0;
-  hipLaunchKernelGGL(mx_dequantize_kernel<DT>, dim3(grid_of(a.T * (a.K / 8))), dim3(256), 0, s,
-                     reinterpret_cast<const uint32_t*>(a.q), a.scale, a.T, a.K, a.y, a.ldx, vec);
+  const bool vec = rows_aligned(a, a.y, DT == NM_F32 ? 4 : 2);
+  hipLaunchKernelGGL(mx_dequantize_kernel<DT>, dim3(grid_of(a.T * (a.K / 8)), unsigned(a.E)), dim3(256), 0, s,
+                     reinterpret_cast<const uint32_t*>(a.q), a.scale, a.T, a.K, a.y, a.ldx, a.stride, vec);
   return hipGetLastError();
 }
 
@@ -670,14 +681,33 @@ hipError_t gemm_out(const MxArgs& a, hipStream_t s) {
 
 }  // namespace
 
+// A stack's matrices, as many a launch as the second dimension of its grid takes.
+template <class F>
+static hipError_t over_stack(MxQuantArgs a, const F& launch) {
+  const int64_t e = a.dtype == NM_F32 ? 4 : 2, E = a.E;
+  for (int64_t m = 0; m < E; m += kGroupMaxExperts) {
+    a.E = std::min(E - m, kGroupMaxExperts);
+    if (hipError_t err = launch(a); err != hipSuccess) return err;
+    if (a.x) a.x = static_cast<const unsigned char*>(a.x) + a.E * a.stride * e;
+    if (a.y) a.y = static_cast<unsigned char*>(a.y) + a.E * a.stride * e;
+    a.q += a.E * a.T * (a.K / 2);
+    a.scale += a.E * ((a.K + 255) / 256) * a.T * 8;
+  }
+  return hipSuccess;
+}
+
 hipError_t launch_mx_quantize(const MxQuantArgs& a, hipStream_t s) {
-  if (a.dtype == NM_F32) return quantize_dt<NM_F32>(a, s);
-  return a.dtype == NM_F16 ? quantize_dt<NM_F16>(a, s) : quantize_dt<NM_BF16>(a, s);
+  return over_stack(a, [s](const MxQuantArgs& a) {
+    if (a.dtype == NM_F32) return quantize_dt<NM_F32>(a, s);
+    return a.dtype == NM_F16 ? quantize_dt<NM_F16>(a, s) : quantize_dt<NM_BF16>(a, s);
+  });
 }
 
 hipError_t launch_mx_dequantize(const MxQuantArgs& a, hipStream_t s) {
-  if (a.dtype == NM_F32) return dequantize_dt<NM_F32>(a, s);
-  return a.dtype == NM_F16 ? dequantize_dt<NM_F16>(a, s) : dequantize_dt<NM_BF16>(a, s);
+  return over_stack(a, [s](const MxQuantArgs& a) {
+    if (a.dtype == NM_F32) return dequantize_dt<NM_F32>(a, s);
+    return a.dtype == NM_F16 ? dequantize_dt<NM_F16>(a, s) : dequantize_dt<NM_BF16>(a, s);
+  });
 }
 
 size_t mx_workspace(int64_t E, int64_t R, int64_t T, bool grouped) {
