@@ -1647,7 +1647,18 @@ static nm_status check_grads(const void* const* grads, const int64_t* counts, co
   nm_status st = check_workspace(workspace, workspace_bytes, nm::grad_workspace(tensors));
   if (st != NM_OK) return st;
   if (!aligned_to(norm, 4)) return fail(NM_ERR_ALIGN, "norm must be 4-byte aligned");
-  Written w[nm::kGradMaxTensors + 2];   // 400 KB of the caller's stack
+  // The ranges of ordinary lists in 6 KB of the caller's stack; those of longer ones, up
+  // to 400 KB, in one array for the process: a thread's whole stack may be smaller, and
+  // no call allocates.
+  constexpr int64_t kFew = 254;
+  static Written many[nm::kGradMaxTensors + 2];
+  static std::mutex many_mutex;
+  Written few[kFew + 2], *w = few;
+  std::unique_lock<std::mutex> hold(many_mutex, std::defer_lock);
+  if (out && tensors > kFew) {
+    hold.lock();
+    w = many;
+  }
   int64_t written = 0;
   auto add = [&](const void* p, size_t bytes, int32_t tensor) {
     const uintptr_t b = reinterpret_cast<uintptr_t>(p);
