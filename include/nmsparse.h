@@ -644,7 +644,9 @@ nm_status nm_mx_gemm(const uint8_t* wq, const uint8_t* wscale, int64_t E, int64_
  *   norm        device fp32 [1];  workspace  device, nm_grad_workspace_size bytes,
  *               16-byte aligned.
  * Squares are summed in 64 bits, so that neither large nor small gradients leave the
- * range; each out_i is rounded once.  A NaN anywhere makes norm and every out_i NaN; an
+ * range, and the norm rounded to fp32.  Of an out_i three things are rounded: the
+ * factor, taken in 64 bits, to fp32, its product with g_i to fp32, and that to the type
+ * (half a step each).  A NaN anywhere makes norm and every out_i NaN; an
  * Inf makes norm Inf, itself NaN and everything else 0 (with max_norm Inf nothing is
  * scaled).  A norm + eps of 0 scales by 1.  Equal calls give equal bits.
  * tensors <= 16384, counts <= 2^36; max_norm >= 0 (Inf: no limit), eps >= 0
