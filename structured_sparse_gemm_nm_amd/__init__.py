@@ -1212,7 +1212,11 @@ class GradList:
     A training loop whose gradients keep their tensors and sizes makes one and passes it to
     nm_grad_norm and nm_grad_clip every step: the tensors are checked here, once, and
     a call only asks each for its address (a tensor that has been given other memory
-    since is noticed, and the list checked again)."""
+    since is noticed, and the list checked again).
+
+    The list scales the tensors it was made of.  Gradients that are set to None between
+    steps (torch's zero_grad does so unless told otherwise) are other tensors in every
+    step: they need a list of their own, or the plain call."""
 
     def __init__(self, grads, out=None):
         self.grads, self.out = list(grads), None if out is None else list(out)
@@ -1259,7 +1263,8 @@ class GradList:
 
 def nm_grad_list(grads, out=None) -> GradList:
     """The gradients (float16, bfloat16 or float32, contiguous, mixed as they come) as a list that
-    nm_grad_norm and nm_grad_clip take without checking it again."""
+    nm_grad_norm and nm_grad_clip take without checking it again: for gradients that keep their
+    tensors from step to step (GradList says when they do not)."""
     return GradList(grads, out)
 
 

@@ -309,7 +309,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void group_few_kernel(const uint16_
 // lane quarter's run is 16 values, so the products differ only in the widening.
 // Of the 8 waves KS share K and 8 / KS take rows of their own; the KS partial tiles
 // are added in wave order through LDS, one barrier a step.
-// 96 tokens of 41 experts of 2816 x 2048 in 1:4: 32 us, 4.2 TB/s of packed bytes.
+// 96 tokens of 41 experts of 2816 x 2048 in 1:4: 32 to 34 us with inputs in turn, 3.9 to
+// 4.2 TB/s of packed bytes.
 // ---------------------------------------------------------------------------
 template <int N, int I = 0, class F>
 __device__ inline void static_for(F&& f) {
@@ -747,7 +748,8 @@ hipError_t launch_few(const GroupArgs& a, hipStream_t s) {
 
 // Units a wave of the streaming kernel keeps its tokens for: as many as its registers
 // hold (fewer, in more shares of K, mean more sums: 41 experts of 2816 x 2048 in 1:4
-// with 1 / 2 / 4 units 34.6 / 27.1 / 28.1 us).
+// with 1 / 2 / 4 units 37.9 / 34.2 / 35.2 us with inputs in turn, 34.6 / 27.1 / 28.1 with
+// the same ones, which the cache keeps).
 constexpr int stream_units(int P) { return P == 0 ? 4 : 2; }
 int stream_shares(const SpmmArgs& b) {
   const int P = b.n == 2 ? 0 : b.m == 4 ? 1 : 2;
@@ -815,12 +817,26 @@ bool stream_applies(const SpmmArgs& b, int64_t E) {
   return std::min(b.T, E) * ((b.R + rows - 1) / rows) >= 4 * 256;
 }
 
-// Which kernel: by the rows an expert has on average, of those that can have any.
+// Which kernel: by the rows an expert has on average, of those that can have any.  Both
+// sides of the limits, us with inputs in turn, on 41 experts of 2816 x 2048 and on 8 of
+// 4096 x 4096, each in 2:4 and in 1:4:
+//   rows        41: 2:4      41: 1:4      8: 2:4       8: 1:4
+//      8     59.0  68.4   36.9  52.1   35.7  43.8   23.1  29.1   stream, few2
+//     12     64.7  71.4   40.8  54.1   39.2  45.1   26.0  30.7   (it leads here as well)
+//     20     80.0  84.4   62.7  66.9   50.9  53.2   36.8  41.1   few2, tile64
+//     24     88.7  85.2   70.0  67.9   59.2  53.4   45.3  41.3
+//     32    101.0  86.7   80.9  69.8   64.3  53.9   49.8  41.8
+//     64    113.9  98.4   99.5  82.9   75.8  65.2   57.7  56.4   tile64, tile128; in 2:4
+//     96    138.5 126.6  124.1 113.8   85.6  88.9   68.1  70.5   lds 72.2, 86.9; 59.9, 61.9
 enum class Pick { stream, few1, few1_wide, few2, tile64, tile128, lds };
 
 Pick pick(const SpmmArgs& b, int64_t E) {
   const int64_t mean = mean_rows(b.T, E);
-  // 64 rows a wave (the tokens are read a quarter as often) where that leaves waves enough
+  // 64 rows a wave (the tokens are read a quarter as often) where that leaves waves enough;
+  // 16 and 64 rows, in 2:4 / 1:4 / 1:8: 2 experts of 4096 x 4096 11.5 and 15.9 us / 9.2 and
+  // 12.5 / 8.3 and 10.9; 3 of them 15.2 and 16.6 / 12.2 and 13.0 / 11.8 and 11.7; 8 of 1571 x
+  // 4128 17.2 and 17.7 / 13.3 and 12.7 / 18.3 and 13.7; 3 of 8192 x 4128 32.2 and 41.0 / 18.4
+  // and 23.1 / 25.4 and 21.8 (where the rows are many it is 1:8 alone that gains)
   if (mean <= 8) {
     if (stream_applies(b, E)) return Pick::stream;
     return std::min(b.T, E) * b.R >= 12288 ? Pick::few1_wide : Pick::few1;
@@ -831,9 +847,11 @@ Pick pick(const SpmmArgs& b, int64_t E) {
   // the single weight's large tiles and their table's launch where 96 of them fill the
   // chip (8 experts of 1024 x 1024: 2048 tokens, 64 tiles, 20.4 us against 13.9 below;
   // 16 experts of 1408 x 2048: 2048 tokens, 96 tiles, 29.4 against 36.4, 8192 tokens of
-  // 4096 x 2048, 1024 tiles, 108 against 180)
+  // 4096 x 2048, 1024 tiles, 108 against 180; all with the same inputs, from the cache)
   if (b.n == 2 && b.K % 128 == 0 && b.R >= 256 && (b.R + 255) / 256 * ((b.T + 127) / 128) >= 96) return Pick::lds;
-  // tiles of 128 tokens where there is one for every compute unit
+  // tiles of 128 tokens where there is one for every compute unit (4 experts of 2048 x 2048
+  // in 1:4 / 1:8, tiles of 64 and of 128: 1536 tokens, 192 tiles, 30.3 and 29.5 us / 33.3 and
+  // 31.2; 2048, 256 tiles, 43.0 and 37.1 / 47.6 and 40.9)
   const int64_t tiles = (b.R + kBR - 1) / kBR * ((b.T + 127) / 128);
   return tiles >= 256 ? Pick::tile128 : Pick::tile64;
 }

@@ -315,9 +315,11 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx_few_kernel(const uint8_t* _
 // Columns past K (the last step's): chunks that reread chunk 0 and enter as zeros
 // with the scale 1, whatever the panel holds there.  Rows past R and tokens past
 // the tile's end reread the last one and are not stored.
-// 4096 x 11008 x 4096 in 256 x 256 tiles: 98 us, 3.8 PFLOP/s, the matrix cores 33% busy,
-// 688 tiles in 2.7 rounds of the chip, bound by the operands' way through LDS; 1999 rows
-// of 7 experts of 2816 x 4096 in 128 x 128 tiles: 25 us, 1.9 PFLOP/s.
+// 4096 x 11008 x 4096 in 256 x 256 tiles: 91 to 98 us, 3.8 to 4.1 PFLOP/s (the instruction
+// alone, from registers: 8.4), 688 tiles in 2.7 rounds of the chip.  The matrix cores are
+// busy 33% of the time, LDS 31%, near half of that with bank conflicts; a wave issues 35%
+// of its time, waits for its turn 37%, for data or the barrier 28%.  1999 rows of 7 experts
+// of 2816 x 4096 in 128 x 128 tiles: 25 us, 1.9 PFLOP/s.
 // ---------------------------------------------------------------------------
 template <int BM_, int BN_, int WM_, int WN_>
 struct MxTile {
@@ -656,7 +658,20 @@ hipError_t launch_tiles(const MxArgs& a, hipStream_t s) {
 }
 
 // Which kernel: by the rows that a weight meets on average, and, where those fill
-// tiles, by whether the largest ones still give every compute unit one.
+// tiles, by whether the largest ones still give every compute unit one.  Both sides of the
+// limits, us with inputs in turn, on 11008 x 4096, 4096 x 4096 and 4096 x 11008:
+//   rows 16     9.5   9.9    5.3   9.2    9.1  19.0   few1, few2
+//        17    13.8   9.8    6.6   9.1   12.8  19.0
+//        32    10.5  12.0    9.8  11.4   20.5  23.8   few2, few4
+//        33    15.0  11.9    9.7  11.3   19.9  23.8
+//        64    13.4  14.6   12.6  14.1   27.5  31.6   few4, middle
+//        65    21.5  14.5   12.5  14.1   26.7  31.6
+//      1280    41.5  33.0   20.6  27.0   43.9  59.5   middle, large (215, 80, 80 tiles)
+//      1536    51.6  57.9   21.1  27.3   47.1  60.7   (258, 96, 96)
+//      4096   112.6  91.0   42.6  35.3   99.5  80.1   (688, 256, 256)
+// The limits are those of the first: where the weight has fewer rows, the smaller kernel
+// of a pair leads beyond its limit.  41 experts of 2816 x 2048: 300 rows, few1 and few2,
+// 35.0 and 30.8; 700 rows 49.2 and 32.5; 2600 rows, few4 and middle, 65.9 and 56.9.
 enum class MxPick { few1, few2, few4, middle, large };
 
 MxPick pick(int64_t E, int64_t R, int64_t T, bool grouped) {

@@ -82,9 +82,10 @@ struct OneWeight {
 };
 // Of the experts' rows (nm_group.h): from the table, by scalar loads, which leave the
 // vector-memory counter that the ring goes by alone.  (7999 tokens of 7 experts of
-// 4096 x 4096, whole call 218 us: 193 here, 0.70 PFLOP/s of stored products; the 1056
-// tiles are 4.1 rounds of 256 compute units, the fifth nearly empty.  16 experts of
-// 4096 x 2048, 8192 tokens, 1024 tiles and more for the ragged ends: 108 us.)
+// 4096 x 4096: 195 us, 0.69 PFLOP/s of stored products, with inputs that the cache keeps
+// from the call before, 228 with inputs in turn; the 1056 tiles are 4.1 rounds of 256
+// compute units, the fifth nearly empty.  16 experts of 4096 x 2048, 8192 tokens, 1024
+// tiles and more for the ragged ends: 108 and 125 us.)
 struct ExpertTiles {
   typedef const __attribute__((address_space(4))) u32x4* constant_ptr;
   const int4* table;

@@ -39,9 +39,12 @@ struct NoGroup {};
 // dX: the tiles, and from one expert's values (index words) to the next.
 // share > 0: workgroup y reduces over that many chunks of R and leaves fp32 sums
 // part_stride bytes from those before it.  (16 experts of 4096 x 2048 in 2:4, 8192
-// tokens: 215 us, 0.64 PFLOP/s of the dense product, the matrix cores 32% busy: bound by
-// LDS, through which every decompressed value goes twice, and by the vector ALUs'
-// decompression beside the products.)
+// tokens: 196 to 215 us, 0.64 to 0.70 PFLOP/s of the dense product.  Nothing is full: the
+// matrix cores are busy 32% of the time, LDS 49%, a third of that with bank conflicts; a
+// wave issues 41% of its time, waits for its turn to issue 41%, for data or the barrier
+// 18%.  The grid is of the most tiles there can be, and those that exist lie in the first
+// XCDs' runs, 158 each in seven and 78 in the last, 2.5 rounds of their compute units:
+// these have work 84% of the time.)
 struct GroupDx {
   GroupRows rows;
   int64_t values_stride, idx_stride;
@@ -50,8 +53,9 @@ struct GroupDx {
 };
 // dW: the experts' rows, from one's index words to the next, and its gradient (bytes).
 // shares > 1: workgroup y sums over a share of its expert's tokens and leaves it
-// part_stride bytes from the one before.  (The same experts and tokens: 180 us,
-// 0.76 PFLOP/s dense, the matrix cores 35% busy, bound by the transpose reads.)
+// part_stride bytes from the one before.  (The same experts and tokens: 173 to 180 us,
+// 0.76 to 0.79 PFLOP/s dense, the matrix cores 35% busy, LDS 31%; a wave issues 35% of its
+// time, waits for its turn 44%, for data or the barrier 21%.)
 struct GroupDw {
   const int32_t* offsets;
   int64_t idx_stride, dw_stride;
